@@ -162,7 +162,8 @@ def prepare(case, seed):
             sms = torch.cuda.get_device_properties(s["q"].device).multi_processor_count
             size = pkv.tree_decode_workspace(s["q"].shape[0], s["c"]["Hq"], s["c"]["D"], sms)
             s["workspace"] = torch.empty(size, dtype=torch.uint8, device=s["q"].device)
-        s["bound"] = {k: pkv.bind(x) for k, x in s.items() if isinstance(x, (torch.Tensor, list)) or x is None}
+        s["bound"] = {k: pkv.bind(x) for k, x in s.items()
+                      if k != "pool" and (x is None or isinstance(x, (torch.Tensor, list)))}
     return s
 
 
