@@ -39,8 +39,10 @@
  *     grid may have written, and before it can finish. Only the decodes
  *     (block tables, seq_lens, a split plan) and the planned merge (the
  *     plan's split counts) read index inputs before that wait, and only the
- *     cache writes and the decodes let their successor start early; no
- *     kernel writes index inputs. Calls on one stream therefore see each
+ *     cache writes and the decodes let their successor start early. The
+ *     calls that write index inputs (pkv_accept_drafts, pkv_resize_sequences,
+ *     pkv_fork_sequences, and pkv_copy into them) do not: whatever follows
+ *     them starts once they are done. Calls on one stream therefore see each
  *     other's results exactly as plain stream order would give.
  *   - Status. The return value reports argument validation and launch
  *     errors only: PKV_ERR_INVALID_ARG / PKV_ERR_UNSUPPORTED are returned
@@ -90,6 +92,9 @@ typedef enum { PKV_BF16 = 0, PKV_FP8_E4M3 = 1, PKV_F32 = 2, PKV_I32 = 3, PKV_FP4
 #define PKV_FLAG_DUPLICATE_SLOT 0x10  /* two tokens of one call map to the same slot         */
 #define PKV_FLAG_WAIT_TIMEOUT   0x20  /* an in-kernel wait gave up after its time limit      */
 #define PKV_FLAG_PLAN_RANGE     0x40  /* a split plan entry outside the batch or its records */
+#define PKV_FLAG_DRAFT_RANGE    0x80  /* drafted tokens' rows, mask or accepted list inconsistent */
+#define PKV_FLAG_POOL_EMPTY     0x100 /* too few free pages left for a sequence              */
+#define PKV_FLAG_PAGE_STATE     0x200 /* a page count or a row contradicts the call          */
 
 typedef struct {
     void*   ptr;        /* device address (NULL allowed only where stated) */
@@ -613,6 +618,184 @@ pkv_status pkv_stream_read(const void* buf, int64_t bytes, uint32_t* sink, int32
  */
 pkv_status pkv_selftest_bounded_wait(int64_t limit_ns, int32_t* err_flag, uint64_t* elapsed_ns,
                                      pkv_stream_t stream);
+
+/*
+ * Speculative and sampled decoding over the same paged caches. (No
+ * counterpart on the pages: these calls are for users of the decode step who
+ * verify several drafted tokens at once, sample several continuations of one
+ * prompt, or let the device hand out the pages of its cache.)
+ *
+ *   pkv_resize_sequences   pages for the tokens to come (or back to the pool)
+ *   pkv_rope_kv_write      the drafted tokens' k and v, at the positions
+ *                          behind the context
+ *   pkv_paged_tree_decode  attention of all drafted tokens in one call
+ *   pkv_accept_drafts      the accepted path's rows moved together, the new
+ *                          lengths
+ *   pkv_fork_sequences     sequences that continue another one
+ *
+ * All of them read every input on the device (lengths, block tables, drafted
+ * and accepted tokens), so a whole step can be captured into a CUDA graph and
+ * replayed while the lengths change.
+ */
+
+/*
+ * pkv_paged_tree_decode -- attention of the drafted tokens of every sequence
+ * over its paged cache.
+ *
+ * Sequence b's drafted tokens are rows [q_start[b], q_start[b+1]) of q, N_b of
+ * them; their k and v are in the cache already, at positions L - N_b + j, L =
+ * seq_lens[b] (which counts them). Row i sees the context (positions < L -
+ * N_b) and those drafted tokens j whose bit is set in its mask row (bit j % 32
+ * of word j / 32), or, without a mask, j <= i (a chain: also the form of a
+ * prompt's next chunk). Over the visible positions t:
+ *   score_t = softmax_scale * sum_d q[r,h,d] * K_t[d]
+ *   out[r,h,:] = bf16( sum_t exp(score_t - m) V_t / sum_t exp(score_t - m) )
+ *   lse_out[r,h] = m + ln sum_t exp(score_t - m)      (natural log)
+ * A row that sees nothing gives 0 and -inf. K and V of positions that a row
+ * does not see have no effect on it, whatever they hold.
+ *
+ * q            [T, Hq, D] bf16 (already rotated), innermost stride 1, rows
+ *              16-byte aligned.
+ * k_cache,
+ * v_cache, k_scale, v_scale, block_tables, seq_lens, layout
+ *              as for pkv_paged_gqa_decode (bf16 or FP8 caches, page size 16).
+ * q_start      [B+1] int32, ascending, within [0, T]. Rows of q outside every
+ *              range are not read and their outputs not written.
+ * tree_mask    [T, W] int32, innermost stride 1, 1 <= W <= 64: one bit per
+ *              drafted token; NULL = chain.
+ * out          [T, Hq, D] bf16, innermost stride 1, rows 16-byte aligned.
+ * lse_out      [T, Hq] float32, or NULL.
+ * workspace,
+ * workspace_bytes  device scratch, 16-byte aligned, of at least
+ *              pkv_tree_decode_workspace() bytes; its contents need no
+ *              preparation. Calls that may run at the same time need one each.
+ * Supported: D in {64, 128}; 1 <= Hq/Hkv <= 16; any N_b; B, Hkv <= 65535.
+ * Errors: a block-table entry outside [0, num_pages) sets PKV_FLAG_PAGE_RANGE
+ * and that page is left out; seq_lens[b] outside [0, 16*max_pages] sets
+ * PKV_FLAG_SEQ_LEN_RANGE and is clamped; q_start not ascending within [0, T]
+ * (clamped), N_b > L (the positions below 0 do not exist) and N_b > 32 W
+ * (drafted tokens past the mask are seen by no row) set PKV_FLAG_DRAFT_RANGE.
+ * Outputs must not alias inputs.
+ */
+pkv_status pkv_paged_tree_decode(const pkv_tensor* q, const pkv_tensor* k_cache, const pkv_tensor* v_cache,
+                                 const pkv_tensor* block_tables, const pkv_tensor* seq_lens,
+                                 const pkv_tensor* q_start, const pkv_tensor* tree_mask, float softmax_scale,
+                                 const pkv_tensor* out, const pkv_tensor* lse_out, void* workspace,
+                                 int64_t workspace_bytes, const pkv_tensor* k_scale, const pkv_tensor* v_scale,
+                                 int32_t layout, int32_t* err_flag, pkv_stream_t stream);
+
+/*
+ * pkv_tree_decode_workspace -- bytes of workspace that pkv_paged_tree_decode
+ * needs for T rows of q (host only); 0 for invalid input. sm_count is the
+ * device's SM count.
+ */
+int64_t pkv_tree_decode_workspace(int64_t T, int32_t Hq, int32_t D, int32_t sm_count);
+
+/*
+ * pkv_accept_drafts -- keep the accepted drafted tokens: their cache rows
+ * moved together behind the context, in every given cache, and the new
+ * lengths.
+ *
+ * For sequence b with N_b = q_start[b+1] - q_start[b] drafted tokens at
+ * positions base + j, base = seq_lens[b] - N_b, and n = num_accepted[b]:
+ *   cache row (base + j) <- cache row (base + accepted[b][j])   for j < n,
+ *   seq_lens_out[b] = base + n.
+ * The accepted indices ascend strictly, so a row is read before it is
+ * overwritten; rows behind base + n - 1 keep what the moves left there.
+ *
+ * caches,
+ * n_caches     an array of n_caches descriptors (0 .. 4096), one per cache
+ *              (each layer's K, V, block scales, latents ...): 4-D as laid out
+ *              by `layout` ([pages, P, H, W] or [pages, H, P, W]) or 3-D
+ *              [pages, P, W], any pkv_dtype, innermost stride 1; all with the
+ *              same number of pages and tokens per page P. No two may overlap.
+ * block_tables [B, max_pages] int32, innermost stride 1; seq_lens, num_accepted
+ *              [B] int32; q_start [B+1] int32; accepted [B, A] int32,
+ *              innermost stride 1, A <= 1024; entries past num_accepted are
+ *              not read.
+ * seq_lens_out [B] int32, not overlapping seq_lens.
+ * Errors: num_accepted outside [0, min(A, N_b)], indices that do not ascend
+ * strictly within [0, N_b), and N_b outside [0, L] set PKV_FLAG_DRAFT_RANGE,
+ * seq_lens outside [0, P*max_pages] sets PKV_FLAG_SEQ_LEN_RANGE: that
+ * sequence is left as it is (seq_lens_out = seq_lens). A move from or to a
+ * page outside [0, num_pages) is left out and sets PKV_FLAG_PAGE_RANGE. Two
+ * sequences must not share the pages of their drafted tokens.
+ */
+pkv_status pkv_accept_drafts(const pkv_tensor* caches, int32_t n_caches, int32_t layout,
+                             const pkv_tensor* block_tables, const pkv_tensor* seq_lens, const pkv_tensor* q_start,
+                             const pkv_tensor* accepted, const pkv_tensor* num_accepted,
+                             const pkv_tensor* seq_lens_out, int32_t* err_flag, pkv_stream_t stream);
+
+/*
+ * Page counts. page_refs [num_pages] int32 holds, for every page of a pool,
+ * how many block-table rows name it; a page is free when its count is 0.
+ * There is no list of free pages: the two calls below take the lowest-numbered
+ * free pages, in order of sequence and entry, so their results depend on
+ * their inputs alone. page_counts [B] int32 holds the entries in use of each
+ * block-table row (which may be more than its tokens need). Pages that
+ * nothing may take (a page of zeros, say) keep a count of 1.
+ */
+
+/*
+ * pkv_resize_sequences -- give each sequence the pages for new_lens[b] tokens:
+ * the entries past ceil(new_lens[b] / page_size) are returned (their counts
+ * lowered, the entries set to -1), missing ones are taken from the pool (their
+ * counts set to 1). All returns come before the first page is taken.
+ * new_lens[b] = 0 frees a sequence, < 0 leaves it as it is.
+ *
+ * block_tables [B, max_pages] int32, innermost stride 1, updated; page_counts
+ *              [B] int32, updated; new_lens [B] int32; page_refs [num_pages]
+ *              int32, contiguous, updated.
+ * page_size    tokens per page, 1 .. 65536. Supported: B <= 16384, num_pages
+ *              <= 2^27, max_pages <= 2^26.
+ * Errors: when the free pages do not reach for the growing sequences up to
+ * and including b (in order of b), b and the growing sequences after it stay
+ * as they are and PKV_FLAG_POOL_EMPTY is set. new_lens[b] past
+ * page_size*max_pages (PKV_FLAG_SEQ_LEN_RANGE) or page_counts[b] outside [0,
+ * max_pages] (PKV_FLAG_PAGE_STATE) leave b as it is. A returned entry outside
+ * [0, num_pages) sets PKV_FLAG_PAGE_RANGE; returning a page whose count is 0
+ * already sets PKV_FLAG_PAGE_STATE and leaves it 0.
+ */
+pkv_status pkv_resize_sequences(const pkv_tensor* block_tables, const pkv_tensor* page_counts,
+                                const pkv_tensor* new_lens, const pkv_tensor* page_refs, int32_t page_size,
+                                int32_t* err_flag, pkv_stream_t stream);
+
+/*
+ * pkv_fork_sequences -- sequences that continue others. For every fork i =
+ * (parent, child), rows of the block table, with L = seq_lens[parent]:
+ *   - the child's first floor(L / P) entries name the parent's pages, whose
+ *     counts rise by one (full pages are never written again, so they are
+ *     shared);
+ *   - when L % P != 0 the child gets the lowest free page for entry
+ *     floor(L / P), and that page becomes a copy of the parent's page, in
+ *     every given cache;
+ *   - page_counts[child] = ceil(L / P), seq_lens[child] = L.
+ * Free pages go to the forks in order of i. Every fork reads the state before
+ * the call. The child's row must hold no pages (page_counts[child] = 0; free
+ * it with pkv_resize_sequences).
+ *
+ * caches, n_caches, layout  as for pkv_accept_drafts; at least one (they name
+ *              the number of pages and tokens per page).
+ * block_tables [R, max_pages] int32, innermost stride 1, updated; page_counts,
+ *              seq_lens [R] int32, updated.
+ * forks        [n, 2] int32 (strides 2, 1); parent < 0 skips the entry. A row
+ *              may be parent many times and child once. n <= 16384.
+ * page_refs    [num_pages] int32, contiguous, updated.
+ * copies       [n, 2] int32 (strides 2, 1), out: the (source, destination)
+ *              page of fork i; (-1, -1) when its length needs no copy, (-2,
+ *              -2) when the fork was not made.
+ * Errors: rows outside [0, R), a child that holds pages or is named by an
+ * earlier fork set PKV_FLAG_PAGE_STATE; a parent whose length its pages do
+ * not hold sets PKV_FLAG_SEQ_LEN_RANGE; a last page outside [0, num_pages)
+ * sets PKV_FLAG_PAGE_RANGE: that fork is not made. When the free pages run
+ * out, the forks from there on that need one are not made
+ * (PKV_FLAG_POOL_EMPTY). A shared entry outside [0, num_pages) is carried over
+ * and sets PKV_FLAG_PAGE_RANGE.
+ */
+pkv_status pkv_fork_sequences(const pkv_tensor* caches, int32_t n_caches, int32_t layout,
+                              const pkv_tensor* block_tables, const pkv_tensor* page_counts,
+                              const pkv_tensor* seq_lens, const pkv_tensor* forks, const pkv_tensor* page_refs,
+                              const pkv_tensor* copies, int32_t* err_flag, pkv_stream_t stream);
 
 /* Static description of a status code. */
 const char* pkv_status_string(int32_t status);

@@ -27,6 +27,9 @@ FLAG_SEQ_LEN_RANGE = 0x08
 FLAG_DUPLICATE_SLOT = 0x10
 FLAG_WAIT_TIMEOUT = 0x20
 FLAG_PLAN_RANGE = 0x40
+FLAG_DRAFT_RANGE = 0x80
+FLAG_POOL_EMPTY = 0x100
+FLAG_PAGE_STATE = 0x200
 
 _DTYPES = {
     torch.bfloat16: 0,
@@ -43,7 +46,8 @@ EXPORTED = ("pkv_rope_kv_write", "pkv_paged_gqa_decode", "pkv_lse_merge", "pkv_c
             "pkv_validate_indices_static", "pkv_rope_kv_write_nvfp4", "pkv_paged_gqa_decode_nvfp4",
             "pkv_mla_cache_write", "pkv_paged_mla_decode", "pkv_choose_num_splits_mla",
             "pkv_selftest_bounded_wait", "pkv_copy", "pkv_plan_splits", "pkv_paged_gqa_decode_planned",
-            "pkv_lse_merge_planned", "pkv_plan_splits_mla", "pkv_paged_mla_decode_planned")
+            "pkv_lse_merge_planned", "pkv_plan_splits_mla", "pkv_paged_mla_decode_planned", "pkv_paged_tree_decode",
+            "pkv_tree_decode_workspace", "pkv_accept_drafts", "pkv_resize_sequences", "pkv_fork_sequences")
 
 
 class PkvTensor(ctypes.Structure):
@@ -91,6 +95,13 @@ def lib() -> ctypes.CDLL:
         L.pkv_lse_merge_planned.argtypes = [T, T, T, T, T, P]
         L.pkv_plan_splits_mla.argtypes = [P, i32, i32, i32, i32, i32, i32, P, P, P, ctypes.c_int64, P]
         L.pkv_paged_mla_decode_planned.argtypes = [T, T, T, T, T, T, ctypes.c_float, T, T, T, T, T, P, P]
+        L.pkv_paged_tree_decode.argtypes = [T, T, T, T, T, T, T, ctypes.c_float, T, T, P, ctypes.c_int64, T, T, i32,
+                                            P, P]
+        L.pkv_tree_decode_workspace.argtypes = [ctypes.c_int64, i32, i32, i32]
+        L.pkv_tree_decode_workspace.restype = ctypes.c_int64
+        L.pkv_accept_drafts.argtypes = [T, i32, i32, T, T, T, T, T, T, P, P]
+        L.pkv_resize_sequences.argtypes = [T, T, T, T, i32, P, P]
+        L.pkv_fork_sequences.argtypes = [T, i32, i32, T, T, T, T, T, T, P, P]
         L.pkv_status_string.argtypes = [i32]
         L.pkv_status_string.restype = ctypes.c_char_p
         for name in ("pkv_rope_kv_write", "pkv_paged_gqa_decode", "pkv_lse_merge", "pkv_validate_indices",
@@ -98,7 +109,8 @@ def lib() -> ctypes.CDLL:
                      "pkv_rope_kv_write_nvfp4", "pkv_paged_gqa_decode_nvfp4", "pkv_mla_cache_write",
                      "pkv_paged_mla_decode", "pkv_choose_num_splits_mla", "pkv_selftest_bounded_wait", "pkv_copy",
                      "pkv_plan_splits", "pkv_paged_gqa_decode_planned", "pkv_lse_merge_planned",
-                     "pkv_plan_splits_mla", "pkv_paged_mla_decode_planned"):
+                     "pkv_plan_splits_mla", "pkv_paged_mla_decode_planned", "pkv_paged_tree_decode",
+                     "pkv_accept_drafts", "pkv_resize_sequences", "pkv_fork_sequences"):
             getattr(L, name).restype = ctypes.c_int32
         _lib = L
     return _lib
@@ -108,11 +120,59 @@ def status_string(status: int) -> str:
     return lib().pkv_status_string(int(status)).decode()
 
 
-def _desc(t: Optional[torch.Tensor], dtype: Optional[int] = None):
+class Bound:
+    """A tensor, or a list of tensors, with its descriptors made once (see
+    bind). Keeps the tensors alive."""
+    __slots__ = ("tensors", "ptr", "n", "data", "nbytes", "device")
+
+    def __init__(self, tensors, ptr, n: int):
+        self.tensors, self.ptr, self.n = tensors, ptr, n
+        first = tensors[0] if tensors else None
+        self.data = first.data_ptr() if first is not None else None
+        self.nbytes = first.numel() * first.element_size() if first is not None else 0
+        self.device = first.get_device() if first is not None else None
+
+
+def bind(t):
+    """Descriptors of a tensor, or of a list of tensors (the caches of a
+    model), made once for buffers that a program passes call after call: every
+    call here takes what bind() returns in place of the tensor, and skips the
+    descriptor's making. The tensor's memory, shape and strides are those at
+    the time of bind()."""
+    if t is None or isinstance(t, Bound):
+        return t
+    if isinstance(t, torch.Tensor):
+        return Bound([t], _desc(t), 1)
+    ts = list(t)
+    if any(x.get_device() != ts[0].get_device() for x in ts):
+        raise ValueError("the tensors of one call are on different devices")
+    arr = (PkvTensor * len(ts))()
+    for i, x in enumerate(ts):
+        arr[i] = _desc(x).contents
+    return Bound(ts, ctypes.cast(arr, ctypes.POINTER(PkvTensor)) if ts else None, len(ts))
+
+
+def _on_current_device(*ts) -> None:
+    """The kernels run on the current device's stream: a tensor of another
+    device would be reached through a peer mapping, or not at all."""
+    dev = torch.cuda.current_device()
+    for t in ts:
+        if t is None:
+            continue
+        d = t.device if isinstance(t, Bound) else t.get_device()
+        if d is not None and d != dev and not (isinstance(t, torch.Tensor) and not t.numel()):
+            raise ValueError(f"a tensor is on device {d}, the current device is {dev}")
+
+
+def _desc(t, dtype: Optional[int] = None):
     """Pointer to a descriptor of t (NULL for None); `dtype` overrides the
     pkv_dtype taken from t.dtype (uint8 NVFP4 value caches)."""
     if t is None:
         return None
+    if isinstance(t, Bound):
+        if dtype is not None:
+            raise TypeError("NVFP4 value caches are passed as tensors, not bound")
+        return t.ptr
     d = PkvTensor()
     if t.dim() > 4:
         raise ValueError("tensors of more than 4 dims are not part of the ABI")
@@ -135,8 +195,10 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+def _ptr(t):
+    if t is None:
+        return None
+    return t.data if isinstance(t, Bound) else t.data_ptr()
 
 
 def _check(fn: str, status: int) -> None:
@@ -297,6 +359,68 @@ def lse_merge_planned(out_partial, lse_partial, splits_per_seq, out, lse_out=Non
     """pkv_lse_merge_planned: each sequence's own records [0, S_b)."""
     _check("pkv_lse_merge_planned", lib().pkv_lse_merge_planned(
         _desc(out_partial), _desc(lse_partial), _desc(splits_per_seq), _desc(out), _desc(lse_out), _stream(stream)))
+
+
+def tree_decode_workspace(T: int, Hq: int, D: int, sm_count: int) -> int:
+    """Bytes of workspace that paged_tree_decode needs for T rows of q."""
+    return int(lib().pkv_tree_decode_workspace(int(T), Hq, D, sm_count))
+
+
+def paged_tree_decode(q, k_cache, v_cache, block_tables, seq_lens, q_start, tree_mask, softmax_scale: float, out,
+                      lse_out, workspace, k_scale=None, v_scale=None, layout: str = "HND", err_flag=None,
+                      stream=None) -> None:
+    """Attention of the drafted tokens (rows q_start[b] .. q_start[b+1] of q
+    [T,Hq,D] for sequence b) over the paged cache that holds them behind the
+    context, under tree_mask [T,W] int32 bits or, with None, as a chain
+    (pkv_paged_tree_decode): out [T,Hq,D] bf16, lse_out [T,Hq] float32 or None.
+    workspace: a contiguous device tensor of tree_decode_workspace() bytes."""
+    _on_current_device(q, k_cache, v_cache, block_tables, seq_lens, q_start, tree_mask, out, lse_out, workspace,
+                       k_scale, v_scale, err_flag)
+    if workspace is None:
+        ws, nbytes = None, 0
+    elif isinstance(workspace, Bound):
+        ws, nbytes = workspace.data, workspace.nbytes
+    else:
+        ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check("pkv_paged_tree_decode", lib().pkv_paged_tree_decode(
+        _desc(q), _desc(k_cache), _desc(v_cache), _desc(block_tables), _desc(seq_lens), _desc(q_start),
+        _desc(tree_mask), softmax_scale, _desc(out), _desc(lse_out), ws, nbytes, _desc(k_scale), _desc(v_scale),
+        LAYOUTS[layout], _ptr(err_flag), _stream(stream)))
+
+
+def accept_drafts(caches, block_tables, seq_lens, q_start, accepted, num_accepted, seq_lens_out, layout: str = "HND",
+                  err_flag=None, stream=None) -> None:
+    """Moves the accepted drafted tokens' rows together behind the context, in
+    every cache of the list `caches`, and writes the new lengths
+    (pkv_accept_drafts)."""
+    caches = bind(caches)
+    _on_current_device(caches, block_tables, seq_lens, q_start, accepted, num_accepted, seq_lens_out, err_flag)
+    _check("pkv_accept_drafts", lib().pkv_accept_drafts(
+        caches.ptr, caches.n, LAYOUTS[layout], _desc(block_tables), _desc(seq_lens), _desc(q_start), _desc(accepted),
+        _desc(num_accepted), _desc(seq_lens_out), _ptr(err_flag), _stream(stream)))
+
+
+def resize_sequences(block_tables, page_counts, new_lens, page_refs, page_size: int = 16, err_flag=None,
+                     stream=None) -> None:
+    """Returns and takes pages so that every sequence holds those of
+    new_lens[b] tokens (< 0: unchanged), the lowest free pages first
+    (pkv_resize_sequences)."""
+    _on_current_device(block_tables, page_counts, new_lens, page_refs, err_flag)
+    _check("pkv_resize_sequences", lib().pkv_resize_sequences(
+        _desc(block_tables), _desc(page_counts), _desc(new_lens), _desc(page_refs), page_size, _ptr(err_flag),
+        _stream(stream)))
+
+
+def fork_sequences(caches, block_tables, page_counts, seq_lens, forks, page_refs, copies, layout: str = "HND",
+                   err_flag=None, stream=None) -> None:
+    """Makes row forks[i][1] continue row forks[i][0]: full pages shared, the
+    partial last page copied in every cache of the list `caches`; copies [n,2]
+    receives the copied pages (pkv_fork_sequences)."""
+    caches = bind(caches)
+    _on_current_device(caches, block_tables, page_counts, seq_lens, forks, page_refs, copies, err_flag)
+    _check("pkv_fork_sequences", lib().pkv_fork_sequences(
+        caches.ptr, caches.n, LAYOUTS[layout], _desc(block_tables), _desc(page_counts), _desc(seq_lens), _desc(forks),
+        _desc(page_refs), _desc(copies), _ptr(err_flag), _stream(stream)))
 
 
 def validate_indices(block_tables, seq_lens, slot_mapping, num_pages: int, err_flag, slot_bitmap=None,

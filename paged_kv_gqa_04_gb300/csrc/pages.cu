@@ -1,0 +1,506 @@
+// pages.cu -- the pages and rows of a paged cache that move between decode
+// steps: accepted drafted tokens, resized and forked sequences.
+//
+// accept_kernel. One CTA per (sequence, cache); each thread owns 16 bytes of
+// a token row and moves them for the accepted tokens in ascending order. The
+// indices ascend strictly, so a destination never lies past its source: four
+// rows are read before the first of them is written, and no later source can
+// have been overwritten.
+//
+// take_kernel (resize, and the first half of a fork). Page counts only, no
+// free list: a page is free when its count is 0, and free pages are handed
+// out lowest first, in order of (sequence, entry). One cluster of CTAs: the
+// demands' prefix sums in shared memory (each CTA computes them all), returns
+// dealt out by element, a cluster barrier, then every warp counts the zeros
+// of a contiguous stretch of page_refs, the CTAs exchange their counts through
+// distributed shared memory, and each zero of rank r < demand goes to the
+// entry that the prefix sums give r (a binary search). Every result follows
+// from the inputs alone: atomics only add and subtract counts.
+//
+// share_kernel (the second half of a fork). CTAs of (fork, cache) copy the
+// partial last page; CTAs of (fork, stretch of the table) copy the shared
+// entries and raise their pages' counts.
+#include <algorithm>
+
+#include "pkv_internal.h"
+#include "pkv_ptx.cuh"
+
+namespace pkv {
+namespace {
+
+template <typename V>
+__device__ __forceinline__ V ld_as(const uint8_t* p) {
+    return *reinterpret_cast<const V*>(p);
+}
+template <typename V>
+__device__ __forceinline__ void st_as(uint8_t* p, V v) {
+    *reinterpret_cast<V*>(p) = v;
+}
+
+// ---- accepted drafted tokens --------------------------------------------------
+constexpr int kAcceptThreads = 128;
+constexpr int kBatch = 4;  // rows in flight per thread
+
+template <typename V>
+__device__ __forceinline__ void move_rows(const PoolPart& c, const int64_t* src, const int64_t* dst, int n) {
+    const int per_row = c.row / static_cast<int>(sizeof(V));
+    const int units = c.n1 * per_row;
+    for (int u = threadIdx.x; u < units; u += kAcceptThreads) {
+        const int h = u / per_row;
+        const int64_t off = h * c.s1 + static_cast<int64_t>(u - h * per_row) * sizeof(V);
+        for (int j = 0; j < n; j += kBatch) {
+            V v[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (j + k < n && src[j + k] >= 0) v[k] = ld_as<V>(c.p + src[j + k] + off);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (j + k < n && src[j + k] >= 0) st_as<V>(c.p + dst[j + k] + off, v[k]);
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const __grid_constant__ AcceptArgs a) {
+    __shared__ int64_t src[kMaxAccepted], dst[kMaxAccepted];
+    __shared__ int bad, n_moves;
+    // seq_lens and the tables may be written by the preceding grid, and
+    // seq_lens_out is an index input of the next: no early trigger.
+    grid_dep_wait();
+    const int b = blockIdx.x;
+    const bool first = blockIdx.y == 0 && a.write_lens;
+    const int L = a.seq_lens[b];
+    const int64_t N64 = static_cast<int64_t>(a.q_start[b + 1]) - a.q_start[b];
+    const int n = a.n_accepted[b];
+    const int64_t cap = static_cast<int64_t>(a.max_pages) * a.page_size;
+    int flags = 0;
+    if (L < 0 || L > cap) flags |= PKV_FLAG_SEQ_LEN_RANGE;
+    else if (N64 < 0 || N64 > L || n < 0 || n > N64 || n > a.A) flags |= PKV_FLAG_DRAFT_RANGE;
+    if (flags) {
+        if (threadIdx.x == 0 && first) {
+            flag_error(a.err, flags);
+            a.seq_lens_out[b] = L;
+        }
+        return;
+    }
+    const int N = static_cast<int>(N64), base = L - N;
+    if (threadIdx.x == 0) bad = 0, n_moves = 0;
+    __syncthreads();
+    for (int j = threadIdx.x; j < n; j += kAcceptThreads) {
+        const int32_t* row = a.accepted + b * a.ac_s0;
+        const int x = row[j], prev = j ? row[j - 1] : -1;
+        if (x <= prev || x >= N) bad = 1;
+    }
+    __syncthreads();
+    if (bad) {
+        if (threadIdx.x == 0 && first) {
+            flag_error(a.err, PKV_FLAG_DRAFT_RANGE);
+            a.seq_lens_out[b] = L;
+        }
+        return;
+    }
+    if (threadIdx.x == 0 && first) a.seq_lens_out[b] = base + n;
+    if (a.n_caches == 0) return;
+    const PoolPart& c = a.c[blockIdx.y];
+    for (int j = threadIdx.x; j < n; j += kAcceptThreads) {
+        const int sp = base + a.accepted[b * a.ac_s0 + j], dp = base + j;
+        int64_t s = -1, d = -1;
+        if (sp != dp) {  // accepted from j on: everything before it is in place already
+            const int ps = a.block_tables[b * a.bt_s0 + sp / a.page_size];
+            const int pd = a.block_tables[b * a.bt_s0 + dp / a.page_size];
+            if (ps < 0 || ps >= a.num_pages || pd < 0 || pd >= a.num_pages) {
+                if (first) flag_error(a.err, PKV_FLAG_PAGE_RANGE);
+            } else {
+                s = ps * c.s_page + (sp % a.page_size) * c.s0;
+                d = pd * c.s_page + (dp % a.page_size) * c.s0;
+            }
+        }
+        src[j] = s;
+        dst[j] = d;
+        if (s >= 0) n_moves = 1;
+    }
+    __syncthreads();
+    if (!n_moves) return;
+    switch (c.vec) {
+        case 16: move_rows<uint4>(c, src, dst, n); break;
+        case 8: move_rows<uint2>(c, src, dst, n); break;
+        case 4: move_rows<uint32_t>(c, src, dst, n); break;
+        default: move_rows<uint8_t>(c, src, dst, n); break;
+    }
+}
+
+// ---- pages taken from and returned to the pool ----------------------------------
+constexpr int kTakeThreads = 1024;
+constexpr int kTakeWarps = kTakeThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr uint32_t kDemandCap = 1u << 30;  // sums saturate here, above any pool
+
+__device__ __forceinline__ uint32_t sat_add(uint32_t x, uint32_t y) { return min(x + y, kDemandCap); }
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+// All threads of the cluster; what they wrote before (shared memory of any
+// CTA, device memory) is visible to all of them after it.
+__device__ __forceinline__ void cluster_barrier() {
+    __threadfence();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void st_cluster(uint32_t local_addr, uint32_t rank, uint32_t v) {
+    asm volatile(
+        "{\n\t.reg .u32 ra;\n\tmapa.shared::cluster.u32 ra, %0, %1;\n\tst.shared::cluster.u32 [ra], %2;\n\t}" ::"r"(
+            local_addr),
+        "r"(rank), "r"(v)
+        : "memory");
+}
+
+// Exclusive saturating prefix sums of x[0, n) in place, x[n] = the total. All
+// threads of the CTA; thread t owns a contiguous stretch.
+__device__ void block_prefix(uint32_t* x, int n, uint32_t* warp_sum) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int seg = (n + kTakeThreads - 1) / kTakeThreads;
+    const int i0 = min(tid * seg, n), i1 = min(i0 + seg, n);
+    __syncthreads();
+    uint32_t sum = 0;
+    for (int i = i0; i < i1; ++i) sum = sat_add(sum, x[i]);
+    uint32_t inc = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc = sat_add(inc, y);
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    uint32_t excl = __shfl_up_sync(0xffffffffu, inc, 1);
+    if (lane == 0) excl = 0;
+    __syncthreads();
+    uint32_t base = 0, total = 0;
+    for (int w = 0; w < kTakeWarps; ++w) {
+        if (w == warp) base = total;
+        total = sat_add(total, warp_sum[w]);
+    }
+    uint32_t run = sat_add(base, excl);
+    for (int i = i0; i < i1; ++i) {
+        const uint32_t d = x[i];
+        x[i] = run;
+        run = sat_add(run, d);
+    }
+    if (tid == 0) x[n] = total;
+    __syncthreads();
+}
+
+// Largest i with x[i] <= r, for x[0] = 0 <= r < x[n].
+__device__ __forceinline__ int owner_of(const uint32_t* x, int n, uint32_t r) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (x[mid] <= r) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// What row b has and is to have; flags set when it stays as it is.
+__device__ __forceinline__ void resize_row(const TakeArgs& a, int b, int& have, int& want, int& flags) {
+    have = a.page_counts[b];
+    const int len = a.new_lens[b];
+    flags = 0;
+    if (have < 0 || have > a.max_pages) {
+        flags = PKV_FLAG_PAGE_STATE;
+        want = have;
+        return;
+    }
+    want = have;
+    if (len < 0) return;
+    const int need = len / a.page_size + (len % a.page_size != 0);
+    if (need > a.max_pages) flags = PKV_FLAG_SEQ_LEN_RANGE;
+    else want = need;
+}
+
+// The four counts from page p on as a mask of the free ones (p a multiple of 4).
+__device__ __forceinline__ uint32_t free_mask(const int32_t* refs, int64_t p, int64_t end, bool vec) {
+    if (p + 4 <= end && vec) {
+        const int4 v = __ldcg(reinterpret_cast<const int4*>(refs + p));
+        return (v.x == 0) | (v.y == 0) << 1 | (v.z == 0) << 2 | (v.w == 0) << 3;
+    }
+    uint32_t m = 0;
+    for (int k = 0; k < 4; ++k)
+        if (p + k < end && __ldcg(refs + p + k) == 0) m |= 1u << k;
+    return m;
+}
+
+template <bool FORK>
+__global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constant__ TakeArgs a) {
+    extern __shared__ uint32_t dyn[];
+    __shared__ uint32_t warp_sum[kTakeWarps], warp_free[kTakeWarps], cta_free[kMaxCluster];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cluster_rank(), C = cluster_size();
+    const int n = a.n;
+    uint32_t* need = dyn;                              // [n + 1]: demands, then their prefix sums
+    uint32_t* give = dyn + (n + 1);                    // resize: [n + 1] returns, then their prefix sums
+    int32_t* len = reinterpret_cast<int32_t*>(give);   // fork: [n] parent's length, -1 = not made
+    int32_t* tail = len + n;                           // fork: [n] page to copy, -1 = none
+
+    // Counts, tables and lengths may be written by the preceding grid. What
+    // this grid writes are index inputs: a resize lets nothing start early, a
+    // fork only its own second half (which waits before it reads).
+    grid_dep_wait();
+    if (FORK) grid_dep_launch();
+
+    int flags = 0;
+    if constexpr (!FORK) {
+        for (int b = tid; b < n; b += kTakeThreads) {
+            int have, want, f;
+            resize_row(a, b, have, want, f);
+            flags |= f;
+            need[b] = want > have ? want - have : 0;
+            give[b] = want < have ? have - want : 0;
+        }
+        block_prefix(give, n, warp_sum);
+        // returns, dealt out one entry at a time over the cluster
+        const uint32_t total = give[n];
+        for (uint32_t e = rank * kTakeThreads + tid; e < total; e += C * kTakeThreads) {
+            const int b = owner_of(give, n, e);
+            int have, want, f;
+            resize_row(a, b, have, want, f);
+            int32_t* entry = a.block_tables + b * a.bt_s0 + want + (e - give[b]);
+            const int page = *entry;
+            *entry = -1;
+            if (page < 0 || page >= a.num_pages) {
+                flag_error(a.err, PKV_FLAG_PAGE_RANGE);
+            } else if (atomicSub(a.page_refs + page, 1) <= 0) {
+                atomicAdd(a.page_refs + page, 1);
+                flag_error(a.err, PKV_FLAG_PAGE_STATE);
+            }
+        }
+    } else {
+        // A child's count of 0 becomes a claim: -(n - i) of its first fork i
+        // (the lowest value stays). Every CTA makes the same claims.
+        for (int i = tid; i < n; i += kTakeThreads) {
+            const int p = a.forks[2 * i], c = a.forks[2 * i + 1];
+            int L = -1, src = -1;
+            if (p >= 0) {
+                if (p >= a.rows || c < 0 || c >= a.rows || a.page_counts[c] > 0) {
+                    flags |= PKV_FLAG_PAGE_STATE;
+                } else {
+                    const int x = a.seq_lens[p];
+                    const int full = x / a.page_size, part = x % a.page_size != 0;
+                    if (x < 0 || full + part > min(max(a.page_counts[p], 0), a.max_pages)) {
+                        flags |= PKV_FLAG_SEQ_LEN_RANGE;
+                    } else {
+                        if (part) src = a.block_tables[p * a.bt_s0 + full];
+                        if (part && (src < 0 || src >= a.num_pages)) {
+                            flags |= PKV_FLAG_PAGE_RANGE;
+                        } else {
+                            L = x;
+                            atomicMin(a.page_counts + c, -(n - i));
+                        }
+                    }
+                }
+            }
+            len[i] = L;
+            tail[i] = L < 0 ? -1 : src;
+        }
+        cluster_barrier();
+        for (int i = tid; i < n; i += kTakeThreads) {
+            if (len[i] >= 0 && __ldcg(a.page_counts + a.forks[2 * i + 1]) != -(n - i)) {
+                flags |= PKV_FLAG_PAGE_STATE;  // an earlier fork has this child
+                len[i] = -1;
+                tail[i] = -1;
+            }
+            need[i] = tail[i] >= 0 ? 1 : 0;
+        }
+    }
+    block_prefix(need, n, warp_sum);
+    cluster_barrier();  // every return is counted
+
+    // ---- free pages: each warp a contiguous stretch ------------------------------
+    const int64_t cta_span = ((a.num_pages + C - 1) / C + 127) / 128 * 128;
+    const int64_t warp_span = ((cta_span + kTakeWarps - 1) / kTakeWarps + 127) / 128 * 128;
+    const int64_t cta0 = rank * cta_span, cta1 = min(cta0 + cta_span, a.num_pages);
+    const int64_t p0 = min(cta0 + warp * warp_span, cta1), p1 = min(p0 + warp_span, cta1);
+    const bool vec = (reinterpret_cast<uintptr_t>(a.page_refs) & 15) == 0;
+    const uint32_t wanted = need[n];
+    uint32_t cnt = 0;
+    if (wanted) {
+#pragma unroll 4
+        for (int64_t p = p0 + 4 * lane; p < p1; p += 128) cnt += __popc(free_mask(a.page_refs, p, p1, vec));
+    }
+    cnt = __reduce_add_sync(0xffffffffu, cnt);
+    if (lane == 0) warp_free[warp] = cnt;
+    __syncthreads();
+    if (warp == 0) {
+        const uint32_t t = __reduce_add_sync(0xffffffffu, warp_free[lane]);
+        if (lane < static_cast<int>(C)) st_cluster(smem_u32(&cta_free[rank]), lane, t);
+    }
+    cluster_barrier();
+    uint32_t at = 0, total_free = 0;
+    for (uint32_t r = 0; r < C; ++r) {
+        if (r == rank) at = total_free;
+        total_free += cta_free[r];
+    }
+    for (int w = 0; w < warp; ++w) at += warp_free[w];
+    const uint32_t last = min(wanted, total_free);  // ranks past it go to nobody
+    for (int64_t g = p0; g < p1 && at < last; g += 128) {
+        const int64_t p = g + 4 * lane;
+        const uint32_t m = p < p1 ? free_mask(a.page_refs, p, p1, vec) : 0;
+        uint32_t inc = __popc(m);
+        const uint32_t own_n = inc;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += y;
+        }
+        uint32_t r = at + inc - own_n;
+        at += __shfl_sync(0xffffffffu, inc, 31);
+        for (int k = 0; k < 4; ++k) {
+            if (!(m >> k & 1)) continue;
+            if (r < last) {
+                const int i = owner_of(need, n, r);
+                if (need[i + 1] <= total_free) {  // i gets all that it needs
+                    const int page = static_cast<int>(p + k);
+                    if constexpr (!FORK) {
+                        a.block_tables[i * a.bt_s0 + a.page_counts[i] + (r - need[i])] = page;
+                    } else {
+                        a.block_tables[a.forks[2 * i + 1] * a.bt_s0 + len[i] / a.page_size] = page;
+                        a.copies[2 * i] = tail[i];
+                        a.copies[2 * i + 1] = page;
+                    }
+                    a.page_refs[page] = 1;
+                }
+            }
+            ++r;
+        }
+    }
+    cluster_barrier();  // every CTA has read the counts and lengths
+    if (rank != 0) return;
+    for (int i = tid; i < n; i += kTakeThreads) {
+        const bool fails = need[i + 1] > need[i] && need[i + 1] > total_free;
+        if (fails) flags |= PKV_FLAG_POOL_EMPTY;
+        if constexpr (!FORK) {
+            int have, want, f;
+            resize_row(a, i, have, want, f);
+            if (!fails && want != have) a.page_counts[i] = want;
+        } else {
+            if (len[i] >= 0) {
+                const int c = a.forks[2 * i + 1], pages = len[i] / a.page_size + (tail[i] >= 0);
+                a.page_counts[c] = fails ? 0 : pages;
+                if (!fails) a.seq_lens[c] = len[i];
+            }
+            if (len[i] < 0 || fails) a.copies[2 * i] = a.copies[2 * i + 1] = -2;
+            else if (tail[i] < 0) a.copies[2 * i] = a.copies[2 * i + 1] = -1;
+        }
+    }
+    if (flags) flag_error(a.err, flags);
+}
+
+// ---- shared entries and copied pages of a fork --------------------------------------
+constexpr int kShareThreads = 256;
+constexpr int kShareSpan = 2048;  // table entries per CTA
+
+template <typename V>
+__device__ __forceinline__ void copy_page(const PoolPart& c, int64_t src, int64_t dst) {
+    const int per_row = c.row / static_cast<int>(sizeof(V));
+    const int units = c.n0 * c.n1 * per_row;
+    auto at = [&](int u) -> int64_t {
+        const int row = u / per_row, i0 = row / c.n1;
+        return i0 * c.s0 + (row - i0 * c.n1) * c.s1 + static_cast<int64_t>(u - row * per_row) * sizeof(V);
+    };
+    for (int u0 = threadIdx.x; u0 < units; u0 += 8 * kShareThreads) {
+        V v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (u0 + k * kShareThreads < units) v[k] = ld_as<V>(c.p + src + at(u0 + k * kShareThreads));
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (u0 + k * kShareThreads < units) st_as<V>(c.p + dst + at(u0 + k * kShareThreads), v[k]);
+    }
+}
+
+__global__ void __launch_bounds__(kShareThreads) share_kernel(const __grid_constant__ ShareArgs a) {
+    grid_dep_wait();  // the first half's results; the table is an index input: no early trigger
+    const int i = blockIdx.x;
+    const int src = a.copies[2 * i], dst = a.copies[2 * i + 1];
+    if (src == -2) return;  // not made
+    const int y = static_cast<int>(blockIdx.y) - a.table_ctas;
+    if (y >= 0) {
+        if (src < 0) return;
+        const PoolPart& c = a.c[y];
+        const int64_t s = src * c.s_page, d = dst * c.s_page;
+        switch (c.vec) {
+            case 16: copy_page<uint4>(c, s, d); break;
+            case 8: copy_page<uint2>(c, s, d); break;
+            case 4: copy_page<uint32_t>(c, s, d); break;
+            default: copy_page<uint8_t>(c, s, d); break;
+        }
+        return;
+    }
+    const int p = a.forks[2 * i], c = a.forks[2 * i + 1];
+    const int full = a.seq_lens[c] / a.page_size;
+    const int j1 = min(full, (static_cast<int>(blockIdx.y) + 1) * kShareSpan);
+    const int32_t* from = a.block_tables + p * a.bt_s0;
+    int32_t* to = a.block_tables + c * a.bt_s0;
+    int bad = 0;
+#pragma unroll 4
+    for (int j = blockIdx.y * kShareSpan + threadIdx.x; j < j1; j += kShareThreads) {
+        const int page = from[j];
+        to[j] = page;
+        if (page < 0 || page >= a.num_pages) bad = 1;
+        else atomicAdd(a.page_refs + page, 1);
+    }
+    if (bad) flag_error(a.err, PKV_FLAG_PAGE_RANGE);
+}
+
+template <bool FORK>
+cudaError_t launch_take(const TakeArgs& a, cudaStream_t s) {
+    auto kern = take_kernel<FORK>;
+    const size_t smem = (FORK ? 3 * static_cast<size_t>(a.n) + 1 : 2 * (static_cast<size_t>(a.n) + 1)) * 4;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    // One CTA counts 16,384 pages in one round of its loads; larger pools are
+    // spread over a cluster.
+    const unsigned C = a.num_pages <= 16384 ? 1 : kMaxCluster;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(C);
+    cfg.blockDim = dim3(kTakeThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+}  // namespace
+
+cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t s) {
+    if (a.B == 0) return cudaSuccess;
+    return launch_dependent(accept_kernel, dim3(a.B, std::max(a.n_caches, 1)), dim3(kAcceptThreads), 0, s, a);
+}
+
+cudaError_t launch_resize(const TakeArgs& a, cudaStream_t s) {
+    return a.n == 0 ? cudaSuccess : launch_take<false>(a, s);
+}
+
+cudaError_t launch_fork_take(const TakeArgs& a, cudaStream_t s) {
+    return a.n == 0 ? cudaSuccess : launch_take<true>(a, s);
+}
+
+cudaError_t launch_fork_share(const ShareArgs& a0, int32_t n, int32_t max_pages, bool tables, cudaStream_t s) {
+    if (n == 0) return cudaSuccess;
+    ShareArgs a = a0;
+    a.table_ctas = tables ? (max_pages + kShareSpan - 1) / kShareSpan : 0;
+    return launch_dependent(share_kernel, dim3(n, a.table_ctas + a.n_caches), dim3(kShareThreads), 0, s, a);
+}
+
+}  // namespace pkv

@@ -1233,4 +1233,352 @@ pkv_status pkv_stream_read(const void* buf, int64_t bytes, uint32_t* sink, int32
     return cuda_status(pkv::launch_stream_read(buf, bytes, sink, ctas, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// ---- drafted tokens, forks and resizes ------------------------------------------
+// i32 vector of n entries, contiguous
+static pkv_status check_i32(const pkv_tensor& t, int64_t n) {
+    if (!shape_ok(t, 1, PKV_I32) || t.shape[0] != n || (n > 0 && !t.ptr)) return PKV_ERR_INVALID_ARG;
+    return n > 1 && t.stride[0] != 1 ? PKV_ERR_UNSUPPORTED : PKV_OK;
+}
+
+// [B, width] i32 block tables with innermost stride 1
+static pkv_status check_tables(const pkv_tensor& t, int64_t* B, int64_t* max_pages) {
+    if (!shape_ok(t, 2, PKV_I32)) return PKV_ERR_INVALID_ARG;
+    *B = t.shape[0];
+    *max_pages = t.shape[1];
+    if (*B > 0 && (!t.ptr || *max_pages < 1)) return PKV_ERR_INVALID_ARG;
+    if (*max_pages > (int64_t{1} << 26) || *B > 0x7FFFFFFF) return PKV_ERR_UNSUPPORTED;
+    return *max_pages > 1 && t.stride[1] != 1 ? PKV_ERR_UNSUPPORTED : PKV_OK;
+}
+
+static bool overlap(const pkv_tensor& x, const pkv_tensor& y, int64_t bytes) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(x.ptr), q = reinterpret_cast<uintptr_t>(y.ptr);
+    return p < q + static_cast<uintptr_t>(bytes) && q < p + static_cast<uintptr_t>(bytes);
+}
+
+// One cache as rows to move: whole pages, or the rows of single tokens.
+static pkv_status pool_part(const pkv_tensor& t, int32_t layout, bool pages, int64_t* num_pages, int64_t* P,
+                            pkv::PoolPart* out) {
+    const int e = elem_bytes(t.dtype);
+    if (!e || (t.ndim != 3 && t.ndim != 4) || !t.ptr) return PKV_ERR_INVALID_ARG;
+    for (int i = 0; i < t.ndim; ++i)
+        if (t.shape[i] < 1 || t.stride[i] < 0) return PKV_ERR_INVALID_ARG;
+    const int tok = t.ndim == 4 && layout == PKV_HND ? 2 : 1;
+    const int last = t.ndim - 1;
+    if (t.shape[last] > 1 && t.stride[last] != 1) return PKV_ERR_UNSUPPORTED;
+    if (t.shape[0] > (int64_t{1} << 27) || t.shape[tok] > 65536) return PKV_ERR_UNSUPPORTED;
+    *num_pages = t.shape[0];
+    *P = t.shape[tok];
+    int64_t row = t.shape[last] * e, nt = t.shape[tok], st = t.stride[tok] * e, nh = 1, sh = 0;
+    if (t.ndim == 4) {
+        nh = t.shape[3 - tok];
+        sh = t.stride[3 - tok] * e;
+    }
+    if (row > (1 << 30) || nh > (1 << 30) || row * nh > (1 << 30) || row * nh * nt > (1 << 30))
+        return PKV_ERR_UNSUPPORTED;
+    if (nh == 1 || sh == row) {  // a token's heads are one row
+        row *= nh;
+        nh = 1;
+        sh = 0;
+    }
+    int64_t n0 = nt, s0 = st, n1 = nh, s1 = sh;
+    if (pages) {
+        if (n1 > 1 && s0 < s1) {
+            std::swap(n0, n1);
+            std::swap(s0, s1);
+        }
+        if (n1 == 1) {
+            n1 = n0;
+            s1 = s0;
+            n0 = 1;
+            s0 = 0;
+        }
+        if (s1 == row || n1 == 1) {
+            row *= n1;
+            n1 = 1;
+            s1 = 0;
+            if (s0 == row || n0 == 1) {
+                row *= n0;
+                n0 = 1;
+                s0 = 0;
+            }
+        }
+    }
+    out->p = static_cast<uint8_t*>(t.ptr);
+    out->s_page = t.stride[0] * e;
+    out->s0 = s0;
+    out->s1 = s1;
+    out->n0 = static_cast<int32_t>(n0);
+    out->n1 = static_cast<int32_t>(n1);
+    out->row = static_cast<int32_t>(row);
+    out->vec = 1;
+    const uint64_t all = reinterpret_cast<uint64_t>(t.ptr) | static_cast<uint64_t>(out->s_page) |
+                         static_cast<uint64_t>(s0) | static_cast<uint64_t>(s1) | static_cast<uint64_t>(row);
+    for (int v : {4, 8, 16})
+        if (all % v == 0) out->vec = v;
+    return PKV_OK;
+}
+
+// Every cache of a set; P and num_pages the same for all.
+static pkv_status check_pool(const pkv_tensor* caches, int32_t n, int32_t layout, bool pages, int64_t* num_pages,
+                             int64_t* P) {
+    if (layout != PKV_NHD && layout != PKV_HND) return PKV_ERR_INVALID_ARG;
+    if (n < 0 || (n > 0 && !caches)) return PKV_ERR_INVALID_ARG;
+    if (n > 4096) return PKV_ERR_UNSUPPORTED;
+    for (int i = 0; i < n; ++i) {
+        int64_t np, p;
+        pkv::PoolPart x;
+        pkv_status st = pool_part(caches[i], layout, pages, &np, &p, &x);
+        if (st != PKV_OK) return st;
+        if (i > 0 && (np != *num_pages || p != *P)) return PKV_ERR_INVALID_ARG;
+        *num_pages = np;
+        *P = p;
+    }
+    return PKV_OK;
+}
+
+pkv_status pkv_accept_drafts(const pkv_tensor* caches, int32_t n_caches, int32_t layout,
+                             const pkv_tensor* block_tables_p, const pkv_tensor* seq_lens_p,
+                             const pkv_tensor* q_start_p, const pkv_tensor* accepted_p,
+                             const pkv_tensor* num_accepted_p, const pkv_tensor* seq_lens_out_p, int32_t* err_flag,
+                             pkv_stream_t stream) {
+    const pkv_tensor& bt = arg(block_tables_p);
+    const pkv_tensor& sl = arg(seq_lens_p);
+    const pkv_tensor& qs = arg(q_start_p);
+    const pkv_tensor& ac = arg(accepted_p);
+    const pkv_tensor& na = arg(num_accepted_p);
+    const pkv_tensor& so = arg(seq_lens_out_p);
+    int64_t num_pages = 1, P = kPageSize, B, max_pages;
+    pkv_status st = check_pool(caches, n_caches, layout, false, &num_pages, &P);
+    if (st != PKV_OK) return st;
+    if ((st = check_tables(bt, &B, &max_pages)) != PKV_OK) return st;
+    if ((st = check_i32(sl, B)) != PKV_OK || (st = check_i32(qs, B + 1)) != PKV_OK ||
+        (st = check_i32(na, B)) != PKV_OK || (st = check_i32(so, B)) != PKV_OK)
+        return st;
+    if (!shape_ok(ac, 2, PKV_I32) || ac.shape[0] != B) return PKV_ERR_INVALID_ARG;
+    const int64_t A = ac.shape[1];
+    if (B * A > 0 && !ac.ptr) return PKV_ERR_INVALID_ARG;
+    if (A > pkv::kMaxAccepted || (A > 1 && ac.stride[1] != 1)) return PKV_ERR_UNSUPPORTED;
+    if (B == 0) return PKV_OK;
+    if (overlap(sl, so, 4 * B)) return PKV_ERR_INVALID_ARG;
+
+    pkv::AcceptArgs a{};
+    a.block_tables = static_cast<const int32_t*>(bt.ptr);
+    a.bt_s0 = bt.stride[0];
+    a.seq_lens = static_cast<const int32_t*>(sl.ptr);
+    a.q_start = static_cast<const int32_t*>(qs.ptr);
+    a.accepted = static_cast<const int32_t*>(ac.ptr);
+    a.ac_s0 = ac.stride[0];
+    a.n_accepted = static_cast<const int32_t*>(na.ptr);
+    a.seq_lens_out = static_cast<int32_t*>(so.ptr);
+    a.num_pages = num_pages;
+    a.max_pages = static_cast<int32_t>(max_pages);
+    a.page_size = static_cast<int32_t>(P);
+    a.B = static_cast<int32_t>(B);
+    a.A = static_cast<int32_t>(A);
+    a.err = err_flag;
+    int32_t done = 0;
+    do {
+        a.n_caches = std::min(n_caches - done, pkv::kMaxParts);
+        a.write_lens = done == 0;
+        for (int i = 0; i < a.n_caches; ++i) pool_part(caches[done + i], layout, false, &num_pages, &P, &a.c[i]);
+        const cudaError_t e = pkv::launch_accept(a, reinterpret_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess) return PKV_ERR_CUDA;
+        done += a.n_caches;
+    } while (done < n_caches);
+    return PKV_OK;
+}
+
+pkv_status pkv_resize_sequences(const pkv_tensor* block_tables_p, const pkv_tensor* page_counts_p,
+                                const pkv_tensor* new_lens_p, const pkv_tensor* page_refs_p, int32_t page_size,
+                                int32_t* err_flag, pkv_stream_t stream) {
+    const pkv_tensor& bt = arg(block_tables_p);
+    const pkv_tensor& pc = arg(page_counts_p);
+    const pkv_tensor& nl = arg(new_lens_p);
+    const pkv_tensor& pr = arg(page_refs_p);
+    int64_t B, max_pages;
+    pkv_status st = check_tables(bt, &B, &max_pages);
+    if (st != PKV_OK) return st;
+    if ((st = check_i32(pc, B)) != PKV_OK || (st = check_i32(nl, B)) != PKV_OK) return st;
+    if (pr.ndim != 1 || (st = check_i32(pr, pr.shape[0])) != PKV_OK) return st != PKV_OK ? st : PKV_ERR_INVALID_ARG;
+    if (page_size < 1) return PKV_ERR_INVALID_ARG;
+    if (page_size > 65536 || B > 16384 || pr.shape[0] > (int64_t{1} << 27)) return PKV_ERR_UNSUPPORTED;
+    pkv::TakeArgs a{};
+    a.block_tables = static_cast<int32_t*>(bt.ptr);
+    a.bt_s0 = bt.stride[0];
+    a.page_counts = static_cast<int32_t*>(pc.ptr);
+    a.page_refs = static_cast<int32_t*>(pr.ptr);
+    a.num_pages = pr.shape[0];
+    a.max_pages = static_cast<int32_t>(max_pages);
+    a.page_size = page_size;
+    a.n = static_cast<int32_t>(B);
+    a.rows = a.n;
+    a.new_lens = static_cast<const int32_t*>(nl.ptr);
+    a.err = err_flag;
+    return cuda_status(pkv::launch_resize(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_fork_sequences(const pkv_tensor* caches, int32_t n_caches, int32_t layout,
+                              const pkv_tensor* block_tables_p, const pkv_tensor* page_counts_p,
+                              const pkv_tensor* seq_lens_p, const pkv_tensor* forks_p, const pkv_tensor* page_refs_p,
+                              const pkv_tensor* copies_p, int32_t* err_flag, pkv_stream_t stream) {
+    const pkv_tensor& bt = arg(block_tables_p);
+    const pkv_tensor& pc = arg(page_counts_p);
+    const pkv_tensor& sl = arg(seq_lens_p);
+    const pkv_tensor& fk = arg(forks_p);
+    const pkv_tensor& pr = arg(page_refs_p);
+    const pkv_tensor& cp = arg(copies_p);
+    int64_t num_pages = 0, P = 0, R, max_pages;
+    if (n_caches < 1) return PKV_ERR_INVALID_ARG;
+    pkv_status st = check_pool(caches, n_caches, layout, true, &num_pages, &P);
+    if (st != PKV_OK) return st;
+    if ((st = check_tables(bt, &R, &max_pages)) != PKV_OK) return st;
+    if ((st = check_i32(pc, R)) != PKV_OK || (st = check_i32(sl, R)) != PKV_OK ||
+        (st = check_i32(pr, num_pages)) != PKV_OK)
+        return st;
+    for (const pkv_tensor* t : {&fk, &cp}) {
+        if (!shape_ok(*t, 2, PKV_I32) || t->shape[1] != 2 || t->shape[0] != fk.shape[0]) return PKV_ERR_INVALID_ARG;
+        if (t->shape[0] > 0 && !t->ptr) return PKV_ERR_INVALID_ARG;
+        if (t->shape[0] > 0 && (t->stride[1] != 1 || (t->shape[0] > 1 && t->stride[0] != 2)))
+            return PKV_ERR_UNSUPPORTED;
+    }
+    const int64_t n = fk.shape[0];
+    if (n > 16384) return PKV_ERR_UNSUPPORTED;
+    if (n == 0) return PKV_OK;
+    if (overlap(fk, cp, 8 * n)) return PKV_ERR_INVALID_ARG;
+    pkv::TakeArgs a{};
+    a.block_tables = static_cast<int32_t*>(bt.ptr);
+    a.bt_s0 = bt.stride[0];
+    a.page_counts = static_cast<int32_t*>(pc.ptr);
+    a.page_refs = static_cast<int32_t*>(pr.ptr);
+    a.num_pages = num_pages;
+    a.max_pages = static_cast<int32_t>(max_pages);
+    a.page_size = static_cast<int32_t>(P);
+    a.n = static_cast<int32_t>(n);
+    a.rows = static_cast<int32_t>(R);
+    a.forks = static_cast<const int32_t*>(fk.ptr);
+    a.seq_lens = static_cast<int32_t*>(sl.ptr);
+    a.copies = static_cast<int32_t*>(cp.ptr);
+    a.err = err_flag;
+    if (pkv::launch_fork_take(a, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return PKV_ERR_CUDA;
+    pkv::ShareArgs h{};
+    h.block_tables = a.block_tables;
+    h.bt_s0 = a.bt_s0;
+    h.seq_lens = a.seq_lens;
+    h.forks = a.forks;
+    h.copies = a.copies;
+    h.page_refs = a.page_refs;
+    h.num_pages = num_pages;
+    h.page_size = a.page_size;
+    h.err = err_flag;
+    for (int32_t done = 0; done < n_caches; done += h.n_caches) {
+        h.n_caches = std::min(n_caches - done, pkv::kMaxParts);
+        for (int i = 0; i < h.n_caches; ++i) pool_part(caches[done + i], layout, true, &num_pages, &P, &h.c[i]);
+        const cudaError_t e = pkv::launch_fork_share(h, a.n, a.max_pages, done == 0, reinterpret_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess) return PKV_ERR_CUDA;
+    }
+    return PKV_OK;
+}
+
+int64_t pkv_tree_decode_workspace(int64_t T, int32_t Hq, int32_t D, int32_t sm_count) {
+    if (T < 0 || T > 0x7FFFFFFF || Hq < 1 || Hq > (1 << 20) || (D != 64 && D != 128) || sm_count < 1 ||
+        sm_count > 4096)
+        return 0;
+    return pkv::tree_decode_workspace(T, Hq, D, sm_count);
+}
+
+pkv_status pkv_paged_tree_decode(const pkv_tensor* q_p, const pkv_tensor* k_cache_p, const pkv_tensor* v_cache_p,
+                                 const pkv_tensor* block_tables_p, const pkv_tensor* seq_lens_p,
+                                 const pkv_tensor* q_start_p, const pkv_tensor* tree_mask_p, float softmax_scale,
+                                 const pkv_tensor* out_p, const pkv_tensor* lse_out_p, void* workspace,
+                                 int64_t workspace_bytes, const pkv_tensor* k_scale_p, const pkv_tensor* v_scale_p,
+                                 int32_t layout, int32_t* err_flag, pkv_stream_t stream) {
+    const pkv_tensor& q = arg(q_p);
+    const pkv_tensor& kc = arg(k_cache_p);
+    const pkv_tensor& vc = arg(v_cache_p);
+    const pkv_tensor& bt = arg(block_tables_p);
+    const pkv_tensor& sl = arg(seq_lens_p);
+    const pkv_tensor& qs = arg(q_start_p);
+    const pkv_tensor& mask = arg(tree_mask_p);
+    const pkv_tensor& out = arg(out_p);
+    const pkv_tensor& lse = arg(lse_out_p);
+    const pkv_tensor& ks = arg(k_scale_p);
+    const pkv_tensor& vs = arg(v_scale_p);
+    int64_t num_pages, B, max_pages;
+    int P, Hkv, D;
+    pkv_status st = check_caches(kc, vc, layout, &num_pages, &P, &Hkv, &D);
+    if (st != PKV_OK) return st;
+    if (!shape_ok(q, 3, PKV_BF16) || q.shape[2] != D) return PKV_ERR_INVALID_ARG;
+    const int64_t T = q.shape[0], Hq = q.shape[1];
+    if (Hq < 1 || Hq % Hkv != 0) return PKV_ERR_INVALID_ARG;
+    if ((st = check_tables(bt, &B, &max_pages)) != PKV_OK) return st;
+    if ((st = check_i32(sl, B)) != PKV_OK || (st = check_i32(qs, B + 1)) != PKV_OK) return st;
+    if (!shape_ok(out, 3, PKV_BF16) || out.shape[0] != T || out.shape[1] != Hq || out.shape[2] != D)
+        return PKV_ERR_INVALID_ARG;
+    if (lse.ptr && (!shape_ok(lse, 2, PKV_F32) || lse.shape[0] != T || lse.shape[1] != Hq)) return PKV_ERR_INVALID_ARG;
+    if (mask.ptr && (!shape_ok(mask, 2, PKV_I32) || mask.shape[0] != T || mask.shape[1] < 1)) return PKV_ERR_INVALID_ARG;
+    if (!std::isfinite(softmax_scale)) return PKV_ERR_INVALID_ARG;
+    const int kind = kc.dtype == PKV_FP8_E4M3 ? pkv::kFp8 : pkv::kBf16;
+    int n_scale = 0;
+    if (kind != pkv::kBf16 && (st = check_scales(ks, vs, Hkv, &n_scale)) != PKV_OK) return st;
+    const int64_t G = Hq / Hkv;
+    if (P != kPageSize || G > 16 || B > 65535 || Hkv > 65535 || T > 0x7FFFFFFF / 16) return PKV_ERR_UNSUPPORTED;
+    if (T == 0 || B == 0) return PKV_OK;
+    if (!q.ptr || !out.ptr) return PKV_ERR_INVALID_ARG;
+    if (!row16(q, 2) || !row16(out, 2)) return PKV_ERR_UNSUPPORTED;
+    if (mask.ptr && (mask.shape[1] > 64 || (mask.shape[1] > 1 && mask.stride[1] != 1))) return PKV_ERR_UNSUPPORTED;
+    int sms = 0;
+    if (pkv::device_sm_count(&sms) != cudaSuccess) return PKV_ERR_CUDA;
+    if (!workspace || workspace_bytes < pkv::tree_decode_workspace(T, static_cast<int32_t>(Hq), D, sms))
+        return PKV_ERR_INVALID_ARG;
+    if (!aligned(workspace, 16)) return PKV_ERR_UNSUPPORTED;
+
+    CUtensorMap tk, tv;
+    if (!make_cache_map(&tk, kc, layout) || !make_cache_map(&tv, vc, layout)) return PKV_ERR_CUDA;
+    const int tok = layout == PKV_HND ? 2 : 1;
+    pkv::TreeArgs a{};
+    a.q = static_cast<const uint16_t*>(q.ptr);
+    a.q_s0 = q.stride[0];
+    a.q_s1 = q.stride[1];
+    a.k_cache = kc.ptr;
+    a.v_cache = vc.ptr;
+    a.kc_s0 = kc.stride[0];
+    a.kc_st = kc.stride[tok];
+    a.kc_sh = kc.stride[3 - tok];
+    a.vc_s0 = vc.stride[0];
+    a.vc_st = vc.stride[tok];
+    a.vc_sh = vc.stride[3 - tok];
+    a.block_tables = static_cast<const int32_t*>(bt.ptr);
+    a.bt_s0 = bt.stride[0];
+    a.max_pages = static_cast<int32_t>(max_pages);
+    a.seq_lens = static_cast<const int32_t*>(sl.ptr);
+    a.q_start = static_cast<const int32_t*>(qs.ptr);
+    if (mask.ptr) {
+        a.mask = static_cast<const uint32_t*>(mask.ptr);
+        a.mask_s0 = mask.stride[0];
+        a.W = static_cast<int32_t>(mask.shape[1]);
+    }
+    a.num_pages = num_pages;
+    a.scale_log2 = softmax_scale * 1.4426950408889634f;
+    a.k_scale = kind != pkv::kBf16 ? static_cast<const float*>(ks.ptr) : nullptr;
+    a.v_scale = kind != pkv::kBf16 ? static_cast<const float*>(vs.ptr) : nullptr;
+    a.n_scale = n_scale;
+    a.out = static_cast<uint16_t*>(out.ptr);
+    a.o_s0 = out.stride[0];
+    a.o_s1 = out.stride[1];
+    a.lse = static_cast<float*>(lse.ptr);
+    a.l_s0 = lse.ptr ? lse.stride[0] : 0;
+    a.l_s1 = lse.ptr ? lse.stride[1] : 0;
+    a.workspace = workspace;
+    a.T = static_cast<int32_t>(T);
+    a.B = static_cast<int32_t>(B);
+    a.Hq = static_cast<int32_t>(Hq);
+    a.Hkv = Hkv;
+    a.D = D;
+    a.G = static_cast<int32_t>(G);
+    a.kind = kind;
+    a.layout = layout;
+    a.err = err_flag;
+    return cuda_status(pkv::launch_tree_decode(a, tk, tv, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

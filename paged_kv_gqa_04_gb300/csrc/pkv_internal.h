@@ -173,6 +173,95 @@ struct ValidateArgs {
     int32_t* err;
 };
 
+// One cache as the page and row movers see it: pages s_page bytes apart, a
+// page n0 x n1 rows of `row` bytes at steps of s0 and s1, moved in units of
+// `vec` bytes (a power of two up to 16 that divides them all). For token moves
+// n0 x s0 are the tokens of a page.
+struct PoolPart {
+    uint8_t* p;
+    int64_t s_page, s0, s1;
+    int32_t n0, n1, row, vec;
+};
+constexpr int kMaxParts = 64;         // caches per launch (a larger set takes more launches)
+constexpr int kMaxAccepted = 1024;    // accepted tokens per sequence
+
+struct AcceptArgs {
+    const int32_t* block_tables;
+    int64_t bt_s0;
+    const int32_t* seq_lens;
+    const int32_t* q_start;
+    const int32_t* accepted;
+    int64_t ac_s0;
+    const int32_t* n_accepted;
+    int32_t* seq_lens_out;
+    int64_t num_pages;
+    int32_t max_pages, page_size, B, A, n_caches;
+    int32_t write_lens;        // this launch writes seq_lens_out and the flags
+    int32_t* err;
+    PoolPart c[kMaxParts];
+};
+
+// A resize (n rows; new_lens) or the first half of a fork (n forks of `rows`
+// rows; forks, seq_lens, copies).
+struct TakeArgs {
+    int32_t* block_tables;
+    int64_t bt_s0;
+    int32_t* page_counts;
+    int32_t* page_refs;
+    int64_t num_pages;
+    int32_t max_pages, page_size, n, rows;
+    const int32_t* new_lens;
+    const int32_t* forks;
+    int32_t* seq_lens;
+    int32_t* copies;
+    int32_t* err;
+};
+
+struct ShareArgs {
+    int32_t* block_tables;
+    int64_t bt_s0;
+    const int32_t* seq_lens;
+    const int32_t* forks;
+    const int32_t* copies;
+    int32_t* page_refs;
+    int64_t num_pages;
+    int32_t page_size, n_caches;
+    int32_t table_ctas;        // CTAs per fork that copy table entries (set by the launcher)
+    int32_t* err;
+    PoolPart c[kMaxParts];
+};
+
+struct TreeArgs {
+    const uint16_t* q;         // [T, Hq, D] bf16 bits
+    int64_t q_s0, q_s1;
+    const void* k_cache;
+    const void* v_cache;
+    int64_t kc_s0, kc_st, kc_sh;  // element strides: page, token, head
+    int64_t vc_s0, vc_st, vc_sh;
+    const int32_t* block_tables;
+    int64_t bt_s0;
+    int32_t max_pages;
+    const int32_t* seq_lens;
+    const int32_t* q_start;    // [B + 1]
+    const uint32_t* mask;      // [T, W] words, null = chain
+    int64_t mask_s0;
+    int32_t W;
+    int64_t num_pages;
+    float scale_log2;          // softmax_scale * log2(e)
+    const float* k_scale;      // fp8 only
+    const float* v_scale;
+    int32_t n_scale;
+    uint16_t* out;             // [T, Hq, D] bf16 bits
+    int64_t o_s0, o_s1;
+    float* lse;                // [T, Hq], may be null
+    int64_t l_s0, l_s1;
+    void* workspace;
+    int32_t T, B, Hq, Hkv, D, G;
+    int32_t kind;              // CacheKind
+    int32_t layout;
+    int32_t* err;
+};
+
 // Launch as a programmatic dependent of the preceding work in the stream:
 // the kernel may start while the preceding kernel finishes, and orders its
 // reads and writes of data that kernel touches after griddepcontrol.wait.
@@ -207,6 +296,13 @@ cudaError_t static_slot_bitmap(uint32_t** ptr, int64_t* words);
 cudaError_t launch_stream_read(const void* buf, int64_t bytes, uint32_t* sink, int ctas, cudaStream_t s);
 cudaError_t launch_copy(void* dst, const void* src, int64_t bytes, cudaStream_t s);
 cudaError_t launch_selftest_wait(uint64_t limit_ns, int32_t* err, uint64_t* elapsed_ns, cudaStream_t s);
+
+cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t s);
+cudaError_t launch_resize(const TakeArgs& a, cudaStream_t s);
+cudaError_t launch_fork_take(const TakeArgs& a, cudaStream_t s);
+cudaError_t launch_fork_share(const ShareArgs& a, int32_t n, int32_t max_pages, bool tables, cudaStream_t s);
+cudaError_t launch_tree_decode(const TreeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s);
+int64_t tree_decode_workspace(int64_t T, int32_t Hq, int32_t D, int32_t sm_count);
 
 // Occupancy-related constants of the decode kernel, shared with the split
 // heuristic on the host.
