@@ -99,6 +99,22 @@ bool make_cache_map(CUtensorMap* m, const pkv_tensor& c, int32_t layout) {
     return r == CUDA_SUCCESS;
 }
 
+// Tile map over q [T, Hq, D] bf16: one box = 128 / G tokens x the G heads of a
+// kv head x 64 values, 128-byte swizzle -- consecutive operand rows.
+bool make_q_map(CUtensorMap* m, const pkv_tensor& q, int G) {
+    auto enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(q.shape[2]), static_cast<cuuint64_t>(q.shape[1]),
+                          static_cast<cuuint64_t>(q.shape[0])};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(q.stride[1] * 2), static_cast<cuuint64_t>(q.stride[0] * 2)};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(128 / G)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q.ptr, dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 // Tile map over an MLA cache [pages, P, W] (W = 512 E4M3 bytes of ckv or 64
 // bf16 values of kpe): one box = the 64 token rows of a page x 128 bytes,
 // 128-byte swizzle.
@@ -1532,8 +1548,9 @@ pkv_status pkv_paged_tree_decode(const pkv_tensor* q_p, const pkv_tensor* k_cach
         return PKV_ERR_INVALID_ARG;
     if (!aligned(workspace, 16)) return PKV_ERR_UNSUPPORTED;
 
-    CUtensorMap tk, tv;
-    if (!make_cache_map(&tk, kc, layout) || !make_cache_map(&tv, vc, layout)) return PKV_ERR_CUDA;
+    CUtensorMap tq, tk, tv;
+    if (!make_q_map(&tq, q, static_cast<int>(G)) || !make_cache_map(&tk, kc, layout) || !make_cache_map(&tv, vc, layout))
+        return PKV_ERR_CUDA;
     const int tok = layout == PKV_HND ? 2 : 1;
     pkv::TreeArgs a{};
     a.q = static_cast<const uint16_t*>(q.ptr);
@@ -1575,10 +1592,11 @@ pkv_status pkv_paged_tree_decode(const pkv_tensor* q_p, const pkv_tensor* k_cach
     a.Hkv = Hkv;
     a.D = D;
     a.G = static_cast<int32_t>(G);
+    a.tile_toks = 128 / a.G;
     a.kind = kind;
     a.layout = layout;
     a.err = err_flag;
-    return cuda_status(pkv::launch_tree_decode(a, tk, tv, reinterpret_cast<cudaStream_t>(stream)));
+    return cuda_status(pkv::launch_tree_decode(a, tq, tk, tv, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

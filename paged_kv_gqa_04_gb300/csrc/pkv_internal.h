@@ -257,6 +257,7 @@ struct TreeArgs {
     int64_t l_s0, l_s1;
     void* workspace;
     int32_t T, B, Hq, Hkv, D, G;
+    int32_t tile_toks;         // tokens per row tile: 128 / G
     int32_t kind;              // CacheKind
     int32_t layout;
     int32_t* err;
@@ -301,7 +302,8 @@ cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t s);
 cudaError_t launch_resize(const TakeArgs& a, cudaStream_t s);
 cudaError_t launch_fork_take(const TakeArgs& a, cudaStream_t s);
 cudaError_t launch_fork_share(const ShareArgs& a, int32_t n, int32_t max_pages, bool tables, cudaStream_t s);
-cudaError_t launch_tree_decode(const TreeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s);
+cudaError_t launch_tree_decode(const TreeArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               cudaStream_t s);
 int64_t tree_decode_workspace(int64_t T, int32_t Hq, int32_t D, int32_t sm_count);
 
 // Occupancy-related constants of the decode kernel, shared with the split

@@ -2,13 +2,13 @@
 // fifth-generation tensor cores: the context in full, the drafted tokens under
 // a tree mask or as a chain.
 //
-// Rows. The N drafted tokens of a sequence and the G query heads of a kv head
-// share the same K and V: row r = i G + g of (sequence, kv head) is head g of
-// token i. With rows on the M side of the MMA (128 tensor-memory lanes), one
-// pass over K and V serves up to 256 rows, a softmax thread owns one row, and
-// its maximum and sum need no exchange.
+// Rows. The drafted tokens of a sequence and the G query heads of a kv head
+// share the same K and V. A row tile is 128 / G tokens (rounded down) times G
+// heads on the M side of the MMA (128 tensor-memory lanes), so q lands in
+// operand layout by TMA, a softmax thread owns one row, and its maximum and
+// sum need no exchange. One pass over K and V serves two row tiles.
 //
-// Work. An item is (sequence, kv head, group of 256 rows); a unit is one tile
+// Work. An item is (sequence, kv head, pair of row tiles); a unit is one tile
 // of 128 positions of one item. All units of the batch, in order, are cut into
 // equal stretches, one per CTA (one CTA per SM): every CTA streams the same
 // number of tiles whatever the lengths are, with no plan from the host. Each
@@ -17,19 +17,22 @@
 // item, the start of another), which a second kernel joins.
 //
 // A CTA's roles, per tile:
-//   warp 0        TMA tile loads of K and V (16 rows x 128 bytes a copy) into a
-//                 ring; pages that do not exist are read out of range, which
-//                 fills zeros
+//   warp 0        TMA tile loads of q (per item) and K into the rings
+//   warp 2        TMA tile loads of V (a warp starts a 16-row x 128-byte copy
+//                 in about 85 cycles: one warp for both would be the limit).
+//                 Pages that do not exist are read out of range, which fills
+//                 zeros
 //   warp 1        S = Q . K^T and O += P . V (M = 128; P from tensor memory, V
 //                 as an MN-major operand: nothing is transposed)
 //   warps 4 - 7,
 //   warps 8 - 11  two softmax groups, each with S, P and O of its own in tensor
-//                 memory. Up to 128 rows: both have the same rows and take the
+//                 memory. One row tile: both have the same rows and take the
 //                 tiles in turn, and their sums are joined at the end (either
-//                 group reads the other's O directly). Past 128: each has its
-//                 own 128 rows of every tile. While one group is in its softmax
-//                 the tensor cores work for the other.
-//   warps 12 - 15 FP8 caches: E4M3 bytes to f16 operand tiles (exact)
+//                 group reads the other's O directly). Two: each has its own
+//                 row tile, and every tile. While one group is in its softmax
+//                 the tensor cores work for the other; the next item's first
+//                 scores are computed while the item before writes its output.
+//   warps 12 - 15 FP8 caches: E4M3 bytes to f16 operand tiles (exact), q too
 //
 // The online softmax keeps a reference maximum per row that moves only when a
 // tile's maximum passes it by more than 8 (log2), so P <= 2^8 and O is scaled
@@ -46,6 +49,7 @@
 // Waits are bounded (about one second): a role that gives up sets
 // PKV_FLAG_WAIT_TIMEOUT and a CTA-wide flag that ends the others' waits.
 #include <algorithm>
+#include <type_traits>
 
 #include "pkv_internal.h"
 #include "pkv_ptx.cuh"
@@ -54,7 +58,7 @@ namespace pkv {
 namespace {
 
 constexpr int kTile = 128;    // positions per tile
-constexpr int kRows = 256;    // rows per item
+constexpr int kRows = 256;    // rows (lanes of two row tiles) per item
 constexpr int kTilePages = kTile / kPageSize;
 constexpr int kSnap = 2;      // no piece of a cut item is shorter than this many tiles
 constexpr int kMinUnits = 2;  // units per CTA before another CTA is used
@@ -69,51 +73,53 @@ struct Cfg {
     static constexpr int BLOCK = kTile * 128;              // one column block of it
     static constexpr int RAW = kTile * D;                  // FP8 tile as it lands
     static constexpr int RBOX = D >= 128 ? 128 : D;        // its row (and swizzle span)
-    static constexpr int ST = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);  // operand ring
-    static constexpr int RST = FP8 ? (D == 128 ? 3 : 6) : 0;                  // raw ring
+    // Rings of K tiles and of V tiles: operand tiles, and (FP8) tiles of bytes.
+    static constexpr int ST = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
+    static constexpr int RST = FP8 ? (D == 128 ? 3 : 6) : 0;
     static constexpr int THREADS = FP8 ? 512 : 384;
-    static constexpr int OFF_Q = 0;
+    // Registers a thread: launched with 168 (128), dealt out again by role.
+    static constexpr int REG_IO = 88, REG_SM = FP8 ? 168 : 208, REG_CV = 88;
+    static constexpr int OFF_Q = 0;                        // two row tiles of q
     static constexpr int OFF_T = OFF_Q + 2 * TILE;
     static constexpr int OFF_R = OFF_T + ST * TILE;
-    static constexpr int OFF_SC = OFF_R + RST * RAW;       // FP8: [256] floats, 2^-k of each row
+    static constexpr int OFF_SC = OFF_R + RST * RAW;       // FP8: [2][128] floats, 2^-k of each row
     static constexpr int OFF_BAR = OFF_SC + (FP8 ? kRows * 4 : 0);
-    static constexpr int NBAR = 2 * ST + 2 * RST + 7;
+    static constexpr int NBAR = 2 * ST + 2 * RST + 13;
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
     static constexpr int SMEM = OFF_MISC + 256 + 1024;     // + alignment slack
     static_assert(SMEM <= 232448, "shared memory of one CTA");
+    static_assert(FP8 ? REG_IO + 2 * REG_SM + REG_CV <= 512 : REG_IO + 2 * REG_SM <= 504, "registers as launched");
     // tensor-memory columns of a softmax group: S (P over it, or beside it where O leaves room), then O
     static constexpr uint32_t P_COL = D == 64 ? 192 : 0;
+    static constexpr uint32_t ML_COL = 64;                 // m and l for the other group, once S is read
     static constexpr uint32_t O_COL = 128;
 };
 
 struct Seq {
-    int q0, N, L, ctx, R, RG;
+    int q0, N, L, ctx, RG;
 };
 // Sequence b, its values clamped; `flags` collects what was out of range.
 __device__ __forceinline__ Seq seq_of(const TreeArgs& a, int b, int& flags) {
     Seq s;
     const int q0 = __ldg(a.q_start + b), q1 = __ldg(a.q_start + b + 1);
+    const int L = __ldg(a.seq_lens + b);
     s.q0 = min(max(q0, 0), a.T);
     const int e = min(max(q1, s.q0), a.T);
     if (s.q0 != q0 || e != q1) flags |= PKV_FLAG_DRAFT_RANGE;
     s.N = e - s.q0;
-    const int cap = a.max_pages * kPageSize;
-    const int L = __ldg(a.seq_lens + b);
-    s.L = min(max(L, 0), cap);
+    s.L = min(max(L, 0), a.max_pages * kPageSize);
     if (s.N > 0) {
         if (s.L != L) flags |= PKV_FLAG_SEQ_LEN_RANGE;
         if (s.N > s.L || (a.mask != nullptr && s.N > 32 * a.W)) flags |= PKV_FLAG_DRAFT_RANGE;
     }
     s.ctx = s.L - s.N;
-    s.R = s.N * a.G;
-    s.RG = (s.R + kRows - 1) / kRows;
+    s.RG = s.N <= 2 * a.tile_toks ? (s.N > 0) : (s.N + 2 * a.tile_toks - 1) / (2 * a.tile_toks);
     return s;
 }
-// Positions that row group rg can see (a chain's earlier rows see less), and its tiles (at least one: a row
-// that sees nothing has an output).
+// Positions that pair rg of row tiles can see (a chain's earlier rows see less), and its tiles (at least one: a
+// row that sees nothing has an output).
 __device__ __forceinline__ int kv_end(const TreeArgs& a, const Seq& s, int rg) {
-    if (a.mask != nullptr) return s.L;
-    return min(s.L, s.ctx + (min(s.R, (rg + 1) * kRows) - 1) / a.G + 1);
+    return a.mask != nullptr ? s.L : min(s.L, s.ctx + min(s.N, (rg + 1) * 2 * a.tile_toks));
 }
 __device__ __forceinline__ int tiles_of(const TreeArgs& a, const Seq& s, int rg) {
     return max((kv_end(a, s, rg) + kTile - 1) / kTile, 1);
@@ -154,12 +160,16 @@ __device__ __forceinline__ Place place_of(const TreeArgs& a, const Seq& s, int b
 
 // The pieces of items between two places, in order. Every role walks them by itself.
 struct Walk {
-    int b, k, t0, t1, nt, kvh, rg, rows;
+    int b, k, t0, t1, nt, kvh, tok0, toks;  // piece [t0, t1) of nt tiles; drafted tokens [tok0, tok0 + toks)
     Seq s;
     Place end;
-    bool first;
-    __device__ __forceinline__ Walk(const Place& from, const Place& to) : b(from.b), k(from.k), t0(from.t), end(to), first(true) {}
-    // Next piece [t0, t1) of item (b, k); false at the end.
+    int piece;                              // its number in this CTA
+    int uses0, uses1;                       // earlier items in each buffer of q
+    int buf;                                // its buffer (one row tile; two row tiles take both)
+    bool two, first;
+    __device__ __forceinline__ Walk(const Place& from, const Place& to)
+        : b(from.b), k(from.k), t0(from.t), end(to), piece(-1), uses0(0), uses1(0), buf(1), two(false), first(true) {}
+    // The next piece; false at the end.
     __device__ __forceinline__ bool next(const TreeArgs& a) {
         int ignored = 0;
         if (first) {
@@ -167,6 +177,8 @@ struct Walk {
             first = false;
             s = seq_of(a, b, ignored);
         } else {
+            uses0 += two || buf == 0;
+            uses1 += two || buf == 1;
             t0 = 0;
             ++k;
         }
@@ -178,15 +190,25 @@ struct Walk {
             s = seq_of(a, b, ignored);
         }
         if (!in_range()) return false;
-        kvh = k / s.RG;
-        rg = k - kvh * s.RG;
-        rows = min(s.R - rg * kRows, kRows);
+        kvh = s.RG == 1 ? k : k / s.RG;
+        const int rg = k - kvh * s.RG;
+        tok0 = rg * 2 * a.tile_toks;
+        toks = min(s.N - tok0, 2 * a.tile_toks);
+        two = toks > a.tile_toks;
+        if (!two) buf ^= 1;
         nt = tiles_of(a, s, rg);
         t1 = b == end.b && k == end.k ? end.t : nt;
+        ++piece;
         return true;
     }
     __device__ __forceinline__ bool in_range() const {
         return b < end.b || (b == end.b && (k < end.k || (k == end.k && end.t > t0)));
+    }
+    // q's buffers of this piece: fn(buffer, uses of it before)
+    template <typename F>
+    __device__ __forceinline__ void buffers(F fn) const {
+        if (two || buf == 0) fn(0, uses0);
+        if (two || buf == 1) fn(1, uses1);
     }
 };
 
@@ -202,16 +224,64 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         : "r"(taddr)
         : "memory");
 }
-// D (tensor memory) = A (tensor memory) . B^T (+ D): 16-bit A, two values per 32-bit column.
-__device__ __forceinline__ void umma_f16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                                 uint32_t accumulate) {
+// The values of a tensor-memory load are used only past this point (which follows its wait).
+template <int N>
+__device__ __forceinline__ void pin(uint32_t (&r)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+// One thread's MMA and commit (the warp forms elect a lane at each call).
+// D (tensor memory) = A . B^T (+ D), both operands in shared memory.
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// A in tensor memory: 16-bit values, two per 32-bit column.
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void umma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// Lane-wise fma and add of two floats.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 w, x, y;\n\t"
+        "mov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ uint16_t lo16(uint32_t w) { return static_cast<uint16_t>(w & 0xFFFFu); }
+__device__ __forceinline__ uint16_t hi16(uint32_t w) { return static_cast<uint16_t>(w >> 16); }
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+// v[k] without an array in local memory
+__device__ __forceinline__ uint32_t word_of(const uint32_t (&v)[4], int k) {
+    return k == 0 ? v[0] : k == 1 ? v[1] : k == 2 ? v[2] : v[3];
+}
 
 // Workspace of partial sums: [2 per CTA][256 rows] of {m, l}, then of D floats.
 __device__ __forceinline__ float* part_ml(void* ws, int slot, int row) {
@@ -226,19 +296,22 @@ __device__ __forceinline__ float* part_o(void* ws, int ctas, int slot, int row) 
 
 template <int D, bool FP8>
 __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
-    tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const TreeArgs a) {
+    tree_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                const __grid_constant__ CUtensorMap tmv, const TreeArgs a) {
     using C = Cfg<D, FP8>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t s0 = smem_u32(smem);
     enum : int { bFull = 0, bFree = C::ST, bRawFull = 2 * C::ST, bRawFree = bRawFull + C::RST, bS = bRawFree + C::RST,
-                 bP = bS + 2, bO = bP + 2, bQ = bO + 2 };
+                 bP = bS + 2, bO = bP + 2, bQ = bO + 2, bQFree = bQ + 2, bQRaw = bQFree + 2, bX = bQRaw + 2 };
+    static_assert(bX + 1 == C::NBAR, "barriers");
     auto bar = [&](int i) -> uint32_t { return s0 + C::OFF_BAR + 8 * i; };
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
     uint32_t* bad_tok = misc + 4;                         // [2 jobs][2 groups][4 words]: drafted tokens, V not finite
     Place* place = reinterpret_cast<Place*>(misc + 20);   // [2]: this CTA's first unit and the one past its last
     int64_t* warp_units = reinterpret_cast<int64_t*>(misc + 26);  // [16]
+    float* q_scale = reinterpret_cast<float*>(smem + C::OFF_SC);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t num_pages = a.num_pages;
@@ -256,11 +329,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             mbar_init(bar(bS + w), 1);
             mbar_init(bar(bP + w), 4);
             mbar_init(bar(bO + w), 1);
+            mbar_init(bar(bQ + w), FP8 ? 4 : 1);
+            mbar_init(bar(bQFree + w), FP8 ? 9 : 1);  // the last Q . K^T; FP8: the row scales are read
+            mbar_init(bar(bQRaw + w), 1);
         }
-        mbar_init(bar(bQ), 8);
+        mbar_init(bar(bX), 8);
         *abort_flag = 0;
         place[0] = place[1] = Place{a.B, 0, 0};
         fence_mbar_init();
+        tma_prefetch_desc(&tmq);
         tma_prefetch_desc(&tmk);
         tma_prefetch_desc(&tmv);
     }
@@ -325,6 +402,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         *abort_flag = 1;
         flag_error(a.err, PKV_FLAG_WAIT_TIMEOUT);
     };
+    auto lane_wait = [&](uint32_t bb, uint32_t par) -> bool {
+        const bool r = mbar_wait_or_abort(bb, par, abort_flag, kWaitLimitNs);
+        if (!r) give_up();
+        return r;
+    };
     auto warp_wait = [&](uint32_t bb, uint32_t par) -> bool {
         const bool r = __all_sync(0xffffffffu, mbar_wait_or_abort(bb, par, abort_flag, kWaitLimitNs));
         if (!r && lane == 0) give_up();
@@ -335,33 +417,49 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     auto stage = [](int n) { return n % C::ST; };
     auto phase = [](int n) -> uint32_t { return (n / C::ST) & 1; };
 
-    if (warp == 0) {
-        // ======================= copies ===========================================
-        constexpr int RING = FP8 ? C::RST : C::ST;
-        constexpr int FULL = FP8 ? bRawFull : bFull, FREE = FP8 ? bRawFree : bFree;
-        constexpr int COPIES = FP8 ? kTilePages : kTilePages * C::NB;  // per tile of K or V
-        const int pg = lane % kTilePages, blk = lane / kTilePages;     // this lane's copy
-        int n = 0;
-        bool ok = true;
-        Walk w(from, to);
-        while (ok && w.next(a)) {
-            // evict-first: one read of the cache serves all rows, unless the item has several row groups
+    if (warp < 4) {
+        reg_dec<C::REG_IO>();
+        if (warp == 0 || warp == 2) {
+            // ======================= copies ===========================================
+            const int v = warp >> 1;                                       // K (and q) or V
+            constexpr int RING = FP8 ? C::RST : C::ST;
+            constexpr int FULL = FP8 ? bRawFull : bFull, FREE = FP8 ? bRawFree : bFree;
+            constexpr int COPIES = FP8 ? kTilePages : kTilePages * C::NB;  // per tile
+            const int pg = lane % kTilePages, blk = lane / kTilePages;     // this lane's copy
+            const bool hnd = a.layout == PKV_HND;
             const uint64_t policy = l2_policy_evict_first();
-            const int npages = (w.s.L + kPageSize - 1) / kPageSize;
-            auto page_at = [&](int t) -> int {
-                const int p = t * kTilePages + pg;
-                return p < npages && t < w.t1 ? __ldg(a.block_tables + w.b * a.bt_s0 + p) : -1;
-            };
-            int nxt = page_at(w.t0);
-            bool bad = false;
-            for (int t = w.t0; ok && t < w.t1; ++t) {
-                int id = nxt;
-                nxt = page_at(t + 1);
-                if (id < 0 || id >= num_pages) {
-                    bad |= t * kTilePages + pg < npages;
-                    id = static_cast<int>(num_pages);  // out of range: the copy fills zeros
+            int n = v, q_done0 = 0, q_done1 = 0;
+            bool ok = true;
+            Walk w(from, to);
+            while (ok && w.next(a)) {
+                const int npages = (w.s.L + kPageSize - 1) / kPageSize;
+                auto page_at = [&](int t) -> int {
+                    const int p = t * kTilePages + pg;
+                    return p < npages && t < w.t1 ? __ldg(a.block_tables + w.b * a.bt_s0 + p) : -1;
+                };
+                int nxt = page_at(w.t0);
+                if (v == 0) {
+                    // q: tile_toks tokens x G heads are consecutive operand rows
+                    w.buffers([&](int bf, int uses) {
+                        if (uses > 0) ok = ok && warp_wait(bar(bQFree + bf), (uses - 1) & 1);
+                        const uint32_t fb = bar((FP8 ? bQRaw : bQ) + bf);
+                        if (ok && lane == 0) mbar_arrive_expect_tx(fb, a.tile_toks * a.G * D * 2);
+                        __syncwarp();
+                        if (ok && lane < C::NB)
+                            tma_load_3d(s0 + C::OFF_Q + bf * C::TILE + lane * C::BLOCK, &tmq, fb, 64 * lane, w.kvh * a.G,
+                                        w.s.q0 + w.tok0 + (w.two ? bf * a.tile_toks : 0), policy);
+                        if (ok) ++(bf ? q_done1 : q_done0);
+                        __syncwarp();
+                    });
                 }
-                for (int v = 0; v < 2; ++v, ++n) {
+                bool bad = false;
+                for (int t = w.t0; ok && t < w.t1; ++t, n += 2) {
+                    int id = nxt;
+                    nxt = page_at(t + 1);
+                    if (id < 0 || id >= num_pages) {
+                        bad |= t * kTilePages + pg < npages;
+                        id = static_cast<int>(num_pages);  // out of range: the copy fills zeros
+                    }
                     const int st = n % RING;
                     if (n >= RING && !warp_wait(bar(FREE + st), (n / RING - 1) & 1)) {
                         ok = false;
@@ -373,144 +471,125 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     if (lane < COPIES) {
                         const uint32_t dst = FP8 ? s0 + C::OFF_R + st * C::RAW + pg * kPageSize * C::RBOX
                                                  : s0 + C::OFF_T + st * C::TILE + blk * C::BLOCK + pg * kPageSize * 128;
-                        const bool hnd = a.layout == PKV_HND;
                         tma_load_4d(dst, v ? &tmv : &tmk, fb, FP8 ? 0 : blk * 64, hnd ? 0 : w.kvh, hnd ? w.kvh : 0, id,
                                     policy);
                     }
                     __syncwarp();
                 }
+                if (bad && blk == 0 && v == 0) flag_error(a.err, PKV_FLAG_PAGE_RANGE);
             }
-            if (bad && blk == 0) flag_error(a.err, PKV_FLAG_PAGE_RANGE);
+            // Copies under way land before the CTA may exit.
+            if (lane == 0) {
+                // (slots whose stage neither copy warp has taken again)
+                for (int i = n - 2; i >= 0 && i > n - 1 - v - RING; i -= 2)
+                    (void)mbar_wait_bounded(bar(FULL + i % RING), (i / RING) & 1, kWaitLimitNs);
+                if (q_done0) (void)mbar_wait_bounded(bar(FP8 ? bQRaw : bQ), (q_done0 - 1) & 1, kWaitLimitNs);
+                if (q_done1) (void)mbar_wait_bounded(bar((FP8 ? bQRaw : bQ) + 1), (q_done1 - 1) & 1, kWaitLimitNs);
+            }
+        } else if (warp == 1 && lane == 0) {
+            // ======================= tensor-core issue (one thread) ===================
+            constexpr int FMT = FP8 ? 0 : 1;  // f16 or bf16 operands
+            // the sign of softmax_scale goes into q (bit 13 negates A)
+            const uint32_t idesc_qk = umma_idesc(128, kTile, FMT, FMT, false, false) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
+            constexpr uint32_t kIdescPv = umma_idesc(128, D, FMT, FMT, false, true);
+            int tile0 = 0;                             // tiles before this piece
+            int pv0 = 0, pv1 = 0, qk0 = 0, qk1 = 0;    // P . V and Q . K^T issued per group
+            bool ok = true;
+            Walk w(from, to);
+            while (ok && w.next(a)) {
+                const int nt = w.t1 - w.t0, nj = w.two ? 2 * nt : nt;
+                auto qk = [&](int j) -> bool {
+                    const int g = j & 1, n = 2 * (tile0 + (w.two ? j >> 1 : j));
+                    if (!lane_wait(bar(bFull + stage(n)), phase(n))) return false;
+                    tc_fence_after();
+                    const uint64_t q = umma_desc_sw128(s0 + C::OFF_Q + (w.two ? g : w.buf) * C::TILE, 16, 1024);
+                    const uint64_t kt = umma_desc_sw128(s0 + C::OFF_T + stage(n) * C::TILE, 16, 1024);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t step = ((k >> 2) * C::BLOCK + (k & 3) * 32) >> 4;
+                        umma_ss(tmem + 256 * g, q + step, kt + step, idesc_qk, k > 0);
+                    }
+                    umma_commit(bar(bS + g));
+                    if (!w.two || g == 1) umma_commit(bar(bFree + stage(n)));
+                    ++(g ? qk1 : qk0);
+                    return true;
+                };
+                auto pv = [&](int j) -> bool {
+                    const int g = j & 1, n = 2 * (tile0 + (w.two ? j >> 1 : j)) + 1;
+                    if (!lane_wait(bar(bFull + stage(n)), phase(n))) return false;
+                    if (!lane_wait(bar(bP + g), (g ? pv1 : pv0) & 1)) return false;
+                    tc_fence_after();
+                    const uint64_t vt = umma_desc_sw128(s0 + C::OFF_T + stage(n) * C::TILE, C::BLOCK, 1024);
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        umma_ts(tmem + 256 * g + C::O_COL, tmem + 256 * g + C::P_COL + 8 * k, vt + k * (2048 >> 4), kIdescPv,
+                                j > 1 || k > 0);
+                    umma_commit(bar(bO + g));
+                    if (!w.two || g == 1) umma_commit(bar(bFree + stage(n)));
+                    ++(g ? pv1 : pv0);
+                    return true;
+                };
+                w.buffers([&](int bf, int uses) { ok = ok && lane_wait(bar(bQ + bf), uses & 1); });
+                // the item before has no more use for S
+                if (w.piece > 0) ok = ok && lane_wait(bar(bX), (w.piece - 1) & 1);
+                ok = ok && qk(0) && (nj < 2 || qk(1));
+                if (ok && nj <= 2) w.buffers([&](int bf, int) { umma_commit(bar(bQFree + bf)); });
+                for (int j = 0; ok && j < nj; ++j) {
+                    ok = pv(j) && (j + 2 >= nj || qk(j + 2));
+                    if (ok && j + 2 == nj - 1) w.buffers([&](int bf, int) { umma_commit(bar(bQFree + bf)); });
+                }
+                tile0 += nt;
+            }
+            // Every operation issued is done before the tensor memory is freed:
+            // the softmax groups wait for their last O, and give-ups for both here.
+            if (!ok) {
+                if (qk0) (void)mbar_wait_bounded(bar(bS), (qk0 - 1) & 1, kWaitLimitNs);
+                if (qk1) (void)mbar_wait_bounded(bar(bS + 1), (qk1 - 1) & 1, kWaitLimitNs);
+                if (pv0) (void)mbar_wait_bounded(bar(bO), (pv0 - 1) & 1, kWaitLimitNs);
+                if (pv1) (void)mbar_wait_bounded(bar(bO + 1), (pv1 - 1) & 1, kWaitLimitNs);
+            }
+        } else if (warp == 3 && lane == 0) {
+            // ---- what the joining kernel is to do with this CTA's cut item --------------
+            int4 meta = make_int4(0, 0, 0, 0);
+            Walk w(from, to);
+            while (w.next(a)) {
+                if (w.t0 != 0 || w.t1 == w.nt) continue;
+                const int64_t i0 = (static_cast<int64_t>(blockIdx.x) + 1) * total / n_ctas - w.t1;
+                const int64_t last = i0 + w.nt - kSnap + 1;  // cuts before this unit are inside the item
+                const int c1 = min(static_cast<int>((last * n_ctas + total - 1) / total) - 1, n_ctas - 1);
+                meta = make_int4(w.s.q0 + w.tok0, w.toks, c1 - static_cast<int>(blockIdx.x) + 1, w.kvh);
+            }
+            reinterpret_cast<int4*>(a.workspace)[blockIdx.x] = meta;
         }
-        // Copies under way land before the CTA may exit.
-        if (lane == 0)
-            for (int i = max(n - RING, 0); i < n; ++i) (void)mbar_wait_bounded(bar(FULL + i % RING), (i / RING) & 1, kWaitLimitNs);
         __syncwarp();
-    } else if (warp == 1) {
-        // ======================= tensor-core issue ================================
-        constexpr int FMT = FP8 ? 0 : 1;  // f16 or bf16 operands
-        constexpr uint32_t kIdescQk = umma_idesc(128, kTile, FMT, FMT, false, false);
-        constexpr uint32_t kIdescPv = umma_idesc(128, D, FMT, FMT, false, true);
-        int tile0 = 0, seg = 0;  // tiles before this piece, pieces
-        int jobs[2] = {0, 0}, scores[2] = {0, 0};  // P . V and Q . K^T issued per group
-        bool ok = true;
-        Walk w(from, to);
-        while (ok && w.next(a)) {
-            const bool two = w.rows > 128;  // each group its own rows of every tile
-            const int nt = w.t1 - w.t0, nj = two ? 2 * nt : nt;
-            auto tile_of = [&](int j) { return tile0 + (two ? j >> 1 : j); };
-            auto qk = [&](int j) -> bool {
-                const int g = j & 1, n = 2 * tile_of(j);
-                if (!warp_wait(bar(bFull + stage(n)), phase(n))) return false;
-                tc_fence_after();
-                const uint32_t q = s0 + C::OFF_Q + (two ? g * C::TILE : 0), kt = s0 + C::OFF_T + stage(n) * C::TILE;
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    umma_f16_warp(tmem + 256 * g, umma_desc_sw128(q + (k >> 2) * C::BLOCK + (k & 3) * 32, 16, 1024),
-                                  umma_desc_sw128(kt + (k >> 2) * C::BLOCK + (k & 3) * 32, 16, 1024), kIdescQk, k > 0);
-                umma_commit_warp(bar(bS + g));
-                if (!two || g == 1) umma_commit_warp(bar(bFree + stage(n)));
-                ++scores[g];
-                return true;
-            };
-            auto pv = [&](int j) -> bool {
-                const int g = j & 1, n = 2 * tile_of(j) + 1;
-                if (!warp_wait(bar(bP + g), jobs[g] & 1)) return false;
-                if (!warp_wait(bar(bFull + stage(n)), phase(n))) return false;
-                tc_fence_after();
-                const uint32_t vt = s0 + C::OFF_T + stage(n) * C::TILE;
-#pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
-                    umma_f16_ts_warp(tmem + 256 * g + C::O_COL, tmem + 256 * g + C::P_COL + 8 * k,
-                                     umma_desc_sw128(vt + k * 2048, C::BLOCK, 1024), kIdescPv, j > 1 || k > 0);
-                umma_commit_warp(bar(bO + g));
-                if (!two || g == 1) umma_commit_warp(bar(bFree + stage(n)));
-                ++jobs[g];
-                return true;
-            };
-            ok = warp_wait(bar(bQ), seg & 1);
-            ++seg;
-            ok = ok && qk(0) && (nj < 2 || qk(1));
-            for (int j = 0; ok && j < nj; ++j) ok = pv(j) && (j + 2 >= nj || qk(j + 2));
-            tile0 += nt;
-        }
-        // Every operation issued is done before the tensor memory is freed:
-        // the softmax groups wait for their last O, and give-ups for both here.
-        if (!ok) {
-            for (int g = 0; g < 2; ++g) {
-                if (scores[g] > 0) (void)mbar_wait_bounded(bar(bS + g), (scores[g] - 1) & 1, kWaitLimitNs);
-                if (jobs[g] > 0) (void)mbar_wait_bounded(bar(bO + g), (jobs[g] - 1) & 1, kWaitLimitNs);
-            }
-        }
-    } else if (warp >= 4 && warp < 12) {
+    } else if (warp < 12) {
         // ======================= softmax ==========================================
+        reg_inc<C::REG_SM>();
         const int grp = (warp - 4) >> 2, wq = warp & 3;
         const int row_l = 32 * wq + lane;              // this thread's lane of tensor memory
         const uint32_t tl = tmem + (static_cast<uint32_t>(wq) << 21);  // lanes 32 wq .. (bits 16 and up)
         const uint32_t tS = tl + 256 * grp, tP = tS + C::P_COL, tO = tS + C::O_COL;
-        float* q_scale = reinterpret_cast<float*>(smem + C::OFF_SC);
-        int tile0 = 0, job = 0;  // tiles before this piece, this group's jobs
+        const int tok_l = row_l / a.G, g_l = row_l - tok_l * a.G;      // its token in the row tile, its head
+        int tile0 = 0, job = 0, job_o = 0;             // tiles before this piece, this and the other group's jobs
         bool ok = true;
         Walk w(from, to);
         while (w.next(a)) {
-            const bool two = w.rows > 128;
-            const int r0 = w.rg * kRows;               // the item's first row
-            // ---- Q rows into the operand tiles (128-byte swizzle) ------------------
-            {
-                const int stid = tid - 128;            // 0 .. 255
-                constexpr int CH = D / 8;              // 16-byte chunks per row
-                const int n_rows = two ? kRows : 128;
-                const int ch = stid % CH;
-                const bool neg = a.scale_log2 < 0.f;   // the sign of the scale goes into q
-                for (int r = stid / CH; r < n_rows; r += 256 / CH) {
-                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < w.rows) {
-                        const int i = (r0 + r) / a.G, g = (r0 + r) - i * a.G;
-                        x = *reinterpret_cast<const uint4*>(a.q + (w.s.q0 + i) * a.q_s0 + (w.kvh * a.G + g) * a.q_s1 + 8 * ch);
-                    }
-                    if (neg) {
-                        x.x ^= 0x80008000u;
-                        x.y ^= 0x80008000u;
-                        x.z ^= 0x80008000u;
-                        x.w ^= 0x80008000u;
-                    }
-                    if constexpr (FP8) {
-                        // 2^k with 2^k max|q| in [2^14, 2^15): exponent arithmetic on the row's largest value
-                        const uint32_t v[4] = {x.x, x.y, x.z, x.w};
-                        uint32_t mx = 0;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) mx = max(mx, max(v[e] & 0x7F80u, (v[e] >> 16) & 0x7F80u));
-#pragma unroll
-                        for (int d = 1; d < CH; d <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                        int ex = static_cast<int>(mx >> 7);                    // biased exponent
-                        ex = ex == 255 ? 127 : max(ex, 20);                    // not finite: as it is; tiny rows: 2^121
-                        const float up = __uint_as_float(static_cast<uint32_t>(127 + 141 - ex) << 23);
-                        if (ch == 0) q_scale[r] = __uint_as_float(static_cast<uint32_t>(127 + ex - 141) << 23);
-                        x.x = pack_f16(bf16_lo(v[0]) * up, bf16_hi(v[0]) * up);
-                        x.y = pack_f16(bf16_lo(v[1]) * up, bf16_hi(v[1]) * up);
-                        x.z = pack_f16(bf16_lo(v[2]) * up, bf16_hi(v[2]) * up);
-                        x.w = pack_f16(bf16_lo(v[3]) * up, bf16_hi(v[3]) * up);
-                    }
-                    sts128u(s0 + C::OFF_Q + (r >> 7) * C::TILE + (ch >> 3) * C::BLOCK + (r & 127) * 128 + ((ch ^ r) & 7) * 16, x.x, x.y,
-                            x.z, x.w);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(bQ));
-                // the other warps wrote parts of the row scales
-                if (FP8) ok = named_bar_and(1, 256, ok);
-            }
-            const int row = two ? 128 * grp + row_l : row_l;
-            const bool live = row < w.rows;
-            const bool warp_live = (two ? 128 * grp : 0) + 32 * wq < w.rows;
-            const int tok = live ? (r0 + row) / a.G : 0;         // this row's drafted token
+            const bool two = w.two;
+            const int tok_t = tok_l + (two ? grp * a.tile_toks : 0);   // token in the pair of row tiles
+            const bool live = tok_l < a.tile_toks && tok_t < w.toks;
+            const bool warp_live = __any_sync(0xffffffffu, live);
+            const int tok = live ? w.tok0 + tok_t : 0;                 // this row's drafted token
+            const int row = (two ? 128 * grp : 0) + row_l;             // its place in partial sums
             const uint32_t* mrow = a.mask != nullptr && live ? a.mask + (w.s.q0 + tok) * a.mask_s0 : nullptr;
-            float sl = fabsf(a.scale_log2);
-            float vs = 1.f;
+            float sl = fabsf(a.scale_log2), vs = 1.f;
             if constexpr (FP8) {
-                sl *= __ldg(a.k_scale + (a.n_scale == 1 ? 0 : w.kvh)) * q_scale[row];
+                w.buffers([&](int bf, int uses) { ok = ok && warp_wait(bar(bQ + bf), uses & 1); });
+                sl *= __ldg(a.k_scale + (a.n_scale == 1 ? 0 : w.kvh)) * q_scale[128 * (two ? grp : w.buf) + row_l];
                 vs = __ldg(a.v_scale + (a.n_scale == 1 ? 0 : w.kvh));
+                __syncwarp();
+                if (lane == 0) w.buffers([&](int bf, int) { mbar_arrive(bar(bQFree + bf)); });
             }
+            sl = fmaxf(sl, 1.2e-38f);                  // -inf times it stays -inf
             const int L = w.s.L, ctx = w.s.ctx;
             const int npages = (L + kPageSize - 1) / kPageSize;
             const int job0 = job;
@@ -532,7 +611,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 const uint32_t pages_now = pages;
                 pages = page_ok(t + step);
                 const bool inner = p0 + kTile <= ctx && pages_now == ~0u;
-                uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+                uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u}, bad[4] = {0u, 0u, 0u, 0u};
                 if (!inner) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -558,7 +637,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 if (ok) ok = warp_wait(bar(bS + grp), job & 1);
                 tc_fence_after();
                 // ---- V rows that a weight of zero would not silence --------------------
-                uint32_t bad[4] = {0u, 0u, 0u, 0u};
                 if (p0 + kTile > ctx) {
                     const bool landed = ok && warp_wait(bar(bFull + stage(n)), phase(n));
                     const int pos = p0 + row_l;                  // thread = row of the tile here
@@ -587,25 +665,42 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     }
                     fence_proxy_async_smem();
                 }
-                if (ok && warp_live) {
-                    // ---- tile maximum ----------------------------------------------------
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t x[32];
-                        tmem_ld32(tS + 32 * c, x);
-                        tmem_wait_ld();
-                        if (inner) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(x[e]));
-                        } else {
+                const bool any_bad = (bad[0] | bad[1] | bad[2] | bad[3]) != 0u;
+                // ---- the tile's softmax: EDGE tiles have masked positions -----------------
+                auto softmax = [&](auto edge) {
+                    constexpr bool EDGE = decltype(edge)::value;
+                    // S is read twice, 32 columns at a time, the next ones on
+                    // their way: holding all 128 would spill.
+                    uint32_t x[2][32];
+                    auto masked = [&](int c, uint32_t (&v)[32]) {
+                        if constexpr (EDGE) {
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
-                                mx = fmaxf(mx, (vis[c] >> e & 1) ? __uint_as_float(x[e]) : -INFINITY);
+                                if (!(vis[c] & (1u << e))) v[e] = 0xFF800000u;
                         }
-                    }
-                    mx *= sl;
-                    if (!(mx == mx)) mx = -INFINITY;             // 0 x -inf: a scale of zero and nothing seen
+                    };
+                    auto columns = [&](auto use) {
+                        tmem_ld32(tS, x[0]);
+                        tmem_wait_ld();
+                        pin(x[0]);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            if (c < 3) tmem_ld32(tS + 32 * (c + 1), x[(c + 1) & 1]);
+                            masked(c, x[c & 1]);
+                            use(c, x[c & 1]);
+                            if (c < 3) {
+                                tmem_wait_ld();
+                                pin(x[(c + 1) & 1]);
+                            }
+                        }
+                    };
+                    float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    columns([&](int, const uint32_t (&v)[32]) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            mx4[(e >> 1) & 3] = fmaxf(fmaxf(mx4[(e >> 1) & 3], __uint_as_float(v[e])), __uint_as_float(v[e + 1]));
+                    });
+                    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl;
                     const bool move = mx > m + kRescaleLog2 || (m == -INFINITY && mx > m);
                     if (__any_sync(0xffffffffu, move)) {
                         const float nm = move ? mx : m;
@@ -613,11 +708,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         if (job > job0) {
                             ok = warp_wait(bar(bO + grp), (job - 1) & 1);
                             tc_fence_after();
-#pragma unroll
+#pragma unroll 2
                             for (int c = 0; c < D / 16; ++c) {
                                 uint32_t o[16];
                                 tmem_ld16(tO + 16 * c, o);
                                 tmem_wait_ld();
+                                pin(o);
 #pragma unroll
                                 for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
                                 tmem_st16(tO + 16 * c, o);
@@ -626,44 +722,44 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         l *= al;
                         m = nm;
                     }
-                    // ---- weights ------------------------------------------------------------
-                    const float mm = m == -INFINITY ? 0.f : m;
-                    float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t x[32], p[16];
-                        tmem_ld32(tS + 32 * c, x);
-                        tmem_wait_ld();
+                    const float mm = m == -INFINITY ? 0.f : -m;
+                    const float2 sl2 = make_float2(sl, sl), mm2 = make_float2(mm, mm);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    columns([&](int c, const uint32_t (&v)[32]) {
+                        uint32_t p[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            float p0f = fast_exp2(fmaf(__uint_as_float(x[2 * e]), sl, -mm));
-                            float p1f = fast_exp2(fmaf(__uint_as_float(x[2 * e + 1]), sl, -mm));
-                            if (!inner) {
-                                if (!(vis[c] >> (2 * e) & 1)) p0f = 0.f;
-                                if (!(vis[c] >> (2 * e + 1) & 1)) p1f = 0.f;
+                            float2 y = fma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sl2, mm2);
+                            y.x = fast_exp2(y.x);
+                            y.y = fast_exp2(y.y);
+                            sum[e & 1] = add2(sum[e & 1], y);
+                            p[e] = FP8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
+                        }
+                        if (EDGE && any_bad) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                if (bad[c] & (1u << (2 * e))) p[e] &= 0xFFFF0000u;
+                                if (bad[c] & (2u << (2 * e))) p[e] &= 0x0000FFFFu;
                             }
-                            s4[(2 * e) & 3] += p0f;
-                            s4[(2 * e + 1) & 3] += p1f;
-                            if (!inner) {
-                                if (bad[c] >> (2 * e) & 1) p0f = 0.f;
-                                if (bad[c] >> (2 * e + 1) & 1) p1f = 0.f;
-                            }
-                            p[e] = FP8 ? pack_f16(p0f, p1f) : pack_bf16(p0f, p1f);
                         }
                         tmem_st16(tP + 16 * c, p);
-                    }
-                    l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                    });
+                    l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
                     tmem_wait_st();
+                };
+                if (ok && warp_live) {
+                    if (inner) softmax(std::false_type{});
+                    else softmax(std::true_type{});
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0 && ok) mbar_arrive(bar(bP + grp));
                 // ---- drafted tokens whose V is not finite, for the rows that see them ----
-                if ((bad[0] | bad[1] | bad[2] | bad[3]) != 0u) {
+                if (any_bad) {
                     if (ok) ok = warp_wait(bar(bO + grp), job & 1);
                     tc_fence_after();
                     for (int j = 0; ok && j < kTile; ++j) {
-                        if (!(bad[j >> 5] >> (j & 31) & 1)) continue;
+                        if (!(word_of(bad, j >> 5) >> (j & 31) & 1)) continue;
                         const int id = __ldg(a.block_tables + w.b * a.bt_s0 + (p0 + j) / kPageSize);
                         if (id < 0 || id >= num_pages) continue;
                         const int off = (p0 + j) % kPageSize;
@@ -675,20 +771,21 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                                     e4m3x2_to_f16x2(static_cast<const uint8_t*>(base)[i]) & 0xFFFFu)));
                             return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(base)[i]) << 16);
                         };
-                        const bool sees = live && (vis[j >> 5] >> (j & 31) & 1);
+                        const bool sees = live && (word_of(vis, j >> 5) >> (j & 31) & 1);
                         float x = 0.f;
                         if (sees) {
-                            const int g = (r0 + row) - tok * a.G;
-                            const uint16_t* qr = a.q + (w.s.q0 + tok) * a.q_s0 + (w.kvh * a.G + g) * a.q_s1;
+                            const uint16_t* qr = a.q + (w.s.q0 + tok) * a.q_s0 + (w.kvh * a.G + g_l) * a.q_s1;
                             for (int d = 0; d < D; ++d)
                                 x += __uint_as_float(static_cast<uint32_t>(qr[d]) << 16) * at(a.k_cache, kb + d);
                             x *= a.scale_log2 * (FP8 ? __ldg(a.k_scale + (a.n_scale == 1 ? 0 : w.kvh)) : 1.f);
                             x = fast_exp2(x - (m == -INFINITY ? 0.f : m));
                         }
+#pragma unroll 1
                         for (int c = 0; c < D / 16; ++c) {
                             uint32_t o[16];
                             tmem_ld16(tO + 16 * c, o);
                             tmem_wait_ld();
+                            pin(o);
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
                                 if (sees) o[e] = __float_as_uint(fmaf(x, at(a.v_cache, vb + 16 * c + e), __uint_as_float(o[e])));
@@ -700,35 +797,42 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 }
             }
             // ---- the piece's sums ---------------------------------------------------
+            const int nt = w.t1 - w.t0;
             const bool mine = job > job0;
-            if (ok && mine) ok = warp_wait(bar(bO + grp), (job - 1) & 1);
-            tc_fence_after();
-            float mo = -INFINITY, lo = 0.f;  // the other group's
-            const bool theirs = !two && w.t1 - w.t0 > 1 - grp;
+            const bool theirs = !two && nt > 1 - grp;
+            job_o += two ? nt : nt - (job - job0);
+            float mo = -INFINITY, lo = 0.f;            // the other group's
             if (!two) {
                 uint32_t x[8] = {__float_as_uint(m), __float_as_uint(l), 0u, 0u, 0u, 0u, 0u, 0u};
-                tmem_st8(tS, x);
+                tmem_st8(tS + C::ML_COL, x);
                 tmem_wait_st();
             }
             tc_fence_before();
-            ok = named_bar_and(1, 256, ok);  // (also: every S of this piece is read, so Q may be overwritten)
+            ok = named_bar_and(1, 256, ok);            // every S of this piece is read
             tc_fence_after();
             if (!ok) break;
             if (!two) {
                 uint32_t x[8];
-                tmem_ld8(tl + 256 * (1 - grp), x);
+                tmem_ld8(tl + 256 * (1 - grp) + C::ML_COL, x);
                 tmem_wait_ld();
+                pin(x);
                 mo = __uint_as_float(x[0]);
                 lo = __uint_as_float(x[1]);
             }
-            if (warp_live) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(bX));       // S may be written for the next item
+            if (mine) ok = warp_wait(bar(bO + grp), (job - 1) & 1);
+            if (theirs) ok = ok && warp_wait(bar(bO + 1 - grp), (job_o - 1) & 1);
+            tc_fence_after();
+            if (ok && warp_live) {
                 const float M = fmaxf(m, mo);
                 const float f0 = m == -INFINITY ? 0.f : fast_exp2(m - M), f1 = mo == -INFINITY ? 0.f : fast_exp2(mo - M);
                 const float sum = (mine ? l * f0 : 0.f) + (theirs ? lo * f1 : 0.f);
                 const bool whole = w.t0 == 0 && w.t1 == w.nt;
                 const bool none = sum == 0.f;
                 const float k0 = whole ? (none ? 0.f : f0 * vs / sum) : f0 * vs, k1 = whole ? (none ? 0.f : f1 * vs / sum) : f1 * vs;
-                const int g = (r0 + row) - tok * a.G, h = w.kvh * a.G + g;
+                const int h = w.kvh * a.G + g_l;
                 const int slot = 2 * static_cast<int>(blockIdx.x) + (w.t0 == 0 ? 1 : 0);
                 uint16_t* out = a.out + (w.s.q0 + tok) * a.o_s0 + h * a.o_s1;
                 float* part = part_o<D>(a.workspace, gridDim.x, slot, row);
@@ -742,51 +846,80 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                             none ? -INFINITY : (M + __log2f(sum)) * 0.69314718055994530942f;
                     }
                 }
-                // two row groups: all of this row's columns; else each group half of them
-                const int c0 = two ? 0 : grp * (D / 32), c1 = two ? D / 16 : c0 + D / 32;
+                // two row tiles: all of this row's columns; else each group half of them
+                const int c0 = two ? 0 : grp * (D / 64), c1 = two ? D / 32 : c0 + D / 64;
 #pragma unroll 1
                 for (int c = c0; c < c1; ++c) {
-                    uint32_t x[16], y[16];
-                    if (mine) tmem_ld16(tO + 16 * c, x);
-                    if (theirs) tmem_ld16(tl + 256 * (1 - grp) + C::O_COL + 16 * c, y);
+                    uint32_t x[32], y[32];
+                    if (mine) tmem_ld32(tO + 32 * c, x);
+                    if (theirs) tmem_ld32(tl + 256 * (1 - grp) + C::O_COL + 32 * c, y);
                     tmem_wait_ld();
-                    float o[16];
+                    pin(x);
+                    pin(y);
+                    float o[32];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
+                    for (int e = 0; e < 32; ++e) {
                         o[e] = mine ? __uint_as_float(x[e]) * k0 : 0.f;
                         if (theirs) o[e] = fmaf(__uint_as_float(y[e]), k1, o[e]);
                     }
                     if (!live) continue;
                     if (whole) {
-                        uint32_t p[8];
+                        uint4* dst = reinterpret_cast<uint4*>(out + 32 * c);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) p[e] = pack_bf16(o[2 * e], o[2 * e + 1]);
-                        uint4* dst = reinterpret_cast<uint4*>(out + 16 * c);
-                        dst[0] = make_uint4(p[0], p[1], p[2], p[3]);
-                        dst[1] = make_uint4(p[4], p[5], p[6], p[7]);
+                        for (int e = 0; e < 4; ++e)
+                            dst[e] = make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
+                                                pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
                     } else {
-                        float4* dst = reinterpret_cast<float4*>(part + 16 * c);
+                        float4* dst = reinterpret_cast<float4*>(part + 32 * c);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                     }
                 }
             }
             tc_fence_before();
-            named_bar_and(1, 256, true);  // O, m and l are read
-            tile0 += w.t1 - w.t0;
+            if (!two) ok = named_bar_and(1, 256, ok);  // either group's O is read by both
+            tile0 += nt;
         }
-    } else if (FP8 && warp >= 12) {
-        // ======================= E4M3 bytes to f16 tiles ==========================
+    } else {
+        // ======================= E4M3 bytes and bf16 q to f16 tiles ===============
+        reg_dec<C::REG_CV>();
         const int ct = tid - 384;
         constexpr int CH = D / 16;  // 16-byte chunks of a raw row
         int n = 0;
         bool ok = true;
         Walk w(from, to);
         while (ok && w.next(a)) {
+            w.buffers([&](int bf, int uses) {
+                ok = ok && warp_wait(bar(bQRaw + bf), uses & 1);
+                if (!ok) return;
+                constexpr int QC = D / 8;              // 16-byte chunks of a row of q
+                const int ch = ct % QC;
+#pragma unroll 2
+                for (int r = ct / QC; r < 128; r += 128 / QC) {
+                    const uint32_t at = s0 + C::OFF_Q + bf * C::TILE + (ch >> 3) * C::BLOCK + r * 128 + ((ch ^ r) & 7) * 16;
+                    const uint4 x = lds128(at);
+                    const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+                    // 2^k with 2^k max|q| in [2^14, 2^15), from the exponent of the row's largest value
+                    uint32_t mx = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx = max(mx, max(v[e] & 0x7F80u, (v[e] >> 16) & 0x7F80u));
+#pragma unroll
+                    for (int d = 1; d < QC; d <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                    int ex = static_cast<int>(mx >> 7);    // biased exponent
+                    ex = ex == 255 ? 127 : max(ex, 20);    // not finite: stays so; tiny rows: 2^121
+                    const float up = __uint_as_float(static_cast<uint32_t>(127 + 141 - ex) << 23);
+                    if (ch == 0) q_scale[128 * bf + r] = __uint_as_float(static_cast<uint32_t>(127 + ex - 141) << 23);
+                    sts128u(at, pack_f16(bf16_lo(v[0]) * up, bf16_hi(v[0]) * up), pack_f16(bf16_lo(v[1]) * up, bf16_hi(v[1]) * up),
+                            pack_f16(bf16_lo(v[2]) * up, bf16_hi(v[2]) * up), pack_f16(bf16_lo(v[3]) * up, bf16_hi(v[3]) * up));
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(bQ + bf));
+            });
             for (int t = w.t0; ok && t < w.t1; ++t) {
                 for (int v = 0; v < 2; ++v, ++n) {
-                    const int rs = n % C::RST;
-                    ok = warp_wait(bar(bRawFull + rs), (n / C::RST) & 1);
+                    const int rs = C::RST ? n % C::RST : 0;
+                    ok = warp_wait(bar(bRawFull + rs), (n / (C::RST ? C::RST : 1)) & 1);
                     if (ok && n >= C::ST) ok = warp_wait(bar(bFree + stage(n)), (n / C::ST - 1) & 1);
                     if (!ok) break;
                     const uint32_t src = s0 + C::OFF_R + rs * C::RAW, dst = s0 + C::OFF_T + stage(n) * C::TILE;
@@ -799,12 +932,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         const int c0 = (2 * ch) & 7;
                         const uint32_t e0 = d0 + ((c0 ^ r) & 7) * 16, e1 = d0 + (((c0 + 1) ^ r) & 7) * 16;
                         uint32_t h[8];
-                        h[0] = e4m3x2_to_f16x2(static_cast<uint16_t>(x.x)), h[1] = e4m3x2_to_f16x2(static_cast<uint16_t>(x.x >> 16));
-                        h[2] = e4m3x2_to_f16x2(static_cast<uint16_t>(x.y)), h[3] = e4m3x2_to_f16x2(static_cast<uint16_t>(x.y >> 16));
-                        h[4] = e4m3x2_to_f16x2(static_cast<uint16_t>(x.z)), h[5] = e4m3x2_to_f16x2(static_cast<uint16_t>(x.z >> 16));
-                        h[6] = e4m3x2_to_f16x2(static_cast<uint16_t>(x.w)), h[7] = e4m3x2_to_f16x2(static_cast<uint16_t>(x.w >> 16));
-                        sts128u(e0, h[0], h[1], h[2], h[3]);
-                        sts128u(e1, h[4], h[5], h[6], h[7]);
+                        h[0] = e4m3x2_to_f16x2(lo16(x.x)), h[1] = e4m3x2_to_f16x2(hi16(x.x));
+                        h[2] = e4m3x2_to_f16x2(lo16(x.y)), h[3] = e4m3x2_to_f16x2(hi16(x.y));
+                        h[4] = e4m3x2_to_f16x2(lo16(x.z)), h[5] = e4m3x2_to_f16x2(hi16(x.z));
+                        h[6] = e4m3x2_to_f16x2(lo16(x.w)), h[7] = e4m3x2_to_f16x2(hi16(x.w));
+                        // either half first, by column block: eight lanes meet all banks once
+                        const bool swap = ch & 4;
+                        sts128u(swap ? e1 : e0, swap ? h[4] : h[0], swap ? h[5] : h[1], swap ? h[6] : h[2], swap ? h[7] : h[3]);
+                        sts128u(swap ? e0 : e1, swap ? h[0] : h[4], swap ? h[1] : h[5], swap ? h[2] : h[6], swap ? h[3] : h[7]);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -817,19 +952,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         }
     }
 
-    // ---- what the joining kernel is to do with this CTA's cut item --------------
-    if (warp == 2 && lane == 0) {
-        int4 meta = make_int4(0, 0, 0, 0);
-        Walk w(from, to);
-        while (w.next(a)) {
-            if (w.t0 != 0 || w.t1 == w.nt) continue;
-            const int64_t i0 = (static_cast<int64_t>(blockIdx.x) + 1) * total / n_ctas - w.t1;
-            const int64_t last = i0 + w.nt - kSnap + 1;  // cuts before this unit are inside the item
-            const int c1 = min(static_cast<int>((last * n_ctas + total - 1) / total) - 1, n_ctas - 1);
-            meta = make_int4(w.s.q0, w.rg * kRows, w.rows | (c1 - static_cast<int>(blockIdx.x) + 1) << 12, w.kvh);
-        }
-        reinterpret_cast<int4*>(a.workspace)[blockIdx.x] = meta;
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -843,10 +965,12 @@ template <int D>
 __global__ void __launch_bounds__(kJoinRows * 32) tree_join_kernel(const TreeArgs a, int ctas) {
     grid_dep_wait();
     const int c = blockIdx.x, lane = threadIdx.x & 31;
-    const int row = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
-    const int4 meta = reinterpret_cast<const int4*>(a.workspace)[c];
-    if (row >= (meta.z & 0xFFF)) return;
-    const int n = meta.z >> 12;  // pieces: slot 1 of CTA c, slot 0 of the next ones
+    const int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5);  // row of the item: token r / G, head r % G
+    const int4 meta = reinterpret_cast<const int4*>(a.workspace)[c];  // first token, tokens, pieces, kv head
+    const int tok = r / a.G, g = r - tok * a.G;
+    if (tok >= meta.y) return;
+    const int row = tok < a.tile_toks ? r : 128 + r - a.tile_toks * a.G;  // its place in the partial sums
+    const int n = meta.z;        // pieces: slot 1 of CTA c, slot 0 of the next ones
     auto slot = [&](int i) { return 2 * (c + i) + (i == 0 ? 1 : 0); };
     float M = -INFINITY;
     for (int i = lane; i < n; i += 32) M = fmaxf(M, part_ml(a.workspace, slot(i), row)[0]);
@@ -872,7 +996,7 @@ __global__ void __launch_bounds__(kJoinRows * 32) tree_join_kernel(const TreeArg
     }
     const bool none = sum == 0.f;
     const float inv = none ? 0.f : 1.f / sum;
-    const int tok = (meta.y + row) / a.G, h = meta.w * a.G + (meta.y + row) - tok * a.G;
+    const int h = meta.w * a.G + g;
     uint32_t* out = reinterpret_cast<uint32_t*>(a.out + (meta.x + tok) * a.o_s0 + h * a.o_s1 + V * lane);
 #pragma unroll
     for (int e = 0; e < V; e += 2) out[e / 2] = pack_bf16(none ? 0.f : o[e] * inv, none ? 0.f : o[e + 1] * inv);
@@ -881,14 +1005,14 @@ __global__ void __launch_bounds__(kJoinRows * 32) tree_join_kernel(const TreeArg
 }
 
 template <int D, bool FP8>
-cudaError_t launch_t(const TreeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+cudaError_t launch_t(const TreeArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
     using C = Cfg<D, FP8>;
     int sms = 0;
     cudaError_t e = device_sm_count(&sms);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(tree_kernel<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(tree_kernel<D, FP8>, dim3(sms), dim3(C::THREADS), C::SMEM, s, tk, tv, a);
+    e = launch_dependent(tree_kernel<D, FP8>, dim3(sms), dim3(C::THREADS), C::SMEM, s, tq, tk, tv, a);
     if (e != cudaSuccess) return e;
     const int rows = static_cast<int>(std::min<int64_t>(kRows, static_cast<int64_t>(a.T) * a.G));
     return launch_dependent(tree_join_kernel<D>, dim3(sms, (rows + kJoinRows - 1) / kJoinRows), dim3(kJoinRows * 32), 0, s, a, sms);
@@ -901,10 +1025,10 @@ int64_t tree_decode_workspace(int64_t T, int32_t Hq, int32_t D, int32_t sm_count
     return kMetaBytes + static_cast<int64_t>(sm_count) * 2 * kRows * (D + 2) * 4;
 }
 
-cudaError_t launch_tree_decode(const TreeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+cudaError_t launch_tree_decode(const TreeArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
     const bool fp8 = a.kind == kFp8;
-    if (a.D == 128) return fp8 ? launch_t<128, true>(a, tk, tv, s) : launch_t<128, false>(a, tk, tv, s);
-    return fp8 ? launch_t<64, true>(a, tk, tv, s) : launch_t<64, false>(a, tk, tv, s);
+    if (a.D == 128) return fp8 ? launch_t<128, true>(a, tq, tk, tv, s) : launch_t<128, false>(a, tq, tk, tv, s);
+    return fp8 ? launch_t<64, true>(a, tq, tk, tv, s) : launch_t<64, false>(a, tq, tk, tv, s);
 }
 
 }  // namespace pkv

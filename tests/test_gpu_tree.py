@@ -195,3 +195,12 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     check_tree(a)
     check_tree(b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("scale", [-0.11, 0.0])
+def test_negative_and_zero_scales(dtype, scale):
+    s = make_tree([700, 90], [9, 40], 8, 2, 128, dtype=dtype, seed=15)
+    s["scale"] = scale
+    run_tree(s)
+    check_tree(s)
