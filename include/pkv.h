@@ -669,7 +669,8 @@ pkv_status pkv_selftest_bounded_wait(int64_t limit_ns, int32_t* err_flag, uint64
  * workspace_bytes  device scratch, 16-byte aligned, of at least
  *              pkv_tree_decode_workspace() bytes; its contents need no
  *              preparation. Calls that may run at the same time need one each.
- * Supported: D in {64, 128}; 1 <= Hq/Hkv <= 16; any N_b; B, Hkv <= 65535.
+ * Supported: D in {64, 128}; 1 <= Hq/Hkv <= 16; any N_b; B, Hkv <= 65535;
+ * Hkv (B + T Hq / (128 Hkv)) max_pages / 8 below 2^31 / 1.1 (tiles of work).
  * Errors: a block-table entry outside [0, num_pages) sets PKV_FLAG_PAGE_RANGE
  * and that page is left out; seq_lens[b] outside [0, 16*max_pages] sets
  * PKV_FLAG_SEQ_LEN_RANGE and is clamped; q_start not ascending within [0, T]

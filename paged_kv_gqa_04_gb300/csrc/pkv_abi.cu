@@ -1542,6 +1542,9 @@ pkv_status pkv_paged_tree_decode(const pkv_tensor* q_p, const pkv_tensor* k_cach
     if (!q.ptr || !out.ptr) return PKV_ERR_INVALID_ARG;
     if (!row16(q, 2) || !row16(out, 2)) return PKV_ERR_UNSUPPORTED;
     if (mask.ptr && (mask.shape[1] > 64 || (mask.shape[1] > 1 && mask.stride[1] != 1))) return PKV_ERR_UNSUPPORTED;
+    // tiles of work, as the kernel counts them, in 32 bits
+    if (static_cast<double>(Hkv) * static_cast<double>(B + T * G / 128 + 1) * (max_pages / 8 + 2) > 2.0e9)
+        return PKV_ERR_UNSUPPORTED;
     int sms = 0;
     if (pkv::device_sm_count(&sms) != cudaSuccess) return PKV_ERR_CUDA;
     if (!workspace || workspace_bytes < pkv::tree_decode_workspace(T, static_cast<int32_t>(Hq), D, sms))

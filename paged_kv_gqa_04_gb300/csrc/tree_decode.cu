@@ -17,11 +17,11 @@
 // item, the start of another), which a second kernel joins.
 //
 // A CTA's roles, per tile:
-//   warp 0        TMA tile loads of q (per item) and K into the rings
-//   warp 2        TMA tile loads of V (a warp starts a 16-row x 128-byte copy
-//                 in about 85 cycles: one warp for both would be the limit).
-//                 Pages that do not exist are read out of range, which fills
-//                 zeros
+//   warps 0, 2    TMA tile loads of K and of V into one ring (a warp starts a
+//                 16-row x 128-byte copy in about 85 cycles: one for both would
+//                 be the limit). Pages that do not exist are read out of
+//                 range, which fills zeros
+//   warp 3        TMA tile loads of q, per item
 //   warp 1        S = Q . K^T and O += P . V (M = 128; P from tensor memory, V
 //                 as an MN-major operand: nothing is transposed)
 //   warps 4 - 7,
@@ -49,7 +49,6 @@
 // Waits are bounded (about one second): a role that gives up sets
 // PKV_FLAG_WAIT_TIMEOUT and a CTA-wide flag that ends the others' waits.
 #include <algorithm>
-#include <type_traits>
 
 #include "pkv_internal.h"
 #include "pkv_ptx.cuh"
@@ -61,7 +60,6 @@ constexpr int kTile = 128;    // positions per tile
 constexpr int kRows = 256;    // rows (lanes of two row tiles) per item
 constexpr int kTilePages = kTile / kPageSize;
 constexpr int kSnap = 2;      // no piece of a cut item is shorter than this many tiles
-constexpr int kMinUnits = 2;  // units per CTA before another CTA is used
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr float kRescaleLog2 = 8.f;
 constexpr int kMetaBytes = 4096 * 16;  // workspace: one int4 per CTA, then the partial sums
@@ -73,7 +71,7 @@ struct Cfg {
     static constexpr int BLOCK = kTile * 128;              // one column block of it
     static constexpr int RAW = kTile * D;                  // FP8 tile as it lands
     static constexpr int RBOX = D >= 128 ? 128 : D;        // its row (and swizzle span)
-    // Rings of K tiles and of V tiles: operand tiles, and (FP8) tiles of bytes.
+    // Rings of K and V tiles in turn: operand tiles, and (FP8) tiles of bytes.
     static constexpr int ST = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
     static constexpr int RST = FP8 ? (D == 128 ? 3 : 6) : 0;
     static constexpr int THREADS = FP8 ? 512 : 384;
@@ -84,7 +82,7 @@ struct Cfg {
     static constexpr int OFF_R = OFF_T + ST * TILE;
     static constexpr int OFF_SC = OFF_R + RST * RAW;       // FP8: [2][128] floats, 2^-k of each row
     static constexpr int OFF_BAR = OFF_SC + (FP8 ? kRows * 4 : 0);
-    static constexpr int NBAR = 2 * ST + 2 * RST + 13;
+    static constexpr int NBAR = 2 * ST + 2 * RST + 15;
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
     static constexpr int SMEM = OFF_MISC + 256 + 1024;     // + alignment slack
     static_assert(SMEM <= 232448, "shared memory of one CTA");
@@ -124,28 +122,46 @@ __device__ __forceinline__ int kv_end(const TreeArgs& a, const Seq& s, int rg) {
 __device__ __forceinline__ int tiles_of(const TreeArgs& a, const Seq& s, int rg) {
     return max((kv_end(a, s, rg) + kTile - 1) / kTile, 1);
 }
-__device__ __forceinline__ int64_t units_per_head(const TreeArgs& a, const Seq& s) {
-    if (s.RG <= 1 || a.mask != nullptr) return s.RG ? static_cast<int64_t>(s.RG) * tiles_of(a, s, 0) : 0;
-    int64_t n = 0;
+// (the host has checked that the batch's units stay below 2^31)
+__device__ __forceinline__ int units_per_head(const TreeArgs& a, const Seq& s) {
+    if (s.RG <= 1 || a.mask != nullptr) return s.RG ? s.RG * tiles_of(a, s, 0) : 0;
+    int n = 0;
     for (int rg = 0; rg < s.RG; ++rg) n += tiles_of(a, s, rg);
     return n;
 }
+
+// CTA c of n starts at unit cut(c); the first total % n stretches are one unit longer.
+struct Cuts {
+    int n, per, rem;
+    __device__ __forceinline__ Cuts(int total, int ctas) : n(min(ctas, total)), per(0), rem(0) {
+        if (n > 0) {
+            per = total / n;
+            rem = total - per * n;
+        }
+    }
+    __device__ __forceinline__ int cut(int c) const { return c * per + min(c, rem); }
+    // the last CTA that starts at or before unit x
+    __device__ __forceinline__ int at_or_before(int x) const {
+        const int c = x < rem * (per + 1) ? x / (per + 1) : rem + (x - rem * (per + 1)) / per;
+        return min(c, n - 1);
+    }
+};
 
 // A place in the order of units: tile t of item k = kvh RG + rg of sequence b.
 struct Place {
     int b, k, t;
 };
 // Unit `off` of sequence b; a cut closer than kSnap to an end of its item moves there.
-__device__ __forceinline__ Place place_of(const TreeArgs& a, const Seq& s, int b, int64_t off) {
-    const int64_t per = units_per_head(a, s);
-    const int kvh = static_cast<int>(off / per);
-    int64_t rem = off - kvh * per;
+__device__ __forceinline__ Place place_of(const TreeArgs& a, const Seq& s, int b, int off) {
+    const int per = units_per_head(a, s);
+    const int kvh = off / per;
+    int rem = off - kvh * per;
     int rg = 0, nt = tiles_of(a, s, 0);
     while (rem >= nt) {
         rem -= nt;
         nt = tiles_of(a, s, ++rg);
     }
-    Place p{b, kvh * s.RG + rg, static_cast<int>(rem)};
+    Place p{b, kvh * s.RG + rg, rem};
     if (p.t < kSnap) {
         p.t = 0;
     } else if (nt - p.t < kSnap) {
@@ -283,7 +299,8 @@ __device__ __forceinline__ uint32_t word_of(const uint32_t (&v)[4], int k) {
     return k == 0 ? v[0] : k == 1 ? v[1] : k == 2 ? v[2] : v[3];
 }
 
-// Workspace of partial sums: [2 per CTA][256 rows] of {m, l}, then of D floats.
+// Workspace of partial sums: [2 per CTA][256 rows] of {m, l}, then [2 per
+// CTA][D / 4][256 rows] of 4 floats (a warp's rows are neighbours).
 __device__ __forceinline__ float* part_ml(void* ws, int slot, int row) {
     return reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kMetaBytes) +
            (static_cast<int64_t>(slot) * kRows + row) * 2;
@@ -291,7 +308,7 @@ __device__ __forceinline__ float* part_ml(void* ws, int slot, int row) {
 template <int D>
 __device__ __forceinline__ float* part_o(void* ws, int ctas, int slot, int row) {
     return reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kMetaBytes) + static_cast<int64_t>(ctas) * 2 * kRows * 2 +
-           (static_cast<int64_t>(slot) * kRows + row) * D;
+           static_cast<int64_t>(slot) * kRows * D + row * 4;
 }
 
 template <int D, bool FP8>
@@ -303,14 +320,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t s0 = smem_u32(smem);
     enum : int { bFull = 0, bFree = C::ST, bRawFull = 2 * C::ST, bRawFree = bRawFull + C::RST, bS = bRawFree + C::RST,
-                 bP = bS + 2, bO = bP + 2, bQ = bO + 2, bQFree = bQ + 2, bQRaw = bQFree + 2, bX = bQRaw + 2 };
+                 bP = bS + 2, bO = bP + 4, bQ = bO + 2, bQFree = bQ + 2, bQRaw = bQFree + 2, bX = bQRaw + 2 };
     static_assert(bX + 1 == C::NBAR, "barriers");
     auto bar = [&](int i) -> uint32_t { return s0 + C::OFF_BAR + 8 * i; };
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
     uint32_t* bad_tok = misc + 4;                         // [2 jobs][2 groups][4 words]: drafted tokens, V not finite
     Place* place = reinterpret_cast<Place*>(misc + 20);   // [2]: this CTA's first unit and the one past its last
-    int64_t* warp_units = reinterpret_cast<int64_t*>(misc + 26);  // [16]
+    int* warp_units = reinterpret_cast<int*>(misc + 26);  // [16]
     float* q_scale = reinterpret_cast<float*>(smem + C::OFF_SC);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -327,10 +344,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(bar(bS + w), 1);
-            mbar_init(bar(bP + w), 4);
+            mbar_init(bar(bP + 2 * w), 4);  // either half of P
+            mbar_init(bar(bP + 2 * w + 1), 4);
             mbar_init(bar(bO + w), 1);
             mbar_init(bar(bQ + w), FP8 ? 4 : 1);
-            mbar_init(bar(bQFree + w), FP8 ? 9 : 1);  // the last Q . K^T; FP8: the row scales are read
+            mbar_init(bar(bQFree + w), 9);  // the last Q . K^T, and the softmax warps (row scales, staged output)
             mbar_init(bar(bQRaw + w), 1);
         }
         mbar_init(bar(bX), 8);
@@ -347,44 +365,38 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     }
 
     // ---- this CTA's stretch of the units (index inputs only) ------------------
-    int64_t total;
-    int n_ctas;
+    int total = 0;
     {
         const int seg = (a.B + C::THREADS - 1) / C::THREADS;
         const int b0 = min(tid * seg, a.B), b1 = min(b0 + seg, a.B);
-        int64_t sum = 0;
-        int flags = 0;
+        int sum = 0, flags = 0;
         for (int b = b0; b < b1; ++b) sum += a.Hkv * units_per_head(a, seq_of(a, b, flags));
         if (flags && blockIdx.x == 0) flag_error(a.err, flags);
-        int64_t inc = sum;
+        int inc = sum;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, inc, d);
+            const int y = __shfl_up_sync(0xffffffffu, inc, d);
             if (lane >= d) inc += y;
         }
         if (lane == 31) warp_units[warp] = inc;
         __syncthreads();
-        int64_t base = 0;
-        total = 0;
+        int base = 0;
         for (int w = 0; w < C::THREADS / 32; ++w) {
             if (w == warp) base = total;
             total += warp_units[w];
         }
-        n_ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), (total + kMinUnits - 1) / kMinUnits));
+        const Cuts cuts(total, gridDim.x);
         const int c = blockIdx.x;
-        if (c < n_ctas) {
-            int64_t at = base + inc - sum;
-            const int64_t x[2] = {c * total / n_ctas, (c + 1) * total / n_ctas};
-            if (x[1] >= at && x[0] < at + sum) {
-                for (int b = b0; b < b1; ++b) {
-                    int ignored = 0;
-                    const Seq s = seq_of(a, b, ignored);
-                    const int64_t n = a.Hkv * units_per_head(a, s);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (x[e] >= at && x[e] < at + n) place[e] = place_of(a, s, b, x[e] - at);
-                    at += n;
-                }
+        int at = base + inc - sum;
+        const int x0 = cuts.cut(c), x1 = cuts.cut(c + 1);
+        if (c < cuts.n && x1 >= at && x0 < at + sum) {
+            for (int b = b0; b < b1; ++b) {
+                int ignored = 0;
+                const Seq s = seq_of(a, b, ignored);
+                const int n = a.Hkv * units_per_head(a, s);
+                if (x0 >= at && x0 < at + n) place[0] = place_of(a, s, b, x0 - at);
+                if (x1 >= at && x1 < at + n) place[1] = place_of(a, s, b, x1 - at);
+                at += n;
             }
         }
     }
@@ -421,14 +433,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         reg_dec<C::REG_IO>();
         if (warp == 0 || warp == 2) {
             // ======================= copies ===========================================
-            const int v = warp >> 1;                                       // K (and q) or V
+            const int v = warp >> 1;                                       // K or V
             constexpr int RING = FP8 ? C::RST : C::ST;
             constexpr int FULL = FP8 ? bRawFull : bFull, FREE = FP8 ? bRawFree : bFree;
             constexpr int COPIES = FP8 ? kTilePages : kTilePages * C::NB;  // per tile
             const int pg = lane % kTilePages, blk = lane / kTilePages;     // this lane's copy
             const bool hnd = a.layout == PKV_HND;
             const uint64_t policy = l2_policy_evict_first();
-            int n = v, q_done0 = 0, q_done1 = 0;
+            int n = v;
             bool ok = true;
             Walk w(from, to);
             while (ok && w.next(a)) {
@@ -438,20 +450,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     return p < npages && t < w.t1 ? __ldg(a.block_tables + w.b * a.bt_s0 + p) : -1;
                 };
                 int nxt = page_at(w.t0);
-                if (v == 0) {
-                    // q: tile_toks tokens x G heads are consecutive operand rows
-                    w.buffers([&](int bf, int uses) {
-                        if (uses > 0) ok = ok && warp_wait(bar(bQFree + bf), (uses - 1) & 1);
-                        const uint32_t fb = bar((FP8 ? bQRaw : bQ) + bf);
-                        if (ok && lane == 0) mbar_arrive_expect_tx(fb, a.tile_toks * a.G * D * 2);
-                        __syncwarp();
-                        if (ok && lane < C::NB)
-                            tma_load_3d(s0 + C::OFF_Q + bf * C::TILE + lane * C::BLOCK, &tmq, fb, 64 * lane, w.kvh * a.G,
-                                        w.s.q0 + w.tok0 + (w.two ? bf * a.tile_toks : 0), policy);
-                        if (ok) ++(bf ? q_done1 : q_done0);
-                        __syncwarp();
-                    });
-                }
                 bool bad = false;
                 for (int t = w.t0; ok && t < w.t1; ++t, n += 2) {
                     int id = nxt;
@@ -483,8 +481,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 // (slots whose stage neither copy warp has taken again)
                 for (int i = n - 2; i >= 0 && i > n - 1 - v - RING; i -= 2)
                     (void)mbar_wait_bounded(bar(FULL + i % RING), (i / RING) & 1, kWaitLimitNs);
-                if (q_done0) (void)mbar_wait_bounded(bar(FP8 ? bQRaw : bQ), (q_done0 - 1) & 1, kWaitLimitNs);
-                if (q_done1) (void)mbar_wait_bounded(bar((FP8 ? bQRaw : bQ) + 1), (q_done1 - 1) & 1, kWaitLimitNs);
             }
         } else if (warp == 1 && lane == 0) {
             // ======================= tensor-core issue (one thread) ===================
@@ -498,9 +494,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             Walk w(from, to);
             while (ok && w.next(a)) {
                 const int nt = w.t1 - w.t0, nj = w.two ? 2 * nt : nt;
-                auto qk = [&](int j) -> bool {
-                    const int g = j & 1, n = 2 * (tile0 + (w.two ? j >> 1 : j));
-                    if (!lane_wait(bar(bFull + stage(n)), phase(n))) return false;
+                auto k_slot = [&](int j) { return 2 * (tile0 + (w.two ? j >> 1 : j)); };
+                auto qk = [&](int j, bool landed) -> bool {
+                    const int g = j & 1, n = k_slot(j);
+                    if (!landed && !lane_wait(bar(bFull + stage(n)), phase(n))) return false;
                     tc_fence_after();
                     const uint64_t q = umma_desc_sw128(s0 + C::OFF_Q + (w.two ? g : w.buf) * C::TILE, 16, 1024);
                     const uint64_t kt = umma_desc_sw128(s0 + C::OFF_T + stage(n) * C::TILE, 16, 1024);
@@ -514,29 +511,34 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     ++(g ? qk1 : qk0);
                     return true;
                 };
+                // P . V of job j, then the scores of job j + 2, which take S from under P:
+                // the tensor cores execute in order of issue
                 auto pv = [&](int j) -> bool {
-                    const int g = j & 1, n = 2 * (tile0 + (w.two ? j >> 1 : j)) + 1;
+                    const int g = j & 1, n = k_slot(j) + 1, n2 = k_slot(j + 2);
                     if (!lane_wait(bar(bFull + stage(n)), phase(n))) return false;
-                    if (!lane_wait(bar(bP + g), (g ? pv1 : pv0) & 1)) return false;
-                    tc_fence_after();
+                    const bool more = j + 2 < nj, landed = more && mbar_test_wait(bar(bFull + stage(n2)), phase(n2));
                     const uint64_t vt = umma_desc_sw128(s0 + C::OFF_T + stage(n) * C::TILE, C::BLOCK, 1024);
 #pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
-                        umma_ts(tmem + 256 * g + C::O_COL, tmem + 256 * g + C::P_COL + 8 * k, vt + k * (2048 >> 4), kIdescPv,
-                                j > 1 || k > 0);
+                    for (int h = 0; h < 2; ++h) {      // the softmax hands P over in halves
+                        if (!lane_wait(bar(bP + 2 * g + h), (g ? pv1 : pv0) & 1)) return false;
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = 4 * h; k < 4 * h + 4; ++k)
+                            umma_ts(tmem + 256 * g + C::O_COL, tmem + 256 * g + C::P_COL + 8 * k, vt + k * (2048 >> 4),
+                                    kIdescPv, j > 1 || k > 0);
+                    }
                     umma_commit(bar(bO + g));
                     if (!w.two || g == 1) umma_commit(bar(bFree + stage(n)));
                     ++(g ? pv1 : pv0);
-                    return true;
+                    return !more || qk(j + 2, landed);
                 };
                 w.buffers([&](int bf, int uses) { ok = ok && lane_wait(bar(bQ + bf), uses & 1); });
                 // the item before has no more use for S
                 if (w.piece > 0) ok = ok && lane_wait(bar(bX), (w.piece - 1) & 1);
-                ok = ok && qk(0) && (nj < 2 || qk(1));
-                if (ok && nj <= 2) w.buffers([&](int bf, int) { umma_commit(bar(bQFree + bf)); });
+                ok = ok && qk(0, false) && (nj < 2 || qk(1, false));
                 for (int j = 0; ok && j < nj; ++j) {
-                    ok = pv(j) && (j + 2 >= nj || qk(j + 2));
-                    if (ok && j + 2 == nj - 1) w.buffers([&](int bf, int) { umma_commit(bar(bQFree + bf)); });
+                    if (j + 2 == max(nj, 2)) w.buffers([&](int bf, int) { umma_commit(bar(bQFree + bf)); });
+                    ok = pv(j);
                 }
                 tile0 += nt;
             }
@@ -549,17 +551,35 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 if (pv1) (void)mbar_wait_bounded(bar(bO + 1), (pv1 - 1) & 1, kWaitLimitNs);
             }
         } else if (warp == 3 && lane == 0) {
-            // ---- what the joining kernel is to do with this CTA's cut item --------------
+            // ---- q: tile_toks tokens x G heads are consecutive operand rows; and what the
+            // ---- joining kernel is to do with this CTA's cut item
             int4 meta = make_int4(0, 0, 0, 0);
+            const Cuts cuts(total, gridDim.x);
+            const uint64_t policy = l2_policy_evict_first();
+            int done0 = 0, done1 = 0;
+            bool ok = true;
             Walk w(from, to);
             while (w.next(a)) {
-                if (w.t0 != 0 || w.t1 == w.nt) continue;
-                const int64_t i0 = (static_cast<int64_t>(blockIdx.x) + 1) * total / n_ctas - w.t1;
-                const int64_t last = i0 + w.nt - kSnap + 1;  // cuts before this unit are inside the item
-                const int c1 = min(static_cast<int>((last * n_ctas + total - 1) / total) - 1, n_ctas - 1);
-                meta = make_int4(w.s.q0 + w.tok0, w.toks, c1 - static_cast<int>(blockIdx.x) + 1, w.kvh);
+                w.buffers([&](int bf, int uses) {
+                    if (ok && uses > 0) ok = lane_wait(bar(bQFree + bf), (uses - 1) & 1);
+                    if (!ok) return;
+                    const uint32_t fb = bar((FP8 ? bQRaw : bQ) + bf);
+                    mbar_arrive_expect_tx(fb, a.tile_toks * a.G * D * 2);
+                    for (int k = 0; k < C::NB; ++k)
+                        tma_load_3d(s0 + C::OFF_Q + bf * C::TILE + k * C::BLOCK, &tmq, fb, 64 * k, w.kvh * a.G,
+                                    w.s.q0 + w.tok0 + (w.two ? bf * a.tile_toks : 0), policy);
+                    ++(bf ? done1 : done0);
+                });
+                if (w.t0 == 0 && w.t1 < w.nt) {
+                    // cuts up to kSnap tiles before the item's end are inside it
+                    const int i0 = cuts.cut(static_cast<int>(blockIdx.x) + 1) - w.t1;
+                    const int c1 = cuts.at_or_before(i0 + w.nt - kSnap);
+                    meta = make_int4(w.s.q0 + w.tok0, w.toks, c1 - static_cast<int>(blockIdx.x) + 1, w.kvh);
+                }
             }
             reinterpret_cast<int4*>(a.workspace)[blockIdx.x] = meta;
+            if (done0) (void)mbar_wait_bounded(bar(FP8 ? bQRaw : bQ), (done0 - 1) & 1, kWaitLimitNs);
+            if (done1) (void)mbar_wait_bounded(bar((FP8 ? bQRaw : bQ) + 1), (done1 - 1) & 1, kWaitLimitNs);
         }
         __syncwarp();
     } else if (warp < 12) {
@@ -586,8 +606,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 w.buffers([&](int bf, int uses) { ok = ok && warp_wait(bar(bQ + bf), uses & 1); });
                 sl *= __ldg(a.k_scale + (a.n_scale == 1 ? 0 : w.kvh)) * q_scale[128 * (two ? grp : w.buf) + row_l];
                 vs = __ldg(a.v_scale + (a.n_scale == 1 ? 0 : w.kvh));
-                __syncwarp();
-                if (lane == 0) w.buffers([&](int bf, int) { mbar_arrive(bar(bQFree + bf)); });
             }
             sl = fmaxf(sl, 1.2e-38f);                  // -inf times it stays -inf
             const int L = w.s.L, ctx = w.s.ctx;
@@ -665,41 +683,37 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     }
                     fence_proxy_async_smem();
                 }
-                const bool any_bad = (bad[0] | bad[1] | bad[2] | bad[3]) != 0u;
-                // ---- the tile's softmax: EDGE tiles have masked positions -----------------
-                auto softmax = [&](auto edge) {
-                    constexpr bool EDGE = decltype(edge)::value;
-                    // S is read twice, 32 columns at a time, the next ones on
-                    // their way: holding all 128 would spill.
-                    uint32_t x[2][32];
-                    auto masked = [&](int c, uint32_t (&v)[32]) {
-                        if constexpr (EDGE) {
+                const bool any_bad = (bad[0] | bad[1] | bad[2] | bad[3]) != 0u;  // (uniform)
+                // ---- the tile's softmax, 64 columns at a time (S is read twice: holding
+                // ---- all of it would spill, and short loops stay in the instruction cache)
+                auto columns = [&](int c, uint32_t (&x)[2][32]) {
+                    tmem_ld32(tS + 64 * c, x[0]);
+                    tmem_ld32(tS + 64 * c + 32, x[1]);
+                    tmem_wait_ld();
+                    pin(x[0]);
+                    pin(x[1]);
+                    if (!inner) {
+                        const uint32_t v0 = c ? vis[2] : vis[0], v1 = c ? vis[3] : vis[1];
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!(vis[c] & (1u << e))) v[e] = 0xFF800000u;
+                        for (int e = 0; e < 32; ++e) {
+                            if (!(v0 & (1u << e))) x[0][e] = 0xFF800000u;
+                            if (!(v1 & (1u << e))) x[1][e] = 0xFF800000u;
                         }
-                    };
-                    auto columns = [&](auto use) {
-                        tmem_ld32(tS, x[0]);
-                        tmem_wait_ld();
-                        pin(x[0]);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            if (c < 3) tmem_ld32(tS + 32 * (c + 1), x[(c + 1) & 1]);
-                            masked(c, x[c & 1]);
-                            use(c, x[c & 1]);
-                            if (c < 3) {
-                                tmem_wait_ld();
-                                pin(x[(c + 1) & 1]);
-                            }
-                        }
-                    };
+                    }
+                };
+                const bool work = ok && warp_live;
+                if (work) {
                     float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    columns([&](int, const uint32_t (&v)[32]) {
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t x[2][32];
+                        columns(c, x);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2)
-                            mx4[(e >> 1) & 3] = fmaxf(fmaxf(mx4[(e >> 1) & 3], __uint_as_float(v[e])), __uint_as_float(v[e + 1]));
-                    });
+                        for (int e = 0; e < 32; e += 2) {
+                            mx4[e & 2] = fmaxf(fmaxf(mx4[e & 2], __uint_as_float(x[0][e])), __uint_as_float(x[0][e + 1]));
+                            mx4[(e & 2) + 1] = fmaxf(fmaxf(mx4[(e & 2) + 1], __uint_as_float(x[1][e])), __uint_as_float(x[1][e + 1]));
+                        }
+                    }
                     const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl;
                     const bool move = mx > m + kRescaleLog2 || (m == -INFINITY && mx > m);
                     if (__any_sync(0xffffffffu, move)) {
@@ -708,52 +722,62 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         if (job > job0) {
                             ok = warp_wait(bar(bO + grp), (job - 1) & 1);
                             tc_fence_after();
-#pragma unroll 2
-                            for (int c = 0; c < D / 16; ++c) {
-                                uint32_t o[16];
-                                tmem_ld16(tO + 16 * c, o);
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[32];
+                                tmem_ld32(tO + 32 * c, o);
                                 tmem_wait_ld();
                                 pin(o);
+                                uint32_t h0[16], h1[16];
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-                                tmem_st16(tO + 16 * c, o);
+                                for (int e = 0; e < 16; ++e) {
+                                    h0[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                                    h1[e] = __float_as_uint(__uint_as_float(o[16 + e]) * al);
+                                }
+                                tmem_st16(tO + 32 * c, h0);
+                                tmem_st16(tO + 32 * c + 16, h1);
                             }
                         }
                         l *= al;
                         m = nm;
                     }
-                    const float mm = m == -INFINITY ? 0.f : -m;
-                    const float2 sl2 = make_float2(sl, sl), mm2 = make_float2(mm, mm);
-                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                    columns([&](int c, const uint32_t (&v)[32]) {
-                        uint32_t p[16];
+                }
+                const float mm = m == -INFINITY ? 0.f : -m;
+                const float2 sl2 = make_float2(sl, sl), mm2 = make_float2(mm, mm);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                    if (work) {
+                        uint32_t x[2][32];
+                        columns(c, x);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float2 y = fma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sl2, mm2);
-                            y.x = fast_exp2(y.x);
-                            y.y = fast_exp2(y.y);
-                            sum[e & 1] = add2(sum[e & 1], y);
-                            p[e] = FP8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
-                        }
-                        if (EDGE && any_bad) {
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t p[16];
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
-                                if (bad[c] & (1u << (2 * e))) p[e] &= 0xFFFF0000u;
-                                if (bad[c] & (2u << (2 * e))) p[e] &= 0x0000FFFFu;
+                                float2 y = fma2(make_float2(__uint_as_float(x[h][2 * e]), __uint_as_float(x[h][2 * e + 1])), sl2, mm2);
+                                y.x = fast_exp2(y.x);
+                                y.y = fast_exp2(y.y);
+                                sum[e & 1] = add2(sum[e & 1], y);
+                                p[e] = FP8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
                             }
+                            if (any_bad) {
+                                const uint32_t b = word_of(bad, 2 * c + h);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    if (b & (1u << (2 * e))) p[e] &= 0xFFFF0000u;
+                                    if (b & (2u << (2 * e))) p[e] &= 0x0000FFFFu;
+                                }
+                            }
+                            tmem_st16(tP + 32 * c + 16 * h, p);
                         }
-                        tmem_st16(tP + 16 * c, p);
-                    });
-                    l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
-                    tmem_wait_st();
-                };
-                if (ok && warp_live) {
-                    if (inner) softmax(std::false_type{});
-                    else softmax(std::true_type{});
+                        tmem_wait_st();
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0 && ok) mbar_arrive(bar(bP + 2 * grp + c));  // this half of P
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0 && ok) mbar_arrive(bar(bP + grp));
+                l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
                 // ---- drafted tokens whose V is not finite, for the rows that see them ----
                 if (any_bad) {
                     if (ok) ok = warp_wait(bar(bO + grp), job & 1);
@@ -834,20 +858,20 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 const float k0 = whole ? (none ? 0.f : f0 * vs / sum) : f0 * vs, k1 = whole ? (none ? 0.f : f1 * vs / sum) : f1 * vs;
                 const int h = w.kvh * a.G + g_l;
                 const int slot = 2 * static_cast<int>(blockIdx.x) + (w.t0 == 0 ? 1 : 0);
-                uint16_t* out = a.out + (w.s.q0 + tok) * a.o_s0 + h * a.o_s1;
                 float* part = part_o<D>(a.workspace, gridDim.x, slot, row);
                 if (live && (two || grp == 0)) {
                     if (!whole) {
-                        float* ml = part_ml(a.workspace, slot, row);
-                        ml[0] = M;
-                        ml[1] = sum;
+                        *reinterpret_cast<float2*>(part_ml(a.workspace, slot, row)) = make_float2(M, sum);
                     } else if (a.lse) {
                         a.lse[(w.s.q0 + tok) * a.l_s0 + h * a.l_s1] =
                             none ? -INFINITY : (M + __log2f(sum)) * 0.69314718055994530942f;
                     }
                 }
-                // two row tiles: all of this row's columns; else each group half of them
+                // Two row tiles: all of this row's columns; else each group half of them.
+                // A whole item's output goes through q's buffer (the warp's own 32
+                // rows), so that the warp writes rows and not columns.
                 const int c0 = two ? 0 : grp * (D / 64), c1 = two ? D / 32 : c0 + D / 64;
+                const uint32_t stage_row = s0 + C::OFF_Q + (two ? grp : w.buf) * C::TILE + row_l * 128;
 #pragma unroll 1
                 for (int c = c0; c < c1; ++c) {
                     uint32_t x[32], y[32];
@@ -862,20 +886,38 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         o[e] = mine ? __uint_as_float(x[e]) * k0 : 0.f;
                         if (theirs) o[e] = fmaf(__uint_as_float(y[e]), k1, o[e]);
                     }
-                    if (!live) continue;
                     if (whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(out + 32 * c);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            dst[e] = make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
-                                                pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
-                    } else {
-                        float4* dst = reinterpret_cast<float4*>(part + 32 * c);
+                        for (int e = 0; e < 4; ++e) {
+                            const int ch = 4 * c + e;
+                            sts128u(stage_row + (ch >> 3) * C::BLOCK + ((ch ^ row_l) & 7) * 16, pack_bf16(o[8 * e], o[8 * e + 1]),
+                                    pack_bf16(o[8 * e + 2], o[8 * e + 3]), pack_bf16(o[8 * e + 4], o[8 * e + 5]),
+                                    pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+                        }
+                    } else if (live) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        for (int e = 0; e < 8; ++e)
+                            *reinterpret_cast<float4*>(part + static_cast<int64_t>(8 * c + e) * kRows * 4) =
+                                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
+                }
+                if (whole) {
+                    __syncwarp();
+                    const int64_t off = live ? (w.s.q0 + tok) * a.o_s0 + h * a.o_s1 : -1;  // this lane's row
+                    const int per_row = 4 * (c1 - c0);                                      // 16-byte chunks: 16, 8 or 4
+                    const int sub = lane / per_row, ch = 4 * c0 + lane - sub * per_row;
+#pragma unroll 4
+                    for (int i = 0; i < per_row; ++i) {
+                        const int r = i * (32 / per_row) + sub;
+                        const int64_t o = __shfl_sync(0xffffffffu, off, r);
+                        const uint4 v = lds128(stage_row + (r - lane) * 128 + (ch >> 3) * C::BLOCK + ((ch ^ r) & 7) * 16);
+                        if (o >= 0) *reinterpret_cast<uint4*>(a.out + o + 8 * ch) = v;
                     }
                 }
             }
+            fence_proxy_async_smem();                  // q's next copy comes after the staged rows
+            __syncwarp();
+            if (lane == 0) w.buffers([&](int bf, int) { mbar_arrive(bar(bQFree + bf)); });
             tc_fence_before();
             if (!two) ok = named_bar_and(1, 256, ok);  // either group's O is read by both
             tile0 += nt;
@@ -959,48 +1001,49 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
 }
 
 // ---- joining the pieces of cut items ------------------------------------------------
-constexpr int kJoinRows = 8;  // rows (warps) per CTA
+// CTA (c, y): 32 rows of the item whose first piece CTA c had; a lane is a
+// row, a warp D / 32 of its quads of columns.
+constexpr int kJoinRows = 32;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinRows * 32) tree_join_kernel(const TreeArgs a, int ctas) {
+__global__ void __launch_bounds__(256) tree_join_kernel(const TreeArgs a, int ctas) {
     grid_dep_wait();
-    const int c = blockIdx.x, lane = threadIdx.x & 31;
-    const int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5);  // row of the item: token r / G, head r % G
+    const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = blockIdx.y * kJoinRows + lane;         // row of the item: token r / G, head r % G
     const int4 meta = reinterpret_cast<const int4*>(a.workspace)[c];  // first token, tokens, pieces, kv head
     const int tok = r / a.G, g = r - tok * a.G;
     if (tok >= meta.y) return;
     const int row = tok < a.tile_toks ? r : 128 + r - a.tile_toks * a.G;  // its place in the partial sums
-    const int n = meta.z;        // pieces: slot 1 of CTA c, slot 0 of the next ones
+    const int n = meta.z;                                // pieces: slot 1 of CTA c, slot 0 of the next ones
     auto slot = [&](int i) { return 2 * (c + i) + (i == 0 ? 1 : 0); };
     float M = -INFINITY;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, part_ml(a.workspace, slot(i), row)[0]);
-    M = warp_max(M);
-    float sum = 0.f;
-    constexpr int V = D / 32;
-    float o[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = 0.f;
 #pragma unroll 8
+    for (int i = 0; i < n; ++i) M = fmaxf(M, part_ml(a.workspace, slot(i), row)[0]);
+    constexpr int Q = D / 32;                            // quads of columns per thread
+    float sum = 0.f;
+    float4 o[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int i = 0; i < n; ++i) {
-        const float* ml = part_ml(a.workspace, slot(i), row);
-        const float f = ml[0] == -INFINITY ? 0.f : fast_exp2(ml[0] - M);
-        const float* p = part_o<D>(a.workspace, ctas, slot(i), row) + V * lane;
-        sum += f * ml[1];
-        if constexpr (V == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(p);
-            o[0] += f * x.x, o[1] += f * x.y, o[2] += f * x.z, o[3] += f * x.w;
-        } else {
-            const float2 x = *reinterpret_cast<const float2*>(p);
-            o[0] += f * x.x, o[1] += f * x.y;
+        const float2 ml = *reinterpret_cast<const float2*>(part_ml(a.workspace, slot(i), row));
+        const float* p = part_o<D>(a.workspace, ctas, slot(i), row);
+        const float f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);
+        sum += f * ml.y;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const float4 x = *reinterpret_cast<const float4*>(p + static_cast<int64_t>(warp * Q + q) * kRows * 4);
+            o[q].x += f * x.x, o[q].y += f * x.y, o[q].z += f * x.z, o[q].w += f * x.w;
         }
     }
     const bool none = sum == 0.f;
     const float inv = none ? 0.f : 1.f / sum;
     const int h = meta.w * a.G + g;
-    uint32_t* out = reinterpret_cast<uint32_t*>(a.out + (meta.x + tok) * a.o_s0 + h * a.o_s1 + V * lane);
+    uint2* out = reinterpret_cast<uint2*>(a.out + (meta.x + tok) * a.o_s0 + h * a.o_s1 + warp * Q * 4);
 #pragma unroll
-    for (int e = 0; e < V; e += 2) out[e / 2] = pack_bf16(none ? 0.f : o[e] * inv, none ? 0.f : o[e + 1] * inv);
-    if (lane == 0 && a.lse)
+    for (int q = 0; q < Q; ++q)
+        out[q] = none ? make_uint2(0u, 0u) : make_uint2(pack_bf16(o[q].x * inv, o[q].y * inv), pack_bf16(o[q].z * inv, o[q].w * inv));
+    if (warp == 0 && a.lse)
         a.lse[(meta.x + tok) * a.l_s0 + h * a.l_s1] = none ? -INFINITY : (M + __log2f(sum)) * 0.69314718055994530942f;
 }
 
@@ -1015,7 +1058,7 @@ cudaError_t launch_t(const TreeArgs& a, const CUtensorMap& tq, const CUtensorMap
     e = launch_dependent(tree_kernel<D, FP8>, dim3(sms), dim3(C::THREADS), C::SMEM, s, tq, tk, tv, a);
     if (e != cudaSuccess) return e;
     const int rows = static_cast<int>(std::min<int64_t>(kRows, static_cast<int64_t>(a.T) * a.G));
-    return launch_dependent(tree_join_kernel<D>, dim3(sms, (rows + kJoinRows - 1) / kJoinRows), dim3(kJoinRows * 32), 0, s, a, sms);
+    return launch_dependent(tree_join_kernel<D>, dim3(sms, (rows + kJoinRows - 1) / kJoinRows), dim3(256), 0, s, a, sms);
 }
 
 }  // namespace
