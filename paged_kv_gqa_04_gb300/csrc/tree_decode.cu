@@ -9,7 +9,7 @@
 // sum need no exchange. One pass over K and V serves two row tiles.
 //
 // Work. An item is (sequence, kv head, pair of row tiles); a unit is one tile
-// of 128 positions of one item. All units of the batch, in order, are cut into
+// of 128 positions of one item, and an item costs two units more. All units of the batch, in order, are cut into
 // equal stretches, one per CTA (one CTA per SM): every CTA streams the same
 // number of tiles whatever the lengths are, with no plan from the host. Each
 // CTA finds its stretch from prefix sums over the batch. An item that is cut
@@ -21,7 +21,8 @@
 //                 16-row x 128-byte copy in about 85 cycles: one for both would
 //                 be the limit). Pages that do not exist are read out of
 //                 range, which fills zeros
-//   warp 3        TMA tile loads of q, per item
+//   warp 3        walks the CTA's items, hands the pieces to the other roles, and
+//                 loads q by TMA
 //   warp 1        S = Q . K^T and O += P . V (M = 128; P from tensor memory, V
 //                 as an MN-major operand: nothing is transposed)
 //   warps 4 - 7,
@@ -60,6 +61,8 @@ constexpr int kTile = 128;    // positions per tile
 constexpr int kRows = 256;    // rows (lanes of two row tiles) per item
 constexpr int kTilePages = kTile / kPageSize;
 constexpr int kSnap = 2;      // no piece of a cut item is shorter than this many tiles
+constexpr int kItemUnits = 2; // what an item costs beyond its tiles (start, output), in tiles
+constexpr int kPieces = 4;    // ring of pieces
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr float kRescaleLog2 = 8.f;
 constexpr int kMetaBytes = 4096 * 16;  // workspace: one int4 per CTA, then the partial sums
@@ -82,9 +85,10 @@ struct Cfg {
     static constexpr int OFF_R = OFF_T + ST * TILE;
     static constexpr int OFF_SC = OFF_R + RST * RAW;       // FP8: [2][128] floats, 2^-k of each row
     static constexpr int OFF_BAR = OFF_SC + (FP8 ? kRows * 4 : 0);
-    static constexpr int NBAR = 2 * ST + 2 * RST + 15;
+    static constexpr int NBAR = 2 * ST + 2 * RST + 15 + 2 * kPieces;
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
-    static constexpr int SMEM = OFF_MISC + 256 + 1024;     // + alignment slack
+    static constexpr int OFF_PIECE = OFF_MISC + 192;       // [kPieces] Piece
+    static constexpr int SMEM = OFF_PIECE + kPieces * 64 + 1024;  // + alignment slack
     static_assert(SMEM <= 232448, "shared memory of one CTA");
     static_assert(FP8 ? REG_IO + 2 * REG_SM + REG_CV <= 512 : REG_IO + 2 * REG_SM <= 504, "registers as launched");
     // tensor-memory columns of a softmax group: S (P over it, or beside it where O leaves room), then O
@@ -122,11 +126,11 @@ __device__ __forceinline__ int kv_end(const TreeArgs& a, const Seq& s, int rg) {
 __device__ __forceinline__ int tiles_of(const TreeArgs& a, const Seq& s, int rg) {
     return max((kv_end(a, s, rg) + kTile - 1) / kTile, 1);
 }
-// (the host has checked that the batch's units stay below 2^31)
+// Units of one kv head (the host has checked that the batch's stay below 2^31).
 __device__ __forceinline__ int units_per_head(const TreeArgs& a, const Seq& s) {
-    if (s.RG <= 1 || a.mask != nullptr) return s.RG ? s.RG * tiles_of(a, s, 0) : 0;
+    if (s.RG <= 1 || a.mask != nullptr) return s.RG ? s.RG * (tiles_of(a, s, 0) + kItemUnits) : 0;
     int n = 0;
-    for (int rg = 0; rg < s.RG; ++rg) n += tiles_of(a, s, rg);
+    for (int rg = 0; rg < s.RG; ++rg) n += tiles_of(a, s, rg) + kItemUnits;
     return n;
 }
 
@@ -157,11 +161,11 @@ __device__ __forceinline__ Place place_of(const TreeArgs& a, const Seq& s, int b
     const int kvh = off / per;
     int rem = off - kvh * per;
     int rg = 0, nt = tiles_of(a, s, 0);
-    while (rem >= nt) {
-        rem -= nt;
+    while (rem >= nt + kItemUnits) {
+        rem -= nt + kItemUnits;
         nt = tiles_of(a, s, ++rg);
     }
-    Place p{b, kvh * s.RG + rg, rem};
+    Place p{b, kvh * s.RG + rg, max(rem - kItemUnits, 0)};
     if (p.t < kSnap) {
         p.t = 0;
     } else if (nt - p.t < kSnap) {
@@ -174,52 +178,12 @@ __device__ __forceinline__ Place place_of(const TreeArgs& a, const Seq& s, int b
     return p;
 }
 
-// The pieces of items between two places, in order. Every role walks them by itself.
-struct Walk {
-    int b, k, t0, t1, nt, kvh, tok0, toks;  // piece [t0, t1) of nt tiles; drafted tokens [tok0, tok0 + toks)
-    Seq s;
-    Place end;
-    int piece;                              // its number in this CTA
-    int uses0, uses1;                       // earlier items in each buffer of q
-    int buf;                                // its buffer (one row tile; two row tiles take both)
-    bool two, first;
-    __device__ __forceinline__ Walk(const Place& from, const Place& to)
-        : b(from.b), k(from.k), t0(from.t), end(to), piece(-1), uses0(0), uses1(0), buf(1), two(false), first(true) {}
-    // The next piece; false at the end.
-    __device__ __forceinline__ bool next(const TreeArgs& a) {
-        int ignored = 0;
-        if (first) {
-            if (!in_range()) return false;
-            first = false;
-            s = seq_of(a, b, ignored);
-        } else {
-            uses0 += two || buf == 0;
-            uses1 += two || buf == 1;
-            t0 = 0;
-            ++k;
-        }
-        while (k >= a.Hkv * s.RG) {
-            k = 0;
-            t0 = 0;
-            ++b;
-            if (!in_range() || b >= a.B) return false;
-            s = seq_of(a, b, ignored);
-        }
-        if (!in_range()) return false;
-        kvh = s.RG == 1 ? k : k / s.RG;
-        const int rg = k - kvh * s.RG;
-        tok0 = rg * 2 * a.tile_toks;
-        toks = min(s.N - tok0, 2 * a.tile_toks);
-        two = toks > a.tile_toks;
-        if (!two) buf ^= 1;
-        nt = tiles_of(a, s, rg);
-        t1 = b == end.b && k == end.k ? end.t : nt;
-        ++piece;
-        return true;
-    }
-    __device__ __forceinline__ bool in_range() const {
-        return b < end.b || (b == end.b && (k < end.k || (k == end.k && end.t > t0)));
-    }
+// A piece: tiles [t0, t1) of an item (its drafted tokens [tok0, tok0 + toks)).
+struct Piece {
+    int b, kvh, q0, L, ctx, tok0, toks;  // b < 0: there are no more
+    int t0, t1, whole;                   // whole: all of the item
+    int two, buf;                        // two row tiles, or one, whose q is in this buffer
+    int uses0, uses1;                    // earlier pieces in either buffer of q
     // q's buffers of this piece: fn(buffer, uses of it before)
     template <typename F>
     __device__ __forceinline__ void buffers(F fn) const {
@@ -320,14 +284,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t s0 = smem_u32(smem);
     enum : int { bFull = 0, bFree = C::ST, bRawFull = 2 * C::ST, bRawFree = bRawFull + C::RST, bS = bRawFree + C::RST,
-                 bP = bS + 2, bO = bP + 4, bQ = bO + 2, bQFree = bQ + 2, bQRaw = bQFree + 2, bX = bQRaw + 2 };
-    static_assert(bX + 1 == C::NBAR, "barriers");
+                 bP = bS + 2, bO = bP + 4, bQ = bO + 2, bQFree = bQ + 2, bQRaw = bQFree + 2, bX = bQRaw + 2,
+                 bPiece = bX + 1, bPieceFree = bPiece + kPieces };
+    static_assert(bPieceFree + kPieces == C::NBAR, "barriers");
     auto bar = [&](int i) -> uint32_t { return s0 + C::OFF_BAR + 8 * i; };
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
     uint32_t* bad_tok = misc + 4;                         // [2 jobs][2 groups][4 words]: drafted tokens, V not finite
     Place* place = reinterpret_cast<Place*>(misc + 20);   // [2]: this CTA's first unit and the one past its last
     int* warp_units = reinterpret_cast<int*>(misc + 26);  // [16]
+    Piece* pieces = reinterpret_cast<Piece*>(smem + C::OFF_PIECE);
     float* q_scale = reinterpret_cast<float*>(smem + C::OFF_SC);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -352,6 +318,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             mbar_init(bar(bQRaw + w), 1);
         }
         mbar_init(bar(bX), 8);
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(bar(bPiece + i), 1);
+            mbar_init(bar(bPieceFree + i), FP8 ? 15 : 11);  // copies, MMA, softmax, conversion
+        }
         *abort_flag = 0;
         place[0] = place[1] = Place{a.B, 0, 0};
         fence_mbar_init();
@@ -415,15 +385,21 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         flag_error(a.err, PKV_FLAG_WAIT_TIMEOUT);
     };
     auto lane_wait = [&](uint32_t bb, uint32_t par) -> bool {
-        const bool r = mbar_wait_or_abort(bb, par, abort_flag, kWaitLimitNs);
-        if (!r) give_up();
-        return r;
+        uint64_t t0 = 0;
+        while (!mbar_try_wait_suspend(bb, par, 20000u)) {
+            const uint64_t now = global_ns();
+            if (t0 == 0) t0 = now;
+            if (*abort_flag || now - t0 > kWaitLimitNs) {
+                give_up();
+                return false;
+            }
+        }
+        return true;
     };
-    auto warp_wait = [&](uint32_t bb, uint32_t par) -> bool {
-        const bool r = __all_sync(0xffffffffu, mbar_wait_or_abort(bb, par, abort_flag, kWaitLimitNs));
-        if (!r && lane == 0) give_up();
-        return r;
-    };
+    auto warp_wait = [&](uint32_t bb, uint32_t par) -> bool { return __all_sync(0xffffffffu, lane_wait(bb, par)); };
+    // Piece i of this CTA, handed over in a ring
+    auto piece_bar = [&](int i) { return bar(bPiece + i % kPieces); };
+    auto piece_par = [](int i) -> uint32_t { return (i / kPieces) & 1; };
     // Slot n of the operand ring (K of tile i is 2 i, V is 2 i + 1; tiles are
     // numbered through the CTA's stretch).
     auto stage = [](int n) { return n % C::ST; };
@@ -442,9 +418,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             const uint64_t policy = l2_policy_evict_first();
             int n = v;
             bool ok = true;
-            Walk w(from, to);
-            while (ok && w.next(a)) {
-                const int npages = (w.s.L + kPageSize - 1) / kPageSize;
+            for (int i = 0; ok; ++i) {
+                ok = warp_wait(piece_bar(i), piece_par(i));
+                const Piece w = pieces[i % kPieces];
+                if (!ok || w.b < 0) break;
+                const int npages = (w.L + kPageSize - 1) / kPageSize;
                 auto page_at = [&](int t) -> int {
                     const int p = t * kTilePages + pg;
                     return p < npages && t < w.t1 ? __ldg(a.block_tables + w.b * a.bt_s0 + p) : -1;
@@ -475,6 +453,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     __syncwarp();
                 }
                 if (bad && blk == 0 && v == 0) flag_error(a.err, PKV_FLAG_PAGE_RANGE);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(bPieceFree + i % kPieces));
             }
             // Copies under way land before the CTA may exit.
             if (lane == 0) {
@@ -491,8 +471,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             int tile0 = 0;                             // tiles before this piece
             int pv0 = 0, pv1 = 0, qk0 = 0, qk1 = 0;    // P . V and Q . K^T issued per group
             bool ok = true;
-            Walk w(from, to);
-            while (ok && w.next(a)) {
+            for (int i = 0; ok; ++i) {
+                ok = lane_wait(piece_bar(i), piece_par(i));
+                const Piece w = pieces[i % kPieces];
+                if (!ok || w.b < 0) break;
                 const int nt = w.t1 - w.t0, nj = w.two ? 2 * nt : nt;
                 auto k_slot = [&](int j) { return 2 * (tile0 + (w.two ? j >> 1 : j)); };
                 auto qk = [&](int j, bool landed) -> bool {
@@ -513,6 +495,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 };
                 // P . V of job j, then the scores of job j + 2, which take S from under P:
                 // the tensor cores execute in order of issue
+                bool landed2 = false;
                 auto pv = [&](int j) -> bool {
                     const int g = j & 1, n = k_slot(j) + 1, n2 = k_slot(j + 2);
                     if (!lane_wait(bar(bFull + stage(n)), phase(n))) return false;
@@ -530,16 +513,18 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     umma_commit(bar(bO + g));
                     if (!w.two || g == 1) umma_commit(bar(bFree + stage(n)));
                     ++(g ? pv1 : pv0);
-                    return !more || qk(j + 2, landed);
+                    landed2 = landed;
+                    return true;
                 };
                 w.buffers([&](int bf, int uses) { ok = ok && lane_wait(bar(bQ + bf), uses & 1); });
                 // the item before has no more use for S
-                if (w.piece > 0) ok = ok && lane_wait(bar(bX), (w.piece - 1) & 1);
-                ok = ok && qk(0, false) && (nj < 2 || qk(1, false));
-                for (int j = 0; ok && j < nj; ++j) {
+                if (i > 0) ok = ok && lane_wait(bar(bX), (i - 1) & 1);
+                for (int j = -2; ok && j < nj; ++j) {
                     if (j + 2 == max(nj, 2)) w.buffers([&](int bf, int) { umma_commit(bar(bQFree + bf)); });
-                    ok = pv(j);
+                    if (j >= 0) ok = pv(j);
+                    if (ok && j + 2 < nj) ok = qk(j + 2, landed2);
                 }
+                mbar_arrive(bar(bPieceFree + i % kPieces));
                 tile0 += nt;
             }
             // Every operation issued is done before the tensor memory is freed:
@@ -551,35 +536,62 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 if (pv1) (void)mbar_wait_bounded(bar(bO + 1), (pv1 - 1) & 1, kWaitLimitNs);
             }
         } else if (warp == 3 && lane == 0) {
-            // ---- q: tile_toks tokens x G heads are consecutive operand rows; and what the
-            // ---- joining kernel is to do with this CTA's cut item
-            int4 meta = make_int4(0, 0, 0, 0);
+            // ======================= the CTA's pieces, and q ==========================
+            // q: tile_toks tokens x G heads are consecutive operand rows
+            int4 meta = make_int4(0, 0, 0, 0);     // what the joining kernel is to do with the cut item
             const Cuts cuts(total, gridDim.x);
             const uint64_t policy = l2_policy_evict_first();
-            int done0 = 0, done1 = 0;
+            int uses0 = 0, uses1 = 0, n = 0, buf = 1, ignored = 0;
             bool ok = true;
-            Walk w(from, to);
-            while (w.next(a)) {
-                w.buffers([&](int bf, int uses) {
-                    if (ok && uses > 0) ok = lane_wait(bar(bQFree + bf), (uses - 1) & 1);
-                    if (!ok) return;
-                    const uint32_t fb = bar((FP8 ? bQRaw : bQ) + bf);
-                    mbar_arrive_expect_tx(fb, a.tile_toks * a.G * D * 2);
-                    for (int k = 0; k < C::NB; ++k)
-                        tma_load_3d(s0 + C::OFF_Q + bf * C::TILE + k * C::BLOCK, &tmq, fb, 64 * k, w.kvh * a.G,
-                                    w.s.q0 + w.tok0 + (w.two ? bf * a.tile_toks : 0), policy);
-                    ++(bf ? done1 : done0);
-                });
-                if (w.t0 == 0 && w.t1 < w.nt) {
-                    // cuts up to kSnap tiles before the item's end are inside it
-                    const int i0 = cuts.cut(static_cast<int>(blockIdx.x) + 1) - w.t1;
-                    const int c1 = cuts.at_or_before(i0 + w.nt - kSnap);
-                    meta = make_int4(w.s.q0 + w.tok0, w.toks, c1 - static_cast<int>(blockIdx.x) + 1, w.kvh);
+            auto publish = [&](const Piece& w) {
+                if (n >= kPieces) ok = lane_wait(bar(bPieceFree + n % kPieces), (n / kPieces - 1) & 1);
+                if (!ok) return;
+                pieces[n % kPieces] = w;
+                mbar_arrive(piece_bar(n));
+                ++n;
+            };
+            int k = from.k, t0 = from.t;
+            for (int b = from.b; ok && b <= to.b && b < a.B; ++b, k = 0) {
+                const Seq s = seq_of(a, b, ignored);
+                const int k1 = b == to.b ? to.k + (to.t > 0) : a.Hkv * s.RG;
+                for (; ok && k < k1; ++k, t0 = 0) {
+                    const int kvh = s.RG == 1 ? k : k / s.RG, rg = k - kvh * s.RG;
+                    const int nt = tiles_of(a, s, rg);
+                    Piece w;
+                    w.b = b, w.kvh = kvh, w.q0 = s.q0, w.L = s.L, w.ctx = s.ctx;
+                    w.tok0 = rg * 2 * a.tile_toks;
+                    w.toks = min(s.N - w.tok0, 2 * a.tile_toks);
+                    w.t0 = t0;
+                    w.t1 = b == to.b && k == to.k ? to.t : nt;
+                    w.whole = t0 == 0 && w.t1 == nt;
+                    w.two = w.toks > a.tile_toks;
+                    if (!w.two) buf ^= 1;
+                    w.buf = buf;
+                    w.uses0 = uses0, w.uses1 = uses1;
+                    publish(w);
+                    w.buffers([&](int bf, int uses) {
+                        if (ok && uses > 0) ok = lane_wait(bar(bQFree + bf), (uses - 1) & 1);
+                        if (!ok) return;
+                        const uint32_t fb = bar((FP8 ? bQRaw : bQ) + bf);
+                        mbar_arrive_expect_tx(fb, a.tile_toks * a.G * D * 2);
+                        for (int c = 0; c < C::NB; ++c)
+                            tma_load_3d(s0 + C::OFF_Q + bf * C::TILE + c * C::BLOCK, &tmq, fb, 64 * c, kvh * a.G,
+                                        w.q0 + w.tok0 + (w.two ? bf * a.tile_toks : 0), policy);
+                        ++(bf ? uses1 : uses0);
+                    });
+                    if (t0 == 0 && w.t1 < nt) {
+                        // cuts up to kSnap tiles before the item's end are inside it
+                        const int c1 = cuts.at_or_before(cuts.cut(static_cast<int>(blockIdx.x) + 1) - w.t1 + nt - kSnap);
+                        meta = make_int4(w.q0 + w.tok0, w.toks, c1 - static_cast<int>(blockIdx.x) + 1, kvh);
+                    }
                 }
             }
+            Piece none{};
+            none.b = -1;
+            if (ok) publish(none);
             reinterpret_cast<int4*>(a.workspace)[blockIdx.x] = meta;
-            if (done0) (void)mbar_wait_bounded(bar(FP8 ? bQRaw : bQ), (done0 - 1) & 1, kWaitLimitNs);
-            if (done1) (void)mbar_wait_bounded(bar((FP8 ? bQRaw : bQ) + 1), (done1 - 1) & 1, kWaitLimitNs);
+            if (uses0) (void)mbar_wait_bounded(bar(FP8 ? bQRaw : bQ), (uses0 - 1) & 1, kWaitLimitNs);
+            if (uses1) (void)mbar_wait_bounded(bar((FP8 ? bQRaw : bQ) + 1), (uses1 - 1) & 1, kWaitLimitNs);
         }
         __syncwarp();
     } else if (warp < 12) {
@@ -592,15 +604,17 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         const int tok_l = row_l / a.G, g_l = row_l - tok_l * a.G;      // its token in the row tile, its head
         int tile0 = 0, job = 0, job_o = 0;             // tiles before this piece, this and the other group's jobs
         bool ok = true;
-        Walk w(from, to);
-        while (w.next(a)) {
+        for (int i = 0;; ++i) {
+            ok = named_bar_and(1, 256, warp_wait(piece_bar(i), piece_par(i)));
+            const Piece& w = pieces[i % kPieces];
+            if (!ok || w.b < 0) break;
             const bool two = w.two;
             const int tok_t = tok_l + (two ? grp * a.tile_toks : 0);   // token in the pair of row tiles
             const bool live = tok_l < a.tile_toks && tok_t < w.toks;
             const bool warp_live = __any_sync(0xffffffffu, live);
             const int tok = live ? w.tok0 + tok_t : 0;                 // this row's drafted token
             const int row = (two ? 128 * grp : 0) + row_l;             // its place in partial sums
-            const uint32_t* mrow = a.mask != nullptr && live ? a.mask + (w.s.q0 + tok) * a.mask_s0 : nullptr;
+            const uint32_t* mrow = a.mask != nullptr && live ? a.mask + (w.q0 + tok) * a.mask_s0 : nullptr;
             float sl = fabsf(a.scale_log2), vs = 1.f;
             if constexpr (FP8) {
                 w.buffers([&](int bf, int uses) { ok = ok && warp_wait(bar(bQ + bf), uses & 1); });
@@ -608,26 +622,29 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 vs = __ldg(a.v_scale + (a.n_scale == 1 ? 0 : w.kvh));
             }
             sl = fmaxf(sl, 1.2e-38f);                  // -inf times it stays -inf
-            const int L = w.s.L, ctx = w.s.ctx;
+            const int L = w.L, ctx = w.ctx, t1 = w.t1, w_t0 = w.t0;
+            const int32_t* table = a.block_tables + w.b * a.bt_s0;
             const int npages = (L + kPageSize - 1) / kPageSize;
             const int job0 = job;
             float m = -INFINITY, l = 0.f;
             const int step = two ? 1 : 2;
-            auto page_ok = [&](int t) -> uint32_t {
-                bool good = true;
-                if (t < w.t1 && lane < kTilePages && t * kTilePages + lane < npages) {
-                    const int id = __ldg(a.block_tables + w.b * a.bt_s0 + t * kTilePages + lane);
-                    good = id >= 0 && id < num_pages;
-                }
-                return __ballot_sync(0xffffffffu, good);
+            // lanes 0-7: the tile's pages, read one tile ahead
+            auto page_id = [&](int t) -> int {
+                const int p = t * kTilePages + lane;
+                return t < t1 && lane < kTilePages && p < npages ? __ldg(table + p) : 0;
             };
-            const int tb = w.t0 + (two ? 0 : grp);
-            uint32_t pages = page_ok(tb);
-            for (int t = tb; t < w.t1; t += step, ++job) {
+            const int tb = w_t0 + (two ? 0 : grp);
+            int id_next = page_id(tb);
+            for (int t = tb; t < t1; t += step, ++job) {
                 const int p0 = t * kTile;
-                const int n = 2 * (tile0 + t - w.t0) + 1;        // ring slot of the tile's V
-                const uint32_t pages_now = pages;
-                pages = page_ok(t + step);
+                const int n = 2 * (tile0 + t - w_t0) + 1;        // ring slot of the tile's V
+                const int id = id_next;
+                id_next = page_id(t + step);
+                // The scores first: they tell that every slot up to this tile's K
+                // has landed, so the wait for V below is at most one phase ahead.
+                if (ok) ok = warp_wait(bar(bS + grp), job & 1);
+                tc_fence_after();
+                const uint32_t pages_now = __ballot_sync(0xffffffffu, id >= 0 && id < num_pages);
                 const bool inner = p0 + kTile <= ctx && pages_now == ~0u;
                 uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u}, bad[4] = {0u, 0u, 0u, 0u};
                 if (!inner) {
@@ -650,10 +667,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         vis[k] = v;
                     }
                 }
-                // The scores first: they tell that every slot up to this tile's K
-                // has landed, so the wait for V below is at most one phase ahead.
-                if (ok) ok = warp_wait(bar(bS + grp), job & 1);
-                tc_fence_after();
                 // ---- V rows that a weight of zero would not silence --------------------
                 if (p0 + kTile > ctx) {
                     const bool landed = ok && warp_wait(bar(bFull + stage(n)), phase(n));
@@ -662,7 +675,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     bool odd = false;
                     if (landed && pos >= ctx && pos < L) {
                         constexpr uint32_t EX = FP8 ? 0x7C00u : 0x7F80u;
-#pragma unroll
+#pragma unroll 4
                         for (int c = 0; c < D / 8; ++c) {
                             const uint4 x = lds128(vrow + (c >> 3) * C::BLOCK + ((c ^ row_l) & 7) * 16);
                             const uint32_t v[4] = {x.x, x.y, x.z, x.w};
@@ -784,7 +797,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     tc_fence_after();
                     for (int j = 0; ok && j < kTile; ++j) {
                         if (!(word_of(bad, j >> 5) >> (j & 31) & 1)) continue;
-                        const int id = __ldg(a.block_tables + w.b * a.bt_s0 + (p0 + j) / kPageSize);
+                        const int id = __ldg(table + (p0 + j) / kPageSize);
                         if (id < 0 || id >= num_pages) continue;
                         const int off = (p0 + j) % kPageSize;
                         const int64_t kb = id * a.kc_s0 + off * a.kc_st + w.kvh * a.kc_sh;
@@ -798,7 +811,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         const bool sees = live && (word_of(vis, j >> 5) >> (j & 31) & 1);
                         float x = 0.f;
                         if (sees) {
-                            const uint16_t* qr = a.q + (w.s.q0 + tok) * a.q_s0 + (w.kvh * a.G + g_l) * a.q_s1;
+                            const uint16_t* qr = a.q + (w.q0 + tok) * a.q_s0 + (w.kvh * a.G + g_l) * a.q_s1;
                             for (int d = 0; d < D; ++d)
                                 x += __uint_as_float(static_cast<uint32_t>(qr[d]) << 16) * at(a.k_cache, kb + d);
                             x *= a.scale_log2 * (FP8 ? __ldg(a.k_scale + (a.n_scale == 1 ? 0 : w.kvh)) : 1.f);
@@ -821,7 +834,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 }
             }
             // ---- the piece's sums ---------------------------------------------------
-            const int nt = w.t1 - w.t0;
+            const int nt = t1 - w_t0;
             const bool mine = job > job0;
             const bool theirs = !two && nt > 1 - grp;
             job_o += two ? nt : nt - (job - job0);
@@ -853,59 +866,59 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 const float M = fmaxf(m, mo);
                 const float f0 = m == -INFINITY ? 0.f : fast_exp2(m - M), f1 = mo == -INFINITY ? 0.f : fast_exp2(mo - M);
                 const float sum = (mine ? l * f0 : 0.f) + (theirs ? lo * f1 : 0.f);
-                const bool whole = w.t0 == 0 && w.t1 == w.nt;
+                const bool whole = w.whole;
                 const bool none = sum == 0.f;
-                const float k0 = whole ? (none ? 0.f : f0 * vs / sum) : f0 * vs, k1 = whole ? (none ? 0.f : f1 * vs / sum) : f1 * vs;
+                const float inv = whole ? (none ? 0.f : vs / sum) : vs, k0 = f0 * inv, k1 = f1 * inv;
                 const int h = w.kvh * a.G + g_l;
-                const int slot = 2 * static_cast<int>(blockIdx.x) + (w.t0 == 0 ? 1 : 0);
+                const int slot = 2 * static_cast<int>(blockIdx.x) + (w_t0 == 0 ? 1 : 0);
                 float* part = part_o<D>(a.workspace, gridDim.x, slot, row);
                 if (live && (two || grp == 0)) {
                     if (!whole) {
                         *reinterpret_cast<float2*>(part_ml(a.workspace, slot, row)) = make_float2(M, sum);
                     } else if (a.lse) {
-                        a.lse[(w.s.q0 + tok) * a.l_s0 + h * a.l_s1] =
+                        a.lse[(w.q0 + tok) * a.l_s0 + h * a.l_s1] =
                             none ? -INFINITY : (M + __log2f(sum)) * 0.69314718055994530942f;
                     }
                 }
                 // Two row tiles: all of this row's columns; else each group half of them.
                 // A whole item's output goes through q's buffer (the warp's own 32
                 // rows), so that the warp writes rows and not columns.
-                const int c0 = two ? 0 : grp * (D / 64), c1 = two ? D / 32 : c0 + D / 64;
+                const int c0 = two ? 0 : grp * (D / 32), c1 = two ? D / 16 : c0 + D / 32;  // 16 columns each
                 const uint32_t stage_row = s0 + C::OFF_Q + (two ? grp : w.buf) * C::TILE + row_l * 128;
 #pragma unroll 1
                 for (int c = c0; c < c1; ++c) {
-                    uint32_t x[32], y[32];
-                    if (mine) tmem_ld32(tO + 32 * c, x);
-                    if (theirs) tmem_ld32(tl + 256 * (1 - grp) + C::O_COL + 32 * c, y);
+                    uint32_t x[16], y[16];
+                    if (mine) tmem_ld16(tO + 16 * c, x);
+                    if (theirs) tmem_ld16(tl + 256 * (1 - grp) + C::O_COL + 16 * c, y);
                     tmem_wait_ld();
                     pin(x);
                     pin(y);
-                    float o[32];
+                    float o[16];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
+                    for (int e = 0; e < 16; ++e) {
                         o[e] = mine ? __uint_as_float(x[e]) * k0 : 0.f;
                         if (theirs) o[e] = fmaf(__uint_as_float(y[e]), k1, o[e]);
                     }
                     if (whole) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int ch = 4 * c + e;
+                        for (int e = 0; e < 2; ++e) {
+                            const int ch = 2 * c + e;
                             sts128u(stage_row + (ch >> 3) * C::BLOCK + ((ch ^ row_l) & 7) * 16, pack_bf16(o[8 * e], o[8 * e + 1]),
                                     pack_bf16(o[8 * e + 2], o[8 * e + 3]), pack_bf16(o[8 * e + 4], o[8 * e + 5]),
                                     pack_bf16(o[8 * e + 6], o[8 * e + 7]));
                         }
                     } else if (live) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            *reinterpret_cast<float4*>(part + static_cast<int64_t>(8 * c + e) * kRows * 4) =
+                        for (int e = 0; e < 4; ++e)
+                            *reinterpret_cast<float4*>(part + static_cast<int64_t>(4 * c + e) * kRows * 4) =
                                 make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                     }
                 }
                 if (whole) {
                     __syncwarp();
-                    const int64_t off = live ? (w.s.q0 + tok) * a.o_s0 + h * a.o_s1 : -1;  // this lane's row
-                    const int per_row = 4 * (c1 - c0);                                      // 16-byte chunks: 16, 8 or 4
-                    const int sub = lane / per_row, ch = 4 * c0 + lane - sub * per_row;
+                    const int64_t off = live ? (w.q0 + tok) * a.o_s0 + h * a.o_s1 : -1;  // this lane's row
+                    const int per_row = 2 * (c1 - c0);                                      // 16-byte chunks: 16, 8 or 4
+                    const int sub = lane / per_row, ch = 2 * c0 + lane - sub * per_row;
 #pragma unroll 4
                     for (int i = 0; i < per_row; ++i) {
                         const int r = i * (32 / per_row) + sub;
@@ -917,7 +930,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             }
             fence_proxy_async_smem();                  // q's next copy comes after the staged rows
             __syncwarp();
-            if (lane == 0) w.buffers([&](int bf, int) { mbar_arrive(bar(bQFree + bf)); });
+            if (lane == 0) {
+                w.buffers([&](int bf, int) { mbar_arrive(bar(bQFree + bf)); });
+                mbar_arrive(bar(bPieceFree + i % kPieces));
+            }
             tc_fence_before();
             if (!two) ok = named_bar_and(1, 256, ok);  // either group's O is read by both
             tile0 += nt;
@@ -929,8 +945,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         constexpr int CH = D / 16;  // 16-byte chunks of a raw row
         int n = 0;
         bool ok = true;
-        Walk w(from, to);
-        while (ok && w.next(a)) {
+        for (int i = 0; ok; ++i) {
+            ok = warp_wait(piece_bar(i), piece_par(i));
+            const Piece w = pieces[i % kPieces];
+            if (!ok || w.b < 0) break;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(bPieceFree + i % kPieces));
             w.buffers([&](int bf, int uses) {
                 ok = ok && warp_wait(bar(bQRaw + bf), uses & 1);
                 if (!ok) return;
