@@ -17,14 +17,18 @@
 // item, the start of another), which a second kernel joins.
 //
 // A CTA's roles, per tile:
-//   warps 0, 2    TMA tile loads of K and of V into one ring (a warp starts a
-//                 16-row x 128-byte copy in about 85 cycles: one for both would
-//                 be the limit). Pages that do not exist are read out of
-//                 range, which fills zeros
-//   warp 3        walks the CTA's items, hands the pieces to the other roles, and
-//                 loads q by TMA
-//   warp 1        S = Q . K^T and O += P . V (M = 128; P from tensor memory, V
-//                 as an MN-major operand: nothing is transposed)
+//   warp 0        walks the CTA's items, hands the pieces to the other roles, and
+//                 loads q and K by TMA
+//   warp 2        TMA tile loads of V, into the same ring (a warp starts a 16-row
+//                 x 128-byte copy in about 85 cycles: one for both would be the
+//                 limit). Pages that do not exist are read out of range, which
+//                 fills zeros
+//   warps 1, 3    one thread each, for one softmax group: S = Q . K^T and O += P . V
+//                 (M = 128; P from tensor memory, V as an MN-major operand:
+//                 nothing is transposed). While the operands stream, shared
+//                 memory answers a barrier in 150 cycles or more; with one
+//                 thread for both groups the tensor cores stood still
+//                 meanwhile (2900 cycles a tile and row tile, of 1024)
 //   warps 4 - 7,
 //   warps 8 - 11  two softmax groups, each with S, P and O of its own in tensor
 //                 memory. One row tile: both have the same rows and take the
@@ -75,7 +79,9 @@ struct Cfg {
     static constexpr int RAW = kTile * D;                  // FP8 tile as it lands
     static constexpr int RBOX = D >= 128 ? 128 : D;        // its row (and swizzle span)
     // Rings of K and V tiles in turn: operand tiles, and (FP8) tiles of bytes.
-    static constexpr int ST = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
+    // (bf16: an even number, so that either copy warp has stages of its own and
+    // its waits for a free one are never two phases behind.)
+    static constexpr int ST = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);
     static constexpr int RST = FP8 ? (D == 128 ? 3 : 6) : 0;
     static constexpr int THREADS = FP8 ? 512 : 384;
     // Registers a thread: launched with 168 (128), dealt out again by role.
@@ -85,7 +91,7 @@ struct Cfg {
     static constexpr int OFF_R = OFF_T + ST * TILE;
     static constexpr int OFF_SC = OFF_R + RST * RAW;       // FP8: [2][128] floats, 2^-k of each row
     static constexpr int OFF_BAR = OFF_SC + (FP8 ? kRows * 4 : 0);
-    static constexpr int NBAR = 2 * ST + 2 * RST + 15 + 2 * kPieces;
+    static constexpr int NBAR = 2 * ST + 2 * RST + 14 + 3 * kPieces;
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
     static constexpr int OFF_PIECE = OFF_MISC + 192;       // [kPieces] Piece
     static constexpr int SMEM = OFF_PIECE + kPieces * 64 + 1024;  // + alignment slack
@@ -177,6 +183,42 @@ __device__ __forceinline__ Place place_of(const TreeArgs& a, const Seq& s, int b
     }
     return p;
 }
+
+// The pieces of items between two places, in order.
+struct Walk {
+    int b, k, t0, t1, nt, kvh, rg;
+    Seq s;
+    Place end;
+    bool first;
+    __device__ __forceinline__ Walk(const Place& from, const Place& to) : b(from.b), k(from.k), t0(from.t), end(to), first(true) {}
+    // Next piece [t0, t1) of item (b, k); false at the end.
+    __device__ __forceinline__ bool next(const TreeArgs& a) {
+        int ignored = 0;
+        bool load = first;
+        if (!first) {
+            t0 = 0;
+            load = ++k >= a.Hkv * s.RG;
+            if (load) {
+                k = 0;
+                ++b;
+            }
+        }
+        first = false;
+        for (;; ++b, k = 0, load = true) {  // past the sequences without drafted tokens
+            if (b >= a.B || !in_range()) return false;
+            if (load) s = seq_of(a, b, ignored);
+            if (k < a.Hkv * s.RG) break;
+        }
+        kvh = s.RG == 1 ? k : k / s.RG;
+        rg = k - kvh * s.RG;
+        nt = tiles_of(a, s, rg);
+        t1 = b == end.b && k == end.k ? end.t : nt;
+        return true;
+    }
+    __device__ __forceinline__ bool in_range() const {
+        return b < end.b || (b == end.b && (k < end.k || (k == end.k && end.t > t0)));
+    }
+};
 
 // A piece: tiles [t0, t1) of an item (its drafted tokens [tok0, tok0 + toks)).
 struct Piece {
@@ -285,7 +327,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     const uint32_t s0 = smem_u32(smem);
     enum : int { bFull = 0, bFree = C::ST, bRawFull = 2 * C::ST, bRawFree = bRawFull + C::RST, bS = bRawFree + C::RST,
                  bP = bS + 2, bO = bP + 4, bQ = bO + 2, bQFree = bQ + 2, bQRaw = bQFree + 2, bX = bQRaw + 2,
-                 bPiece = bX + 1, bPieceFree = bPiece + kPieces };
+                 bPiece = bX + kPieces, bPieceFree = bPiece + kPieces };
     static_assert(bPieceFree + kPieces == C::NBAR, "barriers");
     auto bar = [&](int i) -> uint32_t { return s0 + C::OFF_BAR + 8 * i; };
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
@@ -302,7 +344,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     if (tid == 0) {
         for (int i = 0; i < C::ST; ++i) {
             mbar_init(bar(bFull + i), FP8 ? 4 : 1);
-            mbar_init(bar(bFree + i), 1);
+            mbar_init(bar(bFree + i), 2);  // either MMA thread: its use, or a tile of the other group seen
         }
         for (int i = 0; i < C::RST; ++i) {
             mbar_init(bar(bRawFull + i), 1);
@@ -314,11 +356,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             mbar_init(bar(bP + 2 * w + 1), 4);
             mbar_init(bar(bO + w), 1);
             mbar_init(bar(bQ + w), FP8 ? 4 : 1);
-            mbar_init(bar(bQFree + w), 9);  // the last Q . K^T, and the softmax warps (row scales, staged output)
+            mbar_init(bar(bQFree + w), 10);  // either group's last Q . K^T, and the softmax warps (staged output)
             mbar_init(bar(bQRaw + w), 1);
         }
-        mbar_init(bar(bX), 8);
         for (int i = 0; i < kPieces; ++i) {
+            mbar_init(bar(bX + i), 8);
             mbar_init(bar(bPiece + i), 1);
             mbar_init(bar(bPieceFree + i), FP8 ? 15 : 11);  // copies, MMA, softmax, conversion
         }
@@ -409,27 +451,81 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         reg_dec<C::REG_IO>();
         if (warp == 0 || warp == 2) {
             // ======================= copies ===========================================
-            const int v = warp >> 1;                                       // K or V
+            // Warp 0 walks the pieces, hands them over, and loads q and K; warp 2 loads V.
+            const int v = warp >> 1;
             constexpr int RING = FP8 ? C::RST : C::ST;
             constexpr int FULL = FP8 ? bRawFull : bFull, FREE = FP8 ? bRawFree : bFree;
             constexpr int COPIES = FP8 ? kTilePages : kTilePages * C::NB;  // per tile
             const int pg = lane % kTilePages, blk = lane / kTilePages;     // this lane's copy
             const bool hnd = a.layout == PKV_HND;
             const uint64_t policy = l2_policy_evict_first();
-            int n = v;
-            bool ok = true;
+            const Cuts cuts(total, gridDim.x);
+            int n = v, uses0 = 0, uses1 = 0, buf = 1;
+            int4 meta = make_int4(0, 0, 0, 0);     // what the joining kernel is to do with the cut item
+            bool ok = true, bad = false;
+            Walk walk(from, to);
             for (int i = 0; ok; ++i) {
-                ok = warp_wait(piece_bar(i), piece_par(i));
-                const Piece w = pieces[i % kPieces];
-                if (!ok || w.b < 0) break;
+                Piece w;
+                int q_wanted = 0;                  // buffers of q (bits) that are not loaded yet
+                if (v == 0) {
+                    w.b = walk.next(a) ? walk.b : -1;
+                    if (w.b >= 0) {
+                        w.kvh = walk.kvh, w.q0 = walk.s.q0, w.L = walk.s.L, w.ctx = walk.s.ctx;
+                        w.tok0 = walk.rg * 2 * a.tile_toks;
+                        w.toks = min(walk.s.N - w.tok0, 2 * a.tile_toks);
+                        w.t0 = walk.t0, w.t1 = walk.t1;
+                        w.whole = w.t0 == 0 && w.t1 == walk.nt;
+                        w.two = w.toks > a.tile_toks;
+                        if (!w.two) buf ^= 1;
+                        w.buf = buf;
+                        w.uses0 = uses0, w.uses1 = uses1;
+                        q_wanted = w.two ? 3 : 1 << buf;
+                        if (w.t0 == 0 && w.t1 < walk.nt) {
+                            // cuts up to kSnap tiles before the item's end are inside it
+                            const int c1 = cuts.at_or_before(cuts.cut(static_cast<int>(blockIdx.x) + 1) - w.t1 + walk.nt - kSnap);
+                            meta = make_int4(w.q0 + w.tok0, w.toks, c1 - static_cast<int>(blockIdx.x) + 1, w.kvh);
+                        }
+                    }
+                    if (i >= kPieces && !warp_wait(bar(bPieceFree + i % kPieces), (i / kPieces - 1) & 1)) break;
+                    if (lane == 0) {
+                        pieces[i % kPieces] = w;
+                        mbar_arrive(piece_bar(i));
+                    }
+                    __syncwarp();
+                } else {
+                    if (!warp_wait(piece_bar(i), piece_par(i))) break;
+                    w = pieces[i % kPieces];
+                    __syncwarp();
+                    if (lane == 0 && w.b >= 0) mbar_arrive(bar(bPieceFree + i % kPieces));
+                }
+                if (w.b < 0) break;
+                // q of this piece, into every wanted buffer that is free: tile_toks
+                // tokens x G heads are consecutive operand rows
+                auto load_q = [&]() {
+#pragma unroll
+                    for (int bf = 0; bf < 2; ++bf) {
+                        int& uses = bf ? uses1 : uses0;
+                        if (!(q_wanted >> bf & 1)) continue;
+                        if (uses > 0 && !__all_sync(0xffffffffu, mbar_test_wait(bar(bQFree + bf), (uses - 1) & 1))) continue;
+                        const uint32_t fb = bar((FP8 ? bQRaw : bQ) + bf);
+                        if (lane == 0) mbar_arrive_expect_tx(fb, a.tile_toks * a.G * D * 2);
+                        __syncwarp();
+                        if (lane < C::NB)
+                            tma_load_3d(s0 + C::OFF_Q + bf * C::TILE + lane * C::BLOCK, &tmq, fb, 64 * lane, w.kvh * a.G,
+                                        w.q0 + w.tok0 + (w.two ? bf * a.tile_toks : 0), policy);
+                        __syncwarp();
+                        ++uses;
+                        q_wanted &= ~(1 << bf);
+                    }
+                };
+                if (q_wanted) load_q();
                 const int npages = (w.L + kPageSize - 1) / kPageSize;
                 auto page_at = [&](int t) -> int {
                     const int p = t * kTilePages + pg;
                     return p < npages && t < w.t1 ? __ldg(a.block_tables + w.b * a.bt_s0 + p) : -1;
                 };
                 int nxt = page_at(w.t0);
-                bool bad = false;
-                for (int t = w.t0; ok && t < w.t1; ++t, n += 2) {
+                for (int t = w.t0; t < w.t1; ++t, n += 2) {
                     int id = nxt;
                     nxt = page_at(t + 1);
                     if (id < 0 || id >= num_pages) {
@@ -437,9 +533,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         id = static_cast<int>(num_pages);  // out of range: the copy fills zeros
                     }
                     const int st = n % RING;
-                    if (n >= RING && !warp_wait(bar(FREE + st), (n / RING - 1) & 1)) {
-                        ok = false;
-                        break;
+                    if (n >= RING) {
+                        const uint32_t fr = bar(FREE + st), par = (n / RING - 1) & 1;
+                        // the ring may be waiting for this very piece's q
+                        while (ok && q_wanted && !__all_sync(0xffffffffu, mbar_try_wait_suspend(fr, par, 1000u))) {
+                            load_q();
+                            ok = !__any_sync(0xffffffffu, *abort_flag != 0);
+                        }
+                        ok = ok && warp_wait(fr, par);
+                        if (!ok) break;
                     }
                     const uint32_t fb = bar(FULL + st);
                     if (lane == 0) mbar_arrive_expect_tx(fb, FP8 ? C::RAW : C::TILE);
@@ -452,146 +554,106 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     }
                     __syncwarp();
                 }
-                if (bad && blk == 0 && v == 0) flag_error(a.err, PKV_FLAG_PAGE_RANGE);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(bPieceFree + i % kPieces));
+                // q's last buffer: free once the piece before has its output written
+                if (ok && (q_wanted & 1) && uses0 > 0) ok = warp_wait(bar(bQFree), (uses0 - 1) & 1);
+                if (ok && (q_wanted & 2) && uses1 > 0) ok = warp_wait(bar(bQFree + 1), (uses1 - 1) & 1);
+                if (ok && q_wanted) load_q();
             }
-            // Copies under way land before the CTA may exit.
+            if (bad && blk == 0 && v == 0) flag_error(a.err, PKV_FLAG_PAGE_RANGE);
             if (lane == 0) {
-                // (slots whose stage neither copy warp has taken again)
+                if (v == 0) reinterpret_cast<int4*>(a.workspace)[blockIdx.x] = meta;
+                // Copies under way land before the CTA may exit (slots whose stage
+                // neither copy warp has taken again).
                 for (int i = n - 2; i >= 0 && i > n - 1 - v - RING; i -= 2)
                     (void)mbar_wait_bounded(bar(FULL + i % RING), (i / RING) & 1, kWaitLimitNs);
+                if (uses0) (void)mbar_wait_bounded(bar(FP8 ? bQRaw : bQ), (uses0 - 1) & 1, kWaitLimitNs);
+                if (uses1) (void)mbar_wait_bounded(bar((FP8 ? bQRaw : bQ) + 1), (uses1 - 1) & 1, kWaitLimitNs);
             }
-        } else if (warp == 1 && lane == 0) {
-            // ======================= tensor-core issue (one thread) ===================
+        } else if (lane == 0) {
+            // ======================= tensor-core issue, one thread per group ==========
+            const int g = warp >> 1;
             constexpr int FMT = FP8 ? 0 : 1;  // f16 or bf16 operands
             // the sign of softmax_scale goes into q (bit 13 negates A)
             const uint32_t idesc_qk = umma_idesc(128, kTile, FMT, FMT, false, false) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
             constexpr uint32_t kIdescPv = umma_idesc(128, D, FMT, FMT, false, true);
-            int tile0 = 0;                             // tiles before this piece
-            int pv0 = 0, pv1 = 0, qk0 = 0, qk1 = 0;    // P . V and Q . K^T issued per group
+            const uint32_t tS = tmem + 256 * g;
+            int tile0 = 0;                    // tiles before this piece
+            int n_qk = 0, n_pv = 0;           // Q . K^T and P . V issued
             bool ok = true;
             for (int i = 0; ok; ++i) {
                 ok = lane_wait(piece_bar(i), piece_par(i));
                 const Piece w = pieces[i % kPieces];
                 if (!ok || w.b < 0) break;
-                const int nt = w.t1 - w.t0, nj = w.two ? 2 * nt : nt;
-                auto k_slot = [&](int j) { return 2 * (tile0 + (w.two ? j >> 1 : j)); };
-                auto qk = [&](int j, bool landed) -> bool {
-                    const int g = j & 1, n = k_slot(j);
-                    if (!landed && !lane_wait(bar(bFull + stage(n)), phase(n))) return false;
-                    tc_fence_after();
-                    const uint64_t q = umma_desc_sw128(s0 + C::OFF_Q + (w.two ? g : w.buf) * C::TILE, 16, 1024);
-                    const uint64_t kt = umma_desc_sw128(s0 + C::OFF_T + stage(n) * C::TILE, 16, 1024);
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t step = ((k >> 2) * C::BLOCK + (k & 3) * 32) >> 4;
-                        umma_ss(tmem + 256 * g, q + step, kt + step, idesc_qk, k > 0);
-                    }
-                    umma_commit(bar(bS + g));
-                    if (!w.two || g == 1) umma_commit(bar(bFree + stage(n)));
-                    ++(g ? qk1 : qk0);
-                    return true;
-                };
-                // P . V of job j, then the scores of job j + 2, which take S from under P:
-                // the tensor cores execute in order of issue
-                bool landed2 = false;
-                auto pv = [&](int j) -> bool {
-                    const int g = j & 1, n = k_slot(j) + 1, n2 = k_slot(j + 2);
-                    if (!lane_wait(bar(bFull + stage(n)), phase(n))) return false;
-                    const bool more = j + 2 < nj, landed = more && mbar_test_wait(bar(bFull + stage(n2)), phase(n2));
-                    const uint64_t vt = umma_desc_sw128(s0 + C::OFF_T + stage(n) * C::TILE, C::BLOCK, 1024);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {      // the softmax hands P over in halves
-                        if (!lane_wait(bar(bP + 2 * g + h), (g ? pv1 : pv0) & 1)) return false;
-                        tc_fence_after();
-#pragma unroll
-                        for (int k = 4 * h; k < 4 * h + 4; ++k)
-                            umma_ts(tmem + 256 * g + C::O_COL, tmem + 256 * g + C::P_COL + 8 * k, vt + k * (2048 >> 4),
-                                    kIdescPv, j > 1 || k > 0);
-                    }
-                    umma_commit(bar(bO + g));
-                    if (!w.two || g == 1) umma_commit(bar(bFree + stage(n)));
-                    ++(g ? pv1 : pv0);
-                    landed2 = landed;
-                    return true;
-                };
+                const int nt = w.t1 - w.t0, step = w.two ? 1 : 2;
                 w.buffers([&](int bf, int uses) { ok = ok && lane_wait(bar(bQ + bf), uses & 1); });
                 // the item before has no more use for S
-                if (i > 0) ok = ok && lane_wait(bar(bX), (i - 1) & 1);
-                for (int j = -2; ok && j < nj; ++j) {
-                    if (j + 2 == max(nj, 2)) w.buffers([&](int bf, int) { umma_commit(bar(bQFree + bf)); });
-                    if (j >= 0) ok = pv(j);
-                    if (ok && j + 2 < nj) ok = qk(j + 2, landed2);
+                if (i > 0) ok = ok && lane_wait(bar(bX + (i - 1) % kPieces), ((i - 1) / kPieces) & 1);
+                const uint64_t q = umma_desc_sw128(s0 + C::OFF_Q + (w.two ? g : w.buf) * C::TILE, 16, 1024);
+                const int first = w.two ? 0 : g;
+                // Both threads see every slot land, in order, and both release it
+                // (the other group's tiles by a plain arrival): a parity wait is
+                // then never two phases off.
+                auto landed = [&](int n) -> bool { return lane_wait(bar(bFull + stage(n)), phase(n)); };
+                auto see_tile = [&](int t) -> bool {
+                    const int n = 2 * (tile0 + t);
+                    if (!landed(n)) return false;
+                    mbar_arrive(bar(bFree + stage(n)));
+                    if (!landed(n + 1)) return false;
+                    mbar_arrive(bar(bFree + stage(n + 1)));
+                    return true;
+                };
+                if (first > 0) ok = ok && see_tile(0);
+                // P . V of a tile, then the scores of this group's next one, which take S
+                // from under P: the tensor cores execute in order of issue
+                for (int t = first - step; ok && t < nt; t += step) {
+                    const int n = 2 * (tile0 + t) + 1, n2 = 2 * (tile0 + t + step);  // V here, the next K
+                    const bool more = t + step < nt;
+                    if (t >= 0) {
+                        if (!landed(n)) ok = false;
+                        const uint64_t vt = umma_desc_sw128(s0 + C::OFF_T + stage(n) * C::TILE, C::BLOCK, 1024);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {      // the softmax hands P over in halves
+                            ok = ok && lane_wait(bar(bP + 2 * g + h), n_pv & 1);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int k = 4 * h; k < 4 * h + 4; ++k)
+                                umma_ts(tS + C::O_COL, tS + C::P_COL + 8 * k, vt + k * (2048 >> 4), kIdescPv, t > first || k > 0);
+                        }
+                        if (!ok) break;
+                        umma_commit(bar(bO + g));
+                        umma_commit(bar(bFree + stage(n)));
+                        ++n_pv;
+                        if (!w.two && t + 1 < nt) ok = see_tile(t + 1);
+                    }
+                    if (ok && more) {
+                        ok = landed(n2);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t kt = umma_desc_sw128(s0 + C::OFF_T + stage(n2) * C::TILE, 16, 1024);
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint32_t at = ((k >> 2) * C::BLOCK + (k & 3) * 32) >> 4;
+                            umma_ss(tS, q + at, kt + at, idesc_qk, k > 0);
+                        }
+                        umma_commit(bar(bS + g));
+                        umma_commit(bar(bFree + stage(n2)));
+                        ++n_qk;
+                        // the last scores: q is done with
+                        if (t + 2 * step >= nt) w.buffers([&](int bf, int) { umma_commit(bar(bQFree + bf)); });
+                    }
                 }
+                if (!ok) break;
+                if (first >= nt) w.buffers([&](int bf, int) { mbar_arrive(bar(bQFree + bf)); });  // no tile for this group
                 mbar_arrive(bar(bPieceFree + i % kPieces));
                 tile0 += nt;
             }
             // Every operation issued is done before the tensor memory is freed:
             // the softmax groups wait for their last O, and give-ups for both here.
             if (!ok) {
-                if (qk0) (void)mbar_wait_bounded(bar(bS), (qk0 - 1) & 1, kWaitLimitNs);
-                if (qk1) (void)mbar_wait_bounded(bar(bS + 1), (qk1 - 1) & 1, kWaitLimitNs);
-                if (pv0) (void)mbar_wait_bounded(bar(bO), (pv0 - 1) & 1, kWaitLimitNs);
-                if (pv1) (void)mbar_wait_bounded(bar(bO + 1), (pv1 - 1) & 1, kWaitLimitNs);
+                if (n_qk) (void)mbar_wait_bounded(bar(bS + g), (n_qk - 1) & 1, kWaitLimitNs);
+                if (n_pv) (void)mbar_wait_bounded(bar(bO + g), (n_pv - 1) & 1, kWaitLimitNs);
             }
-        } else if (warp == 3 && lane == 0) {
-            // ======================= the CTA's pieces, and q ==========================
-            // q: tile_toks tokens x G heads are consecutive operand rows
-            int4 meta = make_int4(0, 0, 0, 0);     // what the joining kernel is to do with the cut item
-            const Cuts cuts(total, gridDim.x);
-            const uint64_t policy = l2_policy_evict_first();
-            int uses0 = 0, uses1 = 0, n = 0, buf = 1, ignored = 0;
-            bool ok = true;
-            auto publish = [&](const Piece& w) {
-                if (n >= kPieces) ok = lane_wait(bar(bPieceFree + n % kPieces), (n / kPieces - 1) & 1);
-                if (!ok) return;
-                pieces[n % kPieces] = w;
-                mbar_arrive(piece_bar(n));
-                ++n;
-            };
-            int k = from.k, t0 = from.t;
-            for (int b = from.b; ok && b <= to.b && b < a.B; ++b, k = 0) {
-                const Seq s = seq_of(a, b, ignored);
-                const int k1 = b == to.b ? to.k + (to.t > 0) : a.Hkv * s.RG;
-                for (; ok && k < k1; ++k, t0 = 0) {
-                    const int kvh = s.RG == 1 ? k : k / s.RG, rg = k - kvh * s.RG;
-                    const int nt = tiles_of(a, s, rg);
-                    Piece w;
-                    w.b = b, w.kvh = kvh, w.q0 = s.q0, w.L = s.L, w.ctx = s.ctx;
-                    w.tok0 = rg * 2 * a.tile_toks;
-                    w.toks = min(s.N - w.tok0, 2 * a.tile_toks);
-                    w.t0 = t0;
-                    w.t1 = b == to.b && k == to.k ? to.t : nt;
-                    w.whole = t0 == 0 && w.t1 == nt;
-                    w.two = w.toks > a.tile_toks;
-                    if (!w.two) buf ^= 1;
-                    w.buf = buf;
-                    w.uses0 = uses0, w.uses1 = uses1;
-                    publish(w);
-                    w.buffers([&](int bf, int uses) {
-                        if (ok && uses > 0) ok = lane_wait(bar(bQFree + bf), (uses - 1) & 1);
-                        if (!ok) return;
-                        const uint32_t fb = bar((FP8 ? bQRaw : bQ) + bf);
-                        mbar_arrive_expect_tx(fb, a.tile_toks * a.G * D * 2);
-                        for (int c = 0; c < C::NB; ++c)
-                            tma_load_3d(s0 + C::OFF_Q + bf * C::TILE + c * C::BLOCK, &tmq, fb, 64 * c, kvh * a.G,
-                                        w.q0 + w.tok0 + (w.two ? bf * a.tile_toks : 0), policy);
-                        ++(bf ? uses1 : uses0);
-                    });
-                    if (t0 == 0 && w.t1 < nt) {
-                        // cuts up to kSnap tiles before the item's end are inside it
-                        const int c1 = cuts.at_or_before(cuts.cut(static_cast<int>(blockIdx.x) + 1) - w.t1 + nt - kSnap);
-                        meta = make_int4(w.q0 + w.tok0, w.toks, c1 - static_cast<int>(blockIdx.x) + 1, kvh);
-                    }
-                }
-            }
-            Piece none{};
-            none.b = -1;
-            if (ok) publish(none);
-            reinterpret_cast<int4*>(a.workspace)[blockIdx.x] = meta;
-            if (uses0) (void)mbar_wait_bounded(bar(FP8 ? bQRaw : bQ), (uses0 - 1) & 1, kWaitLimitNs);
-            if (uses1) (void)mbar_wait_bounded(bar((FP8 ? bQRaw : bQ) + 1), (uses1 - 1) & 1, kWaitLimitNs);
         }
         __syncwarp();
     } else if (warp < 12) {
@@ -858,7 +920,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(bX));       // S may be written for the next item
+            if (lane == 0) mbar_arrive(bar(bX + i % kPieces));  // S may be written for the next item
             if (mine) ok = warp_wait(bar(bO + grp), (job - 1) & 1);
             if (theirs) ok = ok && warp_wait(bar(bO + 1 - grp), (job_o - 1) & 1);
             tc_fence_after();
