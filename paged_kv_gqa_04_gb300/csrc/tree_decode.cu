@@ -91,7 +91,7 @@ struct Cfg {
     static constexpr int OFF_R = OFF_T + ST * TILE;
     static constexpr int OFF_SC = OFF_R + RST * RAW;       // FP8: [2][128] floats, 2^-k of each row
     static constexpr int OFF_BAR = OFF_SC + (FP8 ? kRows * 4 : 0);
-    static constexpr int NBAR = 2 * ST + 2 * RST + 14 + 3 * kPieces;
+    static constexpr int NBAR = 2 * ST + 2 * RST + 16 + 3 * kPieces;
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
     static constexpr int OFF_PIECE = OFF_MISC + 192;       // [kPieces] Piece
     static constexpr int SMEM = OFF_PIECE + kPieces * 64 + 1024;  // + alignment slack
@@ -253,20 +253,23 @@ __device__ __forceinline__ void pin(uint32_t (&r)[N]) {
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 // One thread's MMA and commit (the warp forms elect a lane at each call).
-// D (tensor memory) = A . B^T (+ D), both operands in shared memory.
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// Descriptors as a start address (>> 4, low word with the leading offset) and
+// a constant high word: a step along K is one 32-bit add.
+// D (tensor memory) = A . B^T (+ D unless FIRST), both operands in shared memory.
+template <bool FIRST>
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "n"(FIRST ? 0 : 1)
         : "memory");
 }
 // A in tensor memory: 16-bit values, two per 32-bit column.
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 __device__ __forceinline__ void umma_commit(uint32_t bar) {
@@ -327,8 +330,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     const uint32_t s0 = smem_u32(smem);
     enum : int { bFull = 0, bFree = C::ST, bRawFull = 2 * C::ST, bRawFree = bRawFull + C::RST, bS = bRawFree + C::RST,
                  bP = bS + 2, bO = bP + 4, bQ = bO + 2, bQFree = bQ + 2, bQRaw = bQFree + 2, bX = bQRaw + 2,
-                 bPiece = bX + kPieces, bPieceFree = bPiece + kPieces };
-    static_assert(bPieceFree + kPieces == C::NBAR, "barriers");
+                 bPiece = bX + kPieces, bPieceFree = bPiece + kPieces, bTurn = bPieceFree + kPieces };
+    static_assert(bTurn + 2 == C::NBAR, "barriers");
     auto bar = [&](int i) -> uint32_t { return s0 + C::OFF_BAR + 8 * i; };
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
@@ -358,6 +361,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             mbar_init(bar(bQ + w), FP8 ? 4 : 1);
             mbar_init(bar(bQFree + w), 10);  // either group's last Q . K^T, and the softmax warps (staged output)
             mbar_init(bar(bQRaw + w), 1);
+            mbar_init(bar(bTurn + w), 1);
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(bar(bX + i), 8);
@@ -576,9 +580,13 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             // the sign of softmax_scale goes into q (bit 13 negates A)
             const uint32_t idesc_qk = umma_idesc(128, kTile, FMT, FMT, false, false) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
             constexpr uint32_t kIdescPv = umma_idesc(128, D, FMT, FMT, false, true);
+            // 128-byte-swizzled operands, 1024 bytes between groups of 8 rows
+            constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
+            auto desc_lo = [](uint32_t addr, uint32_t lead) { return ((addr >> 4) & 0x3FFFu) | (lead >> 4) << 16; };
             const uint32_t tS = tmem + 256 * g;
             int tile0 = 0;                    // tiles before this piece
             int n_qk = 0, n_pv = 0;           // Q . K^T and P . V issued
+            int turns = 0;                    // of items with two row tiles
             bool ok = true;
             for (int i = 0; ok; ++i) {
                 ok = lane_wait(piece_bar(i), piece_par(i));
@@ -588,7 +596,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 w.buffers([&](int bf, int uses) { ok = ok && lane_wait(bar(bQ + bf), uses & 1); });
                 // the item before has no more use for S
                 if (i > 0) ok = ok && lane_wait(bar(bX + (i - 1) % kPieces), ((i - 1) / kPieces) & 1);
-                const uint64_t q = umma_desc_sw128(s0 + C::OFF_Q + (w.two ? g : w.buf) * C::TILE, 16, 1024);
+                const uint32_t q = desc_lo(s0 + C::OFF_Q + (w.two ? g : w.buf) * C::TILE, 16);
                 const int first = w.two ? 0 : g;
                 // Both threads see every slot land, in order, and both release it
                 // (the other group's tiles by a plain arrival): a parity wait is
@@ -608,33 +616,54 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 for (int t = first - step; ok && t < nt; t += step) {
                     const int n = 2 * (tile0 + t) + 1, n2 = 2 * (tile0 + t + step);  // V here, the next K
                     const bool more = t + step < nt;
-                    if (t >= 0) {
-                        if (!landed(n)) ok = false;
-                        const uint64_t vt = umma_desc_sw128(s0 + C::OFF_T + stage(n) * C::TILE, C::BLOCK, 1024);
+                    if (t >= 0) ok = landed(n);
+                    const uint32_t vt = desc_lo(s0 + C::OFF_T + stage(n) * C::TILE, C::BLOCK);
+                    const uint32_t kt = desc_lo(s0 + C::OFF_T + stage(n2) * C::TILE, 16);
+                    const uint32_t more_o = t > first;  // O goes on, or starts
+                    auto pv = [&](int h) {             // half h of the tile's positions
+                        tc_fence_after();
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {      // the softmax hands P over in halves
-                            ok = ok && lane_wait(bar(bP + 2 * g + h), n_pv & 1);
-                            if (!ok) break;
-                            tc_fence_after();
-#pragma unroll
-                            for (int k = 4 * h; k < 4 * h + 4; ++k)
-                                umma_ts(tS + C::O_COL, tS + C::P_COL + 8 * k, vt + k * (2048 >> 4), kIdescPv, t > first || k > 0);
-                        }
+                        for (int k = 0; k < 4; ++k)
+                            umma_ts(tS + C::O_COL, tS + C::P_COL + 32 * h + 8 * k, vt + (4 * h + k) * (2048 >> 4), kDescHi, kIdescPv,
+                                    h + k > 0 ? 1u : more_o);
+                    };
+                    auto p_ready = [&](int h) { return lane_wait(bar(bP + 2 * g + h), n_pv & 1); };
+                    if (w.two) {
+                        // Both groups are at the same tile: they take turns at the tensor
+                        // cores, so that one computes weights while the other's products
+                        // run (interleaved, both would finish, and wait, at the same time).
+                        if (t >= 0) ok = ok && p_ready(0) && p_ready(1);
+                        if (more) ok = ok && landed(n2);
+                        ok = ok && lane_wait(bar(bTurn + g), (turns - 1 + g) & 1);
                         if (!ok) break;
+                        ++turns;
+                        if (t >= 0) {
+                            pv(0);
+                            pv(1);
+                        }
+                    } else if (t >= 0) {
+                        ok = ok && p_ready(0);         // the softmax hands P over in halves
+                        if (!ok) break;
+                        pv(0);
+                        ok = p_ready(1);
+                        if (!ok) break;
+                        pv(1);
+                    }
+                    if (t >= 0) {
                         umma_commit(bar(bO + g));
                         umma_commit(bar(bFree + stage(n)));
                         ++n_pv;
                         if (!w.two && t + 1 < nt) ok = see_tile(t + 1);
                     }
-                    if (ok && more) {
-                        ok = landed(n2);
+                    if (more) {
+                        if (!w.two) ok = ok && landed(n2);
                         if (!ok) break;
                         tc_fence_after();
-                        const uint64_t kt = umma_desc_sw128(s0 + C::OFF_T + stage(n2) * C::TILE, 16, 1024);
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k) {
                             const uint32_t at = ((k >> 2) * C::BLOCK + (k & 3) * 32) >> 4;
-                            umma_ss(tS, q + at, kt + at, idesc_qk, k > 0);
+                            if (k == 0) umma_ss<true>(tS, q, kt, kDescHi, idesc_qk);
+                            else umma_ss<false>(tS, q + at, kt + at, kDescHi, idesc_qk);
                         }
                         umma_commit(bar(bS + g));
                         umma_commit(bar(bFree + stage(n2)));
@@ -642,6 +671,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         // the last scores: q is done with
                         if (t + 2 * step >= nt) w.buffers([&](int bf, int) { umma_commit(bar(bQFree + bf)); });
                     }
+                    if (w.two) mbar_arrive(bar(bTurn + 1 - g));
                 }
                 if (!ok) break;
                 if (first >= nt) w.buffers([&](int bf, int) { mbar_arrive(bar(bQFree + bf)); });  // no tile for this group
@@ -1083,49 +1113,53 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
 }
 
 // ---- joining the pieces of cut items ------------------------------------------------
-// CTA (c, y): 32 rows of the item whose first piece CTA c had; a lane is a
-// row, a warp D / 32 of its quads of columns.
-constexpr int kJoinRows = 32;
+// CTA (c, y): 8 rows of the item whose first piece CTA c had. A warp has 8 rows
+// x 4 quads of columns (128-byte runs of the partial sums), D / 16 warps a row.
+constexpr int kJoinRows = 8;
 
 template <int D>
-__global__ void __launch_bounds__(256) tree_join_kernel(const TreeArgs a, int ctas) {
+__global__ void __launch_bounds__(2 * D) tree_join_kernel(const TreeArgs a, int ctas) {
     grid_dep_wait();
-    const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int r = blockIdx.y * kJoinRows + lane;         // row of the item: token r / G, head r % G
+    const int c = blockIdx.x, lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) * 4 + (lane >> 3);
+    const int r = blockIdx.y * kJoinRows + (lane & 7);   // row of the item: token r / G, head r % G
     const int4 meta = reinterpret_cast<const int4*>(a.workspace)[c];  // first token, tokens, pieces, kv head
     const int tok = r / a.G, g = r - tok * a.G;
     if (tok >= meta.y) return;
     const int row = tok < a.tile_toks ? r : 128 + r - a.tile_toks * a.G;  // its place in the partial sums
     const int n = meta.z;                                // pieces: slot 1 of CTA c, slot 0 of the next ones
     auto slot = [&](int i) { return 2 * (c + i) + (i == 0 ? 1 : 0); };
-    float M = -INFINITY;
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) M = fmaxf(M, part_ml(a.workspace, slot(i), row)[0]);
-    constexpr int Q = D / 32;                            // quads of columns per thread
-    float sum = 0.f;
-    float4 o[Q];
+    float M = -INFINITY, sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < n; i0 += 8) {                  // online over the pieces, eight on their way at a time
+        float2 ml[8];
+        float4 x[8];
+        float m = M;
 #pragma unroll
-    for (int q = 0; q < Q; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-        const float2 ml = *reinterpret_cast<const float2*>(part_ml(a.workspace, slot(i), row));
-        const float* p = part_o<D>(a.workspace, ctas, slot(i), row);
-        const float f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);
-        sum += f * ml.y;
+        for (int k = 0; k < 8; ++k) {
+            const int i = min(i0 + k, n - 1);
+            ml[k] = *reinterpret_cast<const float2*>(part_ml(a.workspace, slot(i), row));
+            x[k] = *reinterpret_cast<const float4*>(part_o<D>(a.workspace, ctas, slot(i), row) +
+                                                    static_cast<int64_t>(quad) * kRows * 4);
+            m = fmaxf(m, ml[k].x);
+        }
+        const float al = M == -INFINITY ? 0.f : fast_exp2(M - m);
+        M = m;
+        sum *= al;
+        o.x *= al, o.y *= al, o.z *= al, o.w *= al;
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            const float4 x = *reinterpret_cast<const float4*>(p + static_cast<int64_t>(warp * Q + q) * kRows * 4);
-            o[q].x += f * x.x, o[q].y += f * x.y, o[q].z += f * x.z, o[q].w += f * x.w;
+        for (int k = 0; k < 8; ++k) {
+            if (i0 + k >= n) break;
+            const float f = ml[k].x == -INFINITY ? 0.f : fast_exp2(ml[k].x - M);
+            sum += f * ml[k].y;
+            o.x += f * x[k].x, o.y += f * x[k].y, o.z += f * x[k].z, o.w += f * x[k].w;
         }
     }
     const bool none = sum == 0.f;
     const float inv = none ? 0.f : 1.f / sum;
     const int h = meta.w * a.G + g;
-    uint2* out = reinterpret_cast<uint2*>(a.out + (meta.x + tok) * a.o_s0 + h * a.o_s1 + warp * Q * 4);
-#pragma unroll
-    for (int q = 0; q < Q; ++q)
-        out[q] = none ? make_uint2(0u, 0u) : make_uint2(pack_bf16(o[q].x * inv, o[q].y * inv), pack_bf16(o[q].z * inv, o[q].w * inv));
-    if (warp == 0 && a.lse)
+    uint2* out = reinterpret_cast<uint2*>(a.out + (meta.x + tok) * a.o_s0 + h * a.o_s1 + quad * 4);
+    *out = none ? make_uint2(0u, 0u) : make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    if (quad == 0 && a.lse)
         a.lse[(meta.x + tok) * a.l_s0 + h * a.l_s1] = none ? -INFINITY : (M + __log2f(sum)) * 0.69314718055994530942f;
 }
 
@@ -1140,7 +1174,7 @@ cudaError_t launch_t(const TreeArgs& a, const CUtensorMap& tq, const CUtensorMap
     e = launch_dependent(tree_kernel<D, FP8>, dim3(sms), dim3(C::THREADS), C::SMEM, s, tq, tk, tv, a);
     if (e != cudaSuccess) return e;
     const int rows = static_cast<int>(std::min<int64_t>(kRows, static_cast<int64_t>(a.T) * a.G));
-    return launch_dependent(tree_join_kernel<D>, dim3(sms, (rows + kJoinRows - 1) / kJoinRows), dim3(256), 0, s, a, sms);
+    return launch_dependent(tree_join_kernel<D>, dim3(sms, (rows + kJoinRows - 1) / kJoinRows), dim3(2 * D), 0, s, a, sms);
 }
 
 }  // namespace
