@@ -131,7 +131,8 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const __grid_con
 // ---- pages taken from and returned to the pool ----------------------------------
 constexpr int kTakeThreads = 1024;
 constexpr int kTakeWarps = kTakeThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
+constexpr int kKeptPages = 1024;           // pages of a warp whose free masks stay in a register
 constexpr uint32_t kDemandCap = 1u << 30;  // sums saturate here, above any pool
 
 __device__ __forceinline__ uint32_t sat_add(uint32_t x, uint32_t y) { return min(x + y, kDemandCap); }
@@ -148,7 +149,6 @@ __device__ __forceinline__ uint32_t cluster_size() {
 // All threads of the cluster; what they wrote before (shared memory of any
 // CTA, device memory) is visible to all of them after it.
 __device__ __forceinline__ void cluster_barrier() {
-    __threadfence();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void st_cluster(uint32_t local_addr, uint32_t rank, uint32_t v) {
@@ -233,6 +233,9 @@ __device__ __forceinline__ uint32_t free_mask(const int32_t* refs, int64_t p, in
     return m;
 }
 
+// Dynamic shared memory: words for n rows or forks, then a page list per warp.
+__host__ __device__ constexpr size_t take_words(int n) { return 3 * static_cast<size_t>(n) + 2; }
+
 template <bool FORK>
 __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constant__ TakeArgs a) {
     extern __shared__ uint32_t dyn[];
@@ -241,9 +244,10 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
     const uint32_t rank = cluster_rank(), C = cluster_size();
     const int n = a.n;
     uint32_t* need = dyn;                              // [n + 1]: demands, then their prefix sums
-    uint32_t* give = dyn + (n + 1);                    // resize: [n + 1] returns, then their prefix sums
-    int32_t* len = reinterpret_cast<int32_t*>(give);   // fork: [n] parent's length, -1 = not made
-    int32_t* tail = len + n;                           // fork: [n] page to copy, -1 = none
+    int32_t* held = reinterpret_cast<int32_t*>(dyn + (n + 1));  // resize: [n] entries in use; fork: parent's length, -1 = not made
+    uint32_t* give = dyn + (2 * n + 1);                // resize: [n + 1] returns, then their prefix sums
+    int32_t* tail = reinterpret_cast<int32_t*>(give);  // fork: [n] page to copy, -1 = none
+    uint32_t* list = dyn + take_words(n) + warp * 128; // this warp's free pages, in order
 
     // Counts, tables and lengths may be written by the preceding grid. What
     // this grid writes are index inputs: a resize lets nothing start early, a
@@ -257,25 +261,40 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
             int have, want, f;
             resize_row(a, b, have, want, f);
             flags |= f;
+            held[b] = have;
             need[b] = want > have ? want - have : 0;
             give[b] = want < have ? have - want : 0;
         }
         block_prefix(give, n, warp_sum);
-        // returns, dealt out one entry at a time over the cluster
-        const uint32_t total = give[n];
-        for (uint32_t e = rank * kTakeThreads + tid; e < total; e += C * kTakeThreads) {
-            const int b = owner_of(give, n, e);
-            int have, want, f;
-            resize_row(a, b, have, want, f);
-            int32_t* entry = a.block_tables + b * a.bt_s0 + want + (e - give[b]);
-            const int page = *entry;
-            *entry = -1;
-            if (page < 0 || page >= a.num_pages) {
-                flag_error(a.err, PKV_FLAG_PAGE_RANGE);
-            } else if (atomicSub(a.page_refs + page, 1) <= 0) {
-                atomicAdd(a.page_refs + page, 1);
-                flag_error(a.err, PKV_FLAG_PAGE_STATE);
+        // Returns, dealt out by entry over the cluster, four per thread on their way.
+        const uint32_t total = give[n], span = C * kTakeThreads;
+        for (uint32_t e0 = rank * kTakeThreads + tid; e0 < total; e0 += 4 * span) {
+            int page[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t e = e0 + k * span;
+                page[k] = -2;
+                if (e < total) {
+                    const int b = owner_of(give, n, e);
+                    // the row keeps held - returns entries
+                    int32_t* entry = a.block_tables + b * a.bt_s0 + held[b] - static_cast<int>(give[b + 1] - e);
+                    page[k] = *entry;
+                    *entry = -1;
+                    if (page[k] < 0 || page[k] >= a.num_pages) {
+                        flags |= PKV_FLAG_PAGE_RANGE;
+                        page[k] = -2;
+                    }
+                }
             }
+            int old[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) old[k] = page[k] >= 0 ? atomicSub(a.page_refs + page[k], 1) : 1;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (old[k] <= 0) {
+                    atomicAdd(a.page_refs + page[k], 1);
+                    flags |= PKV_FLAG_PAGE_STATE;
+                }
         }
     } else {
         // A child's count of 0 becomes a claim: -(n - i) of its first fork i
@@ -302,14 +321,14 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
                     }
                 }
             }
-            len[i] = L;
+            held[i] = L;
             tail[i] = L < 0 ? -1 : src;
         }
         cluster_barrier();
         for (int i = tid; i < n; i += kTakeThreads) {
-            if (len[i] >= 0 && __ldcg(a.page_counts + a.forks[2 * i + 1]) != -(n - i)) {
+            if (held[i] >= 0 && __ldcg(a.page_counts + a.forks[2 * i + 1]) != -(n - i)) {
                 flags |= PKV_FLAG_PAGE_STATE;  // an earlier fork has this child
-                len[i] = -1;
+                held[i] = -1;
                 tail[i] = -1;
             }
             need[i] = tail[i] >= 0 ? 1 : 0;
@@ -324,11 +343,21 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
     const int64_t cta0 = rank * cta_span, cta1 = min(cta0 + cta_span, a.num_pages);
     const int64_t p0 = min(cta0 + warp * warp_span, cta1), p1 = min(p0 + warp_span, cta1);
     const bool vec = (reinterpret_cast<uintptr_t>(a.page_refs) & 15) == 0;
+    const bool kept = warp_span <= kKeptPages;
     const uint32_t wanted = need[n];
-    uint32_t cnt = 0;
+    uint32_t cnt = 0, masks = 0;                       // masks: 4 bits per group of 128 pages, when kept
     if (wanted) {
-#pragma unroll 4
-        for (int64_t p = p0 + 4 * lane; p < p1; p += 128) cnt += __popc(free_mask(a.page_refs, p, p1, vec));
+        if (kept) {
+#pragma unroll
+            for (int g = 0; g < kKeptPages / 128; ++g) {
+                const int64_t p = p0 + 128 * g + 4 * lane;
+                if (p < p1) masks |= free_mask(a.page_refs, p, p1, vec) << (4 * g);
+            }
+            cnt = __popc(masks);
+        } else {
+#pragma unroll 8
+            for (int64_t p = p0 + 4 * lane; p < p1; p += 128) cnt += __popc(free_mask(a.page_refs, p, p1, vec));
+        }
     }
     cnt = __reduce_add_sync(0xffffffffu, cnt);
     if (lane == 0) warp_free[warp] = cnt;
@@ -345,9 +374,10 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
     }
     for (int w = 0; w < warp; ++w) at += warp_free[w];
     const uint32_t last = min(wanted, total_free);  // ranks past it go to nobody
-    for (int64_t g = p0; g < p1 && at < last; g += 128) {
+    int group = 0;
+    for (int64_t g = p0; g < p1 && at < last; g += 128, ++group) {
         const int64_t p = g + 4 * lane;
-        const uint32_t m = p < p1 ? free_mask(a.page_refs, p, p1, vec) : 0;
+        uint32_t m = kept ? masks >> (4 * group) & 15u : p < p1 ? free_mask(a.page_refs, p, p1, vec) : 0u;
         uint32_t inc = __popc(m);
         const uint32_t own_n = inc;
 #pragma unroll
@@ -355,47 +385,55 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
             const uint32_t y = __shfl_up_sync(0xffffffffu, inc, d);
             if (lane >= d) inc += y;
         }
-        uint32_t r = at + inc - own_n;
-        at += __shfl_sync(0xffffffffu, inc, 31);
-        for (int k = 0; k < 4; ++k) {
-            if (!(m >> k & 1)) continue;
-            if (r < last) {
-                const int i = owner_of(need, n, r);
-                if (need[i + 1] <= total_free) {  // i gets all that it needs
-                    const int page = static_cast<int>(p + k);
-                    if constexpr (!FORK) {
-                        a.block_tables[i * a.bt_s0 + a.page_counts[i] + (r - need[i])] = page;
-                    } else {
-                        a.block_tables[a.forks[2 * i + 1] * a.bt_s0 + len[i] / a.page_size] = page;
-                        a.copies[2 * i] = tail[i];
-                        a.copies[2 * i + 1] = page;
-                    }
-                    a.page_refs[page] = 1;
-                }
-            }
-            ++r;
+        const uint32_t found = __shfl_sync(0xffffffffu, inc, 31);
+        // the group's free pages side by side, so that neighbouring lanes write
+        // neighbouring entries
+        uint32_t o = inc - own_n;
+        while (m) {
+            const int k = __ffs(m) - 1;
+            m &= m - 1;
+            list[o++] = static_cast<uint32_t>(p + k);
         }
+        __syncwarp();
+#pragma unroll 4
+        for (uint32_t k = lane; k < found; k += 32) {
+            const uint32_t r = at + k;
+            if (r >= last) break;
+            const int page = static_cast<int>(list[k]);
+            const int i = owner_of(need, n, r);
+            if (need[i + 1] > total_free) break;       // i, and everyone after it, gets nothing
+            if constexpr (!FORK) {
+                a.block_tables[i * a.bt_s0 + held[i] + (r - need[i])] = page;
+            } else {
+                a.block_tables[a.forks[2 * i + 1] * a.bt_s0 + held[i] / a.page_size] = page;
+                a.copies[2 * i] = tail[i];
+                a.copies[2 * i + 1] = page;
+            }
+            a.page_refs[page] = 1;
+        }
+        at += found;
+        __syncwarp();
     }
+    if (flags) flag_error(a.err, flags);
     cluster_barrier();  // every CTA has read the counts and lengths
     if (rank != 0) return;
     for (int i = tid; i < n; i += kTakeThreads) {
-        const bool fails = need[i + 1] > need[i] && need[i + 1] > total_free;
-        if (fails) flags |= PKV_FLAG_POOL_EMPTY;
+        const uint32_t grow = need[i + 1] - need[i];
+        const bool fails = grow > 0 && need[i + 1] > total_free;
+        if (fails) flag_error(a.err, PKV_FLAG_POOL_EMPTY);
         if constexpr (!FORK) {
-            int have, want, f;
-            resize_row(a, i, have, want, f);
-            if (!fails && want != have) a.page_counts[i] = want;
+            const int back = static_cast<int>(give[i + 1] - give[i]);
+            if (back || (grow && !fails)) a.page_counts[i] = held[i] - back + static_cast<int>(grow);
         } else {
-            if (len[i] >= 0) {
-                const int c = a.forks[2 * i + 1], pages = len[i] / a.page_size + (tail[i] >= 0);
+            if (held[i] >= 0) {
+                const int c = a.forks[2 * i + 1], pages = held[i] / a.page_size + (tail[i] >= 0);
                 a.page_counts[c] = fails ? 0 : pages;
-                if (!fails) a.seq_lens[c] = len[i];
+                if (!fails) a.seq_lens[c] = held[i];
             }
-            if (len[i] < 0 || fails) a.copies[2 * i] = a.copies[2 * i + 1] = -2;
+            if (held[i] < 0 || fails) a.copies[2 * i] = a.copies[2 * i + 1] = -2;
             else if (tail[i] < 0) a.copies[2 * i] = a.copies[2 * i + 1] = -1;
         }
     }
-    if (flags) flag_error(a.err, flags);
 }
 
 // ---- shared entries and copied pages of a fork --------------------------------------
@@ -458,12 +496,16 @@ __global__ void __launch_bounds__(kShareThreads) share_kernel(const __grid_const
 template <bool FORK>
 cudaError_t launch_take(const TakeArgs& a, cudaStream_t s) {
     auto kern = take_kernel<FORK>;
-    const size_t smem = (FORK ? 3 * static_cast<size_t>(a.n) + 1 : 2 * (static_cast<size_t>(a.n) + 1)) * 4;
+    const size_t smem = (take_words(a.n) + kTakeWarps * 128) * 4;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    // One CTA counts 16,384 pages in one round of its loads; larger pools are
-    // spread over a cluster.
-    const unsigned C = a.num_pages <= 16384 ? 1 : kMaxCluster;
+    // A CTA keeps the free masks of 32,768 pages in registers; larger pools are
+    // spread over a cluster (16 CTAs, the largest there is, is past the portable 8).
+    const unsigned C = a.num_pages <= 8192 ? 1 : a.num_pages <= 32768 ? 4 : kMaxCluster;
+    if (C > 8) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(C);
     cfg.blockDim = dim3(kTakeThreads);
