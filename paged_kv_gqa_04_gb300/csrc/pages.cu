@@ -17,8 +17,8 @@
 // entry that the prefix sums give r (a binary search). Every result follows
 // from the inputs alone: atomics only add and subtract counts.
 //
-// share_kernel (the second half of a fork). CTAs of (fork, cache) copy the
-// partial last page; CTAs of (fork, stretch of the table) copy the shared
+// share_kernel (the second half of a fork). CTAs of (fork, cache, 16 KB) copy
+// the partial last page; CTAs of (fork, stretch of the table) copy the shared
 // entries and raise their pages' counts.
 #include <algorithm>
 
@@ -221,6 +221,44 @@ __device__ __forceinline__ void resize_row(const TakeArgs& a, int b, int& have, 
     else want = need;
 }
 
+// Returns of a large batch, by all SMs: a warp takes 256 entries of a row. The
+// counts of entries stay as they are for the take behind it.
+constexpr int kReturnSpan = 256;
+__global__ void __launch_bounds__(256) return_kernel(const __grid_constant__ TakeArgs a) {
+    grid_dep_wait();  // (the table is an index input: no early trigger, but for the take, which waits)
+    grid_dep_launch();
+    const int b = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (b >= a.n) return;
+    int have, want, flags;
+    resize_row(a, b, have, want, flags);
+    flags = 0;  // the take reports them
+    const int j0 = max(want, static_cast<int>(blockIdx.y) * kReturnSpan);
+    const int j1 = min(have, static_cast<int>(blockIdx.y + 1) * kReturnSpan);
+    int page[kReturnSpan / 32], old[kReturnSpan / 32];
+#pragma unroll
+    for (int k = 0; k < kReturnSpan / 32; ++k) {
+        const int j = j0 + lane + 32 * k;
+        page[k] = -2;
+        if (j < j1) {
+            page[k] = a.block_tables[b * a.bt_s0 + j];
+            a.block_tables[b * a.bt_s0 + j] = -1;
+            if (page[k] < 0 || page[k] >= a.num_pages) {
+                flags |= PKV_FLAG_PAGE_RANGE;
+                page[k] = -2;
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kReturnSpan / 32; ++k) old[k] = page[k] >= 0 ? atomicSub(a.page_refs + page[k], 1) : 1;
+#pragma unroll
+    for (int k = 0; k < kReturnSpan / 32; ++k)
+        if (old[k] <= 0) {
+            atomicAdd(a.page_refs + page[k], 1);
+            flags |= PKV_FLAG_PAGE_STATE;
+        }
+    if (flags) flag_error(a.err, flags);
+}
+
 // The four counts from page p on as a mask of the free ones (p a multiple of 4).
 __device__ __forceinline__ uint32_t free_mask(const int32_t* refs, int64_t p, int64_t end, bool vec) {
     if (p + 4 <= end && vec) {
@@ -266,8 +304,9 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
             give[b] = want < have ? have - want : 0;
         }
         block_prefix(give, n, warp_sum);
-        // Returns, dealt out by entry over the cluster, four per thread on their way.
-        const uint32_t total = give[n], span = C * kTakeThreads;
+        // Returns (unless a kernel of their own made them), dealt out by entry
+        // over the cluster, four per thread on their way.
+        const uint32_t total = a.returned ? 0 : give[n], span = C * kTakeThreads;
         for (uint32_t e0 = rank * kTakeThreads + tid; e0 < total; e0 += 4 * span) {
             int page[4];
 #pragma unroll
@@ -395,13 +434,21 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
             list[o++] = static_cast<uint32_t>(p + k);
         }
         __syncwarp();
-#pragma unroll 4
-        for (uint32_t k = lane; k < found; k += 32) {
-            const uint32_t r = at + k;
-            if (r >= last) break;
-            const int page = static_cast<int>(list[k]);
-            const int i = owner_of(need, n, r);
-            if (need[i + 1] > total_free) break;       // i, and everyone after it, gets nothing
+        for (uint32_t k0 = 0; k0 < found && at + k0 < last; k0 += 32) {
+            const uint32_t r = at + k0 + lane;
+            // 32 neighbouring ranks mostly have few owners: the first one's (a
+            // search by the warp's lanes alike) and the rows behind it
+            const int i0 = owner_of(need, n, at + k0);
+            const uint32_t ends = i0 + 1 + lane <= n ? need[i0 + 1 + lane] : ~0u;
+            int i = 0;
+#pragma unroll
+            for (int d = 16; d; d >>= 1)
+                if (__shfl_sync(0xffffffffu, ends, i + d - 1) <= r) i += d;
+            i += i0 + (__shfl_sync(0xffffffffu, ends, i) <= r);
+            if (k0 + lane >= found || r >= last) continue;
+            if (need[i + 1] <= r) i = owner_of(need, n, r);  // more than 31 rows on (rows without a demand among them)
+            const int page = static_cast<int>(list[k0 + lane]);
+            if (need[i + 1] > total_free) continue;    // i, and everyone after it, gets nothing
             if constexpr (!FORK) {
                 a.block_tables[i * a.bt_s0 + held[i] + (r - need[i])] = page;
             } else {
@@ -459,7 +506,31 @@ __device__ __forceinline__ void copy_page(const PoolPart& c, int64_t src, int64_
     }
 }
 
+// A page in one piece, 16-byte aligned: kBulkBytes of it through shared memory
+// by two bulk copies of one thread (loads and stores by 256 threads moved a batch
+// of 16 KB pages at 4.2 TB/s, bulk copies at BULKRATE).
+constexpr int kBulkBytes = 16384;
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(dst)), "r"(src),
+                 "r"(bytes)
+                 : "memory");
+}
+__device__ void copy_bulk(uint8_t* dst, const uint8_t* src, uint32_t bytes, uint32_t buf, uint32_t bar, int32_t* err) {
+    mbar_init(bar, 1);
+    fence_mbar_init();
+    mbar_arrive_expect_tx(bar, bytes);
+    bulk_load(buf, src, bytes, bar, l2_policy_evict_first());
+    if (!mbar_wait_bounded(bar, 0, 1000000000ull)) {
+        flag_error(err, PKV_FLAG_WAIT_TIMEOUT);
+        return;
+    }
+    bulk_store(dst, buf, bytes);
+    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 __global__ void __launch_bounds__(kShareThreads) share_kernel(const __grid_constant__ ShareArgs a) {
+    __shared__ __align__(128) uint8_t buf[kBulkBytes];
+    __shared__ uint64_t bar;
     grid_dep_wait();  // the first half's results; the table is an index input: no early trigger
     const int i = blockIdx.x;
     const int src = a.copies[2 * i], dst = a.copies[2 * i + 1];
@@ -469,6 +540,14 @@ __global__ void __launch_bounds__(kShareThreads) share_kernel(const __grid_const
         if (src < 0) return;
         const PoolPart& c = a.c[y];
         const int64_t s = src * c.s_page, d = dst * c.s_page;
+        if (c.vec == 16 && c.n0 * c.n1 == 1) {
+            const int64_t o = static_cast<int64_t>(blockIdx.z) * kBulkBytes;
+            if (threadIdx.x == 0 && o < c.row && src != dst)
+                copy_bulk(c.p + d + o, c.p + s + o, static_cast<uint32_t>(min(static_cast<int64_t>(kBulkBytes), c.row - o)),
+                          smem_u32(buf), smem_u32(&bar), a.err);
+            return;
+        }
+        if (blockIdx.z > 0) return;
         switch (c.vec) {
             case 16: copy_page<uint4>(c, s, d); break;
             case 8: copy_page<uint2>(c, s, d); break;
@@ -477,6 +556,7 @@ __global__ void __launch_bounds__(kShareThreads) share_kernel(const __grid_const
         }
         return;
     }
+    if (blockIdx.z > 0) return;
     const int p = a.forks[2 * i], c = a.forks[2 * i + 1];
     const int full = a.seq_lens[c] / a.page_size;
     const int j1 = min(full, (static_cast<int>(blockIdx.y) + 1) * kShareSpan);
@@ -530,8 +610,19 @@ cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t s) {
     return launch_dependent(accept_kernel, dim3(a.B, std::max(a.n_caches, 1)), dim3(kAcceptThreads), 0, s, a);
 }
 
-cudaError_t launch_resize(const TakeArgs& a, cudaStream_t s) {
-    return a.n == 0 ? cudaSuccess : launch_take<false>(a, s);
+cudaError_t launch_resize(const TakeArgs& a0, cudaStream_t s) {
+    if (a0.n == 0) return cudaSuccess;
+    TakeArgs a = a0;
+    // With room for 64 Ki entries in the tables and more, the returns may be more
+    // than the take's one cluster does quickly, and are worth a launch of their
+    // own (resize_pool's shape: 36 us a call in one kernel, RETURNS in two).
+    a.returned = static_cast<int64_t>(a.n) * a.max_pages >= 65536;
+    if (a.returned) {
+        const cudaError_t e = launch_dependent(return_kernel, dim3((a.n + 7) / 8, (a.max_pages + kReturnSpan - 1) / kReturnSpan),
+                                               dim3(256), 0, s, a);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_take<false>(a, s);
 }
 
 cudaError_t launch_fork_take(const TakeArgs& a, cudaStream_t s) {
@@ -542,7 +633,11 @@ cudaError_t launch_fork_share(const ShareArgs& a0, int32_t n, int32_t max_pages,
     if (n == 0) return cudaSuccess;
     ShareArgs a = a0;
     a.table_ctas = tables ? (max_pages + kShareSpan - 1) / kShareSpan : 0;
-    return launch_dependent(share_kernel, dim3(n, a.table_ctas + a.n_caches), dim3(kShareThreads), 0, s, a);
+    int chunks = 1;
+    for (int i = 0; i < a.n_caches; ++i)
+        if (a.c[i].vec == 16 && a.c[i].n0 * a.c[i].n1 == 1)
+            chunks = std::max(chunks, (a.c[i].row + kBulkBytes - 1) / kBulkBytes);
+    return launch_dependent(share_kernel, dim3(n, a.table_ctas + a.n_caches, chunks), dim3(kShareThreads), 0, s, a);
 }
 
 }  // namespace pkv

@@ -210,6 +210,7 @@ struct TakeArgs {
     int32_t* page_refs;
     int64_t num_pages;
     int32_t max_pages, page_size, n, rows;
+    int32_t returned;          // the returns have been made by a kernel of their own (set by the launcher)
     const int32_t* new_lens;
     const int32_t* forks;
     int32_t* seq_lens;
