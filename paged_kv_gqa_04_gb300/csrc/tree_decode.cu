@@ -25,10 +25,11 @@
 //                 fills zeros
 //   warps 1, 3    one thread each, for one softmax group: S = Q . K^T and O += P . V
 //                 (M = 128; P from tensor memory, V as an MN-major operand:
-//                 nothing is transposed). While the operands stream, shared
-//                 memory answers a barrier in 150 cycles or more; with one
-//                 thread for both groups the tensor cores stood still
-//                 meanwhile (2900 cycles a tile and row tile, of 1024)
+//                 nothing is transposed). A tcgen05.commit holds the products
+//                 behind it up for about 105 cycles (16 MMAs: 1054 cycles, 1481
+//                 with four commits), so a tile has one, for S: that S is there
+//                 also says that its K, and the V and the P before it, are done
+//                 with, and the softmax warps release them
 //   warps 4 - 11,
 //   warps 12 - 19 two softmax groups of eight warps (four for the 128 rows times
 //                 two for the halves of a tile's positions: with one warp for
@@ -329,6 +330,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     Place* place = reinterpret_cast<Place*>(misc + 36);   // [2]: this CTA's first unit and the one past its last
     int* warp_units = reinterpret_cast<int*>(misc + 42);  // [24]
     Piece* pieces = reinterpret_cast<Piece*>(smem + C::OFF_PIECE);
+    uint32_t* go_on = misc + 2;                           // [2 groups]: O has been started by hand
     float* q_scale = reinterpret_cast<float*>(smem + C::OFF_SC);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -337,7 +339,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     if (tid == 0) {
         for (int i = 0; i < C::ST; ++i) {
             mbar_init(bar(bFull + i), FP8 ? 4 : 1);
-            mbar_init(bar(bFree + i), 2);  // either MMA thread: its use, or a tile of the other group seen
+            mbar_init(bar(bFree + i), 2);  // either group: its use, or (its MMA thread) a tile of the other group seen
         }
         for (int i = 0; i < C::RST; ++i) {
             mbar_init(bar(bRawFull + i), 1);
@@ -349,7 +351,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             mbar_init(bar(bP + 2 * w + 1), 4);
             mbar_init(bar(bO + w), 1);
             mbar_init(bar(bQ + w), FP8 ? 4 : 1);
-            mbar_init(bar(bQFree + w), 18);  // either group's last Q . K^T, and the softmax warps (staged output)
+            mbar_init(bar(bQFree + w), 16);  // the softmax warps (the last S, and the staged output)
             mbar_init(bar(bQRaw + w), 1);
             mbar_init(bar(bTurn + w), 1);
         }
@@ -574,7 +576,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             auto desc_lo = [](uint32_t addr, uint32_t lead) { return ((addr >> 4) & 0x3FFFu) | (lead >> 4) << 16; };
             const uint32_t tS = tmem + 256 * g;
             int tile0 = 0;                    // tiles before this piece
-            int n_qk = 0, n_pv = 0;           // Q . K^T and P . V issued
+            int n_qk = 0, n_pv = 0, n_o = 0;  // Q . K^T, P . V and last P . V of an item issued
             int turns = 0;                    // of items with two row tiles
             bool ok = true;
             for (int i = 0; ok; ++i) {
@@ -582,9 +584,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 const Piece w = pieces[i % kPieces];
                 if (!ok || w.b < 0) break;
                 const int nt = w.t1 - w.t0, step = w.two ? 1 : 2;
-                w.buffers([&](int bf, int uses) { ok = ok && lane_wait(bar(bQ + bf), uses & 1); });
-                // the item before has no more use for S
-                if (i > 0) ok = ok && lane_wait(bar(bX + (i - 1) % kPieces), ((i - 1) / kPieces) & 1);
+                if (nt > (w.two ? 0 : g)) {            // (a group without a tile here only sees them land)
+                    // the item before has no more use for S
+                    if (i > 0) ok = lane_wait(bar(bX + (i - 1) % kPieces), ((i - 1) / kPieces) & 1);
+                    w.buffers([&](int bf, int uses) { ok = ok && lane_wait(bar(bQ + bf), uses & 1); });
+                }
                 const uint32_t q = desc_lo(s0 + C::OFF_Q + (w.two ? g : w.buf) * C::TILE, 16);
                 const int first = w.two ? 0 : g;
                 // Both threads see every slot land, in order, and both release it
@@ -608,13 +612,22 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     if (t >= 0) ok = landed(n);
                     const uint32_t vt = desc_lo(s0 + C::OFF_T + stage(n) * C::TILE, C::BLOCK);
                     const uint32_t kt = desc_lo(s0 + C::OFF_T + stage(n2) * C::TILE, 16);
-                    const uint32_t more_o = t > first;  // O goes on, or starts
                     auto pv = [&](int h) {             // half h of the tile's positions
                         tc_fence_after();
+                        const uint32_t more_o = t > first || *reinterpret_cast<volatile uint32_t*>(go_on + g) != 0u;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             umma_ts(tS + C::O_COL, tS + C::P_COL + C::P_HALF * h + 8 * k, vt + (4 * h + k) * (2048 >> 4), kDescHi, kIdescPv,
                                     h + k > 0 ? 1u : more_o);
+                    };
+                    auto qk = [&]() {
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint32_t at = ((k >> 2) * C::BLOCK + (k & 3) * 32) >> 4;
+                            if (k == 0) umma_ss<true>(tS, q, kt, kDescHi, idesc_qk);
+                            else umma_ss<false>(tS, q + at, kt + at, kDescHi, idesc_qk);
+                        }
                     };
                     auto p_ready = [&](int h) { return lane_wait(bar(bP + 2 * g + h), n_pv & 1); };
                     if (w.two) {
@@ -630,40 +643,36 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                             pv(0);
                             pv(1);
                         }
-                    } else if (t >= 0) {
-                        ok = ok && p_ready(0);         // the softmax hands P over in halves
-                        if (!ok) break;
-                        pv(0);
-                        ok = p_ready(1);
-                        if (!ok) break;
-                        pv(1);
-                    }
-                    if (t >= 0) {
-                        umma_commit(bar(bO + g));
-                        umma_commit(bar(bFree + stage(n)));
-                        ++n_pv;
-                        if (!w.two && t + 1 < nt) ok = see_tile(t + 1);
-                    }
-                    if (more) {
-                        if (!w.two) ok = ok && landed(n2);
-                        if (!ok) break;
-                        tc_fence_after();
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t at = ((k >> 2) * C::BLOCK + (k & 3) * 32) >> 4;
-                            if (k == 0) umma_ss<true>(tS, q, kt, kDescHi, idesc_qk);
-                            else umma_ss<false>(tS, q + at, kt + at, kDescHi, idesc_qk);
+                        if (more) qk();
+                        mbar_arrive(bar(bTurn + 1 - g));
+                    } else {
+                        if (t >= 0) {
+                            ok = ok && p_ready(0);     // the softmax hands P over in halves
+                            if (!ok) break;
+                            pv(0);
+                            ok = p_ready(1);
+                            if (!ok) break;
+                            pv(1);
+                            // (one row tile is bound by memory: V's stage is wanted back at once)
+                            umma_commit(bar(bFree + stage(n)));
+                            if (t + 1 < nt) ok = see_tile(t + 1);
                         }
-                        umma_commit(bar(bS + g));
-                        umma_commit(bar(bFree + stage(n2)));
-                        ++n_qk;
-                        // the last scores: q is done with
-                        if (t + 2 * step >= nt) w.buffers([&](int bf, int) { umma_commit(bar(bQFree + bf)); });
+                        if (more) {
+                            ok = ok && landed(n2);
+                            if (!ok) break;
+                            qk();
+                        }
                     }
-                    if (w.two) mbar_arrive(bar(bTurn + 1 - g));
+                    if (t >= 0) ++n_pv;
+                    if (more) {
+                        umma_commit(bar(bS + g));
+                        ++n_qk;
+                    } else if (t >= 0) {
+                        umma_commit(bar(bO + g));      // the item's O
+                        ++n_o;
+                    }
                 }
                 if (!ok) break;
-                if (first >= nt) w.buffers([&](int bf, int) { mbar_arrive(bar(bQFree + bf)); });  // no tile for this group
                 mbar_arrive(bar(bPieceFree + i % kPieces));
                 tile0 += nt;
             }
@@ -671,7 +680,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             // the softmax groups wait for their last O, and give-ups for both here.
             if (!ok) {
                 if (n_qk) (void)mbar_wait_bounded(bar(bS + g), (n_qk - 1) & 1, kWaitLimitNs);
-                if (n_pv) (void)mbar_wait_bounded(bar(bO + g), (n_pv - 1) & 1, kWaitLimitNs);
+                if (n_o) (void)mbar_wait_bounded(bar(bO + g), (n_o - 1) & 1, kWaitLimitNs);
+                umma_commit(bar(bO + g));
+                (void)mbar_wait_bounded(bar(bO + g), n_o & 1, kWaitLimitNs);
             }
         }
         __syncwarp();
@@ -685,7 +696,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         float* row_max = reinterpret_cast<float*>(smem + C::OFF_MAX) + 256 * grp;
         // barriers: 1 all softmax warps, 2 and 3 a group, 4 .. 11 the two warps of the same rows
         const int pair_bar = 4 + 4 * grp + wq;
-        int tile0 = 0, job = 0, job_o = 0;             // tiles before this piece, this and the other group's jobs
+        int tile0 = 0, job = 0;                        // tiles before this piece, this group's jobs
+        int n_o = 0, n_oo = 0;                         // items that this and the other group had a part in
+        const bool speaker = half == 0 && wq == 0 && lane == 0;  // for its group
         bool ok = true;
         for (int i = 0;; ++i) {
             ok = named_bar_and(1, 512, warp_wait(piece_bar(i), piece_par(i)));
@@ -723,8 +736,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 id_next = page_id(t + step);
                 // The scores first: they tell that every slot up to this tile's K
                 // has landed, so the wait for V below is at most one phase ahead.
+                // P . V of the job before is done with, too.
                 if (ok) ok = warp_wait(bar(bS + grp), job & 1);
                 tc_fence_after();
+                if (speaker && ok) {
+                    mbar_arrive(bar(bFree + stage(n - 1)));                            // K
+                    if (two && job > job0) mbar_arrive(bar(bFree + stage(n - 2)));     // the V before
+                    if (job == job0) *reinterpret_cast<volatile uint32_t*>(go_on + grp) = 0u;
+                }
                 const uint32_t pages_now = __ballot_sync(0xffffffffu, id >= 0 && id < num_pages);
                 const bool inner = p0 + kTile <= ctx && pages_now == ~0u;
                 uint32_t vis0 = ~0u, vis1 = ~0u, bad0 = 0u, bad1 = 0u;  // of this half's 64 positions
@@ -825,8 +844,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     const float nm = move ? mx : m;
                     const float al = move ? fast_exp2(m - nm) : 1.f;
                     if (job > job0) {
-                        if (ok) ok = warp_wait(bar(bO + grp), (job - 1) & 1);
-                        tc_fence_after();
 #pragma unroll 1
                         for (int c = half * (D / 32); c < (half + 1) * (D / 32); ++c) {  // this half's columns of O
                             uint32_t o[16];
@@ -873,14 +890,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
                     tmem_wait_st();
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0 && ok) mbar_arrive(bar(bP + 2 * grp + half));  // this half of P
                 // ---- drafted tokens whose V is not finite, for the rows that see them ----
                 if (any_bad) {
-                    if (ok) ok = warp_wait(bar(bO + grp), job & 1);
-                    tc_fence_after();
                     const uint32_t* words = bad_tok + 16 * (job & 1) + 8 * grp;
+                    if (job == job0) {  // there is no O yet: it starts here, and P . V goes on from it
+                        const uint32_t zero[16] = {};
+#pragma unroll 1
+                        for (int c = half * (D / 32); c < (half + 1) * (D / 32); ++c) tmem_st16(tO + 16 * c, zero);
+                        tmem_wait_st();
+                        if (speaker) *reinterpret_cast<volatile uint32_t*>(go_on + grp) = 1u;
+                    }
 #pragma unroll 1
                     for (int j = 0; ok && j < kTile; ++j) {
                         if (!((words[j >> 5] | words[4 + (j >> 5)]) >> (j & 31) & 1)) continue;
@@ -921,14 +940,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         }
                     }
                     tc_fence_before();
-                    named_bar_and(pair_bar, 64, true);           // all of O before the next P of either half
+                    named_bar_and(pair_bar, 64, true);           // all of O before either half's P
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0 && ok) mbar_arrive(bar(bP + 2 * grp + half));  // this half of P
             }
             // ---- the piece's sums ---------------------------------------------------
             const int nt = t1 - w_t0;
             const bool mine = job > job0;
             const bool theirs = !two && nt > 1 - grp;
-            job_o += two ? nt : nt - (job - job0);
             {
                 uint32_t x[8] = {__float_as_uint(m), __float_as_uint(l), 0u, 0u, 0u, 0u, 0u, 0u};
                 tmem_st8(tG + C::ML_COL + C::ML_HALF * half, x);
@@ -957,9 +978,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(bX + i % kPieces));  // S may be written for the next item
-            if (mine) ok = warp_wait(bar(bO + grp), (job - 1) & 1);
-            if (theirs) ok = ok && warp_wait(bar(bO + 1 - grp), (job_o - 1) & 1);
+            if (mine) ok = warp_wait(bar(bO + grp), n_o & 1);
+            if (theirs) ok = ok && warp_wait(bar(bO + 1 - grp), n_oo & 1);
             tc_fence_after();
+            n_o += mine;
+            n_oo += two || nt > 1 - grp;
+            if (speaker && ok && two) mbar_arrive(bar(bFree + stage(2 * (tile0 + nt) - 1)));  // the last V
             if (ok && warp_live) {
                 const float M = fmaxf(m, mo);
                 const float f0 = m == -INFINITY ? 0.f : fast_exp2(m - M), f1 = mo == -INFINITY ? 0.f : fast_exp2(mo - M);
