@@ -30,18 +30,15 @@
 //                 with four commits), so a tile has one, for S: that S is there
 //                 also says that its K, and the V and the P before it, are done
 //                 with, and the softmax warps release them
-//   warps 4 - 11,
-//   warps 12 - 19 two softmax groups of eight warps (four for the 128 rows times
-//                 two for the halves of a tile's positions: with one warp for
-//                 a row's 128 positions the schedulers were idle two cycles of
-//                 three, waiting on dependent instructions), each with S, P and O of its own in tensor
+//   warps 4 - 7,
+//   warps 8 - 11  two softmax groups, each with S, P and O of its own in tensor
 //                 memory. One row tile: both have the same rows and take the
 //                 tiles in turn, and their sums are joined at the end (either
 //                 group reads the other's O directly). Two: each has its own
 //                 row tile, and every tile. While one group is in its softmax
 //                 the tensor cores work for the other; the next item's first
 //                 scores are computed while the item before writes its output.
-//   warps 20 - 23 FP8 caches: E4M3 bytes to f16 operand tiles (exact), q too
+//   warps 12 - 15 FP8 caches: E4M3 bytes to f16 operand tiles (exact), q too
 //
 // The online softmax keeps a reference maximum per row that moves only when a
 // tile's maximum passes it by more than 8 (log2), so P <= 2^8 and O is scaled
@@ -87,23 +84,23 @@ struct Cfg {
     // its waits for a free one are never two phases behind.)
     static constexpr int ST = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);
     static constexpr int RST = FP8 ? (D == 128 ? 3 : 6) : 0;
-    static constexpr int THREADS = FP8 ? 768 : 640;
+    static constexpr int THREADS = FP8 ? 512 : 384;
+    // Registers a thread: launched with 168 (128), dealt out again by role.
+    static constexpr int REG_IO = 88, REG_SM = FP8 ? 168 : 208, REG_CV = 88;
     static constexpr int OFF_Q = 0;                        // two row tiles of q
     static constexpr int OFF_T = OFF_Q + 2 * TILE;
     static constexpr int OFF_R = OFF_T + ST * TILE;
     static constexpr int OFF_SC = OFF_R + RST * RAW;       // FP8: [2][128] floats, 2^-k of each row
     static constexpr int OFF_BAR = OFF_SC + (FP8 ? kRows * 4 : 0);
-    static constexpr int NBAR = 2 * ST + 2 * RST + 16 + 3 * kPieces;
+    static constexpr int NBAR = 2 * ST + 2 * RST + 14 + 3 * kPieces;
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
-    static constexpr int OFF_PIECE = OFF_MISC + 320;       // [kPieces] Piece
-    static constexpr int OFF_MAX = OFF_PIECE + kPieces * 64;      // [2 groups][2 halves][128] row maxima
-    static constexpr int SMEM = OFF_MAX + 4 * 128 * 4 + 1024;     // + alignment slack
+    static constexpr int OFF_PIECE = OFF_MISC + 192;       // [kPieces] Piece
+    static constexpr int SMEM = OFF_PIECE + kPieces * 64 + 1024;  // + alignment slack
     static_assert(SMEM <= 232448, "shared memory of one CTA");
-    // Tensor-memory columns of a softmax group: S, then O. Either half's P lies
-    // over its own half of S (or behind O, where that leaves room), and its m
-    // and l for the others too.
-    static constexpr uint32_t P_COL = D == 64 ? 192 : 0, P_HALF = D == 64 ? 32 : 64;
-    static constexpr uint32_t ML_COL = 32, ML_HALF = 64;
+    static_assert(FP8 ? REG_IO + 2 * REG_SM + REG_CV <= 512 : REG_IO + 2 * REG_SM <= 504, "registers as launched");
+    // Tensor-memory columns of a softmax group: S (P over it, or behind O, where that leaves room), then O.
+    static constexpr uint32_t P_COL = D == 64 ? 192 : 0;
+    static constexpr uint32_t ML_COL = 64;                 // m and l for the other group, once S is read
     static constexpr uint32_t O_COL = 128;
 };
 
@@ -279,6 +276,14 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b_lo, u
 __device__ __forceinline__ void umma_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 // Lane-wise fma and add of two floats.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 r;
@@ -299,6 +304,11 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 __device__ __forceinline__ uint16_t lo16(uint32_t w) { return static_cast<uint16_t>(w & 0xFFFFu); }
 __device__ __forceinline__ uint16_t hi16(uint32_t w) { return static_cast<uint16_t>(w >> 16); }
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+// v[k] without an array in local memory
+__device__ __forceinline__ uint32_t word_of(const uint32_t (&v)[4], int k) {
+    return k == 0 ? v[0] : k == 1 ? v[1] : k == 2 ? v[2] : v[3];
+}
+
 // Workspace of partial sums: [2 per CTA][256 rows] of {m, l}, then [2 per
 // CTA][D / 4][256 rows] of 4 floats (a warp's rows are neighbours).
 __device__ __forceinline__ float* part_ml(void* ws, int slot, int row) {
@@ -320,15 +330,15 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t s0 = smem_u32(smem);
     enum : int { bFull = 0, bFree = C::ST, bRawFull = 2 * C::ST, bRawFree = bRawFull + C::RST, bS = bRawFree + C::RST,
-                 bP = bS + 2, bO = bP + 4, bQ = bO + 2, bQFree = bQ + 2, bQRaw = bQFree + 2, bX = bQRaw + 2,
+                 bP = bS + 2, bO = bP + 2, bQ = bO + 2, bQFree = bQ + 2, bQRaw = bQFree + 2, bX = bQRaw + 2,
                  bPiece = bX + kPieces, bPieceFree = bPiece + kPieces, bTurn = bPieceFree + kPieces };
     static_assert(bTurn + 2 == C::NBAR, "barriers");
     auto bar = [&](int i) -> uint32_t { return s0 + C::OFF_BAR + 8 * i; };
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
-    uint32_t* bad_tok = misc + 4;                         // [2 jobs][2 groups][2 halves][4 words]: drafted tokens, V not finite
-    Place* place = reinterpret_cast<Place*>(misc + 36);   // [2]: this CTA's first unit and the one past its last
-    int* warp_units = reinterpret_cast<int*>(misc + 42);  // [24]
+    uint32_t* bad_tok = misc + 4;                         // [2 jobs][2 groups][4 words]: drafted tokens, V not finite
+    Place* place = reinterpret_cast<Place*>(misc + 20);   // [2]: this CTA's first unit and the one past its last
+    int* warp_units = reinterpret_cast<int*>(misc + 26);  // [16]
     Piece* pieces = reinterpret_cast<Piece*>(smem + C::OFF_PIECE);
     uint32_t* go_on = misc + 2;                           // [2 groups]: O has been started by hand
     float* q_scale = reinterpret_cast<float*>(smem + C::OFF_SC);
@@ -347,18 +357,17 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(bar(bS + w), 1);
-            mbar_init(bar(bP + 2 * w), 4);  // either half of P
-            mbar_init(bar(bP + 2 * w + 1), 4);
+            mbar_init(bar(bP + w), 4);
             mbar_init(bar(bO + w), 1);
             mbar_init(bar(bQ + w), FP8 ? 4 : 1);
-            mbar_init(bar(bQFree + w), 16);  // the softmax warps (the last S, and the staged output)
+            mbar_init(bar(bQFree + w), 8);  // the softmax warps (the last S, and the staged output)
             mbar_init(bar(bQRaw + w), 1);
             mbar_init(bar(bTurn + w), 1);
         }
         for (int i = 0; i < kPieces; ++i) {
-            mbar_init(bar(bX + i), 16);
+            mbar_init(bar(bX + i), 8);
             mbar_init(bar(bPiece + i), 1);
-            mbar_init(bar(bPieceFree + i), FP8 ? 23 : 19);  // V copies, MMA, softmax, conversion
+            mbar_init(bar(bPieceFree + i), FP8 ? 15 : 11);  // V copies, MMA, softmax, conversion
         }
         *abort_flag = 0;
         place[0] = place[1] = Place{a.B, 0, 0};
@@ -444,6 +453,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     auto phase = [](int n) -> uint32_t { return (n / C::ST) & 1; };
 
     if (warp < 4) {
+        reg_dec<C::REG_IO>();
         if (warp == 0 || warp == 2) {
             // ======================= copies ===========================================
             // Warp 0 walks the pieces, hands them over, and loads q and K; warp 2 loads V.
@@ -617,7 +627,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         const uint32_t more_o = t > first || *reinterpret_cast<volatile uint32_t*>(go_on + g) != 0u;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            umma_ts(tS + C::O_COL, tS + C::P_COL + C::P_HALF * h + 8 * k, vt + (4 * h + k) * (2048 >> 4), kDescHi, kIdescPv,
+                            umma_ts(tS + C::O_COL, tS + C::P_COL + 32 * h + 8 * k, vt + (4 * h + k) * (2048 >> 4), kDescHi, kIdescPv,
                                     h + k > 0 ? 1u : more_o);
                     };
                     auto qk = [&]() {
@@ -629,14 +639,22 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                             else umma_ss<false>(tS, q + at, kt + at, kDescHi, idesc_qk);
                         }
                     };
-                    auto p_ready = [&](int h) { return lane_wait(bar(bP + 2 * g + h), n_pv & 1); };
+                    // (a wait costs 100 cycles when the phase is over, and 200 more when it
+                    // ends meanwhile: what has landed is looked up before P is waited for)
+                    bool here = false;
+                    if (t >= 0) {
+                        here = more && w.two == 0 && mbar_test_wait(bar(bFull + stage(n2)), phase(n2));
+                        if (more && w.two) ok = ok && landed(n2);
+                        ok = ok && lane_wait(bar(bP + g), n_pv & 1);
+                    } else if (w.two) {
+                        ok = ok && landed(n2);
+                    }
+                    if (!ok) break;
                     if (w.two) {
                         // Both groups are at the same tile: they take turns at the tensor
                         // cores, so that one computes weights while the other's products
                         // run (interleaved, both would finish, and wait, at the same time).
-                        if (t >= 0) ok = ok && p_ready(0) && p_ready(1);
-                        if (more) ok = ok && landed(n2);
-                        ok = ok && lane_wait(bar(bTurn + g), (turns - 1 + g) & 1);
+                        ok = lane_wait(bar(bTurn + g), (turns - 1 + g) & 1);
                         if (!ok) break;
                         ++turns;
                         if (t >= 0) {
@@ -647,18 +665,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         mbar_arrive(bar(bTurn + 1 - g));
                     } else {
                         if (t >= 0) {
-                            ok = ok && p_ready(0);     // the softmax hands P over in halves
-                            if (!ok) break;
                             pv(0);
-                            ok = p_ready(1);
-                            if (!ok) break;
                             pv(1);
                             // (one row tile is bound by memory: V's stage is wanted back at once)
                             umma_commit(bar(bFree + stage(n)));
                             if (t + 1 < nt) ok = see_tile(t + 1);
                         }
                         if (more) {
-                            ok = ok && landed(n2);
+                            ok = ok && (here || landed(n2));
                             if (!ok) break;
                             qk();
                         }
@@ -686,22 +700,20 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             }
         }
         __syncwarp();
-    } else if (warp < 20) {
+    } else if (warp < 12) {
         // ======================= softmax ==========================================
-        const int grp = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, wq = warp & 3;
+        reg_inc<C::REG_SM>();
+        const int grp = (warp - 4) >> 2, wq = warp & 3;
         const int row_l = 32 * wq + lane;              // this thread's lane of tensor memory
         const uint32_t tl = tmem + (static_cast<uint32_t>(wq) << 21);  // lanes 32 wq .. (bits 16 and up)
-        const uint32_t tG = tl + 256 * grp, tS = tG + 64 * half, tP = tG + C::P_COL + C::P_HALF * half, tO = tG + C::O_COL;
+        const uint32_t tS = tl + 256 * grp, tP = tS + C::P_COL, tO = tS + C::O_COL;
         const int tok_l = row_l / a.G, g_l = row_l - tok_l * a.G;      // its token in the row tile, its head
-        float* row_max = reinterpret_cast<float*>(smem + C::OFF_MAX) + 256 * grp;
-        // barriers: 1 all softmax warps, 2 and 3 a group, 4 .. 11 the two warps of the same rows
-        const int pair_bar = 4 + 4 * grp + wq;
         int tile0 = 0, job = 0;                        // tiles before this piece, this group's jobs
         int n_o = 0, n_oo = 0;                         // items that this and the other group had a part in
-        const bool speaker = half == 0 && wq == 0 && lane == 0;  // for its group
+        const bool speaker = wq == 0 && lane == 0;     // for its group
         bool ok = true;
         for (int i = 0;; ++i) {
-            ok = named_bar_and(1, 512, warp_wait(piece_bar(i), piece_par(i)));
+            ok = named_bar_and(1, 256, warp_wait(piece_bar(i), piece_par(i)));
             const Piece& w = pieces[i % kPieces];
             if (!ok || w.b < 0) break;
             const bool two = w.two;
@@ -709,6 +721,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             const bool live = tok_l < a.tile_toks && tok_t < w.toks;
             const bool warp_live = __any_sync(0xffffffffu, live);
             const int tok = live ? w.tok0 + tok_t : 0;                 // this row's drafted token
+            const int row = (two ? 128 * grp : 0) + row_l;             // its place in partial sums
+            const uint32_t* mrow = a.mask != nullptr && live ? a.mask + (w.q0 + tok) * a.mask_s0 : nullptr;
             float sl = fabsf(a.scale_log2), vs = 1.f;
             if constexpr (FP8) {
                 w.buffers([&](int bf, int uses) { ok = ok && warp_wait(bar(bQ + bf), uses & 1); });
@@ -720,7 +734,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             const int32_t* table = a.block_tables + w.b * a.bt_s0;
             const int npages = (L + kPageSize - 1) / kPageSize;
             const int job0 = job;
-            float m = -INFINITY, l = 0.f;              // the row's reference maximum; this half's sum
+            float m = -INFINITY, l = 0.f;
             const int step = two ? 1 : 2;
             // lanes 0-7: the tile's pages, read one tile ahead
             auto page_id = [&](int t) -> int {
@@ -730,29 +744,17 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             const int tb = w_t0 + (two ? 0 : grp);
             int id_next = page_id(tb);
             for (int t = tb; t < t1; t += step, ++job) {
-                const int p0 = t * kTile, h0 = p0 + 64 * half;   // first position of the tile, of this half
+                const int p0 = t * kTile;
                 const int n = 2 * (tile0 + t - w_t0) + 1;        // ring slot of the tile's V
                 const int id = id_next;
                 id_next = page_id(t + step);
-                // The scores first: they tell that every slot up to this tile's K
-                // has landed, so the wait for V below is at most one phase ahead.
-                // P . V of the job before is done with, too.
-                if (ok) ok = warp_wait(bar(bS + grp), job & 1);
-                tc_fence_after();
-                if (speaker && ok) {
-                    mbar_arrive(bar(bFree + stage(n - 1)));                            // K
-                    if (two && job > job0) mbar_arrive(bar(bFree + stage(n - 2)));     // the V before
-                    if (job == job0) *reinterpret_cast<volatile uint32_t*>(go_on + grp) = 0u;
-                }
                 const uint32_t pages_now = __ballot_sync(0xffffffffu, id >= 0 && id < num_pages);
                 const bool inner = p0 + kTile <= ctx && pages_now == ~0u;
-                uint32_t vis0 = ~0u, vis1 = ~0u, bad0 = 0u, bad1 = 0u;  // of this half's 64 positions
-                bool any_bad = false;                            // (uniform, of the tile)
+                uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u}, bad[4] = {0u, 0u, 0u, 0u};
                 if (!inner) {
-                    const uint32_t* mrow = a.mask != nullptr && live ? a.mask + (w.q0 + tok) * a.mask_s0 : nullptr;
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int q0 = h0 + 32 * k, j0 = q0 - ctx;
+                    for (int k = 0; k < 4; ++k) {
+                        const int q0 = p0 + 32 * k, j0 = q0 - ctx;
                         uint32_t v = live ? low_bits(L - q0) : 0u;
                         if (j0 > -32) {
                             if (a.mask == nullptr) {
@@ -764,22 +766,31 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                                 v &= __funnelshift_r(lo, hi, j0 & 31);
                             }
                         }
-                        const uint32_t pg = pages_now >> (4 * half + 2 * k);
-                        if (!(pg & 1)) v &= 0xFFFF0000u;
-                        if (!(pg & 2)) v &= 0x0000FFFFu;
-                        (k ? vis1 : vis0) = v;
+                        if (!(pages_now >> (2 * k) & 1)) v &= 0xFFFF0000u;
+                        if (!(pages_now >> (2 * k + 1) & 1)) v &= 0x0000FFFFu;
+                        vis[k] = v;
                     }
+                }
+                // The scores first: they tell that every slot up to this tile's K
+                // has landed, so the wait for V below is at most one phase ahead.
+                // P . V of the job before is done with, too.
+                if (ok) ok = warp_wait(bar(bS + grp), job & 1);
+                tc_fence_after();
+                if (speaker && ok) {
+                    mbar_arrive(bar(bFree + stage(n - 1)));                            // K
+                    if (two && job > job0) mbar_arrive(bar(bFree + stage(n - 2)));     // the V before
+                    if (job == job0) *reinterpret_cast<volatile uint32_t*>(go_on + grp) = 0u;
                 }
                 // ---- V rows that a weight of zero would not silence --------------------
                 if (p0 + kTile > ctx) {
                     const bool landed = ok && warp_wait(bar(bFull + stage(n)), phase(n));
-                    const int pos = p0 + row_l;                  // thread = half a row of the tile here
+                    const int pos = p0 + row_l;                  // thread = row of the tile here
                     const uint32_t vrow = s0 + C::OFF_T + stage(n) * C::TILE + row_l * 128;
                     bool odd = false;
                     if (landed && pos >= ctx && pos < L) {
                         constexpr uint32_t EX = FP8 ? 0x7C00u : 0x7F80u;
 #pragma unroll 4
-                        for (int c = half * (D / 16); c < (half + 1) * (D / 16); ++c) {
+                        for (int c = 0; c < D / 8; ++c) {
                             const uint4 x = lds128(vrow + (c >> 3) * C::BLOCK + ((c ^ row_l) & 7) * 16);
                             const uint32_t v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -787,137 +798,131 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         }
                     }
                     const uint32_t word = __ballot_sync(0xffffffffu, odd);
-                    uint32_t* words = bad_tok + 16 * (job & 1) + 8 * grp;
-                    if (lane == 0) words[4 * half + wq] = word;
+                    uint32_t* words = bad_tok + 8 * (job & 1) + 4 * grp;
+                    if (lane == 0) words[wq] = word;
                     // all who share the tile have looked at it before a row is zeroed
-                    ok = two ? named_bar_and(1, 512, landed) : named_bar_and(2 + grp, 256, landed);
-                    uint32_t all = 0u;
+                    ok = two ? named_bar_and(1, 256, landed) : named_bar_and(2 + grp, 128, landed);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) all |= words[k] | words[4 + k];
-                    any_bad = all != 0u;
-                    bad0 = words[2 * half] | words[4 + 2 * half];
-                    bad1 = words[2 * half + 1] | words[5 + 2 * half];
-                    if (ok && (((words[wq] | words[4 + wq]) >> lane & 1) || pos >= L)) {
-#pragma unroll 4
-                        for (int c = half * (D / 16); c < (half + 1) * (D / 16); ++c)
-                            sts128u(vrow + (c >> 3) * C::BLOCK + c % 8 * 16, 0u, 0u, 0u, 0u);
+                    for (int k = 0; k < 4; ++k) bad[k] = words[k];
+                    if (ok && (odd || pos >= L)) {
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c) sts128u(vrow + (c >> 3) * C::BLOCK + c % 8 * 16, 0u, 0u, 0u, 0u);
                     }
                     fence_proxy_async_smem();
-                    // either half's zeros come before either half's weights
-                    ok = two ? named_bar_and(1, 512, ok) : named_bar_and(2 + grp, 256, ok);
                 }
-                // ---- this half's scores, 32 columns at a time (read twice: holding them
-                // ---- would spill)
-                auto columns = [&](int c, uint32_t (&x)[32]) {
-                    tmem_ld32(tS + 32 * c, x);
+                const bool any_bad = (bad[0] | bad[1] | bad[2] | bad[3]) != 0u;  // (uniform)
+                // ---- the tile's softmax, 64 columns at a time (S is read twice: holding
+                // ---- all of it would spill, and short loops stay in the instruction cache)
+                auto columns = [&](int c, uint32_t (&x)[2][32]) {
+                    tmem_ld32(tS + 64 * c, x[0]);
+                    tmem_ld32(tS + 64 * c + 32, x[1]);
                     tmem_wait_ld();
-                    pin(x);
+                    pin(x[0]);
+                    pin(x[1]);
                     if (!inner) {
-                        const uint32_t v = c ? vis1 : vis0;
+                        const uint32_t v0 = c ? vis[2] : vis[0], v1 = c ? vis[3] : vis[1];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!(v & (1u << e))) x[e] = 0xFF800000u;
+                        for (int e = 0; e < 32; ++e) {
+                            if (!(v0 & (1u << e))) x[0][e] = 0xFF800000u;
+                            if (!(v1 & (1u << e))) x[1][e] = 0xFF800000u;
+                        }
                     }
                 };
                 const bool work = ok && warp_live;
-                float mx = -INFINITY;
                 if (work) {
                     float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
                     for (int c = 0; c < 2; ++c) {
-                        uint32_t x[32];
+                        uint32_t x[2][32];
                         columns(c, x);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2)
-                            mx4[e / 2 & 3] = fmaxf(fmaxf(mx4[e / 2 & 3], __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
-                    }
-                    mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl;
-                }
-                // The two halves of a row keep one reference maximum: they confer only
-                // when either wants to move it.
-                auto moves = [&](float x) { return x > m + kRescaleLog2 || (m == -INFINITY && x > m); };
-                if (!named_bar_and(pair_bar, 64, !moves(mx))) {
-                    row_max[128 * half + row_l] = mx;
-                    named_bar_and(pair_bar, 64, true);
-                    mx = fmaxf(mx, row_max[128 * (1 - half) + row_l]);
-                    const bool move = moves(mx);
-                    const float nm = move ? mx : m;
-                    const float al = move ? fast_exp2(m - nm) : 1.f;
-                    if (job > job0) {
-#pragma unroll 1
-                        for (int c = half * (D / 32); c < (half + 1) * (D / 32); ++c) {  // this half's columns of O
-                            uint32_t o[16];
-                            tmem_ld16(tO + 16 * c, o);
-                            tmem_wait_ld();
-                            pin(o);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-                            tmem_st16(tO + 16 * c, o);
+                        for (int e = 0; e < 32; e += 2) {
+                            mx4[e & 2] = fmaxf(fmaxf(mx4[e & 2], __uint_as_float(x[0][e])), __uint_as_float(x[0][e + 1]));
+                            mx4[(e & 2) + 1] = fmaxf(fmaxf(mx4[(e & 2) + 1], __uint_as_float(x[1][e])), __uint_as_float(x[1][e + 1]));
                         }
-                        tmem_wait_st();
-                        tc_fence_before();
-                        named_bar_and(pair_bar, 64, true);       // all of O before either half's P
                     }
-                    l *= al;
-                    m = nm;
-                }
-                if (work) {
-                    const float mm = m == -INFINITY ? 0.f : -m;
-                    const float2 sl2 = make_float2(sl, sl), mm2 = make_float2(mm, mm);
-                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl;
+                    const bool move = mx > m + kRescaleLog2 || (m == -INFINITY && mx > m);
+                    if (__any_sync(0xffffffffu, move)) {
+                        const float nm = move ? mx : m;
+                        const float al = move ? fast_exp2(m - nm) : 1.f;
+                        if (job > job0) {
 #pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t x[32], p[16];
-                        columns(c, x);
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[32];
+                                tmem_ld32(tO + 32 * c, o);
+                                tmem_wait_ld();
+                                pin(o);
+                                uint32_t h0[16], h1[16];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float2 y = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sl2, mm2);
-                            y.x = fast_exp2(y.x);
-                            y.y = fast_exp2(y.y);
-                            sum[e & 1] = add2(sum[e & 1], y);
-                            p[e] = FP8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
-                        }
-                        if (any_bad) {
-                            const uint32_t b = c ? bad1 : bad0;
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                if (b & (1u << (2 * e))) p[e] &= 0xFFFF0000u;
-                                if (b & (2u << (2 * e))) p[e] &= 0x0000FFFFu;
+                                for (int e = 0; e < 16; ++e) {
+                                    h0[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                                    h1[e] = __float_as_uint(__uint_as_float(o[16 + e]) * al);
+                                }
+                                tmem_st16(tO + 32 * c, h0);
+                                tmem_st16(tO + 32 * c + 16, h1);
                             }
                         }
-                        tmem_st16(tP + 16 * c, p);
+                        l *= al;
+                        m = nm;
                     }
-                    l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
-                    tmem_wait_st();
                 }
+                const float mm = m == -INFINITY ? 0.f : -m;
+                const float2 sl2 = make_float2(sl, sl), mm2 = make_float2(mm, mm);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                    if (work) {
+                        uint32_t x[2][32];
+                        columns(c, x);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t p[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float2 y = fma2(make_float2(__uint_as_float(x[h][2 * e]), __uint_as_float(x[h][2 * e + 1])), sl2, mm2);
+                                y.x = fast_exp2(y.x);
+                                y.y = fast_exp2(y.y);
+                                sum[e & 1] = add2(sum[e & 1], y);
+                                p[e] = FP8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
+                            }
+                            if (any_bad) {
+                                const uint32_t b = word_of(bad, 2 * c + h);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    if (b & (1u << (2 * e))) p[e] &= 0xFFFF0000u;
+                                    if (b & (2u << (2 * e))) p[e] &= 0x0000FFFFu;
+                                }
+                            }
+                            tmem_st16(tP + 32 * c + 16 * h, p);
+                        }
+                    }
+                }
+                tmem_wait_st();
+                l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
                 // ---- drafted tokens whose V is not finite, for the rows that see them ----
                 if (any_bad) {
-                    const uint32_t* words = bad_tok + 16 * (job & 1) + 8 * grp;
                     if (job == job0) {  // there is no O yet: it starts here, and P . V goes on from it
                         const uint32_t zero[16] = {};
 #pragma unroll 1
-                        for (int c = half * (D / 32); c < (half + 1) * (D / 32); ++c) tmem_st16(tO + 16 * c, zero);
+                        for (int c = 0; c < D / 16; ++c) tmem_st16(tO + 16 * c, zero);
                         tmem_wait_st();
                         if (speaker) *reinterpret_cast<volatile uint32_t*>(go_on + grp) = 1u;
                     }
-#pragma unroll 1
                     for (int j = 0; ok && j < kTile; ++j) {
-                        if (!((words[j >> 5] | words[4 + (j >> 5)]) >> (j & 31) & 1)) continue;
-                        const int pos = p0 + j, jd = pos - ctx;
-                        const int pid = __ldg(table + pos / kPageSize);
-                        if (pid < 0 || pid >= num_pages) continue;
-                        const int off = pos % kPageSize;
-                        const int64_t kb = pid * a.kc_s0 + off * a.kc_st + w.kvh * a.kc_sh;
-                        const int64_t vb = pid * a.vc_s0 + off * a.vc_st + w.kvh * a.vc_sh;
+                        if (!(word_of(bad, j >> 5) >> (j & 31) & 1)) continue;
+                        const int id = __ldg(table + (p0 + j) / kPageSize);
+                        if (id < 0 || id >= num_pages) continue;
+                        const int off = (p0 + j) % kPageSize;
+                        const int64_t kb = id * a.kc_s0 + off * a.kc_st + w.kvh * a.kc_sh;
+                        const int64_t vb = id * a.vc_s0 + off * a.vc_st + w.kvh * a.vc_sh;
                         auto at = [&](const void* base, int64_t i) -> float {
                             if constexpr (FP8)
                                 return __half2float(__ushort_as_half(static_cast<unsigned short>(
                                     e4m3x2_to_f16x2(static_cast<const uint8_t*>(base)[i]) & 0xFFFFu)));
                             return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(base)[i]) << 16);
                         };
-                        const bool sees = live && (a.mask == nullptr
-                                                       ? jd <= tok
-                                                       : jd < 32 * a.W && (__ldg(a.mask + (w.q0 + tok) * a.mask_s0 + (jd >> 5)) >> (jd & 31) & 1));
+                        const bool sees = live && (word_of(vis, j >> 5) >> (j & 31) & 1);
                         float x = 0.f;
                         if (sees) {
                             const uint16_t* qr = a.q + (w.q0 + tok) * a.q_s0 + (w.kvh * a.G + g_l) * a.q_s1;
@@ -927,7 +932,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                             x = fast_exp2(x - (m == -INFINITY ? 0.f : m));
                         }
 #pragma unroll 1
-                        for (int c = half * (D / 32); c < (half + 1) * (D / 32); ++c) {
+                        for (int c = 0; c < D / 16; ++c) {
                             uint32_t o[16];
                             tmem_ld16(tO + 16 * c, o);
                             tmem_wait_ld();
@@ -939,41 +944,32 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                             tmem_wait_st();
                         }
                     }
-                    tc_fence_before();
-                    named_bar_and(pair_bar, 64, true);           // all of O before either half's P
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0 && ok) mbar_arrive(bar(bP + 2 * grp + half));  // this half of P
+                if (lane == 0 && ok) mbar_arrive(bar(bP + grp));
             }
             // ---- the piece's sums ---------------------------------------------------
             const int nt = t1 - w_t0;
             const bool mine = job > job0;
             const bool theirs = !two && nt > 1 - grp;
-            {
+            float mo = -INFINITY, lo = 0.f;            // the other group's
+            if (!two) {
                 uint32_t x[8] = {__float_as_uint(m), __float_as_uint(l), 0u, 0u, 0u, 0u, 0u, 0u};
-                tmem_st8(tG + C::ML_COL + C::ML_HALF * half, x);
+                tmem_st8(tS + C::ML_COL, x);
                 tmem_wait_st();
             }
             tc_fence_before();
-            ok = named_bar_and(1, 512, ok);            // every S of this piece is read
+            ok = named_bar_and(1, 256, ok);            // every S of this piece is read
             tc_fence_after();
             if (!ok) break;
-            float mo = -INFINITY, lo = 0.f;            // the other group's
-            {
-                uint32_t x[8], y[8], z[8];
-                tmem_ld8(tG + C::ML_COL + C::ML_HALF * (1 - half), x);
-                tmem_ld8(tl + 256 * (1 - grp) + C::ML_COL, y);
-                tmem_ld8(tl + 256 * (1 - grp) + C::ML_COL + C::ML_HALF, z);
+            if (!two) {
+                uint32_t x[8];
+                tmem_ld8(tl + 256 * (1 - grp) + C::ML_COL, x);
                 tmem_wait_ld();
                 pin(x);
-                pin(y);
-                pin(z);
-                l += __uint_as_float(x[1]);
-                if (!two) {
-                    mo = __uint_as_float(y[0]);
-                    lo = __uint_as_float(y[1]) + __uint_as_float(z[1]);
-                }
+                mo = __uint_as_float(x[0]);
+                lo = __uint_as_float(x[1]);
             }
             tc_fence_before();
             __syncwarp();
@@ -992,10 +988,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 const bool none = sum == 0.f;
                 const float inv = whole ? (none ? 0.f : vs / sum) : vs, k0 = f0 * inv, k1 = f1 * inv;
                 const int h = w.kvh * a.G + g_l;
-                const int row = (two ? 128 * grp : 0) + row_l;             // its place in partial sums
                 const int slot = 2 * static_cast<int>(blockIdx.x) + (w_t0 == 0 ? 1 : 0);
                 float* part = part_o<D>(a.workspace, gridDim.x, slot, row);
-                if (live && (two || grp == 0) && half == 0) {
+                if (live && (two || grp == 0)) {
                     if (!whole) {
                         *reinterpret_cast<float2*>(part_ml(a.workspace, slot, row)) = make_float2(M, sum);
                     } else if (a.lse) {
@@ -1003,11 +998,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                             none ? -INFINITY : (M + __log2f(sum)) * 0.69314718055994530942f;
                     }
                 }
-                // Two row tiles: either half has half of this row's columns; else all
-                // four warps of the row a quarter. A whole item's output goes through
-                // q's buffer (the warp's own 32 rows), so that the warp writes rows and
-                // not columns.
-                const int c0 = two ? half * (D / 32) : (2 * grp + half) * (D / 64), c1 = c0 + (two ? D / 32 : D / 64);  // 16 columns each
+                // Two row tiles: all of this row's columns; else each group half of them.
+                // A whole item's output goes through q's buffer (the warp's own 32
+                // rows), so that the warp writes rows and not columns.
+                const int c0 = two ? 0 : grp * (D / 32), c1 = two ? D / 16 : c0 + D / 32;  // 16 columns each
                 const uint32_t stage_row = s0 + C::OFF_Q + (two ? grp : w.buf) * C::TILE + row_l * 128;
 #pragma unroll 1
                 for (int c = c0; c < c1; ++c) {
@@ -1041,11 +1035,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 if (whole) {
                     __syncwarp();
                     const int64_t off = live ? (w.q0 + tok) * a.o_s0 + h * a.o_s1 : -1;  // this lane's row
-                    const int per_row = 2 * (c1 - c0);                                    // 16-byte chunks: 8, 4 or 2
+                    const int per_row = 2 * (c1 - c0);                                      // 16-byte chunks: 16, 8 or 4
                     const int sub = lane / per_row, ch = 2 * c0 + lane - sub * per_row;
-#pragma unroll 2
-                    for (int k = 0; k < per_row; ++k) {
-                        const int r = k * (32 / per_row) + sub;
+#pragma unroll 4
+                    for (int i = 0; i < per_row; ++i) {
+                        const int r = i * (32 / per_row) + sub;
                         const int64_t o = __shfl_sync(0xffffffffu, off, r);
                         const uint4 v = lds128(stage_row + (r - lane) * 128 + (ch >> 3) * C::BLOCK + ((ch ^ r) & 7) * 16);
                         if (o >= 0) *reinterpret_cast<uint4*>(a.out + o + 8 * ch) = v;
@@ -1059,13 +1053,13 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 mbar_arrive(bar(bPieceFree + i % kPieces));
             }
             tc_fence_before();
-            // O is read by both halves, and by both groups
-            ok = two ? named_bar_and(2 + grp, 256, ok) : named_bar_and(1, 512, ok);
+            if (!two) ok = named_bar_and(1, 256, ok);  // either group's O is read by both
             tile0 += nt;
         }
     } else {
         // ======================= E4M3 bytes and bf16 q to f16 tiles ===============
-        const int ct = tid - 640;
+        reg_dec<C::REG_CV>();
+        const int ct = tid - 384;
         constexpr int CH = D / 16;  // 16-byte chunks of a raw row
         int n = 0;
         bool ok = true;
