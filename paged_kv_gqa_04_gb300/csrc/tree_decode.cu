@@ -79,10 +79,19 @@ struct Cfg {
     static constexpr int BLOCK = kTile * 128;              // one column block of it
     static constexpr int RAW = kTile * D;                  // FP8 tile as it lands
     static constexpr int RBOX = D >= 128 ? 128 : D;        // its row (and swizzle span)
-    // Rings of K and V tiles in turn: operand tiles, and (FP8) tiles of bytes.
-    // (bf16: an even number, so that either copy warp has stages of its own and
-    // its waits for a free one are never two phases behind.)
-    static constexpr int ST = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);
+    // Operand tiles: K and V have rings of their own (so either copy warp's waits
+    // for a free stage are never two phases behind). FP8: one ring of K and V in
+    // turn, filled in order by the conversion, and one of tiles of bytes.
+    static constexpr int SK = D == 128 ? 3 : 4, SV = D == 128 ? 2 : 4;
+    static constexpr int ST = FP8 ? (D == 128 ? 3 : 6) : SK + SV;
+    // Slot n: K of tile n / 2 or, n odd, its V (tiles numbered through the CTA's stretch).
+    static __device__ __forceinline__ int stage(int n) {
+        return FP8 ? n % ST : n & 1 ? SK + (n >> 1) % SV : (n >> 1) % SK;
+    }
+    static __device__ __forceinline__ int round(int n) { return FP8 ? n / ST : n & 1 ? (n >> 1) / SV : (n >> 1) / SK; }
+    // The same for the ring that the copies fill.
+    static __device__ __forceinline__ int copy_stage(int n) { return FP8 ? n % RST : stage(n); }
+    static __device__ __forceinline__ int copy_round(int n) { return FP8 ? n / RST : round(n); }
     static constexpr int RST = FP8 ? (D == 128 ? 3 : 6) : 0;
     static constexpr int THREADS = FP8 ? 512 : 384;
     // Registers a thread: launched with 168 (128), dealt out again by role.
@@ -447,10 +456,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     // Piece i of this CTA, handed over in a ring
     auto piece_bar = [&](int i) { return bar(bPiece + i % kPieces); };
     auto piece_par = [](int i) -> uint32_t { return (i / kPieces) & 1; };
-    // Slot n of the operand ring (K of tile i is 2 i, V is 2 i + 1; tiles are
-    // numbered through the CTA's stretch).
-    auto stage = [](int n) { return n % C::ST; };
-    auto phase = [](int n) -> uint32_t { return (n / C::ST) & 1; };
+    auto stage = [](int n) { return C::stage(n); };
+    auto phase = [](int n) -> uint32_t { return C::round(n) & 1; };
 
     if (warp < 4) {
         reg_dec<C::REG_IO>();
@@ -458,7 +465,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             // ======================= copies ===========================================
             // Warp 0 walks the pieces, hands them over, and loads q and K; warp 2 loads V.
             const int v = warp >> 1;
-            constexpr int RING = FP8 ? C::RST : C::ST;
             constexpr int FULL = FP8 ? bRawFull : bFull, FREE = FP8 ? bRawFree : bFree;
             constexpr int COPIES = FP8 ? kTilePages : kTilePages * C::NB;  // per tile
             const int pg = lane % kTilePages, blk = lane / kTilePages;     // this lane's copy
@@ -537,9 +543,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         bad |= t * kTilePages + pg < npages;
                         id = static_cast<int>(num_pages);  // out of range: the copy fills zeros
                     }
-                    const int st = n % RING;
-                    if (n >= RING) {
-                        const uint32_t fr = bar(FREE + st), par = (n / RING - 1) & 1;
+                    const int st = C::copy_stage(n), rd = C::copy_round(n);
+                    if (rd > 0) {
+                        const uint32_t fr = bar(FREE + st), par = (rd - 1) & 1;
                         // the ring may be waiting for this very piece's q
                         while (ok && q_wanted && !__all_sync(0xffffffffu, mbar_try_wait_suspend(fr, par, 1000u))) {
                             load_q();
@@ -567,10 +573,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             if (bad && blk == 0 && v == 0) flag_error(a.err, PKV_FLAG_PAGE_RANGE);
             if (lane == 0) {
                 if (v == 0) reinterpret_cast<int4*>(a.workspace)[blockIdx.x] = meta;
-                // Copies under way land before the CTA may exit (slots whose stage
-                // neither copy warp has taken again).
-                for (int i = n - 2; i >= 0 && i > n - 1 - v - RING; i -= 2)
-                    (void)mbar_wait_bounded(bar(FULL + i % RING), (i / RING) & 1, kWaitLimitNs);
+                // Copies under way land before the CTA may exit: the last ones of every
+                // stage that neither copy warp has taken again.
+                constexpr int BACK = FP8 ? C::RST : 2 * (C::SK > C::SV ? C::SK : C::SV);
+                for (int i = n - 2; i >= 0 && i > n - 1 - v - BACK; i -= 2)
+                    if (FP8 || i + 2 * (v ? C::SV : C::SK) >= n)
+                        (void)mbar_wait_bounded(bar(FULL + C::copy_stage(i)), C::copy_round(i) & 1, kWaitLimitNs);
                 if (uses0) (void)mbar_wait_bounded(bar(FP8 ? bQRaw : bQ), (uses0 - 1) & 1, kWaitLimitNs);
                 if (uses1) (void)mbar_wait_bounded(bar((FP8 ? bQRaw : bQ) + 1), (uses1 - 1) & 1, kWaitLimitNs);
             }
@@ -1100,7 +1108,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 for (int v = 0; v < 2; ++v, ++n) {
                     const int rs = C::RST ? n % C::RST : 0;
                     ok = warp_wait(bar(bRawFull + rs), (n / (C::RST ? C::RST : 1)) & 1);
-                    if (ok && n >= C::ST) ok = warp_wait(bar(bFree + stage(n)), (n / C::ST - 1) & 1);
+                    if (ok && n >= C::ST) ok = warp_wait(bar(bFree + stage(n)), (C::round(n) - 1) & 1);
                     if (!ok) break;
                     const uint32_t src = s0 + C::OFF_R + rs * C::RAW, dst = s0 + C::OFF_T + stage(n) * C::TILE;
                     const int ch = ct % CH;
