@@ -17,19 +17,19 @@
 // item, the start of another), which a second kernel joins.
 //
 // A CTA's roles, per tile:
-//   warp 0        walks the CTA's items, hands the pieces to the other roles, and
-//                 loads q and K by TMA
-//   warp 2        TMA tile loads of V, into the same ring (a warp starts a 16-row
-//                 x 128-byte copy in about 85 cycles: one for both would be the
-//                 limit). Pages that do not exist are read out of range, which
-//                 fills zeros
-//   warps 1, 3    one thread each, for one softmax group: S = Q . K^T and O += P . V
-//                 (M = 128; P from tensor memory, V as an MN-major operand:
-//                 nothing is transposed). A tcgen05.commit holds the products
-//                 behind it up for about 105 cycles (16 MMAs: 1054 cycles, 1481
-//                 with four commits), so a tile has one, for S: that S is there
-//                 also says that its K, and the V and the P before it, are done
-//                 with, and the softmax warps release them
+//   warps 0, 2    TMA tile loads of K and of V (a warp starts a 16-row x 128-byte
+//                 copy in about 85 cycles: one for both would be the limit).
+//                 Pages that do not exist are read out of range, which fills
+//                 zeros
+//   warp 3        walks the CTA's items, hands the pieces to the other roles, and
+//                 loads q by TMA
+//   warp 1        one thread issues S = Q . K^T and O += P . V (M = 128; P from
+//                 tensor memory, V as an MN-major operand: nothing is
+//                 transposed). A tcgen05.commit holds the products behind it
+//                 up for about 105 cycles (16 MMAs: 1054 cycles, 1481 with four
+//                 commits), so a tile has one, for S: that S is there also says
+//                 that its K, and the V and the P before it, are done with, and
+//                 the softmax warps release them
 //   warps 4 - 7,
 //   warps 8 - 11  two softmax groups, each with S, P and O of its own in tensor
 //                 memory. One row tile: both have the same rows and take the
@@ -101,7 +101,7 @@ struct Cfg {
     static constexpr int OFF_R = OFF_T + ST * TILE;
     static constexpr int OFF_SC = OFF_R + RST * RAW;       // FP8: [2][128] floats, 2^-k of each row
     static constexpr int OFF_BAR = OFF_SC + (FP8 ? kRows * 4 : 0);
-    static constexpr int NBAR = 2 * ST + 2 * RST + 14 + 3 * kPieces;
+    static constexpr int NBAR = 2 * ST + 2 * RST + 13 + 3 * kPieces;
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
     static constexpr int OFF_PIECE = OFF_MISC + 192;       // [kPieces] Piece
     static constexpr int SMEM = OFF_PIECE + kPieces * 64 + 1024;  // + alignment slack
@@ -340,8 +340,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     const uint32_t s0 = smem_u32(smem);
     enum : int { bFull = 0, bFree = C::ST, bRawFull = 2 * C::ST, bRawFree = bRawFull + C::RST, bS = bRawFree + C::RST,
                  bP = bS + 2, bO = bP + 2, bQ = bO + 2, bQFree = bQ + 2, bQRaw = bQFree + 2, bX = bQRaw + 2,
-                 bPiece = bX + kPieces, bPieceFree = bPiece + kPieces, bTurn = bPieceFree + kPieces };
-    static_assert(bTurn + 2 == C::NBAR, "barriers");
+                 bPiece = bX + kPieces, bPieceFree = bPiece + kPieces, bEnd = bPieceFree + kPieces };
+    static_assert(bEnd + 1 == C::NBAR, "barriers");
     auto bar = [&](int i) -> uint32_t { return s0 + C::OFF_BAR + 8 * i; };
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     if (tid == 0) {
         for (int i = 0; i < C::ST; ++i) {
             mbar_init(bar(bFull + i), FP8 ? 4 : 1);
-            mbar_init(bar(bFree + i), 2);  // either group: its use, or (its MMA thread) a tile of the other group seen
+            mbar_init(bar(bFree + i), 2);  // either group's use (two arrivals where one group has the tile)
         }
         for (int i = 0; i < C::RST; ++i) {
             mbar_init(bar(bRawFull + i), 1);
@@ -371,12 +371,12 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             mbar_init(bar(bQ + w), FP8 ? 4 : 1);
             mbar_init(bar(bQFree + w), 8);  // the softmax warps (the last S, and the staged output)
             mbar_init(bar(bQRaw + w), 1);
-            mbar_init(bar(bTurn + w), 1);
         }
+        mbar_init(bar(bEnd), 1);
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(bar(bX + i), 8);
             mbar_init(bar(bPiece + i), 1);
-            mbar_init(bar(bPieceFree + i), FP8 ? 15 : 11);  // V copies, MMA, softmax, conversion
+            mbar_init(bar(bPieceFree + i), FP8 ? 15 : 11);  // copies, MMA, softmax, conversion
         }
         *abort_flag = 0;
         place[0] = place[1] = Place{a.B, 0, 0};
@@ -462,74 +462,21 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     if (warp < 4) {
         reg_dec<C::REG_IO>();
         if (warp == 0 || warp == 2) {
-            // ======================= copies ===========================================
-            // Warp 0 walks the pieces, hands them over, and loads q and K; warp 2 loads V.
+            // ======================= copies of K, of V ================================
             const int v = warp >> 1;
             constexpr int FULL = FP8 ? bRawFull : bFull, FREE = FP8 ? bRawFree : bFree;
             constexpr int COPIES = FP8 ? kTilePages : kTilePages * C::NB;  // per tile
             const int pg = lane % kTilePages, blk = lane / kTilePages;     // this lane's copy
             const bool hnd = a.layout == PKV_HND;
             const uint64_t policy = l2_policy_evict_first();
-            const Cuts cuts(total, gridDim.x);
-            int n = v, uses0 = 0, uses1 = 0, buf = 1;
-            int4 meta = make_int4(0, 0, 0, 0);     // what the joining kernel is to do with the cut item
+            int n = v;
             bool ok = true, bad = false;
-            Walk walk(from, to);
             for (int i = 0; ok; ++i) {
-                Piece w;
-                int q_wanted = 0;                  // buffers of q (bits) that are not loaded yet
-                if (v == 0) {
-                    w.b = walk.next(a) ? walk.b : -1;
-                    if (w.b >= 0) {
-                        w.kvh = walk.kvh, w.q0 = walk.s.q0, w.L = walk.s.L, w.ctx = walk.s.ctx;
-                        w.tok0 = walk.rg * 2 * a.tile_toks;
-                        w.toks = min(walk.s.N - w.tok0, 2 * a.tile_toks);
-                        w.t0 = walk.t0, w.t1 = walk.t1;
-                        w.whole = w.t0 == 0 && w.t1 == walk.nt;
-                        w.two = w.toks > a.tile_toks;
-                        if (!w.two) buf ^= 1;
-                        w.buf = buf;
-                        w.uses0 = uses0, w.uses1 = uses1;
-                        q_wanted = w.two ? 3 : 1 << buf;
-                        if (w.t0 == 0 && w.t1 < walk.nt) {
-                            // cuts up to kSnap tiles before the item's end are inside it
-                            const int c1 = cuts.at_or_before(cuts.cut(static_cast<int>(blockIdx.x) + 1) - w.t1 + walk.nt - kSnap);
-                            meta = make_int4(w.q0 + w.tok0, w.toks, c1 - static_cast<int>(blockIdx.x) + 1, w.kvh);
-                        }
-                    }
-                    if (i >= kPieces && !warp_wait(bar(bPieceFree + i % kPieces), (i / kPieces - 1) & 1)) break;
-                    if (lane == 0) {
-                        pieces[i % kPieces] = w;
-                        mbar_arrive(piece_bar(i));
-                    }
-                    __syncwarp();
-                } else {
-                    if (!warp_wait(piece_bar(i), piece_par(i))) break;
-                    w = pieces[i % kPieces];
-                    __syncwarp();
-                    if (lane == 0 && w.b >= 0) mbar_arrive(bar(bPieceFree + i % kPieces));
-                }
+                if (!warp_wait(piece_bar(i), piece_par(i))) break;
+                const Piece w = pieces[i % kPieces];
+                __syncwarp();
                 if (w.b < 0) break;
-                // q of this piece, into every wanted buffer that is free: tile_toks
-                // tokens x G heads are consecutive operand rows
-                auto load_q = [&]() {
-#pragma unroll
-                    for (int bf = 0; bf < 2; ++bf) {
-                        int& uses = bf ? uses1 : uses0;
-                        if (!(q_wanted >> bf & 1)) continue;
-                        if (uses > 0 && !__all_sync(0xffffffffu, mbar_test_wait(bar(bQFree + bf), (uses - 1) & 1))) continue;
-                        const uint32_t fb = bar((FP8 ? bQRaw : bQ) + bf);
-                        if (lane == 0) mbar_arrive_expect_tx(fb, a.tile_toks * a.G * D * 2);
-                        __syncwarp();
-                        if (lane < C::NB)
-                            tma_load_3d(s0 + C::OFF_Q + bf * C::TILE + lane * C::BLOCK, &tmq, fb, 64 * lane, w.kvh * a.G,
-                                        w.q0 + w.tok0 + (w.two ? bf * a.tile_toks : 0), policy);
-                        __syncwarp();
-                        ++uses;
-                        q_wanted &= ~(1 << bf);
-                    }
-                };
-                if (q_wanted) load_q();
+                if (lane == 0) mbar_arrive(bar(bPieceFree + i % kPieces));
                 const int npages = (w.L + kPageSize - 1) / kPageSize;
                 auto page_at = [&](int t) -> int {
                     const int p = t * kTilePages + pg;
@@ -544,16 +491,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         id = static_cast<int>(num_pages);  // out of range: the copy fills zeros
                     }
                     const int st = C::copy_stage(n), rd = C::copy_round(n);
-                    if (rd > 0) {
-                        const uint32_t fr = bar(FREE + st), par = (rd - 1) & 1;
-                        // the ring may be waiting for this very piece's q
-                        while (ok && q_wanted && !__all_sync(0xffffffffu, mbar_try_wait_suspend(fr, par, 1000u))) {
-                            load_q();
-                            ok = !__any_sync(0xffffffffu, *abort_flag != 0);
-                        }
-                        ok = ok && warp_wait(fr, par);
-                        if (!ok) break;
-                    }
+                    if (rd > 0) ok = warp_wait(bar(FREE + st), (rd - 1) & 1);
+                    if (!ok) break;
                     const uint32_t fb = bar(FULL + st);
                     if (lane == 0) mbar_arrive_expect_tx(fb, FP8 ? C::RAW : C::TILE);
                     __syncwarp();
@@ -565,26 +504,64 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     }
                     __syncwarp();
                 }
-                // q's last buffer: free once the piece before has its output written
-                if (ok && (q_wanted & 1) && uses0 > 0) ok = warp_wait(bar(bQFree), (uses0 - 1) & 1);
-                if (ok && (q_wanted & 2) && uses1 > 0) ok = warp_wait(bar(bQFree + 1), (uses1 - 1) & 1);
-                if (ok && q_wanted) load_q();
             }
             if (bad && blk == 0 && v == 0) flag_error(a.err, PKV_FLAG_PAGE_RANGE);
             if (lane == 0) {
-                if (v == 0) reinterpret_cast<int4*>(a.workspace)[blockIdx.x] = meta;
                 // Copies under way land before the CTA may exit: the last ones of every
                 // stage that neither copy warp has taken again.
                 constexpr int BACK = FP8 ? C::RST : 2 * (C::SK > C::SV ? C::SK : C::SV);
                 for (int i = n - 2; i >= 0 && i > n - 1 - v - BACK; i -= 2)
                     if (FP8 || i + 2 * (v ? C::SV : C::SK) >= n)
                         (void)mbar_wait_bounded(bar(FULL + C::copy_stage(i)), C::copy_round(i) & 1, kWaitLimitNs);
-                if (uses0) (void)mbar_wait_bounded(bar(FP8 ? bQRaw : bQ), (uses0 - 1) & 1, kWaitLimitNs);
-                if (uses1) (void)mbar_wait_bounded(bar((FP8 ? bQRaw : bQ) + 1), (uses1 - 1) & 1, kWaitLimitNs);
             }
-        } else if (lane == 0) {
-            // ======================= tensor-core issue, one thread per group ==========
-            const int g = warp >> 1;
+        } else if (warp == 3 && lane == 0) {
+            // ======================= the CTA's pieces, and q ==========================
+            int4 meta = make_int4(0, 0, 0, 0);     // what the joining kernel is to do with the cut item
+            const Cuts cuts(total, gridDim.x);
+            const uint64_t policy = l2_policy_evict_first();
+            int uses0 = 0, uses1 = 0, buf = 1;
+            bool ok = true;
+            Walk walk(from, to);
+            for (int i = 0; ok; ++i) {
+                Piece w;
+                w.b = walk.next(a) ? walk.b : -1;
+                if (w.b >= 0) {
+                    w.kvh = walk.kvh, w.q0 = walk.s.q0, w.L = walk.s.L, w.ctx = walk.s.ctx;
+                    w.tok0 = walk.rg * 2 * a.tile_toks;
+                    w.toks = min(walk.s.N - w.tok0, 2 * a.tile_toks);
+                    w.t0 = walk.t0, w.t1 = walk.t1;
+                    w.whole = w.t0 == 0 && w.t1 == walk.nt;
+                    w.two = w.toks > a.tile_toks;
+                    if (!w.two) buf ^= 1;
+                    w.buf = buf;
+                    w.uses0 = uses0, w.uses1 = uses1;
+                    if (w.t0 == 0 && w.t1 < walk.nt) {
+                        // cuts up to kSnap tiles before the item's end are inside it
+                        const int c1 = cuts.at_or_before(cuts.cut(static_cast<int>(blockIdx.x) + 1) - w.t1 + walk.nt - kSnap);
+                        meta = make_int4(w.q0 + w.tok0, w.toks, c1 - static_cast<int>(blockIdx.x) + 1, w.kvh);
+                    }
+                }
+                if (i >= kPieces && !lane_wait(bar(bPieceFree + i % kPieces), (i / kPieces - 1) & 1)) break;
+                pieces[i % kPieces] = w;
+                mbar_arrive(piece_bar(i));
+                if (w.b < 0) break;
+                // q, once the buffer is free: tile_toks tokens x G heads are consecutive operand rows
+                w.buffers([&](int bf, int uses) {
+                    if (ok && uses > 0) ok = lane_wait(bar(bQFree + bf), (uses - 1) & 1);
+                    if (!ok) return;
+                    const uint32_t fb = bar((FP8 ? bQRaw : bQ) + bf);
+                    mbar_arrive_expect_tx(fb, a.tile_toks * a.G * D * 2);
+                    for (int c = 0; c < C::NB; ++c)
+                        tma_load_3d(s0 + C::OFF_Q + bf * C::TILE + c * C::BLOCK, &tmq, fb, 64 * c, w.kvh * a.G,
+                                    w.q0 + w.tok0 + (w.two ? bf * a.tile_toks : 0), policy);
+                    ++(bf ? uses1 : uses0);
+                });
+            }
+            reinterpret_cast<int4*>(a.workspace)[blockIdx.x] = meta;
+            if (uses0) (void)mbar_wait_bounded(bar(FP8 ? bQRaw : bQ), (uses0 - 1) & 1, kWaitLimitNs);
+            if (uses1) (void)mbar_wait_bounded(bar((FP8 ? bQRaw : bQ) + 1), (uses1 - 1) & 1, kWaitLimitNs);
+        } else if (warp == 1 && lane == 0) {
+            // ======================= tensor-core issue (one thread) ===================
             constexpr int FMT = FP8 ? 0 : 1;  // f16 or bf16 operands
             // the sign of softmax_scale goes into q (bit 13 negates A)
             const uint32_t idesc_qk = umma_idesc(128, kTile, FMT, FMT, false, false) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
@@ -592,119 +569,74 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             // 128-byte-swizzled operands, 1024 bytes between groups of 8 rows
             constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
             auto desc_lo = [](uint32_t addr, uint32_t lead) { return ((addr >> 4) & 0x3FFFu) | (lead >> 4) << 16; };
-            const uint32_t tS = tmem + 256 * g;
-            int tile0 = 0;                    // tiles before this piece
-            int n_qk = 0, n_pv = 0, n_o = 0;  // Q . K^T, P . V and last P . V of an item issued
-            int turns = 0;                    // of items with two row tiles
+            int tile0 = 0;                             // tiles before this piece
+            int p0 = 0, p1 = 0, n_qk = 0, n_o = 0;     // P taken of either group, scores and items issued
             bool ok = true;
             for (int i = 0; ok; ++i) {
                 ok = lane_wait(piece_bar(i), piece_par(i));
                 const Piece w = pieces[i % kPieces];
                 if (!ok || w.b < 0) break;
-                const int nt = w.t1 - w.t0, step = w.two ? 1 : 2;
-                if (nt > (w.two ? 0 : g)) {            // (a group without a tile here only sees them land)
-                    // the item before has no more use for S
-                    if (i > 0) ok = lane_wait(bar(bX + (i - 1) % kPieces), ((i - 1) / kPieces) & 1);
-                    w.buffers([&](int bf, int uses) { ok = ok && lane_wait(bar(bQ + bf), uses & 1); });
-                }
-                const uint32_t q = desc_lo(s0 + C::OFF_Q + (w.two ? g : w.buf) * C::TILE, 16);
-                const int first = w.two ? 0 : g;
-                // Both threads see every slot land, in order, and both release it
-                // (the other group's tiles by a plain arrival): a parity wait is
-                // then never two phases off.
+                const int nt = w.t1 - w.t0, nj = w.two ? 2 * nt : nt;
+                // the item before has no more use for S
+                if (i > 0) ok = lane_wait(bar(bX + (i - 1) % kPieces), ((i - 1) / kPieces) & 1);
+                w.buffers([&](int bf, int uses) { ok = ok && lane_wait(bar(bQ + bf), uses & 1); });
                 auto landed = [&](int n) -> bool { return lane_wait(bar(bFull + stage(n)), phase(n)); };
-                auto see_tile = [&](int t) -> bool {
-                    const int n = 2 * (tile0 + t);
-                    if (!landed(n)) return false;
-                    mbar_arrive(bar(bFree + stage(n)));
-                    if (!landed(n + 1)) return false;
-                    mbar_arrive(bar(bFree + stage(n + 1)));
-                    return true;
-                };
-                if (first > 0) ok = ok && see_tile(0);
-                // P . V of a tile, then the scores of this group's next one, which take S
-                // from under P: the tensor cores execute in order of issue
-                for (int t = first - step; ok && t < nt; t += step) {
-                    const int n = 2 * (tile0 + t) + 1, n2 = 2 * (tile0 + t + step);  // V here, the next K
-                    const bool more = t + step < nt;
-                    if (t >= 0) ok = landed(n);
-                    const uint32_t vt = desc_lo(s0 + C::OFF_T + stage(n) * C::TILE, C::BLOCK);
-                    const uint32_t kt = desc_lo(s0 + C::OFF_T + stage(n2) * C::TILE, 16);
-                    auto pv = [&](int h) {             // half h of the tile's positions
+                // Job j is tile j / 2 for group j % 2 (two row tiles), or tile j for group
+                // j % 2. P . V of a job, then the scores of that group's next one, which
+                // take S from under P: the tensor cores execute in order of issue.
+                for (int j = -2; ok && j < nj; ++j) {
+                    const int g = j & 1, t = w.two ? j >> 1 : j, tn = w.two ? t + 1 : t + 2;
+                    const int n = 2 * (tile0 + t) + 1, n2 = 2 * (tile0 + tn);  // V here, the next K
+                    const uint32_t tS = tmem + 256 * g;
+                    const bool more = j + 2 < nj;
+                    bool here = false;
+                    if (j >= 0) {
+                        // (a wait costs 100 cycles when the phase is over, and 200 more when it
+                        // ends meanwhile: what has landed is looked up before P is waited for)
+                        ok = landed(n);
+                        here = ok && more && mbar_test_wait(bar(bFull + stage(n2)), phase(n2));
+                        ok = ok && lane_wait(bar(bP + g), (g ? p1 : p0) & 1);
+                        if (!ok) break;
+                        ++(g ? p1 : p0);
                         tc_fence_after();
-                        const uint32_t more_o = t > first || *reinterpret_cast<volatile uint32_t*>(go_on + g) != 0u;
+                        const uint32_t vt = desc_lo(s0 + C::OFF_T + stage(n) * C::TILE, C::BLOCK);
+                        const uint32_t more_o = j > 1 || *reinterpret_cast<volatile uint32_t*>(go_on + g) != 0u;  // O goes on, or starts
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            umma_ts(tS + C::O_COL, tS + C::P_COL + 32 * h + 8 * k, vt + (4 * h + k) * (2048 >> 4), kDescHi, kIdescPv,
-                                    h + k > 0 ? 1u : more_o);
-                    };
-                    auto qk = [&]() {
+                        for (int k = 0; k < kTile / 16; ++k)
+                            umma_ts(tS + C::O_COL, tS + C::P_COL + 8 * k, vt + k * (2048 >> 4), kDescHi, kIdescPv, k > 0 ? 1u : more_o);
+                        if (!w.two) {
+                            // (one row tile is bound by memory: V's stage is wanted back at once)
+                            mbar_arrive(bar(bFree + stage(n)));
+                            umma_commit(bar(bFree + stage(n)));
+                        }
+                    }
+                    if (more) {
+                        ok = here || landed(n2);
+                        if (!ok) break;
                         tc_fence_after();
+                        const uint32_t q = desc_lo(s0 + C::OFF_Q + (w.two ? g : w.buf) * C::TILE, 16);
+                        const uint32_t kt = desc_lo(s0 + C::OFF_T + stage(n2) * C::TILE, 16);
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k) {
                             const uint32_t at = ((k >> 2) * C::BLOCK + (k & 3) * 32) >> 4;
                             if (k == 0) umma_ss<true>(tS, q, kt, kDescHi, idesc_qk);
                             else umma_ss<false>(tS, q + at, kt + at, kDescHi, idesc_qk);
                         }
-                    };
-                    // (a wait costs 100 cycles when the phase is over, and 200 more when it
-                    // ends meanwhile: what has landed is looked up before P is waited for)
-                    bool here = false;
-                    if (t >= 0) {
-                        here = more && w.two == 0 && mbar_test_wait(bar(bFull + stage(n2)), phase(n2));
-                        if (more && w.two) ok = ok && landed(n2);
-                        ok = ok && lane_wait(bar(bP + g), n_pv & 1);
-                    } else if (w.two) {
-                        ok = ok && landed(n2);
-                    }
-                    if (!ok) break;
-                    if (w.two) {
-                        // Both groups are at the same tile: they take turns at the tensor
-                        // cores, so that one computes weights while the other's products
-                        // run (interleaved, both would finish, and wait, at the same time).
-                        ok = lane_wait(bar(bTurn + g), (turns - 1 + g) & 1);
-                        if (!ok) break;
-                        ++turns;
-                        if (t >= 0) {
-                            pv(0);
-                            pv(1);
-                        }
-                        if (more) qk();
-                        mbar_arrive(bar(bTurn + 1 - g));
-                    } else {
-                        if (t >= 0) {
-                            pv(0);
-                            pv(1);
-                            // (one row tile is bound by memory: V's stage is wanted back at once)
-                            umma_commit(bar(bFree + stage(n)));
-                            if (t + 1 < nt) ok = see_tile(t + 1);
-                        }
-                        if (more) {
-                            ok = ok && (here || landed(n2));
-                            if (!ok) break;
-                            qk();
-                        }
-                    }
-                    if (t >= 0) ++n_pv;
-                    if (more) {
                         umma_commit(bar(bS + g));
                         ++n_qk;
-                    } else if (t >= 0) {
+                    } else if (j >= 0) {
                         umma_commit(bar(bO + g));      // the item's O
                         ++n_o;
                     }
                 }
-                if (!ok) break;
                 mbar_arrive(bar(bPieceFree + i % kPieces));
                 tile0 += nt;
             }
-            // Every operation issued is done before the tensor memory is freed:
-            // the softmax groups wait for their last O, and give-ups for both here.
-            if (!ok) {
-                if (n_qk) (void)mbar_wait_bounded(bar(bS + g), (n_qk - 1) & 1, kWaitLimitNs);
-                if (n_o) (void)mbar_wait_bounded(bar(bO + g), (n_o - 1) & 1, kWaitLimitNs);
-                umma_commit(bar(bO + g));
-                (void)mbar_wait_bounded(bar(bO + g), n_o & 1, kWaitLimitNs);
+            // Every operation issued is done before the tensor memory is freed: the
+            // softmax groups wait for their last O, and a give-up for all of them here.
+            if (!ok && n_qk + n_o > 0) {
+                umma_commit(bar(bEnd));
+                (void)mbar_wait_bounded(bar(bEnd), 0, kWaitLimitNs);
             }
         }
         __syncwarp();
@@ -786,6 +718,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 tc_fence_after();
                 if (speaker && ok) {
                     mbar_arrive(bar(bFree + stage(n - 1)));                            // K
+                    if (!two) mbar_arrive(bar(bFree + stage(n - 1)));
                     if (two && job > job0) mbar_arrive(bar(bFree + stage(n - 2)));     // the V before
                     if (job == job0) *reinterpret_cast<volatile uint32_t*>(go_on + grp) = 0u;
                 }
