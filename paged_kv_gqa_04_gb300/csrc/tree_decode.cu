@@ -1080,54 +1080,118 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
 }
 
 // ---- joining the pieces of cut items ------------------------------------------------
-// CTA (c, y): 8 rows of the item whose first piece CTA c had. A warp has 8 rows
-// x 4 quads of columns (128-byte runs of the partial sums), D / 16 warps a row.
-constexpr int kJoinRows = 8;
+// The work is blocks of rows of the cut items (entry c of the CTAs' notes: the
+// item whose first piece CTA c had), numbered through and dealt to a grid that is
+// resident at once. A warp reads 8 rows x 4 quads of columns at a time (128-byte
+// runs of the partial sums), eight reads of 16 bytes per thread on their way: of
+// four row blocks of two pieces (items cut once), or of eight pieces.
+template <int D, int R, int U>
+__device__ __forceinline__ void join_rows(const TreeArgs& a, int ctas, int c, const int4 meta, int r0) {
+    const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) * 4 + (lane >> 3);
+    const int n = meta.z;                                // pieces: slot 1 of CTA c, slot 0 of the next ones
+    int row[R];                                          // places in the partial sums; rows past the item: the last one
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        const int r = min(r0 + 8 * k + (lane & 7), meta.y * a.G - 1);  // row: token r / G, head r % G
+        row[k] = r < a.tile_toks * a.G ? r : 128 + r - a.tile_toks * a.G;
+    }
+    float M[R], sum[R];
+    float4 o[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        M[k] = -INFINITY;
+        sum[k] = 0.f;
+        o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int i0 = 0; i0 < n; i0 += U) {                  // online over the pieces
+        float2 ml[U][R];
+        float4 x[U][R];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u, slot = 2 * (c + i) + (i == 0 ? 1 : 0);
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                ml[u][k] = make_float2(-INFINITY, 0.f);
+                x[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < n) {
+                    ml[u][k] = *reinterpret_cast<const float2*>(part_ml(a.workspace, slot, row[k]));
+                    x[u][k] = *reinterpret_cast<const float4*>(part_o<D>(a.workspace, ctas, slot, row[k]) + quad * (kRows * 4));
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            float m = M[k];
+#pragma unroll
+            for (int u = 0; u < U; ++u) m = fmaxf(m, ml[u][k].x);
+            const float al = M[k] == -INFINITY ? 0.f : fast_exp2(M[k] - m);
+            M[k] = m;
+            sum[k] *= al;
+            o[k].x *= al, o[k].y *= al, o[k].z *= al, o[k].w *= al;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (i0 + u >= n) break;
+                const float f = ml[u][k].x == -INFINITY ? 0.f : fast_exp2(ml[u][k].x - m);
+                sum[k] += f * ml[u][k].y;
+                o[k].x += f * x[u][k].x, o[k].y += f * x[u][k].y, o[k].z += f * x[u][k].z, o[k].w += f * x[u][k].w;
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        const int r = r0 + 8 * k + (lane & 7), tok = r / a.G, g = r - tok * a.G;
+        if (tok >= meta.y) continue;
+        const bool none = sum[k] == 0.f;
+        const float inv = none ? 0.f : 1.f / sum[k];
+        const int h = meta.w * a.G + g;
+        uint2* out = reinterpret_cast<uint2*>(a.out + (meta.x + tok) * a.o_s0 + h * a.o_s1 + quad * 4);
+        *out = none ? make_uint2(0u, 0u) : make_uint2(pack_bf16(o[k].x * inv, o[k].y * inv), pack_bf16(o[k].z * inv, o[k].w * inv));
+        if (quad == 0 && a.lse)
+            a.lse[(meta.x + tok) * a.l_s0 + h * a.l_s1] =
+                none ? -INFINITY : (M[k] + __log2f(sum[k])) * 0.69314718055994530942f;
+    }
+}
 
 template <int D>
 __global__ void __launch_bounds__(2 * D) tree_join_kernel(const TreeArgs a, int ctas) {
+    extern __shared__ int first[];                       // [ctas + 1]: the first block of entry c's item
+    const int4* notes = reinterpret_cast<const int4*>(a.workspace);  // first token, tokens, pieces, kv head
+    auto rows_per_block = [](int4 m) { return m.z <= 2 ? 32 : 8; };
     grid_dep_wait();
-    const int c = blockIdx.x, lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) * 4 + (lane >> 3);
-    const int r = blockIdx.y * kJoinRows + (lane & 7);   // row of the item: token r / G, head r % G
-    const int4 meta = reinterpret_cast<const int4*>(a.workspace)[c];  // first token, tokens, pieces, kv head
-    const int tok = r / a.G, g = r - tok * a.G;
-    if (tok >= meta.y) return;
-    const int row = tok < a.tile_toks ? r : 128 + r - a.tile_toks * a.G;  // its place in the partial sums
-    const int n = meta.z;                                // pieces: slot 1 of CTA c, slot 0 of the next ones
-    auto slot = [&](int i) { return 2 * (c + i) + (i == 0 ? 1 : 0); };
-    float M = -INFINITY, sum = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < n; i0 += 8) {                  // online over the pieces, eight on their way at a time
-        float2 ml[8];
-        float4 x[8];
-        float m = M;
+    for (int c = threadIdx.x; c < ctas; c += 2 * D) {
+        const int4 m = notes[c];
+        first[c + 1] = (m.y * a.G + rows_per_block(m) - 1) / rows_per_block(m);
+    }
+    if (threadIdx.x == 0) first[0] = 0;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        int base = 0;
+        for (int c0 = 0; c0 < ctas; c0 += 32) {
+            const int c = c0 + threadIdx.x;
+            int v = c < ctas ? first[c + 1] : 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int i = min(i0 + k, n - 1);
-            ml[k] = *reinterpret_cast<const float2*>(part_ml(a.workspace, slot(i), row));
-            x[k] = *reinterpret_cast<const float4*>(part_o<D>(a.workspace, ctas, slot(i), row) +
-                                                    static_cast<int64_t>(quad) * kRows * 4);
-            m = fmaxf(m, ml[k].x);
-        }
-        const float al = M == -INFINITY ? 0.f : fast_exp2(M - m);
-        M = m;
-        sum *= al;
-        o.x *= al, o.y *= al, o.z *= al, o.w *= al;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            if (i0 + k >= n) break;
-            const float f = ml[k].x == -INFINITY ? 0.f : fast_exp2(ml[k].x - M);
-            sum += f * ml[k].y;
-            o.x += f * x[k].x, o.y += f * x[k].y, o.z += f * x[k].z, o.w += f * x[k].w;
+            for (int d = 1; d < 32; d <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, v, d);
+                if (static_cast<int>(threadIdx.x) >= d) v += y;
+            }
+            if (c < ctas) first[c + 1] = base + v;
+            base += __shfl_sync(0xffffffffu, v, 31);
         }
     }
-    const bool none = sum == 0.f;
-    const float inv = none ? 0.f : 1.f / sum;
-    const int h = meta.w * a.G + g;
-    uint2* out = reinterpret_cast<uint2*>(a.out + (meta.x + tok) * a.o_s0 + h * a.o_s1 + quad * 4);
-    *out = none ? make_uint2(0u, 0u) : make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-    if (quad == 0 && a.lse)
-        a.lse[(meta.x + tok) * a.l_s0 + h * a.l_s1] = none ? -INFINITY : (M + __log2f(sum)) * 0.69314718055994530942f;
+    __syncthreads();
+    const int blocks = first[ctas];
+    for (int b = blockIdx.x; b < blocks; b += gridDim.x) {
+        int lo = 0, hi = ctas;                           // the entry with first[c] <= b < first[c + 1]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (first[mid] <= b) lo = mid;
+            else hi = mid;
+        }
+        const int4 m = notes[lo];
+        const int r0 = (b - first[lo]) * rows_per_block(m);
+        if (m.z <= 2) join_rows<D, 4, 2>(a, ctas, lo, m, r0);
+        else join_rows<D, 1, 8>(a, ctas, lo, m, r0);
+    }
 }
 
 template <int D, bool FP8>
@@ -1140,8 +1204,9 @@ cudaError_t launch_t(const TreeArgs& a, const CUtensorMap& tq, const CUtensorMap
     if (e != cudaSuccess) return e;
     e = launch_dependent(tree_kernel<D, FP8>, dim3(sms), dim3(C::THREADS), C::SMEM, s, tq, tk, tv, a);
     if (e != cudaSuccess) return e;
-    const int rows = static_cast<int>(std::min<int64_t>(kRows, static_cast<int64_t>(a.T) * a.G));
-    return launch_dependent(tree_join_kernel<D>, dim3(sms, (rows + kJoinRows - 1) / kJoinRows), dim3(2 * D), 0, s, a, sms);
+    // Every SM can hold four of these (D = 128) at once; no more than there are blocks of 8 rows.
+    const int grid = static_cast<int>(std::min<int64_t>(4 * sms, (static_cast<int64_t>(a.T) * a.Hq + 7) / 8));
+    return launch_dependent(tree_join_kernel<D>, dim3(grid), dim3(2 * D), (sms + 1) * sizeof(int), s, a, sms);
 }
 
 }  // namespace
