@@ -670,12 +670,14 @@ pkv_status pkv_selftest_bounded_wait(int64_t limit_ns, int32_t* err_flag, uint64
  *              pkv_tree_decode_workspace() bytes; its contents need no
  *              preparation. Calls that may run at the same time need one each.
  * Supported: D in {64, 128}; 1 <= Hq/Hkv <= 16; any N_b; B, Hkv <= 65535;
- * Hkv (B + T Hq / (128 Hkv)) max_pages / 8 below 2^31 / 1.1 (tiles of work).
+ * Hkv (B + 1 + T Hq / (128 Hkv)) (max_pages / 8 + 8) <= 2e9 (tiles of work).
  * Errors: a block-table entry outside [0, num_pages) sets PKV_FLAG_PAGE_RANGE
  * and that page is left out; seq_lens[b] outside [0, 16*max_pages] sets
  * PKV_FLAG_SEQ_LEN_RANGE and is clamped; q_start not ascending within [0, T]
  * (clamped), N_b > L (the positions below 0 do not exist) and N_b > 32 W
  * (drafted tokens past the mask are seen by no row) set PKV_FLAG_DRAFT_RANGE.
+ * Where ranges that do not ascend come to 2^31 tiles of work and more, nothing
+ * is computed.
  * Outputs must not alias inputs.
  */
 pkv_status pkv_paged_tree_decode(const pkv_tensor* q, const pkv_tensor* k_cache, const pkv_tensor* v_cache,
@@ -717,8 +719,8 @@ int64_t pkv_tree_decode_workspace(int64_t T, int32_t Hq, int32_t D, int32_t sm_c
  * seq_lens_out [B] int32, not overlapping seq_lens.
  * Errors: num_accepted outside [0, min(A, N_b)], indices that do not ascend
  * strictly within [0, N_b), and N_b outside [0, L] set PKV_FLAG_DRAFT_RANGE,
- * seq_lens outside [0, P*max_pages] sets PKV_FLAG_SEQ_LEN_RANGE: that
- * sequence is left as it is (seq_lens_out = seq_lens). A move from or to a
+ * seq_lens outside [0, P*max_pages] sets PKV_FLAG_SEQ_LEN_RANGE (without
+ * caches P counts as 65536): that sequence is left as it is (seq_lens_out = seq_lens). A move from or to a
  * page outside [0, num_pages) is left out and sets PKV_FLAG_PAGE_RANGE. Two
  * sequences must not share the pages of their drafted tokens.
  */

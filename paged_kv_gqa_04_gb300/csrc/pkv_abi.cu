@@ -1289,7 +1289,7 @@ static pkv_status pool_part(const pkv_tensor& t, int32_t layout, bool pages, int
         nh = t.shape[3 - tok];
         sh = t.stride[3 - tok] * e;
     }
-    if (row > (1 << 30) || nh > (1 << 30) || row * nh > (1 << 30) || row * nh * nt > (1 << 30))
+    if (row > (1 << 30) || nh > (1 << 30) || row * nh > (1 << 30) || row * nh * nt >= (1 << 30))
         return PKV_ERR_UNSUPPORTED;
     if (nh == 1 || sh == row) {  // a token's heads are one row
         row *= nh;
@@ -1363,7 +1363,7 @@ pkv_status pkv_accept_drafts(const pkv_tensor* caches, int32_t n_caches, int32_t
     const pkv_tensor& ac = arg(accepted_p);
     const pkv_tensor& na = arg(num_accepted_p);
     const pkv_tensor& so = arg(seq_lens_out_p);
-    int64_t num_pages = 1, P = kPageSize, B, max_pages;
+    int64_t num_pages = 1, P = 65536, B, max_pages;  // (without caches: the longest pages there are)
     pkv_status st = check_pool(caches, n_caches, layout, false, &num_pages, &P);
     if (st != PKV_OK) return st;
     if ((st = check_tables(bt, &B, &max_pages)) != PKV_OK) return st;
@@ -1543,7 +1543,7 @@ pkv_status pkv_paged_tree_decode(const pkv_tensor* q_p, const pkv_tensor* k_cach
     if (!row16(q, 2) || !row16(out, 2)) return PKV_ERR_UNSUPPORTED;
     if (mask.ptr && (mask.shape[1] > 64 || (mask.shape[1] > 1 && mask.stride[1] != 1))) return PKV_ERR_UNSUPPORTED;
     // tiles of work, as the kernel counts them, in 32 bits
-    if (static_cast<double>(Hkv) * static_cast<double>(B + T * G / 128 + 1) * (max_pages / 8 + 2) > 2.0e9)
+    if (static_cast<double>(Hkv) * static_cast<double>(B + T * G / 128 + 1) * (max_pages / 8 + 8) > 2.0e9)
         return PKV_ERR_UNSUPPORTED;
     int sms = 0;
     if (pkv::device_sm_count(&sms) != cudaSuccess) return PKV_ERR_CUDA;

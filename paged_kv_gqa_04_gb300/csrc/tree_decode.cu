@@ -9,9 +9,11 @@
 // sum need no exchange. One pass over K and V serves two row tiles.
 //
 // Work. An item is (sequence, kv head, pair of row tiles); a unit is one tile
-// of 128 positions of one item, and an item costs two units more. All units of the batch, in order, are cut into
-// equal stretches, one per CTA (one CTA per SM): every CTA streams the same
-// number of tiles whatever the lengths are, with no plan from the host. Each
+// of 128 positions of one item, and an item counts five units more for its
+// start and output (measured: counting two, 64 contexts of 1 to 8192 with 32
+// query heads took 103 us and not 88). All units of the batch, in order, are cut into
+// equal stretches, one per CTA (one CTA per SM): every CTA does the same
+// amount of work whatever the lengths are, with no plan from the host. Each
 // CTA finds its stretch from prefix sums over the batch. An item that is cut
 // leaves partial sums in the workspace (at most two per CTA: the end of one
 // item, the start of another), which a second kernel joins.
@@ -66,7 +68,7 @@ constexpr int kTile = 128;    // positions per tile
 constexpr int kRows = 256;    // rows (lanes of two row tiles) per item
 constexpr int kTilePages = kTile / kPageSize;
 constexpr int kSnap = 2;      // no piece of a cut item is shorter than this many tiles
-constexpr int kItemUnits = 2; // what an item costs beyond its tiles (start, output), in tiles
+constexpr int kItemUnits = 5; // what an item costs beyond its tiles (start, output, joining), in tiles
 constexpr int kPieces = 4;    // ring of pieces
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr float kRescaleLog2 = 8.f;
@@ -142,12 +144,19 @@ __device__ __forceinline__ int kv_end(const TreeArgs& a, const Seq& s, int rg) {
 __device__ __forceinline__ int tiles_of(const TreeArgs& a, const Seq& s, int rg) {
     return max((kv_end(a, s, rg) + kTile - 1) / kTile, 1);
 }
-// Units of one kv head (the host has checked that the batch's stay below 2^31).
+// Units of one kv head.
 __device__ __forceinline__ int units_per_head(const TreeArgs& a, const Seq& s) {
     if (s.RG <= 1 || a.mask != nullptr) return s.RG ? s.RG * (tiles_of(a, s, 0) + kItemUnits) : 0;
     int n = 0;
     for (int rg = 0; rg < s.RG; ++rg) n += tiles_of(a, s, rg) + kItemUnits;
     return n;
+}
+
+// Sums of units. The host has checked that the drafted tokens' come to less than
+// kMaxUnits; those of ranges that overlap may not, and stay there.
+constexpr int kMaxUnits = 0x7FFFFFFF;
+__device__ __forceinline__ int add_units(int x, int y) {
+    return static_cast<int>(min(static_cast<uint32_t>(x) + static_cast<uint32_t>(y), static_cast<uint32_t>(kMaxUnits)));
 }
 
 // CTA c of n starts at unit cut(c); the first total % n stretches are one unit longer.
@@ -396,21 +405,22 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         const int seg = (a.B + C::THREADS - 1) / C::THREADS;
         const int b0 = min(tid * seg, a.B), b1 = min(b0 + seg, a.B);
         int sum = 0, flags = 0;
-        for (int b = b0; b < b1; ++b) sum += a.Hkv * units_per_head(a, seq_of(a, b, flags));
+        for (int b = b0; b < b1; ++b) sum = add_units(sum, a.Hkv * units_per_head(a, seq_of(a, b, flags)));
         if (flags && blockIdx.x == 0) flag_error(a.err, flags);
         int inc = sum;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, inc, d);
-            if (lane >= d) inc += y;
+            if (lane >= d) inc = add_units(inc, y);
         }
         if (lane == 31) warp_units[warp] = inc;
         __syncthreads();
         int base = 0;
         for (int w = 0; w < C::THREADS / 32; ++w) {
             if (w == warp) base = total;
-            total += warp_units[w];
+            total = add_units(total, warp_units[w]);
         }
+        if (total == kMaxUnits) total = 0;             // (ranges that overlap; flagged)
         const Cuts cuts(total, gridDim.x);
         const int c = blockIdx.x;
         int at = base + inc - sum;

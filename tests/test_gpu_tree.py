@@ -158,6 +158,23 @@ def test_row_ranges_are_clamped(start):
     check_tree(s, flags=_abi.FLAG_DRAFT_RANGE if bad else 0)
 
 
+def test_overlapping_ranges_past_the_work_that_is_counted():
+    """32,768 sequences of 2^18 drafted tokens each, in the same rows of q: 3.2e9 tiles of work."""
+    if torch.cuda.get_device_properties(0).total_memory < 40e9:
+        pytest.skip("needs 1.5 GB")
+    B, T = 65535, 1 << 18
+    s = make_tree([300], [9], 16, 1, 64, seed=11)
+    start = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    start[1::2] = T
+    s.update(q=torch.zeros((T, 16, 64), dtype=torch.bfloat16, device="cuda"), q_start=start, lse=None,
+             seq_lens=torch.full((B,), 300, dtype=torch.int32, device="cuda"), bt=s["bt"].repeat(B, 1),
+             mask=torch.zeros((T, 1), dtype=torch.int32, device="cuda"))
+    s["out"] = torch.full_like(s["q"], 7.0)
+    run_tree(s)
+    torch.cuda.synchronize()
+    assert int(s["err"].item()) == _abi.FLAG_DRAFT_RANGE and bool((s["out"] == 7).all())
+
+
 def test_pool_past_32_bit_offsets():
     """Pages whose element and byte offsets pass 2^31 and 2^32."""
     if torch.cuda.get_device_properties(0).total_memory < 40e9:
