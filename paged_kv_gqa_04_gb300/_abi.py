@@ -170,6 +170,8 @@ def _desc(t, dtype: Optional[int] = None):
     if isinstance(t, Bound):
         if dtype is not None:
             raise TypeError("NVFP4 value caches are passed as tensors, not bound")
+        if t.n != 1:
+            raise TypeError("a bound list of tensors where one tensor is expected")
         return t.ptr
     d = PkvTensor()
     if t.dim() > 4:

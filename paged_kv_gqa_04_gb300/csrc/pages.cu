@@ -227,13 +227,13 @@ constexpr int kReturnSpan = 256;
 __global__ void __launch_bounds__(256) return_kernel(const __grid_constant__ TakeArgs a) {
     grid_dep_wait();  // (the table is an index input: no early trigger, but for the take, which waits)
     grid_dep_launch();
-    const int b = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int b = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (b >= a.n) return;
     int have, want, flags;
     resize_row(a, b, have, want, flags);
     flags = 0;  // the take reports them
-    const int j0 = max(want, static_cast<int>(blockIdx.y) * kReturnSpan);
-    const int j1 = min(have, static_cast<int>(blockIdx.y + 1) * kReturnSpan);
+    const int j0 = max(want, static_cast<int>(blockIdx.x) * kReturnSpan);
+    const int j1 = min(have, static_cast<int>(blockIdx.x + 1) * kReturnSpan);
     int page[kReturnSpan / 32], old[kReturnSpan / 32];
 #pragma unroll
     for (int k = 0; k < kReturnSpan / 32; ++k) {
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
     }
     for (int w = 0; w < warp; ++w) at += warp_free[w];
     const uint32_t last = min(wanted, total_free);  // ranks past it go to nobody
-    int group = 0;
+    int group = 0, owner = -1;                      // the row of the last rank seen
     for (int64_t g = p0; g < p1 && at < last; g += 128, ++group) {
         const int64_t p = g + 4 * lane;
         uint32_t m = kept ? masks >> (4 * group) & 15u : p < p1 ? free_mask(a.page_refs, p, p1, vec) : 0u;
@@ -435,18 +435,21 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
         }
         __syncwarp();
         for (uint32_t k0 = 0; k0 < found && at + k0 < last; k0 += 32) {
-            const uint32_t r = at + k0 + lane;
-            // 32 neighbouring ranks mostly have few owners: the first one's (a
-            // search by the warp's lanes alike) and the rows behind it
-            const int i0 = owner_of(need, n, at + k0);
+            const uint32_t end = min(at + found, last);
+            const uint32_t r = min(at + k0 + lane, end - 1);
+            // 32 neighbouring ranks mostly have few owners: that of the rank before
+            // them (at first, a search by the warp's lanes alike) and the rows behind it
+            const int i0 = owner < 0 ? owner_of(need, n, at + k0) : owner;
             const uint32_t ends = i0 + 1 + lane <= n ? need[i0 + 1 + lane] : ~0u;
             int i = 0;
 #pragma unroll
             for (int d = 16; d; d >>= 1)
                 if (__shfl_sync(0xffffffffu, ends, i + d - 1) <= r) i += d;
             i += i0 + (__shfl_sync(0xffffffffu, ends, i) <= r);
-            if (k0 + lane >= found || r >= last) continue;
             if (need[i + 1] <= r) i = owner_of(need, n, r);  // more than 31 rows on (rows without a demand among them)
+            __syncwarp();
+            owner = __shfl_sync(0xffffffffu, i, 31);
+            if (at + k0 + lane >= end) continue;
             const int page = static_cast<int>(list[k0 + lane]);
             if (need[i + 1] > total_free) continue;    // i, and everyone after it, gets nothing
             if constexpr (!FORK) {
@@ -465,13 +468,15 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
     cluster_barrier();  // every CTA has read the counts and lengths
     if (rank != 0) return;
     for (int i = tid; i < n; i += kTakeThreads) {
-        const uint32_t grow = need[i + 1] - need[i];
-        const bool fails = grow > 0 && need[i + 1] > total_free;
-        if (fails) flag_error(a.err, PKV_FLAG_POOL_EMPTY);
         if constexpr (!FORK) {
-            const int back = static_cast<int>(give[i + 1] - give[i]);
-            if (back || (grow && !fails)) a.page_counts[i] = held[i] - back + static_cast<int>(grow);
+            int have, want, f;  // (again: the sums saturate)
+            resize_row(a, i, have, want, f);
+            const bool fails = want > have && need[i + 1] > total_free;
+            if (fails) flag_error(a.err, PKV_FLAG_POOL_EMPTY);
+            else if (want != have) a.page_counts[i] = want;
         } else {
+            const bool fails = tail[i] >= 0 && need[i + 1] > total_free;
+            if (fails) flag_error(a.err, PKV_FLAG_POOL_EMPTY);
             if (held[i] >= 0) {
                 const int c = a.forks[2 * i + 1], pages = held[i] / a.page_size + (tail[i] >= 0);
                 a.page_counts[c] = fails ? 0 : pages;
@@ -618,7 +623,7 @@ cudaError_t launch_resize(const TakeArgs& a0, cudaStream_t s) {
     // own (resize_pool's shape: 36 us a call in one kernel, RETURNS in two).
     a.returned = static_cast<int64_t>(a.n) * a.max_pages >= 65536;
     if (a.returned) {
-        const cudaError_t e = launch_dependent(return_kernel, dim3((a.n + 7) / 8, (a.max_pages + kReturnSpan - 1) / kReturnSpan),
+        const cudaError_t e = launch_dependent(return_kernel, dim3((a.max_pages + kReturnSpan - 1) / kReturnSpan, (a.n + 7) / 8),
                                                dim3(256), 0, s, a);
         if (e != cudaSuccess) return e;
     }

@@ -132,6 +132,14 @@ def test_accept_without_caches_gives_lengths():
     assert out.tolist() == [18, 25] and int(err.item()) == 0
 
 
+def test_accept_without_caches_takes_any_page_size():
+    """No cache says how long pages are: a length that 16-token pages would not hold is no error."""
+    err, out = _i32([0]), _i32([0])
+    pkv.accept_drafts([], _i32([[0, 1]]), _i32([100]), _i32([0, 4]), _i32([[1]]), _i32([1]), out, err_flag=err)
+    torch.cuda.synchronize()
+    assert out.tolist() == [97] and int(err.item()) == 0
+
+
 # ---- resize --------------------------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("B,pages,P,width", [(1, 1, 16, 1), (3, 40, 16, 12), (200, 3000, 16, 40), (7, 16385, 64, 2000),
@@ -183,6 +191,37 @@ def test_resize_of_nothing_and_of_an_empty_pool():
     pkv.resize_sequences(bt, c, _i32([5]), e, err_flag=err)
     torch.cuda.synchronize()
     assert int(err.item()) == _abi.FLAG_POOL_EMPTY and c.tolist() == [0] and bt.tolist() == [[-1, -1]]
+
+
+def test_resize_of_the_widest_tables():
+    """Rows of 2^26 entries (as many as there may be); one gives pages back, one cannot have that many."""
+    width, err = 1 << 26, _i32([0])
+    bt = torch.full((3, width), -1, dtype=torch.int32, device="cuda")
+    bt[0, :20] = torch.arange(20, dtype=torch.int32)
+    bt[2, 0] = 30
+    counts, refs = _i32([20, 0, 1]), _i32([1] * 20 + [0] * 10 + [1])
+    pkv.resize_sequences(bt, counts, _i32([3, width, -1]), refs, 1, err_flag=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == _abi.FLAG_POOL_EMPTY and counts.tolist() == [3, 0, 1]
+    assert refs.tolist() == [1] * 3 + [0] * 27 + [1]
+    assert bt[0, :5].tolist() == [0, 1, 2, -1, -1] and int((bt >= 0).sum()) == 4
+
+
+@pytest.mark.parametrize("every", [1, 3, 40])
+def test_resize_where_few_rows_grow(every):
+    """Ranks whose owners lie far apart: only every so-many-th row takes pages."""
+    B, pages, P, width = 3000, 20000, 16, 8
+    r = np.random.RandomState(every)
+    refs = (r.rand(pages) < 0.3).astype(np.int32)
+    bt, counts = np.full((B, width), -1, np.int32), np.zeros(B, np.int32)
+    lens = np.where(np.arange(B) % every == every - 1, r.randint(1, width * P + 1, B), -1).astype(np.int32)
+    d, err = [_i32(x) for x in (bt, counts, refs)], _i32([0])
+    bt, counts, refs, flags = resize_reference(bt, counts, lens, refs, P)
+    pkv.resize_sequences(d[0], d[1], _i32(lens), d[2], P, err_flag=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == flags
+    for x, y in zip(d, (bt, counts, refs)):
+        assert np.array_equal(x.cpu().numpy(), y)
 
 
 # ---- fork ----------------------------------------------------------------------------------------------------------

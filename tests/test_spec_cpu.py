@@ -68,6 +68,14 @@ def test_tree_decode_refusals(lib):
     assert call(kc=fp4, vc=fp4) == BAD
 
 
+def test_bound_lists_are_not_taken_for_a_tensor():
+    import torch
+    x = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(TypeError, match="list"):
+        _abi._desc(_abi.Bound([x, x], None, 2))
+    assert _abi._desc(_abi.Bound([x], 5, 1)) == 5
+
+
 def test_workspace_sizes(lib):
     assert pkv.tree_decode_workspace(100, 32, 128, 152) > 0
     for bad in ((-1, 8, 128, 152), (5, 0, 128, 152), (5, 8, 96, 152), (5, 8, 128, 0)):
