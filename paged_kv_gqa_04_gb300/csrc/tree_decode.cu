@@ -67,7 +67,6 @@ namespace {
 constexpr int kTile = 128;    // positions per tile
 constexpr int kRows = 256;    // rows (lanes of two row tiles) per item
 constexpr int kTilePages = kTile / kPageSize;
-constexpr int kSnap = 2;      // no piece of a cut item is shorter than this many tiles
 constexpr int kItemUnits = 5; // what an item costs beyond its tiles (start, output, joining), in tiles
 constexpr int kPieces = 4;    // ring of pieces
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
@@ -180,7 +179,7 @@ struct Cuts {
 struct Place {
     int b, k, t;
 };
-// Unit `off` of sequence b; a cut closer than kSnap to an end of its item moves there.
+// Unit `off` of sequence b.
 __device__ __forceinline__ Place place_of(const TreeArgs& a, const Seq& s, int b, int off) {
     const int per = units_per_head(a, s);
     const int kvh = off / per;
@@ -190,17 +189,7 @@ __device__ __forceinline__ Place place_of(const TreeArgs& a, const Seq& s, int b
         rem -= nt + kItemUnits;
         nt = tiles_of(a, s, ++rg);
     }
-    Place p{b, kvh * s.RG + rg, max(rem - kItemUnits, 0)};
-    if (p.t < kSnap) {
-        p.t = 0;
-    } else if (nt - p.t < kSnap) {
-        p.t = 0;
-        if (++p.k == a.Hkv * s.RG) {
-            p.k = 0;
-            ++p.b;
-        }
-    }
-    return p;
+    return Place{b, kvh * s.RG + rg, max(rem - kItemUnits, 0)};
 }
 
 // The pieces of items between two places, in order.
@@ -451,8 +440,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         flag_error(a.err, PKV_FLAG_WAIT_TIMEOUT);
     };
     auto lane_wait = [&](uint32_t bb, uint32_t par) -> bool {
+        if (mbar_test_wait(bb, par)) return true;  // (cheaper than try_wait when the phase is over)
         uint64_t t0 = 0;
-        while (!mbar_try_wait_suspend(bb, par, 20000u)) {
+        while (!mbar_try_wait(bb, par)) {
             const uint64_t now = global_ns();
             if (t0 == 0) t0 = now;
             if (*abort_flag || now - t0 > kWaitLimitNs) {
@@ -546,8 +536,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     w.buf = buf;
                     w.uses0 = uses0, w.uses1 = uses1;
                     if (w.t0 == 0 && w.t1 < walk.nt) {
-                        // cuts up to kSnap tiles before the item's end are inside it
-                        const int c1 = cuts.at_or_before(cuts.cut(static_cast<int>(blockIdx.x) + 1) - w.t1 + walk.nt - kSnap);
+                        // the CTA that has the item's last unit
+                        const int c1 = cuts.at_or_before(cuts.cut(static_cast<int>(blockIdx.x) + 1) - w.t1 + walk.nt - 1);
                         meta = make_int4(w.q0 + w.tok0, w.toks, c1 - static_cast<int>(blockIdx.x) + 1, w.kvh);
                     }
                 }
@@ -601,8 +591,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     const bool more = j + 2 < nj;
                     bool here = false;
                     if (j >= 0) {
-                        // (a wait costs 100 cycles when the phase is over, and 200 more when it
-                        // ends meanwhile: what has landed is looked up before P is waited for)
+                        // (what has landed is looked up before P is waited for)
                         ok = landed(n);
                         here = ok && more && mbar_test_wait(bar(bFull + stage(n2)), phase(n2));
                         ok = ok && lane_wait(bar(bP + g), (g ? p1 : p0) & 1);
@@ -762,35 +751,30 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     fence_proxy_async_smem();
                 }
                 const bool any_bad = (bad[0] | bad[1] | bad[2] | bad[3]) != 0u;  // (uniform)
-                // ---- the tile's softmax, 64 columns at a time (S is read twice: holding
-                // ---- all of it would spill, and short loops stay in the instruction cache)
-                auto columns = [&](int c, uint32_t (&x)[2][32]) {
-                    tmem_ld32(tS + 64 * c, x[0]);
-                    tmem_ld32(tS + 64 * c + 32, x[1]);
+                // ---- the tile's softmax, 32 columns at a time: short loops stay in the
+                // ---- instruction cache (64 at a time, and 128 held so that S is read only
+                // ---- once, were slower by 2% and 8%)
+                auto columns = [&](int c, uint32_t (&x)[32]) {
+                    tmem_ld32(tS + 32 * c, x);
                     tmem_wait_ld();
-                    pin(x[0]);
-                    pin(x[1]);
+                    pin(x);
                     if (!inner) {
-                        const uint32_t v0 = c ? vis[2] : vis[0], v1 = c ? vis[3] : vis[1];
+                        const uint32_t v0 = word_of(vis, c);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            if (!(v0 & (1u << e))) x[0][e] = 0xFF800000u;
-                            if (!(v1 & (1u << e))) x[1][e] = 0xFF800000u;
-                        }
+                        for (int e = 0; e < 32; ++e)
+                            if (!(v0 & (1u << e))) x[e] = 0xFF800000u;
                     }
                 };
                 const bool work = ok && warp_live;
                 if (work) {
                     float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t x[2][32];
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t x[32];
                         columns(c, x);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            mx4[e & 2] = fmaxf(fmaxf(mx4[e & 2], __uint_as_float(x[0][e])), __uint_as_float(x[0][e + 1]));
-                            mx4[(e & 2) + 1] = fmaxf(fmaxf(mx4[(e & 2) + 1], __uint_as_float(x[1][e])), __uint_as_float(x[1][e + 1]));
-                        }
+                        for (int e = 0; e < 32; e += 2)
+                            mx4[e >> 1 & 3] = fmaxf(fmaxf(mx4[e >> 1 & 3], __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
                     }
                     const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl;
                     const bool move = mx > m + kRescaleLog2 || (m == -INFINITY && mx > m);
@@ -822,31 +806,28 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 const float2 sl2 = make_float2(sl, sl), mm2 = make_float2(mm, mm);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
-                for (int c = 0; c < 2; ++c) {
+                for (int c = 0; c < 4; ++c) {
                     if (work) {
-                        uint32_t x[2][32];
+                        uint32_t x[32];
                         columns(c, x);
+                        uint32_t p[16];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t p[16];
+                        for (int e = 0; e < 16; ++e) {
+                            float2 y = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sl2, mm2);
+                            y.x = fast_exp2(y.x);
+                            y.y = fast_exp2(y.y);
+                            sum[e & 1] = add2(sum[e & 1], y);
+                            p[e] = FP8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
+                        }
+                        if (any_bad) {
+                            const uint32_t b = word_of(bad, c);
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
-                                float2 y = fma2(make_float2(__uint_as_float(x[h][2 * e]), __uint_as_float(x[h][2 * e + 1])), sl2, mm2);
-                                y.x = fast_exp2(y.x);
-                                y.y = fast_exp2(y.y);
-                                sum[e & 1] = add2(sum[e & 1], y);
-                                p[e] = FP8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
+                                if (b & (1u << (2 * e))) p[e] &= 0xFFFF0000u;
+                                if (b & (2u << (2 * e))) p[e] &= 0x0000FFFFu;
                             }
-                            if (any_bad) {
-                                const uint32_t b = word_of(bad, 2 * c + h);
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) {
-                                    if (b & (1u << (2 * e))) p[e] &= 0xFFFF0000u;
-                                    if (b & (2u << (2 * e))) p[e] &= 0x0000FFFFu;
-                                }
-                            }
-                            tmem_st16(tP + 32 * c + 16 * h, p);
                         }
+                        tmem_st16(tP + 16 * c, p);
                     }
                 }
                 tmem_wait_st();
