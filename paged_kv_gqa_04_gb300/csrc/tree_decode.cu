@@ -535,16 +535,16 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     if (!w.two) buf ^= 1;
                     w.buf = buf;
                     w.uses0 = uses0, w.uses1 = uses1;
-                    if (w.t0 == 0 && w.t1 < walk.nt) {
-                        // the CTA that has the item's last unit
-                        const int c1 = cuts.at_or_before(cuts.cut(static_cast<int>(blockIdx.x) + 1) - w.t1 + walk.nt - 1);
-                        meta = make_int4(w.q0 + w.tok0, w.toks, c1 - static_cast<int>(blockIdx.x) + 1, w.kvh);
-                    }
                 }
                 if (i >= kPieces && !lane_wait(bar(bPieceFree + i % kPieces), (i / kPieces - 1) & 1)) break;
                 pieces[i % kPieces] = w;
                 mbar_arrive(piece_bar(i));
                 if (w.b < 0) break;
+                if (w.t0 == 0 && w.t1 < walk.nt) {
+                    // the CTA that has the item's last unit
+                    const int c1 = cuts.at_or_before(cuts.cut(static_cast<int>(blockIdx.x) + 1) - w.t1 + walk.nt - 1);
+                    meta = make_int4(w.q0 + w.tok0, w.toks, c1 - static_cast<int>(blockIdx.x) + 1, w.kvh);
+                }
                 // q, once the buffer is free: tile_toks tokens x G heads are consecutive operand rows
                 w.buffers([&](int bf, int uses) {
                     if (ok && uses > 0) ok = lane_wait(bar(bQFree + bf), (uses - 1) & 1);
@@ -1145,12 +1145,14 @@ __device__ __forceinline__ void join_rows(const TreeArgs& a, int ctas, int c, co
 
 template <int D>
 __global__ void __launch_bounds__(2 * D) tree_join_kernel(const TreeArgs a, int ctas) {
-    extern __shared__ int first[];                       // [ctas + 1]: the first block of entry c's item
+    extern __shared__ int4 note[];                       // [ctas]
+    int* first = reinterpret_cast<int*>(note + ctas);    // [ctas + 1]: the first block of entry c's item
     const int4* notes = reinterpret_cast<const int4*>(a.workspace);  // first token, tokens, pieces, kv head
     auto rows_per_block = [](int4 m) { return m.z <= 2 ? 32 : 8; };
     grid_dep_wait();
     for (int c = threadIdx.x; c < ctas; c += 2 * D) {
         const int4 m = notes[c];
+        note[c] = m;
         first[c + 1] = (m.y * a.G + rows_per_block(m) - 1) / rows_per_block(m);
     }
     if (threadIdx.x == 0) first[0] = 0;
@@ -1178,7 +1180,7 @@ __global__ void __launch_bounds__(2 * D) tree_join_kernel(const TreeArgs a, int 
             if (first[mid] <= b) lo = mid;
             else hi = mid;
         }
-        const int4 m = notes[lo];
+        const int4 m = note[lo];
         const int r0 = (b - first[lo]) * rows_per_block(m);
         if (m.z <= 2) join_rows<D, 4, 2>(a, ctas, lo, m, r0);
         else join_rows<D, 1, 8>(a, ctas, lo, m, r0);
@@ -1197,7 +1199,7 @@ cudaError_t launch_t(const TreeArgs& a, const CUtensorMap& tq, const CUtensorMap
     if (e != cudaSuccess) return e;
     // Every SM can hold four of these (D = 128) at once; no more than there are blocks of 8 rows.
     const int grid = static_cast<int>(std::min<int64_t>(4 * sms, (static_cast<int64_t>(a.T) * a.Hq + 7) / 8));
-    return launch_dependent(tree_join_kernel<D>, dim3(grid), dim3(2 * D), (sms + 1) * sizeof(int), s, a, sms);
+    return launch_dependent(tree_join_kernel<D>, dim3(grid), dim3(2 * D), sms * sizeof(int4) + (sms + 1) * sizeof(int), s, a, sms);
 }
 
 }  // namespace
