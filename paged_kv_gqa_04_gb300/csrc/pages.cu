@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const __grid_con
 // ---- pages taken from and returned to the pool ----------------------------------
 constexpr int kTakeThreads = 1024;
 constexpr int kTakeWarps = kTakeThreads / 32;
+static_assert(kTakeWarps == 32, "a warp reads the warps' sums, one per lane");
 constexpr int kMaxCluster = 16;
 constexpr int kKeptPages = 1024;           // pages of a warp whose free masks stay in a register
 constexpr uint32_t kDemandCap = 1u << 30;  // sums saturate here, above any pool
@@ -178,12 +179,15 @@ __device__ void block_prefix(uint32_t* x, int n, uint32_t* warp_sum) {
     uint32_t excl = __shfl_up_sync(0xffffffffu, inc, 1);
     if (lane == 0) excl = 0;
     __syncthreads();
-    uint32_t base = 0, total = 0;
-    for (int w = 0; w < kTakeWarps; ++w) {
-        if (w == warp) base = total;
-        total = sat_add(total, warp_sum[w]);
+    uint32_t sums = warp_sum[lane];                    // (as many warps as lanes)
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, sums, d);
+        if (lane >= d) sums = sat_add(sums, y);
     }
-    uint32_t run = sat_add(base, excl);
+    const uint32_t total = __shfl_sync(0xffffffffu, sums, 31);
+    const uint32_t base = __shfl_sync(0xffffffffu, sums, (warp + 31) & 31);
+    uint32_t run = warp ? sat_add(base, excl) : excl;
     for (int i = i0; i < i1; ++i) {
         const uint32_t d = x[i];
         x[i] = run;
@@ -406,12 +410,9 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
         if (lane < static_cast<int>(C)) st_cluster(smem_u32(&cta_free[rank]), lane, t);
     }
     cluster_barrier();
-    uint32_t at = 0, total_free = 0;
-    for (uint32_t r = 0; r < C; ++r) {
-        if (r == rank) at = total_free;
-        total_free += cta_free[r];
-    }
-    for (int w = 0; w < warp; ++w) at += warp_free[w];
+    const uint32_t of_cta = lane < static_cast<int>(C) ? cta_free[lane] : 0;
+    const uint32_t total_free = __reduce_add_sync(0xffffffffu, of_cta);
+    uint32_t at = __reduce_add_sync(0xffffffffu, (lane < static_cast<int>(rank) ? of_cta : 0) + (lane < warp ? warp_free[lane] : 0));
     const uint32_t last = min(wanted, total_free);  // ranks past it go to nobody
     int group = 0, owner = -1;                      // the row of the last rank seen
     for (int64_t g = p0; g < p1 && at < last; g += 128, ++group) {
