@@ -208,21 +208,17 @@ __device__ __forceinline__ int owner_of(const uint32_t* x, int n, uint32_t r) {
     return lo;
 }
 
-// What row b has and is to have; flags set when it stays as it is.
-__device__ __forceinline__ void resize_row(const TakeArgs& a, int b, int& have, int& want, int& flags) {
-    have = a.page_counts[b];
-    const int len = a.new_lens[b];
-    flags = 0;
+// The pages that a row of `have` pages is to have for `len` tokens; flags set when it stays as it is.
+__device__ __forceinline__ int pages_wanted(const TakeArgs& a, int have, int len, int& flags) {
     if (have < 0 || have > a.max_pages) {
-        flags = PKV_FLAG_PAGE_STATE;
-        want = have;
-        return;
+        flags |= PKV_FLAG_PAGE_STATE;
+        return have;
     }
-    want = have;
-    if (len < 0) return;
+    if (len < 0) return have;
     const int need = len / a.page_size + (len % a.page_size != 0);
-    if (need > a.max_pages) flags = PKV_FLAG_SEQ_LEN_RANGE;
-    else want = need;
+    if (need <= a.max_pages) return need;
+    flags |= PKV_FLAG_SEQ_LEN_RANGE;
+    return have;
 }
 
 // Returns of a large batch, by all SMs: a warp takes 256 entries of a row. The
@@ -233,8 +229,8 @@ __global__ void __launch_bounds__(256) return_kernel(const __grid_constant__ Tak
     grid_dep_launch();
     const int b = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (b >= a.n) return;
-    int have, want, flags;
-    resize_row(a, b, have, want, flags);
+    int flags = 0;
+    const int have = a.page_counts[b], want = pages_wanted(a, have, a.new_lens[b], flags);
     flags = 0;  // the take reports them
     const int j0 = max(want, static_cast<int>(blockIdx.x) * kReturnSpan);
     const int j1 = min(have, static_cast<int>(blockIdx.x + 1) * kReturnSpan);
@@ -287,7 +283,7 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
     const int n = a.n;
     uint32_t* need = dyn;                              // [n + 1]: demands, then their prefix sums
     int32_t* held = reinterpret_cast<int32_t*>(dyn + (n + 1));  // resize: [n] entries in use; fork: parent's length, -1 = not made
-    uint32_t* give = dyn + (2 * n + 1);                // resize: [n + 1] returns, then their prefix sums
+    uint32_t* give = dyn + (2 * n + 1);                // resize: [n + 1] returns, then their prefix sums; entries wanted where they are made already
     int32_t* tail = reinterpret_cast<int32_t*>(give);  // fork: [n] page to copy, -1 = none
     uint32_t* list = dyn + take_words(n) + warp * 128; // this warp's free pages, in order
 
@@ -299,17 +295,27 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
 
     int flags = 0;
     if constexpr (!FORK) {
-        for (int b = tid; b < n; b += kTakeThreads) {
-            int have, want, f;
-            resize_row(a, b, have, want, f);
-            flags |= f;
-            held[b] = have;
-            need[b] = want > have ? want - have : 0;
-            give[b] = want < have ? have - want : 0;
+        for (int b0 = tid; b0 < n; b0 += 4 * kTakeThreads) {
+            int have[4], len[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int b = b0 + k * kTakeThreads;
+                have[k] = b < n ? a.page_counts[b] : 0;
+                len[k] = b < n ? a.new_lens[b] : -1;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int b = b0 + k * kTakeThreads;
+                if (b >= n) break;
+                const int want = pages_wanted(a, have[k], len[k], flags);
+                held[b] = have[k];
+                need[b] = want > have[k] ? want - have[k] : 0;
+                give[b] = a.returned ? want : want < have[k] ? have[k] - want : 0;
+            }
         }
-        block_prefix(give, n, warp_sum);
         // Returns (unless a kernel of their own made them), dealt out by entry
         // over the cluster, four per thread on their way.
+        if (!a.returned) block_prefix(give, n, warp_sum);
         const uint32_t total = a.returned ? 0 : give[n], span = C * kTakeThreads;
         for (uint32_t e0 = rank * kTakeThreads + tid; e0 < total; e0 += 4 * span) {
             int page[4];
@@ -429,11 +435,9 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
         // the group's free pages side by side, so that neighbouring lanes write
         // neighbouring entries
         uint32_t o = inc - own_n;
-        while (m) {
-            const int k = __ffs(m) - 1;
-            m &= m - 1;
-            list[o++] = static_cast<uint32_t>(p + k);
-        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (m >> k & 1) list[o++] = static_cast<uint32_t>(p + k);
         __syncwarp();
         for (uint32_t k0 = 0; k0 < found && at + k0 < last; k0 += 32) {
             const uint32_t end = min(at + found, last);
@@ -470,11 +474,11 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
     if (rank != 0) return;
     for (int i = tid; i < n; i += kTakeThreads) {
         if constexpr (!FORK) {
-            int have, want, f;  // (again: the sums saturate)
-            resize_row(a, i, have, want, f);
-            const bool fails = want > have && need[i + 1] > total_free;
+            // (tables of returns made here are small: their sums do not saturate)
+            const int want = static_cast<int>(a.returned ? give[i] : held[i] + (need[i + 1] - need[i]) - (give[i + 1] - give[i]));
+            const bool fails = want > held[i] && need[i + 1] > total_free;
             if (fails) flag_error(a.err, PKV_FLAG_POOL_EMPTY);
-            else if (want != have) a.page_counts[i] = want;
+            else if (want != held[i]) a.page_counts[i] = want;
         } else {
             const bool fails = tail[i] >= 0 && need[i + 1] > total_free;
             if (fails) flag_error(a.err, PKV_FLAG_POOL_EMPTY);
