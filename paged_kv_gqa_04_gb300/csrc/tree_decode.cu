@@ -1163,6 +1163,9 @@ __global__ void __launch_bounds__(2 * D) tree_join_kernel(const TreeArgs a, int 
     int* first = reinterpret_cast<int*>(note + ctas);    // [ctas + 1]: the first block of entry c's item
     const int4* notes = reinterpret_cast<const int4*>(a.workspace);  // first token, tokens, pieces, kv head
     auto rows_per_block = [](int4 m) { return m.z <= 2 ? 32 : 8; };
+    // The next grid may start: everything before the tree kernel is done (it began
+    // this one behind its own wait), and neither of the two writes index inputs.
+    grid_dep_launch();
     grid_dep_wait();
     for (int c = threadIdx.x; c < ctas; c += 2 * D) {
         const int4 m = notes[c];
