@@ -1215,6 +1215,8 @@ cudaError_t launch_t(const TreeArgs& a, const CUtensorMap& tq, const CUtensorMap
     if (e != cudaSuccess) return e;
     e = launch_dependent(tree_kernel<D, FP8>, dim3(sms), dim3(C::THREADS), C::SMEM, s, tq, tk, tv, a);
     if (e != cudaSuccess) return e;
+    // An item of one tile is not cut (two short chats: 9.5 us with a joining kernel, 7.6 without).
+    if (a.max_pages * kPageSize <= kTile) return cudaSuccess;
     // Every SM can hold four of these (D = 128) at once; no more than there are blocks of 8 rows.
     const int grid = static_cast<int>(std::min<int64_t>(4 * sms, (static_cast<int64_t>(a.T) * a.Hq + 7) / 8));
     return launch_dependent(tree_join_kernel<D>, dim3(grid), dim3(2 * D), sms * sizeof(int4) + (sms + 1) * sizeof(int), s, a, sms);
