@@ -446,10 +446,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     const uint32_t tmem = misc[0];
     const Place from = place[0], to = place[1];
 
-    // q and the cache may still be being written by the preceding grid.
-    grid_dep_wait();
-    grid_dep_launch();
-
+    // q, the mask, the scales and the cache may still be being written by the
+    // preceding grid: every role waits for it, the walker and the copies once
+    // they have the first piece and its pages, which are index inputs too (1 us
+    // a call, back to back).
     auto give_up = [&]() {
         *abort_flag = 1;
         flag_error(a.err, PKV_FLAG_WAIT_TIMEOUT);
@@ -498,6 +498,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     return p < npages && t < w.t1 ? __ldg(a.block_tables + w.b * a.bt_s0 + p) : -1;
                 };
                 int nxt = page_at(w.t0);
+                if (i == 0) grid_dep_wait();
                 for (int t = w.t0; t < w.t1; ++t, n += 2) {
                     int id = nxt;
                     nxt = page_at(t + 1);
@@ -560,6 +561,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     const int c1 = cuts.at_or_before(cuts.cut(static_cast<int>(blockIdx.x) + 1) - w.t1 + walk.nt - 1);
                     meta = make_int4(w.q0 + w.tok0, w.toks, c1 - static_cast<int>(blockIdx.x) + 1, w.kvh);
                 }
+                if (i == 0) grid_dep_wait();
                 // q, once the buffer is free: tile_toks tokens x G heads are consecutive operand rows
                 w.buffers([&](int bf, int uses) {
                     if (ok && uses > 0) ok = lane_wait(bar(bQFree + bf), (uses - 1) & 1);
@@ -572,11 +574,13 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     ++(bf ? uses1 : uses0);
                 });
             }
+            grid_dep_wait();
             reinterpret_cast<int4*>(a.workspace)[blockIdx.x] = meta;
             if (uses0) (void)mbar_wait_bounded(bar(FP8 ? bQRaw : bQ), (uses0 - 1) & 1, kWaitLimitNs);
             if (uses1) (void)mbar_wait_bounded(bar((FP8 ? bQRaw : bQ) + 1), (uses1 - 1) & 1, kWaitLimitNs);
         } else if (warp == 1 && lane == 0) {
             // ======================= tensor-core issue (one thread) ===================
+            grid_dep_wait();  // (so that its bounded waits begin behind the preceding grid)
             constexpr int FMT = FP8 ? 0 : 1;  // f16 or bf16 operands
             // the sign of softmax_scale goes into q (bit 13 negates A)
             const uint32_t idesc_qk = umma_idesc(128, kTile, FMT, FMT, false, false) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
@@ -657,6 +661,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     } else if (warp < 12) {
         // ======================= softmax ==========================================
         reg_inc<C::REG_SM>();
+        grid_dep_wait();
+        grid_dep_launch();
         const int grp = (warp - 4) >> 2, wq = warp & 3;
         const int row_l = 32 * wq + lane;              // this thread's lane of tensor memory
         const uint32_t tl = tmem + (static_cast<uint32_t>(wq) << 21);  // lanes 32 wq .. (bits 16 and up)
@@ -1006,6 +1012,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     } else {
         // ======================= E4M3 bytes and bf16 q to f16 tiles ===============
         reg_dec<C::REG_CV>();
+        grid_dep_wait();
         const int ct = tid - 384;
         constexpr int CH = D / 16;  // 16-byte chunks of a raw row
         int n = 0;
@@ -1217,8 +1224,9 @@ cudaError_t launch_t(const TreeArgs& a, const CUtensorMap& tq, const CUtensorMap
     if (e != cudaSuccess) return e;
     // An item of one tile is not cut (two short chats: 9.5 us with a joining kernel, 7.6 without).
     if (a.max_pages * kPageSize <= kTile) return cudaSuccess;
-    // Every SM can hold four of these (D = 128) at once; no more than there are blocks of 8 rows.
-    const int grid = static_cast<int>(std::min<int64_t>(4 * sms, (static_cast<int64_t>(a.T) * a.Hq + 7) / 8));
+    // An SM holds three of these at once (D = 128; 64 registers a thread, for four, spill: 43 us and not
+    // 38 for two long contexts); no more than there are blocks of 8 rows.
+    const int grid = static_cast<int>(std::min<int64_t>(3 * sms, (static_cast<int64_t>(a.T) * a.Hq + 7) / 8));
     return launch_dependent(tree_join_kernel<D>, dim3(grid), dim3(2 * D), sms * sizeof(int4) + (sms + 1) * sizeof(int), s, a, sms);
 }
 
