@@ -26,7 +26,7 @@
 // share_kernel (the second half of a fork). CTAs of (fork, cache, 16 KB) copy
 // the partial last page; CTAs of (fork, stretch of the table) copy the shared
 // entries and raise their pages' counts. Bound by memory: 96 forks in 64 caches
-// of 16 KB pages (195 MB) take 20 us of the call's 27.
+// of 16 KB pages (195 MB) take 20 us of the call's 26.
 #include <algorithm>
 
 #include "pkv_internal.h"
@@ -155,9 +155,12 @@ __device__ __forceinline__ uint32_t cluster_size() {
     return r;
 }
 // All threads of the cluster; what they wrote before (shared memory of any
-// CTA, device memory) is visible to all of them after it.
+// CTA, device memory) is visible to all of them after it. (SOLO: one CTA, whose
+// own barrier does: sixteen forks in 28 layers 21 us and not 23.)
+template <bool SOLO>
 __device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if constexpr (SOLO) __syncthreads();
+    else asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void st_cluster(uint32_t local_addr, uint32_t rank, uint32_t v) {
     asm volatile(
@@ -281,12 +284,12 @@ __device__ __forceinline__ uint32_t free_mask(const int32_t* refs, int64_t p, in
 // Dynamic shared memory: words for n rows or forks, then a page list per warp.
 __host__ __device__ constexpr size_t take_words(int n) { return 3 * static_cast<size_t>(n) + 2; }
 
-template <bool FORK>
+template <bool FORK, bool SOLO>
 __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constant__ TakeArgs a) {
     extern __shared__ uint32_t dyn[];
     __shared__ uint32_t warp_sum[kTakeWarps], warp_free[kTakeWarps], cta_free[kMaxCluster];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t rank = cluster_rank(), C = cluster_size();
+    const uint32_t rank = SOLO ? 0 : cluster_rank(), C = SOLO ? 1 : cluster_size();
     const int n = a.n;
     uint32_t* need = dyn;                              // [n + 1]: demands, then their prefix sums
     int32_t* held = reinterpret_cast<int32_t*>(dyn + (n + 1));  // resize: [n] entries in use; fork: parent's length, -1 = not made
@@ -380,7 +383,7 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
             held[i] = L;
             tail[i] = L < 0 ? -1 : src;
         }
-        cluster_barrier();
+        cluster_barrier<SOLO>();
         for (int i = tid; i < n; i += kTakeThreads) {
             if (held[i] >= 0 && __ldcg(a.page_counts + a.forks[2 * i + 1]) != -(n - i)) {
                 flags |= PKV_FLAG_PAGE_STATE;  // an earlier fork has this child
@@ -391,7 +394,7 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
         }
     }
     block_prefix(need, n, warp_sum);
-    cluster_barrier();  // every return is counted
+    cluster_barrier<SOLO>();  // every return is counted
 
     // ---- free pages: each warp a contiguous stretch ------------------------------
     const int64_t cta_span = ((a.num_pages + C - 1) / C + 127) / 128 * 128;
@@ -420,9 +423,10 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
     __syncthreads();
     if (warp == 0) {
         const uint32_t t = __reduce_add_sync(0xffffffffu, warp_free[lane]);
-        if (lane < static_cast<int>(C)) st_cluster(smem_u32(&cta_free[rank]), lane, t);
+        if (SOLO) cta_free[0] = t;
+        else if (lane < static_cast<int>(C)) st_cluster(smem_u32(&cta_free[rank]), lane, t);
     }
-    cluster_barrier();
+    cluster_barrier<SOLO>();
     const uint32_t of_cta = lane < static_cast<int>(C) ? cta_free[lane] : 0;
     const uint32_t total_free = __reduce_add_sync(0xffffffffu, of_cta);
     uint32_t at = __reduce_add_sync(0xffffffffu, (lane < static_cast<int>(rank) ? of_cta : 0) + (lane < warp ? warp_free[lane] : 0));
@@ -477,7 +481,7 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
         __syncwarp();
     }
     if (flags) flag_error(a.err, flags);
-    cluster_barrier();  // every CTA has read the counts and lengths
+    cluster_barrier<SOLO>();  // every CTA has read the counts and lengths
     if (rank != 0) return;
     for (int i = tid; i < n; i += kTakeThreads) {
         if constexpr (!FORK) {
@@ -592,13 +596,13 @@ __global__ void __launch_bounds__(kShareThreads) share_kernel(const __grid_const
 
 template <bool FORK>
 cudaError_t launch_take(const TakeArgs& a, cudaStream_t s) {
-    auto kern = take_kernel<FORK>;
-    const size_t smem = (take_words(a.n) + kTakeWarps * 128) * 4;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
     // A CTA keeps the free masks of 32,768 pages in registers; larger pools are
     // spread over a cluster (16 CTAs, the largest there is, is past the portable 8).
     const unsigned C = a.num_pages <= 8192 ? 1 : a.num_pages <= 32768 ? 4 : kMaxCluster;
+    auto kern = C == 1 ? take_kernel<FORK, true> : take_kernel<FORK, false>;
+    const size_t smem = (take_words(a.n) + kTakeWarps * 128) * 4;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
     if (C > 8) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;

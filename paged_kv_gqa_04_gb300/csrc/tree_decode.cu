@@ -56,12 +56,12 @@
 //
 // Bound. With one row tile a tile of K and V (64 KB, bf16, D = 128) takes 2600 to
 // 2900 cycles, HBM's share of an SM is 2830; 64 contexts of 1 to 8192 (413 MB)
-// take 83 us in all, 5.0 TB/s, the rest being the start (6 us to the first
+// take 81 us in all, 5.1 TB/s, the rest being the start (6 us to the first
 // scores), the ends of items and the joining kernel. With two row tiles it
 // takes about 4300: scores, softmax, P and P . V of a group follow one another,
 // and tensor memory has room for two groups (S and O of each, 512 columns), so
 // the products' 2048 cycles are half of it; 16 contexts of 8 Ki with 64 drafted
-// tokens (519 MB, 129 GFLOP) take 144 us, 3.6 TB/s and 0.90 PFLOP/s. FP8 adds the
+// tokens (519 MB, 129 GFLOP) take 141 us, 3.7 TB/s and 0.91 PFLOP/s. FP8 adds the
 // conversion, which shares a pipe with the exponentials. Measured and not kept
 // (that last case): scores and P in two halves of 64 positions each with its own
 // barriers (199 us: products of 64 columns take as long as those of 128, and the
