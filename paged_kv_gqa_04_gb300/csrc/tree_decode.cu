@@ -72,6 +72,7 @@
 // Waits are bounded (about one second): a role that gives up sets
 // PKV_FLAG_WAIT_TIMEOUT and a CTA-wide flag that ends the others' waits.
 #include <algorithm>
+#include <atomic>
 
 #include "pkv_internal.h"
 #include "pkv_ptx.cuh"
@@ -122,7 +123,8 @@ struct Cfg {
     static constexpr int OFF_PIECE = OFF_MISC + 192;       // [kPieces] Piece
     static constexpr int SMEM = OFF_PIECE + kPieces * 64 + 1024;  // + alignment slack
     static_assert(SMEM <= 232448, "shared memory of one CTA");
-    static_assert(FP8 ? REG_IO + 2 * REG_SM + REG_CV <= 512 : REG_IO + 2 * REG_SM <= 504, "registers as launched");
+    static constexpr int REGS = 128 * (REG_IO + 2 * REG_SM + (FP8 ? REG_CV : 0));
+    static_assert(REGS <= (FP8 ? 128 : 168) * THREADS, "registers as launched");
     // Tensor-memory columns of a softmax group: S (P over it, or behind O, where that leaves room), then O.
     static constexpr uint32_t P_COL = D == 64 ? 192 : 0;
     static constexpr uint32_t ML_COL = 64;                 // m and l for the other group, once S is read
@@ -1218,6 +1220,16 @@ cudaError_t launch_t(const TreeArgs& a, const CUtensorMap& tq, const CUtensorMap
     int sms = 0;
     cudaError_t e = device_sm_count(&sms);
     if (e != cudaSuccess) return e;
+    // The roles deal out the registers that the kernel is launched with: as many
+    // as assumed, or it would wait for more that never come.
+    static std::atomic<bool> as_assumed{false};
+    if (!as_assumed.load(std::memory_order_relaxed)) {
+        cudaFuncAttributes at{};
+        e = cudaFuncGetAttributes(&at, tree_kernel<D, FP8>);
+        if (e != cudaSuccess) return e;
+        if (at.numRegs * C::THREADS < C::REGS) return cudaErrorInvalidConfiguration;
+        as_assumed.store(true, std::memory_order_relaxed);
+    }
     e = cudaFuncSetAttribute(tree_kernel<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     e = launch_dependent(tree_kernel<D, FP8>, dim3(sms), dim3(C::THREADS), C::SMEM, s, tq, tk, tv, a);
