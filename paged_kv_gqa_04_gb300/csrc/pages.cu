@@ -19,7 +19,7 @@
 // distributed shared memory, and each zero of rank r < demand goes to the
 // entry that the prefix sums give r. Every result follows from the inputs
 // alone: atomics only add and subtract counts. Bound by latency: five round
-// trips to memory and as many barriers of the CTA (256 rows, 16384 pages: 6.7 us
+// trips to memory and as many barriers of the CTA (256 rows, 16384 pages: 6.6 us
 // a call), then, when very many pages are given out, by the instructions of 16
 // SMs (4096 rows of up to 100 pages, 524288 pages: 19 us a call on average).
 //
@@ -170,40 +170,48 @@ __device__ __forceinline__ void st_cluster(uint32_t local_addr, uint32_t rank, u
         : "memory");
 }
 
-// Exclusive saturating prefix sums of x[0, n) in place, x[n] = the total. All
-// threads of the CTA; thread t owns a contiguous stretch.
-__device__ void block_prefix(uint32_t* x, int n, uint32_t* warp_sum) {
+// Exclusive saturating prefix sums of each of the arrays x[k][0, n) in place,
+// x[k][n] = the total. All threads of the CTA; thread t owns a contiguous stretch.
+template <int K>
+__device__ void block_prefix(uint32_t* const (&x)[K], int n, uint32_t (*warp_sum)[kTakeWarps]) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int seg = (n + kTakeThreads - 1) / kTakeThreads;
     const int i0 = min(tid * seg, n), i1 = min(i0 + seg, n);
     __syncthreads();
-    uint32_t sum = 0;
-    for (int i = i0; i < i1; ++i) sum = sat_add(sum, x[i]);
-    uint32_t inc = sum;
+    uint32_t excl[K];
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc = sat_add(inc, y);
+    for (int k = 0; k < K; ++k) {
+        uint32_t sum = 0;
+        for (int i = i0; i < i1; ++i) sum = sat_add(sum, x[k][i]);
+        uint32_t inc = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc = sat_add(inc, y);
+        }
+        if (lane == 31) warp_sum[k][warp] = inc;
+        excl[k] = __shfl_up_sync(0xffffffffu, inc, 1);
+        if (lane == 0) excl[k] = 0;
     }
-    if (lane == 31) warp_sum[warp] = inc;
-    uint32_t excl = __shfl_up_sync(0xffffffffu, inc, 1);
-    if (lane == 0) excl = 0;
     __syncthreads();
-    uint32_t sums = warp_sum[lane];                    // (as many warps as lanes)
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, sums, d);
-        if (lane >= d) sums = sat_add(sums, y);
+    for (int k = 0; k < K; ++k) {
+        uint32_t sums = warp_sum[k][lane];             // (as many warps as lanes)
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, sums, d);
+            if (lane >= d) sums = sat_add(sums, y);
+        }
+        const uint32_t total = __shfl_sync(0xffffffffu, sums, 31);
+        const uint32_t base = __shfl_sync(0xffffffffu, sums, (warp + 31) & 31);
+        uint32_t run = warp ? sat_add(base, excl[k]) : excl[k];
+        for (int i = i0; i < i1; ++i) {
+            const uint32_t d = x[k][i];
+            x[k][i] = run;
+            run = sat_add(run, d);
+        }
+        if (tid == 0) x[k][n] = total;
     }
-    const uint32_t total = __shfl_sync(0xffffffffu, sums, 31);
-    const uint32_t base = __shfl_sync(0xffffffffu, sums, (warp + 31) & 31);
-    uint32_t run = warp ? sat_add(base, excl) : excl;
-    for (int i = i0; i < i1; ++i) {
-        const uint32_t d = x[i];
-        x[i] = run;
-        run = sat_add(run, d);
-    }
-    if (tid == 0) x[n] = total;
     __syncthreads();
 }
 
@@ -287,7 +295,7 @@ __host__ __device__ constexpr size_t take_words(int n) { return 3 * static_cast<
 template <bool FORK, bool SOLO>
 __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constant__ TakeArgs a) {
     extern __shared__ uint32_t dyn[];
-    __shared__ uint32_t warp_sum[kTakeWarps], warp_free[kTakeWarps], cta_free[kMaxCluster];
+    __shared__ uint32_t warp_sum[2][kTakeWarps], warp_free[kTakeWarps], cta_free[kMaxCluster];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = SOLO ? 0 : cluster_rank(), C = SOLO ? 1 : cluster_size();
     const int n = a.n;
@@ -325,7 +333,8 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
         }
         // Returns (unless a kernel of their own made them), dealt out by entry
         // over the cluster, four per thread on their way.
-        if (!a.returned) block_prefix(give, n, warp_sum);
+        if (a.returned) block_prefix<1>({need}, n, warp_sum);
+        else block_prefix<2>({need, give}, n, warp_sum);
         const uint32_t total = a.returned ? 0 : give[n], span = C * kTakeThreads;
         for (uint32_t e0 = rank * kTakeThreads + tid; e0 < total; e0 += 4 * span) {
             int page[4];
@@ -392,8 +401,8 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
             }
             need[i] = tail[i] >= 0 ? 1 : 0;
         }
+        block_prefix<1>({need}, n, warp_sum);
     }
-    block_prefix(need, n, warp_sum);
     cluster_barrier<SOLO>();  // every return is counted
 
     // ---- free pages: each warp a contiguous stretch ------------------------------
