@@ -196,9 +196,8 @@ struct Cuts {
 struct Place {
     int b, k, t;
 };
-// Unit `off` of sequence b.
-__device__ __forceinline__ Place place_of(const TreeArgs& a, const Seq& s, int b, int off) {
-    const int per = units_per_head(a, s);
+// Unit `off` of sequence b, of `per` units a kv head.
+__device__ __forceinline__ Place place_of(const TreeArgs& a, const Seq& s, int per, int b, int off) {
     const int kvh = off / per;
     int rem = off - kvh * per;
     int rg = 0, nt = tiles_of(a, s, 0);
@@ -370,7 +369,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t num_pages = a.num_pages;
 
-    if (tid == 0) {
+    if (tid == C::THREADS - 32) {  // (the first threads have sequences to look at)
         for (int i = 0; i < C::ST; ++i) {
             mbar_init(bar(bFull + i), FP8 ? 4 : 1);
             mbar_init(bar(bFree + i), 2);  // either group's use (two arrivals where one group has the tile)
@@ -410,8 +409,13 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
     {
         const int seg = (a.B + C::THREADS - 1) / C::THREADS;
         const int b0 = min(tid * seg, a.B), b1 = min(b0 + seg, a.B);
-        int sum = 0, flags = 0;
-        for (int b = b0; b < b1; ++b) sum = add_units(sum, a.Hkv * units_per_head(a, seq_of(a, b, flags)));
+        int sum = 0, flags = 0, per = 0;
+        Seq s{};
+        for (int b = b0; b < b1; ++b) {
+            s = seq_of(a, b, flags);
+            per = units_per_head(a, s);
+            sum = add_units(sum, a.Hkv * per);
+        }
         if (flags && blockIdx.x == 0) flag_error(a.err, flags);
         int inc = sum;
 #pragma unroll
@@ -433,11 +437,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         const int x0 = cuts.cut(c), x1 = cuts.cut(c + 1);
         if (c < cuts.n && x1 >= at && x0 < at + sum) {
             for (int b = b0; b < b1; ++b) {
-                int ignored = 0;
-                const Seq s = seq_of(a, b, ignored);
-                const int n = a.Hkv * units_per_head(a, s);
-                if (x0 >= at && x0 < at + n) place[0] = place_of(a, s, b, x0 - at);
-                if (x1 >= at && x1 < at + n) place[1] = place_of(a, s, b, x1 - at);
+                if (seg > 1) {
+                    int ignored = 0;
+                    s = seq_of(a, b, ignored);
+                    per = units_per_head(a, s);
+                }
+                const int n = a.Hkv * per;
+                if (x0 >= at && x0 < at + n) place[0] = place_of(a, s, per, b, x0 - at);
+                if (x1 >= at && x1 < at + n) place[1] = place_of(a, s, per, b, x1 - at);
                 at += n;
             }
         }
