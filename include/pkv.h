@@ -653,6 +653,9 @@ pkv_status pkv_selftest_bounded_wait(int64_t limit_ns, int32_t* err_flag, uint64
  *   lse_out[r,h] = m + ln sum_t exp(score_t - m)      (natural log)
  * A row that sees nothing gives 0 and -inf. K and V of positions that a row
  * does not see have no effect on it, whatever they hold.
+ * Scores and sums are fp32. The weights meet V as for pkv_paged_gqa_decode:
+ * bf16 caches as a bf16 term and the bf16 rest (2^-16 of the weight), FP8
+ * caches as f16 (2^-11).
  *
  * q            [T, Hq, D] bf16 (already rotated), innermost stride 1, rows
  *              16-byte aligned.

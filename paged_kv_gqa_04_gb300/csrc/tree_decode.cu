@@ -44,9 +44,13 @@
 //
 // The online softmax keeps a reference maximum per row that moves only when a
 // tile's maximum passes it by more than 8 (log2), so P <= 2^8 and O is scaled
-// rarely. P is rounded to bf16 (f16 for FP8 caches): half a step of 2^-8
-// (2^-11) of each weight, which the bf16 output's own 2^-8 covers; the sums of
-// the weights are taken before the rounding, in fp32. For FP8 caches q is
+// rarely. bf16 alone is too few bits for P where the weighted values cancel, so
+// P is its bf16 rounding (2^-8 of it) and the rest, rounded again (2^-16 in all),
+// and V meets both, as in the one-token decode; the scores' columns hold both.
+// One term: 64 contexts of 1 to 8192 82 us and not 92, 16 of 8 Ki with 64 drafted
+// tokens 141 and not 180, but outputs of weights near one another up to 11 times
+// their bound off. (FP8 caches: one f16 term, 2^-11.) The sums of the weights are
+// taken before the rounding, in fp32. For FP8 caches q is
 // scaled by a power of two per row into f16's range, which is exact for
 // every value within 2^29 of the row's largest.
 //
@@ -126,9 +130,14 @@ struct Cfg {
     static constexpr int REGS = 128 * (REG_IO + 2 * REG_SM + (FP8 ? REG_CV : 0));
     static_assert(REGS <= (FP8 ? 128 : 168) * THREADS, "registers as launched");
     // Tensor-memory columns of a softmax group: S (P over it, or behind O, where that leaves room), then O.
-    static constexpr uint32_t P_COL = D == 64 ? 192 : 0;
-    static constexpr uint32_t ML_COL = 64;                 // m and l for the other group, once S is read
+    // 32 positions of P are 16 columns; bf16: those of the rounded rest beside those of the rounded term, the
+    // columns of S that they were.
+    static constexpr int TERMS = FP8 ? 1 : 2;
+    static constexpr uint32_t P_COL = FP8 && D == 64 ? 192 : 0;
     static constexpr uint32_t O_COL = 128;
+    static __device__ __forceinline__ constexpr uint32_t p_col(int k, int term) {  // of positions 16 k ..
+        return P_COL + 16 * TERMS * (k >> 1) + 8 * (k & 1) + 16 * term;
+    }
 };
 
 struct Seq {
@@ -268,6 +277,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
           "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr)
+        : "memory");
+}
+// 32 columns: the 16 of r, then the 16 of q; complete after tmem_wait_st().
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[16], const uint32_t (&q)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,"
+        "%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(q[0]), "r"(q[1]), "r"(q[2]),
+        "r"(q[3]), "r"(q[4]), "r"(q[5]), "r"(q[6]), "r"(q[7]), "r"(q[8]), "r"(q[9]), "r"(q[10]), "r"(q[11]), "r"(q[12]),
+        "r"(q[13]), "r"(q[14]), "r"(q[15])
         : "memory");
 }
 // The values of a tensor-memory load are used only past this point (which follows its wait).
@@ -630,7 +651,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         const uint32_t more_o = j > 1 || *reinterpret_cast<volatile uint32_t*>(go_on + g) != 0u;  // O goes on, or starts
 #pragma unroll
                         for (int k = 0; k < kTile / 16; ++k)
-                            umma_ts(tS + C::O_COL, tS + C::P_COL + 8 * k, vt + k * (2048 >> 4), kDescHi, kIdescPv, k > 0 ? 1u : more_o);
+#pragma unroll
+                            for (int e = 0; e < C::TERMS; ++e)
+                                umma_ts(tS + C::O_COL, tS + C::p_col(k, e), vt + k * (2048 >> 4), kDescHi, kIdescPv,
+                                        k + e > 0 ? 1u : more_o);
                         if (!w.two) {
                             // (one row tile is bound by memory: V's stage is wanted back at once)
                             mbar_arrive(bar(bFree + stage(n)));
@@ -675,7 +699,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
         const int grp = (warp - 4) >> 2, wq = warp & 3;
         const int row_l = 32 * wq + lane;              // this thread's lane of tensor memory
         const uint32_t tl = tmem + (static_cast<uint32_t>(wq) << 21);  // lanes 32 wq .. (bits 16 and up)
-        const uint32_t tS = tl + 256 * grp, tP = tS + C::P_COL, tO = tS + C::O_COL;
+        const uint32_t tS = tl + 256 * grp, tO = tS + C::O_COL;
         const int tok_l = row_l / a.G, g_l = row_l - tok_l * a.G;      // its token in the row tile, its head
         int tile0 = 0, job = 0;                        // tiles before this piece, this group's jobs
         int n_o = 0, n_oo = 0;                         // items that this and the other group had a part in
@@ -840,24 +864,35 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     if (work) {
                         uint32_t x[32];
                         columns(c, x);
-                        uint32_t p[16];
+                        uint32_t p[16], rest[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             float2 y = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sl2, mm2);
                             y.x = fast_exp2(y.x);
                             y.y = fast_exp2(y.y);
                             sum[e & 1] = add2(sum[e & 1], y);
-                            p[e] = FP8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
+                            if constexpr (FP8) {
+                                p[e] = pack_f16(y.x, y.y);
+                            } else {
+                                p[e] = pack_bf16(y.x, y.y);
+                                y = fma2(make_float2(bf16_lo(p[e]), bf16_hi(p[e])), make_float2(-1.f, -1.f), y);  // (exact)
+                                rest[e] = pack_bf16(y.x, y.y);
+                            }
                         }
                         if (any_bad) {
                             const uint32_t b = word_of(bad, c);
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
-                                if (b & (1u << (2 * e))) p[e] &= 0xFFFF0000u;
-                                if (b & (2u << (2 * e))) p[e] &= 0x0000FFFFu;
+                                const uint32_t keep = (b & (1u << (2 * e)) ? 0u : 0x0000FFFFu) | (b & (2u << (2 * e)) ? 0u : 0xFFFF0000u);
+                                p[e] &= keep;
+                                if constexpr (!FP8) rest[e] &= keep;
                             }
                         }
-                        tmem_st16(tP + 16 * c, p);
+                        if constexpr (FP8) {
+                            tmem_st16(tS + C::p_col(2 * c, 0), p);
+                        } else {
+                            tmem_st32(tS + C::p_col(2 * c, 0), p, rest);
+                        }
                     }
                 }
                 tmem_wait_st();
@@ -916,26 +951,25 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             const bool mine = job > job0;
             const bool theirs = !two && nt > 1 - grp;
             float mo = -INFINITY, lo = 0.f;            // the other group's
-            if (!two) {
-                uint32_t x[8] = {__float_as_uint(m), __float_as_uint(l), 0u, 0u, 0u, 0u, 0u, 0u};
-                tmem_st8(tS + C::ML_COL, x);
-                tmem_wait_st();
-            }
             tc_fence_before();
-            ok = named_bar_and(1, 256, ok);            // every S of this piece is read
+            ok = named_bar_and(1, 256, ok);            // every S of this piece is read, and q done with
             tc_fence_after();
             if (!ok) break;
-            if (!two) {
-                uint32_t x[8];
-                tmem_ld8(tl + 256 * (1 - grp) + C::ML_COL, x);
-                tmem_wait_ld();
-                pin(x);
-                mo = __uint_as_float(x[0]);
-                lo = __uint_as_float(x[1]);
-            }
-            tc_fence_before();
-            __syncwarp();
             if (lane == 0) mbar_arrive(bar(bX + i % kPieces));  // S may be written for the next item
+            // q's buffer is free for m and l, and then the output
+            const uint32_t stage_row = s0 + C::OFF_Q + (two ? grp : w.buf) * C::TILE + row_l * 128;
+            if (!two) {
+                // where the thread that reads them writes its first 16 bytes of output
+                auto ml_at = [&](int reader) -> uint32_t {
+                    const int ch = reader * (D / 16);
+                    return stage_row + (ch >> 3) * C::BLOCK + ((ch ^ row_l) & 7) * 16;
+                };
+                sts128u(ml_at(1 - grp), __float_as_uint(m), __float_as_uint(l), 0u, 0u);
+                (void)named_bar_and(1, 256, true);
+                const uint4 x = lds128(ml_at(grp));
+                mo = __uint_as_float(x.x);
+                lo = __uint_as_float(x.y);
+            }
             if (mine) ok = warp_wait(bar(bO + grp), n_o & 1);
             if (theirs) ok = ok && warp_wait(bar(bO + 1 - grp), n_oo & 1);
             tc_fence_after();
@@ -964,7 +998,6 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 // A whole item's output goes through q's buffer (the warp's own 32
                 // rows), so that the warp writes rows and not columns.
                 const int c0 = two ? 0 : grp * (D / 32), c1 = two ? D / 16 : c0 + D / 32;  // 16 columns each
-                const uint32_t stage_row = s0 + C::OFF_Q + (two ? grp : w.buf) * C::TILE + row_l * 128;
 #pragma unroll 1
                 for (int c = c0; c < c1; ++c) {
                     uint32_t x[16], y[16];
