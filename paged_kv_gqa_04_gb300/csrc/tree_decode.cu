@@ -49,7 +49,10 @@
 // and V meets both, as in the one-token decode; the scores' columns hold both.
 // One term: 64 contexts of 1 to 8192 82 us and not 92, 16 of 8 Ki with 64 drafted
 // tokens 141 and not 180, but outputs of weights near one another up to 11 times
-// their bound off. (FP8 caches: one f16 term, 2^-11.) The sums of the weights are
+// their bound off. FP8 caches: one f16 term of 2^7 P (<= 2^15), 2^-11 of it down to
+// weights of 2^-21 of the reference, 2^-32 of the reference below (P itself would
+// lose all weights below 2^-25 beside one dominant position: 0.03 of V after 2^20
+// others). The sums of the weights are
 // taken before the rounding, in fp32. For FP8 caches q is
 // scaled by a power of two per row into f16's range, which is exact for
 // every value within 2^29 of the row's largest.
@@ -133,6 +136,7 @@ struct Cfg {
     // 32 positions of P are 16 columns; bf16: those of the rounded rest beside those of the rounded term, the
     // columns of S that they were.
     static constexpr int TERMS = FP8 ? 1 : 2;
+    static constexpr float P_LOG2 = FP8 ? 7.f : 0.f;       // P and its sums are held times 2^this (P <= 2^15)
     static constexpr uint32_t P_COL = FP8 && D == 64 ? 192 : 0;
     static constexpr uint32_t O_COL = 128;
     static __device__ __forceinline__ constexpr uint32_t p_col(int k, int term) {  // of positions 16 k ..
@@ -856,7 +860,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                         m = nm;
                     }
                 }
-                const float mm = m == -INFINITY ? 0.f : -m;
+                const float mm = m == -INFINITY ? 0.f : C::P_LOG2 - m;
                 const float2 sl2 = make_float2(sl, sl), mm2 = make_float2(mm, mm);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
@@ -926,7 +930,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                             for (int d = 0; d < D; ++d)
                                 x += __uint_as_float(static_cast<uint32_t>(qr[d]) << 16) * at(a.k_cache, kb + d);
                             x *= a.scale_log2 * (FP8 ? __ldg(a.k_scale + (a.n_scale == 1 ? 0 : w.kvh)) : 1.f);
-                            x = fast_exp2(x - (m == -INFINITY ? 0.f : m));
+                            x = fast_exp2(x + mm);
                         }
 #pragma unroll 1
                         for (int c = 0; c < D / 16; ++c) {
@@ -977,7 +981,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             n_oo += two || nt > 1 - grp;
             if (speaker && ok && two) mbar_arrive(bar(bFree + stage(2 * (tile0 + nt) - 1)));  // the last V
             if (ok && warp_live) {
-                const float M = fmaxf(m, mo);
+                const float M = fmaxf(m, mo), M0 = M - C::P_LOG2;  // (M0: what P and its sums are relative to)
                 const float f0 = m == -INFINITY ? 0.f : fast_exp2(m - M), f1 = mo == -INFINITY ? 0.f : fast_exp2(mo - M);
                 const float sum = (mine ? l * f0 : 0.f) + (theirs ? lo * f1 : 0.f);
                 const bool whole = w.whole;
@@ -988,10 +992,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                 float* part = part_o<D>(a.workspace, gridDim.x, slot, row);
                 if (live && (two || grp == 0)) {
                     if (!whole) {
-                        *reinterpret_cast<float2*>(part_ml(a.workspace, slot, row)) = make_float2(M, sum);
+                        *reinterpret_cast<float2*>(part_ml(a.workspace, slot, row)) = make_float2(M0, sum);
                     } else if (a.lse) {
                         a.lse[(w.q0 + tok) * a.l_s0 + h * a.l_s1] =
-                            none ? -INFINITY : (M + __log2f(sum)) * 0.69314718055994530942f;
+                            none ? -INFINITY : (M0 + __log2f(sum)) * 0.69314718055994530942f;
                     }
                 }
                 // Two row tiles: all of this row's columns; else each group half of them.
