@@ -723,10 +723,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             float sl = fabsf(a.scale_log2), vs = 1.f;
             if constexpr (FP8) {
                 w.buffers([&](int bf, int uses) { ok = ok && warp_wait(bar(bQ + bf), uses & 1); });
-                sl *= __ldg(a.k_scale + (a.n_scale == 1 ? 0 : w.kvh)) * q_scale[128 * (two ? grp : w.buf) + row_l];
+                sl *= fabsf(__ldg(a.k_scale + (a.n_scale == 1 ? 0 : w.kvh))) * q_scale[128 * (two ? grp : w.buf) + row_l];
                 vs = __ldg(a.v_scale + (a.n_scale == 1 ? 0 : w.kvh));
             }
-            sl = fmaxf(sl, 1.2e-38f);                  // -inf times it stays -inf
+            sl = fmaxf(sl, 1.2e-38f);                  // -inf times it stays -inf (a scale that is no number: see q)
             const int L = w.L, ctx = w.ctx, t1 = w.t1, w_t0 = w.t0;
             const int32_t* table = a.block_tables + w.b * a.bt_s0;
             const int npages = (L + kPageSize - 1) / kPageSize;
@@ -1069,6 +1069,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
             if (!ok || w.b < 0) break;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(bPieceFree + i % kPieces));
+            // q takes the sign of k_scale, or its being no number, which then reaches the scores of the positions
+            // that a row sees (as a factor of the masked ones' -inf it would not leave them out)
+            const float ks = __ldg(a.k_scale + (a.n_scale == 1 ? 0 : w.kvh));
+            const float sign = ks != ks ? ks : copysignf(1.f, ks);
             w.buffers([&](int bf, int uses) {
                 ok = ok && warp_wait(bar(bQRaw + bf), uses & 1);
                 if (!ok) return;
@@ -1087,7 +1091,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::THREADS, 1)
                     for (int d = 1; d < QC; d <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, d));
                     int ex = static_cast<int>(mx >> 7);    // biased exponent
                     ex = ex == 255 ? 127 : max(ex, 20);    // not finite: stays so; tiny rows: 2^121
-                    const float up = __uint_as_float(static_cast<uint32_t>(127 + 141 - ex) << 23);
+                    const float up = sign * __uint_as_float(static_cast<uint32_t>(127 + 141 - ex) << 23);
                     if (ch == 0) q_scale[128 * bf + r] = __uint_as_float(static_cast<uint32_t>(127 + ex - 141) << 23);
                     sts128u(at, pack_f16(bf16_lo(v[0]) * up, bf16_hi(v[0]) * up), pack_f16(bf16_lo(v[1]) * up, bf16_hi(v[1]) * up),
                             pack_f16(bf16_lo(v[2]) * up, bf16_hi(v[2]) * up), pack_f16(bf16_lo(v[3]) * up, bf16_hi(v[3]) * up));

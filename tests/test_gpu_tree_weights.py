@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import paged_kv_gqa_04_gb300 as pkv
-from tests._spec import make_tree, run_tree
+from tests._spec import check_tree, make_tree, run_tree
 
 pytestmark = pytest.mark.gpu
 
@@ -177,3 +177,20 @@ def test_every_row_of_v_has_its_weight(dtype, drafts, Hq, Hkv, D, mask):
         # exact weights: half a step of the output, and the roundings of 1 / sum, the scale and the joining
         assert bool(((got - want).abs() <= (2.0 ** -8 + 2.0 ** -20) * want).all()), base
     assert int(s["err"].item()) == 0
+
+
+@pytest.mark.parametrize("per_head", [True, False])
+@pytest.mark.parametrize("bad", [float("nan"), -0.03])
+def test_k_scales_that_are_no_number_or_negative(bad, per_head):
+    """As in the decode step the scale multiplies the scores, whatever it is; rows that see nothing have none."""
+    s = make_tree([6, 700, 90], [6, 9, 40], 8, 2, 128, dtype="fp8", seed=34)
+    s["mask"][:6] = 0
+    x = s["v"].view(torch.uint8)
+    t = 700 - 9 + 3                                                         # a drafted token whose V is not finite
+    x[s["bt"][1, t // 16].long(), 1, t % 16, 5] = 0x7F
+    if per_head:
+        s["k_scale"][0] = bad
+    else:
+        s["k_scale"], s["v_scale"] = torch.tensor([bad], device="cuda"), s["v_scale"][:1].clone()
+    run_tree(s)
+    check_tree(s)
