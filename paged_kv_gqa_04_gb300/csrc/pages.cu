@@ -28,6 +28,7 @@
 // entries and raise their pages' counts. Bound by memory: 96 forks in 64 caches
 // of 16 KB pages (195 MB) take 20 us of the call's 26.
 #include <algorithm>
+#include <atomic>
 
 #include "pkv_internal.h"
 #include "pkv_ptx.cuh"
@@ -140,6 +141,8 @@ constexpr int kTakeThreads = 1024;
 constexpr int kTakeWarps = kTakeThreads / 32;
 static_assert(kTakeWarps == 32, "a warp reads the warps' sums, one per lane");
 constexpr int kMaxCluster = 16;
+// Pools that one CTA, and that four, look through; larger ones take 16.
+constexpr int64_t kSoloPages = 8192, kSmallPoolPages = 32768;
 constexpr int kKeptPages = 1024;           // pages of a warp whose free masks stay in a register
 constexpr uint32_t kDemandCap = 1u << 30;  // sums saturate here, above any pool
 
@@ -603,23 +606,54 @@ __global__ void __launch_bounds__(kShareThreads) share_kernel(const __grid_const
     if (bad) flag_error(a.err, PKV_FLAG_PAGE_RANGE);
 }
 
+// The CTAs of a take over a pool of so many pages, its kernel's attributes set:
+// before anything of the call is queued, so that a call that cannot be made leaves
+// the state as it is. The attributes are of the kernel, not of the call, and
+// another host thread may be about to launch it: always the same values.
+constexpr size_t kTakeSmemMax = (take_words(kMaxRows) + kTakeWarps * 128) * 4;
+
 template <bool FORK>
-cudaError_t launch_take(const TakeArgs& a, cudaStream_t s) {
-    // A CTA keeps the free masks of 32,768 pages in registers; larger pools are
-    // spread over a cluster (16 CTAs, the largest there is, is past the portable 8).
-    const unsigned C = a.num_pages <= 8192 ? 1 : a.num_pages <= 32768 ? 4 : kMaxCluster;
-    auto kern = C == 1 ? take_kernel<FORK, true> : take_kernel<FORK, false>;
-    const size_t smem = (take_words(a.n) + kTakeWarps * 128) * 4;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+cudaError_t plan_take(int64_t num_pages, unsigned* ctas) {
+    static std::atomic<unsigned> largest[64];              // per device: the largest cluster that fits, at most 16
+    *ctas = num_pages <= kSoloPages ? 1 : num_pages <= kSmallPoolPages ? 4 : kMaxCluster;
+    auto kern = *ctas == 1 ? take_kernel<FORK, true> : take_kernel<FORK, false>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kTakeSmemMax));
+    if (e != cudaSuccess || *ctas <= 8) return e;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    if (C > 8) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    unsigned C = dev < 64 ? largest[dev].load(std::memory_order_relaxed) : 0;
+    if (C == 0) {
+        // 16 CTAs are past the portable 8 and need not fit (part of a GPU, say)
+        cudaLaunchConfig_t cfg{};
+        cudaLaunchAttribute attr[1];
+        cfg.gridDim = dim3(kMaxCluster);
+        cfg.blockDim = dim3(kTakeThreads);
+        cfg.dynamicSmemBytes = kTakeSmemMax;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = kMaxCluster;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        C = cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0 ? kMaxCluster : 8;
+        if (C == 8) (void)cudaGetLastError();
+        if (dev < 64) largest[dev].store(C, std::memory_order_relaxed);
     }
+    *ctas = C;
+    return cudaSuccess;
+}
+
+template <bool FORK>
+cudaError_t launch_take(const TakeArgs& a, unsigned C, cudaStream_t s) {
+    auto kern = C == 1 ? take_kernel<FORK, true> : take_kernel<FORK, false>;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(C);
     cfg.blockDim = dim3(kTakeThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = (take_words(a.n) + kTakeWarps * 128) * 4;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -643,21 +677,26 @@ cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t s) {
 cudaError_t launch_resize(const TakeArgs& a0, cudaStream_t s) {
     if (a0.n == 0) return cudaSuccess;
     TakeArgs a = a0;
+    unsigned C = 0;
+    cudaError_t e = plan_take<false>(a.num_pages, &C);
+    if (e != cudaSuccess) return e;
     // With room for 64 Ki entries in the tables and more, the returns may be more
     // than the take's one cluster does quickly, and are worth a launch of their
     // own (4096 rows, 100 K entries returned and as many taken: 36 us a call in one
     // kernel, 30 in two).
     a.returned = static_cast<int64_t>(a.n) * a.max_pages >= 65536;
     if (a.returned) {
-        const cudaError_t e = launch_dependent(return_kernel, dim3((a.max_pages + kReturnSpan - 1) / kReturnSpan, (a.n + 7) / 8),
-                                               dim3(256), 0, s, a);
+        e = launch_dependent(return_kernel, dim3((a.max_pages + kReturnSpan - 1) / kReturnSpan, (a.n + 7) / 8), dim3(256), 0, s, a);
         if (e != cudaSuccess) return e;
     }
-    return launch_take<false>(a, s);
+    return launch_take<false>(a, C, s);
 }
 
 cudaError_t launch_fork_take(const TakeArgs& a, cudaStream_t s) {
-    return a.n == 0 ? cudaSuccess : launch_take<true>(a, s);
+    if (a.n == 0) return cudaSuccess;
+    unsigned C = 0;
+    const cudaError_t e = plan_take<true>(a.num_pages, &C);
+    return e != cudaSuccess ? e : launch_take<true>(a, C, s);
 }
 
 cudaError_t launch_fork_share(const ShareArgs& a0, int32_t n, int32_t max_pages, bool tables, cudaStream_t s) {

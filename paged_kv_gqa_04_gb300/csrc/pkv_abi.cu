@@ -1417,7 +1417,7 @@ pkv_status pkv_resize_sequences(const pkv_tensor* block_tables_p, const pkv_tens
     if ((st = check_i32(pc, B)) != PKV_OK || (st = check_i32(nl, B)) != PKV_OK) return st;
     if (pr.ndim != 1 || (st = check_i32(pr, pr.shape[0])) != PKV_OK) return st != PKV_OK ? st : PKV_ERR_INVALID_ARG;
     if (page_size < 1) return PKV_ERR_INVALID_ARG;
-    if (page_size > 65536 || B > 16384 || pr.shape[0] > (int64_t{1} << 27)) return PKV_ERR_UNSUPPORTED;
+    if (page_size > 65536 || B > pkv::kMaxRows || pr.shape[0] > (int64_t{1} << 27)) return PKV_ERR_UNSUPPORTED;
     pkv::TakeArgs a{};
     a.block_tables = static_cast<int32_t*>(bt.ptr);
     a.bt_s0 = bt.stride[0];
@@ -1458,7 +1458,7 @@ pkv_status pkv_fork_sequences(const pkv_tensor* caches, int32_t n_caches, int32_
             return PKV_ERR_UNSUPPORTED;
     }
     const int64_t n = fk.shape[0];
-    if (n > 16384) return PKV_ERR_UNSUPPORTED;
+    if (n > pkv::kMaxRows) return PKV_ERR_UNSUPPORTED;
     if (n == 0) return PKV_OK;
     if (overlap(fk, cp, 8 * n)) return PKV_ERR_INVALID_ARG;
     pkv::TakeArgs a{};

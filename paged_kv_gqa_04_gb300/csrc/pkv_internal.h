@@ -184,6 +184,7 @@ struct PoolPart {
 };
 constexpr int kMaxParts = 64;         // caches per launch (a larger set takes more launches)
 constexpr int kMaxAccepted = 1024;    // accepted tokens per sequence
+constexpr int kMaxRows = 16384;       // rows of a resize, forks of a call
 
 struct AcceptArgs {
     const int32_t* block_tables;

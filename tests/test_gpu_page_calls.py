@@ -1,0 +1,56 @@
+"""GPU tests of the page operators as programs use them: from several host
+threads, with pages that sequences share, and with the rotary positions of a
+tree of drafted tokens."""
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_gqa_04_gb300 as pkv
+from tests._spec import resize_reference
+
+pytestmark = pytest.mark.gpu
+
+
+def _i32(x):
+    return torch.from_numpy(np.ascontiguousarray(x, dtype=np.int32)).cuda()
+
+
+def test_two_host_threads_resize_batches_of_different_sizes():
+    """Two threads, a stream and a pool each: 16384 rows (the largest shared memory there is, returns by a kernel of
+    their own) and 3 rows, at the same time. No call fails, and both pools end as the calls one by one give."""
+    calls, failed = 2000, []
+
+    def state(B, width, pages, seed):
+        r = np.random.RandomState(seed)
+        lens = [r.randint(0, 16 * width + 1, B).astype(np.int32) for _ in range(2)]
+        bt, counts, refs = np.full((B, width), -1, np.int32), np.zeros(B, np.int32), np.zeros(pages, np.int32)
+        want = (bt, counts, refs)
+        d = [_i32(x) for x in want]
+        for x in lens:                     # every later pair of calls starts from the same counts
+            want = resize_reference(*want[:2], x, want[2], 16)[:3]
+        return d, [_i32(x) for x in lens], want
+
+    def work(d, lens, stream, err, gate):
+        try:
+            b = [pkv.bind(x) for x in d + lens + [err]]
+            gate.wait()
+            for i in range(calls):
+                pkv.resize_sequences(b[0], b[1], b[3 + i % 2], b[2], 16, err_flag=b[5], stream=stream)
+        except Exception as e:             # noqa: BLE001 (a failed call is what this looks for)
+            failed.append(repr(e))
+    sets = [state(16384, 4, 70000, 1), state(3, 4, 20000, 2)]
+    errs = [_i32([0]), _i32([0])]
+    torch.cuda.synchronize()
+    gate = threading.Barrier(2)
+    threads = [threading.Thread(target=work, args=(s[0], s[1], torch.cuda.Stream(), e, gate)) for s, e in zip(sets, errs)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    assert not failed, failed[0]
+    assert [int(e.item()) for e in errs] == [0, 0]
+    for d, lens, want in sets:
+        assert np.array_equal(d[1].cpu().numpy(), want[1])
+        held, refs = d[0][d[0] >= 0].cpu().numpy(), d[2].cpu().numpy()
+        assert np.array_equal(np.bincount(held, minlength=len(refs)), refs) and refs.max() == 1
