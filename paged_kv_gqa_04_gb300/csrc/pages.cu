@@ -555,6 +555,8 @@ __device__ void copy_bulk(uint8_t* dst, const uint8_t* src, uint32_t bytes, uint
     bulk_load(buf, src, bytes, bar, l2_policy_evict_first());
     if (!mbar_wait_bounded(bar, 0, 1000000000ull)) {
         flag_error(err, PKV_FLAG_WAIT_TIMEOUT);
+        // the copy under way lands, if it still does, before the CTA gives its shared memory back
+        (void)mbar_wait_bounded(bar, 0, 1000000000ull);
         return;
     }
     bulk_store(dst, buf, bytes);
