@@ -719,7 +719,7 @@ int64_t pkv_tree_decode_workspace(int64_t T, int32_t Hq, int32_t D, int32_t sm_c
  *              [B] int32; q_start [B+1] int32; accepted [B, A] int32,
  *              innermost stride 1, A <= 1024; entries past num_accepted are
  *              not read.
- * seq_lens_out [B] int32, not overlapping seq_lens.
+ * seq_lens_out [B] int32, overlapping none of the other arrays.
  * Errors: num_accepted outside [0, min(A, N_b)], indices that do not ascend
  * strictly within [0, N_b), and N_b outside [0, L] set PKV_FLAG_DRAFT_RANGE,
  * seq_lens outside [0, P*max_pages] sets PKV_FLAG_SEQ_LEN_RANGE (without

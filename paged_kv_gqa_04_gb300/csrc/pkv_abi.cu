@@ -1266,9 +1266,21 @@ static pkv_status check_tables(const pkv_tensor& t, int64_t* B, int64_t* max_pag
     return *max_pages > 1 && t.stride[1] != 1 ? PKV_ERR_UNSUPPORTED : PKV_OK;
 }
 
-static bool overlap(const pkv_tensor& x, const pkv_tensor& y, int64_t bytes) {
-    const uintptr_t p = reinterpret_cast<uintptr_t>(x.ptr), q = reinterpret_cast<uintptr_t>(y.ptr);
-    return p < q + static_cast<uintptr_t>(bytes) && q < p + static_cast<uintptr_t>(bytes);
+// The bytes from a tensor's first element to behind its last.
+static void extent(const pkv_tensor& t, intptr_t* lo, intptr_t* hi) {
+    *lo = *hi = reinterpret_cast<intptr_t>(t.ptr);
+    for (int i = 0; i < t.ndim; ++i) {
+        if (t.shape[i] == 0) return;
+        (t.stride[i] < 0 ? *lo : *hi) += (t.shape[i] - 1) * t.stride[i] * elem_bytes(t.dtype);
+    }
+    *hi += elem_bytes(t.dtype);
+}
+
+static bool overlap(const pkv_tensor& x, const pkv_tensor& y) {
+    intptr_t x0, x1, y0, y1;
+    extent(x, &x0, &x1);
+    extent(y, &y0, &y1);
+    return x0 < y1 && y0 < x1;
 }
 
 // One cache as rows to move: whole pages, or the rows of single tokens.
@@ -1375,7 +1387,9 @@ pkv_status pkv_accept_drafts(const pkv_tensor* caches, int32_t n_caches, int32_t
     if (B * A > 0 && !ac.ptr) return PKV_ERR_INVALID_ARG;
     if (A > pkv::kMaxAccepted || (A > 1 && ac.stride[1] != 1)) return PKV_ERR_UNSUPPORTED;
     if (B == 0) return PKV_OK;
-    if (overlap(sl, so, 4 * B)) return PKV_ERR_INVALID_ARG;
+    // (a sequence's other CTAs, and later launches, read these while or after its length is written)
+    for (const pkv_tensor* t : {&bt, &sl, &qs, &ac, &na})
+        if (overlap(*t, so)) return PKV_ERR_INVALID_ARG;
 
     pkv::AcceptArgs a{};
     a.block_tables = static_cast<const int32_t*>(bt.ptr);
@@ -1460,7 +1474,7 @@ pkv_status pkv_fork_sequences(const pkv_tensor* caches, int32_t n_caches, int32_
     const int64_t n = fk.shape[0];
     if (n > pkv::kMaxRows) return PKV_ERR_UNSUPPORTED;
     if (n == 0) return PKV_OK;
-    if (overlap(fk, cp, 8 * n)) return PKV_ERR_INVALID_ARG;
+    if (overlap(fk, cp)) return PKV_ERR_INVALID_ARG;
     pkv::TakeArgs a{};
     a.block_tables = static_cast<int32_t*>(bt.ptr);
     a.bt_s0 = bt.stride[0];

@@ -1,0 +1,33 @@
+"""CPU tests of further refusals of the drafted-token and page calls, before any
+CUDA work (fake, never dereferenced pointers)."""
+import pytest
+
+import paged_kv_gqa_04_gb300 as pkv
+from paged_kv_gqa_04_gb300 import _abi, _build
+from tests.test_abi_cpu import _t
+from tests.test_spec_cpu import _caches
+
+BAD, NO = _abi.PKV_ERR_INVALID_ARG, _abi.PKV_ERR_UNSUPPORTED
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return pkv.lib()
+
+
+@pytest.mark.parametrize("name", ["bt", "sl", "qs", "ac", "na"])
+@pytest.mark.parametrize("offset", [0, 4, -8])
+def test_accepted_lengths_go_over_no_input(lib, name, offset):
+    """Several CTAs read a sequence's inputs while one of them writes its new length."""
+    B, A = 3, 5
+    base = dict(bt=_t((B, 4), "i32", ptr=0x1000), sl=_t((B,), "i32", ptr=0x2000), qs=_t((B + 1,), "i32", ptr=0x3000),
+                ac=_t((B, A), "i32", ptr=0x4000, strides=(A + 3, 1)), na=_t((B,), "i32", ptr=0x5000))
+    caches = _caches(_t((10, 2, 16, 64), "bf16", ptr=0x100000))
+
+    def call(ptr):
+        return lib.pkv_accept_drafts(caches[0], caches[1], 1, base["bt"], base["sl"], base["qs"], base["ac"], base["na"],
+                                     _t((B,), "i32", ptr=ptr), None, None)
+    assert call(base[name].contents.ptr + offset) == BAD
+    last = {"bt": (B * 4 - 1) * 4, "sl": 8, "qs": 12, "ac": ((B - 1) * (A + 3) + A - 1) * 4, "na": 8}[name]
+    assert call(base[name].contents.ptr + last) == BAD
