@@ -714,7 +714,8 @@ int64_t pkv_tree_decode_workspace(int64_t T, int32_t Hq, int32_t D, int32_t sm_c
  *              (each layer's K, V, block scales, latents ...): 4-D as laid out
  *              by `layout` ([pages, P, H, W] or [pages, H, P, W]) or 3-D
  *              [pages, P, W], any pkv_dtype, innermost stride 1; all with the
- *              same number of pages and tokens per page P. No two may overlap.
+ *              same number of pages and tokens per page P, a page of at most
+ *              65535 * 16384 bytes. No two may overlap.
  * block_tables [B, max_pages] int32, innermost stride 1; seq_lens, num_accepted
  *              [B] int32; q_start [B+1] int32; accepted [B, A] int32,
  *              innermost stride 1, A <= 1024; entries past num_accepted are

@@ -1301,7 +1301,9 @@ static pkv_status pool_part(const pkv_tensor& t, int32_t layout, bool pages, int
         nh = t.shape[3 - tok];
         sh = t.stride[3 - tok] * e;
     }
-    if (row > (1 << 30) || nh > (1 << 30) || row * nh > (1 << 30) || row * nh * nt >= (1 << 30))
+    // (as many bytes as a grid of one CTA per 16 KB copies; units of them fit 32 bits)
+    constexpr int64_t kPageBytes = 65535 * int64_t{16384};
+    if (row > kPageBytes || nh > kPageBytes || row * nh > kPageBytes || row * nh * nt > kPageBytes)
         return PKV_ERR_UNSUPPORTED;
     if (nh == 1 || sh == row) {  // a token's heads are one row
         row *= nh;

@@ -31,3 +31,16 @@ def test_accepted_lengths_go_over_no_input(lib, name, offset):
     assert call(base[name].contents.ptr + offset) == BAD
     last = {"bt": (B * 4 - 1) * 4, "sl": 8, "qs": 12, "ac": ((B - 1) * (A + 3) + A - 1) * 4, "na": 8}[name]
     assert call(base[name].contents.ptr + last) == BAD
+
+
+def test_pages_past_what_one_grid_copies_are_refused(lib):
+    """A page in one piece is copied by CTAs of 16 KB, of which a grid has 65,535: a larger one would have been
+    found out only behind the call's first half."""
+    def call(nbytes):
+        page = _t((10, 16, nbytes // 16), "fp8", strides=(nbytes, nbytes // 16, 1))
+        c = _caches(page)
+        return lib.pkv_fork_sequences(c[0], c[1], 1, _t((4, 4), "i32"), _t((4,), "i32"), _t((4,), "i32"),
+                                      _t((0, 2), "i32"), _t((10,), "i32"), _t((0, 2), "i32"), None, None)
+    assert call(65535 * 16384) == _abi.PKV_OK
+    assert call(65535 * 16384 + 16) == NO
+    assert call((1 << 30) - 16) == NO
