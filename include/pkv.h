@@ -791,8 +791,8 @@ pkv_status pkv_resize_sequences(const pkv_tensor* block_tables, const pkv_tensor
  * copies       [n, 2] int32 (strides 2, 1), out: the (source, destination)
  *              page of fork i; (-1, -1) when its length needs no copy, (-2,
  *              -2) when the fork was not made.
- * Errors: rows outside [0, R), a child that holds pages or is named by an
- * earlier fork set PKV_FLAG_PAGE_STATE; a parent whose length its pages do
+ * Errors: rows outside [0, R), a child whose page_counts is not 0 or that is
+ * named by an earlier fork set PKV_FLAG_PAGE_STATE; a parent whose length its pages do
  * not hold sets PKV_FLAG_SEQ_LEN_RANGE; a last page outside [0, num_pages)
  * sets PKV_FLAG_PAGE_RANGE: that fork is not made. When the free pages run
  * out, the forks from there on that need one are not made

@@ -368,13 +368,16 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
                 }
         }
     } else {
-        // A child's count of 0 becomes a claim: -(n - i) of its first fork i
-        // (the lowest value stays). Every CTA makes the same claims.
+        // A child's count of 0 becomes a claim: kClaim + i of its first fork i (the
+        // lowest value stays). Every CTA makes the same claims, and none takes
+        // another's for a count: those start where the claims end.
+        constexpr int kClaim = INT32_MIN;
+        auto no_child = [&](int count) { return count > 0 || (count < 0 && count >= kClaim + n); };
         for (int i = tid; i < n; i += kTakeThreads) {
             const int p = a.forks[2 * i], c = a.forks[2 * i + 1];
             int L = -1, src = -1;
             if (p >= 0) {
-                if (p >= a.rows || c < 0 || c >= a.rows || a.page_counts[c] > 0) {
+                if (p >= a.rows || c < 0 || c >= a.rows || no_child(a.page_counts[c])) {
                     flags |= PKV_FLAG_PAGE_STATE;
                 } else {
                     const int x = a.seq_lens[p];
@@ -387,7 +390,7 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
                             flags |= PKV_FLAG_PAGE_RANGE;
                         } else {
                             L = x;
-                            atomicMin(a.page_counts + c, -(n - i));
+                            atomicMin(a.page_counts + c, kClaim + i);
                         }
                     }
                 }
@@ -397,7 +400,7 @@ __global__ void __launch_bounds__(kTakeThreads) take_kernel(const __grid_constan
         }
         cluster_barrier<SOLO>();
         for (int i = tid; i < n; i += kTakeThreads) {
-            if (held[i] >= 0 && __ldcg(a.page_counts + a.forks[2 * i + 1]) != -(n - i)) {
+            if (held[i] >= 0 && __ldcg(a.page_counts + a.forks[2 * i + 1]) != kClaim + i) {
                 flags |= PKV_FLAG_PAGE_STATE;  // an earlier fork has this child
                 held[i] = -1;
                 tail[i] = -1;

@@ -54,3 +54,25 @@ def test_two_host_threads_resize_batches_of_different_sizes():
         assert np.array_equal(d[1].cpu().numpy(), want[1])
         held, refs = d[0][d[0] >= 0].cpu().numpy(), d[2].cpu().numpy()
         assert np.array_equal(np.bincount(held, minlength=len(refs)), refs) and refs.max() == 1
+
+
+@pytest.mark.parametrize("pages", [40, 9000, 40000])
+@pytest.mark.parametrize("count", [-1, -2, -5, -16384, -16385, -2 ** 31 + 16384])
+def test_children_with_negative_page_counts_are_refused(count, pages):
+    """page_counts[child] has to be 0; others are a contradiction, alike for all numbers of forks and CTAs. A row
+    that is refused stays as it is, and so does its parent."""
+    bt, lens = _i32([[3, 4], [-1, -1], [-1, -1], [-1, -1]]), _i32([20, 0, 0, 0])
+    counts, refs, err = _i32([2, count, 0, count]), torch.zeros(pages, dtype=torch.int32, device="cuda"), _i32([0])
+    refs[3:5] = 1
+    cache = torch.randn((pages, 1, 16, 8), device="cuda")
+    before = cache.clone()
+    forks, copies = _i32([[0, 1], [0, 2], [0, 3], [0, 3]]), _i32(np.zeros((4, 2)))
+    pkv.fork_sequences([cache], bt, counts, lens, forks, refs, copies, err_flag=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == pkv.FLAG_PAGE_STATE
+    assert counts.tolist() == [2, count, 2, count] and lens.tolist() == [20, 0, 20, 0]
+    assert copies.tolist() == [[-2, -2], [4, 0], [-2, -2], [-2, -2]]
+    assert bt.tolist() == [[3, 4], [-1, -1], [3, 0], [-1, -1]]
+    before[0] = before[4]
+    assert torch.equal(cache, before)
+    assert refs[:5].tolist() == [1, 0, 0, 2, 1] and int(refs.sum()) == 4
