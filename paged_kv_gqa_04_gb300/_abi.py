@@ -123,7 +123,7 @@ def status_string(status: int) -> str:
 class Bound:
     """A tensor, or a list of tensors, with its descriptors made once (see
     bind). Keeps the tensors alive."""
-    __slots__ = ("tensors", "ptr", "n", "data", "nbytes", "device")
+    __slots__ = ("tensors", "ptr", "n", "data", "nbytes", "device", "_other")
 
     def __init__(self, tensors, ptr, n: int):
         self.tensors, self.ptr, self.n = tensors, ptr, n
@@ -131,6 +131,25 @@ class Bound:
         self.data = first.data_ptr() if first is not None else None
         self.nbytes = first.numel() * first.element_size() if first is not None else 0
         self.device = first.get_device() if first is not None else None
+        self._other = None
+
+    def tensor(self) -> torch.Tensor:
+        if self.n != 1:
+            raise TypeError("a bound list of tensors where one tensor is expected")
+        return self.tensors[0]
+
+    def as_dtype(self, dtype: int):
+        """The descriptor under another pkv_dtype (the one that _desc's `dtype` gives), made once too."""
+        self.tensor()
+        if self._other is None or self._other.contents.dtype != dtype:
+            d = PkvTensor.from_buffer_copy(self.ptr.contents)
+            d.dtype = dtype
+            self._other = ctypes.pointer(d)
+        return self._other
+
+
+def _tensor(t):
+    return t.tensor() if isinstance(t, Bound) else t
 
 
 def bind(t):
@@ -169,7 +188,7 @@ def _desc(t, dtype: Optional[int] = None):
         return None
     if isinstance(t, Bound):
         if dtype is not None:
-            raise TypeError("NVFP4 value caches are passed as tensors, not bound")
+            return t.as_dtype(dtype)
         if t.n != 1:
             raise TypeError("a bound list of tensors where one tensor is expected")
         return t.ptr
@@ -228,7 +247,7 @@ def paged_gqa_decode(q, k_cache, v_cache, block_tables, seq_lens, softmax_scale:
 
 
 def _fp4(t):
-    if t is not None and t.dtype != torch.uint8:
+    if t is not None and _tensor(t).dtype != torch.uint8:
         raise TypeError("NVFP4 value caches are uint8 tensors of packed E2M1 pairs")
     return _desc(t, PKV_FP4_E2M1X2)
 
@@ -448,6 +467,7 @@ def validate_indices_static(block_tables, seq_lens, slot_mapping, num_pages: int
 def selftest_bounded_wait(limit_ns: int, err_flag: torch.Tensor, elapsed_ns: torch.Tensor, stream=None) -> None:
     """Self-test of the bounded in-kernel waits (pkv_selftest_bounded_wait):
     err_flag an int32 device word, elapsed_ns two int64 device words."""
+    err_flag, elapsed_ns = _tensor(err_flag), _tensor(elapsed_ns)
     if not (err_flag.is_cuda and err_flag.dtype == torch.int32 and elapsed_ns.is_cuda
             and elapsed_ns.dtype == torch.int64 and elapsed_ns.numel() >= 2):
         raise ValueError("int32 device flag and two int64 device words expected")
@@ -459,6 +479,7 @@ def copy(dst: torch.Tensor, src: torch.Tensor, stream=None) -> None:
     """pkv_copy: dst <- src byte for byte by the SMs; each a contiguous tensor
     in device memory or in pinned host memory (e.g. from pin_memory()), the
     same number of bytes."""
+    dst, src = _tensor(dst), _tensor(src)
     if not (dst.is_contiguous() and src.is_contiguous()):
         raise ValueError("copy: dst and src must be contiguous")
     n = src.numel() * src.element_size()
@@ -470,6 +491,7 @@ def copy(dst: torch.Tensor, src: torch.Tensor, stream=None) -> None:
 def stream_read(buf: torch.Tensor, sink: torch.Tensor, stream=None) -> None:
     """Streaming-read ceiling (pkv_stream_read): read all of `buf` once in
     one launch of sink.numel() CTAs."""
+    buf, sink = _tensor(buf), _tensor(sink)
     if not (buf.is_cuda and sink.is_cuda and sink.dtype == torch.int32):
         raise ValueError("device buffer and int32 device sink expected")
     _check("pkv_stream_read", lib().pkv_stream_read(buf.data_ptr(), buf.numel() * buf.element_size(),

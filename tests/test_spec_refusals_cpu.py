@@ -1,6 +1,9 @@
 """CPU tests of further refusals of the drafted-token and page calls, before any
 CUDA work (fake, never dereferenced pointers)."""
+import ctypes
+
 import pytest
+import torch
 
 import paged_kv_gqa_04_gb300 as pkv
 from paged_kv_gqa_04_gb300 import _abi, _build
@@ -44,3 +47,18 @@ def test_pages_past_what_one_grid_copies_are_refused(lib):
     assert call(65535 * 16384) == _abi.PKV_OK
     assert call(65535 * 16384 + 16) == NO
     assert call((1 << 30) - 16) == NO
+
+
+def test_bound_nvfp4_values_have_their_descriptor():
+    """bind() cannot know that uint8 values are pairs of E2M1; the NVFP4 calls say so."""
+    x = torch.zeros((2, 3, 16, 32), dtype=torch.uint8)
+    desc = _t(tuple(x.shape), "fp8", ptr=0x4000)
+    b = _abi.Bound([x], desc, 1)
+    d = _abi._fp4(b).contents
+    assert d.dtype == _abi.PKV_FP4_E2M1X2 and d.ptr == 0x4000 and list(d.shape) == [2, 3, 16, 32]
+    assert list(d.stride) == list(desc.contents.stride) and desc.contents.dtype == 1
+    assert ctypes.addressof(_abi._fp4(b).contents) == ctypes.addressof(d)   # made once
+    with pytest.raises(TypeError, match="uint8"):
+        _abi._fp4(_abi.Bound([x.float()], desc, 1))
+    with pytest.raises(TypeError, match="list"):
+        _abi._fp4(_abi.Bound([x, x], desc, 2))
