@@ -129,7 +129,8 @@ class Bound:
         self.tensors, self.ptr, self.n = tensors, ptr, n
         first = tensors[0] if tensors else None
         self.data = first.data_ptr() if first is not None else None
-        self.nbytes = first.numel() * first.element_size() if first is not None else 0
+        # (as a workspace: None where the elements are not one stretch of memory)
+        self.nbytes = 0 if first is None else first.numel() * first.element_size() if first.is_contiguous() else None
         self.device = first.get_device() if first is not None else None
         self._other = None
 
@@ -380,6 +381,20 @@ def lse_merge_planned(out_partial, lse_partial, splits_per_seq, out, lse_out=Non
         _desc(out_partial), _desc(lse_partial), _desc(splits_per_seq), _desc(out), _desc(lse_out), _stream(stream)))
 
 
+def _workspace(t):
+    """Address and bytes of a workspace."""
+    if t is None:
+        return None, 0
+    if isinstance(t, Bound):
+        t.tensor()
+        ptr, nbytes = t.data, t.nbytes
+    else:
+        ptr, nbytes = t.data_ptr(), t.numel() * t.element_size() if t.is_contiguous() else None
+    if nbytes is None:
+        raise ValueError("a workspace is a contiguous tensor")
+    return ptr, nbytes
+
+
 def tree_decode_workspace(T: int, Hq: int, D: int, sm_count: int) -> int:
     """Bytes of workspace that paged_tree_decode needs for T rows of q."""
     return int(lib().pkv_tree_decode_workspace(int(T), Hq, D, sm_count))
@@ -395,12 +410,7 @@ def paged_tree_decode(q, k_cache, v_cache, block_tables, seq_lens, q_start, tree
     workspace: a contiguous device tensor of tree_decode_workspace() bytes."""
     _on_current_device(q, k_cache, v_cache, block_tables, seq_lens, q_start, tree_mask, out, lse_out, workspace,
                        k_scale, v_scale, err_flag)
-    if workspace is None:
-        ws, nbytes = None, 0
-    elif isinstance(workspace, Bound):
-        ws, nbytes = workspace.data, workspace.nbytes
-    else:
-        ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    ws, nbytes = _workspace(workspace)
     _check("pkv_paged_tree_decode", lib().pkv_paged_tree_decode(
         _desc(q), _desc(k_cache), _desc(v_cache), _desc(block_tables), _desc(seq_lens), _desc(q_start),
         _desc(tree_mask), softmax_scale, _desc(out), _desc(lse_out), ws, nbytes, _desc(k_scale), _desc(v_scale),

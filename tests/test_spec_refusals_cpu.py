@@ -62,3 +62,15 @@ def test_bound_nvfp4_values_have_their_descriptor():
         _abi._fp4(_abi.Bound([x.float()], desc, 1))
     with pytest.raises(TypeError, match="list"):
         _abi._fp4(_abi.Bound([x, x], desc, 2))
+
+
+@pytest.mark.parametrize("bound", [False, True])
+def test_a_workspace_is_as_large_as_its_memory(bound):
+    """An expanded tensor has more elements than bytes behind them, and a strided one does not own all of its span."""
+    make = (lambda x: _abi.Bound([x], None, 1)) if bound else (lambda x: x)
+    x = torch.zeros(64, dtype=torch.uint8)
+    assert _abi._workspace(make(x)) == (x.data_ptr(), 64)
+    assert _abi._workspace(None) == (None, 0)
+    for bad in (torch.zeros(1).expand(1 << 20), torch.zeros(8, 8)[:, ::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            _abi._workspace(make(bad))
