@@ -422,7 +422,7 @@ def accept_drafts(caches, block_tables, seq_lens, q_start, accepted, num_accepte
     """Moves the accepted drafted tokens' rows together behind the context, in
     every cache of the list `caches`, and writes the new lengths
     (pkv_accept_drafts)."""
-    caches = bind(caches)
+    caches = bind([] if caches is None else caches)
     _on_current_device(caches, block_tables, seq_lens, q_start, accepted, num_accepted, seq_lens_out, err_flag)
     _check("pkv_accept_drafts", lib().pkv_accept_drafts(
         caches.ptr, caches.n, LAYOUTS[layout], _desc(block_tables), _desc(seq_lens), _desc(q_start), _desc(accepted),
@@ -445,7 +445,7 @@ def fork_sequences(caches, block_tables, page_counts, seq_lens, forks, page_refs
     """Makes row forks[i][1] continue row forks[i][0]: full pages shared, the
     partial last page copied in every cache of the list `caches`; copies [n,2]
     receives the copied pages (pkv_fork_sequences)."""
-    caches = bind(caches)
+    caches = bind([] if caches is None else caches)
     _on_current_device(caches, block_tables, page_counts, seq_lens, forks, page_refs, copies, err_flag)
     _check("pkv_fork_sequences", lib().pkv_fork_sequences(
         caches.ptr, caches.n, LAYOUTS[layout], _desc(block_tables), _desc(page_counts), _desc(seq_lens), _desc(forks),

@@ -74,3 +74,14 @@ def test_a_workspace_is_as_large_as_its_memory(bound):
     for bad in (torch.zeros(1).expand(1 << 20), torch.zeros(8, 8)[:, ::2]):
         with pytest.raises(ValueError, match="contiguous"):
             _abi._workspace(make(bad))
+
+
+def test_no_caches_may_be_none(lib, monkeypatch):
+    """accept_drafts(None, ...) is accept_drafts([], ...), as a null pointer is in C."""
+    seen = []
+    monkeypatch.setattr(_abi, "_on_current_device", lambda *a: None)
+    monkeypatch.setattr(_abi, "_stream", lambda s: None)
+    monkeypatch.setattr(_abi, "lib", lambda: type("L", (), {"pkv_accept_drafts": lambda *a: seen.append(a[1:3]) or 0}))
+    for caches in (None, []):
+        _abi.accept_drafts(caches, None, None, None, None, None, None)
+    assert seen == [(0, 1), (0, 1)]
