@@ -626,8 +626,8 @@ pkv_status pkv_selftest_bounded_wait(int64_t limit_ns, int32_t* err_flag, uint64
  * prompt, or let the device hand out the pages of its cache.)
  *
  *   pkv_resize_sequences   pages for the tokens to come (or back to the pool)
- *   pkv_rope_kv_write      the drafted tokens' k and v, at the positions
- *                          behind the context
+ *   pkv_rope_kv_write      the drafted tokens' k and v, in the slots behind
+ *                          the context
  *   pkv_paged_tree_decode  attention of all drafted tokens in one call
  *   pkv_accept_drafts      the accepted path's rows moved together, the new
  *                          lengths
@@ -636,6 +636,13 @@ pkv_status pkv_selftest_bounded_wait(int64_t limit_ns, int32_t* err_flag, uint64
  * All of them read every input on the device (lengths, block tables, drafted
  * and accepted tokens), so a whole step can be captured into a CUDA graph and
  * replayed while the lengths change.
+ *
+ * Drafted token j of a sequence with base tokens of context lies in the cache
+ * at position base + j (its slot), and is rotated at base + depth(j), depth(j)
+ * being the number of drafted tokens above it in its tree: the position that
+ * it has if its path is accepted (positions of pkv_rope_kv_write, for q and
+ * k). pkv_accept_drafts moves k as it was rotated, so a path then lies in the
+ * cache as if it had been written token by token. In a chain depth(j) = j.
  */
 
 /*
@@ -706,7 +713,8 @@ int64_t pkv_tree_decode_workspace(int64_t T, int32_t Hq, int32_t D, int32_t sm_c
  * positions base + j, base = seq_lens[b] - N_b, and n = num_accepted[b]:
  *   cache row (base + j) <- cache row (base + accepted[b][j])   for j < n,
  *   seq_lens_out[b] = base + n.
- * The accepted indices ascend strictly, so a row is read before it is
+ * The accepted indices ascend strictly (a path from the tree's top down, where
+ * every token's index is above its parent's), so a row is read before it is
  * overwritten; rows behind base + n - 1 keep what the moves left there.
  *
  * caches,

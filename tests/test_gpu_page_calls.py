@@ -76,3 +76,71 @@ def test_children_with_negative_page_counts_are_refused(count, pages):
     before[0] = before[4]
     assert torch.equal(cache, before)
     assert refs[:5].tolist() == [1, 0, 0, 2, 1] and int(refs.sum()) == 4
+
+
+@pytest.mark.parametrize("layout", ["HND", "NHD"])
+def test_accepted_path_of_a_tree_is_what_one_token_at_a_time_leaves(layout):
+    """Drafted token j of a tree is rotated at base + its depth (the position it has if its path is accepted) and
+    stored at base + j. Every row's attention is then that of its path written token by token, and the cache
+    behind an accepted path is byte for byte what those writes leave."""
+    Hq, Hkv, D, base, pages = 8, 2, 128, 37, 6
+    parent = [-1, -1, 0, 0, 2, 1, 2, 6, 3, 7]             # ten drafted tokens; -1 hangs below the context
+    N = len(parent)
+    depth = []
+    for p in parent:
+        depth.append(depth[p] + 1 if p >= 0 else 0)
+
+    def path(j):
+        return path(parent[j]) + [j] if j >= 0 else []
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+
+    def rnd(*s):
+        return torch.randn(s, generator=g, device="cuda").bfloat16()
+    q, k, v = rnd(N, Hq, D), rnd(base + N, Hkv, D), rnd(base + N, Hkv, D)   # the context's k and v, then the drafts'
+    cs, err = torch.randn((64, D), generator=g, device="cuda"), _i32([0])
+    shape = (pages, Hkv, 16, D) if layout == "HND" else (pages, 16, Hkv, D)
+    table = np.array([4, 1, 5, 0], np.int32)
+
+    def cache_of(rows, positions, stored, q=None):
+        kc, vc = torch.zeros(shape, device="cuda").bfloat16(), torch.zeros(shape, device="cuda").bfloat16()
+        slots = table[np.array(stored) // 16] * 16 + np.array(stored) % 16
+        pkv.rope_kv_write(None, k[rows], v[rows], _i32(positions), cs, kc, vc, _i32(slots), layout=layout, err_flag=err)
+        return kc, vc
+    ctx = list(range(base))
+    kc, vc = cache_of(ctx + [base + j for j in range(N)], ctx + [base + d for d in depth], ctx + [base + j for j in range(N)])
+    qr = q.clone()
+    scratch = [torch.zeros(shape, device="cuda").bfloat16() for _ in range(2)]
+    pkv.rope_kv_write(qr, k[base:], v[base:], _i32([base + d for d in depth]), cs, *scratch,
+                      _i32(np.arange(N)), layout=layout, err_flag=err)
+    bits = [sum(1 << x for x in path(j)) for j in range(N)]
+    out, lse = torch.zeros_like(q), torch.zeros((N, Hq), device="cuda")
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    ws = torch.empty(pkv.tree_decode_workspace(N, Hq, D, sms), dtype=torch.uint8, device="cuda")
+    bt = _i32(table[None])
+    pkv.paged_tree_decode(qr, kc, vc, bt, _i32([base + N]), _i32([0, N]), _i32(np.array(bits)[:, None]), D ** -0.5, out, lse,
+                          ws, layout=layout, err_flag=err)
+    for j in range(N):
+        p = path(j)
+        L = base + len(p)
+        ks, vs = cache_of(ctx + [base + x for x in p], list(range(L)), list(range(L)))
+        op, lp = torch.empty((1, 2, Hq, D), device="cuda"), torch.empty((1, 2, Hq), device="cuda")
+        o1, l1 = torch.empty((1, Hq, D), device="cuda").bfloat16(), torch.empty((1, Hq), device="cuda")
+        pkv.paged_gqa_decode(qr[j:j + 1], ks, vs, bt, _i32([L]), D ** -0.5, 2, op, lp, layout=layout, err_flag=err)
+        pkv.lse_merge(op, lp, o1, l1)
+        # the same scores and weights but for the order of fp32 sums and 2^-16 of a weight (|v| < 5); then either
+        # output is within half a step of bf16 of its value
+        d = (out[j] - o1[0]).double().abs()
+        assert bool((d <= 2 * 2.0 ** -8 * o1[0].double().abs() + 5 * 2.0 ** -13).all())
+        assert bool(((lse[j] - l1[0]).abs() <= 2.0 ** -14).all())
+        # the path accepted: in a copy of the cache, its rows moved together
+        kj, vj, new = kc.clone(), vc.clone(), _i32([0])
+        pkv.accept_drafts([kj, vj], bt, _i32([base + N]), _i32([0, N]), _i32([p]), _i32([len(p)]), new, layout=layout,
+                          err_flag=err)
+        assert new.tolist() == [L]
+        for a, b in ((kj, ks), (vj, vs)):
+            for t in range(L):
+                page, off = int(table[t // 16]), t % 16
+                x, y = (a[page, :, off], b[page, :, off]) if layout == "HND" else (a[page, off], b[page, off])
+                assert torch.equal(x, y), (j, t)
+    assert int(err.item()) == 0
