@@ -757,6 +757,11 @@ pkv_status pkv_accept_drafts(const pkv_tensor* caches, int32_t n_caches, int32_t
  * lowered, the entries set to -1), missing ones are taken from the pool (their
  * counts set to 1). All returns come before the first page is taken.
  * new_lens[b] = 0 frees a sequence, < 0 leaves it as it is.
+ * A row that was forked may be trimmed below the length it had then. If that
+ * ends inside a page which other rows name (a count above 1), its next token
+ * must not be written there: it would change their tokens too. Continue it as
+ * a fork of itself instead, into a row without pages (which gets a copy of
+ * that page), and free the old row.
  *
  * block_tables [B, max_pages] int32, innermost stride 1, updated; page_counts
  *              [B] int32, updated; new_lens [B] int32; page_refs [num_pages]
@@ -779,8 +784,8 @@ pkv_status pkv_resize_sequences(const pkv_tensor* block_tables, const pkv_tensor
  * pkv_fork_sequences -- sequences that continue others. For every fork i =
  * (parent, child), rows of the block table, with L = seq_lens[parent]:
  *   - the child's first floor(L / P) entries name the parent's pages, whose
- *     counts rise by one (full pages are never written again, so they are
- *     shared);
+ *     counts rise by one (shared: a full page is not written again, unless
+ *     a row is trimmed below it, see pkv_resize_sequences);
  *   - when L % P != 0 the child gets the lowest free page for entry
  *     floor(L / P), and that page becomes a copy of the parent's page, in
  *     every given cache;

@@ -144,3 +144,26 @@ def test_accepted_path_of_a_tree_is_what_one_token_at_a_time_leaves(layout):
                 x, y = (a[page, :, off], b[page, :, off]) if layout == "HND" else (a[page, off], b[page, off])
                 assert torch.equal(x, y), (j, t)
     assert int(err.item()) == 0
+
+
+def test_a_row_trimmed_into_a_shared_page_goes_on_as_a_fork():
+    """A trim below the fork point leaves a row whose last page another one still reads. A fork of it gets a page of
+    its own for the tokens to come, and the other sequence's tokens stay."""
+    pages, err = 12, _i32([0])
+    cache = torch.randn((pages, 1, 16, 8), device="cuda")
+    bt, counts, lens = _i32(np.full((4, 4), -1)), _i32([0] * 4), _i32([40, 0, 0, 0])
+    refs, copies = torch.zeros(pages, dtype=torch.int32, device="cuda"), _i32(np.zeros((1, 2)))
+    pkv.resize_sequences(bt, counts, _i32([40, -1, -1, -1]), refs, 16, err_flag=err)
+    pkv.fork_sequences([cache], bt, counts, lens, _i32([[0, 1]]), refs, copies, err_flag=err)
+    assert bt[:2].tolist() == [[0, 1, 2, -1], [0, 1, 3, -1]] and refs[:4].tolist() == [2, 2, 1, 1]
+    # row 0 back to 20 tokens, in the middle of page 1, which row 1 reads: it goes on as row 2
+    pkv.resize_sequences(bt, counts, _i32([20, -1, -1, -1]), refs, 16, err_flag=err)
+    lens[0] = 20
+    assert bt[0].tolist() == [0, 1, -1, -1] and refs[:4].tolist() == [2, 2, 0, 1]
+    pkv.fork_sequences([cache], bt, counts, lens, _i32([[0, 2]]), refs, copies, err_flag=err)
+    pkv.resize_sequences(bt, counts, _i32([0, -1, 33, -1]), refs, 16, err_flag=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and copies.tolist() == [[1, 2]]
+    assert bt.tolist() == [[-1] * 4, [0, 1, 3, -1], [0, 2, 4, -1], [-1] * 4]
+    assert refs[:5].tolist() == [2, 1, 1, 1, 1] and counts.tolist() == [0, 3, 3, 0] and lens.tolist() == [20, 40, 20, 0]
+    assert torch.equal(cache[2], cache[1])                # tokens 16 .. 19 of row 2 (and what lies behind them)
