@@ -242,8 +242,9 @@ __device__ __forceinline__ int pages_wanted(const TakeArgs& a, int have, int len
     return have;
 }
 
-// Returns of a large batch, by all SMs: a warp takes 256 entries of a row. The
-// counts of entries stay as they are for the take behind it.
+// Returns of a large batch, by all SMs: a warp takes 256 entries of a row at a
+// time, every gridDim.x-th such stretch. The counts of entries stay as they are
+// for the take behind it.
 constexpr int kReturnSpan = 256;
 __global__ void __launch_bounds__(256) return_kernel(const __grid_constant__ TakeArgs a) {
     grid_dep_wait();  // (the table is an index input: no early trigger, but for the take, which waits)
@@ -253,30 +254,32 @@ __global__ void __launch_bounds__(256) return_kernel(const __grid_constant__ Tak
     int flags = 0;
     const int have = a.page_counts[b], want = pages_wanted(a, have, a.new_lens[b], flags);
     flags = 0;  // the take reports them
-    const int j0 = max(want, static_cast<int>(blockIdx.x) * kReturnSpan);
-    const int j1 = min(have, static_cast<int>(blockIdx.x + 1) * kReturnSpan);
-    int page[kReturnSpan / 32], old[kReturnSpan / 32];
+    for (int64_t j0 = want + static_cast<int64_t>(blockIdx.x) * kReturnSpan; j0 < have; j0 += static_cast<int64_t>(gridDim.x) * kReturnSpan) {
+        int32_t* entry = a.block_tables + b * a.bt_s0 + j0;
+        const int m = static_cast<int>(min(static_cast<int64_t>(kReturnSpan), have - j0));
+        int page[kReturnSpan / 32], old[kReturnSpan / 32];
 #pragma unroll
-    for (int k = 0; k < kReturnSpan / 32; ++k) {
-        const int j = j0 + lane + 32 * k;
-        page[k] = -2;
-        if (j < j1) {
-            page[k] = a.block_tables[b * a.bt_s0 + j];
-            a.block_tables[b * a.bt_s0 + j] = -1;
-            if (page[k] < 0 || page[k] >= a.num_pages) {
-                flags |= PKV_FLAG_PAGE_RANGE;
-                page[k] = -2;
+        for (int k = 0; k < kReturnSpan / 32; ++k) {
+            const int j = lane + 32 * k;
+            page[k] = -2;
+            if (j < m) {
+                page[k] = entry[j];
+                entry[j] = -1;
+                if (page[k] < 0 || page[k] >= a.num_pages) {
+                    flags |= PKV_FLAG_PAGE_RANGE;
+                    page[k] = -2;
+                }
             }
         }
+#pragma unroll
+        for (int k = 0; k < kReturnSpan / 32; ++k) old[k] = page[k] >= 0 ? atomicSub(a.page_refs + page[k], 1) : 1;
+#pragma unroll
+        for (int k = 0; k < kReturnSpan / 32; ++k)
+            if (old[k] <= 0) {
+                atomicAdd(a.page_refs + page[k], 1);
+                flags |= PKV_FLAG_PAGE_STATE;
+            }
     }
-#pragma unroll
-    for (int k = 0; k < kReturnSpan / 32; ++k) old[k] = page[k] >= 0 ? atomicSub(a.page_refs + page[k], 1) : 1;
-#pragma unroll
-    for (int k = 0; k < kReturnSpan / 32; ++k)
-        if (old[k] <= 0) {
-            atomicAdd(a.page_refs + page[k], 1);
-            flags |= PKV_FLAG_PAGE_STATE;
-        }
     if (flags) flag_error(a.err, flags);
 }
 
@@ -687,11 +690,20 @@ cudaError_t launch_resize(const TakeArgs& a0, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     // With room for 64 Ki entries in the tables and more, the returns may be more
     // than the take's one cluster does quickly, and are worth a launch of their
-    // own (4096 rows, 100 K entries returned and as many taken: 36 us a call in one
-    // kernel, 30 in two).
+    // own: their number is known on the device alone. A trim and a growth, captured,
+    // us a pair in one kernel and in two: 256 rows of 2048 entries that change by a
+    // page 12.4 and 13.6, by 500 pages 27 and 21; 4096 rows of 100 entries, by a
+    // page 35.4 and 34.6, by 50 57 and 41.
     a.returned = static_cast<int64_t>(a.n) * a.max_pages >= 65536;
     if (a.returned) {
-        e = launch_dependent(return_kernel, dim3((a.max_pages + kReturnSpan - 1) / kReturnSpan, (a.n + 7) / 8), dim3(256), 0, s, a);
+        // One warp per row, and as many more as four CTAs per SM leave room for:
+        // a grid for the tables' width was 131,072 CTAs for 4096 rows of 65,536
+        // entries, whatever is returned.
+        int sms = 0;
+        e = device_sm_count(&sms);
+        if (e != cudaSuccess) return e;
+        const int rows = (a.n + 7) / 8, spans = (a.max_pages + kReturnSpan - 1) / kReturnSpan;
+        e = launch_dependent(return_kernel, dim3(std::min(spans, std::max(1, 4 * sms / rows)), rows), dim3(256), 0, s, a);
         if (e != cudaSuccess) return e;
     }
     return launch_take<false>(a, C, s);

@@ -167,3 +167,24 @@ def test_a_row_trimmed_into_a_shared_page_goes_on_as_a_fork():
     assert bt.tolist() == [[-1] * 4, [0, 1, 3, -1], [0, 2, 4, -1], [-1] * 4]
     assert refs[:5].tolist() == [2, 1, 1, 1, 1] and counts.tolist() == [0, 3, 3, 0] and lens.tolist() == [20, 40, 20, 0]
     assert torch.equal(cache[2], cache[1])                # tokens 16 .. 19 of row 2 (and what lies behind them)
+
+
+@pytest.mark.parametrize("B,width", [(5000, 400), (1300, 1700)])
+def test_rows_that_return_more_than_a_grid_takes_at_once(B, width):
+    """More rows than SMs have warps for, and returns of several stretches of 256 entries each, bad ones among them."""
+    r = np.random.RandomState(B)
+    counts = r.randint(width // 2, width + 1, B).astype(np.int32)
+    pages = int(counts.sum()) + 7
+    bt = np.full((B, width), -1, np.int32)
+    bt[np.arange(width) < counts[:, None]] = r.permutation(pages)[:counts.sum()]
+    refs = np.zeros(pages, np.int32)
+    refs[bt[bt >= 0]] = 1
+    bt[3, 5], bt[7, 2] = pages, bt[7, 3]
+    lens = (r.randint(0, width // 3, B) * 16).astype(np.int32)
+    lens[[0, 3, 7]] = 0
+    want = resize_reference(bt, counts, lens, refs, 16)
+    d, err = [_i32(x) for x in (bt, counts, refs)], _i32([0])
+    pkv.resize_sequences(d[0], d[1], _i32(lens), d[2], 16, err_flag=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == want[3] == pkv.FLAG_PAGE_RANGE | pkv.FLAG_PAGE_STATE
+    assert all(np.array_equal(x.cpu().numpy(), y) for x, y in zip(d, want))
