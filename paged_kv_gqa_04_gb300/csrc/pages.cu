@@ -141,8 +141,12 @@ constexpr int kTakeThreads = 1024;
 constexpr int kTakeWarps = kTakeThreads / 32;
 static_assert(kTakeWarps == 32, "a warp reads the warps' sums, one per lane");
 constexpr int kMaxCluster = 16;
-// Pools that one CTA, and that four, look through; larger ones take 16.
-constexpr int64_t kSoloPages = 8192, kSmallPoolPages = 32768;
+// Pools that one CTA looks through; larger ones take a cluster of 16. A trim and a
+// growth, captured, us by one CTA and by 16: 256 rows that change by a page, 8192
+// pages 12.1 and 13.5, 32,768 14.1 and 13.3, 131,072 19.3 and 15.2; 1024 rows given
+// up and taken again, 16,384 pages 27.8 and 15.5. (Four CTAs: 2% better than 16 at
+// most, 30% worse.)
+constexpr int64_t kSoloPages = 8192;
 constexpr int kKeptPages = 1024;           // pages of a warp whose free masks stay in a register
 constexpr uint32_t kDemandCap = 1u << 30;  // sums saturate here, above any pool
 
@@ -623,10 +627,10 @@ constexpr size_t kTakeSmemMax = (take_words(kMaxRows) + kTakeWarps * 128) * 4;
 template <bool FORK>
 cudaError_t plan_take(int64_t num_pages, unsigned* ctas) {
     static std::atomic<unsigned> largest[64];              // per device: the largest cluster that fits, at most 16
-    *ctas = num_pages <= kSoloPages ? 1 : num_pages <= kSmallPoolPages ? 4 : kMaxCluster;
+    *ctas = num_pages <= kSoloPages ? 1 : kMaxCluster;
     auto kern = *ctas == 1 ? take_kernel<FORK, true> : take_kernel<FORK, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kTakeSmemMax));
-    if (e != cudaSuccess || *ctas <= 8) return e;
+    if (e != cudaSuccess || *ctas == 1) return e;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     int dev = 0;
