@@ -699,8 +699,9 @@ pkv_status pkv_paged_tree_decode(const pkv_tensor* q, const pkv_tensor* k_cache,
 
 /*
  * pkv_tree_decode_workspace -- bytes of workspace that pkv_paged_tree_decode
- * needs for T rows of q (host only); 0 for invalid input. sm_count is the
- * device's SM count.
+ * needs (host only); 0 for invalid input. sm_count is the device's SM count.
+ * The size depends on D and sm_count alone, so one workspace serves calls of any
+ * T and Hq (which are only checked).
  */
 int64_t pkv_tree_decode_workspace(int64_t T, int32_t Hq, int32_t D, int32_t sm_count);
 

@@ -396,7 +396,8 @@ def _workspace(t):
 
 
 def tree_decode_workspace(T: int, Hq: int, D: int, sm_count: int) -> int:
-    """Bytes of workspace that paged_tree_decode needs for T rows of q."""
+    """Bytes of workspace that paged_tree_decode needs (the same for any T and
+    Hq, which are only checked)."""
     return int(lib().pkv_tree_decode_workspace(int(T), Hq, D, sm_count))
 
 

@@ -9,10 +9,11 @@
 // sum need no exchange. One pass over K and V serves two row tiles.
 //
 // Work. An item is (sequence, kv head, pair of row tiles); a unit is one tile
-// of 128 positions of one item, and an item counts five units more for its
+// of 128 positions of one item, and an item counts four units more for its
 // start and output (measured: counting two, 64 contexts of 1 to 8192 with 32
-// query heads took 103 us and not 88). All units of the batch, in order, are cut into
-// equal stretches, one per CTA (one CTA per SM): every CTA does the same
+// query heads took 105 us and not 91, counting five or three 93 and 96; FP8, 16
+// contexts of 2 to 16 Ki, 73 and not 68). All units of the batch, in order, are cut
+// into equal stretches, one per CTA (one CTA per SM): every CTA does the same
 // amount of work whatever the lengths are, with no plan from the host. Each
 // CTA finds its stretch from prefix sums over the batch. An item that is cut
 // leaves partial sums in the workspace (at most two per CTA: the end of one
@@ -47,34 +48,35 @@
 // rarely. bf16 alone is too few bits for P where the weighted values cancel, so
 // P is its bf16 rounding (2^-8 of it) and the rest, rounded again (2^-16 in all),
 // and V meets both, as in the one-token decode; the scores' columns hold both.
-// One term: 64 contexts of 1 to 8192 82 us and not 92, 16 of 8 Ki with 64 drafted
-// tokens 141 and not 180, but outputs of weights near one another up to 11 times
+// One term: 64 contexts of 1 to 8192 82 us and not 91, 16 of 8 Ki with 64 drafted
+// tokens 141 and not 176, but outputs of weights near one another up to 11 times
 // their bound off. FP8 caches: one f16 term of 2^7 P (<= 2^15), 2^-11 of it down to
 // weights of 2^-21 of the reference, 2^-32 of the reference below (P itself would
 // lose all weights below 2^-25 beside one dominant position: 0.03 of V after 2^20
-// others). The sums of the weights are
-// taken before the rounding, in fp32. For FP8 caches q is
-// scaled by a power of two per row into f16's range, which is exact for
-// every value within 2^29 of the row's largest.
+// others). The sums of the weights are taken before the rounding, in fp32. For
+// FP8 caches q is scaled by a power of two per row into f16's range, which is
+// exact for every value within 2^29 of the row's largest.
 //
 // Weights of zero do not cover values that are not finite: rows of V behind
 // the sequence's end are zeroed in the tile, and a drafted token whose V is
 // not finite is zeroed there too and added to the rows that see it by hand.
 //
-// Bound. With one row tile a tile of K and V (64 KB, bf16, D = 128) takes 2600 to
-// 2900 cycles, HBM's share of an SM is 2830; 64 contexts of 1 to 8192 (413 MB)
-// take 81 us in all, 5.1 TB/s, the rest being the start (6 us to the first
-// scores), the ends of items and the joining kernel. With two row tiles it
-// takes about 4300: scores, softmax, P and P . V of a group follow one another,
-// and tensor memory has room for two groups (S and O of each, 512 columns), so
-// the products' 2048 cycles are half of it; 16 contexts of 8 Ki with 64 drafted
-// tokens (519 MB, 129 GFLOP) take 141 us, 3.7 TB/s and 0.91 PFLOP/s. FP8 adds the
+// Bound. With one row tile a tile of K and V (64 KB, bf16, D = 128) takes an SM
+// 1.43 us, HBM's rate (7.0 TB/s); 64 contexts of 1 to 8192 (413 MB) take 91 us in
+// all, 4.5 TB/s, the rest being the start (6 us to the first scores), the ends of
+// items and the joining kernel. With two row tiles it takes 2.7 us: scores,
+// softmax, P and P . V of a group follow one another, and tensor memory has room
+// for two groups (S and O of each, 512 columns); the products are 3072 cycles of
+// it. 16 contexts of 8 Ki with 64 drafted tokens (519 MB, 129 GFLOP) take 176 us,
+// 2.9 TB/s and 0.73 PFLOP/s, P . V counted once. FP8 (32 KB): 1.74 and 2.3 us, the
 // conversion, which shares a pipe with the exponentials. Measured and not kept
-// (that last case): scores and P in two halves of 64 positions each with its own
-// barriers (199 us: products of 64 columns take as long as those of 128, and the
-// issuing thread becomes the limit), sixteen softmax warps (169 and not 150), all
-// eight warps on every set of scores (160 and not 144), two issuing threads, P
-// handed over in halves (147 and not 144).
+// (that case, by one term of P, 141 us at the end): scores and P in two halves of
+// 64 positions each with its own barriers (199 us: products of 64 columns take as
+// long as those of 128, and the issuing thread becomes the limit), sixteen softmax
+// warps (169 and not 150), all eight warps on every set of scores (160 and not
+// 144), two issuing threads, P handed over in halves (147 and not 144). By two
+// terms: the rest of the truncated weight (180), the split by fused
+// multiply-adds (185), the terms by two stores (183).
 //
 // Waits are bounded (about one second): a role that gives up sets
 // PKV_FLAG_WAIT_TIMEOUT and a CTA-wide flag that ends the others' waits.
@@ -90,7 +92,7 @@ namespace {
 constexpr int kTile = 128;    // positions per tile
 constexpr int kRows = 256;    // rows (lanes of two row tiles) per item
 constexpr int kTilePages = kTile / kPageSize;
-constexpr int kItemUnits = 5; // what an item costs beyond its tiles (start, output, joining), in tiles
+constexpr int kItemUnits = 4; // what an item costs beyond its tiles (start, output, joining), in tiles
 constexpr int kPieces = 4;    // ring of pieces
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr float kRescaleLog2 = 8.f;
@@ -1293,7 +1295,7 @@ cudaError_t launch_t(const TreeArgs& a, const CUtensorMap& tq, const CUtensorMap
 }  // namespace
 
 int64_t tree_decode_workspace(int64_t T, int32_t Hq, int32_t D, int32_t sm_count) {
-    (void)T, (void)Hq;
+    (void)T, (void)Hq;  // (at most two cut items per CTA, whatever the rows)
     return kMetaBytes + static_cast<int64_t>(sm_count) * 2 * kRows * (D + 2) * 4;
 }
 
