@@ -1270,7 +1270,10 @@ static pkv_status check_tables(const pkv_tensor& t, int64_t* B, int64_t* max_pag
 static void extent(const pkv_tensor& t, intptr_t* lo, intptr_t* hi) {
     *lo = *hi = reinterpret_cast<intptr_t>(t.ptr);
     for (int i = 0; i < t.ndim; ++i) {
-        if (t.shape[i] == 0) return;
+        if (t.shape[i] == 0) {  // (nothing, nowhere)
+            *lo = *hi = 0;
+            return;
+        }
         (t.stride[i] < 0 ? *lo : *hi) += (t.shape[i] - 1) * t.stride[i] * elem_bytes(t.dtype);
     }
     *hi += elem_bytes(t.dtype);

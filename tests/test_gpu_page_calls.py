@@ -1,6 +1,7 @@
 """GPU tests of the page operators as programs use them: from several host
 threads, with pages that sequences share, and with the rotary positions of a
 tree of drafted tokens."""
+import ctypes
 import threading
 
 import numpy as np
@@ -8,6 +9,7 @@ import pytest
 import torch
 
 import paged_kv_gqa_04_gb300 as pkv
+from paged_kv_gqa_04_gb300 import _abi
 from tests._spec import resize_reference
 
 pytestmark = pytest.mark.gpu
@@ -188,3 +190,16 @@ def test_rows_that_return_more_than_a_grid_takes_at_once(B, width):
     torch.cuda.synchronize()
     assert int(err.item()) == want[3] == pkv.FLAG_PAGE_RANGE | pkv.FLAG_PAGE_STATE
     assert all(np.array_equal(x.cpu().numpy(), y) for x, y in zip(d, want))
+
+
+def test_an_empty_list_overlaps_nothing():
+    """No accepted tokens at all (A = 0), wherever the list's pointer points: the new lengths' own memory here."""
+    lens, start, none, err = _i32([20, 5, 3]), _i32([0, 4, 4, 7]), _i32([0, 0, 0]), _i32([0])
+    bt, out = _i32(np.arange(6).reshape(3, 2)), _i32([7, 7, 7])
+    empty = _abi.PkvTensor.from_buffer_copy(_abi._desc(bt).contents)
+    empty.ptr, empty.shape[1] = out.data_ptr() + 4, 0
+    d = [_abi._desc(x) for x in (bt, lens, start)]
+    st = _abi.lib().pkv_accept_drafts(None, 0, 1, *d, ctypes.pointer(empty), _abi._desc(none), _abi._desc(out),
+                                      err.data_ptr(), _abi._stream(None))
+    torch.cuda.synchronize()
+    assert st == _abi.PKV_OK and int(err.item()) == 0 and out.tolist() == [16, 5, 0]
