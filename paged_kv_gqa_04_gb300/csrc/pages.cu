@@ -8,7 +8,8 @@
 // have been overwritten. Bound by its chain of dependent loads (length, list,
 // table, rows): in a captured graph 64 sequences in 64 caches of 8 heads (41 MB
 // moved, in L2) take 7.5 us and one sequence in 56 caches 2.7; otherwise the
-// host's call is longer (12 us with the caches bound, 190 without: README).
+// host's call is longer (12 us with the caches' descriptors made once, 190
+// with them made at every call).
 //
 // take_kernel (resize, and the first half of a fork). Page counts only, no
 // free list: a page is free when its count is 0, and free pages are handed
