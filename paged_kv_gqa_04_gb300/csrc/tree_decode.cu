@@ -66,10 +66,10 @@
 // all, 4.5 TB/s, the rest being the start (6 us to the first scores), the ends of
 // items and the joining kernel. With two row tiles it takes 2.7 us: scores,
 // softmax, P and P . V of a group follow one another, and tensor memory has room
-// for two groups (S and O of each, 512 columns); the products are 3072 cycles of
-// it. 16 contexts of 8 Ki with 64 drafted tokens (519 MB, 129 GFLOP) take 176 us,
-// 2.9 TB/s and 0.73 PFLOP/s, P . V counted once. FP8 (32 KB): 1.74 and 2.3 us, the
-// conversion, which shares a pipe with the exponentials. Measured and not kept
+// for two groups (S and O of each, 512 columns); the products are 1536 cycles
+// of either group. 16 contexts of 8 Ki with 64 drafted tokens (519 MB, 129 GFLOP)
+// take 176 us, 2.9 TB/s and 0.73 PFLOP/s, P . V counted once. FP8 (32 KB): 1.74 and
+// 2.3 us, the conversion, which shares a pipe with the exponentials. Measured and not kept
 // (that case, by one term of P, 141 us at the end): scores and P in two halves of
 // 64 positions each with its own barriers (199 us: products of 64 columns take as
 // long as those of 128, and the issuing thread becomes the limit), sixteen softmax
