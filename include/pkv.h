@@ -95,6 +95,7 @@ typedef enum { PKV_BF16 = 0, PKV_FP8_E4M3 = 1, PKV_F32 = 2, PKV_I32 = 3, PKV_FP4
 #define PKV_FLAG_DRAFT_RANGE    0x80  /* drafted tokens' rows, mask or accepted list inconsistent */
 #define PKV_FLAG_POOL_EMPTY     0x100 /* too few free pages left for a sequence              */
 #define PKV_FLAG_PAGE_STATE     0x200 /* a page count or a row contradicts the call          */
+#define PKV_FLAG_ROW_RANGE      0x400 /* sequences' ranges of packed rows inconsistent       */
 
 typedef struct {
     void*   ptr;        /* device address (NULL allowed only where stated) */
@@ -817,6 +818,64 @@ pkv_status pkv_fork_sequences(const pkv_tensor* caches, int32_t n_caches, int32_
                               const pkv_tensor* block_tables, const pkv_tensor* page_counts,
                               const pkv_tensor* seq_lens, const pkv_tensor* forks, const pkv_tensor* page_refs,
                               const pkv_tensor* copies, int32_t* err_flag, pkv_stream_t stream);
+
+/*
+ * A prompt's path beside the same paged caches. (No counterpart on the pages:
+ * these calls are for users of the decode step whose prompts, or whose models'
+ * norms of queries and keys, it does not cover.)
+ *
+ *   pkv_qk_norm_rope_kv_write  pkv_rope_kv_write with an RMS norm of every q and
+ *                              k head before the rotation; also keeps the keys
+ *   pkv_prompt_attention       causal attention of packed prompts, or of new
+ *                              tokens behind packed keys and values
+ *   pkv_gather_kv              cached keys and values as packed bf16 rows
+ */
+
+/*
+ * pkv_prompt_attention -- causal attention over whole prompts of different
+ * lengths, packed one behind the other, with grouped heads.
+ *
+ * Sequence b's tokens are rows [q_start[b], q_start[b+1]) of q, N_b of them; its
+ * keys and values are rows [k_start[b], k_start[b+1]) of k and v, L_b >= N_b of
+ * them, the last N_b being those of its tokens. Row i of the sequence sees keys
+ * j <= L_b - N_b + i. Query head h reads kv head h / (Hq/Hkv):
+ *   score_j = softmax_scale * sum_d q[r,h,d] * k[j,d]
+ *   out[r,h,:] = bf16( sum_j exp(score_j - m) v[j,:] / sum_j exp(score_j - m) )
+ *   lse_out[r,h] = m + ln sum_j exp(score_j - m)      (natural log)
+ * A row that sees nothing gives 0 and -inf. Keys and values that a row does not
+ * see have no effect on it, whatever they hold. Scores and sums are fp32; the
+ * weights exp(score_j - m) are rounded to bf16 (half a step: 2^-8 of each) where
+ * they meet v, and their sum is taken before that.
+ *
+ * q            [T, Hq, D] bf16 (already rotated); k, v [Tk, Hkv, D] bf16;
+ *              innermost stride 1, rows 16-byte aligned. Strided views of a
+ *              packed QKV buffer are accepted.
+ * q_start      [B+1] int32, ascending, within [0, T]. Rows of q outside every
+ *              range are not read and their outputs not written.
+ * k_start      [B+1] int32, ascending, within [0, Tk]; NULL = q_start (whole
+ *              prompts; then Tk = T).
+ * out          [T, Hq, D] bf16, innermost stride 1, rows 16-byte aligned.
+ * lse_out      [T, Hq] float32, or NULL.
+ * workspace,
+ * workspace_bytes  device scratch, 16-byte aligned, of at least
+ *              pkv_prompt_attention_workspace() bytes; its contents need no
+ *              preparation. Calls that may run at the same time need one each.
+ * Supported: D in {64, 128}; 1 <= Hq/Hkv <= 16; B, Hkv <= 65535; T, Tk < 2^27;
+ * Tk >= 1. out and lse_out must not overlap q, k or v (by their extents).
+ * Errors: starts that do not ascend within their rows (clamped) and L_b < N_b
+ * (the first rows see nothing) set PKV_FLAG_ROW_RANGE.
+ */
+pkv_status pkv_prompt_attention(const pkv_tensor* q, const pkv_tensor* k, const pkv_tensor* v,
+                                const pkv_tensor* q_start, const pkv_tensor* k_start, float softmax_scale,
+                                const pkv_tensor* out, const pkv_tensor* lse_out, void* workspace,
+                                int64_t workspace_bytes, int32_t* err_flag, pkv_stream_t stream);
+
+/*
+ * pkv_prompt_attention_workspace -- bytes of workspace that pkv_prompt_attention
+ * needs, whatever its rows and heads (host only); 0 for invalid input. sm_count
+ * is the device's SM count.
+ */
+int64_t pkv_prompt_attention_workspace(int32_t D, int32_t sm_count);
 
 /* Static description of a status code. */
 const char* pkv_status_string(int32_t status);

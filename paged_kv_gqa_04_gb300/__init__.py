@@ -10,11 +10,12 @@ CUDA kernels behind the C ABI of include/pkv.h (libpkv.so). This package is the 
 library is loaded on first use; without it every call raises.
 """
 from ._abi import (EXPORTED, FLAG_DRAFT_RANGE, FLAG_DUPLICATE_SLOT, FLAG_PAGE_RANGE, FLAG_PAGE_STATE,
-                   FLAG_PLAN_RANGE, FLAG_POOL_EMPTY, FLAG_POSITION_RANGE, FLAG_SEQ_LEN_RANGE, FLAG_SLOT_RANGE,
+                   FLAG_PLAN_RANGE, FLAG_POOL_EMPTY, FLAG_ROW_RANGE, FLAG_POSITION_RANGE, FLAG_SEQ_LEN_RANGE, FLAG_SLOT_RANGE,
                    FLAG_WAIT_TIMEOUT, PkvError, accept_drafts, bind, choose_num_splits, choose_num_splits_mla, copy,
                    fork_sequences, lib, lse_merge, lse_merge_planned, mla_cache_write, paged_gqa_decode,
                    paged_gqa_decode_nvfp4, paged_gqa_decode_planned, paged_mla_decode, paged_mla_decode_planned,
-                   paged_tree_decode, plan_splits, plan_splits_mla, resize_sequences, rope_kv_write,
+                   paged_tree_decode, plan_splits, plan_splits_mla, prompt_attention,
+                   prompt_attention_workspace, resize_sequences, rope_kv_write,
                    rope_kv_write_nvfp4, selftest_bounded_wait, status_string, stream_read, tree_decode_workspace,
                    validate_indices, validate_indices_static)
 

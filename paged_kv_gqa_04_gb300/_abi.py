@@ -30,6 +30,7 @@ FLAG_PLAN_RANGE = 0x40
 FLAG_DRAFT_RANGE = 0x80
 FLAG_POOL_EMPTY = 0x100
 FLAG_PAGE_STATE = 0x200
+FLAG_ROW_RANGE = 0x400
 
 _DTYPES = {
     torch.bfloat16: 0,
@@ -47,7 +48,8 @@ EXPORTED = ("pkv_rope_kv_write", "pkv_paged_gqa_decode", "pkv_lse_merge", "pkv_c
             "pkv_mla_cache_write", "pkv_paged_mla_decode", "pkv_choose_num_splits_mla",
             "pkv_selftest_bounded_wait", "pkv_copy", "pkv_plan_splits", "pkv_paged_gqa_decode_planned",
             "pkv_lse_merge_planned", "pkv_plan_splits_mla", "pkv_paged_mla_decode_planned", "pkv_paged_tree_decode",
-            "pkv_tree_decode_workspace", "pkv_accept_drafts", "pkv_resize_sequences", "pkv_fork_sequences")
+            "pkv_tree_decode_workspace", "pkv_accept_drafts", "pkv_resize_sequences", "pkv_fork_sequences",
+            "pkv_prompt_attention", "pkv_prompt_attention_workspace")
 
 
 class PkvTensor(ctypes.Structure):
@@ -102,6 +104,9 @@ def lib() -> ctypes.CDLL:
         L.pkv_accept_drafts.argtypes = [T, i32, i32, T, T, T, T, T, T, P, P]
         L.pkv_resize_sequences.argtypes = [T, T, T, T, i32, P, P]
         L.pkv_fork_sequences.argtypes = [T, i32, i32, T, T, T, T, T, T, P, P]
+        L.pkv_prompt_attention.argtypes = [T, T, T, T, T, ctypes.c_float, T, T, P, ctypes.c_int64, P, P]
+        L.pkv_prompt_attention_workspace.argtypes = [i32, i32]
+        L.pkv_prompt_attention_workspace.restype = ctypes.c_int64
         L.pkv_status_string.argtypes = [i32]
         L.pkv_status_string.restype = ctypes.c_char_p
         for name in ("pkv_rope_kv_write", "pkv_paged_gqa_decode", "pkv_lse_merge", "pkv_validate_indices",
@@ -110,7 +115,7 @@ def lib() -> ctypes.CDLL:
                      "pkv_paged_mla_decode", "pkv_choose_num_splits_mla", "pkv_selftest_bounded_wait", "pkv_copy",
                      "pkv_plan_splits", "pkv_paged_gqa_decode_planned", "pkv_lse_merge_planned",
                      "pkv_plan_splits_mla", "pkv_paged_mla_decode_planned", "pkv_paged_tree_decode",
-                     "pkv_accept_drafts", "pkv_resize_sequences", "pkv_fork_sequences"):
+                     "pkv_accept_drafts", "pkv_resize_sequences", "pkv_fork_sequences", "pkv_prompt_attention"):
             getattr(L, name).restype = ctypes.c_int32
         _lib = L
     return _lib
@@ -451,6 +456,25 @@ def fork_sequences(caches, block_tables, page_counts, seq_lens, forks, page_refs
     _check("pkv_fork_sequences", lib().pkv_fork_sequences(
         caches.ptr, caches.n, LAYOUTS[layout], _desc(block_tables), _desc(page_counts), _desc(seq_lens), _desc(forks),
         _desc(page_refs), _desc(copies), _ptr(err_flag), _stream(stream)))
+
+
+def prompt_attention_workspace(D: int, sm_count: int) -> int:
+    """Bytes of workspace that prompt_attention needs, whatever its rows and heads."""
+    return int(lib().pkv_prompt_attention_workspace(D, sm_count))
+
+
+def prompt_attention(q, k, v, q_start, k_start, softmax_scale: float, out, lse_out, workspace, err_flag=None,
+                     stream=None) -> None:
+    """Causal attention of packed prompts (pkv_prompt_attention): rows
+    q_start[b] .. q_start[b+1] of q [T,Hq,D] over rows k_start[b] ..
+    k_start[b+1] of k, v [Tk,Hkv,D] (None: q_start), whose last ones are
+    theirs: out [T,Hq,D] bf16, lse_out [T,Hq] float32 or None. workspace: a
+    contiguous device tensor of prompt_attention_workspace() bytes."""
+    _on_current_device(q, k, v, q_start, k_start, out, lse_out, workspace, err_flag)
+    ws, nbytes = _workspace(workspace)
+    _check("pkv_prompt_attention", lib().pkv_prompt_attention(
+        _desc(q), _desc(k), _desc(v), _desc(q_start), _desc(k_start), softmax_scale, _desc(out), _desc(lse_out), ws,
+        nbytes, _ptr(err_flag), _stream(stream)))
 
 
 def validate_indices(block_tables, seq_lens, slot_mapping, num_pages: int, err_flag, slot_bitmap=None,

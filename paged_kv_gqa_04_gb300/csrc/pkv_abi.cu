@@ -1621,4 +1621,79 @@ pkv_status pkv_paged_tree_decode(const pkv_tensor* q_p, const pkv_tensor* k_cach
     return cuda_status(pkv::launch_tree_decode(a, tq, tk, tv, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+int64_t pkv_prompt_attention_workspace(int32_t D, int32_t sm_count) {
+    if ((D != 64 && D != 128) || sm_count < 1 || sm_count > 4096) return 0;
+    return pkv::prompt_attention_workspace(D, sm_count);
+}
+
+pkv_status pkv_prompt_attention(const pkv_tensor* q_p, const pkv_tensor* k_p, const pkv_tensor* v_p,
+                                const pkv_tensor* q_start_p, const pkv_tensor* k_start_p, float softmax_scale,
+                                const pkv_tensor* out_p, const pkv_tensor* lse_out_p, void* workspace,
+                                int64_t workspace_bytes, int32_t* err_flag, pkv_stream_t stream) {
+    const pkv_tensor& q = arg(q_p);
+    const pkv_tensor& k = arg(k_p);
+    const pkv_tensor& v = arg(v_p);
+    const pkv_tensor& qs = arg(q_start_p);
+    const pkv_tensor& ks = arg(k_start_p);
+    const pkv_tensor& out = arg(out_p);
+    const pkv_tensor& lse = arg(lse_out_p);
+    if (!shape_ok(q, 3, PKV_BF16) || !shape_ok(k, 3, PKV_BF16) || !shape_ok(v, 3, PKV_BF16)) return PKV_ERR_INVALID_ARG;
+    const int64_t T = q.shape[0], Hq = q.shape[1], D = q.shape[2], Tk = k.shape[0], Hkv = k.shape[1];
+    if (k.shape[2] != D || v.shape[0] != Tk || v.shape[1] != Hkv || v.shape[2] != D) return PKV_ERR_INVALID_ARG;
+    if (Hkv < 1 || Hq < 1 || Hq % Hkv != 0) return PKV_ERR_INVALID_ARG;
+    if (qs.ndim != 1 || qs.shape[0] < 1) return PKV_ERR_INVALID_ARG;
+    const int64_t B = qs.shape[0] - 1;
+    pkv_status st = check_i32(qs, B + 1);
+    if (st != PKV_OK) return st;
+    if (ks.ptr ? (st = check_i32(ks, B + 1)) != PKV_OK : false) return st;
+    if (!ks.ptr && Tk != T) return PKV_ERR_INVALID_ARG;
+    if (!shape_ok(out, 3, PKV_BF16) || out.shape[0] != T || out.shape[1] != Hq || out.shape[2] != D)
+        return PKV_ERR_INVALID_ARG;
+    if (lse.ptr && (!shape_ok(lse, 2, PKV_F32) || lse.shape[0] != T || lse.shape[1] != Hq)) return PKV_ERR_INVALID_ARG;
+    if (!std::isfinite(softmax_scale)) return PKV_ERR_INVALID_ARG;
+    const int64_t G = Hq / Hkv;
+    if ((D != 64 && D != 128) || G > 16 || B > 65535 || Hkv > 65535 || T > 0x7FFFFFFF / 16 || Tk > 0x7FFFFFFF / 16)
+        return PKV_ERR_UNSUPPORTED;
+    if (T == 0 || B == 0) return PKV_OK;
+    if (!q.ptr || !out.ptr || (Tk > 0 && (!k.ptr || !v.ptr))) return PKV_ERR_INVALID_ARG;
+    if (Tk == 0) return PKV_ERR_UNSUPPORTED;  // (nothing to attend to, and nothing to make a descriptor of)
+    if (!row16(q, 2) || !row16(k, 2) || !row16(v, 2) || !row16(out, 2)) return PKV_ERR_UNSUPPORTED;
+    // (the rows that other CTAs have yet to read)
+    for (const pkv_tensor* t : {&q, &k, &v})
+        if (overlap(out, *t) || (lse.ptr && overlap(lse, *t))) return PKV_ERR_INVALID_ARG;
+    int sms = 0;
+    if (pkv::device_sm_count(&sms) != cudaSuccess) return PKV_ERR_CUDA;
+    if (!workspace || workspace_bytes < pkv::prompt_attention_workspace(static_cast<int32_t>(D), sms))
+        return PKV_ERR_INVALID_ARG;
+    if (!aligned(workspace, 16)) return PKV_ERR_UNSUPPORTED;
+
+    // K and V: one box = 128 tokens of one kv head x 64 values
+    CUtensorMap tq, tk, tv;
+    if (!make_q_map(&tq, q, static_cast<int>(G)) || !make_q_map(&tk, k, 1) || !make_q_map(&tv, v, 1)) return PKV_ERR_CUDA;
+    pkv::PromptArgs a{};
+    a.v = static_cast<const uint16_t*>(v.ptr);
+    a.v_s0 = v.stride[0];
+    a.v_s1 = v.stride[1];
+    a.q_start = static_cast<const int32_t*>(qs.ptr);
+    a.k_start = static_cast<const int32_t*>(ks.ptr);
+    a.scale_log2 = softmax_scale * 1.4426950408889634f;
+    a.out = static_cast<uint16_t*>(out.ptr);
+    a.o_s0 = out.stride[0];
+    a.o_s1 = out.stride[1];
+    a.lse = static_cast<float*>(lse.ptr);
+    a.l_s0 = lse.ptr ? lse.stride[0] : 0;
+    a.l_s1 = lse.ptr ? lse.stride[1] : 0;
+    a.workspace = workspace;
+    a.T = static_cast<int32_t>(T);
+    a.Tk = static_cast<int32_t>(Tk);
+    a.B = static_cast<int32_t>(B);
+    a.Hq = static_cast<int32_t>(Hq);
+    a.Hkv = static_cast<int32_t>(Hkv);
+    a.D = static_cast<int32_t>(D);
+    a.G = static_cast<int32_t>(G);
+    a.tile_toks = 128 / a.G;
+    a.err = err_flag;
+    return cuda_status(pkv::launch_prompt_attention(a, tq, tk, tv, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

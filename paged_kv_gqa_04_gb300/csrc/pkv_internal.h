@@ -265,6 +265,22 @@ struct TreeArgs {
     int32_t* err;
 };
 
+struct PromptArgs {
+    const uint16_t* v;         // [Tk, Hkv, D] bf16 bits
+    int64_t v_s0, v_s1;
+    const int32_t* q_start;    // [B + 1]
+    const int32_t* k_start;    // [B + 1], null = q_start
+    float scale_log2;          // softmax_scale * log2(e)
+    uint16_t* out;             // [T, Hq, D] bf16 bits
+    int64_t o_s0, o_s1;
+    float* lse;                // [T, Hq], may be null
+    int64_t l_s0, l_s1;
+    void* workspace;
+    int32_t T, Tk, B, Hq, Hkv, D, G;
+    int32_t tile_toks;         // tokens per row tile: 128 / G
+    int32_t* err;
+};
+
 // Launch as a programmatic dependent of the preceding work in the stream:
 // the kernel may start while the preceding kernel finishes, and orders its
 // reads and writes of data that kernel touches after griddepcontrol.wait.
@@ -306,6 +322,11 @@ cudaError_t launch_fork_take(const TakeArgs& a, cudaStream_t s);
 cudaError_t launch_fork_share(const ShareArgs& a, int32_t n, int32_t max_pages, bool tables, cudaStream_t s);
 cudaError_t launch_tree_decode(const TreeArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                cudaStream_t s);
+// Joins the partial sums of cut items (of a: T, Hq, D, G, tile_toks, out, lse, workspace).
+cudaError_t launch_row_join(const TreeArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_prompt_attention(const PromptArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                    cudaStream_t s);
+int64_t prompt_attention_workspace(int32_t D, int32_t sm_count);
 int64_t tree_decode_workspace(int64_t T, int32_t Hq, int32_t D, int32_t sm_count);
 
 // Occupancy-related constants of the decode kernel, shared with the split

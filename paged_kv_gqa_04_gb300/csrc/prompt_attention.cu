@@ -1,0 +1,886 @@
+// prompt_attention.cu -- causal attention over packed prompts on the
+// fifth-generation tensor cores.
+//
+// Rows. The tokens of a sequence and the G query heads of a kv head share the
+// same K and V. A row tile is 128 / G tokens (rounded down) times G heads on the
+// M side of the MMA (128 tensor-memory lanes): q lands in operand layout by
+// TMA, and a softmax thread owns one row. One pass over K and V serves two row
+// tiles.
+//
+// Work. An item is (sequence, kv head, pair of row tiles). Its cost is counted
+// in keys: those that its last row sees, and kItemKeys for its start and
+// output. All items of the call, in order, are cut into equal stretches, one per
+// CTA (one CTA per SM), so every CTA does the same amount of work whatever the
+// lengths are, with no plan from the host; sums over a sequence's items are
+// closed forms. An item that is cut leaves partial sums in the workspace (at
+// most two per CTA), which a second kernel joins. Where no item is longer than
+// what partial sums and joining cost (kSnapKeys), the cuts are moved to the
+// next item's start instead.
+//
+// A CTA's roles:
+//   warp 0        TMA loads of K and V, 128 positions at a time
+//   warp 1        one thread issues S = Q . K^T and O += P . V (M = 128; P from
+//                 tensor memory, V as an MN-major operand: nothing is transposed)
+//   warp 2        V of the tiles that some row sees in part: zeroes rows behind
+//                 the sequence's end and rows that are not finite, which a
+//                 weight of zero would not silence, and notes the latter
+//   warp 3        walks the CTA's items, hands the pieces to the other roles, and
+//                 loads q by TMA
+//   warps 4 - 7,
+//   warps 8 - 11  two softmax groups, each with a row tile, S, P and O of its own
+//                 in tensor memory. While one group is in its softmax the tensor
+//                 cores work for the other: P . V and the next scores of one
+//                 group (1024 cycles, D = 128) hide the other's softmax. An
+//                 item's first scores are computed while the item before writes
+//                 its output.
+//
+// Softmax. The weights are exp2(score - m) with a reference m per row, which is
+// the maximum of the row's first tile and moves only when a tile's weights sum
+// to more than 2^kRaiseLog2: one pass over S per tile, with no maximum in it.
+// m is a score of the row or more than 2^-kRaiseLog2 of its weights away from
+// one, so nothing that counts underflows. Sums and O are fp32. P meets V as
+// bf16, rounded once (2^-9 of a weight on average less, at most 2^-8): its
+// rounding and the output's are of one size, and independent. A second term, as
+// in the attention of drafted tokens, is half as much tensor work again.
+//
+// Waits are bounded (about one second): a role that gives up sets
+// PKV_FLAG_WAIT_TIMEOUT and a CTA-wide flag that ends the others' waits.
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
+#include "pkv_internal.h"
+#include "pkv_ptx.cuh"
+#include "umma_row.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kTile = 128;      // positions per tile
+constexpr int kItemKeys = 512;  // what an item costs beyond its tiles, in keys
+constexpr int kSnapKeys = 1536; // longest item (keys and kItemKeys) up to which items are not cut
+constexpr int kPieces = 4;      // ring of pieces
+constexpr uint64_t kWaitLimitNs = 1000000000ull;
+constexpr int kFix = 4;         // ring of the fixed tiles' notes: no fewer than there are stages of V
+constexpr float kRaise = 65536.f;  // sum of a tile's weights that moves the reference
+
+template <int D>
+struct Cfg {
+    static constexpr int NB = D / 64;            // 128-byte column blocks of an operand row
+    static constexpr int TILE = kTile * D * 2;
+    static constexpr int BLOCK = kTile * 128;    // one column block of it
+    static constexpr int SK = D == 128 ? 2 : 4, SV = D == 128 ? 3 : 4;  // stages of K, of V
+    static constexpr int THREADS = 384;
+    // Registers a thread: launched with 168, dealt out again by role.
+    static constexpr int REG_IO = 88, REG_SM = 208;
+    static constexpr int REGS = 128 * (REG_IO + 2 * REG_SM);
+    static_assert(REGS <= 168 * THREADS, "registers as launched");
+    static constexpr int OFF_Q = 0;              // two row tiles of q
+    static constexpr int OFF_K = OFF_Q + 2 * TILE;
+    static constexpr int OFF_V = OFF_K + SK * TILE;
+    static constexpr int OFF_BAR = OFF_V + SV * TILE;
+    static constexpr int NBAR = 2 * SK + 2 * SV + kFix + 2 * 6 + 1 + 2 * kPieces;
+    static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
+    static constexpr int OFF_PIECE = (OFF_MISC + 512 + 15) / 16 * 16;  // [kPieces] Piece
+    static constexpr int SMEM = OFF_PIECE + kPieces * 80 + 1024;       // + alignment slack
+    static_assert(SMEM <= 232448, "shared memory of one CTA");
+    // tensor-memory columns of a softmax group: S (P over it), then O
+    static constexpr uint32_t O_COL = 128;
+};
+
+struct Seq {
+    int q0, N, k0, L, ctx, RG, W;  // W: tokens of a pair of row tiles
+    // Keys that pair rg may see (where there are fewer keys than tokens: that many, the rest masked).
+    __device__ __forceinline__ int end(int rg) const { return max(ctx, 0) + min(N, (rg + 1) * W); }
+    __device__ __forceinline__ int tiles(int rg) const { return (end(rg) + kTile - 1) / kTile; }
+    // Cost of the pairs before rg < RG, and of all of them.
+    __device__ __forceinline__ int64_t before(int64_t rg) const {
+        return rg * (kItemKeys + max(ctx, 0)) + rg * (rg + 1) / 2 * W;
+    }
+    __device__ __forceinline__ int64_t all() const { return RG ? before(RG - 1) + kItemKeys + end(RG - 1) : 0; }
+};
+// Sequence b, its values clamped; `flags` collects what was out of range.
+__device__ __forceinline__ Seq seq_of(const PromptArgs& a, int b, int& flags) {
+    Seq s;
+    const int q0 = __ldg(a.q_start + b), q1 = __ldg(a.q_start + b + 1);
+    s.q0 = min(max(q0, 0), a.T);
+    const int e = min(max(q1, s.q0), a.T);
+    s.N = e - s.q0;
+    s.k0 = s.q0;
+    s.L = s.N;
+    bool bad = s.q0 != q0 || e != q1;
+    if (a.k_start != nullptr) {
+        const int k0 = __ldg(a.k_start + b), k1 = __ldg(a.k_start + b + 1);
+        s.k0 = min(max(k0, 0), a.Tk);
+        s.L = min(max(k1, s.k0), a.Tk) - s.k0;
+        bad |= s.k0 != k0 || s.k0 + s.L != k1 || s.N > s.L;
+    }
+    if (bad) flags |= PKV_FLAG_ROW_RANGE;
+    s.ctx = s.L - s.N;
+    s.W = 2 * a.tile_toks;
+    s.RG = s.N <= s.W ? (s.N > 0) : (s.N + s.W - 1) / s.W;
+    return s;
+}
+
+// CTA c of n starts at unit cut(c); the first total % n stretches are one unit longer.
+struct Cuts {
+    int n;
+    int64_t per, rem;
+    __device__ __forceinline__ Cuts(int64_t total, int ctas) : n(0), per(0), rem(0) {
+        // (stretches of a tile and more: cuts of one item are a tile apart)
+        n = static_cast<int>(min(static_cast<int64_t>(ctas), (total + kTile - 1) / kTile));
+        if (n > 1 && total / n < kTile) --n;
+        if (n > 0) {
+            per = total / n;
+            rem = total - per * n;
+        }
+    }
+    __device__ __forceinline__ int64_t cut(int c) const { return c * per + min(static_cast<int64_t>(c), rem); }
+    // the last CTA that starts at or before unit x
+    __device__ __forceinline__ int at_or_before(int64_t x) const {
+        const int64_t c = x < rem * (per + 1) ? x / (per + 1) : rem + (x - rem * (per + 1)) / per;
+        return static_cast<int>(min(c, static_cast<int64_t>(n - 1)));
+    }
+};
+
+// A place in the order of items: tile t of item k = kvh RG + rg of sequence b; the item's first unit.
+struct Place {
+    int b, k, t, pad;
+    int64_t item;
+};
+// Unit `off` of sequence b, whose first unit is `base`.
+__device__ __forceinline__ Place place_of(const Seq& s, int64_t per_head, int b, int64_t base, int64_t off, bool snap) {
+    const int kvh = static_cast<int>(off / per_head);
+    const int64_t rem = off - kvh * per_head;
+    // the last rg with before(rg) <= rem
+    const double w = s.W, h = kItemKeys + max(s.ctx, 0) + 0.5 * w;
+    int rg = static_cast<int>((sqrt(h * h + 2.0 * w * static_cast<double>(rem)) - h) / w);
+    rg = min(max(rg, 0), s.RG - 1);
+    while (rg > 0 && s.before(rg) > rem) --rg;
+    while (rg + 1 < s.RG && s.before(rg + 1) <= rem) ++rg;
+    const int64_t in = rem - s.before(rg);
+    Place p{b, kvh * s.RG + rg, 0, 0, base + kvh * per_head + s.before(rg)};
+    if (snap) {
+        if (in > 0) ++p.k;  // (which may be one past the sequence's last)
+    } else {
+        p.t = static_cast<int>(max(in - kItemKeys, static_cast<int64_t>(0)) / kTile);
+    }
+    return p;
+}
+
+// The pieces of items between two places, in order.
+struct Walk {
+    int b, k, t0, t1, nt, kvh, rg;
+    Seq s;
+    Place end;
+    bool first;
+    __device__ __forceinline__ Walk(const Place& from, const Place& to)
+        : b(from.b), k(from.k), t0(from.t), end(to), first(true) {}
+    // Next piece [t0, t1) of item (b, k); false at the end.
+    __device__ __forceinline__ bool next(const PromptArgs& a) {
+        int ignored = 0;
+        bool load = first;
+        if (!first) {
+            t0 = 0;
+            load = ++k >= a.Hkv * s.RG;
+            if (load) {
+                k = 0;
+                ++b;
+            }
+        }
+        first = false;
+        for (;; ++b, k = 0, load = true) {  // past the sequences without tokens
+            if (b >= a.B || !in_range()) return false;
+            if (load) s = seq_of(a, b, ignored);
+            if (k < a.Hkv * s.RG) break;
+        }
+        kvh = s.RG == 1 ? k : k / s.RG;
+        rg = k - kvh * s.RG;
+        nt = s.tiles(rg);
+        t1 = b == end.b && k == end.k ? end.t : nt;
+        return true;
+    }
+    __device__ __forceinline__ bool in_range() const {
+        return b < end.b || (b == end.b && (k < end.k || (k == end.k && end.t > t0)));
+    }
+};
+
+// A piece: tiles [t0, t1) of an item (the tokens [tok0, tok0 + toks) of sequence b).
+struct Piece {
+    int b, kvh, q0, k0;      // b < 0: there are no more
+    int L, ctx, tok0, toks;
+    int t0, t1, whole, two;  // whole: all of the item; two: two row tiles
+    int tf;                  // tiles before this one are seen in full by every row
+    int pad[7];
+    // Keys that row tile g may see, and the columns of tile t among them in steps of 16.
+    __device__ __forceinline__ int end(int g, int tile_toks) const {
+        return ctx + tok0 + min(toks, (g + 1) * tile_toks);
+    }
+    __device__ __forceinline__ int cols(int g, int t, int tile_toks) const {
+        return min(max((end(g, tile_toks) - t * kTile + 15) & ~15, 16), kTile);
+    }
+};
+static_assert(sizeof(Piece) == 80, "as laid out");
+
+template <int D>
+__global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                  const __grid_constant__ CUtensorMap tmv, const PromptArgs a) {
+    using C = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t s0 = smem_u32(smem);
+    enum : int { bKFull = 0, bKFree = C::SK, bVFull = 2 * C::SK, bVFree = bVFull + C::SV, bFix = bVFree + C::SV,
+                 bS = bFix + kFix, bP = bS + 2, bO = bP + 2, bOFree = bO + 2, bQ = bOFree + 2, bQFree = bQ + 2,
+                 bPiece = bQFree + 2, bPieceFree = bPiece + kPieces, bEnd = bPieceFree + kPieces };
+    static_assert(bEnd + 1 == C::NBAR, "barriers");
+    auto bar = [&](int i) -> uint32_t { return s0 + C::OFF_BAR + 8 * i; };
+    uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+    volatile uint32_t* go_on = misc + 2;                       // [2 groups]: O has been started by hand
+    volatile uint32_t* bad_rows = misc + 64;                   // [kFix][4 words]: rows of V that are not finite
+    int64_t* warp_units = reinterpret_cast<int64_t*>(misc + 12);        // [12]
+    int* warp_longest = reinterpret_cast<int*>(misc + 36);              // [12]
+    Place* place = reinterpret_cast<Place*>(misc + 48);                 // [2]: from, to
+    static_assert(sizeof(Place) == 24, "as laid out");
+    Piece* pieces = reinterpret_cast<Piece*>(smem + C::OFF_PIECE);
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    if (tid == C::THREADS - 32) {  // (the first threads have sequences to look at)
+        for (int i = 0; i < C::SK; ++i) {
+            mbar_init(bar(bKFull + i), 1);
+            mbar_init(bar(bKFree + i), 1);
+        }
+        for (int i = 0; i < C::SV; ++i) {
+            mbar_init(bar(bVFull + i), 1);
+            mbar_init(bar(bVFree + i), 2);  // the last P . V, and warp 2
+        }
+        static_assert(kFix >= C::SV, "a note lasts as long as its tile");
+        for (int i = 0; i < kFix; ++i) mbar_init(bar(bFix + i), 1);
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(bar(bS + w), 1);
+            mbar_init(bar(bP + w), 4);
+            mbar_init(bar(bO + w), 1);
+            mbar_init(bar(bOFree + w), 4);
+            mbar_init(bar(bQ + w), 1);
+            mbar_init(bar(bQFree + w), 1);
+        }
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(bar(bPiece + i), 1);
+            mbar_init(bar(bPieceFree + i), 11);  // copies, MMA, V, softmax
+        }
+        mbar_init(bar(bEnd), 1);
+        *abort_flag = 0;
+        place[0] = place[1] = Place{a.B, 0, 0, 0, 0};
+        fence_mbar_init();
+        tma_prefetch_desc(&tmq);
+        tma_prefetch_desc(&tmk);
+        tma_prefetch_desc(&tmv);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(misc), 512);
+        tmem_relinquish();
+    }
+
+    // ---- this CTA's stretch (index inputs only) --------------------------------
+    int64_t total = 0;
+    bool snap = false;
+    {
+        const int seg = (a.B + C::THREADS - 1) / C::THREADS;
+        const int b0 = min(tid * seg, a.B), b1 = min(b0 + seg, a.B);
+        int64_t sum = 0, per = 0;
+        int flags = 0, longest = 0;
+        Seq s{};
+        for (int b = b0; b < b1; ++b) {
+            s = seq_of(a, b, flags);
+            per = s.all();
+            sum += a.Hkv * per;
+            if (s.RG) longest = max(longest, kItemKeys + s.end(s.RG - 1));
+        }
+        if (flags && blockIdx.x == 0) flag_error(a.err, flags);
+        int64_t inc = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += y;
+        }
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        if (lane == 31) {
+            warp_units[warp] = inc;
+            warp_longest[warp] = longest;
+        }
+        __syncthreads();
+        int64_t base = 0;
+        for (int w = 0; w < C::THREADS / 32; ++w) {
+            if (w == warp) base = total;
+            total += warp_units[w];
+            longest = max(longest, warp_longest[w]);
+        }
+        snap = longest <= kSnapKeys;
+        const Cuts cuts(total, gridDim.x);
+        const int c = blockIdx.x;
+        int64_t at = base + inc - sum;
+        if (c < cuts.n && sum > 0) {
+            const int64_t x0 = cuts.cut(c), x1 = cuts.cut(c + 1);
+            if (x1 >= at && x0 < at + sum) {
+                for (int b = b0; b < b1; ++b) {
+                    if (seg > 1) {
+                        int ignored = 0;
+                        s = seq_of(a, b, ignored);
+                        per = s.all();
+                    }
+                    const int64_t n = a.Hkv * per;
+                    if (x0 >= at && x0 < at + n) place[0] = place_of(s, per, b, at, x0 - at, snap);
+                    if (x1 >= at && x1 < at + n) place[1] = place_of(s, per, b, at, x1 - at, snap);
+                    at += n;
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+    const Place from = place[0], to = place[1];
+
+    // q, k and v may still be being written by the preceding grid: every role waits for it
+    auto give_up = [&]() {
+        *abort_flag = 1;
+        flag_error(a.err, PKV_FLAG_WAIT_TIMEOUT);
+    };
+    auto lane_wait = [&](uint32_t bb, uint32_t par) -> bool {
+        if (mbar_test_wait(bb, par)) return true;
+        uint64_t t0 = 0;
+        while (!mbar_try_wait(bb, par)) {
+            const uint64_t now = global_ns();
+            if (t0 == 0) t0 = now;
+            if (*abort_flag || now - t0 > kWaitLimitNs) {
+                give_up();
+                return false;
+            }
+        }
+        return true;
+    };
+    auto warp_wait = [&](uint32_t bb, uint32_t par) -> bool { return __all_sync(0xffffffffu, lane_wait(bb, par)); };
+    auto piece_bar = [&](int i) { return bar(bPiece + i % kPieces); };
+    auto piece_par = [](int i) -> uint32_t { return (i / kPieces) & 1; };
+
+    if (warp < 4) {
+        reg_dec<C::REG_IO>();
+        if (warp == 0 && lane == 0) {
+            // ======================= copies of K and V ================================
+            grid_dep_wait();
+            int n = 0;  // tiles
+            bool ok = true;
+            for (int i = 0; ok; ++i) {
+                if (!lane_wait(piece_bar(i), piece_par(i))) break;
+                const Piece w = pieces[i % kPieces];
+                mbar_arrive(bar(bPieceFree + i % kPieces));
+                if (w.b < 0) break;
+                for (int t = w.t0; t < w.t1; ++t, ++n) {
+                    const int row = w.k0 + t * kTile;
+                    const int sk = n % C::SK, sv = n % C::SV;
+                    if (n >= C::SK && !(ok = lane_wait(bar(bKFree + sk), (n / C::SK - 1) & 1))) break;
+                    mbar_arrive_expect_tx(bar(bKFull + sk), C::TILE);
+                    for (int c = 0; c < C::NB; ++c)
+                        tma_load_3d(s0 + C::OFF_K + sk * C::TILE + c * C::BLOCK, &tmk, bar(bKFull + sk), 64 * c, w.kvh,
+                                    row);
+                    if (n >= C::SV && !(ok = lane_wait(bar(bVFree + sv), (n / C::SV - 1) & 1))) {
+                        // (this tile's K is on its way, its V is not)
+                        (void)mbar_wait_bounded(bar(bKFull + sk), (n / C::SK) & 1, kWaitLimitNs);
+                        break;
+                    }
+                    mbar_arrive_expect_tx(bar(bVFull + sv), C::TILE);
+                    for (int c = 0; c < C::NB; ++c)
+                        tma_load_3d(s0 + C::OFF_V + sv * C::TILE + c * C::BLOCK, &tmv, bar(bVFull + sv), 64 * c, w.kvh,
+                                    row);
+                }
+            }
+            // Copies under way land before the CTA may exit.
+            for (int i = max(n - C::SK, 0); i < n; ++i)
+                (void)mbar_wait_bounded(bar(bKFull + i % C::SK), (i / C::SK) & 1, kWaitLimitNs);
+            for (int i = max(n - C::SV, 0); i < n; ++i)
+                (void)mbar_wait_bounded(bar(bVFull + i % C::SV), (i / C::SV) & 1, kWaitLimitNs);
+        } else if (warp == 3 && lane == 0) {
+            // ======================= the CTA's pieces, and q ==========================
+            int4 meta = make_int4(0, 0, 0, 0);  // what the joining kernel is to do with the cut item
+            const Cuts cuts(total, gridDim.x);
+            const uint64_t policy = l2_policy_evict_first();
+            int uses[2] = {0, 0};
+            bool ok = true;
+            Walk walk(from, to);
+            for (int i = 0; ok; ++i) {
+                Piece w{};
+                w.b = walk.next(a) ? walk.b : -1;
+                if (w.b >= 0) {
+                    w.kvh = walk.kvh, w.q0 = walk.s.q0, w.k0 = walk.s.k0, w.L = walk.s.L, w.ctx = walk.s.ctx;
+                    w.tok0 = walk.rg * 2 * a.tile_toks;
+                    w.toks = min(walk.s.N - w.tok0, 2 * a.tile_toks);
+                    w.t0 = walk.t0, w.t1 = walk.t1;
+                    w.whole = w.t0 == 0 && w.t1 == walk.nt;
+                    w.two = w.toks > a.tile_toks;
+                    w.tf = max(min(w.ctx + w.tok0 + 1, w.L), 0) / kTile;
+                }
+                if (i >= kPieces && !lane_wait(bar(bPieceFree + i % kPieces), (i / kPieces - 1) & 1)) break;
+                pieces[i % kPieces] = w;
+                mbar_arrive(piece_bar(i));
+                if (w.b < 0) break;
+                if (w.t0 == 0 && w.t1 < walk.nt) {
+                    // the CTA that has the item's last unit
+                    const int c1 = cuts.at_or_before(to.item + kItemKeys + walk.s.end(walk.rg) - 1);
+                    meta = make_int4(w.q0 + w.tok0, w.toks, c1 - static_cast<int>(blockIdx.x) + 1, w.kvh);
+                }
+                if (i == 0) grid_dep_wait();
+                // tile_toks tokens x G heads are consecutive operand rows
+                for (int g = 0; ok && g <= w.two; ++g) {
+                    if (uses[g] > 0) ok = lane_wait(bar(bQFree + g), (uses[g] - 1) & 1);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(bar(bQ + g), a.tile_toks * a.G * D * 2);
+                    for (int c = 0; c < C::NB; ++c)
+                        tma_load_3d(s0 + C::OFF_Q + g * C::TILE + c * C::BLOCK, &tmq, bar(bQ + g), 64 * c, w.kvh * a.G,
+                                    w.q0 + w.tok0 + g * a.tile_toks, policy);
+                    ++uses[g];
+                }
+            }
+            grid_dep_wait();
+            reinterpret_cast<int4*>(a.workspace)[blockIdx.x] = meta;
+            for (int g = 0; g < 2; ++g)
+                if (uses[g]) (void)mbar_wait_bounded(bar(bQ + g), (uses[g] - 1) & 1, kWaitLimitNs);
+        } else if (warp == 1 && lane == 0) {
+            // ======================= tensor-core issue (one thread) ===================
+            grid_dep_wait();
+            // the sign of softmax_scale goes into q (bit 13 negates A); N in bits 17 and up
+            const uint32_t idesc_qk = umma_idesc(128, 0, 1, 1, false, false) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
+            constexpr uint32_t kIdescPv = umma_idesc(128, D, 1, 1, false, true);
+            // 128-byte-swizzled operands, 1024 bytes between groups of 8 rows
+            constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
+            auto desc_lo = [](uint32_t addr, uint32_t lead) { return ((addr >> 4) & 0x3FFFu) | (lead >> 4) << 16; };
+            int items[2] = {0, 0}, n_p[2] = {0, 0};
+            int n = 0, n_fix = 0, issued = 0;
+            bool ok = true;
+            // Scores of tile t (the CTA's tile nn) for row tile g.
+            auto scores = [&](const Piece& w, int g, int t, int nn) {
+                if (g == 0) ok = ok && lane_wait(bar(bKFull + nn % C::SK), (nn / C::SK) & 1);
+                if (t == w.t0) ok = ok && lane_wait(bar(bQ + g), items[g]++ & 1);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t q = desc_lo(s0 + C::OFF_Q + g * C::TILE, 16);
+                const uint32_t kt = desc_lo(s0 + C::OFF_K + (nn % C::SK) * C::TILE, 16);
+                const uint32_t idesc = idesc_qk | static_cast<uint32_t>(w.cols(g, t, a.tile_toks) >> 3) << 17;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t at = ((k >> 2) * C::BLOCK + (k & 3) * 32) >> 4;
+                    if (k == 0) umma_ss<true>(tmem + 256 * g, q, kt, kDescHi, idesc);
+                    else umma_ss<false>(tmem + 256 * g, q + at, kt + at, kDescHi, idesc);
+                }
+                umma_commit(bar(bS + g));
+                ++issued;
+            };
+            Piece w, next;
+            w.b = -1;
+            if (lane_wait(piece_bar(0), piece_par(0))) w = pieces[0];
+            if (w.b >= 0) {
+                scores(w, 0, w.t0, 0);
+                if (w.two) scores(w, 1, w.t0, 0);
+            }
+            for (int i = 0; ok && w.b >= 0; ++i) {
+                next.b = -1;
+                for (int t = w.t0; ok && t < w.t1; ++t, ++n) {
+                    for (int g = 0; ok && g <= w.two; ++g) {
+                        if (g == 0) {
+                            if (t >= w.tf) {
+                                ok = lane_wait(bar(bFix + n_fix % kFix), (n_fix / kFix) & 1);
+                                ++n_fix;
+                            } else {
+                                ok = lane_wait(bar(bVFull + n % C::SV), (n / C::SV) & 1);
+                            }
+                        }
+                        ok = ok && lane_wait(bar(bP + g), n_p[g]++ & 1);
+                        // the item before has been read out of O
+                        if (t == w.t0 && items[g] > 1) ok = ok && lane_wait(bar(bOFree + g), (items[g] - 2) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t tS = tmem + 256 * g;
+                        const uint32_t vt = desc_lo(s0 + C::OFF_V + (n % C::SV) * C::TILE, C::BLOCK);
+                        const uint32_t more_o = t > w.t0 || go_on[g] != 0u;  // O goes on, or starts
+                        const int steps = w.cols(g, t, a.tile_toks) >> 4;
+                        if (steps == kTile / 16) {
+#pragma unroll
+                            for (int k = 0; k < kTile / 16; ++k)
+                                umma_ts(tS + C::O_COL, tS + 8 * k, vt + k * (2048 >> 4), kDescHi, kIdescPv, k > 0 ? 1u : more_o);
+                        } else {
+                            for (int k = 0; k < steps; ++k)
+                                umma_ts(tS + C::O_COL, tS + 8 * k, vt + k * (2048 >> 4), kDescHi, kIdescPv, k > 0 ? 1u : more_o);
+                        }
+                        ++issued;
+                        if (t + 1 < w.t1) {
+                            scores(w, g, t + 1, n + 1);
+                        } else {
+                            umma_commit(bar(bO + g));
+                            if (g == 0) {
+                                ok = lane_wait(piece_bar(i + 1), piece_par(i + 1));
+                                if (ok) next = pieces[(i + 1) % kPieces];
+                            }
+                            if (ok && next.b >= 0 && g <= next.two) scores(next, g, next.t0, n + 1);
+                        }
+                    }
+                }
+                if (ok && next.b >= 0 && next.two && !w.two) scores(next, 1, next.t0, n);
+                mbar_arrive(bar(bPieceFree + i % kPieces));
+                w = next;
+            }
+            // Every operation issued is done before the tensor memory is freed: the
+            // softmax groups wait for their last O, and a give-up for all of them here.
+            if (!ok && issued > 0) {
+                umma_commit(bar(bEnd));
+                (void)mbar_wait_bounded(bar(bEnd), 0, kWaitLimitNs);
+            }
+        } else if (warp == 2) {
+            // ======================= V of partly visible tiles ========================
+            grid_dep_wait();
+            int n = 0, n_fix = 0;
+            bool ok = true;
+            for (int i = 0; ok; ++i) {
+                if (!warp_wait(piece_bar(i), piece_par(i))) break;
+                const Piece w = pieces[i % kPieces];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(bPieceFree + i % kPieces));
+                if (w.b < 0) break;
+                const int lim = max(min(w.ctx + w.tok0 + 1, w.L), 0);  // keys that every row sees
+                for (int t = w.t0; t < w.t1; ++t, ++n) {
+                    ok = warp_wait(bar(bVFull + n % C::SV), (n / C::SV) & 1);
+                    if (!ok) break;
+                    if (t < w.tf) {
+                        if (lane == 0) mbar_arrive(bar(bVFree + n % C::SV));
+                        continue;
+                    }
+                    const uint32_t tile = s0 + C::OFF_V + (n % C::SV) * C::TILE;
+                    uint32_t words[4];
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = 32 * k + lane, pos = t * kTile + r;
+                        const uint32_t row = tile + r * 128;
+                        uint32_t acc = 0u;  // sums of 0 v: zero unless some v is not finite
+                        if (pos >= lim && pos < w.L) {
+#pragma unroll
+                            for (int c = 0; c < D / 8; ++c) {
+                                const uint4 x = lds128(row + (c >> 3) * C::BLOCK + ((c ^ r) & 7) * 16);
+                                acc = fma_bf16x2(x.x, 0u, acc);
+                                acc = fma_bf16x2(x.y, 0u, acc);
+                                acc = fma_bf16x2(x.z, 0u, acc);
+                                acc = fma_bf16x2(x.w, 0u, acc);
+                            }
+                        }
+                        const bool odd = (acc & 0x7FFF7FFFu) != 0u;
+                        words[k] = __ballot_sync(0xffffffffu, odd);
+                        if (odd || pos >= w.L) {
+#pragma unroll
+                            for (int c = 0; c < D / 8; ++c)
+                                sts128u(row + (c >> 3) * C::BLOCK + c % 8 * 16, 0u, 0u, 0u, 0u);
+                        }
+                    }
+                    if (lane < 4)
+                        bad_rows[4 * (n_fix % kFix) + lane] = lane == 0 ? words[0] : lane == 1 ? words[1] : lane == 2 ? words[2] : words[3];
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(bFix + n_fix % kFix));
+                    if (lane == 0) mbar_arrive(bar(bVFree + n % C::SV));
+                    ++n_fix;
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ======================= softmax ==========================================
+        reg_inc<C::REG_SM>();
+        grid_dep_wait();
+        grid_dep_launch();
+        const int grp = (warp - 4) >> 2, wq = warp & 3;
+        const int row_l = 32 * wq + lane;              // this thread's lane of tensor memory
+        const uint32_t tl = tmem + (static_cast<uint32_t>(wq) << 21);  // lanes 32 wq .. (bits 16 and up)
+        const uint32_t tS = tl + 256 * grp, tO = tS + C::O_COL;
+        const int tok_l = row_l / a.G, g_l = row_l - tok_l * a.G;      // its token in the row tile, its head
+        const bool speaker = wq == 0 && lane == 0;     // for its group
+        const float sl = fmaxf(fabsf(a.scale_log2), 1.2e-38f);         // -inf times it stays -inf
+        const float2 sl2 = make_float2(sl, sl);
+        int n = 0, job = 0, n_o = 0, n_fix = 0;        // the CTA's tiles, this group's jobs and items, fixed tiles
+        bool ok = true;
+        for (int i = 0;; ++i) {
+            ok = warp_wait(piece_bar(i), piece_par(i));
+            const Piece w = pieces[i % kPieces];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(bPieceFree + i % kPieces));
+            if (!ok || w.b < 0) break;
+            const int nt = w.t1 - w.t0;
+            if (grp > w.two) {
+                n += nt;
+                n_fix += max(w.t1 - max(w.t0, w.tf), 0);
+                continue;
+            }
+            const bool frees = grp == w.two;           // the tile's last use is this group's
+            const int tok_t = tok_l + grp * a.tile_toks;               // token in the pair of row tiles
+            const bool live = tok_l < a.tile_toks && tok_t < w.toks;
+            const int tok = w.tok0 + tok_t;
+            const int lim = live ? min(w.ctx + tok + 1, w.L) : 0;      // positions that this row sees
+            // tiles that every row of this group sees in full
+            const int inner_end = max(min(w.ctx + w.tok0 + grp * a.tile_toks + 1, w.L), 0) / kTile;
+            float m = -INFINITY, l = 0.f;
+            for (int t = w.t0; t < w.t1; ++t, ++n, ++job) {
+                const bool first = t == w.t0;
+                ok = ok && warp_wait(bar(bS + grp), job & 1);
+                tc_fence_after();
+                if (speaker && ok) {
+                    if (frees) {
+                        mbar_arrive(bar(bKFree + n % C::SK));
+                        if (!first) mbar_arrive(bar(bVFree + (n - 1) % C::SV));
+                    }
+                    if (t == w.t1 - 1) mbar_arrive(bar(bQFree + grp));
+                    if (first) go_on[grp] = 0u;
+                }
+                uint32_t bad[4] = {0u, 0u, 0u, 0u};
+                if (t >= w.tf) {
+                    ok = ok && warp_wait(bar(bFix + n_fix % kFix), (n_fix / kFix) & 1);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) bad[k] = bad_rows[4 * (n_fix % kFix) + k];
+                    ++n_fix;
+                }
+                if (ok) {
+                    const int vis = lim - t * kTile;       // columns that this row sees (any value)
+                    const bool inner = t < inner_end;
+                    const int warp_vis = inner ? kTile : __reduce_max_sync(0xffffffffu, vis);
+                    auto masked = [&](int c, uint32_t (&x)[32]) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * c + e >= vis) x[e] = 0xFF800000u;
+                    };
+                    // Moves the reference to the tile's maximum (rows where `move`), and what is held with it.
+                    auto raise = [&](bool move) {
+                        float mx = -INFINITY;
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            if (32 * c >= warp_vis) break;
+                            uint32_t x[32];
+                            tmem_ld32(tS + 32 * c, x);
+                            tmem_wait_ld();
+                            pin(x);
+                            if (!inner) masked(c, x);
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2)
+                                mx = fmaxf(fmaxf(mx, __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
+                        }
+                        mx *= sl;
+                        const float nm = move && mx > m ? mx : m;
+                        const float al = nm == m ? 1.f : fast_exp2(m - nm);
+                        if (!first && __any_sync(0xffffffffu, nm != m)) {
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[32];
+                                tmem_ld32(tO + 32 * c, o);
+                                tmem_wait_ld();
+                                pin(o);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                                tmem_st32(tO + 32 * c, o);
+                            }
+                        }
+                        l *= al;
+                        m = nm;
+                    };
+                    if (first) raise(true);
+                    uint32_t p[64];
+                    float sum;
+                    // The tile's weights and their sum.
+                    auto weights = [&](auto masks) {
+                        constexpr bool MASK = decltype(masks)::value;
+                        const float mm = m == -INFINITY ? 0.f : -m;
+                        const float2 mm2 = make_float2(mm, mm);
+                        float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                        uint32_t x[2][32];
+                        tmem_ld32(tS, x[0]);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            tmem_wait_ld();
+                            pin(x[c & 1]);
+                            if (c < 3) tmem_ld32(tS + 32 * (c + 1), x[(c + 1) & 1]);
+                            if (MASK && 32 * c >= warp_vis) {
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) p[16 * c + e] = 0u;
+                                continue;
+                            }
+                            if constexpr (MASK) masked(c, x[c & 1]);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float2 y = fma2(make_float2(__uint_as_float(x[c & 1][2 * e]), __uint_as_float(x[c & 1][2 * e + 1])),
+                                                sl2, mm2);
+                                y.x = fast_exp2(y.x);
+                                y.y = fast_exp2(y.y);
+                                s2[e & 1] = add2(s2[e & 1], y);
+                                p[16 * c + e] = pack_bf16(y.x, y.y);
+                            }
+                        }
+                        sum = (s2[0].x + s2[1].x) + (s2[0].y + s2[1].y);
+                    };
+                    auto all_weights = [&]() {
+                        if (inner) weights(std::false_type{});
+                        else weights(std::true_type{});
+                    };
+                    all_weights();
+                    // (a row whose scores so far are all -inf has no reference yet)
+                    const bool again = live && (sum > kRaise || (m == -INFINITY && vis > 0 && !first));
+                    if (__any_sync(0xffffffffu, again)) {
+                        raise(again);
+                        all_weights();
+                    }
+                    l += sum;
+                    {
+                        uint32_t h[32];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) h[e] = p[32 * c + e];
+                            tmem_st32(tS + 32 * c, h);
+                        }
+                    }
+                    tmem_wait_st();
+                    // ---- rows of V that are not finite, for the rows that see them ---------
+                    if ((bad[0] | bad[1] | bad[2] | bad[3]) != 0u) {  // (uniform)
+                        if (first) {  // there is no O yet: it starts here, and P . V goes on from it
+                            uint32_t zero[32];
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) zero[e] = 0u;
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) tmem_st32(tO + 32 * c, zero);
+                            tmem_wait_st();
+                            if (speaker) go_on[grp] = 1u;
+                        }
+#pragma unroll 1
+                        for (int j = 0; j < kTile; ++j) {
+                            if (!(word_of(bad, j >> 5) >> (j & 31) & 1)) continue;
+                            const float pj = tmem_ld_half(tS + (j >> 1), j & 1);
+                            const bool sees = live && j < vis;
+                            const uint16_t* vr = a.v + static_cast<int64_t>(w.k0 + t * kTile + j) * a.v_s0 +
+                                                 static_cast<int64_t>(w.kvh) * a.v_s1;
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[32];
+                                tmem_ld32(tO + 32 * c, o);
+                                tmem_wait_ld();
+                                pin(o);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (sees)
+                                        o[e] = __float_as_uint(fmaf(
+                                            pj, __uint_as_float(static_cast<uint32_t>(vr[32 * c + e]) << 16), __uint_as_float(o[e])));
+                                tmem_st32(tO + 32 * c, o);
+                                tmem_wait_st();
+                            }
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0 && ok) mbar_arrive(bar(bP + grp));
+            }
+            // ---- the piece's output, or its partial sums -----------------------------
+            ok = ok && warp_wait(bar(bO + grp), n_o & 1);
+            ++n_o;
+            if (!ok) break;
+            tc_fence_after();
+            if (speaker && frees) mbar_arrive(bar(bVFree + (n - 1) % C::SV));
+            {
+                const bool none = l == 0.f;
+                const int h = w.kvh * a.G + g_l;
+                const int64_t q_row = w.q0 + tok;
+                const int row = 128 * grp + row_l;             // its place in partial sums
+                const int slot = 2 * static_cast<int>(blockIdx.x) + (w.t0 == 0 ? 1 : 0);
+                const float inv = w.whole ? (none ? 0.f : 1.f / l) : 1.f;
+                if (live) {
+                    if (!w.whole) {
+                        *reinterpret_cast<float2*>(part_ml(a.workspace, slot, row)) = make_float2(m, l);
+                    } else if (a.lse) {
+                        a.lse[q_row * a.l_s0 + h * a.l_s1] = none ? -INFINITY : (m + __log2f(l)) * 0.69314718055994530942f;
+                    }
+                }
+                float* part = part_o<D>(a.workspace, gridDim.x, slot, row);
+                uint16_t* out = a.out + q_row * a.o_s0 + h * a.o_s1;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + 32 * c, o);
+                    tmem_wait_ld();
+                    pin(o);
+                    if (c == D / 32 - 1) {  // O is read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(bOFree + grp));
+                    }
+                    if (!live) continue;
+                    if (w.whole) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(none ? 0.f : __uint_as_float(o[e]) * inv);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            reinterpret_cast<uint4*>(out)[4 * c + e] =
+                                make_uint4(pack_bf16(__uint_as_float(o[8 * e]), __uint_as_float(o[8 * e + 1])),
+                                           pack_bf16(__uint_as_float(o[8 * e + 2]), __uint_as_float(o[8 * e + 3])),
+                                           pack_bf16(__uint_as_float(o[8 * e + 4]), __uint_as_float(o[8 * e + 5])),
+                                           pack_bf16(__uint_as_float(o[8 * e + 6]), __uint_as_float(o[8 * e + 7])));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            *reinterpret_cast<uint4*>(part + static_cast<int64_t>(8 * c + e) * kJoinRows * 4) =
+                                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch_t(const PromptArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+    using C = Cfg<D>;
+    int sms = 0;
+    cudaError_t e = device_sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    // The roles deal out the registers that the kernel is launched with: as many
+    // as assumed, or it would wait for more that never come.
+    static std::atomic<bool> as_assumed{false};
+    if (!as_assumed.load(std::memory_order_relaxed)) {
+        cudaFuncAttributes at{};
+        e = cudaFuncGetAttributes(&at, prompt_kernel<D>);
+        if (e != cudaSuccess) return e;
+        if (at.numRegs * C::THREADS < C::REGS) return cudaErrorInvalidConfiguration;
+        as_assumed.store(true, std::memory_order_relaxed);
+    }
+    e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(prompt_kernel<D>, dim3(sms), dim3(C::THREADS), C::SMEM, s, tq, tk, tv, a);
+    if (e != cudaSuccess) return e;
+    // No sequence has more keys than there are: nothing is cut.
+    if (a.Tk + kItemKeys <= kSnapKeys) return cudaSuccess;
+    TreeArgs j{};
+    j.T = a.T, j.Hq = a.Hq, j.G = a.G, j.tile_toks = a.tile_toks, j.D = D;
+    j.out = a.out, j.o_s0 = a.o_s0, j.o_s1 = a.o_s1;
+    j.lse = a.lse, j.l_s0 = a.l_s0, j.l_s1 = a.l_s1;
+    j.workspace = a.workspace;
+    return launch_row_join(j, sms, s);
+}
+
+}  // namespace
+
+int64_t prompt_attention_workspace(int32_t D, int32_t sm_count) {
+    return kJoinMetaBytes + static_cast<int64_t>(sm_count) * 2 * kJoinRows * (D + 2) * 4;
+}
+
+cudaError_t launch_prompt_attention(const PromptArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                    cudaStream_t s) {
+    return a.D == 128 ? launch_t<128>(a, tq, tk, tv, s) : launch_t<64>(a, tq, tk, tv, s);
+}
+
+}  // namespace pkv
