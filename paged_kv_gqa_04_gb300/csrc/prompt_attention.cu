@@ -34,14 +34,17 @@
 //                 item's first scores are computed while the item before writes
 //                 its output.
 //
-// Softmax. The weights are exp2(score - m) with a reference m per row, which is
-// the maximum of the row's first tile and moves only when a tile's weights sum
-// to more than 2^kRaiseLog2: one pass over S per tile, with no maximum in it.
-// m is a score of the row or more than 2^-kRaiseLog2 of its weights away from
-// one, so nothing that counts underflows. Sums and O are fp32. P meets V as
-// bf16, rounded once (2^-9 of a weight on average less, at most 2^-8): its
-// rounding and the output's are of one size, and independent. A second term, as
-// in the attention of drafted tokens, is half as much tensor work again.
+// Softmax. The weights are exp2(score - m) with a reference m per row: the
+// maximum (rounded up) of the 64 positions where it last moved, which it does
+// where the sum of a tile's first 64 weights passes 2^12. So one pass over S
+// does, with no maximum in it, and O is scaled rarely. A tile's second 64 weights
+// move it past 2^60 only: by then P . V of the first ones may be under way, and
+// the warp has to ask for O to come to rest (pending, at_rest). fp32 holds what
+// is between: nothing that counts underflows, and O stays finite for values up
+// to 2^-60 of fp32's largest. Sums and O are fp32. P meets V as bf16, rounded once (by
+// at most 2^-8 of a weight): that rounding and the output's are of one size, and
+// independent. A second term, as in the attention of drafted tokens, is half as
+// much tensor work again.
 //
 // Waits are bounded (about one second): a role that gives up sets
 // PKV_FLAG_WAIT_TIMEOUT and a CTA-wide flag that ends the others' waits.
@@ -60,9 +63,11 @@ constexpr int kTile = 128;      // positions per tile
 constexpr int kItemKeys = 512;  // what an item costs beyond its tiles, in keys
 constexpr int kSnapKeys = 1536; // longest item (keys and kItemKeys) up to which items are not cut
 constexpr int kPieces = 4;      // ring of pieces
+// Sums of 64 weights past which their row's reference moves: those of a tile's first half; of its second.
+constexpr float kRaise = 4096.f, kMost = 1152921504606846976.f;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
+constexpr uint32_t kPolls = 1u << 25;  // 20 to 40 ns each
 constexpr int kFix = 4;         // ring of the fixed tiles' notes: no fewer than there are stages of V
-constexpr float kRaise = 65536.f;  // sum of a tile's weights that moves the reference
 
 template <int D>
 struct Cfg {
@@ -79,7 +84,7 @@ struct Cfg {
     static constexpr int OFF_K = OFF_Q + 2 * TILE;
     static constexpr int OFF_V = OFF_K + SK * TILE;
     static constexpr int OFF_BAR = OFF_V + SV * TILE;
-    static constexpr int NBAR = 2 * SK + 2 * SV + kFix + 2 * 6 + 1 + 2 * kPieces;
+    static constexpr int NBAR = 2 * SK + 2 * SV + kFix + 2 * 8 + 1 + 2 * kPieces;
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
     static constexpr int OFF_PIECE = (OFF_MISC + 512 + 15) / 16 * 16;  // [kPieces] Piece
     static constexpr int SMEM = OFF_PIECE + kPieces * 80 + 1024;       // + alignment slack
@@ -212,12 +217,9 @@ struct Piece {
     int t0, t1, whole, two;  // whole: all of the item; two: two row tiles
     int tf;                  // tiles before this one are seen in full by every row
     int pad[7];
-    // Keys that row tile g may see, and the columns of tile t among them in steps of 16.
+    // Keys that row tile g may see.
     __device__ __forceinline__ int end(int g, int tile_toks) const {
         return ctx + tok0 + min(toks, (g + 1) * tile_toks);
-    }
-    __device__ __forceinline__ int cols(int g, int t, int tile_toks) const {
-        return min(max((end(g, tile_toks) - t * kTile + 15) & ~15, 16), kTile);
     }
 };
 static_assert(sizeof(Piece) == 80, "as laid out");
@@ -231,13 +233,15 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t s0 = smem_u32(smem);
     enum : int { bKFull = 0, bKFree = C::SK, bVFull = 2 * C::SK, bVFree = bVFull + C::SV, bFix = bVFree + C::SV,
-                 bS = bFix + kFix, bP = bS + 2, bO = bP + 2, bOFree = bO + 2, bQ = bOFree + 2, bQFree = bQ + 2,
+                 bS = bFix + kFix, bP = bS + 2, bX = bP + 4, bO = bX + 2, bOFree = bO + 2, bQ = bOFree + 2, bQFree = bQ + 2,
                  bPiece = bQFree + 2, bPieceFree = bPiece + kPieces, bEnd = bPieceFree + kPieces };
     static_assert(bEnd + 1 == C::NBAR, "barriers");
     auto bar = [&](int i) -> uint32_t { return s0 + C::OFF_BAR + 8 * i; };
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
-    volatile uint32_t* go_on = misc + 2;                       // [2 groups]: O has been started by hand
+    // [2 groups]: warps that want O at rest between the halves of P . V; O is
+    volatile uint32_t* pending = misc + 2;
+    volatile uint32_t* at_rest = misc + 10;
     volatile uint32_t* bad_rows = misc + 64;                   // [kFix][4 words]: rows of V that are not finite
     int64_t* warp_units = reinterpret_cast<int64_t*>(misc + 12);        // [12]
     int* warp_longest = reinterpret_cast<int*>(misc + 36);              // [12]
@@ -260,7 +264,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         for (int i = 0; i < kFix; ++i) mbar_init(bar(bFix + i), 1);
         for (int w = 0; w < 2; ++w) {
             mbar_init(bar(bS + w), 1);
-            mbar_init(bar(bP + w), 4);
+            mbar_init(bar(bP + 2 * w), 4);      // positions 0 - 63 of either group's P
+            mbar_init(bar(bP + 2 * w + 1), 4);  // and the rest
+            mbar_init(bar(bX + w), 1);
             mbar_init(bar(bO + w), 1);
             mbar_init(bar(bOFree + w), 4);
             mbar_init(bar(bQ + w), 1);
@@ -272,6 +278,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         }
         mbar_init(bar(bEnd), 1);
         *abort_flag = 0;
+        pending[0] = pending[1] = at_rest[0] = at_rest[1] = 0u;
         place[0] = place[1] = Place{a.B, 0, 0, 0, 0};
         fence_mbar_init();
         tma_prefetch_desc(&tmq);
@@ -345,21 +352,16 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     const Place from = place[0], to = place[1];
 
     // q, k and v may still be being written by the preceding grid: every role waits for it
-    auto give_up = [&]() {
-        *abort_flag = 1;
-        flag_error(a.err, PKV_FLAG_WAIT_TIMEOUT);
-    };
+    // Polls, and gives up after kPolls of them. (try_wait and a clock are 85 instructions
+    // a wait, these 20: the code of the waits is what the softmax and the MMAs share
+    // the instruction cache with.)
     auto lane_wait = [&](uint32_t bb, uint32_t par) -> bool {
-        if (mbar_test_wait(bb, par)) return true;
-        uint64_t t0 = 0;
-        while (!mbar_try_wait(bb, par)) {
-            const uint64_t now = global_ns();
-            if (t0 == 0) t0 = now;
-            if (*abort_flag || now - t0 > kWaitLimitNs) {
-                give_up();
+#pragma unroll 1
+        for (uint32_t n = 1; !mbar_test_wait(bb, par); ++n)
+            if (n % 4096 == 0 && (*abort_flag || n == kPolls)) {
+                *abort_flag = 1;
                 return false;
             }
-        }
         return true;
     };
     auto warp_wait = [&](uint32_t bb, uint32_t par) -> bool { return __all_sync(0xffffffffu, lane_wait(bb, par)); };
@@ -447,93 +449,170 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             reinterpret_cast<int4*>(a.workspace)[blockIdx.x] = meta;
             for (int g = 0; g < 2; ++g)
                 if (uses[g]) (void)mbar_wait_bounded(bar(bQ + g), (uses[g] - 1) & 1, kWaitLimitNs);
-        } else if (warp == 1 && lane == 0) {
-            // ======================= tensor-core issue (one thread) ===================
+        } else if (warp == 1) {
+            // ======================= tensor-core issue ================================
+            // The whole warp runs this, on values that are the same in every lane, and
+            // one lane issues: see elect_one().
             grid_dep_wait();
+            const bool me = elect_one();
+            auto uniform = [](int x) { return __reduce_or_sync(0xffffffffu, x); };
+            const uint32_t tm = uniform(tmem), smem0 = uniform(s0);
             // the sign of softmax_scale goes into q (bit 13 negates A); N in bits 17 and up
             const uint32_t idesc_qk = umma_idesc(128, 0, 1, 1, false, false) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
             constexpr uint32_t kIdescPv = umma_idesc(128, D, 1, 1, false, true);
             // 128-byte-swizzled operands, 1024 bytes between groups of 8 rows
-            constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
-            auto desc_lo = [](uint32_t addr, uint32_t lead) { return ((addr >> 4) & 0x3FFFu) | (lead >> 4) << 16; };
-            int items[2] = {0, 0}, n_p[2] = {0, 0};
-            int n = 0, n_fix = 0, issued = 0;
-            bool ok = true;
-            // Scores of tile t (the CTA's tile nn) for row tile g.
-            auto scores = [&](const Piece& w, int g, int t, int nn) {
-                if (g == 0) ok = ok && lane_wait(bar(bKFull + nn % C::SK), (nn / C::SK) & 1);
-                if (t == w.t0) ok = ok && lane_wait(bar(bQ + g), items[g]++ & 1);
-                if (!ok) return;
-                tc_fence_after();
-                const uint32_t q = desc_lo(s0 + C::OFF_Q + g * C::TILE, 16);
-                const uint32_t kt = desc_lo(s0 + C::OFF_K + (nn % C::SK) * C::TILE, 16);
-                const uint32_t idesc = idesc_qk | static_cast<uint32_t>(w.cols(g, t, a.tile_toks) >> 3) << 17;
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t at = ((k >> 2) * C::BLOCK + (k & 3) * 32) >> 4;
-                    if (k == 0) umma_ss<true>(tmem + 256 * g, q, kt, kDescHi, idesc);
-                    else umma_ss<false>(tmem + 256 * g, q + at, kt + at, kDescHi, idesc);
-                }
-                umma_commit(bar(bS + g));
-                ++issued;
+            constexpr uint64_t kDescHi = static_cast<uint64_t>((1024 >> 4) | (1u << 14) | (2u << 29)) << 32;
+            auto desc = [](uint32_t addr, uint32_t lead) -> uint64_t { return kDescHi | ((addr >> 4) & 0x3FFFu) | (lead >> 4) << 16; };
+            struct Job {  // what a piece is to the tensor cores
+                int there, nt, two, fix, cols0, cols1;  // fix: its first tile with a note; cols: keys of either row tile from t0 on
             };
-            Piece w, next;
-            w.b = -1;
-            if (lane_wait(piece_bar(0), piece_par(0))) w = pieces[0];
-            if (w.b >= 0) {
-                scores(w, 0, w.t0, 0);
-                if (w.two) scores(w, 1, w.t0, 0);
-            }
-            for (int i = 0; ok && w.b >= 0; ++i) {
-                next.b = -1;
-                for (int t = w.t0; ok && t < w.t1; ++t, ++n) {
-                    for (int g = 0; ok && g <= w.two; ++g) {
-                        if (g == 0) {
-                            if (t >= w.tf) {
-                                ok = lane_wait(bar(bFix + n_fix % kFix), (n_fix / kFix) & 1);
-                                ++n_fix;
-                            } else {
-                                ok = lane_wait(bar(bVFull + n % C::SV), (n / C::SV) & 1);
-                            }
-                        }
-                        ok = ok && lane_wait(bar(bP + g), n_p[g]++ & 1);
-                        // the item before has been read out of O
-                        if (t == w.t0 && items[g] > 1) ok = ok && lane_wait(bar(bOFree + g), (items[g] - 2) & 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t tS = tmem + 256 * g;
-                        const uint32_t vt = desc_lo(s0 + C::OFF_V + (n % C::SV) * C::TILE, C::BLOCK);
-                        const uint32_t more_o = t > w.t0 || go_on[g] != 0u;  // O goes on, or starts
-                        const int steps = w.cols(g, t, a.tile_toks) >> 4;
-                        if (steps == kTile / 16) {
+            auto job_of = [&](const Piece& w) {
+                Job j;
+                j.there = uniform(w.b >= 0);
+                j.nt = uniform(w.t1 - w.t0);
+                j.two = uniform(w.two);
+                j.fix = uniform(max(w.tf - w.t0, 0));
+                j.cols0 = uniform(max(w.end(0, a.tile_toks) - w.t0 * kTile, 0));
+                j.cols1 = uniform(max(w.end(1, a.tile_toks) - w.t0 * kTile, 0));
+                return j;
+            };
+            auto cols_of = [](const Job& j, int g, int t) { return min(max(((g ? j.cols1 : j.cols0) - t * kTile + 15) & ~15, 16), kTile); };
+            // Stages and phases of the next tile of K, of V; per group, in either half of a word: P taken, items
+            // whose scores were begun.
+            int sk = 0, sv = 0, n_fix = 0;
+            uint32_t pk = 0, pv = 0, px = 0, n_p = 0, items = 0;
+            bool ok = true, issued = false;
+            // Scores for row tile g of the tile of K that is next.
+            auto scores = [&](int g, int cols) {
+                const uint64_t q = desc(smem0 + C::OFF_Q + g * C::TILE, 16), kt = desc(smem0 + C::OFF_K + sk * C::TILE, 16);
+                const uint32_t idesc = idesc_qk | static_cast<uint32_t>(cols >> 3) << 17;
+                tc_fence_after();
+                if (me) {
 #pragma unroll
-                            for (int k = 0; k < kTile / 16; ++k)
-                                umma_ts(tS + C::O_COL, tS + 8 * k, vt + k * (2048 >> 4), kDescHi, kIdescPv, k > 0 ? 1u : more_o);
-                        } else {
-                            for (int k = 0; k < steps; ++k)
-                                umma_ts(tS + C::O_COL, tS + 8 * k, vt + k * (2048 >> 4), kDescHi, kIdescPv, k > 0 ? 1u : more_o);
-                        }
-                        ++issued;
-                        if (t + 1 < w.t1) {
-                            scores(w, g, t + 1, n + 1);
-                        } else {
-                            umma_commit(bar(bO + g));
-                            if (g == 0) {
-                                ok = lane_wait(piece_bar(i + 1), piece_par(i + 1));
-                                if (ok) next = pieces[(i + 1) % kPieces];
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t at = ((k >> 2) * C::BLOCK + (k & 3) * 32) >> 4;
+                        umma_ss(tm + 256 * g, q + at, kt + at, idesc, k > 0);
+                    }
+                    umma_commit(bar(bS + g));
+                }
+                issued = true;
+            };
+            auto next_k = [&]() {
+                if (++sk == C::SK) sk = 0, pk ^= 1;
+            };
+            auto next_v = [&]() {
+                if (++sv == C::SV) sv = 0, pv ^= 1;
+            };
+            // P of row tile g, positions 64 h ..
+            auto have_p = [&](int g, int h) {
+                ok = ok && warp_wait(bar(bP + 2 * g + h), n_p >> (16 * g) & 1);
+                if (h == 1 && __any_sync(0xffffffffu, ok && pending[g] != 0u)) {  // (rare)
+                    if (me) umma_commit(bar(bX + g));
+                    ok = warp_wait(bar(bX + g), px >> g & 1);
+                    px ^= 1u << g;
+                    at_rest[g] = 1u;
+                    for (uint32_t k = 0; ok && __any_sync(0xffffffffu, pending[g] != 0u); ++k) ok = k < kPolls && !*abort_flag;
+                    __threadfence_block();
+                    at_rest[g] = 0u;
+                }
+                tc_fence_after();
+            };
+            // The first scores of a piece for row tile g.
+            auto begin = [&](const Job& w, int g) {
+                if (g == 0) ok = ok && warp_wait(bar(bKFull + sk), pk);
+                ok = ok && warp_wait(bar(bQ + g), items >> (16 * g) & 1);
+                items += 1u << (16 * g);
+                if (ok) scores(g, cols_of(w, g, 0));
+                if (g == w.two) next_k();
+            };
+            ok = warp_wait(piece_bar(0), piece_par(0));
+            Job w{}, next{};
+            if (ok) w = job_of(pieces[0]);
+#pragma unroll 1
+            for (int g = 0; ok && w.there && g <= w.two; ++g) begin(w, g);
+#pragma unroll 1
+            for (int i = 0; ok && w.there; ++i) {
+                int t = 0;
+                // Tiles that both row tiles see in full, with another behind them (the code to be fast).
+                if (w.two) {
+#pragma unroll 1
+                    for (const int end = min(w.fix, w.nt - 1); ok && t < end; ++t) {
+                        ok = warp_wait(bar(bVFull + sv), pv);
+                        const uint64_t vt = desc(smem0 + C::OFF_V + sv * C::TILE, C::BLOCK);
+                        const int cols1 = cols_of(w, 1, t + 1), cols0 = cols_of(w, 0, t + 1);
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            if (t == 0 && (items >> (16 * g) & 0xFFFFu) > 1) ok = ok && warp_wait(bar(bOFree + g), items >> (16 * g) & 1);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                if (h == 1 && g == 0) ok = ok && warp_wait(bar(bKFull + sk), pk);
+                                have_p(g, h);
+                                if (!ok) break;
+                                if (me) {
+#pragma unroll
+                                    for (int k = 4 * h; k < 4 * h + 4; ++k)
+                                        umma_ts(tm + 256 * g + C::O_COL, tm + 256 * g + 8 * k, vt + k * (2048 >> 4), kIdescPv, k + t > 0);
+                                }
                             }
-                            if (ok && next.b >= 0 && g <= next.two) scores(next, g, next.t0, n + 1);
+                            if (ok) scores(g, g ? cols1 : cols0);
                         }
+                        n_p += 0x10001u;
+                        next_v();
+                        next_k();
                     }
                 }
-                if (ok && next.b >= 0 && next.two && !w.two) scores(next, 1, next.t0, n);
-                mbar_arrive(bar(bPieceFree + i % kPieces));
+                next.there = next.two = 0;
+#pragma unroll 1
+                for (; ok && t < w.nt; ++t) {
+                    const bool last = t + 1 == w.nt;
+                    if (t >= w.fix) {
+                        ok = warp_wait(bar(bFix + n_fix % kFix), (n_fix / kFix) & 1);
+                        ++n_fix;
+                    } else {
+                        ok = warp_wait(bar(bVFull + sv), pv);
+                    }
+                    const uint64_t vt = desc(smem0 + C::OFF_V + sv * C::TILE, C::BLOCK);
+                    // (the next piece may have scores for a row tile that this one does not have)
+#pragma unroll 1
+                    for (int g = 0; ok && g <= (w.two | (last ? next.two : 0)); ++g) {
+                        if (g <= w.two) {
+                            // the item before has been read out of O
+                            if (t == 0 && (items >> (16 * g) & 0xFFFFu) > 1) ok = warp_wait(bar(bOFree + g), items >> (16 * g) & 1);
+                            const int steps = cols_of(w, g, t) >> 4;
+#pragma unroll 1
+                            for (int h = 0; ok && h < 2; ++h) {
+                                have_p(g, h);
+                                if (ok && me) {
+#pragma unroll 1
+                                    for (int k = 4 * h; k < min(steps, 4 * h + 4); ++k)
+                                        umma_ts(tm + 256 * g + C::O_COL, tm + 256 * g + 8 * k, vt + k * (2048 >> 4), kIdescPv, k + t > 0);
+                                }
+                            }
+                            if (!ok) break;
+                            n_p += 1u << (16 * g);
+                            if (last && me) umma_commit(bar(bO + g));
+                        }
+                        if (!last) {
+                            if (g == 0) ok = warp_wait(bar(bKFull + sk), pk);
+                            if (ok) scores(g, cols_of(w, g, t + 1));
+                            if (g == w.two) next_k();
+                        } else {
+                            if (g == 0) {
+                                ok = warp_wait(piece_bar(i + 1), piece_par(i + 1));
+                                if (ok) next = job_of(pieces[(i + 1) % kPieces]);
+                            }
+                            if (ok && next.there && g <= next.two) begin(next, g);
+                        }
+                    }
+                    next_v();
+                }
+                if (lane == 0) mbar_arrive(bar(bPieceFree + i % kPieces));
                 w = next;
             }
             // Every operation issued is done before the tensor memory is freed: the
             // softmax groups wait for their last O, and a give-up for all of them here.
-            if (!ok && issued > 0) {
-                umma_commit(bar(bEnd));
+            if (!ok && issued) {
+                if (me) umma_commit(bar(bEnd));
                 (void)mbar_wait_bounded(bar(bEnd), 0, kWaitLimitNs);
             }
         } else if (warp == 2) {
@@ -635,7 +714,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                         if (!first) mbar_arrive(bar(bVFree + (n - 1) % C::SV));
                     }
                     if (t == w.t1 - 1) mbar_arrive(bar(bQFree + grp));
-                    if (first) go_on[grp] = 0u;
                 }
                 uint32_t bad[4] = {0u, 0u, 0u, 0u};
                 if (t >= w.tf) {
@@ -644,142 +722,149 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                     for (int k = 0; k < 4; ++k) bad[k] = bad_rows[4 * (n_fix % kFix) + k];
                     ++n_fix;
                 }
-                if (ok) {
-                    const int vis = lim - t * kTile;       // columns that this row sees (any value)
-                    const bool inner = t < inner_end;
-                    const int warp_vis = inner ? kTile : __reduce_max_sync(0xffffffffu, vis);
-                    auto masked = [&](int c, uint32_t (&x)[32]) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (32 * c + e >= vis) x[e] = 0xFF800000u;
-                    };
-                    // Moves the reference to the tile's maximum (rows where `move`), and what is held with it.
-                    auto raise = [&](bool move) {
-                        float mx = -INFINITY;
+                const int vis = lim - t * kTile;           // columns that this row sees (any value)
+                const bool inner = t < inner_end;
+                const bool by_hand = (bad[0] | bad[1] | bad[2] | bad[3]) != 0u;  // (uniform)
+                // O += P V of the positions of one half whose V is not finite
+                auto hand = [&](int half) {
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            if (32 * c >= warp_vis) break;
-                            uint32_t x[32];
-                            tmem_ld32(tS + 32 * c, x);
+                    for (int j = 64 * half; j < 64 * half + 64; ++j) {
+                        if (!(word_of(bad, j >> 5) >> (j & 31) & 1)) continue;
+                        const float pj = tmem_ld_half(tS + (j >> 1), j & 1);
+                        const bool sees = live && j < vis;
+                        const uint16_t* vr = a.v + static_cast<int64_t>(w.k0 + t * kTile + j) * a.v_s0 +
+                                             static_cast<int64_t>(w.kvh) * a.v_s1;
+#pragma unroll 1
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(tO + 16 * c, o);
                             tmem_wait_ld();
-                            pin(x);
-                            if (!inner) masked(c, x);
+                            pin(o);
 #pragma unroll
-                            for (int e = 0; e < 32; e += 2)
-                                mx = fmaxf(fmaxf(mx, __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
-                        }
-                        mx *= sl;
-                        const float nm = move && mx > m ? mx : m;
-                        const float al = nm == m ? 1.f : fast_exp2(m - nm);
-                        if (!first && __any_sync(0xffffffffu, nm != m)) {
-#pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t o[32];
-                                tmem_ld32(tO + 32 * c, o);
-                                tmem_wait_ld();
-                                pin(o);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-                                tmem_st32(tO + 32 * c, o);
-                            }
-                        }
-                        l *= al;
-                        m = nm;
-                    };
-                    if (first) raise(true);
-                    uint32_t p[64];
-                    float sum;
-                    // The tile's weights and their sum.
-                    auto weights = [&](auto masks) {
-                        constexpr bool MASK = decltype(masks)::value;
-                        const float mm = m == -INFINITY ? 0.f : -m;
-                        const float2 mm2 = make_float2(mm, mm);
-                        float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                        uint32_t x[2][32];
-                        tmem_ld32(tS, x[0]);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            tmem_wait_ld();
-                            pin(x[c & 1]);
-                            if (c < 3) tmem_ld32(tS + 32 * (c + 1), x[(c + 1) & 1]);
-                            if (MASK && 32 * c >= warp_vis) {
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) p[16 * c + e] = 0u;
-                                continue;
-                            }
-                            if constexpr (MASK) masked(c, x[c & 1]);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                float2 y = fma2(make_float2(__uint_as_float(x[c & 1][2 * e]), __uint_as_float(x[c & 1][2 * e + 1])),
-                                                sl2, mm2);
-                                y.x = fast_exp2(y.x);
-                                y.y = fast_exp2(y.y);
-                                s2[e & 1] = add2(s2[e & 1], y);
-                                p[16 * c + e] = pack_bf16(y.x, y.y);
-                            }
-                        }
-                        sum = (s2[0].x + s2[1].x) + (s2[0].y + s2[1].y);
-                    };
-                    auto all_weights = [&]() {
-                        if (inner) weights(std::false_type{});
-                        else weights(std::true_type{});
-                    };
-                    all_weights();
-                    // (a row whose scores so far are all -inf has no reference yet)
-                    const bool again = live && (sum > kRaise || (m == -INFINITY && vis > 0 && !first));
-                    if (__any_sync(0xffffffffu, again)) {
-                        raise(again);
-                        all_weights();
-                    }
-                    l += sum;
-                    {
-                        uint32_t h[32];
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) h[e] = p[32 * c + e];
-                            tmem_st32(tS + 32 * c, h);
-                        }
-                    }
-                    tmem_wait_st();
-                    // ---- rows of V that are not finite, for the rows that see them ---------
-                    if ((bad[0] | bad[1] | bad[2] | bad[3]) != 0u) {  // (uniform)
-                        if (first) {  // there is no O yet: it starts here, and P . V goes on from it
-                            uint32_t zero[32];
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) zero[e] = 0u;
-#pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) tmem_st32(tO + 32 * c, zero);
+                            for (int e = 0; e < 16; ++e)
+                                if (sees)
+                                    o[e] = __float_as_uint(fmaf(
+                                        pj, __uint_as_float(static_cast<uint32_t>(vr[16 * c + e]) << 16), __uint_as_float(o[e])));
+                            tmem_st16(tO + 16 * c, o);
                             tmem_wait_st();
-                            if (speaker) go_on[grp] = 1u;
-                        }
-#pragma unroll 1
-                        for (int j = 0; j < kTile; ++j) {
-                            if (!(word_of(bad, j >> 5) >> (j & 31) & 1)) continue;
-                            const float pj = tmem_ld_half(tS + (j >> 1), j & 1);
-                            const bool sees = live && j < vis;
-                            const uint16_t* vr = a.v + static_cast<int64_t>(w.k0 + t * kTile + j) * a.v_s0 +
-                                                 static_cast<int64_t>(w.kvh) * a.v_s1;
-#pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t o[32];
-                                tmem_ld32(tO + 32 * c, o);
-                                tmem_wait_ld();
-                                pin(o);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (sees)
-                                        o[e] = __float_as_uint(fmaf(
-                                            pj, __uint_as_float(static_cast<uint32_t>(vr[32 * c + e]) << 16), __uint_as_float(o[e])));
-                                tmem_st32(tO + 32 * c, o);
-                                tmem_wait_st();
-                            }
                         }
                     }
+                };
+                bool held = false;                     // O is at rest, the tensor cores wait for this warp
+                if (ok) {
+                    // The tile's weights, 64 columns at a time (one short loop: the code of
+                    // a whole tile does not stay in the instruction cache).
+                    bool start = first, raised = false, given = false;  // start: there is no reference yet
+                    float sum0 = 0.f;
+#pragma unroll 1
+                    for (int half = 0; half < 2;) {
+                        const int v = vis - 64 * half; // columns of this half that the row sees
+                        uint32_t p[32];
+                        float sum = 0.f;
+                        if (!start) {
+                            const float mm = m == -INFINITY ? 0.f : -m;
+                            const float2 mm2 = make_float2(mm, mm);
+                            float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                            uint32_t x[2][32];
+                            tmem_ld32(tS + 64 * half, x[0]);
+                            tmem_ld32(tS + 64 * half + 32, x[1]);
+                            tmem_wait_ld();
+                            pin(x[0]);
+                            pin(x[1]);
+                            if (half == 1 && !given) { // the first half's P is there by now
+                                tmem_wait_st();
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(bar(bP + 2 * grp));
+                                given = true;
+                            }
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                if (!inner) {
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e)
+                                        if (32 * c + e >= v) x[c][e] = 0xFF800000u;
+                                }
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    float2 y = fma2(make_float2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), sl2, mm2);
+                                    y.x = fast_exp2(y.x);
+                                    y.y = fast_exp2(y.y);
+                                    s2[e & 1] = add2(s2[e & 1], y);
+                                    p[16 * c + e] = pack_bf16(y.x, y.y);
+                                }
+                            }
+                            sum = (s2[0].x + s2[1].x) + (s2[0].y + s2[1].y);
+                        }
+                        const bool move = live && (sum > (half ? kMost : kRaise) || (m == -INFINITY && v > 0));
+                        const bool raise = start || (!raised && __any_sync(0xffffffffu, move));
+                        if (half == 1 && !held && (raise || by_hand)) {
+                            // P . V of the first half may be under way: O is touched once it is done
+                            __syncwarp();
+                            if (lane == 0) {
+                                atomicAdd(const_cast<uint32_t*>(pending) + grp, 1u);
+                                mbar_arrive(bar(bP + 2 * grp + 1));
+                            }
+                            held = true;
+                            for (uint32_t k = 0; ok && at_rest[grp] == 0u; ++k) ok = k < kPolls && !*abort_flag;
+                            ok = __all_sync(0xffffffffu, ok);
+                            tc_fence_after();
+                            if (!ok) break;
+                            if (by_hand) hand(0);
+                        }
+                        if (raise) {
+                            // The reference of the rows with `move` goes up to the half's maximum (a whole
+                            // number: what is held is scaled by a power of two, exactly), and once more.
+                            float mx = -INFINITY;
+#pragma unroll 1
+                            for (int c = 0; c < 4; ++c) {
+                                uint32_t x[16];
+                                tmem_ld16(tS + 64 * half + 16 * c, x);
+                                tmem_wait_ld();
+                                pin(x);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    if (16 * c + e < v || inner) mx = fmaxf(mx, __uint_as_float(x[e]));
+                            }
+                            const float nm = move || start ? fmaxf(m, ceilf(mx * sl)) : m;
+                            const float up = nm - m;
+                            const float al = up < 126.f ? __uint_as_float((127u - static_cast<uint32_t>(up)) << 23) : 0.f;
+                            const bool moved = __any_sync(0xffffffffu, nm != m);
+                            l *= al;
+                            sum0 *= al;
+                            m = nm;
+                            start = false;
+                            raised = true;
+                            if (moved && (!first || half == 1)) {
+#pragma unroll 1
+                                for (int c = 0; c < D / 16; ++c) {
+                                    uint32_t o[16];
+                                    tmem_ld16(tO + 16 * c, o);
+                                    tmem_wait_ld();
+                                    pin(o);
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                                    tmem_st16(tO + 16 * c, o);
+                                }
+                            }
+                            continue;
+                        }
+                        tmem_st32(tS + 32 * half, p);
+                        sum0 += sum;
+                        raised = false;
+                        ++half;
+                    }
+                    l += sum0;
+                    tmem_wait_st();
+                    if (held && by_hand && ok) hand(1);
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0 && ok) mbar_arrive(bar(bP + grp));
+                if (lane == 0 && held) {
+                    __threadfence_block();
+                    atomicSub(const_cast<uint32_t*>(pending) + grp, 1u);
+                }
+                if (lane == 0 && !held && ok) mbar_arrive(bar(bP + 2 * grp + 1));
             }
             // ---- the piece's output, or its partial sums -----------------------------
             ok = ok && warp_wait(bar(bO + grp), n_o & 1);
@@ -839,6 +924,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (tid == 0 && *abort_flag) flag_error(a.err, PKV_FLAG_WAIT_TIMEOUT);
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
