@@ -63,9 +63,8 @@ constexpr int kTile = 128;      // positions per tile
 constexpr int kItemKeys = 512;  // what an item costs beyond its tiles, in keys
 constexpr int kSnapKeys = 1536; // longest item (keys and kItemKeys) up to which items are not cut
 constexpr int kPieces = 4;      // ring of pieces
-// Sums of 64 weights past which their row's reference moves: those of a tile's first half; of its second.
-constexpr float kRaise = 4096.f, kMost = 1152921504606846976.f;
-constexpr uint64_t kWaitLimitNs = 1000000000ull;
+constexpr float kRaise = 4096.f; // sum of 64 weights past which their row's reference moves
+constexpr uint32_t kWaitLimitNs = 1000000000u;
 constexpr uint32_t kPolls = 1u << 25;  // 20 to 40 ns each
 constexpr int kFix = 4;         // ring of the fixed tiles' notes: no fewer than there are stages of V
 
@@ -75,19 +74,19 @@ struct Cfg {
     static constexpr int TILE = kTile * D * 2;
     static constexpr int BLOCK = kTile * 128;    // one column block of it
     static constexpr int SK = D == 128 ? 2 : 4, SV = D == 128 ? 3 : 4;  // stages of K, of V
-    static constexpr int THREADS = 384;
-    // Registers a thread: launched with 168, dealt out again by role.
-    static constexpr int REG_IO = 88, REG_SM = 208;
-    static constexpr int REGS = 128 * (REG_IO + 2 * REG_SM);
-    static_assert(REGS <= 168 * THREADS, "registers as launched");
+    static constexpr int THREADS = 640;
+    // Registers a thread: launched with 96, dealt out again by role.
+    static constexpr int REG_IO = 64, REG_SM = 104;
+    static constexpr int REGS = 128 * (REG_IO + 4 * REG_SM);
+    static_assert(REGS <= 96 * THREADS, "registers as launched");
     static constexpr int OFF_Q = 0;              // two row tiles of q
     static constexpr int OFF_K = OFF_Q + 2 * TILE;
     static constexpr int OFF_V = OFF_K + SK * TILE;
     static constexpr int OFF_BAR = OFF_V + SV * TILE;
-    static constexpr int NBAR = 2 * SK + 2 * SV + kFix + 2 * 8 + 1 + 2 * kPieces;
+    static constexpr int NBAR = 2 * SK + 2 * SV + kFix + 2 * 6 + 1 + 2 * kPieces;
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
-    static constexpr int OFF_PIECE = (OFF_MISC + 512 + 15) / 16 * 16;  // [kPieces] Piece
-    static constexpr int SMEM = OFF_PIECE + kPieces * 80 + 1024;       // + alignment slack
+    static constexpr int OFF_PIECE = (OFF_MISC + 128 + 2048 + 15) / 16 * 16;  // [kPieces] Piece
+    static constexpr int SMEM = OFF_PIECE + kPieces * 80;
     static_assert(SMEM <= 232448, "shared memory of one CTA");
     // tensor-memory columns of a softmax group: S (P over it), then O
     static constexpr uint32_t O_COL = 128;
@@ -229,23 +228,21 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                   const __grid_constant__ CUtensorMap tmv, const PromptArgs a) {
     using C = Cfg<D>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t s0 = smem_u32(smem);
     enum : int { bKFull = 0, bKFree = C::SK, bVFull = 2 * C::SK, bVFree = bVFull + C::SV, bFix = bVFree + C::SV,
-                 bS = bFix + kFix, bP = bS + 2, bX = bP + 4, bO = bX + 2, bOFree = bO + 2, bQ = bOFree + 2, bQFree = bQ + 2,
+                 bS = bFix + kFix, bP = bS + 2, bO = bP + 2, bOFree = bO + 2, bQ = bOFree + 2, bQFree = bQ + 2,
                  bPiece = bQFree + 2, bPieceFree = bPiece + kPieces, bEnd = bPieceFree + kPieces };
     static_assert(bEnd + 1 == C::NBAR, "barriers");
     auto bar = [&](int i) -> uint32_t { return s0 + C::OFF_BAR + 8 * i; };
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
-    // [2 groups]: warps that want O at rest between the halves of P . V; O is
-    volatile uint32_t* pending = misc + 2;
-    volatile uint32_t* at_rest = misc + 10;
-    volatile uint32_t* bad_rows = misc + 64;                   // [kFix][4 words]: rows of V that are not finite
-    int64_t* warp_units = reinterpret_cast<int64_t*>(misc + 12);        // [12]
-    int* warp_longest = reinterpret_cast<int*>(misc + 36);              // [12]
-    Place* place = reinterpret_cast<Place*>(misc + 48);                 // [2]: from, to
+    volatile uint32_t* go_on = misc + 2;                       // [2 groups]: O has been started by hand
+    volatile uint32_t* bad_rows = misc + 4;                    // [kFix][4 words]: rows of V that are not finite
+    Place* place = reinterpret_cast<Place*>(misc + 20);                 // [2]: from, to
+    int64_t* warp_units = reinterpret_cast<int64_t*>(misc + 32);        // [THREADS / 32]
+    int* warp_longest = reinterpret_cast<int*>(misc + 72);              // [THREADS / 32]
+    float* theirs = reinterpret_cast<float*>(misc + 32);                // (later) [2 groups][2 halves][128 rows]: what the halves tell each other
     static_assert(sizeof(Place) == 24, "as laid out");
     Piece* pieces = reinterpret_cast<Piece*>(smem + C::OFF_PIECE);
 
@@ -264,21 +261,18 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         for (int i = 0; i < kFix; ++i) mbar_init(bar(bFix + i), 1);
         for (int w = 0; w < 2; ++w) {
             mbar_init(bar(bS + w), 1);
-            mbar_init(bar(bP + 2 * w), 4);      // positions 0 - 63 of either group's P
-            mbar_init(bar(bP + 2 * w + 1), 4);  // and the rest
-            mbar_init(bar(bX + w), 1);
+            mbar_init(bar(bP + w), 8);
             mbar_init(bar(bO + w), 1);
-            mbar_init(bar(bOFree + w), 4);
+            mbar_init(bar(bOFree + w), 8);
             mbar_init(bar(bQ + w), 1);
             mbar_init(bar(bQFree + w), 1);
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(bar(bPiece + i), 1);
-            mbar_init(bar(bPieceFree + i), 11);  // copies, MMA, V, softmax
+            mbar_init(bar(bPieceFree + i), 19);  // copies, MMA, V, softmax
         }
         mbar_init(bar(bEnd), 1);
         *abort_flag = 0;
-        pending[0] = pending[1] = at_rest[0] = at_rest[1] = 0u;
         place[0] = place[1] = Place{a.B, 0, 0, 0, 0};
         fence_mbar_init();
         tma_prefetch_desc(&tmq);
@@ -352,16 +346,18 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     const Place from = place[0], to = place[1];
 
     // q, k and v may still be being written by the preceding grid: every role waits for it
-    // Polls, and gives up after kPolls of them. (try_wait and a clock are 85 instructions
-    // a wait, these 20: the code of the waits is what the softmax and the MMAs share
-    // the instruction cache with.)
+    // (small: the code of the waits is what the softmax and the MMAs share the instruction cache with)
     auto lane_wait = [&](uint32_t bb, uint32_t par) -> bool {
+        uint32_t t0 = 0;
 #pragma unroll 1
-        for (uint32_t n = 1; !mbar_test_wait(bb, par); ++n)
-            if (n % 4096 == 0 && (*abort_flag || n == kPolls)) {
+        while (!mbar_try_wait(bb, par)) {
+            const uint32_t now = global_ns_lo() | 1u;
+            if (t0 == 0) t0 = now;
+            if (*abort_flag || now - t0 > kWaitLimitNs) {
                 *abort_flag = 1;
                 return false;
             }
+        }
         return true;
     };
     auto warp_wait = [&](uint32_t bb, uint32_t par) -> bool { return __all_sync(0xffffffffu, lane_wait(bb, par)); };
@@ -480,7 +476,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             // Stages and phases of the next tile of K, of V; per group, in either half of a word: P taken, items
             // whose scores were begun.
             int sk = 0, sv = 0, n_fix = 0;
-            uint32_t pk = 0, pv = 0, px = 0, n_p = 0, items = 0;
+            uint32_t pk = 0, pv = 0, n_p = 0, items = 0;
             bool ok = true, issued = false;
             // Scores for row tile g of the tile of K that is next.
             auto scores = [&](int g, int cols) {
@@ -502,20 +498,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             };
             auto next_v = [&]() {
                 if (++sv == C::SV) sv = 0, pv ^= 1;
-            };
-            // P of row tile g, positions 64 h ..
-            auto have_p = [&](int g, int h) {
-                ok = ok && warp_wait(bar(bP + 2 * g + h), n_p >> (16 * g) & 1);
-                if (h == 1 && __any_sync(0xffffffffu, ok && pending[g] != 0u)) {  // (rare)
-                    if (me) umma_commit(bar(bX + g));
-                    ok = warp_wait(bar(bX + g), px >> g & 1);
-                    px ^= 1u << g;
-                    at_rest[g] = 1u;
-                    for (uint32_t k = 0; ok && __any_sync(0xffffffffu, pending[g] != 0u); ++k) ok = k < kPolls && !*abort_flag;
-                    __threadfence_block();
-                    at_rest[g] = 0u;
-                }
-                tc_fence_after();
             };
             // The first scores of a piece for row tile g.
             auto begin = [&](const Job& w, int g) {
@@ -543,18 +525,17 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
                             if (t == 0 && (items >> (16 * g) & 0xFFFFu) > 1) ok = ok && warp_wait(bar(bOFree + g), items >> (16 * g) & 1);
+                            if (g == 0) ok = ok && warp_wait(bar(bKFull + sk), pk);
+                            ok = ok && warp_wait(bar(bP + g), n_p >> (16 * g) & 1);
+                            if (!ok) break;
+                            tc_fence_after();
+                            if (me) {
+                                const uint32_t more_o = t > 0 ? 1u : go_on[g];  // O goes on, or starts
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                if (h == 1 && g == 0) ok = ok && warp_wait(bar(bKFull + sk), pk);
-                                have_p(g, h);
-                                if (!ok) break;
-                                if (me) {
-#pragma unroll
-                                    for (int k = 4 * h; k < 4 * h + 4; ++k)
-                                        umma_ts(tm + 256 * g + C::O_COL, tm + 256 * g + 8 * k, vt + k * (2048 >> 4), kIdescPv, k + t > 0);
-                                }
+                                for (int k = 0; k < kTile / 16; ++k)
+                                    umma_ts(tm + 256 * g + C::O_COL, tm + 256 * g + 8 * k, vt + k * (2048 >> 4), kIdescPv, k > 0 ? 1u : more_o);
                             }
-                            if (ok) scores(g, g ? cols1 : cols0);
+                            scores(g, g ? cols1 : cols0);
                         }
                         n_p += 0x10001u;
                         next_v();
@@ -579,17 +560,16 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                             // the item before has been read out of O
                             if (t == 0 && (items >> (16 * g) & 0xFFFFu) > 1) ok = warp_wait(bar(bOFree + g), items >> (16 * g) & 1);
                             const int steps = cols_of(w, g, t) >> 4;
-#pragma unroll 1
-                            for (int h = 0; ok && h < 2; ++h) {
-                                have_p(g, h);
-                                if (ok && me) {
-#pragma unroll 1
-                                    for (int k = 4 * h; k < min(steps, 4 * h + 4); ++k)
-                                        umma_ts(tm + 256 * g + C::O_COL, tm + 256 * g + 8 * k, vt + k * (2048 >> 4), kIdescPv, k + t > 0);
-                                }
-                            }
+                            ok = ok && warp_wait(bar(bP + g), n_p >> (16 * g) & 1);
                             if (!ok) break;
                             n_p += 1u << (16 * g);
+                            tc_fence_after();
+                            if (me) {
+                                const uint32_t more_o = t > 0 ? 1u : go_on[g];
+#pragma unroll 1
+                                for (int k = 0; k < steps; ++k)
+                                    umma_ts(tm + 256 * g + C::O_COL, tm + 256 * g + 8 * k, vt + k * (2048 >> 4), kIdescPv, k > 0 ? 1u : more_o);
+                            }
                             if (last && me) umma_commit(bar(bO + g));
                         }
                         if (!last) {
@@ -674,38 +654,43 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         reg_inc<C::REG_SM>();
         grid_dep_wait();
         grid_dep_launch();
-        const int grp = (warp - 4) >> 2, wq = warp & 3;
+        const int grp = (warp - 4) >> 3, half = (warp - 4) >> 2 & 1, wq = warp & 3;
         const int row_l = 32 * wq + lane;              // this thread's lane of tensor memory
         const uint32_t tl = tmem + (static_cast<uint32_t>(wq) << 21);  // lanes 32 wq .. (bits 16 and up)
-        const uint32_t tS = tl + 256 * grp, tO = tS + C::O_COL;
+        // its columns of S, of P, of O (the row's other half is warp + 4's or warp - 4's)
+        const uint32_t tS = tl + 256 * grp + 64 * half, tP = tl + 256 * grp + 32 * half;
+        const uint32_t tO = tl + 256 * grp + C::O_COL + D / 2 * half;
         const int tok_l = row_l / a.G, g_l = row_l - tok_l * a.G;      // its token in the row tile, its head
-        const bool speaker = wq == 0 && lane == 0;     // for its group
+        const bool speaker = wq == 0 && half == 0 && lane == 0;        // for its group
+        const int pair = 1 + 4 * grp + wq;             // barrier of the two warps that share rows
+        float* mine = theirs + (2 * grp + half) * 128 + row_l;
+        const float* other = theirs + (2 * grp + 1 - half) * 128 + row_l;
         const float sl = fmaxf(fabsf(a.scale_log2), 1.2e-38f);         // -inf times it stays -inf
         const float2 sl2 = make_float2(sl, sl);
         int n = 0, job = 0, n_o = 0, n_fix = 0;        // the CTA's tiles, this group's jobs and items, fixed tiles
         bool ok = true;
         for (int i = 0;; ++i) {
             ok = warp_wait(piece_bar(i), piece_par(i));
-            const Piece w = pieces[i % kPieces];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(bPieceFree + i % kPieces));
+            const Piece& w = pieces[i % kPieces];
             if (!ok || w.b < 0) break;
-            const int nt = w.t1 - w.t0;
+            const int t0 = w.t0, t1 = w.t1, tf = w.tf;
             if (grp > w.two) {
-                n += nt;
-                n_fix += max(w.t1 - max(w.t0, w.tf), 0);
+                n += t1 - t0;
+                n_fix += max(t1 - max(t0, tf), 0);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(bPieceFree + i % kPieces));
                 continue;
             }
-            const bool frees = grp == w.two;           // the tile's last use is this group's
+            const bool frees = speaker && grp == w.two;                // the tile's last use is this group's
             const int tok_t = tok_l + grp * a.tile_toks;               // token in the pair of row tiles
             const bool live = tok_l < a.tile_toks && tok_t < w.toks;
             const int tok = w.tok0 + tok_t;
             const int lim = live ? min(w.ctx + tok + 1, w.L) : 0;      // positions that this row sees
             // tiles that every row of this group sees in full
             const int inner_end = max(min(w.ctx + w.tok0 + grp * a.tile_toks + 1, w.L), 0) / kTile;
-            float m = -INFINITY, l = 0.f;
-            for (int t = w.t0; t < w.t1; ++t, ++n, ++job) {
-                const bool first = t == w.t0;
+            float m = -INFINITY, l = 0.f;              // (l: of this half's columns)
+            for (int t = t0; t < t1; ++t, ++n, ++job) {
+                const bool first = t == t0;
                 ok = ok && warp_wait(bar(bS + grp), job & 1);
                 tc_fence_after();
                 if (speaker && ok) {
@@ -713,81 +698,45 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                         mbar_arrive(bar(bKFree + n % C::SK));
                         if (!first) mbar_arrive(bar(bVFree + (n - 1) % C::SV));
                     }
-                    if (t == w.t1 - 1) mbar_arrive(bar(bQFree + grp));
+                    if (t == t1 - 1) mbar_arrive(bar(bQFree + grp));
+                    if (first) go_on[grp] = 0u;
                 }
                 uint32_t bad[4] = {0u, 0u, 0u, 0u};
-                if (t >= w.tf) {
+                if (t >= tf) {
                     ok = ok && warp_wait(bar(bFix + n_fix % kFix), (n_fix / kFix) & 1);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) bad[k] = bad_rows[4 * (n_fix % kFix) + k];
                     ++n_fix;
                 }
-                const int vis = lim - t * kTile;           // columns that this row sees (any value)
+                const int vis = lim - t * kTile - 64 * half;   // of this half's columns, those that the row sees
                 const bool inner = t < inner_end;
-                const bool by_hand = (bad[0] | bad[1] | bad[2] | bad[3]) != 0u;  // (uniform)
-                // O += P V of the positions of one half whose V is not finite
-                auto hand = [&](int half) {
-#pragma unroll 1
-                    for (int j = 64 * half; j < 64 * half + 64; ++j) {
-                        if (!(word_of(bad, j >> 5) >> (j & 31) & 1)) continue;
-                        const float pj = tmem_ld_half(tS + (j >> 1), j & 1);
-                        const bool sees = live && j < vis;
-                        const uint16_t* vr = a.v + static_cast<int64_t>(w.k0 + t * kTile + j) * a.v_s0 +
-                                             static_cast<int64_t>(w.kvh) * a.v_s1;
-#pragma unroll 1
-                        for (int c = 0; c < D / 16; ++c) {
-                            uint32_t o[16];
-                            tmem_ld16(tO + 16 * c, o);
-                            tmem_wait_ld();
-                            pin(o);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                if (sees)
-                                    o[e] = __float_as_uint(fmaf(
-                                        pj, __uint_as_float(static_cast<uint32_t>(vr[16 * c + e]) << 16), __uint_as_float(o[e])));
-                            tmem_st16(tO + 16 * c, o);
-                            tmem_wait_st();
-                        }
-                    }
-                };
-                bool held = false;                     // O is at rest, the tensor cores wait for this warp
                 if (ok) {
-                    // The tile's weights, 64 columns at a time (one short loop: the code of
-                    // a whole tile does not stay in the instruction cache).
-                    bool start = first, raised = false, given = false;  // start: there is no reference yet
-                    float sum0 = 0.f;
+                    // The half's weights; where their sum asks for another reference, twice.
+                    bool start = first;                // there is no reference yet
+                    uint32_t p[32];
+                    float sum;
+                    bool raised = false;
 #pragma unroll 1
-                    for (int half = 0; half < 2;) {
-                        const int v = vis - 64 * half; // columns of this half that the row sees
-                        uint32_t p[32];
-                        float sum = 0.f;
+                    for (;;) {
+                        sum = 0.f;
                         if (!start) {
                             const float mm = m == -INFINITY ? 0.f : -m;
                             const float2 mm2 = make_float2(mm, mm);
                             float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                            uint32_t x[2][32];
-                            tmem_ld32(tS + 64 * half, x[0]);
-                            tmem_ld32(tS + 64 * half + 32, x[1]);
-                            tmem_wait_ld();
-                            pin(x[0]);
-                            pin(x[1]);
-                            if (half == 1 && !given) { // the first half's P is there by now
-                                tmem_wait_st();
-                                tc_fence_before();
-                                __syncwarp();
-                                if (lane == 0) mbar_arrive(bar(bP + 2 * grp));
-                                given = true;
-                            }
 #pragma unroll
                             for (int c = 0; c < 2; ++c) {
+                                uint32_t x[32];
+                                tmem_ld32(tS + 32 * c, x);
+                                tmem_wait_ld();
+                                pin(x);
                                 if (!inner) {
 #pragma unroll
                                     for (int e = 0; e < 32; ++e)
-                                        if (32 * c + e >= v) x[c][e] = 0xFF800000u;
+                                        if (32 * c + e >= vis) x[e] = 0xFF800000u;
                                 }
 #pragma unroll
                                 for (int e = 0; e < 16; ++e) {
-                                    float2 y = fma2(make_float2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), sl2, mm2);
+                                    float2 y = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sl2, mm2);
                                     y.x = fast_exp2(y.x);
                                     y.y = fast_exp2(y.y);
                                     s2[e & 1] = add2(s2[e & 1], y);
@@ -795,112 +744,129 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                                 }
                             }
                             sum = (s2[0].x + s2[1].x) + (s2[0].y + s2[1].y);
+                            // (also: both have read S, and P may go over it)
+                            const bool move = !raised && live && (sum > kRaise || (m == -INFINITY && vis > 0));
+                            if (named_bar_and(pair, 64, !move)) break;
                         }
-                        const bool move = live && (sum > (half ? kMost : kRaise) || (m == -INFINITY && v > 0));
-                        const bool raise = start || (!raised && __any_sync(0xffffffffu, move));
-                        if (half == 1 && !held && (raise || by_hand)) {
-                            // P . V of the first half may be under way: O is touched once it is done
-                            __syncwarp();
-                            if (lane == 0) {
-                                atomicAdd(const_cast<uint32_t*>(pending) + grp, 1u);
-                                mbar_arrive(bar(bP + 2 * grp + 1));
-                            }
-                            held = true;
-                            for (uint32_t k = 0; ok && at_rest[grp] == 0u; ++k) ok = k < kPolls && !*abort_flag;
-                            ok = __all_sync(0xffffffffu, ok);
-                            tc_fence_after();
-                            if (!ok) break;
-                            if (by_hand) hand(0);
-                        }
-                        if (raise) {
-                            // The reference of the rows with `move` goes up to the half's maximum (a whole
-                            // number: what is held is scaled by a power of two, exactly), and once more.
-                            float mx = -INFINITY;
+                        // The reference goes up to the tile's maximum (a whole number: what is held is
+                        // scaled by a power of two, exactly).
+                        float mx = -INFINITY;
 #pragma unroll 1
-                            for (int c = 0; c < 4; ++c) {
-                                uint32_t x[16];
-                                tmem_ld16(tS + 64 * half + 16 * c, x);
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t x[16];
+                            tmem_ld16(tS + 16 * c, x);
+                            tmem_wait_ld();
+                            pin(x);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if (16 * c + e < vis || inner) mx = fmaxf(mx, __uint_as_float(x[e]));
+                        }
+                        *mine = mx;
+                        (void)named_bar_and(pair, 64, true);
+                        mx = fmaxf(mx, *other);
+                        const float nm = fmaxf(m, ceilf(mx * sl)), up = nm - m;
+                        const float al = up < 126.f ? __uint_as_float((127u - static_cast<uint32_t>(up)) << 23) : 0.f;
+                        l *= al;
+                        m = nm;
+                        if (!first) {
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[16];
+                                tmem_ld16(tO + 16 * c, o);
                                 tmem_wait_ld();
-                                pin(x);
+                                pin(o);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                                tmem_st16(tO + 16 * c, o);
+                            }
+                        }
+                        start = false;
+                        raised = true;
+                    }
+                    tmem_st32(tP, p);
+                    l += sum;
+                    tmem_wait_st();
+                    // ---- rows of V that are not finite, for the rows that see them ---------
+                    if ((bad[0] | bad[1] | bad[2] | bad[3]) != 0u) {  // (uniform)
+                        if (first) {  // there is no O yet: it starts here, and P . V goes on from it
+                            uint32_t zero[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) zero[e] = 0u;
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) tmem_st16(tO + 16 * c, zero);
+                            tmem_wait_st();
+                            if (speaker) go_on[grp] = 1u;
+                        }
+                        tc_fence_before();
+                        (void)named_bar_and(pair, 64, true);
+                        tc_fence_after();
+                        const int sees = live ? vis + 64 * half : 0;
+#pragma unroll 1
+                        for (int j = 0; j < kTile; ++j) {
+                            if (!(word_of(bad, j >> 5) >> (j & 31) & 1)) continue;
+                            const float pj = tmem_ld_half(tl + 256 * grp + (j >> 1), j & 1);
+                            const uint16_t* vr = a.v + static_cast<int64_t>(w.k0 + t * kTile + j) * a.v_s0 +
+                                                 static_cast<int64_t>(w.kvh) * a.v_s1 + D / 2 * half;
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[16];
+                                tmem_ld16(tO + 16 * c, o);
+                                tmem_wait_ld();
+                                pin(o);
 #pragma unroll
                                 for (int e = 0; e < 16; ++e)
-                                    if (16 * c + e < v || inner) mx = fmaxf(mx, __uint_as_float(x[e]));
+                                    if (j < sees)
+                                        o[e] = __float_as_uint(fmaf(
+                                            pj, __uint_as_float(static_cast<uint32_t>(vr[16 * c + e]) << 16), __uint_as_float(o[e])));
+                                tmem_st16(tO + 16 * c, o);
+                                tmem_wait_st();
                             }
-                            const float nm = move || start ? fmaxf(m, ceilf(mx * sl)) : m;
-                            const float up = nm - m;
-                            const float al = up < 126.f ? __uint_as_float((127u - static_cast<uint32_t>(up)) << 23) : 0.f;
-                            const bool moved = __any_sync(0xffffffffu, nm != m);
-                            l *= al;
-                            sum0 *= al;
-                            m = nm;
-                            start = false;
-                            raised = true;
-                            if (moved && (!first || half == 1)) {
-#pragma unroll 1
-                                for (int c = 0; c < D / 16; ++c) {
-                                    uint32_t o[16];
-                                    tmem_ld16(tO + 16 * c, o);
-                                    tmem_wait_ld();
-                                    pin(o);
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-                                    tmem_st16(tO + 16 * c, o);
-                                }
-                            }
-                            continue;
                         }
-                        tmem_st32(tS + 32 * half, p);
-                        sum0 += sum;
-                        raised = false;
-                        ++half;
                     }
-                    l += sum0;
-                    tmem_wait_st();
-                    if (held && by_hand && ok) hand(1);
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0 && held) {
-                    __threadfence_block();
-                    atomicSub(const_cast<uint32_t*>(pending) + grp, 1u);
-                }
-                if (lane == 0 && !held && ok) mbar_arrive(bar(bP + 2 * grp + 1));
+                if (lane == 0 && ok) mbar_arrive(bar(bP + grp));
             }
             // ---- the piece's output, or its partial sums -----------------------------
             ok = ok && warp_wait(bar(bO + grp), n_o & 1);
             ++n_o;
             if (!ok) break;
             tc_fence_after();
-            if (speaker && frees) mbar_arrive(bar(bVFree + (n - 1) % C::SV));
+            if (frees) mbar_arrive(bar(bVFree + (n - 1) % C::SV));
             {
-                const bool none = l == 0.f;
+                *mine = l;
+                (void)named_bar_and(pair, 64, true);
+                l += *other;
+                (void)named_bar_and(pair, 64, true);
+                const bool none = l == 0.f, whole = w.whole;
                 const int h = w.kvh * a.G + g_l;
                 const int64_t q_row = w.q0 + tok;
                 const int row = 128 * grp + row_l;             // its place in partial sums
-                const int slot = 2 * static_cast<int>(blockIdx.x) + (w.t0 == 0 ? 1 : 0);
-                const float inv = w.whole ? (none ? 0.f : 1.f / l) : 1.f;
-                if (live) {
-                    if (!w.whole) {
+                const int slot = 2 * static_cast<int>(blockIdx.x) + (t0 == 0 ? 1 : 0);
+                const float inv = whole ? (none ? 0.f : 1.f / l) : 1.f;
+                if (live && half == 0) {
+                    if (!whole) {
                         *reinterpret_cast<float2*>(part_ml(a.workspace, slot, row)) = make_float2(m, l);
                     } else if (a.lse) {
                         a.lse[q_row * a.l_s0 + h * a.l_s1] = none ? -INFINITY : (m + __log2f(l)) * 0.69314718055994530942f;
                     }
                 }
-                float* part = part_o<D>(a.workspace, gridDim.x, slot, row);
-                uint16_t* out = a.out + q_row * a.o_s0 + h * a.o_s1;
+                float* part = part_o<D>(a.workspace, gridDim.x, slot, row) + static_cast<int64_t>(D / 8 * half) * kJoinRows * 4;
+                uint16_t* out = a.out + q_row * a.o_s0 + h * a.o_s1 + D / 2 * half;
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
+                for (int c = 0; c < D / 64; ++c) {
                     uint32_t o[32];
                     tmem_ld32(tO + 32 * c, o);
                     tmem_wait_ld();
                     pin(o);
-                    if (c == D / 32 - 1) {  // O is read
+                    if (c == D / 64 - 1) {  // O is read
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(bOFree + grp));
                     }
                     if (!live) continue;
-                    if (w.whole) {
+                    if (whole) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(none ? 0.f : __uint_as_float(o[e]) * inv);
 #pragma unroll
@@ -918,6 +884,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                     }
                 }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(bPieceFree + i % kPieces));
         }
     }
 
