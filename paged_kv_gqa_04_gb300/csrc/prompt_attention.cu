@@ -65,7 +65,7 @@ constexpr int kSnapKeys = 1536; // longest item (keys and kItemKeys) up to which
 constexpr int kPieces = 4;      // ring of pieces
 constexpr float kRaise = 4096.f; // sum of 64 weights past which their row's reference moves
 constexpr uint32_t kWaitLimitNs = 1000000000u;
-constexpr uint32_t kPolls = 1u << 25;  // 20 to 40 ns each
+constexpr uint32_t kPolls = 1u << 24;  // 40 to 80 ns each
 constexpr int kFix = 4;         // ring of the fixed tiles' notes: no fewer than there are stages of V
 
 template <int D>
@@ -75,10 +75,8 @@ struct Cfg {
     static constexpr int BLOCK = kTile * 128;    // one column block of it
     static constexpr int SK = D == 128 ? 2 : 4, SV = D == 128 ? 3 : 4;  // stages of K, of V
     static constexpr int THREADS = 640;
-    // Registers a thread: launched with 96, dealt out again by role.
-    static constexpr int REG_IO = 64, REG_SM = 104;
-    static constexpr int REGS = 128 * (REG_IO + 4 * REG_SM);
-    static_assert(REGS <= 96 * THREADS, "registers as launched");
+    // (96 registers a thread, the same for all roles: handing them over from the copies' and the MMAs' warps made
+    // those spill, which took 10% more)
     static constexpr int OFF_Q = 0;              // two row tiles of q
     static constexpr int OFF_K = OFF_Q + 2 * TILE;
     static constexpr int OFF_V = OFF_K + SK * TILE;
@@ -215,11 +213,8 @@ struct Piece {
     int L, ctx, tok0, toks;
     int t0, t1, whole, two;  // whole: all of the item; two: two row tiles
     int tf;                  // tiles before this one are seen in full by every row
-    int pad[7];
-    // Keys that row tile g may see.
-    __device__ __forceinline__ int end(int g, int tile_toks) const {
-        return ctx + tok0 + min(toks, (g + 1) * tile_toks);
-    }
+    int end[2];              // keys that either row tile may see
+    int pad[5];
 };
 static_assert(sizeof(Piece) == 80, "as laid out");
 
@@ -345,54 +340,62 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     const uint32_t tmem = misc[0];
     const Place from = place[0], to = place[1];
 
-    // q, k and v may still be being written by the preceding grid: every role waits for it
-    // (small: the code of the waits is what the softmax and the MMAs share the instruction cache with)
-    auto lane_wait = [&](uint32_t bb, uint32_t par) -> bool {
-        uint32_t t0 = 0;
+    // q, k and v may still be being written by the preceding grid: every role waits for it.
+    //
+    // A wait that gives up raises the CTA's flag and returns like any other: what
+    // follows works on what is there, in bounds, until the role sees the flag at its
+    // next piece. (Results to look at are branches, which cost more here than the
+    // waits: a wait for a barrier that is complete takes 45 cycles, with its result
+    // voted on and branched upon 180.)
+    auto lane_wait = [&](uint32_t bb, uint32_t par) {
+        uint32_t n = 0;
 #pragma unroll 1
-        while (!mbar_try_wait(bb, par)) {
-            const uint32_t now = global_ns_lo() | 1u;
-            if (t0 == 0) t0 = now;
-            if (*abort_flag || now - t0 > kWaitLimitNs) {
+        while (!mbar_test_wait(bb, par))
+            if (++n == kPolls || *abort_flag) {
                 *abort_flag = 1;
-                return false;
+                break;
             }
-        }
-        return true;
     };
-    auto warp_wait = [&](uint32_t bb, uint32_t par) -> bool { return __all_sync(0xffffffffu, lane_wait(bb, par)); };
+    auto warp_wait = [&](uint32_t bb, uint32_t par) {
+        uint32_t n = 0;
+#pragma unroll 1
+        while (!__any_sync(0xffffffffu, mbar_test_wait(bb, par)))
+            if (__any_sync(0xffffffffu, ++n == kPolls || *abort_flag)) {
+                *abort_flag = 1;
+                break;
+            }
+    };
     auto piece_bar = [&](int i) { return bar(bPiece + i % kPieces); };
     auto piece_par = [](int i) -> uint32_t { return (i / kPieces) & 1; };
 
     if (warp < 4) {
-        reg_dec<C::REG_IO>();
+        if constexpr (D == 64) reg_dec<96>();
         if (warp == 0 && lane == 0) {
             // ======================= copies of K and V ================================
             grid_dep_wait();
             int n = 0;  // tiles
-            bool ok = true;
-            for (int i = 0; ok; ++i) {
-                if (!lane_wait(piece_bar(i), piece_par(i))) break;
+            for (int i = 0;; ++i) {
+                lane_wait(piece_bar(i), piece_par(i));
                 const Piece w = pieces[i % kPieces];
                 mbar_arrive(bar(bPieceFree + i % kPieces));
-                if (w.b < 0) break;
+                if (w.b < 0 || *abort_flag) break;
                 for (int t = w.t0; t < w.t1; ++t, ++n) {
                     const int row = w.k0 + t * kTile;
                     const int sk = n % C::SK, sv = n % C::SV;
-                    if (n >= C::SK && !(ok = lane_wait(bar(bKFree + sk), (n / C::SK - 1) & 1))) break;
+                    if (n >= C::SK) lane_wait(bar(bKFree + sk), (n / C::SK - 1) & 1);
                     mbar_arrive_expect_tx(bar(bKFull + sk), C::TILE);
                     for (int c = 0; c < C::NB; ++c)
                         tma_load_3d(s0 + C::OFF_K + sk * C::TILE + c * C::BLOCK, &tmk, bar(bKFull + sk), 64 * c, w.kvh,
                                     row);
-                    if (n >= C::SV && !(ok = lane_wait(bar(bVFree + sv), (n / C::SV - 1) & 1))) {
-                        // (this tile's K is on its way, its V is not)
-                        (void)mbar_wait_bounded(bar(bKFull + sk), (n / C::SK) & 1, kWaitLimitNs);
-                        break;
-                    }
+                    if (n >= C::SV) lane_wait(bar(bVFree + sv), (n / C::SV - 1) & 1);
                     mbar_arrive_expect_tx(bar(bVFull + sv), C::TILE);
                     for (int c = 0; c < C::NB; ++c)
                         tma_load_3d(s0 + C::OFF_V + sv * C::TILE + c * C::BLOCK, &tmv, bar(bVFull + sv), 64 * c, w.kvh,
                                     row);
+                    if (*abort_flag) {
+                        ++n;
+                        break;
+                    }
                 }
             }
             // Copies under way land before the CTA may exit.
@@ -406,9 +409,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             const Cuts cuts(total, gridDim.x);
             const uint64_t policy = l2_policy_evict_first();
             int uses[2] = {0, 0};
-            bool ok = true;
             Walk walk(from, to);
-            for (int i = 0; ok; ++i) {
+            for (int i = 0;; ++i) {
                 Piece w{};
                 w.b = walk.next(a) ? walk.b : -1;
                 if (w.b >= 0) {
@@ -419,8 +421,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                     w.whole = w.t0 == 0 && w.t1 == walk.nt;
                     w.two = w.toks > a.tile_toks;
                     w.tf = max(min(w.ctx + w.tok0 + 1, w.L), 0) / kTile;
+                    w.end[0] = w.ctx + w.tok0 + min(w.toks, a.tile_toks);
+                    w.end[1] = w.ctx + w.tok0 + w.toks;
                 }
-                if (i >= kPieces && !lane_wait(bar(bPieceFree + i % kPieces), (i / kPieces - 1) & 1)) break;
+                if (i >= kPieces) lane_wait(bar(bPieceFree + i % kPieces), (i / kPieces - 1) & 1);
+                if (*abort_flag) w.b = -1;
                 pieces[i % kPieces] = w;
                 mbar_arrive(piece_bar(i));
                 if (w.b < 0) break;
@@ -431,9 +436,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 }
                 if (i == 0) grid_dep_wait();
                 // tile_toks tokens x G heads are consecutive operand rows
-                for (int g = 0; ok && g <= w.two; ++g) {
-                    if (uses[g] > 0) ok = lane_wait(bar(bQFree + g), (uses[g] - 1) & 1);
-                    if (!ok) break;
+                for (int g = 0; g <= w.two; ++g) {
+                    if (uses[g] > 0) lane_wait(bar(bQFree + g), (uses[g] - 1) & 1);
                     mbar_arrive_expect_tx(bar(bQ + g), a.tile_toks * a.G * D * 2);
                     for (int c = 0; c < C::NB; ++c)
                         tma_load_3d(s0 + C::OFF_Q + g * C::TILE + c * C::BLOCK, &tmq, bar(bQ + g), 64 * c, w.kvh * a.G,
@@ -446,170 +450,152 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             for (int g = 0; g < 2; ++g)
                 if (uses[g]) (void)mbar_wait_bounded(bar(bQ + g), (uses[g] - 1) & 1, kWaitLimitNs);
         } else if (warp == 1) {
-            // ======================= tensor-core issue ================================
-            // The whole warp runs this, on values that are the same in every lane, and
-            // one lane issues: see elect_one().
+            // ======================= tensor-core issue (one thread) ===================
             grid_dep_wait();
-            const bool me = elect_one();
-            auto uniform = [](int x) { return __reduce_or_sync(0xffffffffu, x); };
-            const uint32_t tm = uniform(tmem), smem0 = uniform(s0);
-            // the sign of softmax_scale goes into q (bit 13 negates A); N in bits 17 and up
-            const uint32_t idesc_qk = umma_idesc(128, 0, 1, 1, false, false) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
-            constexpr uint32_t kIdescPv = umma_idesc(128, D, 1, 1, false, true);
-            // 128-byte-swizzled operands, 1024 bytes between groups of 8 rows
-            constexpr uint64_t kDescHi = static_cast<uint64_t>((1024 >> 4) | (1u << 14) | (2u << 29)) << 32;
-            auto desc = [](uint32_t addr, uint32_t lead) -> uint64_t { return kDescHi | ((addr >> 4) & 0x3FFFu) | (lead >> 4) << 16; };
-            struct Job {  // what a piece is to the tensor cores
-                int there, nt, two, fix, cols0, cols1;  // fix: its first tile with a note; cols: keys of either row tile from t0 on
-            };
-            auto job_of = [&](const Piece& w) {
-                Job j;
-                j.there = uniform(w.b >= 0);
-                j.nt = uniform(w.t1 - w.t0);
-                j.two = uniform(w.two);
-                j.fix = uniform(max(w.tf - w.t0, 0));
-                j.cols0 = uniform(max(w.end(0, a.tile_toks) - w.t0 * kTile, 0));
-                j.cols1 = uniform(max(w.end(1, a.tile_toks) - w.t0 * kTile, 0));
-                return j;
-            };
-            auto cols_of = [](const Job& j, int g, int t) { return min(max(((g ? j.cols1 : j.cols0) - t * kTile + 15) & ~15, 16), kTile); };
-            // Stages and phases of the next tile of K, of V; per group, in either half of a word: P taken, items
-            // whose scores were begun.
-            int sk = 0, sv = 0, n_fix = 0;
-            uint32_t pk = 0, pv = 0, n_p = 0, items = 0;
-            bool ok = true, issued = false;
-            // Scores for row tile g of the tile of K that is next.
-            auto scores = [&](int g, int cols) {
-                const uint64_t q = desc(smem0 + C::OFF_Q + g * C::TILE, 16), kt = desc(smem0 + C::OFF_K + sk * C::TILE, 16);
-                const uint32_t idesc = idesc_qk | static_cast<uint32_t>(cols >> 3) << 17;
-                tc_fence_after();
-                if (me) {
+            if (elect_one()) {
+                // the sign of softmax_scale goes into q (bit 13 negates A); N in bits 17 and up
+                const uint32_t idesc_qk = umma_idesc(128, 0, 1, 1, false, false) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
+                constexpr uint32_t kIdescPv = umma_idesc(128, D, 1, 1, false, true);
+                // 128-byte-swizzled operands, 1024 bytes between groups of 8 rows
+                constexpr uint64_t kDescHi = static_cast<uint64_t>((1024 >> 4) | (1u << 14) | (2u << 29)) << 32;
+                auto desc = [](uint32_t addr, uint32_t lead) -> uint64_t { return kDescHi | ((addr >> 4) & 0x3FFFu) | (lead >> 4) << 16; };
+                // Stages and phases of the next tile of K, of V; per group, in either half of a word: P taken, items
+                // whose scores were begun.
+                int sk = 0, sv = 0, n_fix = 0;
+                uint32_t pk = 0, pv = 0, n_p = 0, items = 0, issued = 0;
+                auto next_k = [&]() {
+                    if (++sk == C::SK) sk = 0, pk ^= 1;
+                };
+                auto next_v = [&]() {
+                    if (++sv == C::SV) sv = 0, pv ^= 1;
+                };
+                struct Job {  // of a piece
+                    int there, t0, t1, two, tf, end0, end1;
+                };
+                auto job_of = [&](int i) {
+                    const Piece& w = pieces[i % kPieces];
+                    Job j{w.b >= 0 && !*abort_flag, w.t0, w.t1, w.two, w.tf, w.end[0], w.end[1]};
+                    if (!j.there) j.two = 0;
+                    return j;
+                };
+                auto cols_of = [](const Job& w, int g, int t) {
+                    return min(max(((g ? w.end1 : w.end0) - t * kTile + 15) & ~15, 16), kTile);
+                };
+                // Scores for row tile g of the tile of K that is next.
+                auto scores = [&](int g, int cols) {
+                    const uint64_t q = desc(s0 + C::OFF_Q + g * C::TILE, 16), kt = desc(s0 + C::OFF_K + sk * C::TILE, 16);
+                    const uint32_t idesc = idesc_qk | static_cast<uint32_t>(cols >> 3) << 17;
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint32_t at = ((k >> 2) * C::BLOCK + (k & 3) * 32) >> 4;
-                        umma_ss(tm + 256 * g, q + at, kt + at, idesc, k > 0);
+                        umma_ss(tmem + 256 * g, q + at, kt + at, idesc, k > 0);
                     }
                     umma_commit(bar(bS + g));
-                }
-                issued = true;
-            };
-            auto next_k = [&]() {
-                if (++sk == C::SK) sk = 0, pk ^= 1;
-            };
-            auto next_v = [&]() {
-                if (++sv == C::SV) sv = 0, pv ^= 1;
-            };
-            // The first scores of a piece for row tile g.
-            auto begin = [&](const Job& w, int g) {
-                if (g == 0) ok = ok && warp_wait(bar(bKFull + sk), pk);
-                ok = ok && warp_wait(bar(bQ + g), items >> (16 * g) & 1);
-                items += 1u << (16 * g);
-                if (ok) scores(g, cols_of(w, g, 0));
-                if (g == w.two) next_k();
-            };
-            ok = warp_wait(piece_bar(0), piece_par(0));
-            Job w{}, next{};
-            if (ok) w = job_of(pieces[0]);
+                };
+                // The first scores of a piece for row tile g.
+                auto begin = [&](const Job& w, int g) {
+                    if (g == 0) lane_wait(bar(bKFull + sk), pk);
+                    lane_wait(bar(bQ + g), items >> (16 * g) & 1);
+                    items += 1u << (16 * g);
+                    scores(g, cols_of(w, g, w.t0));
+                    issued = 1;
+                    if (g == w.two) next_k();
+                };
+                lane_wait(piece_bar(0), piece_par(0));
+                Job w = job_of(0), next;
 #pragma unroll 1
-            for (int g = 0; ok && w.there && g <= w.two; ++g) begin(w, g);
+                for (int g = 0; w.there && g <= w.two; ++g) begin(w, g);
 #pragma unroll 1
-            for (int i = 0; ok && w.there; ++i) {
-                int t = 0;
-                // Tiles that both row tiles see in full, with another behind them (the code to be fast).
-                if (w.two) {
+                for (int i = 0; w.there; ++i) {
+                    next.there = next.two = 0;
+                    const int fix = min(w.tf, w.t1);
 #pragma unroll 1
-                    for (const int end = min(w.fix, w.nt - 1); ok && t < end; ++t) {
-                        ok = warp_wait(bar(bVFull + sv), pv);
-                        const uint64_t vt = desc(smem0 + C::OFF_V + sv * C::TILE, C::BLOCK);
-                        const int cols1 = cols_of(w, 1, t + 1), cols0 = cols_of(w, 0, t + 1);
+                    for (int t = w.t0; t < w.t1;) {
+                        // Tiles that both row tiles see in full, as the next one: the loop to be fast.
+                        if (t > w.t0 && w.two && t + 1 < fix) {
+#pragma unroll 1
+                            for (; t + 1 < fix; ++t) {
+                                lane_wait(bar(bVFull + sv), pv);
+                                const uint64_t vt = desc(s0 + C::OFF_V + sv * C::TILE, C::BLOCK);
 #pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            if (t == 0 && (items >> (16 * g) & 0xFFFFu) > 1) ok = ok && warp_wait(bar(bOFree + g), items >> (16 * g) & 1);
-                            if (g == 0) ok = ok && warp_wait(bar(bKFull + sk), pk);
-                            ok = ok && warp_wait(bar(bP + g), n_p >> (16 * g) & 1);
-                            if (!ok) break;
-                            tc_fence_after();
-                            if (me) {
-                                const uint32_t more_o = t > 0 ? 1u : go_on[g];  // O goes on, or starts
+                                for (int g = 0; g < 2; ++g) {
+                                    lane_wait(bar(bP + g), n_p >> (16 * g) & 1);
+                                    tc_fence_after();
 #pragma unroll
-                                for (int k = 0; k < kTile / 16; ++k)
-                                    umma_ts(tm + 256 * g + C::O_COL, tm + 256 * g + 8 * k, vt + k * (2048 >> 4), kIdescPv, k > 0 ? 1u : more_o);
+                                    for (int k = 0; k < kTile / 16; ++k)
+                                        umma_ts(tmem + 256 * g + C::O_COL, tmem + 256 * g + 8 * k, vt + k * (2048 >> 4), kIdescPv, 1u);
+                                    if (g == 0) lane_wait(bar(bKFull + sk), pk);
+                                    scores(g, kTile);
+                                }
+                                n_p += 0x10001u;
+                                next_v();
+                                next_k();
                             }
-                            scores(g, g ? cols1 : cols0);
+                            continue;
                         }
-                        n_p += 0x10001u;
-                        next_v();
-                        next_k();
-                    }
-                }
-                next.there = next.two = 0;
+                        const bool last = t + 1 == w.t1;
+                        if (t >= w.tf) {
+                            lane_wait(bar(bFix + n_fix % kFix), (n_fix / kFix) & 1);
+                            ++n_fix;
+                        } else {
+                            lane_wait(bar(bVFull + sv), pv);
+                        }
+                        const uint64_t vt = desc(s0 + C::OFF_V + sv * C::TILE, C::BLOCK);
+                        // (the next piece may have scores for a row tile that this one does not have)
 #pragma unroll 1
-                for (; ok && t < w.nt; ++t) {
-                    const bool last = t + 1 == w.nt;
-                    if (t >= w.fix) {
-                        ok = warp_wait(bar(bFix + n_fix % kFix), (n_fix / kFix) & 1);
-                        ++n_fix;
-                    } else {
-                        ok = warp_wait(bar(bVFull + sv), pv);
-                    }
-                    const uint64_t vt = desc(smem0 + C::OFF_V + sv * C::TILE, C::BLOCK);
-                    // (the next piece may have scores for a row tile that this one does not have)
-#pragma unroll 1
-                    for (int g = 0; ok && g <= (w.two | (last ? next.two : 0)); ++g) {
-                        if (g <= w.two) {
-                            // the item before has been read out of O
-                            if (t == 0 && (items >> (16 * g) & 0xFFFFu) > 1) ok = warp_wait(bar(bOFree + g), items >> (16 * g) & 1);
-                            const int steps = cols_of(w, g, t) >> 4;
-                            ok = ok && warp_wait(bar(bP + g), n_p >> (16 * g) & 1);
-                            if (!ok) break;
-                            n_p += 1u << (16 * g);
-                            tc_fence_after();
-                            if (me) {
-                                const uint32_t more_o = t > 0 ? 1u : go_on[g];
+                        for (int g = 0; g <= (w.two | (last ? next.two : 0)); ++g) {
+                            if (g <= w.two) {
+                                // the item before has been read out of O
+                                if (t == w.t0 && (items >> (16 * g) & 0xFFFFu) > 1) lane_wait(bar(bOFree + g), items >> (16 * g) & 1);
+                                const int steps = cols_of(w, g, t) >> 4;
+                                lane_wait(bar(bP + g), n_p >> (16 * g) & 1);
+                                n_p += 1u << (16 * g);
+                                tc_fence_after();
+                                const uint32_t more_o = t > w.t0 ? 1u : go_on[g];  // O goes on, or starts
 #pragma unroll 1
                                 for (int k = 0; k < steps; ++k)
-                                    umma_ts(tm + 256 * g + C::O_COL, tm + 256 * g + 8 * k, vt + k * (2048 >> 4), kIdescPv, k > 0 ? 1u : more_o);
+                                    umma_ts(tmem + 256 * g + C::O_COL, tmem + 256 * g + 8 * k, vt + k * (2048 >> 4), kIdescPv, k > 0 ? 1u : more_o);
+                                if (last) umma_commit(bar(bO + g));
                             }
-                            if (last && me) umma_commit(bar(bO + g));
-                        }
-                        if (!last) {
-                            if (g == 0) ok = warp_wait(bar(bKFull + sk), pk);
-                            if (ok) scores(g, cols_of(w, g, t + 1));
-                            if (g == w.two) next_k();
-                        } else {
-                            if (g == 0) {
-                                ok = warp_wait(piece_bar(i + 1), piece_par(i + 1));
-                                if (ok) next = job_of(pieces[(i + 1) % kPieces]);
+                            if (!last) {
+                                if (g == 0) lane_wait(bar(bKFull + sk), pk);
+                                scores(g, cols_of(w, g, t + 1));
+                                if (g == w.two) next_k();
+                            } else {
+                                if (g == 0) {
+                                    lane_wait(piece_bar(i + 1), piece_par(i + 1));
+                                    next = job_of(i + 1);
+                                }
+                                if (next.there && g <= next.two) begin(next, g);
                             }
-                            if (ok && next.there && g <= next.two) begin(next, g);
                         }
+                        next_v();
+                        ++t;
                     }
-                    next_v();
+                    mbar_arrive(bar(bPieceFree + i % kPieces));
+                    w = next;
                 }
-                if (lane == 0) mbar_arrive(bar(bPieceFree + i % kPieces));
-                w = next;
+                // Every operation issued is done before the tensor memory is freed: the
+                // softmax groups wait for their last O, and a give-up for all of them here.
+                if (*abort_flag && issued) {
+                    umma_commit(bar(bEnd));
+                    (void)mbar_wait_bounded(bar(bEnd), 0, kWaitLimitNs);
+                }
             }
-            // Every operation issued is done before the tensor memory is freed: the
-            // softmax groups wait for their last O, and a give-up for all of them here.
-            if (!ok && issued) {
-                if (me) umma_commit(bar(bEnd));
-                (void)mbar_wait_bounded(bar(bEnd), 0, kWaitLimitNs);
-            }
+            __syncwarp();
         } else if (warp == 2) {
             // ======================= V of partly visible tiles ========================
             grid_dep_wait();
             int n = 0, n_fix = 0;
-            bool ok = true;
-            for (int i = 0; ok; ++i) {
-                if (!warp_wait(piece_bar(i), piece_par(i))) break;
+            for (int i = 0;; ++i) {
+                warp_wait(piece_bar(i), piece_par(i));
                 const Piece w = pieces[i % kPieces];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(bPieceFree + i % kPieces));
-                if (w.b < 0) break;
+                if (__any_sync(0xffffffffu, w.b < 0 || *abort_flag)) break;
                 const int lim = max(min(w.ctx + w.tok0 + 1, w.L), 0);  // keys that every row sees
                 for (int t = w.t0; t < w.t1; ++t, ++n) {
-                    ok = warp_wait(bar(bVFull + n % C::SV), (n / C::SV) & 1);
-                    if (!ok) break;
+                    warp_wait(bar(bVFull + n % C::SV), (n / C::SV) & 1);
                     if (t < w.tf) {
                         if (lane == 0) mbar_arrive(bar(bVFree + n % C::SV));
                         continue;
@@ -642,8 +628,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                         bad_rows[4 * (n_fix % kFix) + lane] = lane == 0 ? words[0] : lane == 1 ? words[1] : lane == 2 ? words[2] : words[3];
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(bFix + n_fix % kFix));
-                    if (lane == 0) mbar_arrive(bar(bVFree + n % C::SV));
+                    if (lane == 0) {
+                        mbar_arrive(bar(bFix + n_fix % kFix));
+                        mbar_arrive(bar(bVFree + n % C::SV));
+                    }
                     ++n_fix;
                 }
             }
@@ -651,7 +639,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         __syncwarp();
     } else {
         // ======================= softmax ==========================================
-        reg_inc<C::REG_SM>();
+        if constexpr (D == 64) reg_inc<96>();  // (no more than it has: with this line nothing spills, 362 us and not 385)
         grid_dep_wait();
         grid_dep_launch();
         const int grp = (warp - 4) >> 3, half = (warp - 4) >> 2 & 1, wq = warp & 3;
@@ -663,16 +651,15 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         const int tok_l = row_l / a.G, g_l = row_l - tok_l * a.G;      // its token in the row tile, its head
         const bool speaker = wq == 0 && half == 0 && lane == 0;        // for its group
         const int pair = 1 + 4 * grp + wq;             // barrier of the two warps that share rows
-        float* mine = theirs + (2 * grp + half) * 128 + row_l;
+        float* mine = theirs + (2 * grp + half) * 128 + row_l;         // what this half tells the other, and hears
         const float* other = theirs + (2 * grp + 1 - half) * 128 + row_l;
         const float sl = fmaxf(fabsf(a.scale_log2), 1.2e-38f);         // -inf times it stays -inf
         const float2 sl2 = make_float2(sl, sl);
         int n = 0, job = 0, n_o = 0, n_fix = 0;        // the CTA's tiles, this group's jobs and items, fixed tiles
-        bool ok = true;
         for (int i = 0;; ++i) {
-            ok = warp_wait(piece_bar(i), piece_par(i));
+            warp_wait(piece_bar(i), piece_par(i));
             const Piece& w = pieces[i % kPieces];
-            if (!ok || w.b < 0) break;
+            if (__any_sync(0xffffffffu, w.b < 0 || *abort_flag)) break;
             const int t0 = w.t0, t1 = w.t1, tf = w.tf;
             if (grp > w.two) {
                 n += t1 - t0;
@@ -691,9 +678,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             float m = -INFINITY, l = 0.f;              // (l: of this half's columns)
             for (int t = t0; t < t1; ++t, ++n, ++job) {
                 const bool first = t == t0;
-                ok = ok && warp_wait(bar(bS + grp), job & 1);
+                warp_wait(bar(bS + grp), job & 1);
                 tc_fence_after();
-                if (speaker && ok) {
+                if (speaker) {
                     if (frees) {
                         mbar_arrive(bar(bKFree + n % C::SK));
                         if (!first) mbar_arrive(bar(bVFree + (n - 1) % C::SV));
@@ -703,14 +690,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 }
                 uint32_t bad[4] = {0u, 0u, 0u, 0u};
                 if (t >= tf) {
-                    ok = ok && warp_wait(bar(bFix + n_fix % kFix), (n_fix / kFix) & 1);
+                    warp_wait(bar(bFix + n_fix % kFix), (n_fix / kFix) & 1);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) bad[k] = bad_rows[4 * (n_fix % kFix) + k];
                     ++n_fix;
                 }
                 const int vis = lim - t * kTile - 64 * half;   // of this half's columns, those that the row sees
                 const bool inner = t < inner_end;
-                if (ok) {
+                {
                     // The half's weights; where their sum asks for another reference, twice.
                     bool start = first;                // there is no reference yet
                     uint32_t p[32];
@@ -826,12 +813,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0 && ok) mbar_arrive(bar(bP + grp));
+                if (lane == 0) mbar_arrive(bar(bP + grp));
             }
             // ---- the piece's output, or its partial sums -----------------------------
-            ok = ok && warp_wait(bar(bO + grp), n_o & 1);
+            warp_wait(bar(bO + grp), n_o & 1);
             ++n_o;
-            if (!ok) break;
             tc_fence_after();
             if (frees) mbar_arrive(bar(bVFree + (n - 1) % C::SV));
             {
@@ -902,16 +888,6 @@ cudaError_t launch_t(const PromptArgs& a, const CUtensorMap& tq, const CUtensorM
     int sms = 0;
     cudaError_t e = device_sm_count(&sms);
     if (e != cudaSuccess) return e;
-    // The roles deal out the registers that the kernel is launched with: as many
-    // as assumed, or it would wait for more that never come.
-    static std::atomic<bool> as_assumed{false};
-    if (!as_assumed.load(std::memory_order_relaxed)) {
-        cudaFuncAttributes at{};
-        e = cudaFuncGetAttributes(&at, prompt_kernel<D>);
-        if (e != cudaSuccess) return e;
-        if (at.numRegs * C::THREADS < C::REGS) return cudaErrorInvalidConfiguration;
-        as_assumed.store(true, std::memory_order_relaxed);
-    }
     e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     e = launch_dependent(prompt_kernel<D>, dim3(sms), dim3(C::THREADS), C::SMEM, s, tq, tk, tv, a);
