@@ -65,7 +65,7 @@ constexpr int kSnapKeys = 1536; // longest item (keys and kItemKeys) up to which
 constexpr int kPieces = 4;      // ring of pieces
 constexpr float kRaise = 4096.f; // sum of 64 weights past which their row's reference moves
 constexpr uint32_t kWaitLimitNs = 1000000000u;
-constexpr uint32_t kPolls = 1u << 24;  // 40 to 80 ns each
+constexpr uint32_t kTries = 1u << 20;  // of about 1 us
 constexpr int kFix = 4;         // ring of the fixed tiles' notes: no fewer than there are stages of V
 
 template <int D>
@@ -347,11 +347,13 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     // next piece. (Results to look at are branches, which cost more here than the
     // waits: a wait for a barrier that is complete takes 45 cycles, with its result
     // voted on and branched upon 180.)
+    // (try_wait holds the warp until the phase is over, for 1 us at most; polling with test_wait takes the issue
+    // slots of the others: 347 us and not 333.)
     auto lane_wait = [&](uint32_t bb, uint32_t par) {
         uint32_t n = 0;
 #pragma unroll 1
-        while (!mbar_test_wait(bb, par))
-            if (++n == kPolls || *abort_flag) {
+        while (!mbar_try_wait(bb, par))
+            if (++n % 256 == 0 && (n == kTries || *abort_flag)) {
                 *abort_flag = 1;
                 break;
             }
@@ -359,8 +361,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     auto warp_wait = [&](uint32_t bb, uint32_t par) {
         uint32_t n = 0;
 #pragma unroll 1
-        while (!__any_sync(0xffffffffu, mbar_test_wait(bb, par)))
-            if (__any_sync(0xffffffffu, ++n == kPolls || *abort_flag)) {
+        while (!__any_sync(0xffffffffu, mbar_try_wait(bb, par)))
+            if (++n % 256 == 0 && __any_sync(0xffffffffu, n == kTries || *abort_flag)) {
                 *abort_flag = 1;
                 break;
             }
@@ -678,6 +680,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             float m = -INFINITY, l = 0.f;              // (l: of this half's columns)
             for (int t = t0; t < t1; ++t, ++n, ++job) {
                 const bool first = t == t0;
+                const int vis = lim - t * kTile - 64 * half;   // of this half's columns, those that the row sees
+                const bool inner = t < inner_end;
                 warp_wait(bar(bS + grp), job & 1);
                 tc_fence_after();
                 if (speaker) {
@@ -695,8 +699,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                     for (int k = 0; k < 4; ++k) bad[k] = bad_rows[4 * (n_fix % kFix) + k];
                     ++n_fix;
                 }
-                const int vis = lim - t * kTile - 64 * half;   // of this half's columns, those that the row sees
-                const bool inner = t < inner_end;
                 {
                     // The half's weights; where their sum asks for another reference, twice.
                     bool start = first;                // there is no reference yet
