@@ -1692,6 +1692,7 @@ pkv_status pkv_prompt_attention(const pkv_tensor* q_p, const pkv_tensor* k_p, co
     a.D = static_cast<int32_t>(D);
     a.G = static_cast<int32_t>(G);
     a.tile_toks = 128 / a.G;
+    a.wide = aligned(out.ptr, 32) && strides_multiple(out, 2, 32);
     a.err = err_flag;
     return cuda_status(pkv::launch_prompt_attention(a, tq, tk, tv, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -278,6 +278,7 @@ struct PromptArgs {
     void* workspace;
     int32_t T, Tk, B, Hq, Hkv, D, G;
     int32_t tile_toks;         // tokens per row tile: 128 / G
+    int32_t wide;              // out's rows are 32-byte aligned
     int32_t* err;
 };
 

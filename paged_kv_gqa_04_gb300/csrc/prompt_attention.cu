@@ -741,14 +741,21 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                         // scaled by a power of two, exactly).
                         float mx = -INFINITY;
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t x[16];
-                            tmem_ld16(tS + 16 * c, x);
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t x[32];
+                            tmem_ld32(tS + 32 * c, x);
                             tmem_wait_ld();
                             pin(x);
+                            if (!inner) {
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                if (16 * c + e < vis || inner) mx = fmaxf(mx, __uint_as_float(x[e]));
+                                for (int e = 0; e < 32; ++e)
+                                    if (32 * c + e >= vis) x[e] = 0xFF800000u;
+                            }
+                            float mx4[4] = {mx, mx, mx, mx};
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2)
+                                mx4[e >> 1 & 3] = fmaxf(fmaxf(mx4[e >> 1 & 3], __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
+                            mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
                         }
                         *mine = mx;
                         (void)named_bar_and(pair, 64, true);
@@ -843,31 +850,33 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 float* part = part_o<D>(a.workspace, gridDim.x, slot, row) + static_cast<int64_t>(D / 8 * half) * kJoinRows * 4;
                 uint16_t* out = a.out + q_row * a.o_s0 + h * a.o_s1 + D / 2 * half;
 #pragma unroll 1
-                for (int c = 0; c < D / 64; ++c) {
-                    uint32_t o[32];
-                    tmem_ld32(tO + 32 * c, o);
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[16];
+                    tmem_ld16(tO + 16 * c, o);
                     tmem_wait_ld();
                     pin(o);
-                    if (c == D / 64 - 1) {  // O is read
+                    if (c == D / 32 - 1) {  // O is read
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(bOFree + grp));
                     }
                     if (!live) continue;
                     if (whole) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(none ? 0.f : __uint_as_float(o[e]) * inv);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            reinterpret_cast<uint4*>(out)[4 * c + e] =
-                                make_uint4(pack_bf16(__uint_as_float(o[8 * e]), __uint_as_float(o[8 * e + 1])),
-                                           pack_bf16(__uint_as_float(o[8 * e + 2]), __uint_as_float(o[8 * e + 3])),
-                                           pack_bf16(__uint_as_float(o[8 * e + 4]), __uint_as_float(o[8 * e + 5])),
-                                           pack_bf16(__uint_as_float(o[8 * e + 6]), __uint_as_float(o[8 * e + 7])));
-                    } else {
+                        uint32_t q[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            *reinterpret_cast<uint4*>(part + static_cast<int64_t>(8 * c + e) * kJoinRows * 4) =
+                            q[e] = none ? 0u : pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                        // (32 rows a store: the load-store unit takes a row at a time, whatever its bytes)
+                        if (a.wide) {
+                            stg256(out + 16 * c, q);
+                        } else {
+                            reinterpret_cast<uint4*>(out)[2 * c] = make_uint4(q[0], q[1], q[2], q[3]);
+                            reinterpret_cast<uint4*>(out)[2 * c + 1] = make_uint4(q[4], q[5], q[6], q[7]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            *reinterpret_cast<uint4*>(part + static_cast<int64_t>(4 * c + e) * kJoinRows * 4) =
                                 make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                     }
                 }
