@@ -543,33 +543,32 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                             lane_wait(bar(bVFull + sv), pv);
                         }
                         const uint64_t vt = desc(s0 + C::OFF_V + sv * C::TILE, C::BLOCK);
-                        // (the next piece may have scores for a row tile that this one does not have)
 #pragma unroll 1
-                        for (int g = 0; g <= (w.two | (last ? next.two : 0)); ++g) {
-                            if (g <= w.two) {
-                                // the item before has been read out of O
-                                if (t == w.t0 && (items >> (16 * g) & 0xFFFFu) > 1) lane_wait(bar(bOFree + g), items >> (16 * g) & 1);
-                                const int steps = cols_of(w, g, t) >> 4;
-                                lane_wait(bar(bP + g), n_p >> (16 * g) & 1);
-                                n_p += 1u << (16 * g);
-                                tc_fence_after();
-                                const uint32_t more_o = t > w.t0 ? 1u : go_on[g];  // O goes on, or starts
+                        for (int g = 0; g <= w.two; ++g) {
+                            // the item before has been read out of O
+                            if (t == w.t0 && (items >> (16 * g) & 0xFFFFu) > 1) lane_wait(bar(bOFree + g), items >> (16 * g) & 1);
+                            const int steps = cols_of(w, g, t) >> 4;
+                            lane_wait(bar(bP + g), n_p >> (16 * g) & 1);
+                            n_p += 1u << (16 * g);
+                            tc_fence_after();
+                            const uint32_t more_o = t > w.t0 ? 1u : go_on[g];  // O goes on, or starts
 #pragma unroll 1
-                                for (int k = 0; k < steps; ++k)
-                                    umma_ts(tmem + 256 * g + C::O_COL, tmem + 256 * g + 8 * k, vt + k * (2048 >> 4), kIdescPv, k > 0 ? 1u : more_o);
-                                if (last) umma_commit(bar(bO + g));
-                            }
-                            if (!last) {
+                            for (int k = 0; k < steps; ++k)
+                                umma_ts(tmem + 256 * g + C::O_COL, tmem + 256 * g + 8 * k, vt + k * (2048 >> 4), kIdescPv, k > 0 ? 1u : more_o);
+                            if (last) {
+                                umma_commit(bar(bO + g));
+                            } else {
                                 if (g == 0) lane_wait(bar(bKFull + sk), pk);
                                 scores(g, cols_of(w, g, t + 1));
                                 if (g == w.two) next_k();
-                            } else {
-                                if (g == 0) {
-                                    lane_wait(piece_bar(i + 1), piece_par(i + 1));
-                                    next = job_of(i + 1);
-                                }
-                                if (next.there && g <= next.two) begin(next, g);
                             }
+                        }
+                        if (last) {
+                            // (q of the next piece may be on its way yet: nothing waits behind it but its scores)
+                            lane_wait(piece_bar(i + 1), piece_par(i + 1));
+                            next = job_of(i + 1);
+#pragma unroll 1
+                            for (int g = 0; next.there && g <= next.two; ++g) begin(next, g);
                         }
                         next_v();
                         ++t;
