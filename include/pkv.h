@@ -832,6 +832,78 @@ pkv_status pkv_fork_sequences(const pkv_tensor* caches, int32_t n_caches, int32_
  */
 
 /*
+ * pkv_qk_norm_rope_kv_write -- pkv_rope_kv_write with an RMS norm of every q and
+ * k head before the rotation, for every cache format.
+ *
+ * For every token t with slot_mapping[t] >= 0 and every head row x of q or k,
+ * w the weight of q or of k:
+ *   r = 1 / sqrt( mean_d x_d^2 + eps ),   y_d = (x_d r) w_d
+ * in float32 (the root and the quotient correctly rounded, each product
+ * rounded), and then what pkv_rope_kv_write (with block scales:
+ * pkv_rope_kv_write_nvfp4) does with q, k and v, y in the place of the rows of q
+ * and k:
+ *   q[t] <- bf16 of the rotated y (in place), the caches <- the rotated y of k,
+ *   and v as it is; and, where k_out is given,
+ *   k_out[t] <- bf16 of the rotated y of k, as pkv_prompt_attention takes it.
+ *
+ * q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping, k_scale,
+ * v_scale, layout, rope_style  as for pkv_rope_kv_write.
+ * q_weight,
+ * k_weight     [D] float32 or bf16 (both the same), contiguous, 16-byte aligned
+ *              (q_weight is not read without q).
+ * eps          >= 0.
+ * k_block_scale,
+ * v_block_scale  NULL (or ptr NULL) for bf16 / FP8 caches; those of
+ *              pkv_rope_kv_write_nvfp4 for NVFP4 caches.
+ * k_out        [T, Hkv, D] bf16, innermost stride 1, rows 16-byte aligned, or
+ *              NULL. It may be k itself (the same view: in place); otherwise it
+ *              must not overlap q, k, v or the caches (by their extents).
+ * The supported sizes and the errors are those of pkv_rope_kv_write (a skipped
+ * token's row of k_out is left as it is).
+ */
+pkv_status pkv_qk_norm_rope_kv_write(const pkv_tensor* q, const pkv_tensor* k, const pkv_tensor* v,
+                                     const pkv_tensor* q_weight, const pkv_tensor* k_weight, float eps,
+                                     const pkv_tensor* positions, const pkv_tensor* cos_sin,
+                                     const pkv_tensor* k_cache, const pkv_tensor* v_cache,
+                                     const pkv_tensor* k_block_scale, const pkv_tensor* v_block_scale,
+                                     const pkv_tensor* slot_mapping, const pkv_tensor* k_scale,
+                                     const pkv_tensor* v_scale, const pkv_tensor* k_out, int32_t layout,
+                                     int32_t rope_style, int32_t* err_flag, pkv_stream_t stream);
+
+/*
+ * pkv_gather_kv -- cached keys and values read back from their pages into
+ * packed bf16 rows (what pkv_prompt_attention takes for tokens behind a context
+ * that is cached already).
+ *
+ * For sequence b and i in [0, start[b+1] - start[b]), with p = first[b] + i:
+ *   k_out[start[b] + i] <- the keys, v_out[...] <- the values at position p of
+ *   the sequence: entry p / P of its block table, token p % P of that page,
+ * as they are (bf16 caches), or as bf16( f32( scale * value ) ), the value an
+ * E4M3 byte's, or s * e of an NVFP4 block (exact), scale the head's static one.
+ *
+ * k_cache, v_cache, k_scale, v_scale, layout  as for pkv_rope_kv_write (any page
+ *              size P), or as for pkv_rope_kv_write_nvfp4 with
+ * k_block_scale,
+ * v_block_scale  its block-scale caches (NULL, or ptr NULL, otherwise).
+ * block_tables [B, max_pages] int32, innermost stride 1.
+ * start        [B+1] int32, ascending, within [0, T]. Rows outside every range
+ *              are not written.
+ * first        [B] int32 (the position of a sequence's first row), or NULL (0).
+ * k_out, v_out [T, Hkv, D] bf16, innermost stride 1, rows 16-byte aligned; they
+ *              must not overlap the caches (by their extents).
+ * Supported: D in {64, 128}; B, Hkv <= 65535.
+ * Errors: a position outside [0, P*max_pages) sets PKV_FLAG_SEQ_LEN_RANGE, a
+ * page outside [0, num_pages) PKV_FLAG_PAGE_RANGE: the row is filled with
+ * zeros. Starts that do not ascend within [0, T] set PKV_FLAG_ROW_RANGE; what the
+ * rows of such ranges hold is not specified.
+ */
+pkv_status pkv_gather_kv(const pkv_tensor* k_cache, const pkv_tensor* v_cache, const pkv_tensor* k_block_scale,
+                         const pkv_tensor* v_block_scale, const pkv_tensor* block_tables, const pkv_tensor* start,
+                         const pkv_tensor* first, const pkv_tensor* k_out, const pkv_tensor* v_out,
+                         const pkv_tensor* k_scale, const pkv_tensor* v_scale, int32_t layout, int32_t* err_flag,
+                         pkv_stream_t stream);
+
+/*
  * pkv_prompt_attention -- causal attention over whole prompts of different
  * lengths, packed one behind the other, with grouped heads.
  *

@@ -49,7 +49,7 @@ EXPORTED = ("pkv_rope_kv_write", "pkv_paged_gqa_decode", "pkv_lse_merge", "pkv_c
             "pkv_selftest_bounded_wait", "pkv_copy", "pkv_plan_splits", "pkv_paged_gqa_decode_planned",
             "pkv_lse_merge_planned", "pkv_plan_splits_mla", "pkv_paged_mla_decode_planned", "pkv_paged_tree_decode",
             "pkv_tree_decode_workspace", "pkv_accept_drafts", "pkv_resize_sequences", "pkv_fork_sequences",
-            "pkv_prompt_attention", "pkv_prompt_attention_workspace")
+            "pkv_qk_norm_rope_kv_write", "pkv_gather_kv", "pkv_prompt_attention", "pkv_prompt_attention_workspace")
 
 
 class PkvTensor(ctypes.Structure):
@@ -104,6 +104,9 @@ def lib() -> ctypes.CDLL:
         L.pkv_accept_drafts.argtypes = [T, i32, i32, T, T, T, T, T, T, P, P]
         L.pkv_resize_sequences.argtypes = [T, T, T, T, i32, P, P]
         L.pkv_fork_sequences.argtypes = [T, i32, i32, T, T, T, T, T, T, P, P]
+        L.pkv_qk_norm_rope_kv_write.argtypes = [T, T, T, T, T, ctypes.c_float, T, T, T, T, T, T, T, T, T, T, i32, i32, P,
+                                                P]
+        L.pkv_gather_kv.argtypes = [T, T, T, T, T, T, T, T, T, T, T, i32, P, P]
         L.pkv_prompt_attention.argtypes = [T, T, T, T, T, ctypes.c_float, T, T, P, ctypes.c_int64, P, P]
         L.pkv_prompt_attention_workspace.argtypes = [i32, i32]
         L.pkv_prompt_attention_workspace.restype = ctypes.c_int64
@@ -115,7 +118,8 @@ def lib() -> ctypes.CDLL:
                      "pkv_paged_mla_decode", "pkv_choose_num_splits_mla", "pkv_selftest_bounded_wait", "pkv_copy",
                      "pkv_plan_splits", "pkv_paged_gqa_decode_planned", "pkv_lse_merge_planned",
                      "pkv_plan_splits_mla", "pkv_paged_mla_decode_planned", "pkv_paged_tree_decode",
-                     "pkv_accept_drafts", "pkv_resize_sequences", "pkv_fork_sequences", "pkv_prompt_attention"):
+                     "pkv_accept_drafts", "pkv_resize_sequences", "pkv_fork_sequences",
+                     "pkv_qk_norm_rope_kv_write", "pkv_gather_kv", "pkv_prompt_attention"):
             getattr(L, name).restype = ctypes.c_int32
         _lib = L
     return _lib
@@ -456,6 +460,37 @@ def fork_sequences(caches, block_tables, page_counts, seq_lens, forks, page_refs
     _check("pkv_fork_sequences", lib().pkv_fork_sequences(
         caches.ptr, caches.n, LAYOUTS[layout], _desc(block_tables), _desc(page_counts), _desc(seq_lens), _desc(forks),
         _desc(page_refs), _desc(copies), _ptr(err_flag), _stream(stream)))
+
+
+def qk_norm_rope_kv_write(q, k, v, q_weight, k_weight, eps: float, positions, cos_sin, k_cache, v_cache, slot_mapping,
+                          k_scale=None, v_scale=None, k_block_scale=None, v_block_scale=None, k_out=None,
+                          layout: str = "HND", rope_style: str = "neox", err_flag=None, stream=None) -> None:
+    """rope_kv_write (with block-scale caches: rope_kv_write_nvfp4) with an RMS
+    norm of every q and k head, weights q_weight and k_weight [D] float32 or
+    bf16, before the rotation; k_out [T,Hkv,D] bf16 (or k itself, or None)
+    receives the normed and rotated keys (pkv_qk_norm_rope_kv_write)."""
+    _on_current_device(q, k, v, q_weight, k_weight, positions, cos_sin, k_cache, v_cache, slot_mapping, k_scale, v_scale,
+                       k_block_scale, v_block_scale, k_out, err_flag)
+    fp4 = k_block_scale is not None
+    kc, vc = (_fp4(k_cache), _fp4(v_cache)) if fp4 else (_desc(k_cache), _desc(v_cache))
+    _check("pkv_qk_norm_rope_kv_write", lib().pkv_qk_norm_rope_kv_write(
+        _desc(q), _desc(k), _desc(v), _desc(q_weight), _desc(k_weight), eps, _desc(positions), _desc(cos_sin), kc, vc,
+        _desc(k_block_scale), _desc(v_block_scale), _desc(slot_mapping), _desc(k_scale), _desc(v_scale), _desc(k_out),
+        LAYOUTS[layout], STYLES[rope_style], _ptr(err_flag), _stream(stream)))
+
+
+def gather_kv(k_cache, v_cache, block_tables, start, first, k_out, v_out, k_scale=None, v_scale=None, k_block_scale=None,
+              v_block_scale=None, layout: str = "HND", err_flag=None, stream=None) -> None:
+    """Cached keys and values as packed bf16 rows (pkv_gather_kv): rows
+    start[b] .. start[b+1] of k_out, v_out [T,Hkv,D] receive positions first[b]
+    (None: 0) and on of sequence b."""
+    _on_current_device(k_cache, v_cache, block_tables, start, first, k_out, v_out, k_scale, v_scale, k_block_scale,
+                       v_block_scale, err_flag)
+    fp4 = k_block_scale is not None
+    kc, vc = (_fp4(k_cache), _fp4(v_cache)) if fp4 else (_desc(k_cache), _desc(v_cache))
+    _check("pkv_gather_kv", lib().pkv_gather_kv(
+        kc, vc, _desc(k_block_scale), _desc(v_block_scale), _desc(block_tables), _desc(start), _desc(first), _desc(k_out),
+        _desc(v_out), _desc(k_scale), _desc(v_scale), LAYOUTS[layout], _ptr(err_flag), _stream(stream)))
 
 
 def prompt_attention_workspace(D: int, sm_count: int) -> int:

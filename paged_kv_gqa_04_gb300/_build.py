@@ -22,7 +22,7 @@ LIB = os.path.join(HERE, "libpkv.so")
 
 SOURCES = ["pkv_abi.cu", "rope_kv_write.cu", "paged_decode.cu", "mla_decode.cu", "lse_merge.cu", "validate.cu",
            "stream_read.cu", "selftest.cu", "copy.cu", "pages.cu", "tree_decode.cu",
-           "prompt_attention.cu"]
+           "prompt_attention.cu", "qk_norm_write.cu", "gather_kv.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -251,15 +251,15 @@ const char* pkv_status_string(int32_t status) {
     }
 }
 
-// The cache write for every cache format; kbs/vbs are the NVFP4 block-scale
-// caches (null otherwise).
-static pkv_status rope_kv_write_impl(const pkv_tensor* q_p, const pkv_tensor* k_p, const pkv_tensor* v_p,
+// The arguments of a cache write, for every cache format; kbs/vbs are the
+// NVFP4 block-scale caches (null otherwise). a->T == 0: nothing to launch.
+static pkv_status make_rope_args(const pkv_tensor* q_p, const pkv_tensor* k_p, const pkv_tensor* v_p,
                                      const pkv_tensor* positions_p, const pkv_tensor* cos_sin_p,
                                      const pkv_tensor* k_cache_p, const pkv_tensor* v_cache_p,
                                      const pkv_tensor* kbs_p, const pkv_tensor* vbs_p,
                                      const pkv_tensor* slot_mapping_p, const pkv_tensor* k_scale_p,
                                      const pkv_tensor* v_scale_p, int32_t layout, int32_t rope_style,
-                                     int32_t* err_flag, pkv_stream_t stream, bool nvfp4) {
+                                     int32_t* err_flag, bool nvfp4, pkv::RopeArgs* out) {
     const pkv_tensor& q = arg(q_p);
     const pkv_tensor& k = arg(k_p);
     const pkv_tensor& v = arg(v_p);
@@ -305,7 +305,7 @@ static pkv_status rope_kv_write_impl(const pkv_tensor* q_p, const pkv_tensor* k_
     if (!row16(cos_sin, 1)) return PKV_ERR_UNSUPPORTED;
     if ((Hq + 2 * Hkv) * (D / 16) > 1024) return PKV_ERR_UNSUPPORTED;  // one token's rows per CTA
 
-    pkv::RopeArgs a{};
+    pkv::RopeArgs& a = *out;
     a.q = static_cast<uint16_t*>(q.ptr);
     a.q_s0 = q.ptr ? q.stride[0] : 0;
     a.q_s1 = q.ptr ? q.stride[1] : 0;
@@ -347,6 +347,20 @@ static pkv_status rope_kv_write_impl(const pkv_tensor* q_p, const pkv_tensor* k_
     a.interleaved = rope_style == PKV_ROPE_INTERLEAVED;
     a.kind = kind;
     a.err = err_flag;
+    return PKV_OK;
+}
+
+static pkv_status rope_kv_write_impl(const pkv_tensor* q_p, const pkv_tensor* k_p, const pkv_tensor* v_p,
+                                     const pkv_tensor* positions_p, const pkv_tensor* cos_sin_p,
+                                     const pkv_tensor* k_cache_p, const pkv_tensor* v_cache_p,
+                                     const pkv_tensor* kbs_p, const pkv_tensor* vbs_p,
+                                     const pkv_tensor* slot_mapping_p, const pkv_tensor* k_scale_p,
+                                     const pkv_tensor* v_scale_p, int32_t layout, int32_t rope_style,
+                                     int32_t* err_flag, pkv_stream_t stream, bool nvfp4) {
+    pkv::RopeArgs a{};
+    const pkv_status st = make_rope_args(q_p, k_p, v_p, positions_p, cos_sin_p, k_cache_p, v_cache_p, kbs_p, vbs_p,
+                                         slot_mapping_p, k_scale_p, v_scale_p, layout, rope_style, err_flag, nvfp4, &a);
+    if (st != PKV_OK || a.T == 0) return st;
     return cuda_status(pkv::launch_rope_kv_write(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -1619,6 +1633,146 @@ pkv_status pkv_paged_tree_decode(const pkv_tensor* q_p, const pkv_tensor* k_cach
     a.layout = layout;
     a.err = err_flag;
     return cuda_status(pkv::launch_tree_decode(a, tq, tk, tv, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// The [D] weights of a norm: float32 or bf16, read with 16-byte vectors.
+static pkv_status check_weight(const pkv_tensor& w, int64_t D, int32_t dtype) {
+    if (!w.ptr || !shape_ok(w, 1, dtype) || w.shape[0] != D) return PKV_ERR_INVALID_ARG;
+    return w.stride[0] != 1 || !aligned(w.ptr, 16) ? PKV_ERR_UNSUPPORTED : PKV_OK;
+}
+
+static bool same_view(const pkv_tensor& x, const pkv_tensor& y) {
+    return x.ptr == y.ptr && x.stride[0] == y.stride[0] && x.stride[1] == y.stride[1];
+}
+
+pkv_status pkv_qk_norm_rope_kv_write(const pkv_tensor* q_p, const pkv_tensor* k_p, const pkv_tensor* v_p,
+                                     const pkv_tensor* q_weight_p, const pkv_tensor* k_weight_p, float eps,
+                                     const pkv_tensor* positions_p, const pkv_tensor* cos_sin_p,
+                                     const pkv_tensor* k_cache_p, const pkv_tensor* v_cache_p,
+                                     const pkv_tensor* kbs_p, const pkv_tensor* vbs_p,
+                                     const pkv_tensor* slot_mapping_p, const pkv_tensor* k_scale_p,
+                                     const pkv_tensor* v_scale_p, const pkv_tensor* k_out_p, int32_t layout,
+                                     int32_t rope_style, int32_t* err_flag, pkv_stream_t stream) {
+    const pkv_tensor& q = arg(q_p);
+    const pkv_tensor& k = arg(k_p);
+    const pkv_tensor& qw = arg(q_weight_p);
+    const pkv_tensor& kw = arg(k_weight_p);
+    const pkv_tensor& ko = arg(k_out_p);
+    const bool nvfp4 = arg(kbs_p).ptr != nullptr;
+    pkv::NormArgs n{};
+    pkv_status st = make_rope_args(q_p, k_p, v_p, positions_p, cos_sin_p, k_cache_p, v_cache_p, nvfp4 ? kbs_p : nullptr,
+                                   nvfp4 ? vbs_p : nullptr, slot_mapping_p, k_scale_p, v_scale_p, layout, rope_style,
+                                   err_flag, nvfp4, &n.rope);
+    if (st != PKV_OK) return st;
+    const int64_t D = k.shape[2];
+    if ((st = check_weight(kw, D, kw.dtype == PKV_BF16 ? PKV_BF16 : PKV_F32)) != PKV_OK) return st;
+    if (q.ptr && (st = check_weight(qw, D, kw.dtype)) != PKV_OK) return st;
+    if (!std::isfinite(eps) || eps < 0.f) return PKV_ERR_INVALID_ARG;
+    if (ko.ptr) {
+        if (!shape_ok(ko, 3, PKV_BF16)) return PKV_ERR_INVALID_ARG;
+        for (int i = 0; i < 3; ++i)
+            if (ko.shape[i] != k.shape[i]) return PKV_ERR_INVALID_ARG;
+        if (!row16(ko, 2)) return PKV_ERR_UNSUPPORTED;
+        if (!same_view(ko, k))
+            for (const pkv_tensor* t : {&q, &k, &arg(v_p), &arg(k_cache_p), &arg(v_cache_p)})
+                if (t->ptr && overlap(ko, *t)) return PKV_ERR_INVALID_ARG;
+    }
+    if (n.rope.T == 0) return PKV_OK;
+    n.q_weight = qw.ptr;
+    n.k_weight = kw.ptr;
+    n.weight_bf16 = kw.dtype == PKV_BF16;
+    n.eps = eps;
+    n.k_out = static_cast<uint16_t*>(ko.ptr);
+    n.ko_s0 = ko.ptr ? ko.stride[0] : 0;
+    n.ko_s1 = ko.ptr ? ko.stride[1] : 0;
+    return cuda_status(pkv::launch_qk_norm_write(n, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_gather_kv(const pkv_tensor* k_cache_p, const pkv_tensor* v_cache_p, const pkv_tensor* kbs_p,
+                         const pkv_tensor* vbs_p, const pkv_tensor* block_tables_p, const pkv_tensor* start_p,
+                         const pkv_tensor* first_p, const pkv_tensor* k_out_p, const pkv_tensor* v_out_p,
+                         const pkv_tensor* k_scale_p, const pkv_tensor* v_scale_p, int32_t layout, int32_t* err_flag,
+                         pkv_stream_t stream) {
+    const pkv_tensor& kc = arg(k_cache_p);
+    const pkv_tensor& vc = arg(v_cache_p);
+    const pkv_tensor& kbs = arg(kbs_p);
+    const pkv_tensor& vbs = arg(vbs_p);
+    const pkv_tensor& bt = arg(block_tables_p);
+    const pkv_tensor& start = arg(start_p);
+    const pkv_tensor& first = arg(first_p);
+    const pkv_tensor& ko = arg(k_out_p);
+    const pkv_tensor& vo = arg(v_out_p);
+    const bool nvfp4 = kbs.ptr != nullptr;
+    int64_t num_pages, B, max_pages;
+    int P, Hkv, D;
+    pkv_status st = check_caches(kc, vc, layout, &num_pages, &P, &Hkv, &D, nvfp4);
+    if (st != PKV_OK) return st;
+    if (nvfp4 && (st = check_block_scales(kc, kbs, vbs, D, false)) != PKV_OK) return st;
+    const int kind = nvfp4 ? pkv::kFp4 : (kc.dtype == PKV_FP8_E4M3 ? pkv::kFp8 : pkv::kBf16);
+    int n_scale = 0;
+    if (kind != pkv::kBf16 && (st = check_scales(arg(k_scale_p), arg(v_scale_p), Hkv, &n_scale)) != PKV_OK) return st;
+    if ((st = check_tables(bt, &B, &max_pages)) != PKV_OK) return st;
+    if ((st = check_i32(start, B + 1)) != PKV_OK) return st;
+    if (first.ptr && (st = check_i32(first, B)) != PKV_OK) return st;
+    if (!shape_ok(ko, 3, PKV_BF16) || !shape_ok(vo, 3, PKV_BF16)) return PKV_ERR_INVALID_ARG;
+    const int64_t T = ko.shape[0];
+    if (ko.shape[1] != Hkv || ko.shape[2] != D || vo.shape[0] != T || vo.shape[1] != Hkv || vo.shape[2] != D)
+        return PKV_ERR_INVALID_ARG;
+    if (T > 0x7FFFFFFF || B > 65535 || Hkv > 65535) return PKV_ERR_UNSUPPORTED;
+    if (T == 0 || B == 0) return PKV_OK;
+    if (!ko.ptr || !vo.ptr) return PKV_ERR_INVALID_ARG;
+    if (!row16(ko, 2) || !row16(vo, 2)) return PKV_ERR_UNSUPPORTED;
+    for (const pkv_tensor* t : {&kc, &vc, &kbs, &vbs})
+        if (t->ptr && (overlap(ko, *t) || overlap(vo, *t))) return PKV_ERR_INVALID_ARG;
+
+    const int tok = layout == PKV_HND ? 2 : 1, head = 3 - tok;
+    pkv::GatherArgs a{};
+    a.k_cache = kc.ptr;
+    a.v_cache = vc.ptr;
+    a.kc_s0 = kc.stride[0];
+    a.kc_st = kc.stride[tok];
+    a.kc_sh = kc.stride[head];
+    a.vc_s0 = vc.stride[0];
+    a.vc_st = vc.stride[tok];
+    a.vc_sh = vc.stride[head];
+    if (nvfp4) {
+        a.k_bs = static_cast<const uint8_t*>(kbs.ptr);
+        a.v_bs = static_cast<const uint8_t*>(vbs.ptr);
+        a.kbs_s0 = kbs.stride[0];
+        a.kbs_st = kbs.stride[tok];
+        a.kbs_sh = kbs.stride[head];
+        a.vbs_s0 = vbs.stride[0];
+        a.vbs_st = vbs.stride[tok];
+        a.vbs_sh = vbs.stride[head];
+    }
+    if (kind != pkv::kBf16) {
+        a.k_scale = static_cast<const float*>(arg(k_scale_p).ptr);
+        a.v_scale = static_cast<const float*>(arg(v_scale_p).ptr);
+        a.n_scale = n_scale;
+    }
+    a.block_tables = static_cast<const int32_t*>(bt.ptr);
+    a.bt_s0 = bt.stride[0];
+    a.max_pages = static_cast<int32_t>(max_pages);
+    a.page_size = P;
+    a.page_shift = -1;
+    for (int sh = 0; sh < 31; ++sh)
+        if ((1 << sh) == P) a.page_shift = sh;
+    a.start = static_cast<const int32_t*>(start.ptr);
+    a.first = static_cast<const int32_t*>(first.ptr);
+    a.k_out = static_cast<uint16_t*>(ko.ptr);
+    a.ko_s0 = ko.stride[0];
+    a.ko_s1 = ko.stride[1];
+    a.v_out = static_cast<uint16_t*>(vo.ptr);
+    a.vo_s0 = vo.stride[0];
+    a.vo_s1 = vo.stride[1];
+    a.num_pages = num_pages;
+    a.T = T;
+    a.B = static_cast<int32_t>(B);
+    a.Hkv = Hkv;
+    a.D = D;
+    a.kind = kind;
+    a.err = err_flag;
+    return cuda_status(pkv::launch_gather_kv(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int64_t pkv_prompt_attention_workspace(int32_t D, int32_t sm_count) {

@@ -265,6 +265,43 @@ struct TreeArgs {
     int32_t* err;
 };
 
+struct NormArgs {
+    RopeArgs rope;
+    const void* q_weight;      // [D], float32 or bf16
+    const void* k_weight;
+    int32_t weight_bf16;
+    float eps;
+    uint16_t* k_out;           // [T, Hkv, D] bf16 bits, may be null
+    int64_t ko_s0, ko_s1;
+};
+
+struct GatherArgs {
+    const void* k_cache;
+    const void* v_cache;
+    int64_t kc_s0, kc_st, kc_sh;     // element strides: page, token, head
+    int64_t vc_s0, vc_st, vc_sh;
+    const uint8_t* k_bs;             // nvfp4 block scales, else null
+    const uint8_t* v_bs;
+    int64_t kbs_s0, kbs_st, kbs_sh;  // bytes
+    int64_t vbs_s0, vbs_st, vbs_sh;
+    const float* k_scale;            // fp8 / nvfp4 only
+    const float* v_scale;
+    int32_t n_scale;
+    const int32_t* block_tables;
+    int64_t bt_s0;
+    int32_t max_pages, page_size, page_shift;  // page_shift: log2 of the size where it is a power of two, else -1
+    const int32_t* start;            // [B + 1]
+    const int32_t* first;            // [B], null = 0
+    uint16_t* k_out;                 // [T, Hkv, D] bf16 bits
+    int64_t ko_s0, ko_s1;
+    uint16_t* v_out;
+    int64_t vo_s0, vo_s1;
+    int64_t num_pages, T;
+    int32_t B, Hkv, D, kind;
+    int32_t rows;                    // rows of a CTA (set by the launcher)
+    int32_t* err;
+};
+
 struct PromptArgs {
     const uint16_t* v;         // [Tk, Hkv, D] bf16 bits
     int64_t v_s0, v_s1;
@@ -325,6 +362,8 @@ cudaError_t launch_tree_decode(const TreeArgs& a, const CUtensorMap& tq, const C
                                cudaStream_t s);
 // Joins the partial sums of cut items (of a: T, Hq, D, G, tile_toks, out, lse, workspace).
 cudaError_t launch_row_join(const TreeArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_qk_norm_write(const NormArgs& a, cudaStream_t s);
+cudaError_t launch_gather_kv(const GatherArgs& a, cudaStream_t s);
 cudaError_t launch_prompt_attention(const PromptArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                     cudaStream_t s);
 int64_t prompt_attention_workspace(int32_t D, int32_t sm_count);

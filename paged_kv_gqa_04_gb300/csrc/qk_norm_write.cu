@@ -1,0 +1,213 @@
+// qk_norm_write.cu -- RMS norm of every q and k head, RoPE and the paged-KV
+// cache write in one pass.
+//
+// Mapping: as rope_kv_write_kernel, thread c of a row's D/16 owns the 8-value
+// chunks at 8c and at D/2 + 8c, partners of one another's rotation pairs. A
+// thread takes up to U heads of one token: its positions, its cos / sin and its
+// weights are loaded once for them, and all of their rows before any is used.
+// Threads are ordered by the kind of row first (q, k, v), then by token and group
+// of heads, so that a row's threads are consecutive lanes of one warp; the sum of
+// a row's squares is a butterfly over them.
+//
+// Arithmetic: r = 1 / sqrt(mean(x^2) + eps), the mean in float32 (its sum in a
+// fixed order), the root and the quotient correctly rounded; y = (x r) w, each
+// product rounded; then the rotation and the cache formats of rope_kv_write.cu, bit
+// for bit.
+//
+// Bound: HBM for fills (24,000 tokens of 32 + 2 x 8 heads, D = 128, bf16, keys
+// kept), latency for a step's tokens.
+#include "pkv_internal.h"
+#include "pkv_ptx.cuh"
+#include "rope_row.cuh"
+
+namespace pkv {
+namespace {
+
+// The thread's 16 weights: chunks 8c and D/2 + 8c of [D] float32 or bf16.
+template <int D>
+__device__ __forceinline__ void load_weights(const void* w, int is_bf16, int c, Chunk8& lo, Chunk8& hi) {
+    if (is_bf16) {
+        const uint16_t* p = static_cast<const uint16_t*>(w);
+        lo = unpack_bf16x8(*reinterpret_cast<const uint4*>(p + 8 * c));
+        hi = unpack_bf16x8(*reinterpret_cast<const uint4*>(p + D / 2 + 8 * c));
+    } else {
+        const float* p = static_cast<const float*>(w);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float4 x = *reinterpret_cast<const float4*>(p + 8 * c + 4 * k);
+            const float4 y = *reinterpret_cast<const float4*>(p + D / 2 + 8 * c + 4 * k);
+            lo.v[4 * k] = x.x, lo.v[4 * k + 1] = x.y, lo.v[4 * k + 2] = x.z, lo.v[4 * k + 3] = x.w;
+            hi.v[4 * k] = y.x, hi.v[4 * k + 1] = y.y, hi.v[4 * k + 2] = y.z, hi.v[4 * k + 3] = y.w;
+        }
+    }
+}
+
+template <int D, bool INTER, int KIND, int U>
+__global__ void __launch_bounds__(U == 1 ? 1024 : 512, U == 1 ? 1 : 2) qk_norm_write_kernel(const NormArgs n) {
+    constexpr int TPR = D / 16;  // threads per row
+    const RopeArgs& a = n.rope;
+    // As rope_kv_write_kernel: a programmatic dependent, whose successor waits for it.
+    grid_dep_wait();
+    grid_dep_launch();
+    const int L = threadIdx.x;
+    const int gq = (a.Hq + U - 1) / U, gk = (a.Hkv + U - 1) / U;  // groups of heads of a token
+    const int nq = a.toks * gq * TPR, nk = a.toks * gk * TPR;
+    const bool is_q = L < nq, is_k = !is_q && L < nq + nk;
+    const int j = is_q ? L : (is_k ? L - nq : L - nq - nk);
+    const int per = (is_q ? gq : gk) * TPR;  // threads of one token's rows of this kind
+    const int tl = j / per;
+    const int h0 = (j - tl * per) / TPR * U;
+    const int c = j % TPR;
+    const int heads = is_q ? a.Hq : a.Hkv;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * a.toks + tl;
+    if (t >= a.T) return;
+
+    // Reading the rows of a skipped token stays inside the [T, heads, D] input.
+    const int64_t s1 = is_q ? a.q_s1 : (is_k ? a.k_s1 : a.v_s1);
+    const uint16_t* src = is_q ? a.q + t * a.q_s0 : (is_k ? a.k + t * a.k_s0 : a.v + t * a.v_s0);
+    const int32_t slot = __ldg(a.slots + t), pos = __ldg(a.positions + t);
+    uint4 wlo[U], whi[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (h0 + u >= heads) break;
+        const uint16_t* p = src + (h0 + u) * s1;
+        wlo[u] = *reinterpret_cast<const uint4*>(p + 8 * c);
+        whi[u] = *reinterpret_cast<const uint4*>(p + D / 2 + 8 * c);
+    }
+    if (slot < 0) return;
+    const bool lead = h0 == 0 && c == 0;  // flags a bad token once per kind
+    if (slot >= a.num_pages * a.page_size) {
+        if (lead) flag_error(a.err, PKV_FLAG_SLOT_RANGE);
+        return;
+    }
+    if (pos < 0 || pos >= a.max_pos) {
+        if (lead) flag_error(a.err, PKV_FLAG_POSITION_RANGE);
+        return;
+    }
+    float cv[8], sv[8];
+    Chunk8 glo, ghi;
+    if (is_q || is_k) {
+        load_cos_sin<D, INTER>(a.cos_sin + pos * a.cs_s0, c, cv, sv);
+        load_weights<D>(is_q ? n.q_weight : n.k_weight, n.weight_bf16, c, glo, ghi);
+    }
+    int64_t page;
+    int off;
+    if (a.page_size == 16) {
+        page = slot >> 4;
+        off = slot & 15;
+    } else {
+        page = slot / a.page_size;
+        off = static_cast<int>(slot - page * a.page_size);
+    }
+    const int64_t* st = is_k ? a.kc_s : a.vc_s;
+    const int64_t cache_row = page * st[0] + off * (a.layout == PKV_HND ? st[2] : st[1]);
+    const int64_t cache_head = a.layout == PKV_HND ? st[1] : st[2];
+    // (the lanes of this row and of the rows beside it in a half, quarter or eighth of the warp are all here)
+    const unsigned row_lanes = ((1u << TPR) - 1u) << (lane_id() & ~(TPR - 1u));
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int h = h0 + u;
+        if (h >= heads) break;
+        Chunk8 lo = unpack_bf16x8(wlo[u]), hi = unpack_bf16x8(whi[u]);
+        if (is_q || is_k) {
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fmaf(lo.v[e], lo.v[e], fmaf(hi.v[e], hi.v[e], ss));
+#pragma unroll
+            for (int d = 1; d < TPR; d <<= 1) ss += __shfl_xor_sync(row_lanes, ss, d);
+            const float r = __frcp_rn(__fsqrt_rn(fmaf(ss, 1.f / D, n.eps)));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                lo.v[e] = __fmul_rn(__fmul_rn(lo.v[e], r), glo.v[e]);
+                hi.v[e] = __fmul_rn(__fmul_rn(hi.v[e], r), ghi.v[e]);
+            }
+            rotate_row<INTER>(lo, hi, cv, sv);
+        }
+        if (is_q || (is_k && n.k_out != nullptr)) {
+            uint16_t* p = is_q ? a.q + t * a.q_s0 + h * a.q_s1 : n.k_out + t * n.ko_s0 + h * n.ko_s1;
+            *reinterpret_cast<uint4*>(p + 8 * c) = pack_bf16x8(lo);
+            *reinterpret_cast<uint4*>(p + D / 2 + 8 * c) = pack_bf16x8(hi);
+        }
+        if (is_q) continue;
+        const int64_t e = cache_row + h * cache_head;
+        if constexpr (KIND == kBf16) {
+            uint16_t* dst = static_cast<uint16_t*>(is_k ? a.k_cache : a.v_cache) + e;
+            *reinterpret_cast<uint4*>(dst + 8 * c) = is_k ? pack_bf16x8(lo) : wlo[u];
+            *reinterpret_cast<uint4*>(dst + D / 2 + 8 * c) = is_k ? pack_bf16x8(hi) : whi[u];
+        } else {
+            const float scale = __ldg((is_k ? a.k_scale : a.v_scale) + (a.n_scale == 1 ? 0 : h));
+            uint8_t* dst = static_cast<uint8_t*>(is_k ? a.k_cache : a.v_cache) + e;
+            if constexpr (KIND == kFp8) {
+                const E4m3Rcp r8 = e4m3_rcp(scale);
+                *reinterpret_cast<uint2*>(dst + 8 * c) = pack_e4m3x8(lo, scale, r8);
+                *reinterpret_cast<uint2*>(dst + D / 2 + 8 * c) = pack_e4m3x8(hi, scale, r8);
+            } else {
+                // both lanes of a pair (chunks c, c^1 of this row) hold a block's halves
+                const float six_g = __fmul_rn(6.f, scale);
+                const E4m3Rcp r6 = bracket_rcp(six_g);
+                const unsigned pair = 3u << (lane_id() & 30u);
+                float am_lo = amax8(lo), am_hi = amax8(hi);
+                am_lo = fmaxf(am_lo, __shfl_xor_sync(pair, am_lo, 1));
+                am_hi = fmaxf(am_hi, __shfl_xor_sync(pair, am_hi, 1));
+                uint32_t s_lo, s_hi;
+                const uint32_t w_lo = nvfp4_half(lo, am_lo, scale, six_g, r6, s_lo);
+                const uint32_t w_hi = nvfp4_half(hi, am_hi, scale, six_g, r6, s_hi);
+                *reinterpret_cast<uint32_t*>(dst + 4 * c) = w_lo;
+                *reinterpret_cast<uint32_t*>(dst + D / 4 + 4 * c) = w_hi;
+                const int64_t* bs = is_k ? a.kbs_s : a.vbs_s;
+                uint8_t* bdst = (is_k ? a.k_bs : a.v_bs) + page * bs[0] +
+                                (a.layout == PKV_HND ? h * bs[1] + off * bs[2] : off * bs[1] + h * bs[2]);
+                if (c & 1)
+                    bdst[D / 32 + c / 2] = static_cast<uint8_t>(s_hi);
+                else
+                    bdst[c / 2] = static_cast<uint8_t>(s_lo);
+            }
+        }
+    }
+}
+
+template <int D, bool INTER, int KIND, int U>
+cudaError_t launch_u(const NormArgs& n, cudaStream_t s) {
+    const RopeArgs& a = n.rope;
+    const int per_tok = ((a.Hq + U - 1) / U + 2 * ((a.Hkv + U - 1) / U)) * (D / 16);  // threads of one token
+    if (per_tok > (U == 1 ? 1024 : 512)) return cudaErrorInvalidConfiguration;
+    const int toks = per_tok >= 256 ? 1 : 256 / per_tok;
+    const int64_t blocks = (a.T + toks - 1) / toks;
+    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    NormArgs b = n;
+    b.rope.toks = toks;
+    return launch_dependent(qk_norm_write_kernel<D, INTER, KIND, U>, dim3(static_cast<unsigned>(blocks)),
+                            dim3(per_tok * toks), 0, s, b);
+}
+
+#ifndef PKV_NORM_HEADS
+#define PKV_NORM_HEADS 4
+#endif
+template <int D, bool INTER, int KIND>
+cudaError_t launch_t(const NormArgs& n, cudaStream_t s) {
+    const RopeArgs& a = n.rope;
+    if (a.T == 0) return cudaSuccess;
+    // Several heads a thread where that still fills the GPU.
+    const int64_t threads = a.T * (a.Hq + 2 * a.Hkv) * (D / 16);
+    if (threads >= 152 * 2048 * 4) return launch_u<D, INTER, KIND, PKV_NORM_HEADS>(n, s);
+    return launch_u<D, INTER, KIND, 1>(n, s);
+}
+
+template <int D, bool INTER>
+cudaError_t launch_k(const NormArgs& n, cudaStream_t s) {
+    switch (n.rope.kind) {
+        case kBf16: return launch_t<D, INTER, kBf16>(n, s);
+        case kFp8: return launch_t<D, INTER, kFp8>(n, s);
+        case kFp4: return launch_t<D, INTER, kFp4>(n, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_qk_norm_write(const NormArgs& n, cudaStream_t s) {
+    if (n.rope.D == 128) return n.rope.interleaved ? launch_k<128, true>(n, s) : launch_k<128, false>(n, s);
+    return n.rope.interleaved ? launch_k<64, true>(n, s) : launch_k<64, false>(n, s);
+}
+
+}  // namespace pkv
