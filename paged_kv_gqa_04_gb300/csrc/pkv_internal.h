@@ -273,6 +273,7 @@ struct NormArgs {
     float eps;
     uint16_t* k_out;           // [T, Hkv, D] bf16 bits, may be null
     int64_t ko_s0, ko_s1;
+    uint32_t ctas_q, ctas_kv;  // CTAs of q, of k (as many of v) (set by the launcher)
 };
 
 struct GatherArgs {

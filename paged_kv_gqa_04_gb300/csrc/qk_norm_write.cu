@@ -3,11 +3,11 @@
 //
 // Mapping: as rope_kv_write_kernel, thread c of a row's D/16 owns the 8-value
 // chunks at 8c and at D/2 + 8c, partners of one another's rotation pairs. A
-// thread takes up to U heads of one token: its positions, its cos / sin and its
-// weights are loaded once for them, and all of their rows before any is used.
-// Threads are ordered by the kind of row first (q, k, v), then by token and group
-// of heads, so that a row's threads are consecutive lanes of one warp; the sum of
-// a row's squares is a butterfly over them.
+// thread takes U heads of one token: its position, its cos / sin and its weights
+// are loaded once for them, and all of their rows before any is used. A CTA's
+// rows are of one kind (the grid is the CTAs of q, then of k, then of v), in the
+// order of tokens and groups of heads; a row's threads are consecutive lanes of
+// one warp, and the sum of its squares is a butterfly over them.
 //
 // Arithmetic: r = 1 / sqrt(mean(x^2) + eps), the mean in float32 (its sum in a
 // fixed order), the root and the quotient correctly rounded; y = (x r) w, each
@@ -42,24 +42,27 @@ __device__ __forceinline__ void load_weights(const void* w, int is_bf16, int c, 
     }
 }
 
+// Small CTAs: one that waits for its loads holds up fewer of the others (32 prompts of 300 to 2000 tokens, bf16,
+// keys kept, four heads a thread: 190 us with 2 CTAs of 256 threads an SM, 172 with 5 of 128, 171 with 10 of 64; 11 of
+// 64 spill, 251).
+constexpr int kThreads = 64;
+constexpr int kCtas = 10;  // an SM's, that registers are budgeted for
+
 template <int D, bool INTER, int KIND, int U>
-__global__ void __launch_bounds__(U == 1 ? 1024 : 512, U == 1 ? 1 : 2) qk_norm_write_kernel(const NormArgs n) {
+__global__ void __launch_bounds__(kThreads, kCtas) qk_norm_write_kernel(const NormArgs n) {
     constexpr int TPR = D / 16;  // threads per row
     const RopeArgs& a = n.rope;
     // As rope_kv_write_kernel: a programmatic dependent, whose successor waits for it.
     grid_dep_wait();
     grid_dep_launch();
-    const int L = threadIdx.x;
-    const int gq = (a.Hq + U - 1) / U, gk = (a.Hkv + U - 1) / U;  // groups of heads of a token
-    const int nq = a.toks * gq * TPR, nk = a.toks * gk * TPR;
-    const bool is_q = L < nq, is_k = !is_q && L < nq + nk;
-    const int j = is_q ? L : (is_k ? L - nq : L - nq - nk);
-    const int per = (is_q ? gq : gk) * TPR;  // threads of one token's rows of this kind
-    const int tl = j / per;
-    const int h0 = (j - tl * per) / TPR * U;
-    const int c = j % TPR;
+    const bool is_q = blockIdx.x < n.ctas_q, is_k = !is_q && blockIdx.x < n.ctas_q + n.ctas_kv;
+    const uint32_t cta = blockIdx.x - (is_q ? 0u : n.ctas_q + (is_k ? 0u : n.ctas_kv));
     const int heads = is_q ? a.Hq : a.Hkv;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * a.toks + tl;
+    const uint32_t groups = (heads + U - 1) / U;   // of heads, of a token
+    const uint32_t item = cta * (kThreads / TPR) + threadIdx.x / TPR;
+    const int64_t t = item / groups;
+    const int h0 = static_cast<int>(item - static_cast<uint32_t>(t) * groups) * U;
+    const int c = threadIdx.x % TPR;
     if (t >= a.T) return;
 
     // Reading the rows of a skipped token stays inside the [T, heads, D] input.
@@ -110,16 +113,22 @@ __global__ void __launch_bounds__(U == 1 ? 1024 : 512, U == 1 ? 1 : 2) qk_norm_w
         if (h >= heads) break;
         Chunk8 lo = unpack_bf16x8(wlo[u]), hi = unpack_bf16x8(whi[u]);
         if (is_q || is_k) {
-            float ss = 0.f;
+            float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(lo.v[e], lo.v[e], fmaf(hi.v[e], hi.v[e], ss));
+            for (int e = 0; e < 8; e += 2) {
+                s2[0] = fma2(make_float2(lo.v[e], lo.v[e + 1]), make_float2(lo.v[e], lo.v[e + 1]), s2[0]);
+                s2[1] = fma2(make_float2(hi.v[e], hi.v[e + 1]), make_float2(hi.v[e], hi.v[e + 1]), s2[1]);
+            }
+            float ss = (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
 #pragma unroll
             for (int d = 1; d < TPR; d <<= 1) ss += __shfl_xor_sync(row_lanes, ss, d);
             const float r = __frcp_rn(__fsqrt_rn(fmaf(ss, 1.f / D, n.eps)));
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                lo.v[e] = __fmul_rn(__fmul_rn(lo.v[e], r), glo.v[e]);
-                hi.v[e] = __fmul_rn(__fmul_rn(hi.v[e], r), ghi.v[e]);
+            for (int e = 0; e < 8; e += 2) {
+                mul_rn_x2(lo.v[e], lo.v[e + 1], r, r, lo.v[e], lo.v[e + 1]);
+                mul_rn_x2(hi.v[e], hi.v[e + 1], r, r, hi.v[e], hi.v[e + 1]);
+                mul_rn_x2(lo.v[e], lo.v[e + 1], glo.v[e], glo.v[e + 1], lo.v[e], lo.v[e + 1]);
+                mul_rn_x2(hi.v[e], hi.v[e + 1], ghi.v[e], ghi.v[e + 1], hi.v[e], hi.v[e + 1]);
             }
             rotate_row<INTER>(lo, hi, cv, sv);
         }
@@ -169,27 +178,26 @@ __global__ void __launch_bounds__(U == 1 ? 1024 : 512, U == 1 ? 1 : 2) qk_norm_w
 template <int D, bool INTER, int KIND, int U>
 cudaError_t launch_u(const NormArgs& n, cudaStream_t s) {
     const RopeArgs& a = n.rope;
-    const int per_tok = ((a.Hq + U - 1) / U + 2 * ((a.Hkv + U - 1) / U)) * (D / 16);  // threads of one token
-    if (per_tok > (U == 1 ? 1024 : 512)) return cudaErrorInvalidConfiguration;
-    const int toks = per_tok >= 256 ? 1 : 256 / per_tok;
-    const int64_t blocks = (a.T + toks - 1) / toks;
-    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    constexpr int kItems = kThreads / (D / 16);
+    auto ctas = [&](int heads) { return (a.T * ((heads + U - 1) / U) + kItems - 1) / kItems; };
+    const int64_t q = ctas(a.Hq), kv = ctas(a.Hkv);
+    if ((q + 2 * kv) * kItems > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     NormArgs b = n;
-    b.rope.toks = toks;
-    return launch_dependent(qk_norm_write_kernel<D, INTER, KIND, U>, dim3(static_cast<unsigned>(blocks)),
-                            dim3(per_tok * toks), 0, s, b);
+    b.ctas_q = static_cast<uint32_t>(q);
+    b.ctas_kv = static_cast<uint32_t>(kv);
+    return launch_dependent(qk_norm_write_kernel<D, INTER, KIND, U>, dim3(static_cast<unsigned>(q + 2 * kv)), dim3(kThreads), 0,
+                            s, b);
 }
 
-#ifndef PKV_NORM_HEADS
-#define PKV_NORM_HEADS 4
-#endif
+// Heads a thread: one where there are few rows, four where there are many (32 + 2 x 8 heads, bf16, keys kept, back to
+// back: 256 tokens 3.0 us and not 3.7, 1024 tokens 5.3 and not 7.5, 16,384 tokens 80 and not 114; 12 + 2 x 2, FP8: 1024
+// tokens 3.4 and 3.6, 2048 tokens 4.8 and not 5.4. Two: between them, but 2.8 us at 256 tokens.)
+constexpr int64_t kManyRows = 20480;
 template <int D, bool INTER, int KIND>
 cudaError_t launch_t(const NormArgs& n, cudaStream_t s) {
     const RopeArgs& a = n.rope;
     if (a.T == 0) return cudaSuccess;
-    // Several heads a thread where that still fills the GPU.
-    const int64_t threads = a.T * (a.Hq + 2 * a.Hkv) * (D / 16);
-    if (threads >= 152 * 2048 * 4) return launch_u<D, INTER, KIND, PKV_NORM_HEADS>(n, s);
+    if (a.T * (a.Hq + 2 * a.Hkv) >= kManyRows) return launch_u<D, INTER, KIND, 4>(n, s);
     return launch_u<D, INTER, KIND, 1>(n, s);
 }
 
