@@ -1674,7 +1674,7 @@ pkv_status pkv_qk_norm_rope_kv_write(const pkv_tensor* q_p, const pkv_tensor* k_
             if (ko.shape[i] != k.shape[i]) return PKV_ERR_INVALID_ARG;
         if (!row16(ko, 2)) return PKV_ERR_UNSUPPORTED;
         if (!same_view(ko, k))
-            for (const pkv_tensor* t : {&q, &k, &arg(v_p), &arg(k_cache_p), &arg(v_cache_p)})
+            for (const pkv_tensor* t : {&q, &k, &arg(v_p), &arg(k_cache_p), &arg(v_cache_p), &arg(kbs_p), &arg(vbs_p)})
                 if (t->ptr && overlap(ko, *t)) return PKV_ERR_INVALID_ARG;
     }
     if (n.rope.T == 0) return PKV_OK;

@@ -461,8 +461,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 // 128-byte-swizzled operands, 1024 bytes between groups of 8 rows
                 constexpr uint64_t kDescHi = static_cast<uint64_t>((1024 >> 4) | (1u << 14) | (2u << 29)) << 32;
                 auto desc = [](uint32_t addr, uint32_t lead) -> uint64_t { return kDescHi | ((addr >> 4) & 0x3FFFu) | (lead >> 4) << 16; };
-                // Stages and phases of the next tile of K, of V; per group, in either half of a word: P taken, items
-                // whose scores were begun.
+                // Stages and phases of the next tile of K, of V. Per group: the phase of the P that is next (bit g), and
+                // in two bits at 2 g the items whose scores were begun, 2 or 3 for all of that parity from there on.
                 int sk = 0, sv = 0, n_fix = 0;
                 uint32_t pk = 0, pv = 0, n_p = 0, items = 0, issued = 0;
                 auto next_k = [&]() {
@@ -497,8 +497,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 // The first scores of a piece for row tile g.
                 auto begin = [&](const Job& w, int g) {
                     if (g == 0) lane_wait(bar(bKFull + sk), pk);
-                    lane_wait(bar(bQ + g), items >> (16 * g) & 1);
-                    items += 1u << (16 * g);
+                    lane_wait(bar(bQ + g), items >> (2 * g) & 1);
+                    items = (items >> (2 * g) & 3u) == 3u ? items ^ 1u << (2 * g) : items + (1u << (2 * g));
                     scores(g, cols_of(w, g, w.t0));
                     issued = 1;
                     if (g == w.two) next_k();
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                                 const uint64_t vt = desc(s0 + C::OFF_V + sv * C::TILE, C::BLOCK);
 #pragma unroll
                                 for (int g = 0; g < 2; ++g) {
-                                    lane_wait(bar(bP + g), n_p >> (16 * g) & 1);
+                                    lane_wait(bar(bP + g), n_p >> g & 1);
                                     tc_fence_after();
 #pragma unroll
                                     for (int k = 0; k < kTile / 16; ++k)
@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                                     if (g == 0) lane_wait(bar(bKFull + sk), pk);
                                     scores(g, kTile);
                                 }
-                                n_p += 0x10001u;
+                                n_p ^= 3u;
                                 next_v();
                                 next_k();
                             }
@@ -546,10 +546,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 #pragma unroll 1
                         for (int g = 0; g <= w.two; ++g) {
                             // the item before has been read out of O
-                            if (t == w.t0 && (items >> (16 * g) & 0xFFFFu) > 1) lane_wait(bar(bOFree + g), items >> (16 * g) & 1);
+                            if (t == w.t0 && (items >> (2 * g) & 2u)) lane_wait(bar(bOFree + g), items >> (2 * g) & 1);
                             const int steps = cols_of(w, g, t) >> 4;
-                            lane_wait(bar(bP + g), n_p >> (16 * g) & 1);
-                            n_p += 1u << (16 * g);
+                            lane_wait(bar(bP + g), n_p >> g & 1);
+                            n_p ^= 1u << g;
                             tc_fence_after();
                             const uint32_t more_o = t > w.t0 ? 1u : go_on[g];  // O goes on, or starts
 #pragma unroll 1

@@ -199,3 +199,31 @@ def test_long_prompt():
     s = make_prompt([20000], [0], 4, 2, 128, seed=15)
     run_prompt(s)
     check_prompt(s, rows=[0, 1, 127, 128, 5000, 9999, 10000, 15001, 19998, 19999])
+
+
+def test_more_tiles_of_a_cta_than_sixteen_bits_count():
+    # 21.6 million tiles: 134,726 a CTA on 160 of them
+    n, H, D = 420_000, 8, 64
+    s = make_prompt([n], [0], H, H, D, seed=31)
+    run_prompt(s)
+    check_prompt(s, rows=[0, 1, 127, 128, 65_537, 131_071, 262_145, 300_001, n - 129, n - 1])
+
+
+def test_more_items_of_a_cta_than_sixteen_bits_count():
+    # One token a sequence, which sees itself alone: its value is the answer. 12 million items.
+    B, H, D = 60_000, 200, 64
+    s = make_prompt([0], [0], H, H, D)
+    g = torch.Generator(device="cuda").manual_seed(32)
+    for x in ("q", "k", "v"):
+        s[x] = torch.randn(B, H, D, generator=g, device="cuda", dtype=torch.bfloat16)
+    s.update(q_start=torch.arange(B + 1, dtype=torch.int32, device="cuda"), k_start=None,
+             out=torch.full_like(s["q"], 7.0), lse=torch.full((B, H), 7.0, device="cuda"))
+    run_prompt(s)
+    torch.cuda.synchronize()
+    assert int(s["err"].item()) == 0
+    # The weight w is one bf16, l its fp32: w v / l and the output's rounding are at most 2^-8 of v each.
+    v = s["v"].float()
+    assert bool(((s["out"].float() - v).abs() <= 2.0 ** -7 * v.abs()).all())
+    x = (s["q"].float() * s["k"].float()).sum(-1) * s["scale"]
+    mag = (s["q"].float() * s["k"].float()).abs().sum(-1) * s["scale"]
+    assert bool(((s["lse"] - x).abs() <= (2 * D + 16) * 2.0 ** -24 * mag + 2.0 ** -20 + 2.0 ** -22 * x.abs()).all())
