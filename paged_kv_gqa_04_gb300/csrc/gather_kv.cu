@@ -11,7 +11,11 @@
 // are exact in f16; the product with the static scale is float32, rounded once
 // more to bf16.
 //
-// Bound: HBM, where there are rows enough.
+// Bound: HBM, where there are rows enough (153,123 rows of 8 heads, D = 128: bf16
+// 1,254 MB in 185 us, a copy's rate; 126,341 of FP8 in 120 us, 95%; 64,760 rows of 4
+// heads, NVFP4: 170 MB in 31 us, 80%, the start and the end of the grid being the
+// rest). 16 values a thread take more registers, so fewer loads in flight (FP8 138 us
+// and not 123, NVFP4 41 and not 32).
 #include <algorithm>
 
 #include "pkv_internal.h"
@@ -108,7 +112,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherArgs a) {
     // (starts that do not ascend within the rows)
     if (blockIdx.x == 0) {
         bool bad = false;
-        for (int b = tid; b <= a.B; b += kThreads) {
+        for (int b = tid; b <= a.B; b += blockDim.x * blockDim.y) {
             const int x = __ldg(a.start + b);
             bad |= x < (b ? __ldg(a.start + b - 1) : 0) || x > a.T;
         }
@@ -152,8 +156,8 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherArgs a) {
             for (int u = 0; u < kUnroll; ++u) {
                 if (page[u] == kNobody) continue;
                 const int64_t t = t0 + r0 + u * Y;
-                *reinterpret_cast<uint4*>(a.k_out + t * a.ko_s0 + h * a.ko_s1 + 8 * c) = values<KIND>(k[u], gk);
-                *reinterpret_cast<uint4*>(a.v_out + t * a.vo_s0 + h * a.vo_s1 + 8 * c) = values<KIND>(v[u], gv);
+                *reinterpret_cast<uint4*>(a.k_out + t * a.ko_s0 + h * a.ko_s1 + 8 * c) = values<KIND>(k[u], page[u] == kZeros ? 0.f : gk);
+                *reinterpret_cast<uint4*>(a.v_out + t * a.vo_s0 + h * a.vo_s1 + 8 * c) = values<KIND>(v[u], page[u] == kZeros ? 0.f : gv);
             }
         }
     }

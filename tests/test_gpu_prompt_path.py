@@ -296,3 +296,26 @@ def test_bound_buffers_and_another_stream():
     run_write({k: pkv.bind(v) if isinstance(v, torch.Tensor) else v for k, v in t.items()}, stream=st)
     torch.cuda.synchronize()
     assert all(torch.equal(s[x], t[x]) for x in ("q", "k_out", "k_cache", "v_cache", "k_bs", "v_bs"))
+
+
+@pytest.mark.parametrize("Hkv", [3, 8])
+def test_read_flags_starts_wherever_they_are(Hkv):
+    # (24 threads a row and 240 a CTA, or 256)
+    for at in (1, 130, 239, 240, 247, 255, 256, 299):
+        s = make_read([1] * 300, [0] * 300, Hkv, 64, seed=11)
+        s["start"][at] = 301
+        run_read(s)
+        torch.cuda.synchronize()
+        assert int(s["err"].item()) & pkv.FLAG_ROW_RANGE, at
+
+
+@pytest.mark.parametrize("dtype", ["fp8", "nvfp4"])
+def test_read_of_bad_pages_gives_zeros_whatever_the_scale(dtype):
+    s = make_read([20], [0], 2, 64, dtype=dtype, seed=12)
+    s["bt"][0, 1] = -1
+    s["k_scale"][:] = float("nan")
+    s["v_scale"][:] = float("inf")
+    run_read(s)
+    torch.cuda.synchronize()
+    assert int(s["err"].item()) == pkv.FLAG_PAGE_RANGE
+    assert bool((s["k_out"][16:] == 0).all()) and bool((s["v_out"][16:] == 0).all())
