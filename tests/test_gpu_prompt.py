@@ -227,3 +227,15 @@ def test_more_items_of_a_cta_than_sixteen_bits_count():
     x = (s["q"].float() * s["k"].float()).sum(-1) * s["scale"]
     mag = (s["q"].float() * s["k"].float()).abs().sum(-1) * s["scale"]
     assert bool(((s["lse"] - x).abs() <= (2 * D + 16) * 2.0 ** -24 * mag + 2.0 ** -20 + 2.0 ** -22 * x.abs()).all())
+
+
+def test_workspace_refusals():
+    s = make_prompt([5], [0], 2, 1, 64)
+    need = workspace(64).numel()
+    big = torch.zeros(need + 64, dtype=torch.uint8, device="cuda")
+    for ws, status in ((None, _abi.PKV_ERR_INVALID_ARG), (big[:need - 1], _abi.PKV_ERR_INVALID_ARG),
+                       (big[8:], _abi.PKV_ERR_UNSUPPORTED)):
+        with pytest.raises(pkv.PkvError) as e:
+            run_prompt(s, ws=ws)
+        assert e.value.status == status
+    assert bool((s["out"] == 7.0).all())
