@@ -32,14 +32,17 @@
  *   - Streams. Every call only enqueues GPU work on `stream` (NULL = the
  *     legacy default stream) and returns; results are ready when that
  *     stream's work completes. Calls contain no host synchronisation.
- *   - Ordering. The step's kernels (cache write, decode, merge, copy) are
- *     launched as programmatic dependents, so one may start its prologue
- *     while its predecessor on the stream finishes; each waits for that
- *     predecessor (griddepcontrol.wait) before it reads anything another
- *     grid may have written, and before it can finish. Only the decodes
- *     (block tables, seq_lens, a split plan) and the planned merge (the
- *     plan's split counts) read index inputs before that wait, and only the
- *     cache writes and the decodes let their successor start early. The
+ *   - Ordering. The step's kernels (cache write, decode, merge, copy) and a
+ *     prompt's (its attention, rows read back) are launched as programmatic
+ *     dependents, so one may start its prologue while its predecessor on the
+ *     stream finishes; each waits for that predecessor (griddepcontrol.wait)
+ *     before it reads anything another grid may have written, and before it
+ *     can finish. Only the decodes
+ *     (block tables, seq_lens, a split plan), the planned merge (the
+ *     plan's split counts) and the prompts' attention (q_start, k_start)
+ *     read index inputs before that wait, and only the cache writes, the
+ *     decodes, the reads of cached rows and the prompts' attention let
+ *     their successor start early. The
  *     calls that write index inputs (pkv_accept_drafts, pkv_resize_sequences,
  *     pkv_fork_sequences, and pkv_copy into them) do not: whatever follows
  *     them starts once they are done. Calls on one stream therefore see each
@@ -917,7 +920,8 @@ pkv_status pkv_gather_kv(const pkv_tensor* k_cache, const pkv_tensor* v_cache, c
  * A row that sees nothing gives 0 and -inf. Keys and values that a row does not
  * see have no effect on it, whatever they hold. Scores and sums are fp32; the
  * weights exp(score_j - m) are rounded to bf16 (half a step: 2^-8 of each) where
- * they meet v, and their sum is taken before that.
+ * they meet v, and their sum is taken before that. (Sums run over weights of up to
+ * 2^12: values of v past 2^100 may overflow.)
  *
  * q            [T, Hq, D] bf16 (already rotated); k, v [Tk, Hkv, D] bf16;
  *              innermost stride 1, rows 16-byte aligned. Strided views of a

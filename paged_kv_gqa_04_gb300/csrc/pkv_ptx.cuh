@@ -61,11 +61,6 @@ __device__ __forceinline__ uint64_t global_ns() {
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
 }
-__device__ __forceinline__ uint32_t global_ns_lo() {
-    uint32_t t;
-    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
-    return t;
-}
 // Wait for the phase with the given parity to complete, giving up after
 // about `limit_ns` nanoseconds. Returns false on timeout. Each retry
 // suspends the thread for at most 100 us, so the limit is checked at least
