@@ -913,8 +913,8 @@ cudaError_t launch_t(const PromptArgs& a, const CUtensorMap& tq, const CUtensorM
     if (e != cudaSuccess) return e;
     e = launch_dependent(prompt_kernel<D>, dim3(sms), dim3(C::THREADS), C::SMEM, s, tq, tk, tv, a);
     if (e != cudaSuccess) return e;
-    // No sequence has more keys than there are: nothing is cut.
-    if (a.Tk + kItemKeys <= kSnapKeys) return cudaSuccess;
+    // No item is longer than all keys, or all tokens where a sequence has more of them than keys: nothing is cut.
+    if (std::max(a.T, a.Tk) + kItemKeys <= kSnapKeys) return cudaSuccess;
     TreeArgs j{};
     j.T = a.T, j.Hq = a.Hq, j.G = a.G, j.tile_toks = a.tile_toks, j.D = D;
     j.out = a.out, j.o_s0 = a.o_s0, j.o_s1 = a.o_s1;

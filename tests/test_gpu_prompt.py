@@ -239,3 +239,13 @@ def test_workspace_refusals():
             run_prompt(s, ws=ws)
         assert e.value.status == status
     assert bool((s["out"] == 7.0).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_more_tokens_than_keys_in_a_long_sequence(D):
+    # flagged; the first 1600 rows see nothing, the others what they should, in items that are cut
+    s = make_prompt([2500], [0], 4, 2, D, seed=33)
+    s["k"], s["v"], s["L"] = s["k"][:900], s["v"][:900], [900]
+    s["k_start"] = torch.tensor([0, 900], dtype=torch.int32, device="cuda")
+    run_prompt(s)
+    check_prompt(s, flags=pkv.FLAG_ROW_RANGE)
