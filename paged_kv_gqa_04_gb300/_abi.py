@@ -218,10 +218,38 @@ def _desc(t, dtype: Optional[int] = None):
     return ctypes.pointer(d)
 
 
+def _descs(dev: int, *ts):
+    """_desc of every tensor, each checked to be on device `dev` as
+    _on_current_device does: one pass over a call's tensors, for calls short
+    enough for the host's share to count."""
+    out = []
+    for t in ts:
+        if type(t) is Bound and t.n == 1 and t.device == dev:
+            out.append(t.ptr)
+        elif t is None:
+            out.append(None)
+        else:
+            _on_current_device(t)
+            out.append(_desc(t))
+    return out
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:  # (torch.cuda.current_stream() makes a Stream object: 3 us a call)
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _stream_of(dev: int, stream) -> Optional[int]:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _flag(dev: int, t):
+    """The error flag's address, checked as _descs does."""
+    if type(t) is Bound and t.n == 1 and t.device == dev:
+        return t.data
+    _on_current_device(t)
+    return _ptr(t)
 
 
 def _ptr(t):
@@ -469,14 +497,15 @@ def qk_norm_rope_kv_write(q, k, v, q_weight, k_weight, eps: float, positions, co
     norm of every q and k head, weights q_weight and k_weight [D] float32 or
     bf16, before the rotation; k_out [T,Hkv,D] bf16 (or k itself, or None)
     receives the normed and rotated keys (pkv_qk_norm_rope_kv_write)."""
-    _on_current_device(q, k, v, q_weight, k_weight, positions, cos_sin, k_cache, v_cache, slot_mapping, k_scale, v_scale,
-                       k_block_scale, v_block_scale, k_out, err_flag)
-    fp4 = k_block_scale is not None
-    kc, vc = (_fp4(k_cache), _fp4(v_cache)) if fp4 else (_desc(k_cache), _desc(v_cache))
-    _check("pkv_qk_norm_rope_kv_write", lib().pkv_qk_norm_rope_kv_write(
-        _desc(q), _desc(k), _desc(v), _desc(q_weight), _desc(k_weight), eps, _desc(positions), _desc(cos_sin), kc, vc,
-        _desc(k_block_scale), _desc(v_block_scale), _desc(slot_mapping), _desc(k_scale), _desc(v_scale), _desc(k_out),
-        LAYOUTS[layout], STYLES[rope_style], _ptr(err_flag), _stream(stream)))
+    dev = torch.cuda.current_device()
+    q, k, v, q_weight, k_weight, positions, cos_sin, kc, vc, kbs, vbs, slot_mapping, k_scale, v_scale, k_out = _descs(
+        dev, q, k, v, q_weight, k_weight, positions, cos_sin, k_cache, v_cache, k_block_scale, v_block_scale, slot_mapping,
+        k_scale, v_scale, k_out)
+    if kbs is not None:
+        kc, vc = _fp4(k_cache), _fp4(v_cache)
+    _check("pkv_qk_norm_rope_kv_write", (_lib or lib()).pkv_qk_norm_rope_kv_write(
+        q, k, v, q_weight, k_weight, eps, positions, cos_sin, kc, vc, kbs, vbs, slot_mapping, k_scale, v_scale, k_out,
+        LAYOUTS[layout], STYLES[rope_style], _flag(dev, err_flag), _stream_of(dev, stream)))
 
 
 def gather_kv(k_cache, v_cache, block_tables, start, first, k_out, v_out, k_scale=None, v_scale=None, k_block_scale=None,
@@ -484,13 +513,14 @@ def gather_kv(k_cache, v_cache, block_tables, start, first, k_out, v_out, k_scal
     """Cached keys and values as packed bf16 rows (pkv_gather_kv): rows
     start[b] .. start[b+1] of k_out, v_out [T,Hkv,D] receive positions first[b]
     (None: 0) and on of sequence b."""
-    _on_current_device(k_cache, v_cache, block_tables, start, first, k_out, v_out, k_scale, v_scale, k_block_scale,
-                       v_block_scale, err_flag)
-    fp4 = k_block_scale is not None
-    kc, vc = (_fp4(k_cache), _fp4(v_cache)) if fp4 else (_desc(k_cache), _desc(v_cache))
-    _check("pkv_gather_kv", lib().pkv_gather_kv(
-        kc, vc, _desc(k_block_scale), _desc(v_block_scale), _desc(block_tables), _desc(start), _desc(first), _desc(k_out),
-        _desc(v_out), _desc(k_scale), _desc(v_scale), LAYOUTS[layout], _ptr(err_flag), _stream(stream)))
+    dev = torch.cuda.current_device()
+    kc, vc, kbs, vbs, block_tables, start, first, k_out, v_out, k_scale, v_scale = _descs(
+        dev, k_cache, v_cache, k_block_scale, v_block_scale, block_tables, start, first, k_out, v_out, k_scale, v_scale)
+    if kbs is not None:
+        kc, vc = _fp4(k_cache), _fp4(v_cache)
+    _check("pkv_gather_kv", (_lib or lib()).pkv_gather_kv(
+        kc, vc, kbs, vbs, block_tables, start, first, k_out, v_out, k_scale, v_scale, LAYOUTS[layout], _flag(dev, err_flag),
+        _stream_of(dev, stream)))
 
 
 def prompt_attention_workspace(D: int, sm_count: int) -> int:
@@ -505,11 +535,12 @@ def prompt_attention(q, k, v, q_start, k_start, softmax_scale: float, out, lse_o
     k_start[b+1] of k, v [Tk,Hkv,D] (None: q_start), whose last ones are
     theirs: out [T,Hq,D] bf16, lse_out [T,Hq] float32 or None. workspace: a
     contiguous device tensor of prompt_attention_workspace() bytes."""
-    _on_current_device(q, k, v, q_start, k_start, out, lse_out, workspace, err_flag)
+    dev = torch.cuda.current_device()
+    q, k, v, q_start, k_start, out, lse_out = _descs(dev, q, k, v, q_start, k_start, out, lse_out)
+    _on_current_device(workspace)
     ws, nbytes = _workspace(workspace)
-    _check("pkv_prompt_attention", lib().pkv_prompt_attention(
-        _desc(q), _desc(k), _desc(v), _desc(q_start), _desc(k_start), softmax_scale, _desc(out), _desc(lse_out), ws,
-        nbytes, _ptr(err_flag), _stream(stream)))
+    _check("pkv_prompt_attention", (_lib or lib()).pkv_prompt_attention(
+        q, k, v, q_start, k_start, softmax_scale, out, lse_out, ws, nbytes, _flag(dev, err_flag), _stream_of(dev, stream)))
 
 
 def validate_indices(block_tables, seq_lens, slot_mapping, num_pages: int, err_flag, slot_bitmap=None,
