@@ -92,9 +92,9 @@ struct Cfg {
     static constexpr int OFF_K = OFF_Q + 2 * TILE;
     static constexpr int OFF_V = OFF_K + SK * TILE;
     static constexpr int OFF_BAR = OFF_V + SV * TILE;
-    static constexpr int NBAR = 2 * SK + 2 * SV + kFix + 2 * 6 + 1 + 2 * kPieces;
+    static constexpr int NBAR = 2 * SK + 2 * SV + kFix + 2 * 6 + 1 + 2 * kPieces + 8;
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
-    static constexpr int OFF_PIECE = (OFF_MISC + 128 + 2048 + 15) / 16 * 16;  // [kPieces] Piece
+    static constexpr int OFF_PIECE = (OFF_MISC + 128 + 2048 + 128 + 15) / 16 * 16;  // [kPieces] Piece
     static constexpr int SMEM = OFF_PIECE + kPieces * 80;
     static_assert(SMEM <= 232448, "shared memory of one CTA");
     // tensor-memory columns of a softmax group: S (P over it), then O
@@ -238,8 +238,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     const uint32_t s0 = smem_u32(smem);
     enum : int { bKFull = 0, bKFree = C::SK, bVFull = 2 * C::SK, bVFree = bVFull + C::SV, bFix = bVFree + C::SV,
                  bS = bFix + kFix, bP = bS + 2, bO = bP + 2, bOFree = bO + 2, bQ = bOFree + 2, bQFree = bQ + 2,
-                 bPiece = bQFree + 2, bPieceFree = bPiece + kPieces, bEnd = bPieceFree + kPieces };
-    static_assert(bEnd + 1 == C::NBAR, "barriers");
+                 bPiece = bQFree + 2, bPieceFree = bPiece + kPieces, bEnd = bPieceFree + kPieces,
+                 bPair = bEnd + 1 };
+    static_assert(bPair + 8 == C::NBAR, "barriers");
     auto bar = [&](int i) -> uint32_t { return s0 + C::OFF_BAR + 8 * i; };
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
@@ -249,6 +250,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     int64_t* warp_units = reinterpret_cast<int64_t*>(misc + 32);        // [THREADS / 32]
     int* warp_longest = reinterpret_cast<int*>(misc + 72);              // [THREADS / 32]
     float* theirs = reinterpret_cast<float*>(misc + 32);                // (later) [2 groups][2 halves][128 rows]: what the halves tell each other
+    volatile int* handed_out = reinterpret_cast<volatile int*>(misc + 544);  // pieces, where a give-up ended them (else -1)
+    volatile uint32_t* pair_uses = misc + 545;                 // [2 groups][4 pairs][2 halves]
     static_assert(sizeof(Place) == 24, "as laid out");
     Piece* pieces = reinterpret_cast<Piece*>(smem + C::OFF_PIECE);
 
@@ -278,6 +281,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             mbar_init(bar(bPieceFree + i), 19);  // copies, MMA, V, softmax
         }
         mbar_init(bar(bEnd), 1);
+        for (int i = 0; i < 8; ++i) mbar_init(bar(bPair + i), 2);
+        for (int i = 0; i < 16; ++i) pair_uses[i] = 0u;
+        *handed_out = -1;
         *abort_flag = 0;
         place[0] = place[1] = Place{a.B, 0, 0, 0, 0};
         fence_mbar_init();
@@ -369,14 +375,15 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 break;
             }
     };
-    auto warp_wait = [&](uint32_t bb, uint32_t par) {
+    auto warp_wait = [&](uint32_t bb, uint32_t par) -> bool {
         uint32_t n = 0;
 #pragma unroll 1
         while (!__any_sync(0xffffffffu, mbar_try_wait(bb, par)))
             if (++n % 256 == 0 && __any_sync(0xffffffffu, n == kTries || *abort_flag)) {
                 *abort_flag = 1;
-                break;
+                return false;
             }
+        return true;
     };
     auto piece_bar = [&](int i) { return bar(bPiece + i % kPieces); };
     auto piece_par = [](int i) -> uint32_t { return (i / kPieces) & 1; };
@@ -438,7 +445,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                     w.end[1] = w.ctx + w.tok0 + w.toks;
                 }
                 if (i >= kPieces) lane_wait(bar(bPieceFree + i % kPieces), (i / kPieces - 1) & 1);
-                if (*abort_flag) w.b = -1;
+                if (*abort_flag) {  // (what is in the ring stays as it is)
+                    *handed_out = i;
+                    break;
+                }
                 pieces[i % kPieces] = w;
                 mbar_arrive(piece_bar(i));
                 if (w.b < 0) break;
@@ -669,9 +679,16 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         const float2 sl2 = make_float2(sl, sl);
         int n = 0, job = 0, n_o = 0, n_fix = 0;        // the CTA's tiles, this group's jobs and items, fixed tiles
         for (int i = 0;; ++i) {
-            warp_wait(piece_bar(i), piece_par(i));
+            // A group's warps meet at barriers, which know no limit: they take up the same pieces, and a wait that was
+            // given up on changes nothing of what they do with one. A warp that gives up waiting for a piece learns
+            // from warp 3, whose waits end too, whether there is one.
+            bool more = true;
+            if (!warp_wait(piece_bar(i), piece_par(i))) {
+                for (uint32_t k = 0; k < 4 * kTries && *handed_out < 0 && !mbar_try_wait(piece_bar(i), piece_par(i)); ++k) {}
+                more = mbar_try_wait(piece_bar(i), piece_par(i));
+            }
             const Piece& w = pieces[i % kPieces];
-            if (__any_sync(0xffffffffu, w.b < 0 || *abort_flag)) break;
+            if (__any_sync(0xffffffffu, !more || w.b < 0)) break;
             const int t0 = w.t0, t1 = w.t1, tf = w.tf;
             if (grp > w.two) {
                 n += t1 - t0;
@@ -804,7 +821,15 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                             if (speaker) go_on[grp] = 1u;
                         }
                         tc_fence_before();
-                        (void)named_bar_and(pair, 64, true);
+                        {   // (a barrier with a limit: where the wait above was given up on, the other half may not be here)
+                            const uint32_t uses = pair_uses[8 * grp + 2 * wq + half];
+                            __syncwarp();
+                            if (lane == 0) {
+                                pair_uses[8 * grp + 2 * wq + half] = uses + 1;
+                                mbar_arrive(bar(bPair + 4 * grp + wq));
+                            }
+                            warp_wait(bar(bPair + 4 * grp + wq), uses & 1);
+                        }
                         tc_fence_after();
                         const int sees = live ? vis + 64 * half : 0;
 #pragma unroll 1
