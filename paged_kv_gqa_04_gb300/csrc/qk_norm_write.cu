@@ -19,6 +19,8 @@
 // are what is in flight); the quantisers' instructions for FP8 and NVFP4 caches
 // (22,197 tokens of 12 + 2 x 2 heads, FP8: 187 MB in 37 us, 75%); latency for a step's
 // tokens (61 of 32 + 2 x 8 heads: 2.3 us within a graph, 7.5 us by itself).
+#include <type_traits>
+
 #include "pkv_internal.h"
 #include "pkv_ptx.cuh"
 #include "rope_row.cuh"
@@ -43,6 +45,56 @@ __device__ __forceinline__ void load_weights(const void* w, int is_bf16, int c, 
             hi.v[4 * k] = y.x, hi.v[4 * k + 1] = y.y, hi.v[4 * k + 2] = y.z, hi.v[4 * k + 3] = y.w;
         }
     }
+}
+
+// Sum of a key's squares, the same in all of its row's lanes: columns 32 apart first, in order, then neighbours in pairs,
+// pairs of pairs and so on: the order of a plain float32 mean over a row of a tensor on this GPU. So a cache holds what
+// plain operations would have put there, bit for bit: one unit in the last place of a norm can move an NVFP4 value by
+// a third of its block's largest. (The D = 128 lanes that share columns 32 apart, c and c ^ 4, take four of the eight sums each.)
+template <int D>
+__device__ __forceinline__ float sum_of_squares(const Chunk8& lo, const Chunk8& hi, int c, unsigned row_lanes) {
+    float a[8], b[8];
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        mul_rn_x2(lo.v[e], lo.v[e + 1], lo.v[e], lo.v[e + 1], a[e], a[e + 1]);
+        mul_rn_x2(hi.v[e], hi.v[e + 1], hi.v[e], hi.v[e + 1], b[e], b[e + 1]);
+    }
+    float ss;
+    if constexpr (D == 128) {
+        const bool up = (c & 4) != 0;
+        float t[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float ga = __shfl_xor_sync(row_lanes, up ? a[e] : a[4 + e], 4);
+            const float gb = __shfl_xor_sync(row_lanes, up ? b[e] : b[4 + e], 4);
+            const float oa = up ? a[4 + e] : a[e], ob = up ? b[4 + e] : b[e];
+            t[e] = ((oa + ga) + (up ? gb : ob)) + (up ? ob : gb);
+        }
+        ss = (t[0] + t[1]) + (t[2] + t[3]);
+        ss += __shfl_xor_sync(row_lanes, ss, 4);
+    } else {
+        ss = (((a[0] + b[0]) + (a[1] + b[1])) + ((a[2] + b[2]) + (a[3] + b[3]))) +
+             (((a[4] + b[4]) + (a[5] + b[5])) + ((a[6] + b[6]) + (a[7] + b[7])));
+    }
+    ss += __shfl_xor_sync(row_lanes, ss, 1);
+    ss += __shfl_xor_sync(row_lanes, ss, 2);
+    return ss;
+}
+
+// The same of a query's, in the fewest instructions (the order above costs 8 more shuffles: 13% of the FP8 fill, if q
+// took it too).
+template <int D>
+__device__ __forceinline__ float quick_sum_of_squares(const Chunk8& lo, const Chunk8& hi, unsigned row_lanes) {
+    float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        s2[0] = fma2(make_float2(lo.v[e], lo.v[e + 1]), make_float2(lo.v[e], lo.v[e + 1]), s2[0]);
+        s2[1] = fma2(make_float2(hi.v[e], hi.v[e + 1]), make_float2(hi.v[e], hi.v[e + 1]), s2[1]);
+    }
+    float ss = (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
+#pragma unroll
+    for (int d = 1; d < D / 16; d <<= 1) ss += __shfl_xor_sync(row_lanes, ss, d);
+    return ss;
 }
 
 // Small CTAs: one that waits for its loads holds up fewer of the others (32 prompts of 300 to 2000 tokens, bf16,
@@ -110,72 +162,71 @@ __global__ void __launch_bounds__(kThreads, kCtas) qk_norm_write_kernel(const No
     const int64_t cache_head = a.layout == PKV_HND ? st[1] : st[2];
     // (the lanes of this row and of the rows beside it in a half, quarter or eighth of the warp are all here)
     const unsigned row_lanes = ((1u << TPR) - 1u) << (lane_id() & ~(TPR - 1u));
+    // A CTA's kind as a constant: its loop over the heads has no branches on it (and keys' sums cost the queries nothing).
+    auto heads_of = [&](auto kind) {
+        constexpr bool kQ = decltype(kind)::value == 0, kK = decltype(kind)::value == 1;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int h = h0 + u;
-        if (h >= heads) break;
-        Chunk8 lo = unpack_bf16x8(wlo[u]), hi = unpack_bf16x8(whi[u]);
-        if (is_q || is_k) {
-            float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        for (int u = 0; u < U; ++u) {
+            const int h = h0 + u;
+            if (h >= heads) break;
+            Chunk8 lo = unpack_bf16x8(wlo[u]), hi = unpack_bf16x8(whi[u]);
+            if constexpr (kQ || kK) {
+                const float ss = kK ? sum_of_squares<D>(lo, hi, c, row_lanes) : quick_sum_of_squares<D>(lo, hi, row_lanes);
+                const float r = rsqrtf(__fadd_rn(ss * (1.f / D), n.eps));
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                s2[0] = fma2(make_float2(lo.v[e], lo.v[e + 1]), make_float2(lo.v[e], lo.v[e + 1]), s2[0]);
-                s2[1] = fma2(make_float2(hi.v[e], hi.v[e + 1]), make_float2(hi.v[e], hi.v[e + 1]), s2[1]);
+                for (int e = 0; e < 8; e += 2) {
+                    mul_rn_x2(lo.v[e], lo.v[e + 1], r, r, lo.v[e], lo.v[e + 1]);
+                    mul_rn_x2(hi.v[e], hi.v[e + 1], r, r, hi.v[e], hi.v[e + 1]);
+                    mul_rn_x2(lo.v[e], lo.v[e + 1], glo.v[e], glo.v[e + 1], lo.v[e], lo.v[e + 1]);
+                    mul_rn_x2(hi.v[e], hi.v[e + 1], ghi.v[e], ghi.v[e + 1], hi.v[e], hi.v[e + 1]);
+                }
+                rotate_row<INTER>(lo, hi, cv, sv);
             }
-            float ss = (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
-#pragma unroll
-            for (int d = 1; d < TPR; d <<= 1) ss += __shfl_xor_sync(row_lanes, ss, d);
-            const float r = __frcp_rn(__fsqrt_rn(fmaf(ss, 1.f / D, n.eps)));
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                mul_rn_x2(lo.v[e], lo.v[e + 1], r, r, lo.v[e], lo.v[e + 1]);
-                mul_rn_x2(hi.v[e], hi.v[e + 1], r, r, hi.v[e], hi.v[e + 1]);
-                mul_rn_x2(lo.v[e], lo.v[e + 1], glo.v[e], glo.v[e + 1], lo.v[e], lo.v[e + 1]);
-                mul_rn_x2(hi.v[e], hi.v[e + 1], ghi.v[e], ghi.v[e + 1], hi.v[e], hi.v[e + 1]);
+            if (kQ || (kK && n.k_out != nullptr)) {
+                uint16_t* p = kQ ? a.q + t * a.q_s0 + h * a.q_s1 : n.k_out + t * n.ko_s0 + h * n.ko_s1;
+                *reinterpret_cast<uint4*>(p + 8 * c) = pack_bf16x8(lo);
+                *reinterpret_cast<uint4*>(p + D / 2 + 8 * c) = pack_bf16x8(hi);
             }
-            rotate_row<INTER>(lo, hi, cv, sv);
-        }
-        if (is_q || (is_k && n.k_out != nullptr)) {
-            uint16_t* p = is_q ? a.q + t * a.q_s0 + h * a.q_s1 : n.k_out + t * n.ko_s0 + h * n.ko_s1;
-            *reinterpret_cast<uint4*>(p + 8 * c) = pack_bf16x8(lo);
-            *reinterpret_cast<uint4*>(p + D / 2 + 8 * c) = pack_bf16x8(hi);
-        }
-        if (is_q) continue;
-        const int64_t e = cache_row + h * cache_head;
-        if constexpr (KIND == kBf16) {
-            uint16_t* dst = static_cast<uint16_t*>(is_k ? a.k_cache : a.v_cache) + e;
-            *reinterpret_cast<uint4*>(dst + 8 * c) = is_k ? pack_bf16x8(lo) : wlo[u];
-            *reinterpret_cast<uint4*>(dst + D / 2 + 8 * c) = is_k ? pack_bf16x8(hi) : whi[u];
-        } else {
-            const float scale = __ldg((is_k ? a.k_scale : a.v_scale) + (a.n_scale == 1 ? 0 : h));
-            uint8_t* dst = static_cast<uint8_t*>(is_k ? a.k_cache : a.v_cache) + e;
-            if constexpr (KIND == kFp8) {
-                const E4m3Rcp r8 = e4m3_rcp(scale);
-                *reinterpret_cast<uint2*>(dst + 8 * c) = pack_e4m3x8(lo, scale, r8);
-                *reinterpret_cast<uint2*>(dst + D / 2 + 8 * c) = pack_e4m3x8(hi, scale, r8);
+            if (kQ) continue;
+            const int64_t e = cache_row + h * cache_head;
+            if constexpr (KIND == kBf16) {
+                uint16_t* dst = static_cast<uint16_t*>(kK ? a.k_cache : a.v_cache) + e;
+                *reinterpret_cast<uint4*>(dst + 8 * c) = kK ? pack_bf16x8(lo) : wlo[u];
+                *reinterpret_cast<uint4*>(dst + D / 2 + 8 * c) = kK ? pack_bf16x8(hi) : whi[u];
             } else {
-                // both lanes of a pair (chunks c, c^1 of this row) hold a block's halves
-                const float six_g = __fmul_rn(6.f, scale);
-                const E4m3Rcp r6 = bracket_rcp(six_g);
-                const unsigned pair = 3u << (lane_id() & 30u);
-                float am_lo = amax8(lo), am_hi = amax8(hi);
-                am_lo = fmaxf(am_lo, __shfl_xor_sync(pair, am_lo, 1));
-                am_hi = fmaxf(am_hi, __shfl_xor_sync(pair, am_hi, 1));
-                uint32_t s_lo, s_hi;
-                const uint32_t w_lo = nvfp4_half(lo, am_lo, scale, six_g, r6, s_lo);
-                const uint32_t w_hi = nvfp4_half(hi, am_hi, scale, six_g, r6, s_hi);
-                *reinterpret_cast<uint32_t*>(dst + 4 * c) = w_lo;
-                *reinterpret_cast<uint32_t*>(dst + D / 4 + 4 * c) = w_hi;
-                const int64_t* bs = is_k ? a.kbs_s : a.vbs_s;
-                uint8_t* bdst = (is_k ? a.k_bs : a.v_bs) + page * bs[0] +
-                                (a.layout == PKV_HND ? h * bs[1] + off * bs[2] : off * bs[1] + h * bs[2]);
-                if (c & 1)
-                    bdst[D / 32 + c / 2] = static_cast<uint8_t>(s_hi);
-                else
-                    bdst[c / 2] = static_cast<uint8_t>(s_lo);
+                const float scale = __ldg((kK ? a.k_scale : a.v_scale) + (a.n_scale == 1 ? 0 : h));
+                uint8_t* dst = static_cast<uint8_t*>(kK ? a.k_cache : a.v_cache) + e;
+                if constexpr (KIND == kFp8) {
+                    const E4m3Rcp r8 = e4m3_rcp(scale);
+                    *reinterpret_cast<uint2*>(dst + 8 * c) = pack_e4m3x8(lo, scale, r8);
+                    *reinterpret_cast<uint2*>(dst + D / 2 + 8 * c) = pack_e4m3x8(hi, scale, r8);
+                } else {
+                    // both lanes of a pair (chunks c, c^1 of this row) hold a block's halves
+                    const float six_g = __fmul_rn(6.f, scale);
+                    const E4m3Rcp r6 = bracket_rcp(six_g);
+                    const unsigned pair = 3u << (lane_id() & 30u);
+                    float am_lo = amax8(lo), am_hi = amax8(hi);
+                    am_lo = fmaxf(am_lo, __shfl_xor_sync(pair, am_lo, 1));
+                    am_hi = fmaxf(am_hi, __shfl_xor_sync(pair, am_hi, 1));
+                    uint32_t s_lo, s_hi;
+                    const uint32_t w_lo = nvfp4_half(lo, am_lo, scale, six_g, r6, s_lo);
+                    const uint32_t w_hi = nvfp4_half(hi, am_hi, scale, six_g, r6, s_hi);
+                    *reinterpret_cast<uint32_t*>(dst + 4 * c) = w_lo;
+                    *reinterpret_cast<uint32_t*>(dst + D / 4 + 4 * c) = w_hi;
+                    const int64_t* bs = kK ? a.kbs_s : a.vbs_s;
+                    uint8_t* bdst = (kK ? a.k_bs : a.v_bs) + page * bs[0] +
+                                    (a.layout == PKV_HND ? h * bs[1] + off * bs[2] : off * bs[1] + h * bs[2]);
+                    if (c & 1)
+                        bdst[D / 32 + c / 2] = static_cast<uint8_t>(s_hi);
+                    else
+                        bdst[c / 2] = static_cast<uint8_t>(s_lo);
+                }
             }
         }
-    }
+    };
+    if (is_q) heads_of(std::integral_constant<int, 0>{});
+    else if (is_k) heads_of(std::integral_constant<int, 1>{});
+    else heads_of(std::integral_constant<int, 2>{});
 }
 
 template <int D, bool INTER, int KIND, int U>
