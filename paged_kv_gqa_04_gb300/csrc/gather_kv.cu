@@ -17,6 +17,7 @@
 // rest). 16 values a thread take more registers, so fewer loads in flight (FP8 138 us
 // and not 123, NVFP4 41 and not 32).
 #include <algorithm>
+#include <type_traits>
 
 #include "pkv_internal.h"
 #include "pkv_ptx.cuh"
@@ -78,6 +79,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherArgs a) {
     grid_dep_launch();
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.rows;
     const int n = static_cast<int>(min(static_cast<int64_t>(a.rows), a.T - t0));
+    bool zeros = false;  // a row here that no page holds
     if (tid < n) {
         const int t = static_cast<int>(t0) + tid;
         // the last sequence that starts at or before row t
@@ -106,6 +108,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherArgs a) {
             }
         }
         if (flags) flag_error(a.err, flags);
+        zeros = page == kZeros;
         page_of[tid] = page;
         off_of[tid] = off;
     }
@@ -118,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherArgs a) {
         }
         if (bad) flag_error(a.err, PKV_FLAG_ROW_RANGE);
     }
-    __syncthreads();
+    zeros = __syncthreads_or(zeros);
 
     const int items = a.Hkv * CPR, X = blockDim.x, Y = blockDim.y;
     for (int it = threadIdx.x; it < items; it += X) {
@@ -128,38 +131,44 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherArgs a) {
             gk = __ldg(a.k_scale + (a.n_scale == 1 ? 0 : h));
             gv = __ldg(a.v_scale + (a.n_scale == 1 ? 0 : h));
         }
-        for (int r0 = threadIdx.y; r0 < n; r0 += kUnroll * Y) {
-            Raw<KIND> k[kUnroll] = {}, v[kUnroll] = {};
-            int page[kUnroll];
+        // (whether there are such rows as a constant: a choice of the factor for each took NVFP4 34 us and not 31)
+        auto copy_rows = [&](auto with_zeros) {
+            for (int r0 = threadIdx.y; r0 < n; r0 += kUnroll * Y) {
+                Raw<KIND> k[kUnroll] = {}, v[kUnroll] = {};
+                int page[kUnroll];
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int r = r0 + u * Y;
-                page[u] = r < n ? page_of[r] : kNobody;
-                if (page[u] < 0) continue;
-                const int64_t p = page[u];
-                const int off = off_of[r];
-                const int64_t ek = p * a.kc_s0 + off * a.kc_st + h * a.kc_sh, ev = p * a.vc_s0 + off * a.vc_st + h * a.vc_sh;
-                if constexpr (KIND == kBf16) {
-                    k[u].w = ldg_nc128(static_cast<const uint16_t*>(a.k_cache) + ek + 8 * c);
-                    v[u].w = ldg_nc128(static_cast<const uint16_t*>(a.v_cache) + ev + 8 * c);
-                } else if constexpr (KIND == kFp8) {
-                    k[u].w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.k_cache) + ek + 8 * c));
-                    v[u].w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.v_cache) + ev + 8 * c));
-                } else {
-                    k[u].w = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.k_cache) + ek + 4 * c));
-                    v[u].w = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v_cache) + ev + 4 * c));
-                    k[u].s = __ldg(a.k_bs + p * a.kbs_s0 + off * a.kbs_st + h * a.kbs_sh + (c >> 1));
-                    v[u].s = __ldg(a.v_bs + p * a.vbs_s0 + off * a.vbs_st + h * a.vbs_sh + (c >> 1));
+                for (int u = 0; u < kUnroll; ++u) {
+                    const int r = r0 + u * Y;
+                    page[u] = r < n ? page_of[r] : kNobody;
+                    if (page[u] < 0) continue;
+                    const int64_t p = page[u];
+                    const int off = off_of[r];
+                    const int64_t ek = p * a.kc_s0 + off * a.kc_st + h * a.kc_sh, ev = p * a.vc_s0 + off * a.vc_st + h * a.vc_sh;
+                    if constexpr (KIND == kBf16) {
+                        k[u].w = ldg_nc128(static_cast<const uint16_t*>(a.k_cache) + ek + 8 * c);
+                        v[u].w = ldg_nc128(static_cast<const uint16_t*>(a.v_cache) + ev + 8 * c);
+                    } else if constexpr (KIND == kFp8) {
+                        k[u].w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.k_cache) + ek + 8 * c));
+                        v[u].w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.v_cache) + ev + 8 * c));
+                    } else {
+                        k[u].w = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.k_cache) + ek + 4 * c));
+                        v[u].w = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v_cache) + ev + 4 * c));
+                        k[u].s = __ldg(a.k_bs + p * a.kbs_s0 + off * a.kbs_st + h * a.kbs_sh + (c >> 1));
+                        v[u].s = __ldg(a.v_bs + p * a.vbs_s0 + off * a.vbs_st + h * a.vbs_sh + (c >> 1));
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) {
+                    if (page[u] == kNobody) continue;
+                    const int64_t t = t0 + r0 + u * Y;
+                    const bool none = decltype(with_zeros)::value && page[u] == kZeros;
+                    *reinterpret_cast<uint4*>(a.k_out + t * a.ko_s0 + h * a.ko_s1 + 8 * c) = values<KIND>(k[u], none ? 0.f : gk);
+                    *reinterpret_cast<uint4*>(a.v_out + t * a.vo_s0 + h * a.vo_s1 + 8 * c) = values<KIND>(v[u], none ? 0.f : gv);
                 }
             }
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                if (page[u] == kNobody) continue;
-                const int64_t t = t0 + r0 + u * Y;
-                *reinterpret_cast<uint4*>(a.k_out + t * a.ko_s0 + h * a.ko_s1 + 8 * c) = values<KIND>(k[u], page[u] == kZeros ? 0.f : gk);
-                *reinterpret_cast<uint4*>(a.v_out + t * a.vo_s0 + h * a.vo_s1 + 8 * c) = values<KIND>(v[u], page[u] == kZeros ? 0.f : gv);
-            }
-        }
+        };
+        if (zeros) copy_rows(std::true_type{});
+        else copy_rows(std::false_type{});
     }
 }
 
