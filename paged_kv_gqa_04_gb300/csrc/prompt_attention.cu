@@ -54,7 +54,7 @@
 // 1271 us, 1.51 PFLOP/s, 79% of the rate of a large library product; a group's softmax
 // of a tile (1400 cycles) and the hand-overs are a little longer than the other
 // group's MMAs. Short prompts: an item's start, the tile on the diagonal and the
-// output (32 prompts of 1 to 2048 tokens, 32 heads: 190 us, 0.79 PFLOP/s of visible
+// output (32 prompts of 1 to 2048 tokens, 32 heads: 193 us, 0.78 PFLOP/s of visible
 // pairs).
 //
 // Waits are bounded (about one second): a role that gives up sets

@@ -9,16 +9,15 @@
 // order of tokens and groups of heads; a row's threads are consecutive lanes of
 // one warp, and the sum of its squares is a butterfly over them.
 //
-// Arithmetic: r = 1 / sqrt(mean(x^2) + eps), the mean in float32 (its sum in a
-// fixed order), the root and the quotient correctly rounded; y = (x r) w, each
-// product rounded; then the rotation and the cache formats of rope_kv_write.cu, bit
-// for bit.
+// Arithmetic: r = rsqrtf(mean(x^2) + eps), the mean in float32 (its sum in a fixed
+// order); y = (x r) w, each product rounded; then the rotation and the cache
+// formats of rope_kv_write.cu, bit for bit.
 //
 // Bound: HBM for fills (39,750 tokens of 32 + 2 x 8 heads, D = 128, bf16, keys kept:
-// 1,060 MB in 171 us, 6.2 TB/s, 91% of a copy's rate; a thread's four heads of loads
+// 1,060 MB in 162 us, 6.5 TB/s, 96% of a copy's rate; a thread's four heads of loads
 // are what is in flight); the quantisers' instructions for FP8 and NVFP4 caches
-// (22,197 tokens of 12 + 2 x 2 heads, FP8: 187 MB in 37 us, 75%); latency for a step's
-// tokens (61 of 32 + 2 x 8 heads: 2.3 us within a graph, 7.5 us by itself).
+// (22,197 tokens of 12 + 2 x 2 heads, FP8: 187 MB in 34.8 us, 79%); latency for a step's
+// tokens (61 of 32 + 2 x 8 heads: 2.3 us within a graph, 7.1 us by itself).
 #include <type_traits>
 
 #include "pkv_internal.h"
@@ -81,8 +80,7 @@ __device__ __forceinline__ float sum_of_squares(const Chunk8& lo, const Chunk8& 
     return ss;
 }
 
-// The same of a query's, in the fewest instructions (the order above costs 8 more shuffles: 13% of the FP8 fill, if q
-// took it too).
+// The same of a query's, in the fewest instructions (the order above takes 8 more shuffles).
 template <int D>
 __device__ __forceinline__ float quick_sum_of_squares(const Chunk8& lo, const Chunk8& hi, unsigned row_lanes) {
     float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -162,7 +160,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) qk_norm_write_kernel(const No
     const int64_t cache_head = a.layout == PKV_HND ? st[1] : st[2];
     // (the lanes of this row and of the rows beside it in a half, quarter or eighth of the warp are all here)
     const unsigned row_lanes = ((1u << TPR) - 1u) << (lane_id() & ~(TPR - 1u));
-    // A CTA's kind as a constant: its loop over the heads has no branches on it (and keys' sums cost the queries nothing).
+    // A CTA's kind as a constant: its loop over the heads has no branches on it, and keys' sums cost the queries nothing
+    // (one loop for all: 171 us and not 162 for the fill above; with the keys' sums in it FP8 40.6 and not 34.8).
     auto heads_of = [&](auto kind) {
         constexpr bool kQ = decltype(kind)::value == 0, kK = decltype(kind)::value == 1;
 #pragma unroll

@@ -183,8 +183,8 @@ def normed(s, x, w):
     """(rotated rows, bound of their float32 errors) in float64.
 
     The sum of squares is off by at most D / 2 + 8 additions' and products' 2^-24 of itself, which halves under the
-    root; the root, the quotient and two products add one each. A rotated value is a difference of two products of
-    such values, each rounded once more, and the sum."""
+    root; the reciprocal root adds four (two units in the last place), two products one each. A rotated value is a
+    difference of two products of such values, each rounded once more, and the sum."""
     x, w, D = x.double(), w.double(), s["D"]
     y = x / (x.pow(2).mean(-1, keepdim=True) + s["eps"]).sqrt() * w
     cs = s["cos_sin"].double()[s["positions"].long().clamp(0, s["cos_sin"].shape[0] - 1)][:, None]
