@@ -76,8 +76,9 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b_lo, u
 __device__ __forceinline__ void umma_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-// One lane of the warp; MMAs in the branch of that lane alone take their operands from uniform registers (5
-// instructions each; 11 in a branch of lane 0).
+// One lane of the warp. Measured, MMAs issued in the branch of the elected lane and in one of lane 0: prompts of 8,192
+// tokens, 28 heads of 128, 331 and 382 us; 32 prompts of 1,000 tokens, 32 heads, 299 and 346; D = 64, 8,192 tokens, 32
+// heads, 324 and 358.
 __device__ __forceinline__ bool elect_one() {
     uint32_t e;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
