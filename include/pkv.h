@@ -613,10 +613,11 @@ pkv_status pkv_stream_read(const void* buf, int64_t bytes, uint32_t* sink, int32
  * pkv_selftest_bounded_wait -- self-test of the bounded in-kernel waits
  * behind PKV_FLAG_WAIT_TIMEOUT (a diagnostic; not one of the decode step's
  * calls). One CTA waits on mbarriers that nothing completes: one warp gives
- * up after about limit_ns and ORs PKV_FLAG_WAIT_TIMEOUT into *err_flag; a
- * second warp, with a limit 100 times longer, stops on the first one's
- * abort signal. elapsed_ns[0] and [1] receive the two waiting times. The
- * GPU context stays usable afterwards.
+ * up after about limit_ns and ORs PKV_FLAG_WAIT_TIMEOUT into *err_flag; the
+ * others, with a limit 100 times longer or none of their own, stop on the
+ * first one's abort signal. elapsed_ns[0] receives the first one's waiting
+ * time, elapsed_ns[1] the longest of the others'. The GPU context stays
+ * usable afterwards.
  * limit_ns: 100,000 .. 10,000,000 (0.1 .. 10 ms); err_flag: device int32
  * (the caller zeroes it); elapsed_ns: device memory of two uint64 words.
  */

@@ -88,6 +88,25 @@ __device__ __forceinline__ bool mbar_wait_or_abort(uint32_t bar, uint32_t parity
     }
 }
 
+// Waits that keep no time of their own: until the phase is complete or
+// *abort_flag is set (false then). They end because some other thread of the CTA
+// waits with mbar_wait_or_abort for what cannot come where these do not get on,
+// and sets the flag when its limit is over. (A try suspends the thread for a
+// limited time, about 1 us.) The second form is a whole warp's, with one answer
+// for all of its lanes.
+__device__ __forceinline__ bool mbar_wait_watched(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity))
+        if (*abort_flag) return false;
+    return true;
+}
+__device__ __forceinline__ bool mbar_warp_wait_watched(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+#pragma unroll 1
+    while (!__any_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+        if (__any_sync(0xffffffffu, *abort_flag)) return false;
+    return true;
+}
+
 // Programmatic dependent launch: wait until the preceding grid in the
 // stream has completed and its writes are visible (a no-op when the kernel
 // was not launched as a programmatic dependent), and let the following grid

@@ -57,8 +57,13 @@
 // output (32 prompts of 1 to 2048 tokens, 32 heads: 193 us, 0.78 PFLOP/s of visible
 // pairs).
 //
-// Waits are bounded (about one second): a role that gives up sets
-// PKV_FLAG_WAIT_TIMEOUT and a CTA-wide flag that ends the others' waits.
+// Waits. The thread that copies K and V is the one that keeps time: what it waits
+// for comes within a tile's turn of the others, whatever the length of an item, and
+// with its last copy done it waits for the other roles' end. After a second
+// without that it sets a CTA-wide flag, which ends the others' waits and the call
+// with PKV_FLAG_WAIT_TIMEOUT. The others keep no time, as some of their waits last as
+// long as an item. From the flag on, copies, MMAs and V's warp leave their
+// tiles; the softmax warps go through the pieces in the ring, no longer waiting.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -75,8 +80,7 @@ constexpr int kItemKeys = 512;  // what an item costs beyond its tiles, in keys
 constexpr int kSnapKeys = 1536; // longest item (keys and kItemKeys) up to which items are not cut
 constexpr int kPieces = 4;      // ring of pieces
 constexpr float kRaise = 4096.f; // sum of 64 weights past which their row's reference moves
-constexpr uint32_t kWaitLimitNs = 1000000000u;
-constexpr uint32_t kTries = 1u << 20;  // of about 1 us
+constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr int kFix = 4;         // ring of the fixed tiles' notes: no fewer than there are stages of V
 
 template <int D>
@@ -92,7 +96,7 @@ struct Cfg {
     static constexpr int OFF_K = OFF_Q + 2 * TILE;
     static constexpr int OFF_V = OFF_K + SK * TILE;
     static constexpr int OFF_BAR = OFF_V + SV * TILE;
-    static constexpr int NBAR = 2 * SK + 2 * SV + kFix + 2 * 6 + 1 + 2 * kPieces + 8;
+    static constexpr int NBAR = 2 * SK + 2 * SV + kFix + 2 * 6 + 1 + 2 * kPieces + 8 + 1;
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
     static constexpr int OFF_PIECE = (OFF_MISC + 128 + 2048 + 128 + 15) / 16 * 16;  // [kPieces] Piece
     static constexpr int SMEM = OFF_PIECE + kPieces * 80;
@@ -239,8 +243,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     enum : int { bKFull = 0, bKFree = C::SK, bVFull = 2 * C::SK, bVFree = bVFull + C::SV, bFix = bVFree + C::SV,
                  bS = bFix + kFix, bP = bS + 2, bO = bP + 2, bOFree = bO + 2, bQ = bOFree + 2, bQFree = bQ + 2,
                  bPiece = bQFree + 2, bPieceFree = bPiece + kPieces, bEnd = bPieceFree + kPieces,
-                 bPair = bEnd + 1 };
-    static_assert(bPair + 8 == C::NBAR, "barriers");
+                 bPair = bEnd + 1, bDone = bPair + 8 };
+    static_assert(bDone + 1 == C::NBAR, "barriers");
     auto bar = [&](int i) -> uint32_t { return s0 + C::OFF_BAR + 8 * i; };
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
@@ -282,6 +286,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         }
         mbar_init(bar(bEnd), 1);
         for (int i = 0; i < 8; ++i) mbar_init(bar(bPair + i), 2);
+        mbar_init(bar(bDone), C::THREADS / 32 - 1);  // all warps but the copies'
         for (int i = 0; i < 16; ++i) pair_uses[i] = 0u;
         *handed_out = -1;
         *abort_flag = 0;
@@ -359,32 +364,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 
     // q, k and v may still be being written by the preceding grid: every role waits for it.
     //
-    // A wait that gives up raises the CTA's flag and returns like any other: what
-    // follows works on what is there, in bounds, until the role sees the flag at its
-    // next piece. (Results to look at are branches, which cost more here than the
-    // waits: a wait for a barrier that is complete takes 45 cycles, with its result
-    // voted on and branched upon 180.)
-    // (try_wait holds the warp until the phase is over, for 1 us at most; polling with test_wait takes the issue
-    // slots of the others: 347 us and not 333.)
-    auto lane_wait = [&](uint32_t bb, uint32_t par) {
-        uint32_t n = 0;
-#pragma unroll 1
-        while (!mbar_try_wait(bb, par))
-            if (++n % 256 == 0 && (n == kTries || *abort_flag)) {
-                *abort_flag = 1;
-                break;
-            }
-    };
-    auto warp_wait = [&](uint32_t bb, uint32_t par) -> bool {
-        uint32_t n = 0;
-#pragma unroll 1
-        while (!__any_sync(0xffffffffu, mbar_try_wait(bb, par)))
-            if (++n % 256 == 0 && __any_sync(0xffffffffu, n == kTries || *abort_flag)) {
-                *abort_flag = 1;
-                return false;
-            }
-        return true;
-    };
+    // Waits that the copying thread watches over. One that is given up on returns like any other: what follows works
+    // on what is there, in bounds, until the role leaves. (try_wait holds the warp until the phase is over, for about
+    // 1 us; polling with test_wait takes the issue slots of the others: 347 us and not 333.)
+    auto lane_wait = [&](uint32_t bb, uint32_t par) -> bool { return mbar_wait_watched(bb, par, abort_flag); };
+    auto warp_wait = [&](uint32_t bb, uint32_t par) -> bool { return mbar_warp_wait_watched(bb, par, abort_flag); };
     auto piece_bar = [&](int i) { return bar(bPiece + i % kPieces); };
     auto piece_par = [](int i) -> uint32_t { return (i / kPieces) & 1; };
 
@@ -393,36 +377,45 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         if (warp == 0 && lane == 0) {
             // ======================= copies of K and V ================================
             grid_dep_wait();
-            int n = 0;  // tiles
-            for (int i = 0;; ++i) {
-                lane_wait(piece_bar(i), piece_par(i));
+            int nk = 0, nv = 0;  // tiles of K, of V
+            auto timed_wait = [&](uint32_t bb, uint32_t par) -> bool {
+                if (mbar_wait_or_abort(bb, par, abort_flag, kWaitLimitNs)) return true;
+                *abort_flag = 1;
+                return false;
+            };
+            for (int i = 0; timed_wait(piece_bar(i), piece_par(i)); ++i) {
                 const Piece w = pieces[i % kPieces];
                 mbar_arrive(bar(bPieceFree + i % kPieces));
-                if (w.b < 0 || *abort_flag) break;
-                for (int t = w.t0; t < w.t1; ++t, ++n) {
+                if (w.b < 0) break;
+                bool ok = true;
+                for (int t = w.t0; t < w.t1; ++t) {
                     const int row = w.k0 + t * kTile;
-                    const int sk = n % C::SK, sv = n % C::SV;
-                    if (n >= C::SK) lane_wait(bar(bKFree + sk), (n / C::SK - 1) & 1);
+                    const int sk = nk % C::SK, sv = nv % C::SV;
+                    ok = nk < C::SK || timed_wait(bar(bKFree + sk), (nk / C::SK - 1) & 1);
+                    if (!ok) break;
                     mbar_arrive_expect_tx(bar(bKFull + sk), C::TILE);
                     for (int c = 0; c < C::NB; ++c)
                         tma_load_3d(s0 + C::OFF_K + sk * C::TILE + c * C::BLOCK, &tmk, bar(bKFull + sk), 64 * c, w.kvh,
                                     row);
-                    if (n >= C::SV) lane_wait(bar(bVFree + sv), (n / C::SV - 1) & 1);
+                    ++nk;
+                    ok = nv < C::SV || timed_wait(bar(bVFree + sv), (nv / C::SV - 1) & 1);
+                    if (!ok) break;
                     mbar_arrive_expect_tx(bar(bVFull + sv), C::TILE);
                     for (int c = 0; c < C::NB; ++c)
                         tma_load_3d(s0 + C::OFF_V + sv * C::TILE + c * C::BLOCK, &tmv, bar(bVFull + sv), 64 * c, w.kvh,
                                     row);
-                    if (*abort_flag) {
-                        ++n;
-                        break;
-                    }
+                    ++nv;
                 }
+                if (!ok) break;
             }
             // Copies under way land before the CTA may exit.
-            for (int i = max(n - C::SK, 0); i < n; ++i)
-                (void)mbar_wait_bounded(bar(bKFull + i % C::SK), (i / C::SK) & 1, kWaitLimitNs);
-            for (int i = max(n - C::SV, 0); i < n; ++i)
-                (void)mbar_wait_bounded(bar(bVFull + i % C::SV), (i / C::SV) & 1, kWaitLimitNs);
+            bool landed = true;
+            for (int i = max(nk - C::SK, 0); landed && i < nk; ++i)
+                landed = mbar_wait_bounded(bar(bKFull + i % C::SK), (i / C::SK) & 1, kWaitLimitNs);
+            for (int i = max(nv - C::SV, 0); landed && i < nv; ++i)
+                landed = mbar_wait_bounded(bar(bVFull + i % C::SV), (i / C::SV) & 1, kWaitLimitNs);
+            if (!landed) *abort_flag = 1;
+            timed_wait(bar(bDone), 0);
         } else if (warp == 3 && lane == 0) {
             // ======================= the CTA's pieces, and q ==========================
             int4 meta = make_int4(0, 0, 0, 0);  // what the joining kernel is to do with the cut item
@@ -460,7 +453,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 if (i == 0) grid_dep_wait();
                 // tile_toks tokens x G heads are consecutive operand rows
                 for (int g = 0; g <= w.two; ++g) {
-                    if (uses[g] > 0) lane_wait(bar(bQFree + g), (uses[g] - 1) & 1);
+                    if (uses[g] > 0 && !lane_wait(bar(bQFree + g), (uses[g] - 1) & 1)) break;
                     mbar_arrive_expect_tx(bar(bQ + g), a.tile_toks * a.G * D * 2);
                     for (int c = 0; c < C::NB; ++c)
                         tma_load_3d(s0 + C::OFF_Q + g * C::TILE + c * C::BLOCK, &tmq, bar(bQ + g), 64 * c, w.kvh * a.G,
@@ -485,6 +478,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 // Stages and phases of the next tile of K, of V. Per group: the phase of the P that is next (bit g), and
                 // in two bits at 2 g the items whose scores were begun, 2 or 3 for all of that parity from there on.
                 int sk = 0, sv = 0, n_fix = 0;
+                bool on = true;  // no wait was given up on
+                auto wait = [&](uint32_t bb, uint32_t par) { on = lane_wait(bb, par) && on; };
                 uint32_t pk = 0, pv = 0, n_p = 0, items = 0, issued = 0;
                 auto next_k = [&]() {
                     if (++sk == C::SK) sk = 0, pk ^= 1;
@@ -517,37 +512,37 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 };
                 // The first scores of a piece for row tile g.
                 auto begin = [&](const Job& w, int g) {
-                    if (g == 0) lane_wait(bar(bKFull + sk), pk);
-                    lane_wait(bar(bQ + g), items >> (2 * g) & 1);
+                    if (g == 0) wait(bar(bKFull + sk), pk);
+                    wait(bar(bQ + g), items >> (2 * g) & 1);
                     items = (items >> (2 * g) & 3u) == 3u ? items ^ 1u << (2 * g) : items + (1u << (2 * g));
                     scores(g, cols_of(w, g, w.t0));
                     issued = 1;
                     if (g == w.two) next_k();
                 };
-                lane_wait(piece_bar(0), piece_par(0));
+                wait(piece_bar(0), piece_par(0));
                 Job w = job_of(0), next;
 #pragma unroll 1
                 for (int g = 0; w.there && g <= w.two; ++g) begin(w, g);
 #pragma unroll 1
-                for (int i = 0; w.there; ++i) {
+                for (int i = 0; on && w.there; ++i) {
                     next.there = next.two = 0;
                     const int fix = min(w.tf, w.t1);
 #pragma unroll 1
-                    for (int t = w.t0; t < w.t1;) {
+                    for (int t = w.t0; on && t < w.t1;) {
                         // Tiles that both row tiles see in full, as the next one: the loop to be fast.
                         if (t > w.t0 && w.two && t + 1 < fix) {
 #pragma unroll 1
-                            for (; t + 1 < fix; ++t) {
-                                lane_wait(bar(bVFull + sv), pv);
+                            for (; on && t + 1 < fix; ++t) {
+                                wait(bar(bVFull + sv), pv);
                                 const uint64_t vt = desc(s0 + C::OFF_V + sv * C::TILE, C::BLOCK);
 #pragma unroll
                                 for (int g = 0; g < 2; ++g) {
-                                    lane_wait(bar(bP + g), n_p >> g & 1);
+                                    wait(bar(bP + g), n_p >> g & 1);
                                     tc_fence_after();
 #pragma unroll
                                     for (int k = 0; k < kTile / 16; ++k)
                                         umma_ts(tmem + 256 * g + C::O_COL, tmem + 256 * g + 8 * k, vt + k * (2048 >> 4), kIdescPv, 1u);
-                                    if (g == 0) lane_wait(bar(bKFull + sk), pk);
+                                    if (g == 0) wait(bar(bKFull + sk), pk);
                                     scores(g, kTile);
                                 }
                                 n_p ^= 3u;
@@ -558,18 +553,18 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                         }
                         const bool last = t + 1 == w.t1;
                         if (t >= w.tf) {
-                            lane_wait(bar(bFix + n_fix % kFix), (n_fix / kFix) & 1);
+                            wait(bar(bFix + n_fix % kFix), (n_fix / kFix) & 1);
                             ++n_fix;
                         } else {
-                            lane_wait(bar(bVFull + sv), pv);
+                            wait(bar(bVFull + sv), pv);
                         }
                         const uint64_t vt = desc(s0 + C::OFF_V + sv * C::TILE, C::BLOCK);
 #pragma unroll 1
                         for (int g = 0; g <= w.two; ++g) {
                             // the item before has been read out of O
-                            if (t == w.t0 && (items >> (2 * g) & 2u)) lane_wait(bar(bOFree + g), items >> (2 * g) & 1);
+                            if (t == w.t0 && (items >> (2 * g) & 2u)) wait(bar(bOFree + g), items >> (2 * g) & 1);
                             const int steps = cols_of(w, g, t) >> 4;
-                            lane_wait(bar(bP + g), n_p >> g & 1);
+                            wait(bar(bP + g), n_p >> g & 1);
                             n_p ^= 1u << g;
                             tc_fence_after();
                             const uint32_t more_o = t > w.t0 ? 1u : go_on[g];  // O goes on, or starts
@@ -579,14 +574,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                             if (last) {
                                 umma_commit(bar(bO + g));
                             } else {
-                                if (g == 0) lane_wait(bar(bKFull + sk), pk);
+                                if (g == 0) wait(bar(bKFull + sk), pk);
                                 scores(g, cols_of(w, g, t + 1));
                                 if (g == w.two) next_k();
                             }
                         }
                         if (last) {
                             // (q of the next piece may be on its way yet: nothing waits behind it but its scores)
-                            lane_wait(piece_bar(i + 1), piece_par(i + 1));
+                            wait(piece_bar(i + 1), piece_par(i + 1));
                             next = job_of(i + 1);
 #pragma unroll 1
                             for (int g = 0; next.there && g <= next.two; ++g) begin(next, g);
@@ -609,15 +604,17 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             // ======================= V of partly visible tiles ========================
             grid_dep_wait();
             int n = 0, n_fix = 0;
-            for (int i = 0;; ++i) {
-                warp_wait(piece_bar(i), piece_par(i));
+            bool on = true;
+            for (int i = 0; on; ++i) {
+                if (!warp_wait(piece_bar(i), piece_par(i))) break;
                 const Piece w = pieces[i % kPieces];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(bPieceFree + i % kPieces));
-                if (__any_sync(0xffffffffu, w.b < 0 || *abort_flag)) break;
+                if (__any_sync(0xffffffffu, w.b < 0)) break;
                 const int lim = max(min(w.ctx + w.tok0 + 1, w.L), 0);  // keys that every row sees
                 for (int t = w.t0; t < w.t1; ++t, ++n) {
-                    warp_wait(bar(bVFull + n % C::SV), (n / C::SV) & 1);
+                    on = warp_wait(bar(bVFull + n % C::SV), (n / C::SV) & 1);
+                    if (!on) break;
                     if (t < w.tf) {
                         if (lane == 0) mbar_arrive(bar(bVFree + n % C::SV));
                         continue;
@@ -684,7 +681,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             // from warp 3, whose waits end too, whether there is one.
             bool more = true;
             if (!warp_wait(piece_bar(i), piece_par(i))) {
-                for (uint32_t k = 0; k < 4 * kTries && *handed_out < 0 && !mbar_try_wait(piece_bar(i), piece_par(i)); ++k) {}
+                const uint64_t t0 = global_ns();
+                while (*handed_out < 0 && !mbar_try_wait(piece_bar(i), piece_par(i)) && global_ns() - t0 < 4 * kWaitLimitNs) {}
                 more = mbar_try_wait(piece_bar(i), piece_par(i));
             }
             const Piece& w = pieces[i % kPieces];
@@ -921,6 +919,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         }
     }
 
+    if (warp != 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bDone));
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
