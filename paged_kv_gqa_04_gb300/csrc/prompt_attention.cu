@@ -44,7 +44,11 @@
 // S. So one pass over S does, with no maximum in it, and O is scaled rarely (a
 // maximum in every tile: 1949 us and not 1566 for 16,384 tokens, with the MMAs from one
 // thread). fp32 holds what is between: nothing that counts underflows, and a tile adds at
-// most 2^13 times its largest value to O. Sums and O are fp32.
+// most 2^13 times its largest value to O. Sums and O are fp32. The tensor cores cut a
+// product off below about 2^-25 of the sum it goes to, so a sum over n keys of one
+// sign falls short by about n 2^-27 of itself (v = 1 with a tenth of noise, 2^20 keys: 0.4
+// to 0.65%; 2^27 ones: a half). After kFold tiles, 2^16 keys, O therefore goes to the
+// workspace and starts anew: a piece of its own, added to what is there at its output.
 // P meets V as bf16, rounded once (by at most 2^-8 of a weight): that rounding
 // and the output's are of one size, and independent (the output is off by 2.3e-3
 // relative to its norm, 1.5e-3 of it the output's own rounding). A second term, as in
@@ -79,6 +83,7 @@ constexpr int kTile = 128;      // positions per tile
 constexpr int kItemKeys = 512;  // what an item costs beyond its tiles, in keys
 constexpr int kSnapKeys = 1536; // longest item (keys and kItemKeys) up to which items are not cut
 constexpr int kPieces = 4;      // ring of pieces
+constexpr int kFold = 512;      // most tiles of a piece
 constexpr float kRaise = 4096.f; // sum of 64 weights past which their row's reference moves
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr int kFix = 4;         // ring of the fixed tiles' notes: no fewer than there are stages of V
@@ -222,14 +227,16 @@ struct Walk {
     }
 };
 
-// A piece: tiles [t0, t1) of an item (the tokens [tok0, tok0 + toks) of sequence b).
+// A piece: tiles [t0, t1) of an item, all of the CTA's or kFold of them (the tokens [tok0, tok0 + toks) of sequence b).
 struct Piece {
     int b, kvh, q0, k0;      // b < 0: there are no more
     int L, ctx, tok0, toks;
-    int t0, t1, whole, two;  // whole: all of the item; two: two row tiles
+    int t0, t1, whole, two;  // whole: with it, all of the item; two: two row tiles
     int tf;                  // tiles before this one are seen in full by every row
     int end[2];              // keys that either row tile may see
-    int pad[5];
+    int cont;                // the item goes on: its O so far is in the workspace
+    int slot;                // where there: 1 if the CTA has the item's first tile
+    int pad[3];
 };
 static_assert(sizeof(Piece) == 80, "as laid out");
 
@@ -423,15 +430,23 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             const uint64_t policy = l2_policy_evict_first();
             int uses[2] = {0, 0};
             Walk walk(from, to);
+            int at = 0, upto = 0;               // the item's tiles yet to be handed out
             for (int i = 0;; ++i) {
                 Piece w{};
-                w.b = walk.next(a) ? walk.b : -1;
-                if (w.b >= 0) {
+                bool there = at < upto;
+                w.cont = there;
+                if (!there && walk.next(a)) {
+                    at = walk.t0, upto = walk.t1;
+                    there = true;
+                }
+                w.b = there ? walk.b : -1;
+                if (there) {
                     w.kvh = walk.kvh, w.q0 = walk.s.q0, w.k0 = walk.s.k0, w.L = walk.s.L, w.ctx = walk.s.ctx;
                     w.tok0 = walk.rg * 2 * a.tile_toks;
                     w.toks = min(walk.s.N - w.tok0, 2 * a.tile_toks);
-                    w.t0 = walk.t0, w.t1 = walk.t1;
-                    w.whole = w.t0 == 0 && w.t1 == walk.nt;
+                    w.t0 = at, w.t1 = at = min(at + kFold, upto);
+                    w.slot = walk.t0 == 0;
+                    w.whole = walk.t0 == 0 && at == walk.nt;
                     w.two = w.toks > a.tile_toks;
                     w.tf = max(min(w.ctx + w.tok0 + 1, w.L), 0) / kTile;
                     w.end[0] = w.ctx + w.tok0 + min(w.toks, a.tile_toks);
@@ -445,7 +460,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 pieces[i % kPieces] = w;
                 mbar_arrive(piece_bar(i));
                 if (w.b < 0) break;
-                if (w.t0 == 0 && w.t1 < walk.nt) {
+                if (walk.t0 == 0 && upto < walk.nt) {
                     // the CTA that has the item's last unit
                     const int c1 = cuts.at_or_before(to.item + kItemKeys + walk.s.end(walk.rg) - 1);
                     meta = make_int4(w.q0 + w.tok0, w.toks, c1 - static_cast<int>(blockIdx.x) + 1, w.kvh);
@@ -674,7 +689,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         const float* other = theirs + (2 * grp + 1 - half) * 128 + row_l;
         const float sl = fmaxf(fabsf(a.scale_log2), 1.2e-38f);         // -inf times it stays -inf
         const float2 sl2 = make_float2(sl, sl);
-        int n = 0, job = 0, n_o = 0, n_fix = 0;        // the CTA's tiles, this group's jobs and items, fixed tiles
+        int n = 0, job = 0, n_o = 0, n_fix = 0;        // the CTA's tiles, this group's jobs and pieces, fixed tiles
+        float m = -INFINITY, l = 0.f;                  // of the item (l: of this half's columns)
         for (int i = 0;; ++i) {
             // A group's warps meet at barriers, which know no limit: they take up the same pieces, and a wait that was
             // given up on changes nothing of what they do with one. A warp that gives up waiting for a piece learns
@@ -702,7 +718,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             const int lim = live ? min(w.ctx + tok + 1, w.L) : 0;      // positions that this row sees
             // tiles that every row of this group sees in full
             const int inner_end = max(min(w.ctx + w.tok0 + grp * a.tile_toks + 1, w.L), 0) / kTile;
-            float m = -INFINITY, l = 0.f;              // (l: of this half's columns)
+            const bool cont = w.cont != 0;
+            if (!cont) m = -INFINITY, l = 0.f;
             for (int t = t0; t < t1; ++t, ++n, ++job) {
                 const bool first = t == t0;
                 const int vis = lim - t * kTile - 64 * half;   // of this half's columns, those that the row sees
@@ -726,7 +743,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 }
                 {
                     // The half's weights; where their sum asks for another reference, twice.
-                    bool start = first;                // there is no reference yet
+                    bool start = first && !cont;       // there is no reference yet
                     uint32_t p[32];
                     float sum;
                     bool raised = false;
@@ -863,21 +880,27 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             tc_fence_after();
             if (frees) mbar_arrive(bar(bVFree + (n - 1) % C::SV));
             {
+                const int row = 128 * grp + row_l;             // its place in partial sums
+                const int slot = 2 * static_cast<int>(blockIdx.x) + w.slot;
+                // What is there of the item was taken against an earlier reference (a whole number below).
+                float older = 0.f;
+                if (cont && live) {
+                    const float m0 = *part_ml(a.workspace, slot, row);
+                    older = m0 == m ? 1.f : exp2f(m0 - m);
+                }
                 *mine = l;
                 (void)named_bar_and(pair, 64, true);
-                l += *other;
+                const float sum = l + *other;
                 (void)named_bar_and(pair, 64, true);
-                const bool none = l == 0.f, whole = w.whole;
+                const bool none = sum == 0.f, whole = w.whole;
                 const int h = w.kvh * a.G + g_l;
                 const int64_t q_row = w.q0 + tok;
-                const int row = 128 * grp + row_l;             // its place in partial sums
-                const int slot = 2 * static_cast<int>(blockIdx.x) + (t0 == 0 ? 1 : 0);
-                const float inv = whole ? (none ? 0.f : 1.f / l) : 1.f;
+                const float inv = whole ? (none ? 0.f : 1.f / sum) : 1.f;
                 if (live && half == 0) {
                     if (!whole) {
-                        *reinterpret_cast<float2*>(part_ml(a.workspace, slot, row)) = make_float2(m, l);
+                        *reinterpret_cast<float2*>(part_ml(a.workspace, slot, row)) = make_float2(m, sum);
                     } else if (a.lse) {
-                        a.lse[q_row * a.l_s0 + h * a.l_s1] = none ? -INFINITY : (m + __log2f(l)) * 0.69314718055994530942f;
+                        a.lse[q_row * a.l_s0 + h * a.l_s1] = none ? -INFINITY : (m + __log2f(sum)) * 0.69314718055994530942f;
                     }
                 }
                 float* part = part_o<D>(a.workspace, gridDim.x, slot, row) + static_cast<int64_t>(D / 8 * half) * kJoinRows * 4;
@@ -894,6 +917,16 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                         if (lane == 0) mbar_arrive(bar(bOFree + grp));
                     }
                     if (!live) continue;
+                    if (cont) {  // (this thread's own, of the piece before)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float4 x = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(4 * c + e) * kJoinRows * 4);
+                            o[4 * e] = __float_as_uint(fmaf(x.x, older, __uint_as_float(o[4 * e])));
+                            o[4 * e + 1] = __float_as_uint(fmaf(x.y, older, __uint_as_float(o[4 * e + 1])));
+                            o[4 * e + 2] = __float_as_uint(fmaf(x.z, older, __uint_as_float(o[4 * e + 2])));
+                            o[4 * e + 3] = __float_as_uint(fmaf(x.w, older, __uint_as_float(o[4 * e + 3])));
+                        }
+                    }
                     if (whole) {
                         uint32_t q[8];
 #pragma unroll

@@ -13,8 +13,8 @@ pytestmark = pytest.mark.gpu
 
 def test_items_that_last_longer_than_the_limit_of_a_wait():
     # 153 pairs of row tiles of one kv head over 2^27 - 1 keys: an item and a piece of the next for every CTA, more
-    # than a second each, with q of the second waiting for the end of the first. Keys are zeros: all weights are one, and
-    # a thread's sum of them, 64 a tile, is exact in fp32 (a whole number of 64s below 2^26).
+    # than a second each. Keys are zeros and values ones: all weights are one, and a thread's sum of them, 64 a tile, is
+    # exact in fp32 (a whole number of 64s below 2^26), as are the values' in runs of 2^16 keys and the runs'.
     D, G, Tk = 64, 16, 2 ** 27 - 1
     T = 153 * 2 * (128 // G)
     if torch.cuda.mem_get_info()[0] < 60 * 2 ** 30:
@@ -34,6 +34,7 @@ def test_items_that_last_longer_than_the_limit_of_a_wait():
     torch.cuda.synchronize()
     assert first.elapsed_time(last) > 1000.0  # (or this tests nothing)
     assert int(err.item()) == 0
+    assert bool((out == 1.0).all())
     # ln of 2^27 - T .. 2^27 - 1: log2 of an exact sum to 2^-22, times ln 2, and two roundings of a number below 32
     want = torch.log((Tk - T + 1 + torch.arange(T, device="cuda")).double())
     assert bool(((lse.double() - want[:, None]).abs() <= (2.0 ** -22 + 2.0 ** -19) * math.log(2) + 2.0 ** -19).all())
