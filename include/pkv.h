@@ -939,7 +939,8 @@ pkv_status pkv_gather_kv(const pkv_tensor* k_cache, const pkv_tensor* v_cache, c
  *              pkv_prompt_attention_workspace() bytes; its contents need no
  *              preparation. Calls that may run at the same time need one each.
  * Supported: D in {64, 128}; 1 <= Hq/Hkv <= 16; B, Hkv <= 65535; T, Tk < 2^27;
- * Tk >= 1. out and lse_out must not overlap q, k or v (by their extents).
+ * Tk >= 1. out, lse_out and the workspace must not overlap one another nor q, k,
+ * v, q_start or k_start (by their extents).
  * Errors: starts that do not ascend within their rows (clamped) and L_b < N_b
  * (the first rows see nothing) set PKV_FLAG_ROW_RANGE.
  */

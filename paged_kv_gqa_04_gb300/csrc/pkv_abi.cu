@@ -1300,6 +1300,13 @@ static bool overlap(const pkv_tensor& x, const pkv_tensor& y) {
     return x0 < y1 && y0 < x1;
 }
 
+static bool overlap_bytes(const pkv_tensor& x, const void* p, int64_t bytes) {
+    intptr_t x0, x1;
+    extent(x, &x0, &x1);
+    const intptr_t p0 = reinterpret_cast<intptr_t>(p);
+    return x0 < p0 + bytes && p0 < x1;
+}
+
 // One cache as rows to move: whole pages, or the rows of single tokens.
 static pkv_status pool_part(const pkv_tensor& t, int32_t layout, bool pages, int64_t* num_pages, int64_t* P,
                             pkv::PoolPart* out) {
@@ -1812,9 +1819,12 @@ pkv_status pkv_prompt_attention(const pkv_tensor* q_p, const pkv_tensor* k_p, co
     if (!q.ptr || !out.ptr || (Tk > 0 && (!k.ptr || !v.ptr))) return PKV_ERR_INVALID_ARG;
     if (Tk == 0) return PKV_ERR_UNSUPPORTED;  // (nothing to attend to, and nothing to make a descriptor of)
     if (!row16(q, 2) || !row16(k, 2) || !row16(v, 2) || !row16(out, 2)) return PKV_ERR_UNSUPPORTED;
-    // (the rows that other CTAs have yet to read)
-    for (const pkv_tensor* t : {&q, &k, &v})
-        if (overlap(out, *t) || (lse.ptr && overlap(lse, *t))) return PKV_ERR_INVALID_ARG;
+    // (what other CTAs have yet to read, or write)
+    for (const pkv_tensor* t : {&q, &k, &v, &qs, &ks})
+        if (t->ptr && (overlap(out, *t) || (lse.ptr && overlap(lse, *t)))) return PKV_ERR_INVALID_ARG;
+    if (lse.ptr && overlap(out, lse)) return PKV_ERR_INVALID_ARG;
+    for (const pkv_tensor* t : {&q, &k, &v, &qs, &ks, &out, &lse})
+        if (workspace && t->ptr && overlap_bytes(*t, workspace, workspace_bytes)) return PKV_ERR_INVALID_ARG;
     int sms = 0;
     if (pkv::device_sm_count(&sms) != cudaSuccess) return PKV_ERR_CUDA;
     if (!workspace || workspace_bytes < pkv::prompt_attention_workspace(static_cast<int32_t>(D), sms))
