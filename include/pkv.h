@@ -895,7 +895,10 @@ pkv_status pkv_qk_norm_rope_kv_write(const pkv_tensor* q, const pkv_tensor* k, c
  *              are not written.
  * first        [B] int32 (the position of a sequence's first row), or NULL (0).
  * k_out, v_out [T, Hkv, D] bf16, innermost stride 1, rows 16-byte aligned; they
- *              must not overlap the caches (by their extents).
+ *              must not overlap the caches or the index inputs (by their
+ *              extents), nor one another (views of one buffer side by side,
+ *              with the same strides, do not; with other strides their extents
+ *              count).
  * Supported: D in {64, 128}; B, Hkv <= 65535.
  * Errors: a position outside [0, P*max_pages) sets PKV_FLAG_SEQ_LEN_RANGE, a
  * page outside [0, num_pages) PKV_FLAG_PAGE_RANGE: the row is filled with

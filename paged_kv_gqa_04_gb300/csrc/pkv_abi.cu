@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <cstdlib>
 #include <vector>
 #include <algorithm>
 #include <cstdint>
@@ -1307,6 +1308,24 @@ static bool overlap_bytes(const pkv_tensor& x, const void* p, int64_t bytes) {
     return x0 < p0 + bytes && p0 < x1;
 }
 
+// Whether two tensors [n, heads, D] of the same shape and type, innermost stride 1, share an element. (Views of one
+// buffer may lie side by side, their extents interleaved: those are told apart where their strides are the same.)
+static bool rows_overlap(const pkv_tensor& x, const pkv_tensor& y) {
+    if (!overlap(x, y)) return false;
+    const int64_t n = x.shape[0], heads = x.shape[1], D = x.shape[2];
+    if ((n > 1 && x.stride[0] != y.stride[0]) || (heads > 1 && x.stride[1] != y.stride[1])) return true;
+    const int64_t row = n > 1 ? x.stride[0] : 0, head = heads > 1 ? x.stride[1] : 0;
+    const int64_t apart = (reinterpret_cast<intptr_t>(y.ptr) - reinterpret_cast<intptr_t>(x.ptr)) / elem_bytes(x.dtype);
+    // rows that are i rows and j heads apart start this many elements from one another; less than D: they meet
+    for (int64_t j = 1 - heads; j < heads; ++j) {
+        const int64_t left = apart + j * head;
+        const int64_t i = row != 0 ? left / row : 0;
+        for (int64_t k = i - 1; k <= i + 1; ++k)
+            if (std::abs(left - std::min(std::max(k, 1 - n), n - 1) * row) < D) return true;
+    }
+    return false;
+}
+
 // One cache as rows to move: whole pages, or the rows of single tokens.
 static pkv_status pool_part(const pkv_tensor& t, int32_t layout, bool pages, int64_t* num_pages, int64_t* P,
                             pkv::PoolPart* out) {
@@ -1729,8 +1748,9 @@ pkv_status pkv_gather_kv(const pkv_tensor* k_cache_p, const pkv_tensor* v_cache_
     if (T == 0 || B == 0) return PKV_OK;
     if (!ko.ptr || !vo.ptr) return PKV_ERR_INVALID_ARG;
     if (!row16(ko, 2) || !row16(vo, 2)) return PKV_ERR_UNSUPPORTED;
-    for (const pkv_tensor* t : {&kc, &vc, &kbs, &vbs})
+    for (const pkv_tensor* t : {&kc, &vc, &kbs, &vbs, &bt, &start, &first})
         if (t->ptr && (overlap(ko, *t) || overlap(vo, *t))) return PKV_ERR_INVALID_ARG;
+    if (rows_overlap(ko, vo)) return PKV_ERR_INVALID_ARG;
 
     const int tok = layout == PKV_HND ? 2 : 1, head = 3 - tok;
     pkv::GatherArgs a{};
