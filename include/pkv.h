@@ -843,8 +843,9 @@ pkv_status pkv_fork_sequences(const pkv_tensor* caches, int32_t n_caches, int32_
  * w the weight of q or of k:
  *   r = 1 / sqrt( mean_d x_d^2 + eps ),   y_d = (x_d r) w_d
  * in float32 (r to two units in the last place, each product rounded; a key's
- * mean is summed in the order of a plain float32 mean over the row, so that
- * a quantised cache holds what plain operations would write), and then what pkv_rope_kv_write (with block scales:
+ * squares, each rounded, are added in a fixed order: those 32 columns apart in
+ * ascending order, then the 32 sums neighbours in pairs, pairs of pairs and so
+ * on), and then what pkv_rope_kv_write (with block scales:
  * pkv_rope_kv_write_nvfp4) does with q, k and v, y in the place of the rows of q
  * and k:
  *   q[t] <- bf16 of the rotated y (in place), the caches <- the rotated y of k,

@@ -46,10 +46,11 @@ __device__ __forceinline__ void load_weights(const void* w, int is_bf16, int c, 
     }
 }
 
-// Sum of a key's squares, the same in all of its row's lanes: columns 32 apart first, in order, then neighbours in pairs,
-// pairs of pairs and so on: the order of a plain float32 mean over a row of a tensor on this GPU. So a cache holds what
-// plain operations would have put there, bit for bit: one unit in the last place of a norm can move an NVFP4 value by
-// a third of its block's largest. (The D = 128 lanes that share columns 32 apart, c and c ^ 4, take four of the eight sums each.)
+// Sum of a key's squares, the same in all of its row's lanes, in one order whatever the launch: columns 32 apart first,
+// ascending, then neighbours in pairs, pairs of pairs and so on. One unit in the last place of a norm can move an NVFP4
+// value by a third of its block's largest, so the order is stated (pkv.h) and tested to the last bit; this one is what a
+// plain float32 mean over the rows gave as well where it was tried (PyTorch 2.9.1 on this GPU, 1 to 318,000 rows). (The
+// D = 128 lanes that share columns 32 apart, c and c ^ 4, take four of the eight sums each.)
 template <int D>
 __device__ __forceinline__ float sum_of_squares(const Chunk8& lo, const Chunk8& hi, int c, unsigned row_lanes) {
     float a[8], b[8];
