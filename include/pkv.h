@@ -927,7 +927,9 @@ pkv_status pkv_gather_kv(const pkv_tensor* k_cache, const pkv_tensor* v_cache, c
  * see have no effect on it, whatever they hold. Scores and sums are fp32; the
  * weights exp(score_j - m) are rounded to bf16 (half a step: 2^-8 of each) where
  * they meet v, and their sum is taken before that. (Sums run over weights of up to
- * 2^12: values of v past 2^100 may overflow.)
+ * 2^12: values of v past 2^100 may overflow. Scores are to stay below 2^28 in
+ * magnitude: from about 2^30 on fp32 has no two of them closer than 2^6, and rows may
+ * come out as NaN or as if they saw nothing.)
  *
  * q            [T, Hq, D] bf16 (already rotated); k, v [Tk, Hkv, D] bf16;
  *              innermost stride 1, rows 16-byte aligned. Strided views of a

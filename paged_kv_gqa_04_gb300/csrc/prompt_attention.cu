@@ -13,9 +13,9 @@
 // CTA (one CTA per SM), so every CTA does the same amount of work whatever the
 // lengths are, with no plan from the host; sums over a sequence's items are
 // closed forms. An item that is cut leaves partial sums in the workspace (at
-// most two per CTA), which a second kernel joins. Where no item is longer than
-// what partial sums and joining cost (kSnapKeys), the cuts are moved to the
-// next item's start instead.
+// most two per CTA), which a second kernel joins. Where no item of the whole call is
+// longer than what partial sums and joining cost (kSnapKeys), the cuts are moved to
+// the next item's start instead.
 //
 // A CTA's roles:
 //   warp 0        TMA loads of K and V, 128 positions at a time
@@ -35,7 +35,8 @@
 //                 its output. Two threads share a row, 64 positions of a tile
 //                 each: 4 warps a group, a thread for a whole row, leave the
 //                 exponential unit waiting for the warps' other instructions
-//                 (8,192 tokens, 28 heads: 418 us and not 390; D = 64 408 and not 343).
+//                 (8,192 tokens, 28 heads: 418 us and not 390 at that step; D = 64, 32
+//                 heads, 408 and not 343).
 //
 // Softmax. The weights are exp2(score - m) with a reference m per row: the
 // maximum of the tile where it last moved, rounded up to a whole number. It moves
@@ -55,11 +56,12 @@
 // the attention of drafted tokens, is half as much tensor work again.
 //
 // Bound: the tensor cores' turns with the softmax. 16,384 tokens of 28 heads, D = 128:
-// 1271 us, 1.51 PFLOP/s, 79% of the rate of a large library product; a group's softmax
+// 1264 us, 1.52 PFLOP/s, 79% of the rate of a large library product; a group's softmax
 // of a tile (1400 cycles) and the hand-overs are a little longer than the other
-// group's MMAs. Short prompts: an item's start, the tile on the diagonal and the
-// output (32 prompts of 1 to 2048 tokens, 32 heads: 193 us, 0.78 PFLOP/s of visible
-// pairs).
+// group's MMAs. D = 64, 8,192 tokens of 32 heads: 323 us, 0.85 PFLOP/s; the same softmax
+// beside half the tensor work. Short prompts: an item's start, the tile on the diagonal
+// and the output (32 prompts of 1 to 2048 tokens, 32 heads: 187 us, 0.81 PFLOP/s of
+// visible pairs).
 //
 // Waits. The thread that copies K and V is the one that keeps time: what it waits
 // for comes within a tile's turn of the others, whatever the length of an item, and
@@ -80,8 +82,13 @@ namespace pkv {
 namespace {
 
 constexpr int kTile = 128;      // positions per tile
-constexpr int kItemKeys = 512;  // what an item costs beyond its tiles, in keys
-constexpr int kSnapKeys = 1536; // longest item (keys and kItemKeys) up to which items are not cut
+// What an item costs beyond its tiles, in keys. (256, 512 and 768: 8,192 tokens, 28 heads 348, 331, 335 us; 32 prompts of 1
+// to 2048 tokens, 32 heads 193, 199, 218, D = 64 156, 165, 183; 2 prompts of 1,000 tokens 36.7, 39.2, 39.2.)
+constexpr int kItemKeys = 512;
+// Longest item (keys and kItemKeys) up to which a call's items are not cut. (0, 1024, 1536 and 2560, 32 heads of 128: a prompt of
+// 600 tokens 22.5, 22.4, 16.9, 16.8 us; of 1,000 31.8, 31.7, 22.1, 22.0; 2 of 1,000 39.7, 39.7, 39.2, 33.2; 4 of 500 31.5,
+// 29.6, 29.7, 24.5; the ragged prompts above, D = 64, 166, 166, 165, 171.)
+constexpr int kSnapKeys = 1536;
 constexpr int kPieces = 4;      // ring of pieces
 constexpr int kFold = 512;      // most tiles of a piece
 constexpr float kRaise = 4096.f; // sum of 64 weights past which their row's reference moves
@@ -380,7 +387,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     auto piece_par = [](int i) -> uint32_t { return (i / kPieces) & 1; };
 
     if (warp < 4) {
-        if constexpr (D == 64) reg_dec<96>();
         if (warp == 0 && lane == 0) {
             // ======================= copies of K and V ================================
             grid_dep_wait();
@@ -673,7 +679,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         __syncwarp();
     } else {
         // ======================= softmax ==========================================
-        if constexpr (D == 64) reg_inc<96>();  // (no more than it has: with this line nothing spills, 362 us and not 385)
         grid_dep_wait();
         grid_dep_launch();
         const int grp = (warp - 4) >> 3, half = (warp - 4) >> 2 & 1, wq = warp & 3;

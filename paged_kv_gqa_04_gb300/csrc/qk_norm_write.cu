@@ -97,8 +97,9 @@ __device__ __forceinline__ float quick_sum_of_squares(const Chunk8& lo, const Ch
 }
 
 // Small CTAs: one that waits for its loads holds up fewer of the others (32 prompts of 300 to 2000 tokens, bf16,
-// keys kept, four heads a thread: 190 us with 2 CTAs of 256 threads an SM, 172 with 5 of 128, 171 with 10 of 64; 11 of
-// 64 spill, 251).
+// keys kept, four heads a thread: 190 us with 2 CTAs of 256 threads an SM, 172 with 5 of 128, 171 with 10 of 64, 251 with 11
+// of 64). At ten a thread has 96 registers, and the four-heads forms spill: bytes stored and loaded, D = 128, bf16 52 and
+// 92, FP8 32 and 144, NVFP4 68 and 176; D = 64, 0, 4 and 32, 36 and 88.
 constexpr int kThreads = 64;
 constexpr int kCtas = 10;  // an SM's, that registers are budgeted for
 
