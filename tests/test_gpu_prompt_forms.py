@@ -48,6 +48,15 @@ def test_keys_and_values_of_different_strides():
     check_prompt(s)
 
 
+@pytest.mark.parametrize("D,G", [(128, 4), (64, 1), (128, 7)])
+def test_heads_outermost(D, G):
+    s = make_prompt([300, 77, 2500], [0, 50, 0], 2 * G, 2, D, seed=8)
+    for x in ("q", "k", "v", "out"):
+        s[x] = s[x].transpose(0, 1).contiguous().transpose(0, 1)
+    run_prompt(s)
+    check_prompt(s)
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("ctx", [[100_000], [997 * i % 9000 for i in range(40)]], ids=["one", "forty"])
 def test_single_tokens_behind_contexts(D, ctx):

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from tests._prompt import make_prompt, run_prompt
-from tests._prompt_rounding import excess, weights
+from tests._prompt_rounding import excess, squares, weights
 
 pytestmark = pytest.mark.gpu
 
@@ -71,3 +71,29 @@ def test_every_tile_of_values_meets_its_own_weights(name):
         tol = (2 * 2.0 ** -8 * 1.01 + min(w.shape[1], 2 ** 16) * 2.0 ** -24 + 2 * mag * (D + 8) * 2.0 ** -24 + 2.0 ** -19) * o
         tol = tol + 2.0 ** -126
         assert bool(((s["out"][at, h].double() - o).abs() <= tol).all()), f"sequence {b}, head {h}"
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_row_that_sees_one_key_gives_its_value(D):
+    # Its weight is one, to within the exponential's 2^-22, and so is their sum: bf16 holds their quotient, v, as it is.
+    s = make_prompt([1, 5, 40, 700, 1], [0] * 5, 8, 2, D, seed=90)
+    run_prompt(s)
+    torch.cuda.synchronize()
+    for at in (0, 1, 6, 46, 746):
+        assert torch.equal(s["out"][at], s["v"][at].repeat_interleave(4, 0))
+
+
+@pytest.mark.parametrize("q_mult", [1.0, 8.0])
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_largest_weight_of_a_short_row_is_exact(D, q_mult):
+    """Rows of up to a tile of keys: as errors of independent roundings, without one of the largest weight."""
+    s = make_prompt([1, 2, 3, 17, 60, 127, 128], [0, 5, 0, 100, 0, 1, 0], 8, 2, D, seed=91, q_mult=q_mult)
+    run_prompt(s)
+    torch.cuda.synchronize()
+    for b, h, at, w, v in each_head(s, None):
+        o = w @ v
+        others = w.scatter(1, w.argmax(1, keepdim=True), 0.0)
+        # (fp32: the exponentials' 2^-20 and the scores' roundings, far below 2^-16 of w |v| each)
+        small = 2.0 ** -32 * (w ** 2) @ (v ** 2).sum(1)
+        err = ((s["out"][at, h].double() - o) ** 2).sum(1)
+        assert bool((err <= 4 * (squares(others, v, o) + small)).all()), f"sequence {b}, head {h}"
